@@ -69,10 +69,57 @@ class hstu_attn_delta_args(ctypes.Structure):
                             "k_cache", "v_cache", "o", "y", "ln_mean", "ln_rstd")]
 
 
+_i32, _i64, _pair = ctypes.c_int32, ctypes.c_int64, ctypes.c_int64 * 2
+
+
+class hstu_qk_desc(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32)] + \
+        [(n, _i32) for n in ("dtype", "Hq", "Hk", "d", "rot_dim", "interleaved", "norm")] + \
+        [("eps", ctypes.c_float), ("reserved", ctypes.c_uint32), ("total_tokens", _i64), ("max_position", _i64)] + \
+        [(n, _pair) for n in ("q_strides", "k_strides", "q_out_strides", "k_out_strides", "dq_strides", "dk_strides")]
+
+
+_QK = ("num_tokens", "positions", "cos", "sin", "q_gain", "k_gain", "q", "k")
+
+
+class hstu_qk_fwd_args(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in _QK + ("q_out", "k_out")]
+
+
+class hstu_qk_bwd_args(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in _QK + ("dq_out", "dk_out", "dq", "dk", "d_q_gain", "d_k_gain")]
+
+
+class hstu_cache_desc(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32)] + \
+        [(n, _i32) for n in ("H", "d", "page_size", "num_pages", "k_exp", "v_exp", "max_pages")] + \
+        [("pages", _vp), ("timestamps", _vp)]
+
+
+class hstu_cache_append_args(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("B", "rot_dim", "interleaved", "norm")] + \
+        [("eps", ctypes.c_float), ("reserved", ctypes.c_uint32), ("total_tokens", _i64), ("max_position", _i64),
+         ("k_strides", _pair), ("v_strides", _pair)] + \
+        [(n, _vp) for n in ("seq_offsets", "cache_lens", "block_table", "token_times", "cos", "sin", "k_gain", "k", "v")]
+
+
+class hstu_cache_read_args(ctypes.Structure):
+    _fields_ = [("B", _i32), ("reserved", ctypes.c_uint32), ("total_tokens", _i64)] + \
+        [(n, _vp) for n in ("seq_offsets", "starts", "block_table", "k", "v", "token_times")]
+
+
+class hstu_attn_cached_args(ctypes.Structure):
+    _fields_ = [("max_rows", _i32), ("reserved", ctypes.c_uint32)] + \
+        [(n, _vp) for n in ("seq_offsets", "cache_lens", "num_targets", "block_table", "row_times", "rab_pos",
+                            "rab_time", "q", "k", "v", "u", "o", "y")]
+
+
 EXPORTED = ("hstu_attn_workspace_size", "hstu_attn_fwd", "hstu_attn_bwd", "hstu_attn_debug_plan",
             "hstu_get_device_error", "hstu_status_string", "hstu_last_launch_count",
             "hstu_time_next_attention_kernel", "hstu_last_error_detail", "hstu_attn_fwd_noalloc",
-            "hstu_layer_workspace_size", "hstu_layer_fwd", "hstu_layer_bwd", "hstu_attn_fwd_delta")
+            "hstu_layer_workspace_size", "hstu_layer_fwd", "hstu_layer_bwd", "hstu_attn_fwd_delta",
+            "hstu_qk_workspace_size", "hstu_qk_norm_rope_fwd", "hstu_qk_norm_rope_bwd", "hstu_cache_bytes",
+            "hstu_cache_append", "hstu_cache_read", "hstu_attn_cached_workspace_size", "hstu_attn_fwd_cached")
 
 _lib = None
 
@@ -109,9 +156,20 @@ def load(build_if_missing: bool = True):
     L.hstu_layer_fwd.argtypes = [P(hstu_attn_desc), P(hstu_layer_fwd_args), _vp, ctypes.c_size_t, _vp]
     L.hstu_layer_bwd.argtypes = [P(hstu_attn_desc), P(hstu_layer_bwd_args), _vp, ctypes.c_size_t, _vp]
     L.hstu_attn_fwd_delta.argtypes = [P(hstu_attn_desc), P(hstu_attn_delta_args), _vp, ctypes.c_size_t, _vp]
+    size_p, sz = P(ctypes.c_size_t), ctypes.c_size_t
+    L.hstu_qk_workspace_size.argtypes = [P(hstu_qk_desc), size_p, size_p]
+    L.hstu_qk_norm_rope_fwd.argtypes = [P(hstu_qk_desc), P(hstu_qk_fwd_args), _vp, sz, _vp]
+    L.hstu_qk_norm_rope_bwd.argtypes = [P(hstu_qk_desc), P(hstu_qk_bwd_args), _vp, sz, _vp]
+    L.hstu_cache_bytes.argtypes = [P(hstu_cache_desc), size_p, size_p]
+    L.hstu_cache_append.argtypes = [P(hstu_cache_desc), P(hstu_cache_append_args), _vp, sz, _vp]
+    L.hstu_cache_read.argtypes = [P(hstu_cache_desc), P(hstu_cache_read_args), _vp, sz, _vp]
+    L.hstu_attn_cached_workspace_size.argtypes = [P(hstu_attn_desc), P(hstu_cache_desc), ctypes.c_int32, size_p]
+    L.hstu_attn_fwd_cached.argtypes = [P(hstu_attn_desc), P(hstu_cache_desc), P(hstu_attn_cached_args), _vp, sz, _vp]
     for name in ("hstu_attn_workspace_size", "hstu_attn_fwd", "hstu_attn_bwd", "hstu_attn_debug_plan",
                  "hstu_get_device_error", "hstu_layer_workspace_size", "hstu_layer_fwd", "hstu_layer_bwd",
-                 "hstu_attn_fwd_delta"):
+                 "hstu_attn_fwd_delta", "hstu_qk_workspace_size", "hstu_qk_norm_rope_fwd", "hstu_qk_norm_rope_bwd",
+                 "hstu_cache_bytes", "hstu_cache_append", "hstu_cache_read", "hstu_attn_cached_workspace_size",
+                 "hstu_attn_fwd_cached"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -209,6 +267,51 @@ def hstu_layer_fwd(desc, args, workspace: int, workspace_bytes: int, stream: int
 def hstu_layer_bwd(desc, args, workspace: int, workspace_bytes: int, stream: int):
     _check(load().hstu_layer_bwd(ctypes.byref(desc), ctypes.byref(args), workspace, workspace_bytes,
                                  stream), "hstu_layer_bwd")
+
+
+def hstu_qk_workspace_size(desc):
+    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(load().hstu_qk_workspace_size(ctypes.byref(desc), ctypes.byref(f), ctypes.byref(b)), "hstu_qk_workspace_size")
+    return int(f.value), int(b.value)
+
+
+def hstu_qk_norm_rope_fwd(desc, args, workspace: int, workspace_bytes: int, stream: int):
+    _check(load().hstu_qk_norm_rope_fwd(ctypes.byref(desc), ctypes.byref(args), workspace, workspace_bytes, stream),
+           "hstu_qk_norm_rope_fwd")
+
+
+def hstu_qk_norm_rope_bwd(desc, args, workspace: int, workspace_bytes: int, stream: int):
+    _check(load().hstu_qk_norm_rope_bwd(ctypes.byref(desc), ctypes.byref(args), workspace, workspace_bytes, stream),
+           "hstu_qk_norm_rope_bwd")
+
+
+def hstu_cache_bytes(cache):
+    """(bytes of one page, bytes of all pages)."""
+    p, t = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(load().hstu_cache_bytes(ctypes.byref(cache), ctypes.byref(p), ctypes.byref(t)), "hstu_cache_bytes")
+    return int(p.value), int(t.value)
+
+
+def hstu_cache_append(cache, args, workspace: int, workspace_bytes: int, stream: int):
+    _check(load().hstu_cache_append(ctypes.byref(cache), ctypes.byref(args), workspace, workspace_bytes, stream),
+           "hstu_cache_append")
+
+
+def hstu_cache_read(cache, args, workspace: int, workspace_bytes: int, stream: int):
+    _check(load().hstu_cache_read(ctypes.byref(cache), ctypes.byref(args), workspace, workspace_bytes, stream),
+           "hstu_cache_read")
+
+
+def hstu_attn_cached_workspace_size(desc, cache, max_rows: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().hstu_attn_cached_workspace_size(ctypes.byref(desc), ctypes.byref(cache), max_rows, ctypes.byref(n)),
+           "hstu_attn_cached_workspace_size")
+    return int(n.value)
+
+
+def hstu_attn_fwd_cached(desc, cache, args, workspace: int, workspace_bytes: int, stream: int):
+    _check(load().hstu_attn_fwd_cached(ctypes.byref(desc), ctypes.byref(cache), ctypes.byref(args), workspace,
+                                       workspace_bytes, stream), "hstu_attn_fwd_cached")
 
 
 def hstu_get_device_error(workspace: int, stream: int) -> int:

@@ -260,6 +260,10 @@ void set_launch_detail(cudaError_t e, const char* kernel, const void* func, int 
 
 namespace hstu {
 void note_launches(int32_t n) { g_launches += n; }
+void reset_launches() {
+  g_launches = 0;
+  clear_detail();
+}
 }  // namespace hstu
 
 extern "C" {

@@ -149,6 +149,8 @@ void set_launch_detail(cudaError_t e, const char* kernel, const void* func, int 
 void set_detail_message(const char* msg);
 // adds n kernels of a composite call (the layer) to hstu_last_launch_count
 void note_launches(int32_t n);
+// starts a call's launch count and error detail afresh
+void reset_launches();
 
 // Launches kernel<<<grid, block, smem, st>>>(args...) with programmatic
 // stream serialization: it may start while the previous kernel in the stream

@@ -391,6 +391,230 @@ typedef struct {
 hstu_status_t hstu_attn_fwd_delta(const hstu_attn_desc* desc, const hstu_attn_delta_args* args,
                                   void* workspace, size_t workspace_bytes, hstu_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Queries and keys on their way into the attention: an RMS norm per head and
+ * a rotation by the token's position, in one pass over both tensors, with its
+ * backward.  For one head's d features x of a token at position p:
+ *
+ *   r = 1 / sqrt(mean(x^2) + eps);  w_i = x_i r gain_i      (norm = 1; else w = x)
+ *   pair i of the first rot_dim features, i < rot_dim / 2:
+ *     (a, b) = (w_i, w_{i + rot_dim/2}), or (w_{2i}, w_{2i+1}) with interleaved
+ *     a' = a cos[p][i] - b sin[p][i];   b' = b cos[p][i] + a sin[p][i]
+ *   the features from rot_dim on stay w.
+ *
+ * The tables are the caller's ([max_position, rot_dim / 2] FP32 each), and
+ * so are the positions: a candidate of the ranking task has the position
+ * h_end of its sequence, like in the attention's position buckets.  Sums and
+ * products are FP32, each output is rounded once.  Backward, with e = the
+ * incoming gradient turned back by the rotation:
+ *   dgain_i = sum over tokens and heads of e_i x_i r
+ *   dx = r (e gain - x r mean(e gain x r))                  (norm = 0: dx = e)
+ *
+ * Either of q, k may be absent (its head count 0).  Tensors are strided: the
+ * d features of a head are contiguous, heads and tokens lie any multiple of
+ * 16 bytes apart (q and k may be parts of one projection's output).  An
+ * output may be its input (same pointer and strides); other overlaps of an
+ * output with anything are the caller's error.  d is 32, 64 or 128, rot_dim a
+ * multiple of 8 (0: no rotation) of at most d.
+ *
+ * The workspace (256-byte aligned) starts with a 256-byte header that must
+ * be zero before its first use.  An error that the device finds (a position
+ * outside the tables: HSTU_ERR_DEVICE_CHECK, that row's output is undefined)
+ * stays in the header, read by hstu_get_device_error, until the caller zeroes
+ * it.  Calls that overlap in time need workspaces of their own.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  uint32_t struct_size;      /* sizeof(hstu_qk_desc) */
+  int32_t dtype;             /* of q, k and everything shaped like them */
+  int32_t Hq, Hk;            /* heads of q and of k; 0: absent */
+  int32_t d;
+  int32_t rot_dim;
+  int32_t interleaved;       /* pairs of neighbours instead of halves */
+  int32_t norm;              /* 1: RMS norm with gain, 0: none */
+  float eps;
+  uint32_t reserved;         /* must be 0 */
+  int64_t total_tokens;      /* T */
+  int64_t max_position;      /* rows of cos and sin */
+  int64_t q_strides[2];      /* of q: elements from token to token, from head to head */
+  int64_t k_strides[2];
+  int64_t q_out_strides[2];  /* of q_out (forward) and dq_out (backward) */
+  int64_t k_out_strides[2];
+  int64_t dq_strides[2];     /* of dq (backward only) */
+  int64_t dk_strides[2];
+} hstu_qk_desc;
+
+typedef struct {
+  const int64_t* num_tokens; /* device: tokens to work on, <= T (e.g. &seq_offsets[B]); rows behind them are left
+                                as they are.  NULL: all T */
+  const int32_t* positions;  /* [T]; may be NULL when rot_dim is 0 */
+  const float* cos;          /* [max_position, rot_dim / 2] */
+  const float* sin;
+  const float* q_gain;       /* [d], shared by all heads, or NULL (ones); only with norm */
+  const float* k_gain;
+  const void* q;             /* [T, Hq, d] strided */
+  const void* k;             /* [T, Hk, d] strided */
+  void* q_out;
+  void* k_out;
+} hstu_qk_fwd_args;
+
+typedef struct {
+  const int64_t* num_tokens;
+  const int32_t* positions;
+  const float* cos;
+  const float* sin;
+  const float* q_gain;
+  const float* k_gain;
+  const void* q;             /* the forward's inputs */
+  const void* k;
+  const void* dq_out;        /* gradients of the forward's outputs */
+  const void* dk_out;
+  void* dq;                  /* out */
+  void* dk;
+  float* d_q_gain;           /* out [d] FP32 or NULL (not wanted); summed in a fixed order */
+  float* d_k_gain;
+} hstu_qk_bwd_args;
+
+hstu_status_t hstu_qk_workspace_size(const hstu_qk_desc* desc, size_t* fwd_bytes, size_t* bwd_bytes);
+hstu_status_t hstu_qk_norm_rope_fwd(const hstu_qk_desc* desc, const hstu_qk_fwd_args* args, void* workspace,
+                                    size_t workspace_bytes, hstu_stream_t stream);
+hstu_status_t hstu_qk_norm_rope_bwd(const hstu_qk_desc* desc, const hstu_qk_bwd_args* args, void* workspace,
+                                    size_t workspace_bytes, hstu_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A paged cache of keys and values in 4 bits, for serving.
+ *
+ * The 16 features [16 g, 16 g + 16) of one head of one token share a scale s
+ * in e4m3 (4 exponent and 3 mantissa bits); each is held as a code in e2m1,
+ * whose magnitudes are 0, .5, 1, 1.5, 2, 3, 4, 6.  With E = k_exp for keys and
+ * v_exp for values, one power of two for the whole cache:
+ *
+ *   s = e4m3(max |x| 2^-E / 6), at most 448;  code = e2m1(x 2^-E / s), at most 6
+ *   value = code s 2^E        (s = 0: all values 0; a NaN in the group: all NaN)
+ *
+ * both rounded to nearest, ties to the even mantissa, as real numbers would be
+ * (the borders are decided exactly).  A value has 6 significant bits: it is a
+ * BF16 number, and before the 2^E a FP16 number too.  A group's smallest
+ * scale is 2^-9, so E should bring the data's usual magnitude near 1.
+ *
+ * pages is [num_pages][H] blocks of 2 page_size (d/2 + d/16) bytes, each
+ *   K codes [page_size][d/2] | K scales [page_size][d/16] | V codes | V scales,
+ * feature 2i in the low half of byte i.  A sequence of L tokens lies in the
+ * pages block_table[b][0 .. ceil(L / page_size)), position j at place
+ * j % page_size of entry j / page_size.  Sequences may share pages that are
+ * only read; a position that is being written belongs to one sequence.
+ * timestamps, when the time bias is wanted, are [num_pages][page_size].
+ *
+ * The calls below take workspaces as hstu_qk_norm_rope_fwd does (zero header,
+ * errors stay until the header is zeroed), and tokens or rows behind
+ * seq_offsets[B] (a batch padded to a fixed total_tokens) are left as they
+ * are.  Inconsistent offsets or lengths and page numbers outside the cache
+ * are found on the device (HSTU_ERR_DEVICE_CHECK); nothing outside the given
+ * buffers is touched then.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  uint32_t struct_size;      /* sizeof(hstu_cache_desc) */
+  int32_t H, d;              /* d = 64 or 128 */
+  int32_t page_size;         /* 32, 64 or 128 */
+  int32_t num_pages;
+  int32_t k_exp, v_exp;      /* -32 .. 32 */
+  int32_t max_pages;         /* entries of a row of the block tables */
+  void* pages;               /* 16-byte aligned */
+  int64_t* timestamps;       /* 16-byte aligned, or NULL */
+} hstu_cache_desc;
+
+/* Append: token i of the n_b = seq_offsets[b+1] - seq_offsets[b] new ones of
+ * sequence b is written at position cache_lens[b] - n_b + i, where cache_lens
+ * counts the new tokens too.  On its way a key goes through the norm and the
+ * rotation of hstu_qk_norm_rope_fwd (p = its position in the cache), without
+ * being rounded in between.  k and v are BF16, strided as there. */
+typedef struct {
+  int32_t B;
+  int32_t rot_dim, interleaved, norm;
+  float eps;
+  uint32_t reserved;           /* must be 0 */
+  int64_t total_tokens;        /* rows of k, v, timestamps */
+  int64_t max_position;        /* rows of cos, sin; every written position lies below it (with rot_dim > 0) */
+  int64_t k_strides[2], v_strides[2];
+  const int64_t* seq_offsets;  /* [B+1], non-decreasing, seq_offsets[0] == 0, seq_offsets[B] <= total_tokens */
+  const int32_t* cache_lens;   /* [B] */
+  const int32_t* block_table;  /* [B][max_pages] */
+  const int64_t* token_times;  /* [total_tokens], written to the cache's timestamps; NULL iff those are NULL */
+  const float* cos;
+  const float* sin;
+  const float* k_gain;         /* [d] or NULL */
+  const void* k;
+  const void* v;
+} hstu_cache_append_args;
+
+/* Read: positions [starts[b], starts[b] + n_b) of sequence b into rows
+ * seq_offsets[b].. of dense BF16 k, v [total_tokens, H, d] (and times). */
+typedef struct {
+  int32_t B;
+  uint32_t reserved;           /* must be 0 */
+  int64_t total_tokens;
+  const int64_t* seq_offsets;  /* [B+1] */
+  const int32_t* starts;       /* [B] first position, or NULL (0) */
+  const int32_t* block_table;
+  void* k;                     /* out, or NULL */
+  void* v;                     /* out, or NULL */
+  int64_t* token_times;        /* out, or NULL */
+} hstu_cache_read_args;
+
+/* Bytes of pages for this descriptor's H, d, page_size and num_pages. */
+hstu_status_t hstu_cache_bytes(const hstu_cache_desc* cache, size_t* page_bytes, size_t* total_bytes);
+/* Workspace: 256 bytes for both. */
+hstu_status_t hstu_cache_append(const hstu_cache_desc* cache, const hstu_cache_append_args* args, void* workspace,
+                                size_t workspace_bytes, hstu_stream_t stream);
+hstu_status_t hstu_cache_read(const hstu_cache_desc* cache, const hstu_cache_read_args* args, void* workspace,
+                              size_t workspace_bytes, hstu_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * HSTU attention of new rows over the paged cache (the delta forward's
+ * serving form).  Sequence b has L = cache_lens[b] cached tokens and
+ * n = seq_offsets[b+1] - seq_offsets[b] rows, of which the last m =
+ * num_targets[b] are candidates and the first n - m are its newest history
+ * tokens, already appended: row r < n - m is the token at position
+ * L - (n - m) + r and sees the cached positions up to its own; a candidate
+ * has position L, sees the whole cache and itself (its own BF16 key and
+ * value, which are not in the cache), never another candidate.  Buckets, 1/N,
+ * norm and gate as in hstu_attn_fwd without contexts.  k, v are read for
+ * candidates only.
+ *
+ * The descriptor is the attention's: dtype and out_dtype BF16, d_qk == d_v ==
+ * the cache's d, H <= its H * d limit, total_tokens = rows, max_seq_len = N
+ * bounding every L + m, no flags, no dropout.  max_rows bounds every n (it
+ * picks the tile's width: 16, 32, 64 or 128 rows).
+ *
+ * Precision: K, V and q enter the tensor cores exactly; 16 SiLU(z) is rounded
+ * once to FP16 (so scores of 4094 and more overflow to infinity; a bias of
+ * minus infinity leaves the pair out); sums, norm and gate are FP32 and o and
+ * y are rounded once.  The cache's tiles are dealt evenly to the CTAs and
+ * partial sums added in a fixed order: equal inputs give equal bits.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t max_rows;
+  uint32_t reserved;             /* must be 0 */
+  const int64_t* seq_offsets;    /* [B+1], seq_offsets[B] <= total_tokens */
+  const int32_t* cache_lens;     /* [B] */
+  const int32_t* num_targets;    /* [B] or NULL (no candidates) */
+  const int32_t* block_table;    /* [B][max_pages] */
+  const int64_t* row_times;      /* [T] or NULL (no time bias); needs the cache's timestamps */
+  const float* rab_pos;          /* [H, P] or NULL */
+  const float* rab_time;         /* [H, Tb] or NULL; ignored without row_times */
+  const void* q;                 /* [T, H, d] dense, like k, v */
+  const void* k;                 /* may be NULL without num_targets */
+  const void* v;
+  const void* u;                 /* [T, H*d] BF16 gate or NULL (one) */
+  void* o;                       /* out [T, H, d] or NULL */
+  void* y;                       /* out [T, H*d] or NULL */
+} hstu_attn_cached_args;
+
+hstu_status_t hstu_attn_cached_workspace_size(const hstu_attn_desc* desc, const hstu_cache_desc* cache,
+                                              int32_t max_rows, size_t* bytes);
+hstu_status_t hstu_attn_fwd_cached(const hstu_attn_desc* desc, const hstu_cache_desc* cache,
+                                   const hstu_attn_cached_args* args, void* workspace, size_t workspace_bytes,
+                                   hstu_stream_t stream);
+
 /* Reads the device error word of the last call that used this workspace
  * (HSTU_OK when none).  Synchronises the stream. */
 hstu_status_t hstu_get_device_error(const void* workspace, hstu_stream_t stream, int32_t* code);
@@ -406,8 +630,8 @@ const char* hstu_status_string(hstu_status_t status);
 const char* hstu_last_error_detail(void);
 
 /* Number of this library's kernels that the last successful hstu_attn_fwd,
- * hstu_attn_bwd, hstu_attn_fwd_delta, hstu_layer_fwd or hstu_layer_bwd call
- * on this thread launched (for launch accounting; cuBLAS's kernels inside
+ * hstu_attn_bwd, hstu_attn_fwd_delta, hstu_layer_*, hstu_qk_* or hstu_cache_*
+ * or hstu_attn_fwd_cached call on this thread launched (for launch accounting; cuBLAS's kernels inside
  * the layer calls are not counted). */
 int32_t hstu_last_launch_count(void);
 
