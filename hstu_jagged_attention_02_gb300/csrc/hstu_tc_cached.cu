@@ -1,0 +1,799 @@
+// Tensor-core kernel of the attention over the paged 4-bit cache
+// (hstu_attn_fwd_cached): for a block of up to N rows of one head, over tiles
+// of 128 cached tokens,
+//
+//   S^T [128 x N] = K Q^T          tcgen05.mma, FP16 x FP16 -> FP32 in TMEM
+//   P   = 16 SiLU(z), rounded once to FP16, 0 where a row does not see a token
+//   O^T [d x N] += V^T P           tcgen05.mma, accumulator in TMEM
+//
+// The cached tokens are the M side of the first product and the features that
+// of the second, so the tensor core's fixed 128 is filled however few rows
+// there are, and N follows the rows (16, 32, 64 or 128): a decode step's one
+// row costs N = 16 columns of products and scores, not 128.  A thread of the
+// score step holds one cached token, whose position and time biases are the
+// same for every candidate of a request: one table lookup a tile and thread
+// where the block's rows share the position and time buckets towards the token,
+// as they do for candidates and for tokens far back; otherwise (rows near the
+// tokens, a time bucket's border inside the block) a lookup a score.
+//
+// The pages reach shared memory as they are (cp.async.bulk, 9/16 byte a
+// feature) and are decoded there to FP16, where code x scale is exact.  q is
+// FP16 too: a BF16 row times the power of two that brings its largest feature
+// to 2^14 is exact down to 2^-28 of that feature; the power goes back in with
+// alpha.
+//
+// Roles (19 warps): 0-7 scores (warp w: TMEM lanes 32 (w % 4), columns half
+// w / 4), 8-15 decoding and q, 16 page copies and the CTA's list of pieces, 17
+// S products and TMEM, 18 PV products.  Two tile buffers {K, V}; P takes K's
+// place once the tile's S is complete.  Work is dealt evenly (hstu_cached.cuh).
+// Every wait is bounded.
+#include "hstu_cached.cuh"
+#include "tc_ptx.cuh"
+
+namespace hstu {
+
+namespace {
+
+using namespace tc;
+
+constexpr int TILE = kCachedTile;
+constexpr int kEpiWarps = 8, kDecWarps = 8;
+constexpr int kDecWarp0 = 8, kCopyWarp = 16, kSWarp = 17, kPvWarp = 18;
+constexpr int kThreads = 19 * 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kPScale = 16.f;
+
+template <int D, int N>
+struct Cfg {
+  static constexpr int NCH = D / 64;                       // 128-byte column chunks of a decoded row
+  static constexpr int CHUNK = TILE * 128;
+  static constexpr int KV_BYTES = NCH * CHUNK;
+  static constexpr int P_BYTES = TILE * N * 2;
+  static constexpr int KP_BYTES = KV_BYTES > P_BYTES ? KV_BYTES : P_BYTES;
+  static constexpr int P_ROW = N >= 64 ? 128 : N * 2;      // bytes of a row of a P chunk
+  static constexpr int QB = N == 128 ? 1 : 2;              // q buffers
+  static constexpr int Q_BYTES = N * D * 2;
+  static constexpr int ITEMS = N == 128 ? 2 : 4;           // piece records in flight
+  static constexpr int NR = D == 64 ? 6 : (N >= 64 ? 3 : 4);   // packed tiles in flight
+  static constexpr int NT = NR + 2;                        // their times live until the scores are done
+  static constexpr int RAW_KS = TILE * D / 2, RAW_V = RAW_KS + TILE * D / 16, RAW_VS = RAW_V + TILE * D / 2;
+  static constexpr int RAW_BYTES = 2 * RAW_V;
+  // shared memory
+  static constexpr int KP_OFF = 0;
+  static constexpr int V_OFF = KP_OFF + 2 * KP_BYTES;
+  static constexpr int Q_OFF = V_OFF + 2 * KV_BYTES;
+  static constexpr int RAW_OFF = Q_OFF + QB * Q_BYTES;
+  static constexpr int TS_OFF = RAW_OFF + NR * RAW_BYTES;
+  static constexpr int QT_OFF = TS_OFF + NT * TILE * 8;    // int64 [ITEMS][N] row times
+  static constexpr int KA_OFF = QT_OFF + ITEMS * N * 8;    // float [ITEMS][N] score factors
+  static constexpr int SLOT_OFF = KA_OFF + ITEMS * N * 4;
+  // barriers
+  static constexpr int RAWFULL = 0, RAWEMPTY = RAWFULL + NR, TSFULL = RAWEMPTY + NR, TSEMPTY = TSFULL + NT,
+                       ITEMFULL = TSEMPTY + NT, ITEMEMPTY = ITEMFULL + ITEMS, QTFULL = ITEMEMPTY + ITEMS,
+                       QFULL = QTFULL + ITEMS, QEMPTY = QFULL + QB, KREADY = QEMPTY + QB, VREADY = KREADY + 2,
+                       STEMPTY = VREADY + 2, SFULL = STEMPTY + 2, PREADY = SFULL + 2, OFULL = PREADY + 2,
+                       OEMPTY = OFULL + 2, DRAIN = OEMPTY + 2, NBAR = DRAIN + 1;
+  static constexpr int BAR_OFF = SLOT_OFF + ITEMS * 96;
+  static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
+  static constexpr int BYTES = MISC_OFF + 512;
+  static constexpr uint32_t TMEM_COLS = 4 * N;             // S 0, 1 and O 0, 1
+  static_assert(BYTES + 1024 <= (int)kMaxSmemPerCta, "one CTA's shared memory");
+};
+
+// A piece of an item, as the copy warp hands it to the other roles.
+struct __align__(16) Piece {
+  int64_t row0;       // first row of the block
+  int64_t tmin, tmax; // of the block's rows (written by the decode warps)
+  int valid;          // 0: no more pieces
+  int b, h, rows;     // rows of the block that exist
+  int L, pos0, hist;  // cached tokens; position of the block's first row; its history rows (the others are at L)
+  int tile0, tile1;   // tiles of the piece
+  int slot;           // of its sum
+};
+static_assert(sizeof(Piece) <= 96, "a slot holds a piece");
+
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity)) {
+    if (globaltimer() - t0 > 200000000ull) break;
+  }
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// the FP16 pair (a, b), a in the low half
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// 16 SiLU(z) of two scores given as w = -log2(e) z: w c / (1 + 2^w) with
+// c = -16 / log2(e).  Beyond w = 60 (z < -41) the value is zero in FP16
+// whatever it is, so w is cut there (a NaN stays one); then 1 + 2^w stays
+// below 2^61 and one reciprocal of the product serves both: the special
+// function unit does three operations a pair instead of four.
+__device__ __forceinline__ uint32_t silu_pair(float2 w) {
+  const float c = -kPScale / kLog2e;
+  const float2 t = make_float2(min_nan(w.x, 60.f), min_nan(w.y, 60.f));
+  const float2 d = __fadd2_rn(make_float2(ex2_approx(t.x), ex2_approx(t.y)), make_float2(1.f, 1.f));
+  const float r = rcp_approx(d.x * d.y);
+  const float2 u = __fmul2_rn(t, make_float2(c, c));
+  const float2 x = __fmul2_rn(u, make_float2(d.y * r, d.x * r));
+  return pack_f16(x.x, x.y);
+}
+
+// The place of 16-byte column chunk c of row r in a swizzled chunk whose rows are ROW bytes.
+template <int ROW>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  constexpr int SH = ROW == 128 ? 0 : (ROW == 64 ? 1 : 2), M = ROW / 16 - 1;
+  return (uint32_t)(r * ROW + ((c ^ ((r >> SH) & M)) << 4));
+}
+
+__device__ __forceinline__ uint32_t mul_half2(__half2 a, __half2 b) {
+  const __half2 r = __hmul2(a, b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// 8 codes (32 bits) times their scale: 8 FP16 values
+__device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s) {
+  return make_uint4(mul_half2(e2m1x2_half2<0>(w), s), mul_half2(e2m1x2_half2<1>(w), s),
+                    mul_half2(e2m1x2_half2<2>(w), s), mul_half2(e2m1x2_half2<3>(w), s));
+}
+
+// A packed tile (codes [128][D/2], scales [128][D/16]) to FP16 rows of 64
+// features a 128-byte swizzled chunk.  A thread takes 32 features of a row at
+// a time; rows from `rows` on become zeros.  With 4 threads a row (D = 128)
+// the upper two write their chunks in the order 2, 3, 0, 1, so that 8
+// neighbouring threads (2 rows) hit 8 different 16-byte banks.
+template <int D>
+__device__ __forceinline__ void decode_tile(const uint8_t* codes, const uint8_t* scales, uint8_t* out, int dw, int lane,
+                                            int rows) {
+  constexpr int SEGS = D / 32, RPW = 32 / SEGS;            // rows a warp takes at a time
+#pragma unroll
+  for (int i = 0; i < TILE / (kDecWarps * RPW); ++i) {
+    const int r = (i * kDecWarps + dw) * RPW + lane / SEGS, seg = lane % SEGS;
+    uint4 w = *reinterpret_cast<const uint4*>(codes + r * (D / 2) + seg * 16);
+    uint32_t sc = *reinterpret_cast<const uint16_t*>(scales + r * (D / 16) + seg * 2);
+    if (r >= rows) {
+      w = make_uint4(0, 0, 0, 0);
+      sc = 0;
+    }
+    const __half2 s = e4m3x2_half2(sc);
+    __half2 s0 = __low2half2(s), s1 = __high2half2(s);
+    const bool swap = SEGS == 4 && seg >= 2;
+    if (SEGS == 4) {
+      const uint4 x = w;
+      const __half2 a = s0, b = s1;
+      w.x = swap ? x.z : x.x; w.y = swap ? x.w : x.y; w.z = swap ? x.x : x.z; w.w = swap ? x.y : x.w;
+      s0 = swap ? b : a; s1 = swap ? a : b;
+    }
+    uint8_t* base = out + (seg / 2) * (TILE * 128);
+    const int c0 = (seg & 1) * 4, x2 = swap ? 2 : 0;
+    *reinterpret_cast<uint4*>(base + swz<128>(r, c0 + (0 ^ x2))) = decode8(w.x, s0);
+    *reinterpret_cast<uint4*>(base + swz<128>(r, c0 + (1 ^ x2))) = decode8(w.y, s0);
+    *reinterpret_cast<uint4*>(base + swz<128>(r, c0 + (2 ^ x2))) = decode8(w.z, s1);
+    *reinterpret_cast<uint4*>(base + swz<128>(r, c0 + (3 ^ x2))) = decode8(w.w, s1);
+  }
+}
+
+// Where the CTA's part of the work begins (found by the whole CTA at its start).
+struct Start {
+  int b, rem, items, total, quota;
+};
+
+template <int D, int N>
+__global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedParams p) {
+  using L = Cfg<D, N>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_u32 = smem_u32(smem_raw);
+  const uint32_t base_u32 = (raw_u32 + 1023u) & ~1023u;
+  uint8_t* base = smem_raw + (base_u32 - raw_u32);
+  auto bar = [&](int i) -> uint32_t { return base_u32 + L::BAR_OFF + 8u * (uint32_t)i; };
+  auto piece_at = [&](uint32_t i) -> Piece& { return *reinterpret_cast<Piece*>(base + L::SLOT_OFF + 96 * (int)i); };
+  int64_t* qt = reinterpret_cast<int64_t*>(base + L::QT_OFF);
+  float* kA = reinterpret_cast<float*>(base + L::KA_OFF);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + L::MISC_OFF + 4);
+  Start* start = reinterpret_cast<Start*>(base + L::MISC_OFF + 16);
+  int* scan = reinterpret_cast<int*>(base + L::MISC_OFF + 64);   // [2][kThreads / 32] warp sums
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::NBAR; ++i) {
+      int n = 1;
+      if ((i >= L::RAWEMPTY && i < L::TSFULL) || (i >= L::QTFULL && i < L::QEMPTY) || (i >= L::KREADY && i < L::STEMPTY))
+        n = kDecWarps;
+      else if ((i >= L::TSEMPTY && i < L::ITEMFULL) || (i >= L::PREADY && i < L::OFULL) || (i >= L::OEMPTY && i < L::DRAIN))
+        n = kEpiWarps;
+      else if (i >= L::ITEMEMPTY && i < L::QTFULL)
+        n = kDecWarps + kEpiWarps + 2;
+      else if (i == L::DRAIN)
+        n = 2;
+      mbar_init(bar(i), n);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kSWarp) {
+    tmem_alloc(smem_u32(tmem_slot), L::TMEM_COLS);
+    tmem_relinquish();
+  }
+  pdl_wait();               // what came before in the stream may have written anything read below
+  pdl_launch_dependents();  // the finishing kernel waits for this grid's end itself
+
+  // ------------------------------------------------------------- the cut
+  // Every CTA counts all sequences' tiles and finds its own beginning.
+  {
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int lo = min((int)threadIdx.x * per, p.B), hi = min(lo + per, p.B);
+    bool bad = threadIdx.x == 0 && (p.off[0] != 0 || p.off[p.B] > p.T);
+    int tiles = 0, items = 0;
+    for (int b = lo; b < hi; ++b) {
+      CachedSeq s;
+      if (!load_seq(p, b, s)) {
+        bad = true;
+        set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, b);
+        break;
+      }
+      const int blocks = (s.n + N - 1) / N;
+      for (int qb = 0; qb < blocks; ++qb) tiles += block_tiles(s, qb, N) * p.H;
+      items += blocks * p.H;
+    }
+    if (bad) set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, -1);
+    int t = tiles, it = items;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, t, o), c = __shfl_up_sync(0xffffffffu, it, o);
+      if (lane >= o) { t += a; it += c; }
+    }
+    if (lane == 31) { scan[warp] = t; scan[kThreads / 32 + warp] = it; }
+    const int any_bad = __syncthreads_or(bad);
+    int total = 0, before = t - tiles, before_items = it - items;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) { before += scan[w]; before_items += scan[kThreads / 32 + w]; }
+      total += scan[w];
+    }
+    if (any_bad) total = 0;
+    const int quota = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int first = (int)blockIdx.x * quota;
+    if (threadIdx.x == 0) {
+      start->total = total;
+      start->quota = quota;
+      if (blockIdx.x == 0) p.hdr[WS_CA_QUOTA] = any_bad ? -1 : quota;
+    }
+    const bool mine = !any_bad && first < total && before <= first && first < before + tiles;
+    if (mine || (blockIdx.x == 0 && !any_bad)) {
+      int at = before, ai = before_items;
+      bool found = false;
+      for (int b = lo; b < hi; ++b) {
+        CachedSeq s;
+        load_seq(p, b, s);
+        const int blocks = (s.n + N - 1) / N;
+        int here = 0;
+        for (int qb = 0; qb < blocks; ++qb) here += block_tiles(s, qb, N) * p.H;
+        if (blockIdx.x == 0) {
+          p.seq_tiles[b] = at;
+          p.seq_items[b] = ai;
+        }
+        if (mine && !found && first < at + here) {
+          start->b = b;
+          start->rem = first - at;
+          start->items = ai;
+          found = true;
+          if (blockIdx.x != 0) break;
+        }
+        at += here;
+        ai += blocks * p.H;
+      }
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int first = (int)blockIdx.x * start->quota;
+  const int todo = min(start->quota, start->total - first);   // <= 0: nothing to do
+
+  Watchdog wd;
+  wd.abort = abort_flag;
+  wd.err = p.hdr + WS_ERR;
+  wd.err_info = p.hdr + WS_ERR_INFO;
+  wd.limit_ns = 2000000000ull;
+  const bool timed = p.times != nullptr;
+
+  if (warp == kCopyWarp) {
+    // -------------------------------------------------- pieces, page copies
+    uint32_t it = 0, tk = 0;     // pieces, tiles so far
+    int left = todo;
+    bool ok = true;
+    int b = start->b, qb = 0, h = 0, tile = 0, items = start->items;
+    const int ppt = TILE / p.page_size;
+    const PageLayout lay(p.page_size, D);
+    CachedSeq s{};
+    int tiles = 0;
+    if (left > 0) {
+      load_seq(p, b, s);
+      int rem = start->rem;
+      tiles = block_tiles(s, qb, N);
+      while (rem >= tiles * p.H) {
+        rem -= tiles * p.H;
+        ++qb;
+        tiles = block_tiles(s, qb, N);
+      }
+      h = rem / tiles;
+      tile = rem % tiles;
+    }
+    while (ok && left > 0) {
+      const int take = min(left, tiles - tile);
+      const uint32_t sl = it % L::ITEMS;
+      if (lane == 0) ok = mbar_wait(bar(L::ITEMEMPTY + sl), ((it / L::ITEMS) & 1) ^ 1, wd, 61);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      if (lane == 0) {
+        Piece& pc = piece_at(sl);
+        const int r0 = qb * N, hist = s.n - s.m;
+        pc.row0 = s.row0 + r0;
+        pc.valid = 1;
+        pc.b = b; pc.h = h; pc.rows = min(N, s.n - r0); pc.L = s.L;
+        pc.hist = max(0, min(hist - r0, pc.rows));
+        pc.pos0 = s.L - hist + r0;
+        pc.tile0 = tile; pc.tile1 = tile + take;
+        pc.slot = items + qb * p.H + h + (int)blockIdx.x;
+        mbar_arrive(bar(L::ITEMFULL + sl));
+      }
+      __syncwarp();
+      ++it;
+      // the block table's entries, 32 at a time: lane i holds entry e0 + i
+      const int32_t* row = p.table + (int64_t)b * p.max_pages;
+      const int npages = (s.L + p.page_size - 1) / p.page_size;
+      int e0 = tile * ppt;
+      int32_t entry = e0 + lane < npages ? row[e0 + lane] : -1;
+      int32_t next = e0 + 32 + lane < npages ? row[e0 + 32 + lane] : -1;
+      for (int t = tile; ok && t < tile + take; ++t, ++tk) {
+        const int e = t * ppt;
+        if (e >= e0 + 32) {
+          e0 += 32;
+          entry = next;
+          next = e0 + 32 + lane < npages ? row[e0 + 32 + lane] : -1;
+        }
+        // lane l: part l % 5 (K codes, K scales, V codes, V scales, times) of page l / 5 of the tile
+        const int pg = lane / 5, kind = lane % 5;
+        const int id = __shfl_sync(0xffffffffu, entry, (e - e0 + min(pg, ppt - 1)) & 31);
+        const bool there = pg < ppt && e + pg < npages;
+        const bool good = there && id >= 0 && id < p.num_pages;
+        if (there && !good) set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, b);
+        const int n = __popc(__ballot_sync(0xffffffffu, good && kind == 0));
+        const uint32_t rs = tk % L::NR, ts = tk % L::NT;
+        if (lane == 0) {
+          ok = mbar_wait(bar(L::RAWEMPTY + rs), ((tk / L::NR) & 1) ^ 1, wd, 62) &&
+               (!timed || mbar_wait(bar(L::TSEMPTY + ts), ((tk / L::NT) & 1) ^ 1, wd, 63));
+          if (ok) {
+            mbar_arrive_expect_tx(bar(L::RAWFULL + rs), (uint32_t)(n * lay.bytes()));
+            if (timed) mbar_arrive_expect_tx(bar(L::TSFULL + ts), (uint32_t)(n * p.page_size * 8));
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (good) {
+          const uint8_t* src = p.pages + ((int64_t)id * p.H + h) * lay.bytes() + (kind >= 2 ? lay.half() : 0);
+          const uint32_t dst = base_u32 + L::RAW_OFF + rs * L::RAW_BYTES + (kind >= 2 ? L::RAW_V : 0);
+          const int codes = p.page_size * (D / 2), scales = p.page_size * (D / 16);
+          if (kind == 4) {
+            if (timed)
+              bulk_load(base_u32 + L::TS_OFF + ts * (TILE * 8) + pg * p.page_size * 8,
+                        p.page_times + (int64_t)id * p.page_size, (uint32_t)(p.page_size * 8), bar(L::TSFULL + ts));
+          } else if (kind & 1) {
+            bulk_load(dst + L::RAW_KS + pg * scales, src + codes, (uint32_t)scales, bar(L::RAWFULL + rs));
+          } else {
+            bulk_load(dst + pg * codes, src, (uint32_t)codes, bar(L::RAWFULL + rs));
+          }
+        }
+      }
+      if (!ok) break;
+      left -= take;
+      // the next item: next head, block, sequence
+      tile = 0;
+      if (left > 0 && ++h == p.H) {
+        h = 0;
+        do {
+          ++qb;
+          if (qb * N >= s.n) {
+            items += ((s.n + N - 1) / N) * p.H;
+            qb = 0;
+            s.n = 0;                 // some later sequence has tiles: left > 0
+            while (s.n == 0 && ++b < p.B) load_seq(p, b, s);
+            if (s.n == 0) break;
+          }
+          tiles = block_tiles(s, qb, N);
+        } while (tiles == 0);
+        if (s.n == 0) left = 0;
+      }
+    }
+    if (ok && lane == 0) {
+      const uint32_t sl = it % L::ITEMS;
+      if (mbar_wait(bar(L::ITEMEMPTY + sl), ((it / L::ITEMS) & 1) ^ 1, wd, 64)) {
+        piece_at(sl).valid = 0;
+        mbar_arrive(bar(L::ITEMFULL + sl));
+      }
+    }
+    // no copy may land in shared memory after the CTA's end
+    if (lane == 0) {
+      for (uint32_t i = 0; i < (uint32_t)L::NR; ++i)
+        if (tk > i) drain(bar(L::RAWFULL + i), ((tk - 1 - i) / L::NR) & 1);
+      for (uint32_t i = 0; timed && i < (uint32_t)L::NT; ++i)
+        if (tk > i) drain(bar(L::TSFULL + i), ((tk - 1 - i) / L::NT) & 1);
+    }
+  } else if (warp >= kDecWarp0 && warp < kDecWarp0 + kDecWarps) {
+    // --------------------------------------------------------- decoding, q
+    const int dw = warp - kDecWarp0;
+    uint32_t it = 0, tk = 0;
+    bool ok = true;
+    while (ok) {
+      const uint32_t sl = it % L::ITEMS, qbuf = it % L::QB;
+      ok = mbar_wait(bar(L::ITEMFULL + sl), (it / L::ITEMS) & 1, wd, 65);
+      if (!ok) break;
+      Piece& pc = piece_at(sl);
+      if (!pc.valid) break;
+      {
+        // q rows: D / 8 lanes a row, 8 features each
+        constexpr int LR = D / 8, RPP = kDecWarps * 32 / LR, PASSES = (N + RPP - 1) / RPP;
+        const int64_t row0 = pc.row0;
+        const int rows = pc.rows, h = pc.h;
+        const int sub = dw * 32 + lane, c = sub % LR;
+        uint4 x[PASSES];
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+          const int r = i * RPP + sub / LR;
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (r < rows) x[i] = *reinterpret_cast<const uint4*>(p.q + ((row0 + r) * p.H + h) * D + c * 8);
+        }
+        if (dw == 0) {   // the rows' times, and their range
+          int64_t mn = INT64_MAX, mx = INT64_MIN;
+          for (int r = lane; r < N; r += 32) {
+            int64_t t = 0;
+            if (timed && r < rows) {
+              t = p.times[row0 + r];
+              mn = t < mn ? t : mn;
+              mx = t > mx ? t : mx;
+            }
+            qt[sl * N + r] = t;
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const int64_t a = __shfl_xor_sync(0xffffffffu, mn, o), b2 = __shfl_xor_sync(0xffffffffu, mx, o);
+            mn = a < mn ? a : mn;
+            mx = b2 > mx ? b2 : mx;
+          }
+          if (lane == 0) {
+            pc.tmin = mn;
+            pc.tmax = mx;
+          }
+        }
+        ok = mbar_wait(bar(L::QEMPTY + qbuf), ((it / L::QB) & 1) ^ 1, wd, 66);
+        if (!ok) break;
+        uint8_t* qs = base + L::Q_OFF + qbuf * L::Q_BYTES;
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+          const int r = i * RPP + sub / LR;
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t top = 0;    // largest magnitude's bits (BF16 in the high half of FP32)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
+#pragma unroll
+          for (int o = LR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // 2^(14 - exponent); rows below 2^-100 are scaled by what 2^-100 takes
+          const int ex = max((int)(top >> 23), 27);
+          const float up = __uint_as_float((uint32_t)(127 + 14 + 127 - ex) << 23);
+          uint32_t f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = pack_f16(bf16_lo_f(w[e]) * up, bf16_hi_f(w[e]) * up);
+          if (N % RPP == 0 || r < N) {
+            *reinterpret_cast<uint4*>(qs + (c / 8) * (N * 128) + swz<128>(r, c % 8)) = make_uint4(f[0], f[1], f[2], f[3]);
+            if (c == 0) kA[sl * N + r] = -kLog2e * p.alpha * p.k_scale * __uint_as_float((uint32_t)(ex - 14) << 23);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(L::QFULL + qbuf));
+          mbar_arrive(bar(L::QTFULL + sl));
+        }
+      }
+      const int t0 = pc.tile0, t1 = pc.tile1, len = pc.L;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::ITEMEMPTY + sl));
+      ++it;
+      for (int t = t0; t < t1; ++t, ++tk) {
+        const uint32_t rs = tk % L::NR, st = tk & 1;
+        ok = mbar_wait(bar(L::RAWFULL + rs), (tk / L::NR) & 1, wd, 67) &&
+             mbar_wait(bar(L::STEMPTY + st), ((tk >> 1) & 1) ^ 1, wd, 68);
+        if (!ok) break;
+        const uint8_t* raw = base + L::RAW_OFF + rs * L::RAW_BYTES;
+        const int rows = len - t * TILE;
+        decode_tile<D>(raw, raw + L::RAW_KS, base + L::KP_OFF + st * L::KP_BYTES, dw, lane, rows);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::KREADY + st));
+        decode_tile<D>(raw + L::RAW_V, raw + L::RAW_VS, base + L::V_OFF + st * L::KV_BYTES, dw, lane, rows);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(L::VREADY + st));
+          mbar_arrive(bar(L::RAWEMPTY + rs));
+        }
+      }
+    }
+  } else if (warp == kSWarp) {
+    // ---------------------------------------------------------- S^T = K Q^T
+    if (lane == 0) {
+      constexpr uint32_t IDESC = idesc_f16(TILE, N, false, false);
+      uint32_t it = 0, tk = 0;
+      bool ok = true;
+      while (ok) {
+        const uint32_t sl = it % L::ITEMS, qbuf = it % L::QB;
+        ok = mbar_wait(bar(L::ITEMFULL + sl), (it / L::ITEMS) & 1, wd, 69);
+        if (!ok) break;
+        const Piece& pc = piece_at(sl);
+        if (!pc.valid) break;
+        const int nt = pc.tile1 - pc.tile0;
+        mbar_arrive(bar(L::ITEMEMPTY + sl));
+        ok = mbar_wait(bar(L::QFULL + qbuf), (it / L::QB) & 1, wd, 70);
+        if (!ok) break;
+        ++it;
+        const SDesc dq = sdesc_w(base_u32 + L::Q_OFF + qbuf * L::Q_BYTES, 16, 1024);
+        for (int t = 0; t < nt; ++t, ++tk) {
+          const uint32_t st = tk & 1;
+          // the S buffer of tile tk - 2 was read before its PV, which freed the tile buffer
+          ok = mbar_wait(bar(L::KREADY + st), (tk >> 1) & 1, wd, 71);
+          if (!ok) break;
+          fence_after_sync();
+          const SDesc dk = sdesc_w(base_u32 + L::KP_OFF + st * L::KP_BYTES, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss_w(tmem + st * N, dk + ((kk >> 2) * L::CHUNK + (kk & 3) * 32), dq + ((kk >> 2) * (N * 128) + (kk & 3) * 32),
+                     IDESC, kk > 0 ? 1u : 0u);
+          mma_commit(bar(L::SFULL + st));
+        }
+        if (!ok) break;
+        mma_commit(bar(L::QEMPTY + qbuf));
+      }
+      mma_commit(bar(L::DRAIN));
+      drain(bar(L::DRAIN), 0);
+    }
+  } else if (warp == kPvWarp) {
+    // --------------------------------------------------------- O^T += V^T P
+    if (lane == 0) {
+      constexpr uint32_t IDESC = idesc_f16(128, N, true, true);
+      uint32_t it = 0, tk = 0;
+      bool ok = true;
+      while (ok) {
+        const uint32_t sl = it % L::ITEMS, ob = it & 1;
+        ok = mbar_wait(bar(L::ITEMFULL + sl), (it / L::ITEMS) & 1, wd, 72);
+        if (!ok) break;
+        const Piece& pc = piece_at(sl);
+        if (!pc.valid) break;
+        const int nt = pc.tile1 - pc.tile0;
+        mbar_arrive(bar(L::ITEMEMPTY + sl));
+        ok = mbar_wait(bar(L::OEMPTY + ob), ((it >> 1) & 1) ^ 1, wd, 73);
+        if (!ok) break;
+        ++it;
+        for (int t = 0; t < nt; ++t, ++tk) {
+          const uint32_t st = tk & 1;
+          ok = mbar_wait(bar(L::VREADY + st), (tk >> 1) & 1, wd, 74) && mbar_wait(bar(L::PREADY + st), (tk >> 1) & 1, wd, 75);
+          if (!ok) break;
+          fence_after_sync();
+          // with 64 features the upper half of M reads the same features again; its rows are not used
+          const SDesc dv = sdesc_w(base_u32 + L::V_OFF + st * L::KV_BYTES, D == 128 ? L::CHUNK : 0, 1024);
+          const SDesc dp = sdesc_rows<L::P_ROW>(base_u32 + L::KP_OFF + st * L::KP_BYTES, N == 128 ? L::CHUNK : 16, 8 * L::P_ROW);
+#pragma unroll
+          for (int kk = 0; kk < TILE / 16; ++kk)
+            mma_ss_w(tmem + (2 + ob) * N, dv + kk * 2048, dp + kk * (16 * L::P_ROW), IDESC, (t > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(bar(L::STEMPTY + st));
+        }
+        if (!ok) break;
+        mma_commit(bar(L::OFULL + ob));
+      }
+      mma_commit(bar(L::DRAIN));
+      drain(bar(L::DRAIN), 0);
+    }
+  } else {
+    // -------------------------------------------------------------- scores
+    constexpr int COLS = N / 2;                    // columns of a warp
+    constexpr int CH = COLS < 32 ? COLS : 32;      // columns in registers at a time
+    const int wq = warp & 3, half = warp >> 2;
+    const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16) + half * COLS;
+    const int r = wq * 32 + lane;                  // this thread's token in a tile, and feature in O
+    uint32_t it = 0, tk = 0;
+    bool ok = true;
+    // a piece's sum is written out after the next piece's first scores
+    bool pend = false;
+    uint32_t pend_it = 0;
+    int pend_slot = 0, pend_rows = 0;
+    auto load_cols = [&](uint32_t addr, uint32_t (&v)[CH]) {
+      if constexpr (CH == 32) tmem_ld32(addr, v);
+      else if constexpr (CH == 16) tmem_ld16(addr, v);
+      else tmem_ld8(addr, v);
+    };
+    auto write_sum = [&]() -> bool {
+      const uint32_t ob = pend_it & 1;
+      if (!mbar_wait(bar(L::OFULL + ob), (pend_it >> 1) & 1, wd, 76)) return false;
+      fence_after_sync();
+      float* dst = p.part + (int64_t)pend_slot * (N * D) + r;
+#pragma unroll 1
+      for (int c0 = 0; c0 < COLS; c0 += CH) {
+        uint32_t v[CH];
+        load_cols(lane_base + (2 + ob) * N + c0, v);
+        tmem_wait_ld();
+        if (D == 128 || wq < 2) {
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+            if (half * COLS + c0 + c < pend_rows) dst[(half * COLS + c0 + c) * D] = __uint_as_float(v[c]);
+        }
+      }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::OEMPTY + ob));
+      pend = false;
+      return true;
+    };
+    while (ok) {
+      const uint32_t sl = it % L::ITEMS;
+      ok = mbar_wait(bar(L::ITEMFULL + sl), (it / L::ITEMS) & 1, wd, 77);
+      if (!ok) break;
+      const Piece& pc = piece_at(sl);
+      if (!pc.valid) break;
+      ok = mbar_wait(bar(L::QTFULL + sl), (it / L::ITEMS) & 1, wd, 78);
+      if (!ok) break;
+      const int len = pc.L, pos0 = pc.pos0, hist = pc.hist, rows = pc.rows, t0 = pc.tile0, t1 = pc.tile1, slot = pc.slot;
+      const int64_t tmin = pc.tmin, tmax = pc.tmax;
+      const int pmin = hist > 0 ? pos0 : len, pmax = hist == rows ? pos0 + rows - 1 : len;
+      const float* rp = p.rab_pos ? p.rab_pos + pc.h * p.P : nullptr;
+      const float* rt = p.rab_time ? p.rab_time + pc.h * p.Tb : nullptr;
+      const float* ka = kA + sl * N + half * COLS;
+      const int64_t* tq = qt + sl * N + half * COLS;
+      for (int t = t0; t < t1; ++t, ++tk) {
+        const uint32_t st = tk & 1, ts = tk % L::NT;
+        const int j = t * TILE + r;
+        int64_t tj = 0;
+        if (timed) {
+          ok = mbar_wait(bar(L::TSFULL + ts), (tk / L::NT) & 1, wd, 79);
+          if (!ok) break;
+          tj = *reinterpret_cast<const int64_t*>(base + L::TS_OFF + ts * (TILE * 8) + r * 8);
+        }
+        // one bias for all of the block's rows?
+        float bias = 0.f;
+        bool same = j >= len || j <= pmin;
+        if (rp) {
+          const int a = min(max(pmin - j, 0), p.P - 1), b = min(max(pmax - j, 0), p.P - 1);
+          same = same && (a == b || j >= len);
+          bias = rp[a];
+        }
+        if (rt) {
+          const int a = time_bucket(tmin, tj, p.Tb), b = time_bucket(tmax, tj, p.Tb);
+          same = same && ((a == b && (tj <= tmin || tj >= tmax)) || j >= len);
+          bias += rt[a];
+        }
+        bias *= -kLog2e;
+        const bool fast = __all_sync(0xffffffffu, same);
+        const bool whole = __all_sync(0xffffffffu, j < len);
+        ok = mbar_wait(bar(L::SFULL + st), (tk >> 1) & 1, wd, 80);
+        if (!ok) break;
+        fence_after_sync();
+        uint8_t* ps = base + L::KP_OFF + st * L::KP_BYTES;
+#pragma unroll 1
+        for (int c0 = 0; c0 < COLS; c0 += CH) {
+          uint32_t v[CH];
+          load_cols(lane_base + st * N + c0, v);
+          tmem_wait_ld();
+          uint32_t h2[CH / 2];
+          if (fast) {
+            const float2 b2 = make_float2(bias, bias);
+#pragma unroll
+            for (int c = 0; c < CH; c += 4) {
+              const float4 k4 = *reinterpret_cast<const float4*>(ka + c0 + c);
+              h2[c / 2] = silu_pair(__ffma2_rn(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
+                                               make_float2(k4.x, k4.y), b2));
+              h2[c / 2 + 1] = silu_pair(__ffma2_rn(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])),
+                                                   make_float2(k4.z, k4.w), b2));
+            }
+            if (!whole) {
+#pragma unroll
+              for (int c = 0; c < CH / 2; ++c) h2[c] = j < len ? h2[c] : 0u;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < CH; c += 2) {
+              float w[2];
+              uint32_t keep = 0;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int col = half * COLS + c0 + c + e;
+                const int pos = col < hist ? pos0 + col : len;
+                float bb = 0.f;
+                if (rp) bb = rp[min(max(pos - j, 0), p.P - 1)];
+                if (rt) bb += rt[time_bucket(tq[c0 + c + e], tj, p.Tb)];
+                w[e] = fmaf(__uint_as_float(v[c + e]), ka[c0 + c + e], -kLog2e * bb);
+                keep |= (j <= pos && j < len) ? 0xffffu << (16 * e) : 0u;
+              }
+              h2[c / 2] = silu_pair(make_float2(w[0], w[1])) & keep;
+            }
+          }
+          // P over K: row = token, 16-byte chunks of 8 columns
+#pragma unroll
+          for (int c = 0; c < CH / 8; ++c) {
+            const int col = half * COLS + c0 + c * 8;
+            const uint32_t at = N >= 64 ? (col / 64) * L::CHUNK + swz<L::P_ROW>(r, (col % 64) / 8) : swz<L::P_ROW>(r, col / 8);
+            *reinterpret_cast<uint4*>(ps + at) = make_uint4(h2[4 * c], h2[4 * c + 1], h2[4 * c + 2], h2[4 * c + 3]);
+          }
+        }
+        fence_before_sync();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(L::PREADY + st));
+          if (timed) mbar_arrive(bar(L::TSEMPTY + ts));
+        }
+        if (pend) {
+          ok = write_sum();
+          if (!ok) break;
+        }
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::ITEMEMPTY + sl));
+      pend = true;
+      pend_it = it;
+      pend_slot = slot;
+      pend_rows = rows;
+      ++it;
+    }
+    if (ok && pend) write_sum();
+  }
+
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == kSWarp) tmem_dealloc(tmem, L::TMEM_COLS);
+}
+
+template <int D, int N>
+cudaError_t launch_t(const CachedParams& p, int ctas, cudaStream_t st) {
+  const size_t smem = Cfg<D, N>::BYTES + 1024;
+  auto kern = cached_tc_kernel<D, N>;
+  const void* fn = reinterpret_cast<const void*>(kern);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, st, p);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    set_launch_detail(e, "cached_tc_kernel", fn, kThreads, smem);
+  }
+  return e;
+}
+
+}  // namespace
+
+// A block is as wide as the longest sequence's rows ask for.
+int cached_block_rows(int max_rows) { return max_rows <= 16 ? 16 : (max_rows <= 32 ? 32 : (max_rows <= 64 ? 64 : 128)); }
+
+cudaError_t launch_tc_cached(const CachedParams& p, int d, int N, int ctas, cudaStream_t st) {
+  if (d == 128)
+    return N == 16 ? launch_t<128, 16>(p, ctas, st) : N == 32 ? launch_t<128, 32>(p, ctas, st)
+         : N == 64 ? launch_t<128, 64>(p, ctas, st) : launch_t<128, 128>(p, ctas, st);
+  return N == 16 ? launch_t<64, 16>(p, ctas, st) : N == 32 ? launch_t<64, 32>(p, ctas, st)
+       : N == 64 ? launch_t<64, 64>(p, ctas, st) : launch_t<64, 128>(p, ctas, st);
+}
+
+}  // namespace hstu

@@ -110,6 +110,14 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// Untiled copy of `bytes` (a multiple of 16, both addresses 16-byte aligned)
+// into shared memory, completion counted on an mbarrier (bytes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 // L2 prefetch of a 2-D tile (no shared-memory destination, no completion
 // to wait for): a later TMA load of the same box then finds it in L2.
 // Same coordinate rules as the loads.
@@ -326,6 +334,22 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major,
          ((b_mn_major ? 1u : 0u) << 16) |              // B major
          ((uint32_t)(N >> 3) << 17) |                  // N / 8
          ((uint32_t)(M >> 4) << 24);                   // M / 16
+}
+
+// The same with FP16 A and B.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return idesc_bf16(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
+// A shared-memory descriptor like sdesc_w for rows of 128, 64 or 32 bytes,
+// swizzled over the row's whole width (swizzle modes 2, 4 and 6).
+template <int ROW_BYTES>
+__device__ __forceinline__ SDesc sdesc_rows(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  static_assert(ROW_BYTES == 128 || ROW_BYTES == 64 || ROW_BYTES == 32, "swizzle widths");
+  constexpr uint32_t mode = ROW_BYTES == 128 ? 2u : (ROW_BYTES == 64 ? 4u : 6u);
+  SDesc d = sdesc_w(saddr, lbo, sbo);
+  d.hi = (d.hi & 0x1fffffffu) | (mode << 29);
+  return d;
 }
 
 // bf16x2 pack: low half = lo, high half = hi (round to nearest even)
