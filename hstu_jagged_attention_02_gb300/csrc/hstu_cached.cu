@@ -240,7 +240,9 @@ hstu_status_t hstu_attn_fwd_cached(const hstu_attn_desc* d, const hstu_cache_des
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = launch_tc_cached(p, c->d, N, sms < kMaxCtas ? sms : kMaxCtas, st);
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  if (e == cudaSuccess)
+    e = N <= 16 ? launch_stream_cached(p, c->d, N, ctas, st) : launch_tc_cached(p, c->d, N, ctas, st);
   if (e == cudaSuccess) {
     const dim3 grid((unsigned)d->total_tokens);
     const bool few = d->total_tokens <= sms;

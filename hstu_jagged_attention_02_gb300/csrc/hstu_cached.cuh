@@ -71,7 +71,196 @@ __device__ __forceinline__ int block_tiles(const CachedSeq& s, int qb, int N) {
   return (seen + kCachedTile - 1) / kCachedTile;
 }
 
-int cached_block_rows(int max_rows);                 // N of a call
+// Where a CTA's part of the work begins.
+struct Start {
+  int b, rem;         // sequence, and tiles of it that belong to CTAs before
+  int items;          // items before the sequence
+  int total, quota;   // tiles in all (0 where the batch is refused), tiles a CTA
+};
+
+// Every CTA counts all sequences' tiles and finds its own beginning; CTA 0
+// also writes the counts for the finishing kernel.  scan: 2 x THREADS / 32
+// ints in shared memory; the caller synchronises before it reads start.
+template <int THREADS>
+__device__ __forceinline__ void cut_work(const CachedParams& p, int N, int* scan, Start* start) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (p.B + THREADS - 1) / THREADS;
+  const int lo = min((int)threadIdx.x * per, p.B), hi = min(lo + per, p.B);
+  bool bad = threadIdx.x == 0 && (p.off[0] != 0 || p.off[p.B] > p.T);
+  int tiles = 0, items = 0;
+  for (int b = lo; b < hi; ++b) {
+    CachedSeq s;
+    if (!load_seq(p, b, s)) {
+      bad = true;
+      set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, b);
+      break;
+    }
+    const int blocks = (s.n + N - 1) / N;
+    for (int qb = 0; qb < blocks; ++qb) tiles += block_tiles(s, qb, N) * p.H;
+    items += blocks * p.H;
+  }
+  if (bad) set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, -1);
+  int t = tiles, it = items;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, t, o), c = __shfl_up_sync(0xffffffffu, it, o);
+    if (lane >= o) { t += a; it += c; }
+  }
+  if (lane == 31) { scan[warp] = t; scan[THREADS / 32 + warp] = it; }
+  const int any_bad = __syncthreads_or(bad);
+  int total = 0, before = t - tiles, before_items = it - items;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) { before += scan[w]; before_items += scan[THREADS / 32 + w]; }
+    total += scan[w];
+  }
+  if (any_bad) total = 0;
+  const int quota = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int first = (int)blockIdx.x * quota;
+  if (threadIdx.x == 0) {
+    start->total = total;
+    start->quota = quota;
+    if (blockIdx.x == 0) p.hdr[WS_CA_QUOTA] = any_bad ? -1 : quota;
+  }
+  const bool mine = !any_bad && first < total && before <= first && first < before + tiles;
+  if (mine || (blockIdx.x == 0 && !any_bad)) {
+    int at = before, ai = before_items;
+    bool found = false;
+    for (int b = lo; b < hi; ++b) {
+      CachedSeq s;
+      load_seq(p, b, s);
+      const int blocks = (s.n + N - 1) / N;
+      int here = 0;
+      for (int qb = 0; qb < blocks; ++qb) here += block_tiles(s, qb, N) * p.H;
+      if (blockIdx.x == 0) {
+        p.seq_tiles[b] = at;
+        p.seq_items[b] = ai;
+      }
+      if (mine && !found && first < at + here) {
+        start->b = b;
+        start->rem = first - at;
+        start->items = ai;
+        found = true;
+        if (blockIdx.x != 0) break;
+      }
+      at += here;
+      ai += blocks * p.H;
+    }
+  }
+}
+
+// A CTA's walk over its pieces: every thread that calls it sees the same.
+struct Walk {
+  CachedSeq s;
+  int b, qb, h, tile, tiles, items, left;
+
+  __device__ __forceinline__ void begin(const CachedParams& p, const Start& st, int N) {
+    const int first = (int)blockIdx.x * st.quota;
+    left = min(st.quota, st.total - first);
+    b = st.b; items = st.items; qb = 0; h = 0; tile = 0; tiles = 0;
+    if (left <= 0) return;
+    load_seq(p, b, s);
+    int rem = st.rem;
+    tiles = block_tiles(s, qb, N);
+    while (rem >= tiles * p.H) {
+      rem -= tiles * p.H;
+      ++qb;
+      tiles = block_tiles(s, qb, N);
+    }
+    h = rem / tiles;
+    tile = rem % tiles;
+  }
+  // the piece at hand: tiles [tile, tile + take())
+  __device__ __forceinline__ int take() const { return min(left, tiles - tile); }
+  __device__ __forceinline__ int slot(const CachedParams& p) const { return items + qb * p.H + h + (int)blockIdx.x; }
+  __device__ __forceinline__ void next(const CachedParams& p, int N) {
+    left -= take();
+    tile = 0;
+    if (left <= 0 || ++h < p.H) return;
+    h = 0;
+    do {
+      ++qb;
+      if (qb * N >= s.n) {
+        items += ((s.n + N - 1) / N) * p.H;
+        qb = 0;
+        s.n = 0;                 // some later sequence has tiles: left > 0
+        while (s.n == 0 && ++b < p.B) load_seq(p, b, s);
+        if (s.n == 0) {
+          left = 0;
+          return;
+        }
+      }
+      tiles = block_tiles(s, qb, N);
+    } while (tiles == 0);
+  }
+};
+
+// --------------------------------------------------------------- arithmetic
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kPScale = 16.f;   // on the scores, against FP16's range
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// the FP16 pair (a, b), a in the low half
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// 16 SiLU(z) of two scores given as w = -log2(e) z: w c / (1 + 2^w) with
+// c = -16 / log2(e).  Beyond w = 60 (z < -41) the value is zero in FP16
+// whatever it is, so w is cut there (a NaN stays one); then 1 + 2^w stays
+// below 2^61 and one reciprocal of the product serves both: the special
+// function unit does three operations a pair instead of four.
+__device__ __forceinline__ uint32_t silu_pair(float2 w) {
+  const float c = -kPScale / kLog2e;
+  const float2 t = make_float2(min_nan(w.x, 60.f), min_nan(w.y, 60.f));
+  const float2 d = __fadd2_rn(make_float2(ex2_approx(t.x), ex2_approx(t.y)), make_float2(1.f, 1.f));
+  const float r = rcp_approx(d.x * d.y);
+  const float2 u = __fmul2_rn(t, make_float2(c, c));
+  const float2 x = __fmul2_rn(u, make_float2(d.y * r, d.x * r));
+  return pack_f16(x.x, x.y);
+}
+
+// The power of two that brings a q row whose largest magnitude has the bits
+// `top` (FP32) to [2^14, 2^15), and its inverse; rows below 2^-100 take
+// what 2^-100 takes.  FP16 then holds the BF16 row exactly down to 2^-28 of
+// its largest feature.
+__device__ __forceinline__ float row_scale(uint32_t top, float& down) {
+  const int ex = max((int)(top >> 23), 27);
+  down = __uint_as_float((uint32_t)(ex - 14) << 23);
+  return __uint_as_float((uint32_t)(127 + 14 + 127 - ex) << 23);
+}
+
+__device__ __forceinline__ uint32_t mul_half2(__half2 a, __half2 b) {
+  const __half2 r = __hmul2(a, b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// 8 codes (32 bits) times their scale: 8 FP16 values
+__device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s) {
+  return make_uint4(mul_half2(e2m1x2_half2<0>(w), s), mul_half2(e2m1x2_half2<1>(w), s),
+                    mul_half2(e2m1x2_half2<2>(w), s), mul_half2(e2m1x2_half2<3>(w), s));
+}
+
+// Rows of a block: as few as the longest sequence asks for.  Up to 16 rows go
+// through the streaming kernel, more through the tensor-memory one.
+inline int cached_block_rows(int max_rows) {
+  return max_rows <= 8 ? 8 : (max_rows <= 16 ? 16 : (max_rows <= 32 ? 32 : (max_rows <= 64 ? 64 : 128)));
+}
+cudaError_t launch_stream_cached(const CachedParams& p, int d, int N, int ctas, cudaStream_t st);
 cudaError_t launch_tc_cached(const CachedParams& p, int d, int N, int ctas, cudaStream_t st);
 
 }  // namespace hstu

@@ -40,8 +40,6 @@ constexpr int TILE = kCachedTile;
 constexpr int kEpiWarps = 8, kDecWarps = 8;
 constexpr int kDecWarp0 = 8, kCopyWarp = 16, kSWarp = 17, kPvWarp = 18;
 constexpr int kThreads = 19 * 32;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kPScale = 16.f;
 
 template <int D, int N>
 struct Cfg {
@@ -99,58 +97,11 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
   }
 }
 
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-// the FP16 pair (a, b), a in the low half
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
-
-// 16 SiLU(z) of two scores given as w = -log2(e) z: w c / (1 + 2^w) with
-// c = -16 / log2(e).  Beyond w = 60 (z < -41) the value is zero in FP16
-// whatever it is, so w is cut there (a NaN stays one); then 1 + 2^w stays
-// below 2^61 and one reciprocal of the product serves both: the special
-// function unit does three operations a pair instead of four.
-__device__ __forceinline__ uint32_t silu_pair(float2 w) {
-  const float c = -kPScale / kLog2e;
-  const float2 t = make_float2(min_nan(w.x, 60.f), min_nan(w.y, 60.f));
-  const float2 d = __fadd2_rn(make_float2(ex2_approx(t.x), ex2_approx(t.y)), make_float2(1.f, 1.f));
-  const float r = rcp_approx(d.x * d.y);
-  const float2 u = __fmul2_rn(t, make_float2(c, c));
-  const float2 x = __fmul2_rn(u, make_float2(d.y * r, d.x * r));
-  return pack_f16(x.x, x.y);
-}
-
 // The place of 16-byte column chunk c of row r in a swizzled chunk whose rows are ROW bytes.
 template <int ROW>
 __device__ __forceinline__ uint32_t swz(int r, int c) {
   constexpr int SH = ROW == 128 ? 0 : (ROW == 64 ? 1 : 2), M = ROW / 16 - 1;
   return (uint32_t)(r * ROW + ((c ^ ((r >> SH) & M)) << 4));
-}
-
-__device__ __forceinline__ uint32_t mul_half2(__half2 a, __half2 b) {
-  const __half2 r = __hmul2(a, b);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-// 8 codes (32 bits) times their scale: 8 FP16 values
-__device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s) {
-  return make_uint4(mul_half2(e2m1x2_half2<0>(w), s), mul_half2(e2m1x2_half2<1>(w), s),
-                    mul_half2(e2m1x2_half2<2>(w), s), mul_half2(e2m1x2_half2<3>(w), s));
 }
 
 // A packed tile (codes [128][D/2], scales [128][D/16]) to FP16 rows of 64
@@ -188,11 +139,6 @@ __device__ __forceinline__ void decode_tile(const uint8_t* codes, const uint8_t*
     *reinterpret_cast<uint4*>(base + swz<128>(r, c0 + (3 ^ x2))) = decode8(w.w, s1);
   }
 }
-
-// Where the CTA's part of the work begins (found by the whole CTA at its start).
-struct Start {
-  int b, rem, items, total, quota;
-};
 
 template <int D, int N>
 __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedParams p) {
@@ -234,78 +180,11 @@ __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedP
   pdl_wait();               // what came before in the stream may have written anything read below
   pdl_launch_dependents();  // the finishing kernel waits for this grid's end itself
 
-  // ------------------------------------------------------------- the cut
-  // Every CTA counts all sequences' tiles and finds its own beginning.
-  {
-    const int per = (p.B + kThreads - 1) / kThreads;
-    const int lo = min((int)threadIdx.x * per, p.B), hi = min(lo + per, p.B);
-    bool bad = threadIdx.x == 0 && (p.off[0] != 0 || p.off[p.B] > p.T);
-    int tiles = 0, items = 0;
-    for (int b = lo; b < hi; ++b) {
-      CachedSeq s;
-      if (!load_seq(p, b, s)) {
-        bad = true;
-        set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, b);
-        break;
-      }
-      const int blocks = (s.n + N - 1) / N;
-      for (int qb = 0; qb < blocks; ++qb) tiles += block_tiles(s, qb, N) * p.H;
-      items += blocks * p.H;
-    }
-    if (bad) set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, -1);
-    int t = tiles, it = items;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, t, o), c = __shfl_up_sync(0xffffffffu, it, o);
-      if (lane >= o) { t += a; it += c; }
-    }
-    if (lane == 31) { scan[warp] = t; scan[kThreads / 32 + warp] = it; }
-    const int any_bad = __syncthreads_or(bad);
-    int total = 0, before = t - tiles, before_items = it - items;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) { before += scan[w]; before_items += scan[kThreads / 32 + w]; }
-      total += scan[w];
-    }
-    if (any_bad) total = 0;
-    const int quota = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-    const int first = (int)blockIdx.x * quota;
-    if (threadIdx.x == 0) {
-      start->total = total;
-      start->quota = quota;
-      if (blockIdx.x == 0) p.hdr[WS_CA_QUOTA] = any_bad ? -1 : quota;
-    }
-    const bool mine = !any_bad && first < total && before <= first && first < before + tiles;
-    if (mine || (blockIdx.x == 0 && !any_bad)) {
-      int at = before, ai = before_items;
-      bool found = false;
-      for (int b = lo; b < hi; ++b) {
-        CachedSeq s;
-        load_seq(p, b, s);
-        const int blocks = (s.n + N - 1) / N;
-        int here = 0;
-        for (int qb = 0; qb < blocks; ++qb) here += block_tiles(s, qb, N) * p.H;
-        if (blockIdx.x == 0) {
-          p.seq_tiles[b] = at;
-          p.seq_items[b] = ai;
-        }
-        if (mine && !found && first < at + here) {
-          start->b = b;
-          start->rem = first - at;
-          start->items = ai;
-          found = true;
-          if (blockIdx.x != 0) break;
-        }
-        at += here;
-        ai += blocks * p.H;
-      }
-    }
-  }
+  cut_work<kThreads>(p, N, scan, start);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int first = (int)blockIdx.x * start->quota;
-  const int todo = min(start->quota, start->total - first);   // <= 0: nothing to do
 
   Watchdog wd;
   wd.abort = abort_flag;
@@ -317,41 +196,28 @@ __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedP
   if (warp == kCopyWarp) {
     // -------------------------------------------------- pieces, page copies
     uint32_t it = 0, tk = 0;     // pieces, tiles so far
-    int left = todo;
     bool ok = true;
-    int b = start->b, qb = 0, h = 0, tile = 0, items = start->items;
     const int ppt = TILE / p.page_size;
     const PageLayout lay(p.page_size, D);
-    CachedSeq s{};
-    int tiles = 0;
-    if (left > 0) {
-      load_seq(p, b, s);
-      int rem = start->rem;
-      tiles = block_tiles(s, qb, N);
-      while (rem >= tiles * p.H) {
-        rem -= tiles * p.H;
-        ++qb;
-        tiles = block_tiles(s, qb, N);
-      }
-      h = rem / tiles;
-      tile = rem % tiles;
-    }
-    while (ok && left > 0) {
-      const int take = min(left, tiles - tile);
+    Walk w;
+    w.begin(p, *start, N);
+    while (ok && w.left > 0) {
+      const int take = w.take(), tile = w.tile, b = w.b, h = w.h;
+      const CachedSeq s = w.s;
       const uint32_t sl = it % L::ITEMS;
       if (lane == 0) ok = mbar_wait(bar(L::ITEMEMPTY + sl), ((it / L::ITEMS) & 1) ^ 1, wd, 61);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       if (lane == 0) {
         Piece& pc = piece_at(sl);
-        const int r0 = qb * N, hist = s.n - s.m;
+        const int r0 = w.qb * N, hist = s.n - s.m;
         pc.row0 = s.row0 + r0;
         pc.valid = 1;
         pc.b = b; pc.h = h; pc.rows = min(N, s.n - r0); pc.L = s.L;
         pc.hist = max(0, min(hist - r0, pc.rows));
         pc.pos0 = s.L - hist + r0;
         pc.tile0 = tile; pc.tile1 = tile + take;
-        pc.slot = items + qb * p.H + h + (int)blockIdx.x;
+        pc.slot = w.slot(p);
         mbar_arrive(bar(L::ITEMFULL + sl));
       }
       __syncwarp();
@@ -403,24 +269,7 @@ __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedP
         }
       }
       if (!ok) break;
-      left -= take;
-      // the next item: next head, block, sequence
-      tile = 0;
-      if (left > 0 && ++h == p.H) {
-        h = 0;
-        do {
-          ++qb;
-          if (qb * N >= s.n) {
-            items += ((s.n + N - 1) / N) * p.H;
-            qb = 0;
-            s.n = 0;                 // some later sequence has tiles: left > 0
-            while (s.n == 0 && ++b < p.B) load_seq(p, b, s);
-            if (s.n == 0) break;
-          }
-          tiles = block_tiles(s, qb, N);
-        } while (tiles == 0);
-        if (s.n == 0) left = 0;
-      }
+      w.next(p, N);
     }
     if (ok && lane == 0) {
       const uint32_t sl = it % L::ITEMS;
@@ -494,15 +343,14 @@ __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedP
           for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
 #pragma unroll
           for (int o = LR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          // 2^(14 - exponent); rows below 2^-100 are scaled by what 2^-100 takes
-          const int ex = max((int)(top >> 23), 27);
-          const float up = __uint_as_float((uint32_t)(127 + 14 + 127 - ex) << 23);
+          float down;
+          const float up = row_scale(top, down);
           uint32_t f[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) f[e] = pack_f16(bf16_lo_f(w[e]) * up, bf16_hi_f(w[e]) * up);
           if (N % RPP == 0 || r < N) {
             *reinterpret_cast<uint4*>(qs + (c / 8) * (N * 128) + swz<128>(r, c % 8)) = make_uint4(f[0], f[1], f[2], f[3]);
-            if (c == 0) kA[sl * N + r] = -kLog2e * p.alpha * p.k_scale * __uint_as_float((uint32_t)(ex - 14) << 23);
+            if (c == 0) kA[sl * N + r] = -kLog2e * p.alpha * p.k_scale * down;
           }
         }
         fence_proxy_async_smem();
@@ -785,15 +633,10 @@ cudaError_t launch_t(const CachedParams& p, int ctas, cudaStream_t st) {
 
 }  // namespace
 
-// A block is as wide as the longest sequence's rows ask for.
-int cached_block_rows(int max_rows) { return max_rows <= 16 ? 16 : (max_rows <= 32 ? 32 : (max_rows <= 64 ? 64 : 128)); }
-
 cudaError_t launch_tc_cached(const CachedParams& p, int d, int N, int ctas, cudaStream_t st) {
   if (d == 128)
-    return N == 16 ? launch_t<128, 16>(p, ctas, st) : N == 32 ? launch_t<128, 32>(p, ctas, st)
-         : N == 64 ? launch_t<128, 64>(p, ctas, st) : launch_t<128, 128>(p, ctas, st);
-  return N == 16 ? launch_t<64, 16>(p, ctas, st) : N == 32 ? launch_t<64, 32>(p, ctas, st)
-       : N == 64 ? launch_t<64, 64>(p, ctas, st) : launch_t<64, 128>(p, ctas, st);
+    return N == 32 ? launch_t<128, 32>(p, ctas, st) : N == 64 ? launch_t<128, 64>(p, ctas, st) : launch_t<128, 128>(p, ctas, st);
+  return N == 32 ? launch_t<64, 32>(p, ctas, st) : N == 64 ? launch_t<64, 64>(p, ctas, st) : launch_t<64, 128>(p, ctas, st);
 }
 
 }  // namespace hstu
