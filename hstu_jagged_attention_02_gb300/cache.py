@@ -10,7 +10,7 @@ import torch
 
 from . import binding as C
 from .attention import _ptr
-from .qk import _need, _on, _rows, _same_device, _stream_of
+from .qk import Launch, _need, _rows, _same_device, device_error
 
 
 class PagedCache:
@@ -70,9 +70,11 @@ class _Call:
         _need(workspace.device == self.device and workspace.dtype == torch.uint8, "workspace must be uint8 on the cache's device")
         self.ws, self.ws_bytes = workspace, workspace.numel()
 
+    def _prepare(self, name, *args):
+        self._launch = Launch(self.device, getattr(C.load(), name), name, *args, self.ws.data_ptr(), self.ws_bytes)
+
     def device_error(self, stream=None) -> int:
-        with _on(self.device):
-            return C.hstu_get_device_error(self.ws.data_ptr(), _stream_of(self.device, stream))
+        return device_error(self.device, self.ws, stream)
 
 
 class AppendProblem(_Call):
@@ -111,10 +113,10 @@ class AppendProblem(_Call):
         a.seq_offsets, a.cache_lens, a.block_table = _ptr(seq_offsets), _ptr(cache_lens), _ptr(block_table)
         a.token_times, a.cos, a.sin, a.k_gain, a.k, a.v = (_ptr(t) for t in (timestamps, cos, sin, k_gain, self.k, self.v))
         self.args = a
+        self._prepare("hstu_cache_append", self.desc, self.args)
 
     def run(self, stream=None):
-        with _on(self.device):
-            C.hstu_cache_append(self.desc, self.args, self.ws.data_ptr(), self.ws_bytes, _stream_of(self.device, stream))
+        self._launch(stream)
 
 
 class ReadProblem(_Call):
@@ -138,10 +140,10 @@ class ReadProblem(_Call):
         a.seq_offsets, a.starts, a.block_table = _ptr(seq_offsets), _ptr(starts), _ptr(block_table)
         a.k, a.v, a.token_times = _ptr(self.k), _ptr(self.v), _ptr(self.timestamps)
         self.args = a
+        self._prepare("hstu_cache_read", self.desc, self.args)
 
     def run(self, stream=None):
-        with _on(self.device):
-            C.hstu_cache_read(self.desc, self.args, self.ws.data_ptr(), self.ws_bytes, _stream_of(self.device, stream))
+        self._launch(stream)
 
 
 class CachedProblem(_Call):
@@ -187,11 +189,10 @@ class CachedProblem(_Call):
         a.row_times, a.rab_pos, a.rab_time = _ptr(timestamps), _ptr(rab_pos), _ptr(rab_time)
         a.q, a.k, a.v, a.u, a.o, a.y = (_ptr(t) for t in (self.q, self.k, self.v, self.u, self.o, self.y))
         self.args = a
+        self._prepare("hstu_attn_fwd_cached", self.desc, self.cache_desc, self.args)
 
     def forward(self, stream=None):
-        with _on(self.device):
-            C.hstu_attn_fwd_cached(self.desc, self.cache_desc, self.args, self.ws.data_ptr(), self.ws_bytes,
-                                   _stream_of(self.device, stream))
+        self._launch(stream)
 
 
 def hstu_cache_append(cache: PagedCache, k, v, seq_offsets, cache_lens, block_table, **kw) -> None:

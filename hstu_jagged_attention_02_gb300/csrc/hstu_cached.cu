@@ -10,7 +10,7 @@
 // cache have many pieces each (one for every CTA that held a part), so there
 // kGroups groups of threads share them and add their sums in shared memory.
 #include "hstu_cached.cuh"
-#include "hstu_vec.cuh"
+#include "hstu_rows.cuh"
 
 namespace hstu {
 

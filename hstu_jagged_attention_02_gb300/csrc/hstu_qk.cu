@@ -4,21 +4,21 @@
 //   angle of the token's position; backward: the incoming gradient turned
 //   back, e = dout R^T, then dgain += e x r and dx = r (e g - x r mean(e g x r)).
 //
-// HBM-bound: every row of d features is read once (backward: twice, x and
-// dout) and written once, in a handful of FP32 operations a feature.  So a
-// lane holds 4 neighbouring features (8 bytes BF16, 16 bytes FP32), d / 4
-// lanes hold a row, and a warp has kRows rows of one token in flight: the
-// tables' 4 cosines and sines are loaded once for all of them.  The row's sum
-// goes over d / 4 lanes by shuffles.  Pairs of halves sit rot_dim / 8 lanes
-// apart (4 shuffles a row), neighbouring pairs in the lane itself.
+// HBM-bound: every row of d features is read once (backward: x and dout)
+// and written once, so what counts is to spend few instructions a byte and to
+// have many loads in flight.  d / 8 lanes hold a row, so that a warp's pass
+// covers 256 features, the row's sum takes few shuffles, and both features of
+// every pair lie in one lane (hstu_rows.cuh): the rotation exchanges nothing.
+// A warp takes up to kPasses passes (heads) of one token, all loads first; the
+// token's cosines and sines are loaded once for them.
 //
-// The backward's gain gradients are sums over all tokens and heads.  One CTA
-// an SM walks tokens and keeps per-lane FP32 partial sums; the CTAs' rows of
+// The backward's gain gradients are sums over all tokens and heads.  The
+// CTAs walk tokens and keep per-lane FP32 partial sums; the CTAs' rows of
 // partial sums land in the workspace and the CTA that finishes last (a
 // counter in the workspace's header) adds them up in row order in FP64, so
 // the result does not depend on the order in which CTAs finish.
 #include "hstu_internal.h"
-#include "hstu_vec.cuh"
+#include "hstu_rows.cuh"
 
 namespace hstu {
 
@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kQkThreads = 256;
 constexpr int kBwdThreads = 512;
+constexpr int kPasses = 4;
 
 struct QkParams {
   const int64_t* num_tokens;
@@ -46,67 +47,6 @@ struct QkParams {
   float eps;
 };
 
-// The 4 cosines and sines of a lane's features [f, f + 4), already signed for
-// the turn: out = w * c + partner * s.
-struct Turn {
-  float c[4], s[4];
-};
-
-// dir +1 turns by the position's angle, -1 back (the backward).
-__device__ __forceinline__ Turn load_turn(const QkParams& p, int64_t pos, int f, float dir) {
-  Turn t;
-  if (f >= p.rot) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) { t.c[e] = 1.f; t.s[e] = 0.f; }
-    return t;
-  }
-  const int half = p.rot >> 1;
-  const float* cr = p.cos + pos * half;
-  const float* sr = p.sin + pos * half;
-  if (p.interleaved) {
-    const float2 c = *reinterpret_cast<const float2*>(cr + (f >> 1));
-    const float2 s = *reinterpret_cast<const float2*>(sr + (f >> 1));
-    t.c[0] = t.c[1] = c.x; t.c[2] = t.c[3] = c.y;
-    t.s[0] = -dir * s.x; t.s[1] = dir * s.x; t.s[2] = -dir * s.y; t.s[3] = dir * s.y;
-  } else {
-    const bool second = f >= half;
-    const int i = second ? f - half : f;
-    const float4 c = *reinterpret_cast<const float4*>(cr + i);
-    const float4 s = *reinterpret_cast<const float4*>(sr + i);
-    const float g = second ? dir : -dir;
-    t.c[0] = c.x; t.c[1] = c.y; t.c[2] = c.z; t.c[3] = c.w;
-    t.s[0] = g * s.x; t.s[1] = g * s.y; t.s[2] = g * s.z; t.s[3] = g * s.w;
-  }
-  return t;
-}
-
-// w turned in place; every lane of the warp takes part
-__device__ __forceinline__ void turn(const Turn& t, bool interleaved, int partner, float (&w)[4]) {
-  float o[4];
-  if (interleaved) {
-    o[0] = w[1]; o[1] = w[0]; o[2] = w[3]; o[3] = w[2];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = __shfl_sync(0xffffffffu, w[e], partner);
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = fmaf(w[e], t.c[e], o[e] * t.s[e]);
-}
-
-template <int LANES>
-__device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// The lane that holds the other halves of this lane's pairs.
-template <int LANES>
-__device__ __forceinline__ int partner_lane(int lane, int rot) {
-  const int l = lane % LANES, h = rot >> 3;   // 4 features a lane
-  return lane - l + (l < h ? l + h : (l < 2 * h ? l - h : l));
-}
-
 // The position's row in the tables; one outside them is recorded and row 0 taken.
 __device__ __forceinline__ int64_t checked_position(const QkParams& p, int64_t t) {
   if (p.rot == 0) return 0;
@@ -126,114 +66,161 @@ __device__ __forceinline__ int64_t live_tokens(const QkParams& p) {
   return n;
 }
 
-// A warp takes kRows x (128 / D) heads of one token.
-template <typename TI, int D, int kRows>
-__global__ void __launch_bounds__(kQkThreads) qk_fwd_kernel(const __grid_constant__ QkParams p, int chunks) {
-  constexpr int LANES = D / 4, PER = 32 / LANES;
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = unit / chunks;
-  const int first = (int)(unit - t * chunks) * kRows * PER;
-  const int heads = p.H[0] + p.H[1];
-  if (t >= live_tokens(p)) return;
-  const int f = (lane % LANES) * 4;
-  float x[kRows][4];
+// The lane's cosines and sines (dir -1: turned back, the backward).
+__device__ __forceinline__ void load_angles(const QkParams& p, const Parts& pt, int64_t pos, int l, float dir, float (&c)[4],
+                                            float (&s)[4]) {
+  if (pt.turns) {
+    const int64_t at = pos * (p.rot >> 1) + 4 * l;
+    load4(p.cos + at, c);
+    load4(p.sin + at, s);
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const int hh = first + r * PER + lane / LANES;
-    const int w = hh >= p.H[0];
-    if (hh < heads)
-      load4(static_cast<const TI*>(p.x[w]) + t * p.xs[w][0] + (int64_t)(hh - (w ? p.H[0] : 0)) * p.xs[w][1] + f, x[r]);
-    else
-      x[r][0] = x[r][1] = x[r][2] = x[r][3] = 0.f;
-  }
-  const Turn tn = load_turn(p, checked_position(p, t), f, 1.f);
-  const int partner = partner_lane<LANES>(lane, p.rot);
+    for (int e = 0; e < 4; ++e) s[e] *= dir;
+  } else {
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const int hh = first + r * PER + lane / LANES;
-    const int w = hh >= p.H[0];
-    if (p.norm) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) ss = fmaf(x[r][e], x[r][e], ss);
-      const float rs = __frsqrt_rn(fmaf(lanes_sum<LANES>(ss), 1.f / D, p.eps));
-      float g[4] = {1.f, 1.f, 1.f, 1.f};
-      if (p.gain[w]) load4(p.gain[w] + f, g);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[r][e] = x[r][e] * rs * g[e];
-    }
-    if (p.rot) turn(tn, p.interleaved, partner, x[r]);
-    if (hh < heads)
-      store4(static_cast<TI*>(p.out[w]) + t * p.os[w][0] + (int64_t)(hh - (w ? p.H[0] : 0)) * p.os[w][1] + f, x[r]);
+    for (int e = 0; e < 4; ++e) { c[e] = 1.f; s[e] = 0.f; }
   }
 }
 
-template <typename TI, int D, int kRows>
+// Pass i of a token: q's heads come first, PER = 256 / D heads a pass.
+struct Pass {
+  int w, head;   // 0: q, 1: k; this lane's head
+  bool on;
+  __device__ __forceinline__ Pass(const QkParams& p, int i, int pq, int per, int sub) {
+    w = i >= pq;
+    head = (i - (w ? pq : 0)) * per + sub;
+    on = head < p.H[w];
+  }
+};
+
+template <typename TI, int D>
+__global__ void __launch_bounds__(kQkThreads) qk_fwd_kernel(const __grid_constant__ QkParams p) {
+  constexpr int LANES = D / 8, PER = 32 / LANES;
+  pdl_wait();
+  const int lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
+  const int64_t t = (int64_t)blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5);
+  if (t >= live_tokens(p)) return;
+  const int pq = (p.H[0] + PER - 1) / PER, pk = (p.H[1] + PER - 1) / PER, i0 = blockIdx.y * kPasses;
+  const Parts pt(l, p.rot, p.interleaved);
+  Raw4<TI> r0[kPasses], r1[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    if (i0 + i >= pq + pk) break;
+    const Pass ps(p, i0 + i, pq, PER, sub);
+    const TI* src = static_cast<const TI*>(p.x[ps.w]) + t * p.xs[ps.w][0] + (ps.on ? ps.head : 0) * p.xs[ps.w][1];
+    r0[i] = fetch4(src + pt.f0);
+    r1[i] = fetch4(src + pt.f1);
+  }
+  float c[4], s[4];
+  load_angles(p, pt, checked_position(p, t), l, 1.f, c, s);
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    if (i0 + i >= pq + pk) break;
+    const Pass ps(p, i0 + i, pq, PER, sub);
+    float x[4], y[4];
+    unpack4(r0[i], x);
+    unpack4(r1[i], y);
+    if (p.norm) {
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
+      const float rs = __frsqrt_rn(fmaf(row_sum<LANES>(ss), 1.f / D, p.eps));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) { x[e] *= rs; y[e] *= rs; }
+      if (p.gain[ps.w]) {
+        float a[4], b[4];
+        load4(p.gain[ps.w] + pt.f0, a);
+        load4(p.gain[ps.w] + pt.f1, b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { x[e] *= a[e]; y[e] *= b[e]; }
+      }
+    }
+    if (pt.turns) turn_pairs(x, y, c, s, p.interleaved);
+    if (ps.on) {
+      TI* dst = static_cast<TI*>(p.out[ps.w]) + t * p.os[ps.w][0] + ps.head * p.os[ps.w][1];
+      store4(dst + pt.f0, x);
+      store4(dst + pt.f1, y);
+    }
+  }
+}
+
+template <typename TI, int D>
 __global__ void __launch_bounds__(kBwdThreads) qk_bwd_kernel(const __grid_constant__ QkParams p, int chunks) {
-  constexpr int LANES = D / 4, PER = 32 / LANES, WARPS = kBwdThreads / 32;
+  constexpr int LANES = D / 8, PER = 32 / LANES, WARPS = kBwdThreads / 32, PASSES = 2;
   __shared__ __align__(16) float red[WARPS][2][D];
   __shared__ int last;
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int f = (lane % LANES) * 4;
-  const int heads = p.H[0] + p.H[1];
-  const int partner = partner_lane<LANES>(lane, p.rot);
-  const int64_t units = live_tokens(p) * chunks;
-  float gain[2][4], dg[2][4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES, sub = lane / LANES;
+  const int pq = (p.H[0] + PER - 1) / PER, pk = (p.H[1] + PER - 1) / PER;
+  const Parts pt(l, p.rot, p.interleaved);
+  const int64_t T = live_tokens(p);
+  float dg[2][2][4];        // [q, k][part]
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
+  for (int w = 0; w < 2; ++w)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) { gain[w][e] = 1.f; dg[w][e] = 0.f; }
-    if (p.norm && p.gain[w]) load4(p.gain[w] + f, gain[w]);
-  }
-  for (int64_t unit = (int64_t)blockIdx.x * WARPS + warp; unit < units; unit += (int64_t)gridDim.x * WARPS) {
-    const int64_t t = unit / chunks;
-    const int first = (int)(unit - t * chunks) * kRows * PER;
-    float x[kRows][4], g[kRows][4];
+    for (int e = 0; e < 4; ++e) dg[w][0][e] = dg[w][1][e] = 0.f;
+  // a warp takes PASSES passes of a token at a time
+  const int step = (int)gridDim.x * WARPS;
+  int unit = (int)blockIdx.x * WARPS + warp;
+  for (int64_t t = unit / chunks; t < T; unit += step, t = unit / chunks) {
+    const int i0 = (unit - (int)t * chunks) * PASSES;
+    Raw4<TI> x0[PASSES], x1[PASSES], g0[PASSES], g1[PASSES];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int hh = first + r * PER + lane / LANES;
-      const int w = hh >= p.H[0], h = hh - (w ? p.H[0] : 0);
-      if (hh < heads) {
-        load4(static_cast<const TI*>(p.g[w]) + t * p.gs[w][0] + (int64_t)h * p.gs[w][1] + f, g[r]);
-        if (p.norm) load4(static_cast<const TI*>(p.x[w]) + t * p.xs[w][0] + (int64_t)h * p.xs[w][1] + f, x[r]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[r][e] = g[r][e] = 0.f;
+    for (int i = 0; i < PASSES; ++i) {
+      if (i0 + i >= pq + pk) break;
+      const Pass ps(p, i0 + i, pq, PER, sub);
+      const int head = ps.on ? ps.head : 0;
+      const TI* gs = static_cast<const TI*>(p.g[ps.w]) + t * p.gs[ps.w][0] + head * p.gs[ps.w][1];
+      g0[i] = fetch4(gs + pt.f0);
+      g1[i] = fetch4(gs + pt.f1);
+      if (p.norm) {
+        const TI* xs = static_cast<const TI*>(p.x[ps.w]) + t * p.xs[ps.w][0] + head * p.xs[ps.w][1];
+        x0[i] = fetch4(xs + pt.f0);
+        x1[i] = fetch4(xs + pt.f1);
       }
     }
-    const Turn tn = load_turn(p, checked_position(p, t), f, -1.f);
+    float c[4], s[4];
+    load_angles(p, pt, checked_position(p, t), l, -1.f, c, s);
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int hh = first + r * PER + lane / LANES;
-      const int w = hh >= p.H[0];
-      if (p.rot) turn(tn, p.interleaved, partner, g[r]);
+    for (int i = 0; i < PASSES; ++i) {
+      if (i0 + i >= pq + pk) break;
+      const Pass ps(p, i0 + i, pq, PER, sub);
+      float a[4], b[4];
+      unpack4(g0[i], a);
+      unpack4(g1[i], b);
+      if (pt.turns) turn_pairs(a, b, c, s, p.interleaved);
       if (p.norm) {
+        float x[4], y[4], ga[4] = {1.f, 1.f, 1.f, 1.f}, gb[4] = {1.f, 1.f, 1.f, 1.f};
+        unpack4(x0[i], x);
+        unpack4(x1[i], y);
+        if (p.gain[ps.w]) {
+          load4(p.gain[ps.w] + pt.f0, ga);
+          load4(p.gain[ps.w] + pt.f1, gb);
+        }
         float ss = 0.f, se = 0.f;
-        float eg[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          eg[e] = g[r][e] * (w ? gain[1][e] : gain[0][e]);
-          ss = fmaf(x[r][e], x[r][e], ss);
-          se = fmaf(eg[e], x[r][e], se);
+          ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
+          se = fmaf(a[e] * ga[e], x[e], fmaf(b[e] * gb[e], y[e], se));
         }
-        ss = lanes_sum<LANES>(ss);
-        se = lanes_sum<LANES>(se);
+        ss = row_sum<LANES>(ss);
+        se = row_sum<LANES>(se);
         const float rs = __frsqrt_rn(fmaf(ss, 1.f / D, p.eps));
         const float m = se * rs * (1.f / D);      // mean(e gain x r)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float xr = x[r][e] * rs;
-          const float add = g[r][e] * xr;
-          dg[0][e] += w ? 0.f : add;
-          dg[1][e] += w ? add : 0.f;
-          g[r][e] = rs * fmaf(-xr, m, eg[e]);
+          const float u = x[e] * rs, v = y[e] * rs;
+          const float du = ps.on ? a[e] * u : 0.f, dv = ps.on ? b[e] * v : 0.f;
+          if (ps.w) { dg[1][0][e] += du; dg[1][1][e] += dv; }
+          else { dg[0][0][e] += du; dg[0][1][e] += dv; }
+          a[e] = rs * fmaf(-u, m, a[e] * ga[e]);
+          b[e] = rs * fmaf(-v, m, b[e] * gb[e]);
         }
       }
-      if (hh < heads)
-        store4(static_cast<TI*>(p.out[w]) + t * p.os[w][0] + (int64_t)(hh - (w ? p.H[0] : 0)) * p.os[w][1] + f, g[r]);
+      if (ps.on) {
+        TI* dst = static_cast<TI*>(p.out[ps.w]) + t * p.os[ps.w][0] + ps.head * p.os[ps.w][1];
+        store4(dst + pt.f0, a);
+        store4(dst + pt.f1, b);
+      }
     }
   }
   if (!p.norm || (!p.dgain[0] && !p.dgain[1])) return;
@@ -241,11 +228,13 @@ __global__ void __launch_bounds__(kBwdThreads) qk_bwd_kernel(const __grid_consta
 #pragma unroll
   for (int w = 0; w < 2; ++w)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int o = LANES; o < 32; o <<= 1) dg[w][e] += __shfl_xor_sync(0xffffffffu, dg[w][e], o);
-      if (lane < LANES) red[warp][w][f + e] = dg[w][e];
-    }
+      for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int o = LANES; o < 32; o <<= 1) dg[w][h][e] += __shfl_xor_sync(0xffffffffu, dg[w][h][e], o);
+        if (lane < LANES) red[warp][w][(h ? pt.f1 : pt.f0) + e] = dg[w][h][e];
+      }
   __syncthreads();
   if (threadIdx.x < 2 * D) {
     const int w = threadIdx.x / D, i = threadIdx.x % D;
@@ -291,9 +280,8 @@ hstu_status_t check_qk_desc(const hstu_qk_desc* d, bool bwd) {
   if (d->rot_dim < 0 || d->rot_dim > d->d || (d->rot_dim > 0 && d->max_position < 1)) return HSTU_ERR_INVALID_ARG;
   if (d->d != 32 && d->d != 64 && d->d != 128) return HSTU_ERR_UNSUPPORTED;
   if (d->rot_dim % 8 != 0) return HSTU_ERR_UNSUPPORTED;
-  // the grid counts chunks of at least 4 rows, 8 a CTA
-  if (d->Hq + (int64_t)d->Hk > 4096 || d->total_tokens > ((int64_t)1 << 32) ||
-      d->total_tokens * (d->Hq + (int64_t)d->Hk) > ((int64_t)1 << 33))
+  // units of work (tokens x passes) are counted in 32 bits
+  if (d->Hq + (int64_t)d->Hk > 4096 || d->total_tokens > ((int64_t)1 << 30) / (d->Hq + (int64_t)d->Hk))
     return HSTU_ERR_UNSUPPORTED;
   const int64_t per = d->dtype == HSTU_BF16 ? 8 : 4;   // elements of 16 bytes
   const int64_t* all[6] = {d->q_strides, d->k_strides, d->q_out_strides, d->k_out_strides, d->dq_strides, d->dk_strides};
@@ -308,24 +296,20 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 size_t qk_bwd_bytes(const hstu_qk_desc* d) { return kWsHeaderBytes + sizeof(float) * kMaxBwdCtas * 2 * (size_t)d->d; }
 
-// every kernel variant's launch: kRows rows of a token in flight a warp
 template <typename TI, int D, bool BWD>
 cudaError_t launch_qk(const QkParams& p, int sms, cudaStream_t st) {
-  constexpr int PER = 128 / D;
-  const int heads = p.H[0] + p.H[1];
+  constexpr int PER = 256 / D;
+  const int passes = (p.H[0] + PER - 1) / PER + (p.H[1] + PER - 1) / PER;
   if constexpr (!BWD) {
-    constexpr int R = 4;
-    const int chunks = (heads + R * PER - 1) / (R * PER);
-    const int64_t ctas = (p.T * chunks + kQkThreads / 32 - 1) / (kQkThreads / 32);
-    return launch_pdl(qk_fwd_kernel<TI, D, R>, dim3((unsigned)ctas), dim3(kQkThreads), 0, st, p, chunks);
+    const dim3 grid((unsigned)((p.T + kQkThreads / 32 - 1) / (kQkThreads / 32)), (unsigned)((passes + kPasses - 1) / kPasses));
+    return launch_pdl(qk_fwd_kernel<TI, D>, grid, dim3(kQkThreads), 0, st, p);
   } else {
-    constexpr int R = 4;
-    const int chunks = (heads + R * PER - 1) / (R * PER);
+    const int chunks = (passes + 1) / 2;
     int64_t ctas = (p.T * chunks + kBwdThreads / 32 - 1) / (kBwdThreads / 32);
     const int64_t most = sms < kMaxBwdCtas ? sms : kMaxBwdCtas;
     if (ctas > most) ctas = most;
     if (ctas < 1) ctas = 1;
-    return launch_pdl(qk_bwd_kernel<TI, D, R>, dim3((unsigned)ctas), dim3(kBwdThreads), 0, st, p, chunks);
+    return launch_pdl(qk_bwd_kernel<TI, D>, dim3((unsigned)ctas), dim3(kBwdThreads), 0, st, p, chunks);
   }
 }
 

@@ -13,7 +13,7 @@ __device__ __forceinline__ int warp_find_sequence(const int64_t* off, int B, int
   const int lane = threadIdx.x & 31;
   int lo = 0, n = B;                     // the answer lies in [lo, lo + n)
   while (n > 1) {
-    const int step = (n + 31) / 32;
+    const int step = (int)((unsigned)(n + 31) >> 5);
     const int at = lo + lane * step;     // pivot `lane`: first sequence of its part
     const bool below = lane * step < n && off[at] <= t;
     const unsigned m = __ballot_sync(0xffffffffu, below);

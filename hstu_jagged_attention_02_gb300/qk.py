@@ -156,41 +156,46 @@ class QKProblem:
             self.bwd_args = C.hstu_qk_bwd_args(*common, _ptr(self.dq_out), _ptr(self.dk_out), _ptr(self.dq), _ptr(self.dk),
                                                _ptr(self.d_q_gain), _ptr(self.d_k_gain))
 
+        lib, w = C.load(), (self.ws.data_ptr(), self.ws_bytes)
+        self._forward = Launch(dev, lib.hstu_qk_norm_rope_fwd, "hstu_qk_norm_rope_fwd", self.desc, self.fwd_args, *w)
+        if backward:
+            self._backward = Launch(dev, lib.hstu_qk_norm_rope_bwd, "hstu_qk_norm_rope_bwd", self.bwd_desc, self.bwd_args, *w)
+
     def forward(self, stream=None):
-        with _on(self.device):
-            C.hstu_qk_norm_rope_fwd(self.desc, self.fwd_args, self.ws.data_ptr(), self.ws_bytes,
-                                    _stream_of(self.device, stream))
+        self._forward(stream)
 
     def backward(self, stream=None):
-        with _on(self.device):
-            C.hstu_qk_norm_rope_bwd(self.bwd_desc, self.bwd_args, self.ws.data_ptr(), self.ws_bytes,
-                                    _stream_of(self.device, stream))
+        self._backward(stream)
 
     def device_error(self, stream=None) -> int:
-        with _on(self.device):
-            return C.hstu_get_device_error(self.ws.data_ptr(), _stream_of(self.device, stream))
+        return device_error(self.device, self.ws, stream)
 
 
-class _Here:
-    def __enter__(self):
-        return None
+class Launch:
+    """One C call with its arguments put together once: calling it launches on
+    the given stream, or on the current one of the tensors' device."""
 
-    def __exit__(self, *a):
-        return False
+    __slots__ = ("index", "fn", "name", "args", "keep")
+
+    def __init__(self, device, fn, name, *args):
+        self.index = device.index if device.index is not None else torch.cuda.current_device()
+        self.fn, self.name, self.keep = fn, name, args
+        self.args = tuple(C.ctypes.byref(a) if isinstance(a, C.ctypes.Structure) else a for a in args)
+
+    def __call__(self, stream=None):
+        if torch._C._cuda_getDevice() != self.index:    # the launches go to the current device
+            with torch.cuda.device(self.index):
+                return self(stream)
+        s = torch._C._cuda_getCurrentRawStream(self.index) if stream is None else stream.cuda_stream
+        status = self.fn(*self.args, s)
+        if status:
+            raise C.HSTUError(status, self.name)
 
 
-_HERE = _Here()
-
-
-def _on(device):
-    """The tensors' device as the current one (the launches go to the current device)."""
-    if device.type == "cuda" and device.index is not None and device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return _HERE
-
-
-def _stream_of(device, stream=None) -> int:
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+def device_error(device, workspace, stream=None) -> int:
+    with torch.cuda.device(device):
+        s = stream if stream is not None else torch.cuda.current_stream()
+        return C.hstu_get_device_error(workspace.data_ptr(), s.cuda_stream)
 
 
 class QKNormRopeFunction(torch.autograd.Function):
