@@ -3,9 +3,12 @@
 //
 // Append: bound by the BF16 rows it reads (2 d bytes in, 9 d / 16 out), if the
 // instructions are few.  d / 8 lanes hold a row (hstu_rows.cuh: both features
-// of a pair in one lane), a warp takes one token, kPasses passes of 256
-// features at a time, all loads first; its place in the cache is looked up
-// once.  A group's maximum goes over the 2 or 4 lanes that share it.
+// of a pair in one lane), a warp takes a token at a time, its keys' and values'
+// passes of 256 features side by side, all loads first.  A warp walks
+// tokens_per_warp neighbouring tokens, so that the sequence and the page are
+// looked up once for them (in a small batch each warp has one token: there the
+// chain of lookups is the time).  A group's maximum goes over the 2 or 4 lanes
+// that share it.
 //
 // Roundings are decided as on real numbers.  A value x that is exact in FP32
 // (a BF16 input) meets a border only exactly: its quotient by the scale (4
@@ -25,8 +28,9 @@ namespace hstu {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kPasses = 4;
-constexpr float kBand = 1.9073486328125e-06f;   // 2^-19: 2^-20 of the terms, and as much for the quotient
+constexpr int kPasses = 2;
+constexpr int kManyTokens = 4;
+constexpr float kBand = 1.05e-06f;   // 2^-20 of a feature's terms, its quotient by the scale included, and a little
 
 struct AppendParams {
   const int64_t* off;
@@ -44,7 +48,7 @@ struct AppendParams {
   int* hdr;
   int64_t T, max_pos;
   int B, H, page_log, num_pages, max_pages;
-  int rot, interleaved, norm;
+  int rot, interleaved, norm, tokens_per_warp;
   float eps;
   float k_scale, v_scale;   // 2^-k_exp, 2^-v_exp
 };
@@ -61,42 +65,47 @@ struct Coded {
   uint32_t scale;   // e4m3 byte
 };
 
-__device__ __forceinline__ float max4(const float (&x)[4]) {
-  return max_nan(max_nan(fabsf(x[0]), fabsf(x[1])), max_nan(fabsf(x[2]), fabsf(x[3])));
-}
-
 // y = x / s for a scale s, rounded to 16 significant bits: right on a border
 // exactly where the quotient of an exact x is.
-__device__ __forceinline__ float quotient(float x, float inv) {
-  return __uint_as_float((__float_as_uint(x * inv) + 0x80u) & 0xffffff00u);
+__device__ __forceinline__ float snap(float y) { return __uint_as_float((__float_as_uint(y) + 0x80u) & 0xffffff00u); }
+
+__device__ __forceinline__ float inverse(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return s > 0.f ? r : 0.f;
 }
 
-// 4 features that are exact in FP32, top the largest magnitude of their group.
-__device__ __forceinline__ Coded encode_exact(const float (&x)[4], float top) {
-  Coded c;
-  c.scale = e4m3_of(__fdiv_rn(top, 6.f));
-  const float s = e4m3_float(c.scale), inv = s > 0.f ? __frcp_rn(s) : 0.f;
-  c.codes = e2m1x2_of(quotient(x[0], inv), quotient(x[1], inv)) | (e2m1x2_of(quotient(x[2], inv), quotient(x[3], inv)) << 8);
-  return c;
-}
-
-// 4 features known to +-d[e], and their group's largest magnitude to [lo, hi]:
-// false where that does not decide the result.
-__device__ __forceinline__ bool encode_banded(const float (&x)[4], const float (&d)[4], float lo, float hi, Coded& c) {
-  c.scale = e4m3_of(hi * (0.16666667f * 1.0000005f));
-  bool sure = c.scale == e4m3_of(lo * (0.16666667f * 0.9999995f));
-  const float s = e4m3_float(c.scale), inv = s > 0.f ? __frcp_rn(s) : 0.f;
-  float a[4], b[4];
+// 8 features that are exact in FP32, top the largest magnitude of their group:
+// codes (32 bits) and the scale's byte.
+__device__ __forceinline__ uint2 encode_exact(const Row8& x, float top) {
+  const float want = snap(top * 0.16666667f);                 // a border lies 2^-14 away, or is met
+  const uint32_t scale = e4m3_of(top == top ? want : top);    // a NaN stays one
+  const float inv = inverse(e4m3_float(scale));
+  uint32_t codes = 0;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float y = x[e] * inv, w = d[e] * inv;
-    a[e] = y - w;
-    b[e] = y + w;
+  for (int e = 0; e < 4; ++e) codes |= e2m1x2_of(snap(x.v[e].x * inv), snap(x.v[e].y * inv)) << (8 * e);
+  return make_uint2(codes, scale);
+}
+
+// 4 features known to +-d, and their group's largest magnitude to [lo, hi]:
+// false where that does not decide the result.
+__device__ __forceinline__ bool encode_banded(const float2 (&x)[2], const float2 (&d)[2], float lo, float hi, Coded& c) {
+  c.scale = e4m3_of(hi * (0.16666667f * 1.0000005f));
+  const bool sure = c.scale == e4m3_of(lo * (0.16666667f * 0.9999995f));
+  const float inv = inverse(e4m3_float(c.scale));
+  const float2 i2 = make_float2(inv, inv), n2 = make_float2(-inv, -inv);
+  uint32_t lower = 0, upper = 0;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float2 y = __fmul2_rn(x[e], i2);
+    const float2 a = __ffma2_rn(d[e], n2, y), b = __ffma2_rn(d[e], i2, y);
+    lower |= e2m1x2_of(a.x, a.y) << (8 * e);
+    upper |= e2m1x2_of(b.x, b.y) << (8 * e);
   }
-  c.codes = e2m1x2_of(a[0], a[1]) | (e2m1x2_of(a[2], a[3]) << 8);
-  const uint32_t other = e2m1x2_of(b[0], b[1]) | (e2m1x2_of(b[2], b[3]) << 8);
+  c.codes = lower;
+  if (lower == upper) return sure;
   // codes that differ, but for the sign of a zero
-  const uint32_t diff = (c.codes ^ other) & 0xffffu, mags = (c.codes | other) & 0x7777u;
+  const uint32_t diff = lower ^ upper, mags = (lower | upper) & 0x7777u;
   const uint32_t nonzero = (mags | (mags >> 1) | (mags >> 2)) & 0x1111u;
   return sure && (diff & (nonzero * 15u)) == 0;
 }
@@ -168,77 +177,74 @@ __device__ __forceinline__ void to_neighbours(F (&x)[4], F (&y)[4], int lane, in
   for (int e = 0; e < 4; ++e) { x[e] = out[0][e]; y[e] = out[1][e]; }
 }
 
-// What a lane knows about turning the token's keys.
+// What a lane knows about turning keys.
 struct KeyTurn {
   Parts pt;        // as loaded and turned
   bool moved;      // then moved to neighbouring features
   bool quad, any_quad;
-  float c[4], s[4];
 };
 
-// Two parts of a key row, normed and turned, coded from FP32; false where FP64 has to decide.
+// A lane's 8 features of a key, normed and turned, coded from FP32; false where FP64 has to decide.
 template <int LANES>
-__device__ __forceinline__ bool key_f32(const AppendParams& p, const KeyTurn& kt, int lane, float (&x)[4], float (&y)[4],
-                                        Coded& cx, Coded& cy) {
+__device__ __forceinline__ bool key_f32(const AppendParams& p, const KeyTurn& kt, const Angles& an, const Row8& gain, int lane,
+                                        Row8 x, Coded& cx, Coded& cy) {
   float rs = p.k_scale;
-  if (p.norm) {
-    float ss = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
-    rs *= __frsqrt_rn(fmaf(row_sum<LANES>(ss), 1.f / (8 * LANES), p.eps));
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) { x[e] *= rs; y[e] *= rs; }
-  if (p.gain) {
-    float a[4], b[4];
-    load4(p.gain + kt.pt.f0, a);
-    load4(p.gain + kt.pt.f1, b);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) { x[e] *= a[e]; y[e] *= b[e]; }
-  }
-  float dx[4], dy[4];
+  if (p.norm) rs *= rsqrtf(fmaf(row_sum<LANES>(x.dot(x)), 1.f / (8 * LANES), p.eps));
+  x.times(rs);
+  if (p.gain) x.times(gain);
+  Row8 d;
+  const float2 band = make_float2(kBand, kBand);
+  auto mag = [](float2 a) { return make_float2(fabsf(a.x), fabsf(a.y)); };
   if (kt.pt.turns) {
+    if (p.interleaved) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {   // the pair's size bounds both of its terms
-      if (p.interleaved) {
-        dx[e] = kBand * (fabsf(x[e]) + fabsf(x[e ^ 1]));
-        dy[e] = kBand * (fabsf(y[e]) + fabsf(y[e ^ 1]));
-      } else {
-        dx[e] = dy[e] = kBand * (fabsf(x[e]) + fabsf(y[e]));
+      for (int e = 0; e < 4; ++e) {
+        const float m = kBand * (fabsf(x.v[e].x) + fabsf(x.v[e].y));
+        d.v[e] = make_float2(m, m);
       }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) d.v[e] = d.v[e + 2] = __fmul2_rn(__fadd2_rn(mag(x.v[e]), mag(x.v[e + 2])), band);
     }
-    turn_pairs(x, y, kt.c, kt.s, p.interleaved);
+    an.turn(x, p.interleaved);
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) { dx[e] = kBand * fabsf(x[e]); dy[e] = kBand * fabsf(y[e]); }
+    for (int e = 0; e < 4; ++e) d.v[e] = __fmul2_rn(mag(x.v[e]), band);
   }
   if (kt.moved) {
-    to_neighbours<LANES>(x, y, lane, p.rot);
-    to_neighbours<LANES>(dx, dy, lane, p.rot);
+    float a[4] = {x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y}, b[4] = {x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y};
+    float u[4] = {d.v[0].x, d.v[0].y, d.v[1].x, d.v[1].y}, v[4] = {d.v[2].x, d.v[2].y, d.v[3].x, d.v[3].y};
+    to_neighbours<LANES>(a, b, lane, p.rot);
+    to_neighbours<LANES>(u, v, lane, p.rot);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      x.v[e] = make_float2(a[2 * e], a[2 * e + 1]); x.v[e + 2] = make_float2(b[2 * e], b[2 * e + 1]);
+      d.v[e] = make_float2(u[2 * e], u[2 * e + 1]); d.v[e + 2] = make_float2(v[2 * e], v[2 * e + 1]);
+    }
   }
-  float hx = 0.f, hy = 0.f, lx = 0.f, ly = 0.f;
+  float h[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    hx = max_nan(hx, fabsf(x[e]) + dx[e]);
-    hy = max_nan(hy, fabsf(y[e]) + dy[e]);
-    lx = max_nan(lx, fabsf(x[e]) - dx[e]);
-    ly = max_nan(ly, fabsf(y[e]) - dy[e]);
+    const float2 m = mag(x.v[e]);
+    const float2 a = __fadd2_rn(m, d.v[e]), b = __fadd2_rn(m, make_float2(-d.v[e].x, -d.v[e].y));
+    h[e >> 1] = max_nan(h[e >> 1], max_nan(a.x, a.y));
+    w[e >> 1] = max_nan(w[e >> 1], max_nan(b.x, b.y));
   }
   auto mx = [](float a, float b) { return max_nan(a, b); };
-  group_tops(hx, hy, kt.quad, kt.any_quad, mx);
-  group_tops(lx, ly, kt.quad, kt.any_quad, mx);
-  const bool a = encode_banded(x, dx, lx, hx, cx), b = encode_banded(y, dy, ly, hy, cy);
+  group_tops(h[0], h[1], kt.quad, kt.any_quad, mx);
+  group_tops(w[0], w[1], kt.quad, kt.any_quad, mx);
+  const float2 x0[2] = {x.v[0], x.v[1]}, x1[2] = {x.v[2], x.v[3]}, d0[2] = {d.v[0], d.v[1]}, d1[2] = {d.v[2], d.v[3]};
+  const bool a = encode_banded(x0, d0, w[0], h[0], cx), b = encode_banded(x1, d1, w[1], h[1], cy);
   return a && b;
 }
 
-// The same in FP64, from the loaded features x, y (cosines c, sines s): the
-// parts' codes in x (low and high half), their scales in y.  how: bit 0
+// The same in FP64, from the loaded features: the parts' codes in x (low and
+// high half), their scales in y.  how: bit 0
 // turns, 1 moved, 2 quad, 3 any_quad.
 template <int LANES>
-__device__ __noinline__ uint2 key_f64(const AppendParams& p, int how, int f0, int f1, int lane, float4 x4, float4 y4, float4 c4,
-                                      float4 s4) {
-  const float x0[4] = {x4.x, x4.y, x4.z, x4.w}, y0[4] = {y4.x, y4.y, y4.z, y4.w};
-  const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+__device__ __noinline__ uint2 key_f64(const AppendParams& p, int how, int f0, int f1, int lane, Row8 v, Angles an) {
+  const float x0[4] = {v.v[0].x, v.v[0].y, v.v[1].x, v.v[1].y}, y0[4] = {v.v[2].x, v.v[2].y, v.v[3].x, v.v[3].y};
+  const float c[4] = {an.c[0].x, an.c[0].y, an.c[1].x, an.c[1].y}, s[4] = {an.s[0].x, an.s[0].y, an.s[1].x, an.s[1].y};
   const bool quad = how & 4, any_quad = how & 8;
   double x[4], y[4], rs = 1.0;
   if (p.norm) {
@@ -251,7 +257,16 @@ __device__ __noinline__ uint2 key_f64(const AppendParams& p, int how, int f0, in
     x[e] = x0[e] * rs * (p.gain ? (double)p.gain[f0 + e] : 1.0) * p.k_scale;
     y[e] = y0[e] * rs * (p.gain ? (double)p.gain[f1 + e] : 1.0) * p.k_scale;
   }
-  if (how & 1) turn_pairs(x, y, c, s, p.interleaved);
+  if (how & 1) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      double& a = p.interleaved ? (e < 2 ? x[2 * e] : y[2 * e - 4]) : x[e];
+      double& b = p.interleaved ? (e < 2 ? x[2 * e + 1] : y[2 * e - 3]) : y[e];
+      const double u = a * c[e] - b * s[e], w = b * c[e] + a * s[e];
+      a = u;
+      b = w;
+    }
+  }
   if (how & 2) to_neighbours<LANES>(x, y, lane, p.rot);
   double tx = 0.0, ty = 0.0;
   double bx = 0.0, by = 0.0;        // 1: a NaN, which the maximum passes over
@@ -290,114 +305,157 @@ __device__ __forceinline__ bool find_slot(const int32_t* table, int max_pages, i
   return ok;
 }
 
+// A walk over neighbouring tokens: the token's sequence and place, looked up
+// again where a sequence or a page ends.  lens: cache lengths after an append
+// (the tokens are the last ones), or starts of a read (NULL: 0).
+template <bool APPEND>
+struct Places {
+  FoundSeq seq;
+  Slot slot;
+  bool found = false;
+
+  // false: no place (recorded), or a padded batch's row (done)
+  template <typename P>
+  __device__ __forceinline__ bool at(const P& p, const int32_t* lens, int64_t t, int64_t total) {
+    if (!found || t >= seq.end) {
+      seq = warp_find_sequence(p.off, lens, p.B, t);
+      found = t < total;
+      if (!found) return false;
+    } else if ((++slot.place & ((1 << p.page_log) - 1)) != 0) {
+      ++slot.pos;                         // the next place of the same page
+      return true;
+    }
+    const int64_t pos = APPEND ? seq.aux - (seq.end - t) : seq.aux + (t - seq.begin);
+    // the first test fails only for offsets that decrease somewhere
+    const bool in = seq.begin <= t && t < seq.end && seq.aux >= (APPEND ? seq.end - seq.begin : 0);
+    if (find_slot(p.table, p.max_pages, p.page_log, p.num_pages, seq.b, in ? pos : -1, p.hdr, slot)) return true;
+    found = false;
+    return false;
+  }
+};
+
+// Offsets that do not fit the rows are recorded; nothing is done then.
+__device__ __forceinline__ bool fits(int64_t first, int64_t total, int64_t T, int* hdr) {
+  if (first == 0 && total >= 0 && total <= T) return true;
+  if ((threadIdx.x & 31) == 0) set_error(hdr, HSTU_ERR_DEVICE_CHECK, -1);
+  return false;
+}
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LANES = D / 8, PER = 32 / LANES;
   pdl_wait();
   const int lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
-  const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  int64_t t = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.tokens_per_warp;
+  const int64_t t_end = t + p.tokens_per_warp < p.T ? t + p.tokens_per_warp : p.T;
   if (t >= p.T) return;
   const bool work = p.rot || p.norm;            // keys change on their way
-  const int ph = (p.H + PER - 1) / PER;         // passes over the keys, then as many over the values
-  const Parts kp(l, work ? p.rot : 0, p.interleaved), vp(l, 0, true);
-  Raw4<__nv_bfloat16> r0[kPasses], r1[kPasses];
-  auto load = [&](int i0) {
+  const int ph = (p.H + PER - 1) / PER;
+  KeyTurn kt = {Parts(l, p.rot, p.interleaved), false, false, false};
+  const int v0 = 8 * l;                         // values lie side by side
+  int f0 = kt.pt.f0, f1 = kt.pt.f1;             // of a key's coded parts
+  if (!p.interleaved && p.rot > 8) {
+    kt.moved = p.rot % 32 != 0;
+    kt.any_quad = !kt.moved;
+    kt.quad = kt.any_quad && kt.pt.turns;
+    if (kt.moved) { f0 = v0; f1 = v0 + 4; }
+  }
+  Raw4<__nv_bfloat16> k0[kPasses], k1[kPasses], u0[kPasses], u1[kPasses];
+  auto load = [&](int64_t tok, int i0) {
+    const __nv_bfloat16 *k = p.k + tok * p.ks[0], *v = p.v + tok * p.vs[0];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      if (i0 + i >= 2 * ph) break;
-      const bool key = i0 + i < ph;
-      const int head = min((i0 + i - (key ? 0 : ph)) * PER + sub, p.H - 1);
-      const __nv_bfloat16* src = key ? p.k + t * p.ks[0] + head * p.ks[1] : p.v + t * p.vs[0] + head * p.vs[1];
-      r0[i] = fetch4(src + (key ? kp.f0 : vp.f0));
-      r1[i] = fetch4(src + (key ? kp.f1 : vp.f1));
+      const int head = (i0 + i) * PER + sub;
+      if (head < p.H) {
+        k0[i] = fetch4(k + head * p.ks[1] + kt.pt.f0);
+        k1[i] = fetch4(k + head * p.ks[1] + kt.pt.f1);
+        u0[i] = fetch4(v + head * p.vs[1] + v0);
+        u1[i] = fetch4(v + head * p.vs[1] + v0 + 4);
+      }
     }
   };
-  load(0);
-  const int64_t total = p.off[p.B];
-  if (total > p.T || p.off[0] != 0) {
-    if (lane == 0) set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, -1);
-    return;
-  }
-  if (t >= total) return;                 // a padded batch's row
-  const int b = warp_find_sequence(p.off, p.B, t);
-  const int64_t o0 = p.off[b], o1 = p.off[b + 1];
-  Slot sl;
-  const bool in = o0 <= t && t < o1;      // false only for offsets that decrease somewhere
-  if (!find_slot(p.table, p.max_pages, p.page_log, p.num_pages, b, in ? p.lens[b] - (o1 - o0) + (t - o0) : -1, p.hdr, sl))
-    return;
-  KeyTurn kt = {kp, false, false, false, {1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}};
-  int f0 = kp.f0, f1 = kp.f1;             // of a key's coded parts
-  if (p.rot) {
-    if (sl.pos >= p.max_pos) {
-      if (lane == 0) set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, b);
-      return;
-    }
-    if (kp.turns) {
-      const int64_t at = (int64_t)sl.pos * (p.rot >> 1) + 4 * l;
-      load4(p.cos + at, kt.c);
-      load4(p.sin + at, kt.s);
-    }
-    if (!p.interleaved && p.rot > 8) {
-      kt.moved = p.rot % 32 != 0;
-      kt.any_quad = !kt.moved;
-      kt.quad = kt.any_quad && kp.turns;
-      if (kt.moved) { f0 = vp.f0; f1 = vp.f1; }
-    }
-  }
+  load(t, 0);
+  const int64_t off0 = p.off[0], total = p.off[p.B];
+  Places<true> pl;
+  Row8 gain;
+  if (p.gain) gain = Row8(fetch4(p.gain + kt.pt.f0), fetch4(p.gain + kt.pt.f1));
   const PageLayout lay(1 << p.page_log, D);
-  uint8_t* block = p.pages + sl.page * p.H * (int64_t)lay.bytes();
-  for (int i0 = 0; i0 < 2 * ph; i0 += kPasses) {
-    if (i0) load(i0);
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      if (i0 + i >= 2 * ph) break;
-      const bool key = i0 + i < ph;
-      const int head = (i0 + i - (key ? 0 : ph)) * PER + sub;
-      float x[4], y[4];
-      unpack4(r0[i], x);
-      unpack4(r1[i], y);
-      Coded cx, cy;
-      if (key && work) {
-        const bool sure = key_f32<LANES>(p, kt, lane, x, y, cx, cy);
-        if (__any_sync(0xffffffffu, !sure)) {
-          unpack4(r0[i], x);
-          unpack4(r1[i], y);
-          const uint2 r = key_f64<LANES>(
-              p, (kp.turns ? 1 : 0) | (kt.moved ? 2 : 0) | (kt.quad ? 4 : 0) | (kt.any_quad ? 8 : 0), kp.f0, kp.f1, lane,
-              make_float4(x[0], x[1], x[2], x[3]), make_float4(y[0], y[1], y[2], y[3]),
-              make_float4(kt.c[0], kt.c[1], kt.c[2], kt.c[3]), make_float4(kt.s[0], kt.s[1], kt.s[2], kt.s[3]));
-          cx.codes = r.x & 0xffffu; cy.codes = r.x >> 16;
-          cx.scale = r.y & 0xffu; cy.scale = r.y >> 8;
-        }
-      } else {
-        const float sc = key ? p.k_scale : p.v_scale;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) { x[e] *= sc; y[e] *= sc; }
-        float top = max_nan(max4(x), max4(y));
-        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        cx = encode_exact(x, top);
-        cy = encode_exact(y, top);
+  for (; t < t_end; ++t) {
+    const bool placed = pl.at(p, p.lens, t, total);
+    if (!fits(off0, total, p.T, p.hdr) || t >= total) return;
+    if (!placed) {
+      if (t + 1 < t_end) load(t + 1, 0);
+      continue;
+    }
+    const Slot sl = pl.slot;
+    Angles an;
+    if (p.rot) {
+      if (sl.pos >= p.max_pos) {
+        if (lane == 0) set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, pl.seq.b);
+        return;
       }
-      if (head < p.H) {
-        uint8_t* part = block + head * lay.bytes() + (key ? 0 : lay.half());
-        uint8_t* codes = part + sl.place * lay.code_row;
-        uint8_t* scales = part + lay.scales() + sl.place * lay.scale_row;
-        const int a = key ? f0 : vp.f0, bb = key ? f1 : vp.f1;
-        if (key && kt.quad) {
-          *reinterpret_cast<uint16_t*>(codes + (a >> 1)) = (uint16_t)cx.codes;
-          *reinterpret_cast<uint16_t*>(codes + (bb >> 1)) = (uint16_t)cy.codes;
-          if ((l & 3) == 0) {
-            scales[a >> 4] = (uint8_t)cx.scale;
-            scales[bb >> 4] = (uint8_t)cy.scale;
+      if (kt.pt.turns) {
+        const int64_t at = (int64_t)sl.pos * (p.rot >> 1) + 4 * l;
+        an.load(p.cos + at, p.sin + at, 1.f);
+      }
+    }
+    uint8_t* block = p.pages + sl.page * p.H * (int64_t)lay.bytes();
+    const int place_c = sl.place * lay.code_row, place_s = lay.scales() + sl.place * lay.scale_row;
+    for (int i0 = 0; i0 < ph; i0 += kPasses) {
+      if (i0) load(t, i0);
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        if (i0 + i >= ph) break;
+        const int head = (i0 + i) * PER + sub;
+        uint8_t* part = block + head * lay.bytes();
+        if (work) {
+          const Row8 x(k0[i], k1[i]);
+          Coded cx, cy;
+          const bool sure = key_f32<LANES>(p, kt, an, gain, lane, x, cx, cy);
+          if (__any_sync(0xffffffffu, !sure && head < p.H)) {
+            const uint2 r = key_f64<LANES>(
+                p, (kt.pt.turns ? 1 : 0) | (kt.moved ? 2 : 0) | (kt.quad ? 4 : 0) | (kt.any_quad ? 8 : 0), kt.pt.f0, kt.pt.f1,
+                lane, x, an);
+            cx.codes = r.x & 0xffffu; cy.codes = r.x >> 16;
+            cx.scale = r.y & 0xffu; cy.scale = r.y >> 8;
           }
-        } else {
-          *reinterpret_cast<uint32_t*>(codes + (a >> 1)) = (cx.codes & 0xffffu) | (cy.codes << 16);
-          if ((l & 1) == 0) scales[a >> 4] = (uint8_t)cx.scale;
+          if (head < p.H) {
+            uint8_t *codes = part + place_c, *scales = part + place_s;
+            if (kt.quad) {
+              *reinterpret_cast<uint16_t*>(codes + (f0 >> 1)) = (uint16_t)cx.codes;
+              *reinterpret_cast<uint16_t*>(codes + (f1 >> 1)) = (uint16_t)cy.codes;
+              if ((l & 3) == 0) {
+                scales[f0 >> 4] = (uint8_t)cx.scale;
+                scales[f1 >> 4] = (uint8_t)cy.scale;
+              }
+            } else {
+              *reinterpret_cast<uint32_t*>(codes + (f0 >> 1)) = cx.codes | (cy.codes << 16);
+              if ((l & 1) == 0) scales[f0 >> 4] = (uint8_t)cx.scale;
+            }
+          }
+        }
+        // values, and keys that go in as they are
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (w == 0 && work) continue;
+          Row8 x = w ? Row8(u0[i], u1[i]) : Row8(k0[i], k1[i]);
+          x.times(w ? p.v_scale : p.k_scale);
+          float top = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max_nan(top, max_nan(fabsf(x.v[e].x), fabsf(x.v[e].y)));
+          top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          const uint2 r = encode_exact(x, top);
+          if (head < p.H) {
+            uint8_t* half = part + (w ? lay.half() : 0);
+            *reinterpret_cast<uint32_t*>(half + place_c + 4 * l) = r.x;
+            if ((l & 1) == 0) half[place_s + (l >> 1)] = (uint8_t)r.y;
+          }
         }
       }
     }
+    if (p.page_times && lane == 0) p.page_times[(sl.page << p.page_log) + sl.place] = p.times[t];
+    if (t + 1 < t_end) load(t + 1, 0);
   }
-  if (p.page_times && lane == 0) p.page_times[(sl.page << p.page_log) + sl.place] = p.times[t];
 }
 
 struct ReadParams {
@@ -411,73 +469,68 @@ struct ReadParams {
   int64_t* times;
   int* hdr;
   int64_t T;
-  int B, H, page_log, num_pages, max_pages;
+  int B, H, page_log, num_pages, max_pages, tokens_per_warp;
   float k_scale, v_scale;   // 2^k_exp, 2^v_exp
 };
 
-// A lane takes 16 features (8 bytes of codes and their scale), a warp one
-// token, 512 features a pass, the loads of kPasses passes first.
+// A lane takes 16 features (8 bytes of codes and their scale), a warp a
+// token's keys and values, 512 features of each a pass.
 template <int D>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadParams p) {
   constexpr int LANES = D / 16, PER = 32 / LANES;
   pdl_wait();
   const int lane = threadIdx.x & 31, g = lane % LANES, sub = lane / LANES;
-  const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  int64_t t = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.tokens_per_warp;
+  const int64_t t_end = t + p.tokens_per_warp < p.T ? t + p.tokens_per_warp : p.T;
   if (t >= p.T) return;
-  const int64_t total = p.off[p.B];
-  if (total > p.T || p.off[0] != 0) {
-    if (lane == 0) set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, -1);
-    return;
-  }
-  if (t >= total) return;
-  const int b = warp_find_sequence(p.off, p.B, t);
-  const int64_t o0 = p.off[b], o1 = p.off[b + 1];
-  const int64_t start = p.starts ? p.starts[b] : 0;
-  Slot sl;
-  if (!find_slot(p.table, p.max_pages, p.page_log, p.num_pages, b, o0 <= t && t < o1 && start >= 0 ? start + (t - o0) : -1,
-                 p.hdr, sl))
-    return;
+  const int64_t off0 = p.off[0], total = p.off[p.B];
+  Places<false> pl;
   const PageLayout lay(1 << p.page_log, D);
-  const uint8_t* block = p.pages + sl.page * p.H * (int64_t)lay.bytes();
-  const uint8_t* codes = block + sl.place * lay.code_row + g * 8;
-  const uint8_t* scales = block + lay.scales() + sl.place * lay.scale_row + g;
   const int ph = (p.H + PER - 1) / PER;
-  for (int i0 = 0; i0 < 2 * ph; i0 += kPasses) {
-    uint2 w[kPasses];
-    uint32_t sc[kPasses];
+  auto two = [&](__half2 v, float s) -> uint32_t {
+    const float2 x = __fmul2_rn(__half22float2(v), make_float2(s, s));
+    const __nv_bfloat162 y = __floats2bfloat162_rn(x.x, x.y);
+    return *reinterpret_cast<const uint32_t*>(&y);
+  };
+  for (; t < t_end; ++t) {
+    const bool placed = pl.at(p, p.starts, t, total);
+    if (!fits(off0, total, p.T, p.hdr) || t >= total) return;
+    if (!placed) continue;
+    const Slot sl = pl.slot;
+    const uint8_t* block = p.pages + sl.page * p.H * (int64_t)lay.bytes();
+    const uint8_t* codes = block + sl.place * lay.code_row + g * 8;
+    const uint8_t* scales = block + lay.scales() + sl.place * lay.scale_row + g;
+    for (int i = 0; i < ph; ++i) {
+      const int head = i * PER + sub;
+      if (head >= p.H) break;
+      const int at = head * lay.bytes();
+      uint2 w[2];
+      uint32_t sc[2];
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      if (i0 + i >= 2 * ph) break;
-      const bool key = i0 + i < ph;
-      const int head = min((i0 + i - (key ? 0 : ph)) * PER + sub, p.H - 1);
-      const int at = head * lay.bytes() + (key ? 0 : lay.half());
-      w[i] = *reinterpret_cast<const uint2*>(codes + at);
-      sc[i] = scales[at];
-    }
+      for (int x = 0; x < 2; ++x) {
+        w[x] = *reinterpret_cast<const uint2*>(codes + at + x * lay.half());
+        sc[x] = scales[at + x * lay.half()];
+      }
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      if (i0 + i >= 2 * ph) break;
-      const bool key = i0 + i < ph;
-      const int head = (i0 + i - (key ? 0 : ph)) * PER + sub;
-      __nv_bfloat16* dst = key ? p.k : p.v;
-      if (head >= p.H || !dst) continue;
-      const float s = e4m3_float(sc[i]) * (key ? p.k_scale : p.v_scale);
-      auto two = [&](__half2 v) -> uint32_t {
-        const float2 x = __half22float2(v);
-        const __nv_bfloat162 y = __floats2bfloat162_rn(x.x * s, x.y * s);
-        return *reinterpret_cast<const uint32_t*>(&y);
-      };
-      uint4* to = reinterpret_cast<uint4*>(dst + (t * p.H + head) * D + g * 16);
-      to[0] = make_uint4(two(e2m1x2_half2<0>(w[i].x)), two(e2m1x2_half2<1>(w[i].x)), two(e2m1x2_half2<2>(w[i].x)),
-                         two(e2m1x2_half2<3>(w[i].x)));
-      to[1] = make_uint4(two(e2m1x2_half2<0>(w[i].y)), two(e2m1x2_half2<1>(w[i].y)), two(e2m1x2_half2<2>(w[i].y)),
-                         two(e2m1x2_half2<3>(w[i].y)));
+      for (int x = 0; x < 2; ++x) {
+        __nv_bfloat16* dst = x ? p.v : p.k;
+        if (!dst) continue;
+        const float s = e4m3_float(sc[x]) * (x ? p.v_scale : p.k_scale);
+        uint4* to = reinterpret_cast<uint4*>(dst + (t * p.H + head) * D + g * 16);
+        to[0] = make_uint4(two(e2m1x2_half2<0>(w[x].x), s), two(e2m1x2_half2<1>(w[x].x), s), two(e2m1x2_half2<2>(w[x].x), s),
+                           two(e2m1x2_half2<3>(w[x].x), s));
+        to[1] = make_uint4(two(e2m1x2_half2<0>(w[x].y), s), two(e2m1x2_half2<1>(w[x].y), s), two(e2m1x2_half2<2>(w[x].y), s),
+                           two(e2m1x2_half2<3>(w[x].y), s));
+      }
     }
+    if (p.times && lane == 0) p.times[t] = p.page_times[(sl.page << p.page_log) + sl.place];
   }
-  if (p.times && lane == 0) p.times[t] = p.page_times[(sl.page << p.page_log) + sl.place];
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// several tokens a warp once every warp the GPU holds has one
+int tokens_per_warp(int64_t T) { return T > 152 * 48 ? kManyTokens : 1; }
 
 int page_log(int page_size) { return page_size == 32 ? 5 : (page_size == 64 ? 6 : 7); }
 
@@ -551,7 +604,8 @@ hstu_status_t hstu_cache_append(const hstu_cache_desc* c, const hstu_cache_appen
   p.B = a->B; p.H = c->H; p.page_log = page_log(c->page_size); p.num_pages = c->num_pages; p.max_pages = c->max_pages;
   p.rot = a->rot_dim; p.interleaved = a->interleaved; p.norm = a->norm; p.eps = a->eps;
   p.k_scale = ldexpf(1.f, -c->k_exp); p.v_scale = ldexpf(1.f, -c->v_exp);
-  const unsigned ctas = (unsigned)((p.T + kWarps - 1) / kWarps);
+  p.tokens_per_warp = tokens_per_warp(p.T);
+  const unsigned ctas = (unsigned)((p.T + kWarps * p.tokens_per_warp - 1) / (kWarps * p.tokens_per_warp));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = c->d == 128 ? launch_pdl(append_kernel<128>, dim3(ctas), dim3(kThreads), 0, st, p)
                                     : launch_pdl(append_kernel<64>, dim3(ctas), dim3(kThreads), 0, st, p);
@@ -582,7 +636,8 @@ hstu_status_t hstu_cache_read(const hstu_cache_desc* c, const hstu_cache_read_ar
   p.T = a->total_tokens;
   p.B = a->B; p.H = c->H; p.page_log = page_log(c->page_size); p.num_pages = c->num_pages; p.max_pages = c->max_pages;
   p.k_scale = ldexpf(1.f, c->k_exp); p.v_scale = ldexpf(1.f, c->v_exp);
-  const unsigned ctas = (unsigned)((p.T + kWarps - 1) / kWarps);
+  p.tokens_per_warp = tokens_per_warp(p.T);
+  const unsigned ctas = (unsigned)((p.T + kWarps * p.tokens_per_warp - 1) / (kWarps * p.tokens_per_warp));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = c->d == 128 ? launch_pdl(read_kernel<128>, dim3(ctas), dim3(kThreads), 0, st, p)
                                     : launch_pdl(read_kernel<64>, dim3(ctas), dim3(kThreads), 0, st, p);

@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kFin* kGroups) finish_kernel(const __grid_cons
   pdl_wait();
   const int quota = p.hdr[WS_CA_QUOTA];
   if (quota < 0 || t >= p.off[p.B]) return;    // a refused batch, a padded batch's row
-  const int b = warp_find_sequence(p.off, p.B, t);
+  const int b = warp_find_sequence(p.off, nullptr, p.B, t).b;
   CachedSeq s;
   if (!load_seq(p, b, s)) return;
   const int r = (int)(t - s.row0), qb = r / N;

@@ -9,14 +9,16 @@
 // have many loads in flight.  d / 8 lanes hold a row, so that a warp's pass
 // covers 256 features, the row's sum takes few shuffles, and both features of
 // every pair lie in one lane (hstu_rows.cuh): the rotation exchanges nothing.
-// A warp takes up to kPasses passes (heads) of one token, all loads first; the
-// token's cosines and sines are loaded once for them.
+// A warp takes a few passes of one token, all loads first; the token's cosines
+// and sines are loaded once for them.
 //
 // The backward's gain gradients are sums over all tokens and heads.  The
 // CTAs walk tokens and keep per-lane FP32 partial sums; the CTAs' rows of
 // partial sums land in the workspace and the CTA that finishes last (a
 // counter in the workspace's header) adds them up in row order in FP64, so
 // the result does not depend on the order in which CTAs finish.
+#include <type_traits>
+
 #include "hstu_internal.h"
 #include "hstu_rows.cuh"
 
@@ -26,7 +28,7 @@ namespace {
 
 constexpr int kQkThreads = 256;
 constexpr int kBwdThreads = 512;
-constexpr int kPasses = 4;
+constexpr int kPasses = 2;   // 256 features each, of q and of k
 
 struct QkParams {
   const int64_t* num_tokens;
@@ -66,32 +68,18 @@ __device__ __forceinline__ int64_t live_tokens(const QkParams& p) {
   return n;
 }
 
-// The lane's cosines and sines (dir -1: turned back, the backward).
-__device__ __forceinline__ void load_angles(const QkParams& p, const Parts& pt, int64_t pos, int l, float dir, float (&c)[4],
-                                            float (&s)[4]) {
-  if (pt.turns) {
-    const int64_t at = pos * (p.rot >> 1) + 4 * l;
-    load4(p.cos + at, c);
-    load4(p.sin + at, s);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] *= dir;
+__device__ __forceinline__ Row8 load_gain(const float* gain, const Parts& pt) {
+  Row8 g;
+  if (gain) {
+    g = Row8(fetch4(gain + pt.f0), fetch4(gain + pt.f1));
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) { c[e] = 1.f; s[e] = 0.f; }
+    for (int e = 0; e < 4; ++e) g.v[e] = make_float2(1.f, 1.f);
   }
+  return g;
 }
 
-// Pass i of a token: q's heads come first, PER = 256 / D heads a pass.
-struct Pass {
-  int w, head;   // 0: q, 1: k; this lane's head
-  bool on;
-  __device__ __forceinline__ Pass(const QkParams& p, int i, int pq, int per, int sub) {
-    w = i >= pq;
-    head = (i - (w ? pq : 0)) * per + sub;
-    on = head < p.H[w];
-  }
-};
-
+// A warp takes kPasses passes of q's heads and as many of k's, of one token.
 template <typename TI, int D>
 __global__ void __launch_bounds__(kQkThreads) qk_fwd_kernel(const __grid_constant__ QkParams p) {
   constexpr int LANES = D / 8, PER = 32 / LANES;
@@ -99,128 +87,130 @@ __global__ void __launch_bounds__(kQkThreads) qk_fwd_kernel(const __grid_constan
   const int lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
   const int64_t t = (int64_t)blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5);
   if (t >= live_tokens(p)) return;
-  const int pq = (p.H[0] + PER - 1) / PER, pk = (p.H[1] + PER - 1) / PER, i0 = blockIdx.y * kPasses;
   const Parts pt(l, p.rot, p.interleaved);
-  Raw4<TI> r0[kPasses], r1[kPasses];
+  const int h0 = blockIdx.y * (kPasses * PER) + sub;
+  Raw4<TI> r0[2][kPasses], r1[2][kPasses];
+  auto load = [&](auto W) {
+    constexpr int w = decltype(W)::value;
+    const TI* src = static_cast<const TI*>(p.x[w]) + t * p.xs[w][0];
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    if (i0 + i >= pq + pk) break;
-    const Pass ps(p, i0 + i, pq, PER, sub);
-    const TI* src = static_cast<const TI*>(p.x[ps.w]) + t * p.xs[ps.w][0] + (ps.on ? ps.head : 0) * p.xs[ps.w][1];
-    r0[i] = fetch4(src + pt.f0);
-    r1[i] = fetch4(src + pt.f1);
-  }
-  float c[4], s[4];
-  load_angles(p, pt, checked_position(p, t), l, 1.f, c, s);
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    if (i0 + i >= pq + pk) break;
-    const Pass ps(p, i0 + i, pq, PER, sub);
-    float x[4], y[4];
-    unpack4(r0[i], x);
-    unpack4(r1[i], y);
-    if (p.norm) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
-      const float rs = __frsqrt_rn(fmaf(row_sum<LANES>(ss), 1.f / D, p.eps));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) { x[e] *= rs; y[e] *= rs; }
-      if (p.gain[ps.w]) {
-        float a[4], b[4];
-        load4(p.gain[ps.w] + pt.f0, a);
-        load4(p.gain[ps.w] + pt.f1, b);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) { x[e] *= a[e]; y[e] *= b[e]; }
+    for (int i = 0; i < kPasses; ++i) {
+      if (h0 + i * PER < p.H[w]) {
+        const TI* row = src + (h0 + i * PER) * p.xs[w][1];
+        r0[w][i] = fetch4(row + pt.f0);
+        r1[w][i] = fetch4(row + pt.f1);
       }
     }
-    if (pt.turns) turn_pairs(x, y, c, s, p.interleaved);
-    if (ps.on) {
-      TI* dst = static_cast<TI*>(p.out[ps.w]) + t * p.os[ps.w][0] + ps.head * p.os[ps.w][1];
-      store4(dst + pt.f0, x);
-      store4(dst + pt.f1, y);
-    }
+  };
+  load(std::integral_constant<int, 0>());
+  load(std::integral_constant<int, 1>());
+  Angles an;
+  if (pt.turns) {
+    const int64_t at = checked_position(p, t) * (p.rot >> 1) + 4 * l;
+    an.load(p.cos + at, p.sin + at, 1.f);
   }
+  auto work = [&](auto W) {
+    constexpr int w = decltype(W)::value;
+    if (blockIdx.y * (kPasses * PER) >= p.H[w]) return;
+    Row8 gain;
+    if (p.norm) gain = load_gain(p.gain[w], pt);
+    TI* dst = static_cast<TI*>(p.out[w]) + t * p.os[w][0];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      if ((int)blockIdx.y * (kPasses * PER) + i * PER >= p.H[w]) break;
+      Row8 x(r0[w][i], r1[w][i]);
+      if (p.norm) {
+        x.times(rsqrtf(fmaf(row_sum<LANES>(x.dot(x)), 1.f / D, p.eps)));
+        x.times(gain);
+      }
+      if (pt.turns) an.turn(x, p.interleaved);
+      if (h0 + i * PER < p.H[w]) {
+        TI* row = dst + (h0 + i * PER) * p.os[w][1];
+        store_part(row + pt.f0, x.v[0], x.v[1]);
+        store_part(row + pt.f1, x.v[2], x.v[3]);
+      }
+    }
+  };
+  work(std::integral_constant<int, 0>());
+  work(std::integral_constant<int, 1>());
 }
 
+// A warp takes one pass of q's heads and one of k's at a time.
 template <typename TI, int D>
 __global__ void __launch_bounds__(kBwdThreads) qk_bwd_kernel(const __grid_constant__ QkParams p, int chunks) {
-  constexpr int LANES = D / 8, PER = 32 / LANES, WARPS = kBwdThreads / 32, PASSES = 2;
+  constexpr int LANES = D / 8, PER = 32 / LANES, WARPS = kBwdThreads / 32;
   __shared__ __align__(16) float red[WARPS][2][D];
   __shared__ int last;
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES, sub = lane / LANES;
-  const int pq = (p.H[0] + PER - 1) / PER, pk = (p.H[1] + PER - 1) / PER;
   const Parts pt(l, p.rot, p.interleaved);
   const int64_t T = live_tokens(p);
-  float dg[2][2][4];        // [q, k][part]
+  float2 dg[2][4];          // [q, k]: sums over this lane's features
 #pragma unroll
   for (int w = 0; w < 2; ++w)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) dg[w][0][e] = dg[w][1][e] = 0.f;
-  // a warp takes PASSES passes of a token at a time
-  const int step = (int)gridDim.x * WARPS;
-  int unit = (int)blockIdx.x * WARPS + warp;
-  for (int64_t t = unit / chunks; t < T; unit += step, t = unit / chunks) {
-    const int i0 = (unit - (int)t * chunks) * PASSES;
-    Raw4<TI> x0[PASSES], x1[PASSES], g0[PASSES], g1[PASSES];
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      if (i0 + i >= pq + pk) break;
-      const Pass ps(p, i0 + i, pq, PER, sub);
-      const int head = ps.on ? ps.head : 0;
-      const TI* gs = static_cast<const TI*>(p.g[ps.w]) + t * p.gs[ps.w][0] + head * p.gs[ps.w][1];
-      g0[i] = fetch4(gs + pt.f0);
-      g1[i] = fetch4(gs + pt.f1);
-      if (p.norm) {
-        const TI* xs = static_cast<const TI*>(p.x[ps.w]) + t * p.xs[ps.w][0] + head * p.xs[ps.w][1];
-        x0[i] = fetch4(xs + pt.f0);
-        x1[i] = fetch4(xs + pt.f1);
+    for (int e = 0; e < 4; ++e) dg[w][e] = make_float2(0.f, 0.f);
+  // unit (t, r): pass r of token t
+  const int step = (int)gridDim.x * WARPS, unit = (int)blockIdx.x * WARPS + warp;
+  const int dt = step / chunks, dr = step - dt * chunks;
+  int64_t t = unit / chunks;
+  int r = unit - (int)t * chunks;
+  while (t < T) {
+    const int h = r * PER + sub;
+    Raw4<TI> x0[2], x1[2], g0[2], g1[2];
+    auto load = [&](auto W) {
+      constexpr int w = decltype(W)::value;
+      if (h < p.H[w]) {
+        const TI* gs = static_cast<const TI*>(p.g[w]) + t * p.gs[w][0] + h * p.gs[w][1];
+        g0[w] = fetch4(gs + pt.f0);
+        g1[w] = fetch4(gs + pt.f1);
+        if (p.norm) {
+          const TI* xs = static_cast<const TI*>(p.x[w]) + t * p.xs[w][0] + h * p.xs[w][1];
+          x0[w] = fetch4(xs + pt.f0);
+          x1[w] = fetch4(xs + pt.f1);
+        }
       }
+    };
+    load(std::integral_constant<int, 0>());
+    load(std::integral_constant<int, 1>());
+    Angles an;
+    if (pt.turns) {
+      const int64_t at = checked_position(p, t) * (p.rot >> 1) + 4 * l;
+      an.load(p.cos + at, p.sin + at, -1.f);
     }
-    float c[4], s[4];
-    load_angles(p, pt, checked_position(p, t), l, -1.f, c, s);
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      if (i0 + i >= pq + pk) break;
-      const Pass ps(p, i0 + i, pq, PER, sub);
-      float a[4], b[4];
-      unpack4(g0[i], a);
-      unpack4(g1[i], b);
-      if (pt.turns) turn_pairs(a, b, c, s, p.interleaved);
+    auto work = [&](auto W) {
+      constexpr int w = decltype(W)::value;
+      if (r * PER >= p.H[w]) return;
+      const bool on = h < p.H[w];
+      Row8 g(g0[w], g1[w]);
+      if (pt.turns) an.turn(g, p.interleaved);
       if (p.norm) {
-        float x[4], y[4], ga[4] = {1.f, 1.f, 1.f, 1.f}, gb[4] = {1.f, 1.f, 1.f, 1.f};
-        unpack4(x0[i], x);
-        unpack4(x1[i], y);
-        if (p.gain[ps.w]) {
-          load4(p.gain[ps.w] + pt.f0, ga);
-          load4(p.gain[ps.w] + pt.f1, gb);
-        }
-        float ss = 0.f, se = 0.f;
+        const Row8 gain = load_gain(p.gain[w], pt);
+        Row8 x(x0[w], x1[w]), e = g;
+        e.times(gain);
+        const float ss = row_sum<LANES>(x.dot(x)), se = row_sum<LANES>(x.dot(e));
+        const float rs = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+        const float m = -se * rs * (1.f / D);      // - mean(e gain x r)
+        x.times(rs);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
-          se = fmaf(a[e] * ga[e], x[e], fmaf(b[e] * gb[e], y[e], se));
-        }
-        ss = row_sum<LANES>(ss);
-        se = row_sum<LANES>(se);
-        const float rs = __frsqrt_rn(fmaf(ss, 1.f / D, p.eps));
-        const float m = se * rs * (1.f / D);      // mean(e gain x r)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float u = x[e] * rs, v = y[e] * rs;
-          const float du = ps.on ? a[e] * u : 0.f, dv = ps.on ? b[e] * v : 0.f;
-          if (ps.w) { dg[1][0][e] += du; dg[1][1][e] += dv; }
-          else { dg[0][0][e] += du; dg[0][1][e] += dv; }
-          a[e] = rs * fmaf(-u, m, a[e] * ga[e]);
-          b[e] = rs * fmaf(-v, m, b[e] * gb[e]);
+        for (int i = 0; i < 4; ++i) {
+          if (on) dg[w][i] = __ffma2_rn(g.v[i], x.v[i], dg[w][i]);
+          g.v[i] = __fmul2_rn(__ffma2_rn(x.v[i], make_float2(m, m), e.v[i]), make_float2(rs, rs));
         }
       }
-      if (ps.on) {
-        TI* dst = static_cast<TI*>(p.out[ps.w]) + t * p.os[ps.w][0] + ps.head * p.os[ps.w][1];
-        store4(dst + pt.f0, a);
-        store4(dst + pt.f1, b);
+      if (on) {
+        TI* dst = static_cast<TI*>(p.out[w]) + t * p.os[w][0] + h * p.os[w][1];
+        store_part(dst + pt.f0, g.v[0], g.v[1]);
+        store_part(dst + pt.f1, g.v[2], g.v[3]);
       }
+    };
+    work(std::integral_constant<int, 0>());
+    work(std::integral_constant<int, 1>());
+    t += dt;
+    r += dr;
+    if (r >= chunks) {
+      r -= chunks;
+      ++t;
     }
   }
   if (!p.norm || (!p.dgain[0] && !p.dgain[1])) return;
@@ -228,13 +218,14 @@ __global__ void __launch_bounds__(kBwdThreads) qk_bwd_kernel(const __grid_consta
 #pragma unroll
   for (int w = 0; w < 2; ++w)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int e = 0; e < 4; ++e) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-#pragma unroll
-        for (int o = LANES; o < 32; o <<= 1) dg[w][h][e] += __shfl_xor_sync(0xffffffffu, dg[w][h][e], o);
-        if (lane < LANES) red[warp][w][(h ? pt.f1 : pt.f0) + e] = dg[w][h][e];
+      for (int o = LANES; o < 32; o <<= 1) {
+        dg[w][e].x += __shfl_xor_sync(0xffffffffu, dg[w][e].x, o);
+        dg[w][e].y += __shfl_xor_sync(0xffffffffu, dg[w][e].y, o);
       }
+      if (lane < LANES) *reinterpret_cast<float2*>(&red[warp][w][(e < 2 ? pt.f0 : pt.f1) + 2 * (e & 1)]) = dg[w][e];
+    }
   __syncthreads();
   if (threadIdx.x < 2 * D) {
     const int w = threadIdx.x / D, i = threadIdx.x % D;
@@ -299,17 +290,16 @@ size_t qk_bwd_bytes(const hstu_qk_desc* d) { return kWsHeaderBytes + sizeof(floa
 template <typename TI, int D, bool BWD>
 cudaError_t launch_qk(const QkParams& p, int sms, cudaStream_t st) {
   constexpr int PER = 256 / D;
-  const int passes = (p.H[0] + PER - 1) / PER + (p.H[1] + PER - 1) / PER;
+  const int heads = p.H[0] > p.H[1] ? p.H[0] : p.H[1], passes = (heads + PER - 1) / PER;
   if constexpr (!BWD) {
     const dim3 grid((unsigned)((p.T + kQkThreads / 32 - 1) / (kQkThreads / 32)), (unsigned)((passes + kPasses - 1) / kPasses));
     return launch_pdl(qk_fwd_kernel<TI, D>, grid, dim3(kQkThreads), 0, st, p);
   } else {
-    const int chunks = (passes + 1) / 2;
-    int64_t ctas = (p.T * chunks + kBwdThreads / 32 - 1) / (kBwdThreads / 32);
+    int64_t ctas = (p.T * passes + kBwdThreads / 32 - 1) / (kBwdThreads / 32);
     const int64_t most = sms < kMaxBwdCtas ? sms : kMaxBwdCtas;
     if (ctas > most) ctas = most;
     if (ctas < 1) ctas = 1;
-    return launch_pdl(qk_bwd_kernel<TI, D>, dim3((unsigned)ctas), dim3(kBwdThreads), 0, st, p, chunks);
+    return launch_pdl(qk_bwd_kernel<TI, D>, dim3((unsigned)ctas), dim3(kBwdThreads), 0, st, p, passes);
   }
 }
 
