@@ -27,8 +27,7 @@ namespace hstu {
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kPasses = 2;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kManyTokens = 4;
 constexpr float kBand = 1.05e-06f;   // 2^-20 of a feature's terms, its quotient by the scale included, and a little
 
@@ -342,7 +341,7 @@ __device__ __forceinline__ bool fits(int64_t first, int64_t total, int64_t T, in
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 5) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LANES = D / 8, PER = 32 / LANES;
   pdl_wait();
   const int lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
@@ -360,18 +359,15 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
     kt.quad = kt.any_quad && kt.pt.turns;
     if (kt.moved) { f0 = v0; f1 = v0 + 4; }
   }
-  Raw4<__nv_bfloat16> k0[kPasses], k1[kPasses], u0[kPasses], u1[kPasses];
-  auto load = [&](int64_t tok, int i0) {
-    const __nv_bfloat16 *k = p.k + tok * p.ks[0], *v = p.v + tok * p.vs[0];
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int head = (i0 + i) * PER + sub;
-      if (head < p.H) {
-        k0[i] = fetch4(k + head * p.ks[1] + kt.pt.f0);
-        k1[i] = fetch4(k + head * p.ks[1] + kt.pt.f1);
-        u0[i] = fetch4(v + head * p.vs[1] + v0);
-        u1[i] = fetch4(v + head * p.vs[1] + v0 + 4);
-      }
+  Raw4<__nv_bfloat16> k0, k1, u0, u1;
+  auto load = [&](int64_t tok, int i) {
+    const int head = i * PER + sub;
+    if (head < p.H) {
+      const __nv_bfloat16 *k = p.k + tok * p.ks[0] + head * p.ks[1], *v = p.v + tok * p.vs[0] + head * p.vs[1];
+      k0 = fetch4(k + kt.pt.f0);
+      k1 = fetch4(k + kt.pt.f1);
+      u0 = fetch4(v + v0);
+      u1 = fetch4(v + v0 + 4);
     }
   };
   load(t, 0);
@@ -401,60 +397,58 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
     }
     uint8_t* block = p.pages + sl.page * p.H * (int64_t)lay.bytes();
     const int place_c = sl.place * lay.code_row, place_s = lay.scales() + sl.place * lay.scale_row;
-    for (int i0 = 0; i0 < ph; i0 += kPasses) {
-      if (i0) load(t, i0);
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        if (i0 + i >= ph) break;
-        const int head = (i0 + i) * PER + sub;
-        uint8_t* part = block + head * lay.bytes();
-        if (work) {
-          const Row8 x(k0[i], k1[i]);
-          Coded cx, cy;
-          const bool sure = key_f32<LANES>(p, kt, an, gain, lane, x, cx, cy);
-          if (__any_sync(0xffffffffu, !sure && head < p.H)) {
-            const uint2 r = key_f64<LANES>(
-                p, (kt.pt.turns ? 1 : 0) | (kt.moved ? 2 : 0) | (kt.quad ? 4 : 0) | (kt.any_quad ? 8 : 0), kt.pt.f0, kt.pt.f1,
-                lane, x, an);
-            cx.codes = r.x & 0xffffu; cy.codes = r.x >> 16;
-            cx.scale = r.y & 0xffu; cy.scale = r.y >> 8;
-          }
-          if (head < p.H) {
-            uint8_t *codes = part + place_c, *scales = part + place_s;
-            if (kt.quad) {
-              *reinterpret_cast<uint16_t*>(codes + (f0 >> 1)) = (uint16_t)cx.codes;
-              *reinterpret_cast<uint16_t*>(codes + (f1 >> 1)) = (uint16_t)cy.codes;
-              if ((l & 3) == 0) {
-                scales[f0 >> 4] = (uint8_t)cx.scale;
-                scales[f1 >> 4] = (uint8_t)cy.scale;
-              }
-            } else {
-              *reinterpret_cast<uint32_t*>(codes + (f0 >> 1)) = cx.codes | (cy.codes << 16);
-              if ((l & 1) == 0) scales[f0 >> 4] = (uint8_t)cx.scale;
+    for (int i = 0; i < ph; ++i) {
+      const int head = i * PER + sub;
+      uint8_t* part = block + head * lay.bytes();
+      const Row8 kx(k0, k1);
+      Row8 vx(u0, u1);
+      // the next pass's rows
+      if (i + 1 < ph) load(t, i + 1);
+      else if (t + 1 < t_end) load(t + 1, 0);
+      if (work) {
+        Coded cx, cy;
+        const bool sure = key_f32<LANES>(p, kt, an, gain, lane, kx, cx, cy);
+        if (__any_sync(0xffffffffu, !sure && head < p.H)) {
+          const uint2 r = key_f64<LANES>(
+              p, (kt.pt.turns ? 1 : 0) | (kt.moved ? 2 : 0) | (kt.quad ? 4 : 0) | (kt.any_quad ? 8 : 0), kt.pt.f0, kt.pt.f1,
+              lane, kx, an);
+          cx.codes = r.x & 0xffffu; cy.codes = r.x >> 16;
+          cx.scale = r.y & 0xffu; cy.scale = r.y >> 8;
+        }
+        if (head < p.H) {
+          uint8_t *codes = part + place_c, *scales = part + place_s;
+          if (kt.quad) {
+            *reinterpret_cast<uint16_t*>(codes + (f0 >> 1)) = (uint16_t)cx.codes;
+            *reinterpret_cast<uint16_t*>(codes + (f1 >> 1)) = (uint16_t)cy.codes;
+            if ((l & 3) == 0) {
+              scales[f0 >> 4] = (uint8_t)cx.scale;
+              scales[f1 >> 4] = (uint8_t)cy.scale;
             }
+          } else {
+            *reinterpret_cast<uint32_t*>(codes + (f0 >> 1)) = cx.codes | (cy.codes << 16);
+            if ((l & 1) == 0) scales[f0 >> 4] = (uint8_t)cx.scale;
           }
         }
-        // values, and keys that go in as they are
+      }
+      // values, and keys that go in as they are
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (w == 0 && work) continue;
-          Row8 x = w ? Row8(u0[i], u1[i]) : Row8(k0[i], k1[i]);
-          x.times(w ? p.v_scale : p.k_scale);
-          float top = 0.f;
+      for (int w = 0; w < 2; ++w) {
+        if (w == 0 && work) continue;
+        Row8 x = w ? vx : kx;
+        x.times(w ? p.v_scale : p.k_scale);
+        float top = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top = max_nan(top, max_nan(fabsf(x.v[e].x), fabsf(x.v[e].y)));
-          top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          const uint2 r = encode_exact(x, top);
-          if (head < p.H) {
-            uint8_t* half = part + (w ? lay.half() : 0);
-            *reinterpret_cast<uint32_t*>(half + place_c + 4 * l) = r.x;
-            if ((l & 1) == 0) half[place_s + (l >> 1)] = (uint8_t)r.y;
-          }
+        for (int e = 0; e < 4; ++e) top = max_nan(top, max_nan(fabsf(x.v[e].x), fabsf(x.v[e].y)));
+        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        const uint2 r = encode_exact(x, top);
+        if (head < p.H) {
+          uint8_t* half = part + (w ? lay.half() : 0);
+          *reinterpret_cast<uint32_t*>(half + place_c + 4 * l) = r.x;
+          if ((l & 1) == 0) half[place_s + (l >> 1)] = (uint8_t)r.y;
         }
       }
     }
     if (p.page_times && lane == 0) p.page_times[(sl.page << p.page_log) + sl.place] = p.times[t];
-    if (t + 1 < t_end) load(t + 1, 0);
   }
 }
 
@@ -473,14 +467,15 @@ struct ReadParams {
   float k_scale, v_scale;   // 2^k_exp, 2^v_exp
 };
 
-// A lane takes 16 features (8 bytes of codes and their scale), a warp a
-// token's keys and values, 512 features of each a pass.
+// A lane takes 8 features (4 bytes of codes, 16 bytes out: a warp's store is
+// whole lines), a warp kManyTokens neighbouring tokens' keys and values, 256
+// features of each a pass, all loads of a pass first.
 template <int D>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadParams p) {
-  constexpr int LANES = D / 16, PER = 32 / LANES;
+  constexpr int LANES = D / 8, PER = 32 / LANES;
   pdl_wait();
   const int lane = threadIdx.x & 31, g = lane % LANES, sub = lane / LANES;
-  int64_t t = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.tokens_per_warp;
+  const int64_t t = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.tokens_per_warp;
   const int64_t t_end = t + p.tokens_per_warp < p.T ? t + p.tokens_per_warp : p.T;
   if (t >= p.T) return;
   const int64_t off0 = p.off[0], total = p.off[p.B];
@@ -492,38 +487,48 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
     const __nv_bfloat162 y = __floats2bfloat162_rn(x.x, x.y);
     return *reinterpret_cast<const uint32_t*>(&y);
   };
-  for (; t < t_end; ++t) {
-    const bool placed = pl.at(p, p.starts, t, total);
-    if (!fits(off0, total, p.T, p.hdr) || t >= total) return;
-    if (!placed) continue;
-    const Slot sl = pl.slot;
-    const uint8_t* block = p.pages + sl.page * p.H * (int64_t)lay.bytes();
-    const uint8_t* codes = block + sl.place * lay.code_row + g * 8;
-    const uint8_t* scales = block + lay.scales() + sl.place * lay.scale_row + g;
-    for (int i = 0; i < ph; ++i) {
-      const int head = i * PER + sub;
-      if (head >= p.H) break;
-      const int at = head * lay.bytes();
-      uint2 w[2];
-      uint32_t sc[2];
+  int64_t from[kManyTokens];    // where a token's codes of head 0 lie; -1: nowhere
+  int rel[kManyTokens];         // of its scales, from there
+#pragma unroll
+  for (int n = 0; n < kManyTokens; ++n) {
+    from[n] = -1;
+    if (t + n >= t_end) continue;
+    const bool placed = pl.at(p, p.starts, t + n, total);
+    if (!fits(off0, total, p.T, p.hdr)) return;
+    if (!placed) continue;      // a padded batch's row, or recorded
+    from[n] = pl.slot.page * p.H * (int64_t)lay.bytes() + pl.slot.place * lay.code_row;
+    rel[n] = lay.scales() + pl.slot.place * (lay.scale_row - lay.code_row);
+    if (p.times && lane == 0) p.times[t + n] = p.page_times[(pl.slot.page << p.page_log) + pl.slot.place];
+  }
+  for (int i = 0; i < ph; ++i) {
+    const int head = i * PER + sub;
+    if (head >= p.H) break;
+    uint32_t w[kManyTokens][2];
+    uint32_t sc[kManyTokens][2];
+#pragma unroll
+    for (int n = 0; n < kManyTokens; ++n) {
+      if (from[n] < 0) continue;
+      const uint8_t* codes = p.pages + from[n] + head * lay.bytes();
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        w[x] = *reinterpret_cast<const uint2*>(codes + at + x * lay.half());
-        sc[x] = scales[at + x * lay.half()];
+        w[n][x] = *reinterpret_cast<const uint32_t*>(codes + x * lay.half() + g * 4);
+        sc[n][x] = codes[x * lay.half() + rel[n] + (g >> 1)];
       }
+    }
+#pragma unroll
+    for (int n = 0; n < kManyTokens; ++n) {
+      if (from[n] < 0) continue;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         __nv_bfloat16* dst = x ? p.v : p.k;
         if (!dst) continue;
-        const float s = e4m3_float(sc[x]) * (x ? p.v_scale : p.k_scale);
-        uint4* to = reinterpret_cast<uint4*>(dst + (t * p.H + head) * D + g * 16);
-        to[0] = make_uint4(two(e2m1x2_half2<0>(w[x].x), s), two(e2m1x2_half2<1>(w[x].x), s), two(e2m1x2_half2<2>(w[x].x), s),
-                           two(e2m1x2_half2<3>(w[x].x), s));
-        to[1] = make_uint4(two(e2m1x2_half2<0>(w[x].y), s), two(e2m1x2_half2<1>(w[x].y), s), two(e2m1x2_half2<2>(w[x].y), s),
-                           two(e2m1x2_half2<3>(w[x].y), s));
+        const float s = e4m3_float(sc[n][x]) * (x ? p.v_scale : p.k_scale);
+        const uint32_t c = w[n][x];
+        *reinterpret_cast<uint4*>(dst + ((t + n) * p.H + head) * D + g * 8) =
+            make_uint4(two(e2m1x2_half2<0>(c), s), two(e2m1x2_half2<1>(c), s), two(e2m1x2_half2<2>(c), s),
+                       two(e2m1x2_half2<3>(c), s));
       }
     }
-    if (p.times && lane == 0) p.times[t] = p.page_times[(sl.page << p.page_log) + sl.place];
   }
 }
 

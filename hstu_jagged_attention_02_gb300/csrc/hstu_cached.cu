@@ -231,7 +231,7 @@ hstu_status_t hstu_attn_fwd_cached(const hstu_attn_desc* d, const hstu_cache_des
   p.seq_items = reinterpret_cast<int*>(ws + w.items);
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.T = d->total_tokens; p.B = d->B; p.H = d->H;
-  p.page_size = c->page_size; p.num_pages = c->num_pages; p.max_pages = c->max_pages;
+  p.page_size = c->page_size; p.page_log = c->page_size == 32 ? 5 : (c->page_size == 64 ? 6 : 7); p.num_pages = c->num_pages; p.max_pages = c->max_pages;
   p.max_rows = a->max_rows; p.max_n = d->max_seq_len; p.P = d->num_pos_buckets; p.Tb = d->num_time_buckets;
   p.norm = d->norm; p.alpha = d->alpha; p.inv_n = 1.f / (float)d->max_seq_len; p.eps = d->ln_eps;
   p.k_scale = ldexpf(1.f, c->k_exp);
@@ -242,7 +242,7 @@ hstu_status_t hstu_attn_fwd_cached(const hstu_attn_desc* d, const hstu_cache_des
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   if (e == cudaSuccess)
-    e = N <= 16 ? launch_stream_cached(p, c->d, N, ctas, st) : launch_tc_cached(p, c->d, N, ctas, st);
+    e = N == 8 ? launch_stream_cached(p, c->d, ctas, st) : launch_tc_cached(p, c->d, N, ctas, st);
   if (e == cudaSuccess) {
     const dim3 grid((unsigned)d->total_tokens);
     const bool few = d->total_tokens <= sms;

@@ -39,7 +39,7 @@ struct CachedParams {
   int* seq_items;             // [B] items before it
   int* hdr;
   int64_t T;
-  int B, H, page_size, num_pages, max_pages, max_rows, max_n, P, Tb, norm;
+  int B, H, page_size, page_log, num_pages, max_pages, max_rows, max_n, P, Tb, norm;
   float alpha, inv_n, eps;
   float k_scale;              // 2^k_exp
   float o_scale;              // 2^v_exp / 16 / N of a tensor-core sum
@@ -255,12 +255,12 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s) {
                     mul_half2(e2m1x2_half2<2>(w), s), mul_half2(e2m1x2_half2<3>(w), s));
 }
 
-// Rows of a block: as few as the longest sequence asks for.  Up to 16 rows go
+// Rows of a block: as few as the longest sequence asks for.  Up to 8 rows go
 // through the streaming kernel, more through the tensor-memory one.
 inline int cached_block_rows(int max_rows) {
-  return max_rows <= 8 ? 8 : (max_rows <= 16 ? 16 : (max_rows <= 32 ? 32 : (max_rows <= 64 ? 64 : 128)));
+  return max_rows <= 8 ? 8 : (max_rows <= 32 ? 32 : (max_rows <= 64 ? 64 : 128));
 }
-cudaError_t launch_stream_cached(const CachedParams& p, int d, int N, int ctas, cudaStream_t st);
+cudaError_t launch_stream_cached(const CachedParams& p, int d, int ctas, cudaStream_t st);
 cudaError_t launch_tc_cached(const CachedParams& p, int d, int N, int ctas, cudaStream_t st);
 
 }  // namespace hstu

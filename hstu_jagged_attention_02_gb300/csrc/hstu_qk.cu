@@ -15,7 +15,7 @@
 // The backward's gain gradients are sums over all tokens and heads.  The
 // CTAs walk tokens and keep per-lane FP32 partial sums; the CTAs' rows of
 // partial sums land in the workspace and the CTA that finishes last (a
-// counter in the workspace's header) adds them up in row order in FP64, so
+// counter in the workspace's header) adds them up in row order, their rounding errors carried along, so
 // the result does not depend on the order in which CTAs finish.
 #include <type_traits>
 
@@ -26,7 +26,7 @@ namespace hstu {
 
 namespace {
 
-constexpr int kQkThreads = 256;
+constexpr int kQkThreads = 128;
 constexpr int kBwdThreads = 512;
 constexpr int kPasses = 2;   // 256 features each, of q and of k
 
@@ -50,9 +50,8 @@ struct QkParams {
 };
 
 // The position's row in the tables; one outside them is recorded and row 0 taken.
-__device__ __forceinline__ int64_t checked_position(const QkParams& p, int64_t t) {
-  if (p.rot == 0) return 0;
-  const int64_t pos = p.positions[t];
+__device__ __forceinline__ int checked_position(const QkParams& p, int64_t t) {
+  const int pos = p.positions[t];
   if (pos >= 0 && pos < p.max_pos) return pos;
   set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, (int)(t & 0x7fffffff));
   return 0;
@@ -79,7 +78,7 @@ __device__ __forceinline__ Row8 load_gain(const float* gain, const Parts& pt) {
   return g;
 }
 
-// A warp takes kPasses passes of q's heads and as many of k's, of one token.
+// A warp takes one token, kPasses passes of q's heads and as many of k's.
 template <typename TI, int D>
 __global__ void __launch_bounds__(kQkThreads) qk_fwd_kernel(const __grid_constant__ QkParams p) {
   constexpr int LANES = D / 8, PER = 32 / LANES;
@@ -89,6 +88,8 @@ __global__ void __launch_bounds__(kQkThreads) qk_fwd_kernel(const __grid_constan
   if (t >= live_tokens(p)) return;
   const Parts pt(l, p.rot, p.interleaved);
   const int h0 = blockIdx.y * (kPasses * PER) + sub;
+  int pos = 0;
+  if (pt.turns) pos = checked_position(p, t);   // another load waits for it: first
   Raw4<TI> r0[2][kPasses], r1[2][kPasses];
   auto load = [&](auto W) {
     constexpr int w = decltype(W)::value;
@@ -106,12 +107,12 @@ __global__ void __launch_bounds__(kQkThreads) qk_fwd_kernel(const __grid_constan
   load(std::integral_constant<int, 1>());
   Angles an;
   if (pt.turns) {
-    const int64_t at = checked_position(p, t) * (p.rot >> 1) + 4 * l;
+    const int64_t at = (int64_t)pos * (p.rot >> 1) + 4 * l;
     an.load(p.cos + at, p.sin + at, 1.f);
   }
   auto work = [&](auto W) {
     constexpr int w = decltype(W)::value;
-    if (blockIdx.y * (kPasses * PER) >= p.H[w]) return;
+    if ((int)blockIdx.y * (kPasses * PER) >= p.H[w]) return;
     Row8 gain;
     if (p.norm) gain = load_gain(p.gain[w], pt);
     TI* dst = static_cast<TI*>(p.out[w]) + t * p.os[w][0];
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kBwdThreads) qk_bwd_kernel(const __grid_consta
     load(std::integral_constant<int, 1>());
     Angles an;
     if (pt.turns) {
-      const int64_t at = checked_position(p, t) * (p.rot >> 1) + 4 * l;
+      const int64_t at = (int64_t)checked_position(p, t) * (p.rot >> 1) + 4 * l;
       an.load(p.cos + at, p.sin + at, -1.f);
     }
     auto work = [&](auto W) {
@@ -239,21 +240,31 @@ __global__ void __launch_bounds__(kBwdThreads) qk_bwd_kernel(const __grid_consta
   __syncthreads();
   if (!last) return;
   __threadfence();
-  // 2 D columns, the rows dealt to kBwdThreads / (2 D) groups, each group's sum in FP64
-  double* dred = reinterpret_cast<double*>(&red[0][0][0]);   // WARPS * 2 * D floats >= kBwdThreads doubles
-  static_assert(WARPS * 2 * D >= 2 * kBwdThreads, "the FP64 sums share the FP32 ones' space");
+  // 2 D columns, the rows dealt to kBwdThreads / (2 D) groups; every sum
+  // carries its rounding errors along (two-sum), as FP64 has a 64th of the rate
+  static_assert(WARPS * 2 * D >= 2 * kBwdThreads, "the groups' sums share the warps' space");
   constexpr int GROUPS = kBwdThreads / (2 * D);
   const int col = threadIdx.x % (2 * D), grp = threadIdx.x / (2 * D);
-  double s = 0.0;
+  float sum = 0.f, err = 0.f;
+  auto add = [&](float v) {
+    const float s = sum + v, back = s - sum;
+    err += (sum - (s - back)) + (v - back);
+    sum = s;
+  };
 #pragma unroll 8
-  for (int b = grp; b < (int)gridDim.x; b += GROUPS) s += (double)__ldcg(p.partial + (size_t)b * 2 * D + col);
+  for (int b = grp; b < (int)gridDim.x; b += GROUPS) add(__ldcg(p.partial + (size_t)b * 2 * D + col));
+  float2* pairs = reinterpret_cast<float2*>(&red[0][0][0]);
   __syncthreads();
-  dred[threadIdx.x] = s;
+  pairs[threadIdx.x] = make_float2(sum, err);
   __syncthreads();
   if (grp == 0) {
-    for (int k = 1; k < GROUPS; ++k) s += dred[k * 2 * D + col];
+    for (int k = 1; k < GROUPS; ++k) {
+      const float2 o = pairs[k * 2 * D + col];
+      add(o.x);
+      err += o.y;
+    }
     float* dst = p.dgain[col / D];
-    if (dst) dst[col % D] = (float)s;
+    if (dst) dst[col % D] = sum + err;
   }
   if (threadIdx.x == 0) p.hdr[WS_NEXT] = 0;   // ready for the workspace's next call
 }
