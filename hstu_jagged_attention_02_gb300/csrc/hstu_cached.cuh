@@ -79,41 +79,58 @@ struct Start {
 };
 
 // Every CTA counts all sequences' tiles and finds its own beginning; CTA 0
-// also writes the counts for the finishing kernel.  scan: 2 x THREADS / 32
-// ints in shared memory; the caller synchronises before it reads start.
+// also writes the counts for the finishing kernel.  A thread takes `per`
+// neighbouring sequences (one, unless there are more of them than threads: then
+// nothing is read twice).  scan: 2 x 32 ints in shared memory; the caller
+// synchronises before it reads start.
 template <int THREADS>
 __device__ __forceinline__ void cut_work(const CachedParams& p, int N, int* scan, Start* start) {
+  constexpr int WARPS = THREADS / 32;
+  static_assert(WARPS <= 32, "the warps' sums are added by one warp");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (p.B + THREADS - 1) / THREADS;
   const int lo = min((int)threadIdx.x * per, p.B), hi = min(lo + per, p.B);
-  bool bad = threadIdx.x == 0 && (p.off[0] != 0 || p.off[p.B] > p.T);
+  bool bad = threadIdx.x == THREADS - 1 && (p.off[0] != 0 || p.off[p.B] > p.T);
   int tiles = 0, items = 0;
-  for (int b = lo; b < hi; ++b) {
+  auto count = [&](int b, int& t, int& i) -> bool {
     CachedSeq s;
-    if (!load_seq(p, b, s)) {
+    if (!load_seq(p, b, s)) return false;
+    const int blocks = (s.n + N - 1) / N;
+    t = 0;
+    for (int qb = 0; qb < blocks; ++qb) t += block_tiles(s, qb, N);
+    t *= p.H;
+    i = blocks * p.H;
+    return true;
+  };
+  for (int b = lo; b < hi; ++b) {
+    int t, i;
+    if (!count(b, t, i)) {
       bad = true;
       set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, b);
       break;
     }
-    const int blocks = (s.n + N - 1) / N;
-    for (int qb = 0; qb < blocks; ++qb) tiles += block_tiles(s, qb, N) * p.H;
-    items += blocks * p.H;
+    tiles += t;
+    items += i;
   }
   if (bad) set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, -1);
-  int t = tiles, it = items;
+  auto scan_warp = [&](int& t, int& it) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int a = __shfl_up_sync(0xffffffffu, t, o), c = __shfl_up_sync(0xffffffffu, it, o);
-    if (lane >= o) { t += a; it += c; }
-  }
-  if (lane == 31) { scan[warp] = t; scan[THREADS / 32 + warp] = it; }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, t, o), c = __shfl_up_sync(0xffffffffu, it, o);
+      if (lane >= o) { t += a; it += c; }
+    }
+  };
+  int t = tiles, it = items;
+  scan_warp(t, it);
+  if (lane == 31) { scan[warp] = t; scan[32 + warp] = it; }
   const int any_bad = __syncthreads_or(bad);
-  int total = 0, before = t - tiles, before_items = it - items;
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) { before += scan[w]; before_items += scan[THREADS / 32 + w]; }
-    total += scan[w];
-  }
-  if (any_bad) total = 0;
+  // every warp adds the warps' sums up for itself
+  int wt = lane < WARPS ? scan[lane] : 0, wi = lane < WARPS ? scan[32 + lane] : 0;
+  scan_warp(wt, wi);
+  const int total = any_bad ? 0 : __shfl_sync(0xffffffffu, wt, 31);
+  int before = t - tiles, before_items = it - items;
+  const int pt = __shfl_sync(0xffffffffu, wt, max(warp - 1, 0)), pi = __shfl_sync(0xffffffffu, wi, max(warp - 1, 0));
+  if (warp > 0) { before += pt; before_items += pi; }
   const int quota = (total + (int)gridDim.x - 1) / (int)gridDim.x;
   const int first = (int)blockIdx.x * quota;
   if (threadIdx.x == 0) {
@@ -121,29 +138,36 @@ __device__ __forceinline__ void cut_work(const CachedParams& p, int N, int* scan
     start->quota = quota;
     if (blockIdx.x == 0) p.hdr[WS_CA_QUOTA] = any_bad ? -1 : quota;
   }
-  const bool mine = !any_bad && first < total && before <= first && first < before + tiles;
-  if (mine || (blockIdx.x == 0 && !any_bad)) {
-    int at = before, ai = before_items;
+  if (any_bad) return;
+  const bool mine = first < total && before <= first && first < before + tiles;
+  if (per == 1) {
+    if (lo < hi && blockIdx.x == 0) {
+      p.seq_tiles[lo] = before;
+      p.seq_items[lo] = before_items;
+    }
+    if (mine) {
+      start->b = lo;
+      start->rem = first - before;
+      start->items = before_items;
+    }
+  } else if (mine || blockIdx.x == 0) {
     bool found = false;
     for (int b = lo; b < hi; ++b) {
-      CachedSeq s;
-      load_seq(p, b, s);
-      const int blocks = (s.n + N - 1) / N;
-      int here = 0;
-      for (int qb = 0; qb < blocks; ++qb) here += block_tiles(s, qb, N) * p.H;
+      int here, i;
+      count(b, here, i);
       if (blockIdx.x == 0) {
-        p.seq_tiles[b] = at;
-        p.seq_items[b] = ai;
+        p.seq_tiles[b] = before;
+        p.seq_items[b] = before_items;
       }
-      if (mine && !found && first < at + here) {
+      if (mine && !found && first < before + here) {
         start->b = b;
-        start->rem = first - at;
-        start->items = ai;
+        start->rem = first - before;
+        start->items = before_items;
         found = true;
         if (blockIdx.x != 0) break;
       }
-      at += here;
-      ai += blocks * p.H;
+      before += here;
+      before_items += i;
     }
   }
 }
@@ -254,6 +278,13 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s) {
   return make_uint4(mul_half2(e2m1x2_half2<0>(w), s), mul_half2(e2m1x2_half2<1>(w), s),
                     mul_half2(e2m1x2_half2<2>(w), s), mul_half2(e2m1x2_half2<3>(w), s));
 }
+
+// Number of binary digits of |a - b|: the time bucket before it is cut to Tb - 1.
+__device__ __forceinline__ int bit_length(int64_t a, int64_t b) {
+  const uint64_t d = a >= b ? (uint64_t)a - (uint64_t)b : (uint64_t)b - (uint64_t)a;
+  return 64 - __clzll((long long)d);
+}
+constexpr int kTimeSlots = 65;   // bit lengths 0 .. 64
 
 // Rows of a block: as few as the longest sequence asks for.  Up to 8 rows go
 // through the streaming kernel, more through the tensor-memory one.

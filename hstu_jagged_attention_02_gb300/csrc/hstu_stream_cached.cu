@@ -19,10 +19,14 @@
 // parities, half as many bank conflicts.  q stays in registers (FP16, scaled
 // per row by a power of two: hstu_cached.cuh), so does O.
 //
-// One warp copies pages, whole (page, head) blocks by cp.async.bulk, into a
-// ring of NR tiles of 128 tokens; the other warps, 8 to a tile, deal the tiles
-// among themselves and add their sums up in shared memory at a piece's end.
-// Every wait is bounded.
+// A piece's 16-token steps are dealt to the warps in turn.  Each warp copies its
+// own steps ahead (cp.async, three in flight) into a ring of its own, so that no
+// warp waits for another; one warp that copied for all of them took 1,650
+// cycles a tile to issue the copies, twice what the others take to use them.  One more warp
+// walks the CTA's pieces and prepares their records (the rows in FP16, their
+// factors, the head's time biases) a few pieces ahead.  At a piece's end each
+// warp leaves its sum in shared memory and goes on; the last one adds them up,
+// in the warps' order.  Every wait on a barrier is bounded.
 #include "hstu_cached.cuh"
 #include "tc_ptx.cuh"
 
@@ -34,32 +38,47 @@ using namespace tc;
 
 constexpr int kRows = 8;       // of a block
 
-// A piece of an item, as the copying warp hands it to the others.
+// A piece of an item, as its record goes to the warps.
 template <int D>
 struct __align__(16) SPiece {
   uint2 q[D / 16][32];         // the products' right operands, a lane's two registers an inner step
   int64_t tq[kRows], tmin, tmax;   // the rows' times and their range
   float ka[kRows];             // score factors
+  float time_bias[kTimeSlots]; // of the head by bucket, times -log2(e)
+  float far_bias;              // of the head's last position bucket, so too
+  const int32_t* table;        // the sequence's pages
   int valid;                   // 0: no more pieces
-  int h, rows, hist;           // head; rows of the block, history rows among them
+  int b, h, rows, hist;        // sequence, head; rows of the block, history rows among them
   int pos0, L;                 // position of its first row, cached tokens
-  int tile0, tile1, slot;
+  int step0, step1, slot;      // 16-token steps; where the sum goes
 };
 
 template <int D>
 struct SCfg {
-  static constexpr int GROUPS = 3;                  // of 8 warps: 25 warps, 7 a sub-partition
-  static constexpr int REGS = 72;
-  static constexpr int WARPS = 8 * GROUPS, THREADS = (WARPS + 1) * 32;
-  static constexpr int TILE_BYTES = 2 * kCachedTile * (D / 2 + D / 16);
-  static constexpr int NR = D == 128 ? 5 : 8;
-  static constexpr int SUM_OFF = NR * TILE_BYTES;                     // float [WARPS][kRows][D]: the warps' sums
-  static constexpr int TS_OFF = SUM_OFF + WARPS * kRows * D * 4;      // int64 [NR][128]
-  static constexpr int PIECE_OFF = TS_OFF + NR * kCachedTile * 8;     // SPiece [2]
-  static constexpr int BAR_OFF = PIECE_OFF + 2 * (int)sizeof(SPiece<D>);   // full, empty [NR], pieces full, empty [2]
-  static constexpr int BYTES = BAR_OFF + (2 * NR + 4) * 8;
+  static constexpr int WARPS = 16, THREADS = (WARPS + 1) * 32;        // 17 warps, 5 a sub-partition
+  static constexpr int REGS = 96;
+  static constexpr int DEPTH = 3;                                     // steps in flight a warp
+  static constexpr int PIECES = DEPTH + 1;   // records: a warp's copies run up to DEPTH pieces ahead of its work
+  // a step: K codes, V codes, K scales, V scales, times
+  static constexpr int CODES = 16 * (D / 2), SCALES = 16 * (D / 16);
+  static constexpr int STEP_V = CODES, STEP_KS = 2 * CODES, STEP_VS = STEP_KS + SCALES, STEP_T = STEP_VS + SCALES;
+  static constexpr int STEP = STEP_T + 128;
+  static constexpr int SUM_OFF = WARPS * DEPTH * STEP;                // float [WARPS][kRows][D], or of half the rows twice
+  static constexpr int PIECE_OFF = SUM_OFF + WARPS * kRows * D * 4;   // SPiece [PIECES]
+  static constexpr int BAR_OFF = PIECE_OFF + PIECES * (int)sizeof(SPiece<D>);   // records full, empty; sums free [2]
+  static constexpr int BYTES = BAR_OFF + (2 * PIECES + 2) * 8;
   static_assert(BYTES <= (int)kMaxSmemPerCta - 1024, "one CTA's shared memory");
+  static_assert(STEP % 128 == 0, "a warp's ring keeps its alignment");
 };
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -90,18 +109,19 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[W]) {
 // The token of row r (0 .. 7) of a matrix instruction.
 __device__ __forceinline__ int token_of(int r) { return ((r & 3) << 1) | (r >> 2); }
 
-// Where a lane's parts of a step lie in a (page, head) block.
+// Where a lane's parts of a step lie in its ring slot.
 template <int D>
 struct LaneOffsets {
+  using C = SCfg<D>;
   int k, ks, v[2], vs[2];
-  __device__ __forceinline__ LaneOffsets(const PageLayout& lay, int lane) {
+  __device__ __forceinline__ explicit LaneOffsets(int lane) {
     const int g = lane >> 2, t = lane & 3;
     k = token_of(g) * (D / 2) + t * (D / 8);
-    ks = lay.scales() + token_of(g) * (D / 16) + t * (D / 64);
+    ks = C::STEP_KS + token_of(g) * (D / 16) + t * (D / 64);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      v[i] = lay.half() + token_of(2 * t + i) * (D / 2) + g * (D / 16);
-      vs[i] = lay.half() + lay.scales() + token_of(2 * t + i) * (D / 16) + (g * (D / 8)) / 16;
+      v[i] = C::STEP_V + token_of(2 * t + i) * (D / 2) + g * (D / 16);
+      vs[i] = C::STEP_VS + token_of(2 * t + i) * (D / 16) + (g * (D / 8)) / 16;
     }
   }
 };
@@ -143,17 +163,22 @@ __device__ __forceinline__ void write_piece(const CachedParams& p, const Walk& w
     tmax = b > tmax ? b : tmax;
   }
   if (lane < kRows) out.tq[lane] = tq;
+  for (int e = lane; e < kTimeSlots; e += 32)
+    out.time_bias[e] = p.rab_time ? -kLog2e * p.rab_time[w.h * p.Tb + min(e, p.Tb - 1)] : 0.f;
   if (lane == 0) {
     out.tmin = tmin;
     out.tmax = tmax;
     out.valid = 1;
+    out.far_bias = p.rab_pos ? -kLog2e * p.rab_pos[w.h * p.P + p.P - 1] : 0.f;
     out.h = w.h;
     out.rows = rows;
     out.hist = max(0, min(hist - r0, rows));
     out.pos0 = w.s.L - hist + r0;
     out.L = w.s.L;
-    out.tile0 = w.tile;
-    out.tile1 = w.tile + w.take();
+    out.b = w.b;
+    out.table = p.table + (int64_t)w.b * p.max_pages;
+    out.step0 = w.tile * (kCachedTile / 16);
+    out.step1 = min((w.tile + w.take()) * (kCachedTile / 16), (w.s.L + 15) / 16);
     out.slot = w.slot(p);
   }
   __syncwarp();
@@ -164,24 +189,23 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
   using C = SCfg<D>;
   constexpr int MT = D / 16;             // 16-feature tiles of O
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int scan[2 * (C::WARPS + 1)];
+  __shared__ int scan[64];
   __shared__ Start start;
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, left_sums[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint32_t smem0 = smem_u32(smem);
-  auto full = [&](uint32_t i) -> uint32_t { return smem0 + C::BAR_OFF + 8 * i; };
-  auto empty = [&](uint32_t i) -> uint32_t { return smem0 + C::BAR_OFF + 8 * (C::NR + i); };
-  auto piece_full = [&](uint32_t i) -> uint32_t { return smem0 + C::BAR_OFF + 8 * (2 * C::NR + i); };
-  auto piece_empty = [&](uint32_t i) -> uint32_t { return smem0 + C::BAR_OFF + 8 * (2 * C::NR + 2 + i); };
+  auto piece_full = [&](uint32_t i) -> uint32_t { return smem0 + C::BAR_OFF + 8 * i; };
+  auto piece_empty = [&](uint32_t i) -> uint32_t { return smem0 + C::BAR_OFF + 8 * (C::PIECES + i); };
+  auto sum_free = [&](uint32_t i) -> uint32_t { return smem0 + C::BAR_OFF + 8 * (2 * C::PIECES + i); };
   SPiece<D>* pieces = reinterpret_cast<SPiece<D>*>(smem + C::PIECE_OFF);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::NR; ++i) {
-      mbar_init(full(i), 1);
-      mbar_init(empty(i), 8);
-    }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::PIECES; ++i) {
       mbar_init(piece_full(i), 1);
       mbar_init(piece_empty(i), C::WARPS);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sum_free(i), 1);
+      left_sums[i] = 0;
     }
     abort_flag = 0;
     fence_mbar_init();
@@ -195,125 +219,132 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
   wd.err = p.hdr + WS_ERR;
   wd.err_info = p.hdr + WS_ERR_INFO;
   wd.limit_ns = 2000000000ull;
-  const PageLayout lay(p.page_size, D);
-  uint32_t rs = 0, ring = 0;             // stage of the ring, and the parity of its round
-  uint32_t np = 0;                       // pieces so far
 
   if (warp == C::WARPS) {
-    // ------------------------------------------------- pieces, page copies
+    // ------------------------------------------------------------- records
     Walk w;
     w.begin(p, start, kRows);
-    const int ppt_log = 7 - p.page_log, ppt = 1 << ppt_log;
-    uint32_t used = 0;                   // stages used at all
     bool ok = true;
-    while (ok) {
-      if (lane == 0) ok = mbar_wait(piece_empty(np & 1), ((np >> 1) & 1) ^ 1, wd, 91);
+    for (uint32_t np = 0; ok; ++np) {
+      const uint32_t at = np % C::PIECES;
+      if (lane == 0) ok = mbar_wait(piece_empty(at), ((np / C::PIECES) & 1) ^ 1, wd, 91);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
-      SPiece<D>& pc = pieces[np & 1];
       const bool some = w.left > 0;
-      if (some) write_piece<D>(p, w, pc);
-      else if (lane == 0) pc.valid = 0;
-      if (lane == 0) mbar_arrive(piece_full(np & 1));
-      ++np;
+      if (some) write_piece<D>(p, w, pieces[at]);
+      else if (lane == 0) pieces[at].valid = 0;
+      if (lane == 0) mbar_arrive(piece_full(at));
       if (!some) break;
-      const int t1 = w.tile + w.take();
-      // the block table's entries, 32 at a time: lane i holds entry e0 + i
-      const int32_t* row = p.table + (int64_t)w.b * p.max_pages;
-      const int npages = (w.s.L + p.page_size - 1) >> p.page_log;
-      int e0 = w.tile << ppt_log;
-      int32_t entry = e0 + lane < npages ? row[e0 + lane] : -1;
-      int32_t next = e0 + 32 + lane < npages ? row[e0 + 32 + lane] : -1;
-      for (int tile = w.tile; tile < t1; ++tile) {
-        const int e = tile << ppt_log;
-        if (e >= e0 + 32) {
-          e0 += 32;
-          entry = next;
-          next = e0 + 32 + lane < npages ? row[e0 + 32 + lane] : -1;
-        }
-        // lanes 0 .. ppt - 1: a page's block each; the next ppt lanes: its times
-        const int pg = lane & (ppt - 1);
-        const int id = __shfl_sync(0xffffffffu, entry, (e - e0 + pg) & 31);
-        const bool there = lane < 2 * ppt && e + pg < npages;
-        const bool good = there && id >= 0 && id < p.num_pages;
-        if (there && !good) set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, w.b);
-        const int n = __popc(__ballot_sync(0xffffffffu, good && lane < ppt));
-        if (lane == 0) {
-          ok = mbar_wait(empty(rs), ring ^ 1, wd, 92);
-          if (ok) mbar_arrive_expect_tx(full(rs), (uint32_t)(n * (lay.bytes() + (p.times ? p.page_size * 8 : 0))));
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        if (good && lane < ppt)
-          bulk_load(smem0 + rs * C::TILE_BYTES + pg * lay.bytes(), p.pages + ((int64_t)id * p.H + w.h) * lay.bytes(),
-                    (uint32_t)lay.bytes(), full(rs));
-        else if (good && p.times)
-          bulk_load(smem0 + C::TS_OFF + rs * (kCachedTile * 8) + pg * p.page_size * 8,
-                    p.page_times + ((int64_t)id << p.page_log), (uint32_t)(p.page_size * 8), full(rs));
-        if (used < (uint32_t)C::NR) ++used;
-        if (++rs == C::NR) {
-          rs = 0;
-          ring ^= 1;
-        }
-      }
       w.next(p, kRows);
-    }
-    // no copy may land in shared memory after the CTA's end: the last round of every stage
-    if (lane == 0) {
-      for (uint32_t i = 0; i < used; ++i) {
-        const uint32_t parity = i < rs ? ring : ring ^ 1;
-        const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(full(i), parity))
-          if (globaltimer() - t0 > 200000000ull) break;
-      }
     }
     return;
   }
 
-  const int group = warp >> 3, local = (warp & 7) * 16;    // of the tiles; this warp's tokens in a tile
-  int turn = 0;                                            // the group whose turn the next tile is
-  const LaneOffsets<D> at(lay, lane);
-  const int in_tile = (local >> p.page_log) * lay.bytes();
-  const int place = local & (p.page_size - 1);
-  const uint32_t code0 = in_tile + place * (D / 2), scale0 = in_tile + place * (D / 16);
+  const LaneOffsets<D> at(lane);
   float* sums = reinterpret_cast<float*>(smem + C::SUM_OFF);
-  bool ok = true;
-  for (;; ++np) {
-    ok = mbar_wait(piece_full(np & 1), (np >> 1) & 1, wd, 93);
-    const SPiece<D>& pc = pieces[np & 1];
-    const bool some = ok && pc.valid;
-    const int rows = some ? pc.rows : 0, slot = pc.slot;
+  const uint8_t* ring = smem + warp * (C::DEPTH * C::STEP);
+  const uint32_t ring0 = smem0 + warp * (C::DEPTH * C::STEP);
+  const int spp_log = p.page_log - 4;    // 16-token steps of a page
+  bool ok = true, wide = false;          // wide: the last piece's sums took the whole space
+
+  // The copies run ahead of the work: `issued` and `worked` steps of this warp
+  // so far; the next one to copy, if it is known yet (have), is ist of piece
+  // ip - 1, its page on its way.  Looking for it never waits: a record that is not there yet
+  // may be waiting for this warp's work on an older piece.
+  uint32_t issued = 0, worked = 0, ip = 0;
+  int ist = 0, ilast = 0, ifirst = warp, ipage = 0, ih = 0, ib = 0;
+  const int32_t* itable = nullptr;
+  bool have = false;
+  const PageLayout lay(p.page_size, D);
+  auto look = [&]() -> bool {
+    while (!have) {
+      if (!__all_sync(0xffffffffu, mbar_test_wait(piece_full(ip % C::PIECES), (ip / C::PIECES) & 1))) return false;
+      const SPiece<D>& pc = pieces[ip % C::PIECES];
+      if (!pc.valid) return false;
+      ist = pc.step0 + ifirst;
+      ilast = pc.step1;
+      ++ip;
+      have = ist < ilast;
+      if (have) {
+        itable = pc.table;
+        ih = pc.h;
+        ib = pc.b;
+        ipage = __ldg(itable + (ist >> spp_log));
+      } else {
+        ifirst = ist - ilast;
+      }
+    }
+    return true;
+  };
+  auto fill = [&]() {
+    while (issued - worked < (uint32_t)C::DEPTH && look()) {
+      if (ipage >= 0 && ipage < p.num_pages) {
+        const int place = (ist & ((1 << spp_log) - 1)) << 4;
+        const uint8_t* block = p.pages + ((int64_t)ipage * p.H + ih) * lay.bytes();
+        const uint8_t* codes = block + place * (D / 2) + lane * 16;
+        const uint32_t dst = ring0 + (issued % C::DEPTH) * C::STEP + lane * 16;
+#pragma unroll
+        for (int i = 0; i < C::CODES / 512; ++i) {
+          copy16(dst + 512 * i, codes + 512 * i);
+          copy16(dst + C::STEP_V + 512 * i, codes + lay.half() + 512 * i);
+        }
+        constexpr int NS = C::SCALES / 16;   // lanes that copy K scales, V scales; 8 more the times
+        const uint8_t* scales = block + lay.scales() + place * (D / 16) + lane * 16;
+        if (lane < NS) copy16(dst + C::STEP_KS, scales);
+        else if (lane < 2 * NS) copy16(dst + C::STEP_KS, scales + lay.half() - C::SCALES);
+        else if (lane < 2 * NS + 8 && p.times)
+          copy16(dst + C::STEP_KS, reinterpret_cast<const uint8_t*>(p.page_times + ((int64_t)ipage << p.page_log) + place) +
+                                       (lane - 2 * NS) * 16);
+      } else if (lane == 0) {
+        set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, ib);
+      }
+      copy_commit();
+      ++issued;
+      ist += C::WARPS;
+      have = ist < ilast;
+      if (have) ipage = __ldg(itable + (ist >> spp_log));
+      else ifirst = ist - ilast;
+    }
+  };
+
+  int first = warp;                      // steps of the next piece before this warp's first
+  for (uint32_t np = 0;; ++np) {
+    ok = mbar_wait(piece_full(np % C::PIECES), (np / C::PIECES) & 1, wd, 93);
+    const SPiece<D>& pc = pieces[np % C::PIECES];
+    if (!ok || !pc.valid) break;
+    __syncwarp();
+    const int rows = pc.rows, slot = pc.slot;
+    if (!have && ip <= np) {             // (pieces in between had no step for this warp)
+      ip = np;
+      ifirst = first;
+    }
+    fill();
     float o[MT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
-    if (some) {
+    {
       const int len = pc.L, pos0 = pc.pos0, nh = pc.hist;  // (rows behind the history rows are at len)
       const int pmin = nh > 0 ? pos0 : len, pmax = nh == rows ? pos0 + rows - 1 : len;
-      const bool one_bias = pmin == pmax && pc.tmin == pc.tmax;    // all rows at one place and time
+      const bool one_time = !p.rab_time || pc.tmin == pc.tmax;
+      const float far_bias = pc.far_bias;
       const float* rp = p.rab_pos ? p.rab_pos + pc.h * p.P : nullptr;
-      const float* rt = p.rab_time ? p.rab_time + pc.h * p.Tb : nullptr;
-      const int t1 = pc.tile1;
+      const int step1 = pc.step1;
+      int step = pc.step0 + first;
 #pragma unroll 1
-      for (int tile = pc.tile0; tile < t1; ++tile) {
-        const uint32_t stage = rs, parity = ring;
-        if (++rs == C::NR) {
-          rs = 0;
-          ring ^= 1;
-        }
-        const bool mine = turn == group;
-        if (++turn == C::GROUPS) turn = 0;
-        if (!mine) continue;
-        ok = mbar_wait(full(stage), parity, wd, 94);
-        if (!ok) break;
-        const int j16 = tile * kCachedTile + local;        // first token of the step
-        if (j16 < len) {
-          const uint8_t *codes = smem + stage * C::TILE_BYTES + code0, *scales = smem + stage * C::TILE_BYTES + scale0;
+      for (; step < step1; step += C::WARPS) {
+        // the oldest of DEPTH copies; with fewer under way, all of them
+        if (issued - worked == (uint32_t)C::DEPTH) copy_wait<C::DEPTH - 1>();
+        else copy_wait<0>();
+        __syncwarp();
+        const uint8_t* part = ring + (worked % C::DEPTH) * C::STEP;
+        const int j16 = step * 16;                         // first token of the step
+        {
           float c[2][4] = {};     // two chains of products, added at their end
           {
             uint32_t k0[D / 32], k1[D / 32];
-            load_words<D / 32>(codes + at.k, k0);
-            load_words<D / 32>(codes + at.k + 8 * (D / 2), k1);
-            const uint8_t* ks = scales + at.ks;
+            load_words<D / 32>(part + at.k, k0);
+            load_words<D / 32>(part + at.k + 8 * (D / 2), k1);
+            const uint8_t* ks = part + at.ks;
             const __half2 s0 = e4m3x2_half2(D == 128 ? *reinterpret_cast<const uint16_t*>(ks) : *ks);
             const __half2 s1 = e4m3x2_half2(D == 128 ? *reinterpret_cast<const uint16_t*>(ks + 8 * (D / 16)) : ks[8 * (D / 16)]);
 #pragma unroll
@@ -331,24 +362,22 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
           // a lane looks up the bias of token lane % 16 towards the block's rows, if they share it
           const int jl = j16 + (lane & 15);
           int64_t tl = 0;
-          if (p.times) tl = reinterpret_cast<const int64_t*>(smem + C::TS_OFF + stage * (kCachedTile * 8))[local + (lane & 15)];
+          if (p.times) tl = reinterpret_cast<const int64_t*>(part + C::STEP_T)[lane & 15];
           bool same = jl <= pmin;
-          float bl = 0.f;
-          if (rp) {
+          float bl = far_bias;
+          if (pmin - (j16 + 15) < p.P - 1 && rp) {         // near tokens: their buckets' own biases, from global memory
             const int a = min(max(pmin - jl, 0), p.P - 1);
-            bl = __ldg(rp + a);
-            if (!one_bias) same = same && a == min(max(pmax - jl, 0), p.P - 1);
+            bl = -kLog2e * __ldg(rp + a);
+            same = same && a == min(max(pmax - jl, 0), p.P - 1);
           }
-          if (rt) {
-            const int64_t tmin = pc.tmin;
-            const int a = time_bucket(tmin, tl, p.Tb);
-            bl += __ldg(rt + a);
-            if (!one_bias) {
-              const int64_t tmax = pc.tmax;
-              same = same && a == time_bucket(tmax, tl, p.Tb) && (tl <= tmin || tl >= tmax);
+          {
+            const int a = bit_length(pc.tmin, tl);
+            bl += pc.time_bias[a];
+            if (!one_time) {
+              const int64_t tmin = pc.tmin, tmax = pc.tmax;
+              same = same && min(a, p.Tb - 1) == min(bit_length(tmax, tl), p.Tb - 1) && (tl <= tmin || tl >= tmax);
             }
           }
-          bl *= -kLog2e;
           // scores of tokens j0 (c[0], c[1]) and j0 + 8 (c[2], c[3]) for rows 2t, 2t + 1
           const int j0 = j16 + token_of(g);
           uint32_t pr[2];
@@ -367,10 +396,8 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
 #pragma unroll
               for (int f = 0; f < 2; ++f) {
                 const int r = 2 * t + f, pos = r < nh ? pos0 + r : len;
-                b[f] = 0.f;
-                if (rp) b[f] = rp[min(max(pos - j, 0), p.P - 1)];
-                if (rt) b[f] += rt[time_bucket(pc.tq[r], tj, p.Tb)];
-                b[f] *= -kLog2e;
+                b[f] = pc.time_bias[bit_length(pc.tq[r], tj)];
+                if (rp) b[f] = fmaf(-kLog2e, rp[min(max(pos - j, 0), p.P - 1)], b[f]);
                 keep |= j <= pos ? 0xffffu << (16 * f) : 0u;
               }
               const float2 cc = e ? make_float2(c[0][2], c[0][3]) : make_float2(c[0][0], c[0][1]);
@@ -381,7 +408,7 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
           }
           uint32_t vs[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) vs[e] = scales[at.vs[e & 1] + 8 * (e >> 1) * (D / 16)];
+          for (int e = 0; e < 4; ++e) vs[e] = part[at.vs[e & 1] + 8 * (e >> 1) * (D / 16)];
           if (j16 + 16 > len) {                            // tokens behind the cache's end: neither scores nor values
 #pragma unroll
             for (int e = 0; e < 2; ++e) pr[e] = j0 + 8 * e < len ? pr[e] : 0u;
@@ -394,7 +421,7 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
           const __half2 s01 = e4m3x2_half2(vs[0] | (vs[1] << 8)), s23 = e4m3x2_half2(vs[2] | (vs[3] << 8));
           uint32_t v[4][D / 64];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) load_words<D / 64>(codes + at.v[e & 1] + 8 * (e >> 1) * (D / 2), v[e]);
+          for (int e = 0; e < 4; ++e) load_words<D / 64>(part + at.v[e & 1] + 8 * (e >> 1) * (D / 2), v[e]);
 #pragma unroll
           for (int x = 0; x < D / 64; ++x) {               // 8 features of the lane's D / 8
             auto even = [](uint32_t a, uint32_t b) { return (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u); };
@@ -408,36 +435,56 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(empty(stage));
+        ++worked;
+        fill();
       }
+      first = step - step1;
     }
-    // the warps' sums: o[m] holds features g D/8 + 2m, + 1 of rows 2t, 2t + 1
+    // the piece's record is free once every warp has read it
+    __syncwarp();
+    if (lane == 0) mbar_arrive(piece_empty(np % C::PIECES));
+    // the warps' sums: o[m] holds features g D/8 + 2m, + 1 of rows 2t, 2t + 1.  Up to 4 rows leave room for two
+    // pieces' sums, so that a warp goes on to the next piece while others finish this one; the last warp to leave
+    // its sum adds them all up.
+    const uint32_t nbuf = rows <= kRows / 2 ? 2u : 1u;
+    float* mine = sums + (nbuf == 2 ? (np & 1) * (C::WARPS * (kRows / 2) * D) : 0);
+    // the buffer's previous piece, np - 2 (or the one before this, with more rows), has been added up
+    ok = mbar_wait(sum_free(np & 1), ((np >> 1) & 1) ^ 1, wd, 95) &&
+         (nbuf == 2 && !wide ? true : np == 0 || mbar_wait(sum_free((np - 1) & 1), ((np - 1) >> 1) & 1, wd, 96));
+    if (!ok) break;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = 2 * t + e;
       if (r < rows) {
-        float* dst = sums + (warp * kRows + r) * D + g * (D / 8);
+        float* dst = mine + (warp * rows + r) * D + g * (D / 8);
 #pragma unroll
         for (int m = 0; m < MT; ++m) *reinterpret_cast<float2*>(dst + 2 * m) = make_float2(o[m][e], o[m][2 + e]);
       }
     }
-    // the warps meet; at the end, or if one of them has given up, all leave
-    uint32_t leave;
-    asm volatile("{\n\t.reg .pred q, r;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred r, 1, %2, q;\n\tselp.u32 %0, 1, 0, r;\n\t}"
-                 : "=r"(leave)
-                 : "r"(ok && some ? 0u : 1u), "n"(C::WARPS * 32)
-                 : "memory");
-    if (leave) break;
-    if (lane == 0) mbar_arrive(piece_empty(np & 1));
-    float* part = p.part + (int64_t)slot * (kRows * D);
-    for (int e = threadIdx.x; e < rows * D; e += C::WARPS * 32) {
-      float x = 0.f;
-#pragma unroll
-      for (int k = 0; k < C::WARPS; ++k) x += sums[k * kRows * D + e];
-      part[e] = x;
+    wide = nbuf == 1;
+    __threadfence_block();
+    __syncwarp();
+    int done = 0;
+    if (lane == 0) done = atomicAdd(&left_sums[np & 1], 1);
+    done = __shfl_sync(0xffffffffu, done, 0);
+    if (done == C::WARPS - 1) {
+      __threadfence_block();
+      float* part = p.part + (int64_t)slot * (kRows * D);
+      for (int e = lane * 4; e < rows * D; e += 128) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = 0; k < C::WARPS; ++k) {
+          const float4 y = *reinterpret_cast<const float4*>(mine + k * rows * D + e);
+          x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+        }
+        *reinterpret_cast<float4*>(part + e) = x;
+      }
+      if (lane == 0) left_sums[np & 1] = 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sum_free(np & 1));
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(C::WARPS * 32) : "memory");
   }
+  copy_wait<0>();
 }
 
 template <int D>

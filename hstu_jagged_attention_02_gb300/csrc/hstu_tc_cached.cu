@@ -64,7 +64,8 @@ struct Cfg {
   static constexpr int TS_OFF = RAW_OFF + NR * RAW_BYTES;
   static constexpr int QT_OFF = TS_OFF + NT * TILE * 8;    // int64 [ITEMS][N] row times
   static constexpr int KA_OFF = QT_OFF + ITEMS * N * 8;    // float [ITEMS][N] score factors
-  static constexpr int SLOT_OFF = KA_OFF + ITEMS * N * 4;
+  static constexpr int TB_OFF = KA_OFF + ITEMS * N * 4;    // float [ITEMS][kTimeSlots + 1] time biases, the far position's
+  static constexpr int SLOT_OFF = (TB_OFF + ITEMS * (kTimeSlots + 1) * 4 + 15) / 16 * 16;
   // barriers
   static constexpr int RAWFULL = 0, RAWEMPTY = RAWFULL + NR, TSFULL = RAWEMPTY + NR, TSEMPTY = TSFULL + NT,
                        ITEMFULL = TSEMPTY + NT, ITEMEMPTY = ITEMFULL + ITEMS, QTFULL = ITEMEMPTY + ITEMS,
@@ -151,10 +152,11 @@ __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedP
   auto piece_at = [&](uint32_t i) -> Piece& { return *reinterpret_cast<Piece*>(base + L::SLOT_OFF + 96 * (int)i); };
   int64_t* qt = reinterpret_cast<int64_t*>(base + L::QT_OFF);
   float* kA = reinterpret_cast<float*>(base + L::KA_OFF);
+  float* tb = reinterpret_cast<float*>(base + L::TB_OFF);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base + L::MISC_OFF + 4);
   Start* start = reinterpret_cast<Start*>(base + L::MISC_OFF + 16);
-  int* scan = reinterpret_cast<int*>(base + L::MISC_OFF + 64);   // [2][kThreads / 32] warp sums
+  int* scan = reinterpret_cast<int*>(base + L::MISC_OFF + 64);   // [2][32] warp sums
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -308,6 +310,11 @@ __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedP
           const int r = i * RPP + sub / LR;
           x[i] = make_uint4(0, 0, 0, 0);
           if (r < rows) x[i] = *reinterpret_cast<const uint4*>(p.q + ((row0 + r) * p.H + h) * D + c * 8);
+        }
+        if (dw == 1) {   // the head's biases, times -log2(e)
+          for (int e = lane; e < kTimeSlots; e += 32)
+            tb[sl * (kTimeSlots + 1) + e] = p.rab_time ? -kLog2e * p.rab_time[h * p.Tb + min(e, p.Tb - 1)] : 0.f;
+          if (lane == 0) tb[sl * (kTimeSlots + 1) + kTimeSlots] = p.rab_pos ? -kLog2e * p.rab_pos[h * p.P + p.P - 1] : 0.f;
         }
         if (dw == 0) {   // the rows' times, and their range
           int64_t mn = INT64_MAX, mx = INT64_MIN;
@@ -509,7 +516,8 @@ __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedP
       const int64_t tmin = pc.tmin, tmax = pc.tmax;
       const int pmin = hist > 0 ? pos0 : len, pmax = hist == rows ? pos0 + rows - 1 : len;
       const float* rp = p.rab_pos ? p.rab_pos + pc.h * p.P : nullptr;
-      const float* rt = p.rab_time ? p.rab_time + pc.h * p.Tb : nullptr;
+      const float* tbl = tb + sl * (kTimeSlots + 1);
+      const bool one_time = !p.rab_time || tmin == tmax;
       const float* ka = kA + sl * N + half * COLS;
       const int64_t* tq = qt + sl * N + half * COLS;
       for (int t = t0; t < t1; ++t, ++tk) {
@@ -522,19 +530,19 @@ __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedP
           tj = *reinterpret_cast<const int64_t*>(base + L::TS_OFF + ts * (TILE * 8) + r * 8);
         }
         // one bias for all of the block's rows?
-        float bias = 0.f;
-        bool same = j >= len || j <= pmin;
-        if (rp) {
-          const int a = min(max(pmin - j, 0), p.P - 1), b = min(max(pmax - j, 0), p.P - 1);
-          same = same && (a == b || j >= len);
-          bias = rp[a];
+        bool same = j <= pmin;
+        float bias = tbl[kTimeSlots];                      // far tokens share the last position bucket
+        if (pmin - (t * TILE + wq * 32 + 31) < p.P - 1 && rp) {
+          const int a = min(max(pmin - j, 0), p.P - 1);
+          same = same && a == min(max(pmax - j, 0), p.P - 1);
+          bias = -kLog2e * __ldg(rp + a);
         }
-        if (rt) {
-          const int a = time_bucket(tmin, tj, p.Tb), b = time_bucket(tmax, tj, p.Tb);
-          same = same && ((a == b && (tj <= tmin || tj >= tmax)) || j >= len);
-          bias += rt[a];
+        {
+          const int a = bit_length(tmin, tj);
+          bias += tbl[a];
+          if (!one_time) same = same && min(a, p.Tb - 1) == min(bit_length(tmax, tj), p.Tb - 1) && (tj <= tmin || tj >= tmax);
         }
-        bias *= -kLog2e;
+        same = same || j >= len;
         const bool fast = __all_sync(0xffffffffu, same);
         const bool whole = __all_sync(0xffffffffu, j < len);
         ok = mbar_wait(bar(L::SFULL + st), (tk >> 1) & 1, wd, 80);
@@ -570,10 +578,9 @@ __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedP
               for (int e = 0; e < 2; ++e) {
                 const int col = half * COLS + c0 + c + e;
                 const int pos = col < hist ? pos0 + col : len;
-                float bb = 0.f;
-                if (rp) bb = rp[min(max(pos - j, 0), p.P - 1)];
-                if (rt) bb += rt[time_bucket(tq[c0 + c + e], tj, p.Tb)];
-                w[e] = fmaf(__uint_as_float(v[c + e]), ka[c0 + c + e], -kLog2e * bb);
+                float bb = tbl[bit_length(tq[c0 + c + e], tj)];
+                if (rp) bb = fmaf(-kLog2e, rp[min(max(pos - j, 0), p.P - 1)], bb);
+                w[e] = fmaf(__uint_as_float(v[c + e]), ka[c0 + c + e], bb);
                 keep |= (j <= pos && j < len) ? 0xffffu << (16 * e) : 0u;
               }
               h2[c / 2] = silu_pair(make_float2(w[0], w[1])) & keep;
