@@ -22,9 +22,9 @@
 // to 2^14 is exact down to 2^-28 of that feature; the power goes back in with
 // alpha.
 //
-// Roles (19 warps): 0-7 scores (warp w: TMEM lanes 32 (w % 4), columns half
-// w / 4), 8-15 decoding and q, 16 page copies and the CTA's list of pieces, 17
-// S products and TMEM, 18 PV products.  Two tile buffers {K, V}; P takes K's
+// Roles (27 warps): 0-15 scores (two groups of 8 that take tiles in turn; warp w
+// of a group: TMEM lanes 32 (w % 4), columns half w / 4), 16-23 decoding and q,
+// 24 page copies and the CTA's list of pieces, 25 S products and TMEM, 26 PV products.  Two tile buffers {K, V}; P takes K's
 // place once the tile's S is complete.  Work is dealt evenly (hstu_cached.cuh).
 // Every wait is bounded.
 #include "hstu_cached.cuh"
@@ -37,9 +37,9 @@ namespace {
 using namespace tc;
 
 constexpr int TILE = kCachedTile;
-constexpr int kEpiWarps = 8, kDecWarps = 8;
-constexpr int kDecWarp0 = 8, kCopyWarp = 16, kSWarp = 17, kPvWarp = 18;
-constexpr int kThreads = 19 * 32;
+constexpr int kEpiWarps = 8, kDecWarps = 8;     // score warps: two groups of 8, one a tile buffer
+constexpr int kDecWarp0 = 2 * kEpiWarps, kCopyWarp = kDecWarp0 + kDecWarps, kSWarp = kCopyWarp + 1, kPvWarp = kSWarp + 1;
+constexpr int kThreads = (kPvWarp + 1) * 32;     // 27 warps, 7 a sub-partition: 72 registers
 
 template <int D, int N>
 struct Cfg {
@@ -142,7 +142,7 @@ __device__ __forceinline__ void decode_tile(const uint8_t* codes, const uint8_t*
 }
 
 template <int D, int N>
-__global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedParams p) {
+__global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedParams p) {
   using L = Cfg<D, N>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -167,7 +167,7 @@ __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedP
       else if ((i >= L::TSEMPTY && i < L::ITEMFULL) || (i >= L::PREADY && i < L::OFULL) || (i >= L::OEMPTY && i < L::DRAIN))
         n = kEpiWarps;
       else if (i >= L::ITEMEMPTY && i < L::QTFULL)
-        n = kDecWarps + kEpiWarps + 2;
+        n = kDecWarps + 2 * kEpiWarps + 2;
       else if (i == L::DRAIN)
         n = 2;
       mbar_init(bar(i), n);
@@ -467,8 +467,8 @@ __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedP
   } else {
     // -------------------------------------------------------------- scores
     constexpr int COLS = N / 2;                    // columns of a warp
-    constexpr int CH = COLS < 32 ? COLS : 32;      // columns in registers at a time
-    const int wq = warp & 3, half = warp >> 2;
+    constexpr int CH = 16;                         // columns in registers at a time
+    const int group = warp >> 3, wq = warp & 3, half = (warp >> 2) & 1;
     const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16) + half * COLS;
     const int r = wq * 32 + lane;                  // this thread's token in a tile, and feature in O
     uint32_t it = 0, tk = 0;
@@ -478,9 +478,7 @@ __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedP
     uint32_t pend_it = 0;
     int pend_slot = 0, pend_rows = 0;
     auto load_cols = [&](uint32_t addr, uint32_t (&v)[CH]) {
-      if constexpr (CH == 32) tmem_ld32(addr, v);
-      else if constexpr (CH == 16) tmem_ld16(addr, v);
-      else tmem_ld8(addr, v);
+      tmem_ld16(addr, v);
     };
     auto write_sum = [&]() -> bool {
       const uint32_t ob = pend_it & 1;
@@ -520,12 +518,14 @@ __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedP
       const bool one_time = !p.rab_time || tmin == tmax;
       const float* ka = kA + sl * N + half * COLS;
       const int64_t* tq = qt + sl * N + half * COLS;
-      for (int t = t0; t < t1; ++t, ++tk) {
-        const uint32_t st = tk & 1, ts = tk % L::NT;
+      const uint32_t tk0 = tk;                           // of the piece's first tile
+      tk += t1 - t0;
+      for (int t = t0 + ((tk0 ^ group) & 1); t < t1; t += 2) {
+        const uint32_t k = tk0 + (t - t0), st = group, ts = k % L::NT;
         const int j = t * TILE + r;
         int64_t tj = 0;
         if (timed) {
-          ok = mbar_wait(bar(L::TSFULL + ts), (tk / L::NT) & 1, wd, 79);
+          ok = mbar_wait(bar(L::TSFULL + ts), (k / L::NT) & 1, wd, 79);
           if (!ok) break;
           tj = *reinterpret_cast<const int64_t*>(base + L::TS_OFF + ts * (TILE * 8) + r * 8);
         }
@@ -545,7 +545,7 @@ __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedP
         same = same || j >= len;
         const bool fast = __all_sync(0xffffffffu, same);
         const bool whole = __all_sync(0xffffffffu, j < len);
-        ok = mbar_wait(bar(L::SFULL + st), (tk >> 1) & 1, wd, 80);
+        ok = mbar_wait(bar(L::SFULL + st), (k >> 1) & 1, wd, 80);
         if (!ok) break;
         fence_after_sync();
         uint8_t* ps = base + L::KP_OFF + st * L::KP_BYTES;
@@ -609,10 +609,16 @@ __global__ void __maxnreg__(96) cached_tc_kernel(const __grid_constant__ CachedP
       if (!ok) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::ITEMEMPTY + sl));
-      pend = true;
-      pend_it = it;
-      pend_slot = slot;
-      pend_rows = rows;
+      if (((tk - 1) & 1) == (uint32_t)group) {           // the group of the piece's last tile writes its sum
+        if (pend) {
+          ok = write_sum();                              // (an older one is out by now, or is waited for here)
+          if (!ok) break;
+        }
+        pend = true;
+        pend_it = it;
+        pend_slot = slot;
+        pend_rows = rows;
+      }
       ++it;
     }
     if (ok && pend) write_sum();
