@@ -2,13 +2,14 @@
 // the entry point, and the kernel that finishes what the tensor-core kernel
 // (hstu_tc_cached.cu) leaves.
 //
-// Finishing: one CTA a row adds up the pieces' FP32 sums of each head in
+// Finishing: one warp a row adds up the pieces' FP32 sums of each head in
 // piece order, adds a candidate's own term, SiLU(z_ii) v_i, and does 1/N, norm
-// and gate on the row's H d features in registers, 4 a thread and step.  It
-// is launched programmatically behind the tensor-core kernel.  HBM traffic is
-// the rows' q, k, v, u, o, y; the sums come from L2.  Few rows over a long
-// cache have many pieces each (one for every CTA that held a part), so there
-// kGroups groups of threads share them and add their sums in shared memory.
+// and gate on the row's H d features in registers.  It is launched
+// programmatically behind the tensor-core kernel, which has written where each
+// row's sums lie, so that the rows' own loads wait for one record only.  HBM
+// traffic is the rows' q, k, v, u, o, y; the sums come from L2.  Few rows over a
+// long cache have many pieces each (one for every CTA that held a part), so
+// there kWarps warps share them and add their sums in shared memory.
 #include "hstu_cached.cuh"
 #include "hstu_rows.cuh"
 
@@ -21,76 +22,84 @@ namespace {
 // zero far below zero, minus infinity included
 __device__ __forceinline__ float silu(float z) { return z < -1e4f ? 0.f : z / (1.f + expf(-z)); }
 
-constexpr int kFin = 128;    // threads that hold a row's features
+constexpr int kFinThreads = 128;   // of a CTA with a warp a row
 
-template <int D, int kGroups>
-__global__ void __launch_bounds__(kFin* kGroups) finish_kernel(const __grid_constant__ CachedParams p, int N) {
+// NV: the row's features in steps of 128 (4 a lane).
+template <int D, int NV, int kWarps>
+__global__ void __launch_bounds__(kWarps == 1 ? kFinThreads : 32 * kWarps) finish_kernel(const __grid_constant__ CachedParams p,
+                                                                                         int N) {
   constexpr int LANES = D / 4;
-  __shared__ float red[2][kFin / 32];
-  __shared__ __align__(16) float sums[kGroups > 1 ? kGroups - 1 : 1][4 * kFin];
-  const int64_t t = blockIdx.x;
-  const int F = p.H * D, tid = threadIdx.x % kFin, group = threadIdx.x / kFin, lane = threadIdx.x & 31;
+  __shared__ __align__(16) float4 sums[kWarps > 1 ? kWarps - 1 : 1][kWarps > 1 ? NV * 32 : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = kWarps == 1 ? (int64_t)blockIdx.x * (kFinThreads / 32) + warp : blockIdx.x;
+  const int F = p.H * D;
   pdl_wait();
+  if (t >= p.T) return;
   const int quota = p.hdr[WS_CA_QUOTA];
-  if (quota < 0 || t >= p.off[p.B]) return;    // a refused batch, a padded batch's row
-  const int b = warp_find_sequence(p.off, nullptr, p.B, t).b;
-  CachedSeq s;
-  if (!load_seq(p, b, s)) return;
-  const int r = (int)(t - s.row0), qb = r / N;
-  const bool candidate = r >= s.n - s.m;
-  // where the block's first item begins among all tiles
-  int before = 0;
-  for (int x = lane; x < qb; x += 32) before += block_tiles(s, x, N);
+  const int64_t total = p.off[p.B];
+  const int4 rec = p.rows[t];
+  if (quota < 0 || t >= total) return;    // a refused batch, a padded batch's row
+  const bool candidate = (rec.w >> 30) & 1;
+  const int64_t row = t * F + lane * 4;
+  // the row's own loads, under way while the sums are added up
+  Raw4<__nv_bfloat16> q[NV], k[NV], v[NV], u[NV];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  const int tiles = block_tiles(s, qb, N);
-  const int tile0 = p.seq_tiles[b] + before * p.H, item0 = p.seq_items[b] + qb * p.H;
-  const float* rows = p.part + (int64_t)(r - qb * N) * D;
-  float o[4][4];
+  for (int i = 0; i < NV; ++i) {
+    const bool on = i * 128 + lane * 4 < F && (kWarps == 1 || warp == 0);
+    q[i].x = k[i].x = v[i].x = make_uint2(0, 0);
+    u[i].x = make_uint2(0x3f803f80u, 0x3f803f80u);   // ones
+    if (on && candidate) {
+      q[i] = fetch4(p.q + row + i * 128);
+      k[i] = fetch4(p.k + row + i * 128);
+      v[i] = fetch4(p.v + row + i * 128);
+    }
+    if (on && p.u && p.y) u[i] = fetch4(p.u + row + i * 128);
+  }
+  const float* rows = p.part + (int64_t)(rec.w & 0x3fffffff) * D;
+  float o[NV][4];
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int f = (i * kFin + tid) * 4;
-    const bool on = f < F;
-    float a[4] = {0.f, 0.f, 0.f, 0.f};
-    if (i * kFin * 4 >= F) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-      continue;
-    }
-    const int h = f / D;
-    if (on && tiles > 0) {
-      const int at = tile0 + h * tiles, c1 = (at + tiles - 1) / quota;
-      const float* src = rows + (int64_t)(item0 + h) * N * D + f % D;
-#pragma unroll 8
-      for (int c = at / quota + group; c <= c1; c += kGroups) {
+  for (int i = 0; i < NV; ++i) {
+    const int f = i * 128 + lane * 4, h = f / D;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (f < F && rec.z > 0) {
+      const int at = rec.x + h * rec.z, c1 = (at + rec.z - 1) / quota;
+      const float* src = rows + (int64_t)(rec.y + h) * N * D + f % D;
+#pragma unroll 4
+      for (int c = at / quota + (kWarps > 1 ? warp : 0); c <= c1; c += kWarps) {
         const float4 x = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)c * N * D));
-        a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
+        a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
       }
     }
-    if (kGroups > 1) {
-      __syncthreads();
-      if (group > 0) *reinterpret_cast<float4*>(&sums[group - 1][tid * 4]) = make_float4(a[0], a[1], a[2], a[3]);
-      __syncthreads();
-      if (group == 0) {
+    o[i][0] = a.x; o[i][1] = a.y; o[i][2] = a.z; o[i][3] = a.w;
+  }
+  if (kWarps > 1) {
+    if (warp > 0) {
 #pragma unroll
-        for (int g = 0; g < kGroups - 1; ++g) {
-          const float4 x = *reinterpret_cast<const float4*>(&sums[g][tid * 4]);
-          a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
-        }
+      for (int i = 0; i < NV; ++i) sums[warp - 1][i * 32 + lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    for (int w = 0; w < kWarps - 1; ++w) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const float4 x = sums[w][i * 32 + lane];
+        o[i][0] += x.x; o[i][1] += x.y; o[i][2] += x.z; o[i][3] += x.w;
       }
     }
+  }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) a[e] *= p.o_scale;
-    if (candidate && group == 0) {
-      const int64_t at = t * F + f;
-      float q[4] = {}, k[4] = {}, v[4] = {};
-      if (on) {
-        load4(p.q + at, q);
-        load4(p.k + at, k);
-        load4(p.v + at, v);
-      }
-      float dot = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
+  for (int i = 0; i < NV; ++i) {
+    const int f = i * 128 + lane * 4, h = f / D;
+    const bool on = f < F;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i][e] *= p.o_scale;
+    if (candidate) {
+      float a[4], b[4];
+      unpack4(q[i], a);
+      unpack4(k[i], b);
+      float dot = a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
+      unpack4(v[i], b);
 #pragma unroll
       for (int x = LANES / 2; x > 0; x >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, x);
       if (on) {
@@ -99,50 +108,51 @@ __global__ void __launch_bounds__(kFin* kGroups) finish_kernel(const __grid_cons
         if (p.rab_time) z += p.rab_time[h * p.Tb];
         const float w = silu(z) * p.inv_n;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a[e] = fmaf(w, v[e], a[e]);
+        for (int e = 0; e < 4; ++e) o[i][e] = fmaf(w, b[e], o[i][e]);
       }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      o[i][e] = a[e];
-      sum += on ? a[e] : 0.f;
-    }
-    if (on && p.o && group == 0) store4(p.o + t * F + f, o[i]);
+    for (int e = 0; e < 4; ++e) sum += on ? o[i][e] : 0.f;
+    if (on && p.o) store4(p.o + row + i * 128, o[i]);
   }
   if (!p.y) return;
-  auto total = [&](float v, int slot) -> float {
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
-    if (lane == 0 && group == 0) red[slot][tid >> 5] = v;
-    __syncthreads();
-    float x = 0.f;
-    for (int w = 0; w < kFin / 32; ++w) x += red[slot][w];
-    return x;
-  };
   float mean = 0.f, rstd = 1.f;
   if (p.norm == HSTU_NORM_LAYERNORM) {
-    mean = total(sum, 0) / F;
+    mean = row_sum<32>(sum) / F;
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float c = o[i][e] - mean;
-        ss += (i * kFin + tid) * 4 < F ? c * c : 0.f;
+        ss += i * 128 + lane * 4 < F ? c * c : 0.f;
       }
-    rstd = __frsqrt_rn(total(ss, 1) / F + p.eps);
+    rstd = rsqrtf(row_sum<32>(ss) / F + p.eps);
   }
-  if (group > 0) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int f = (i * kFin + tid) * 4;
-    if (f >= F) continue;
-    float u[4] = {1.f, 1.f, 1.f, 1.f};
-    if (p.u) load4(p.u + t * F + f, u);
+  for (int i = 0; i < NV; ++i) {
+    if (i * 128 + lane * 4 >= F) continue;
+    float g[4];
+    unpack4(u[i], g);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) u[e] *= (o[i][e] - mean) * rstd;
-    store4(p.y + t * F + f, u);
+    for (int e = 0; e < 4; ++e) g[e] *= (o[i][e] - mean) * rstd;
+    store4(p.y + row + i * 128, g);
   }
+}
+
+template <int D, int NV>
+cudaError_t launch_finish(const CachedParams& p, int N, bool few, cudaStream_t st) {
+  if (few) return launch_pdl(finish_kernel<D, NV, 8>, dim3((unsigned)p.T), dim3(256), 0, st, p, N);
+  const unsigned ctas = (unsigned)((p.T + kFinThreads / 32 - 1) / (kFinThreads / 32));
+  return launch_pdl(finish_kernel<D, NV, 1>, dim3(ctas), dim3(kFinThreads), 0, st, p, N);
+}
+
+template <int D>
+cudaError_t dispatch_finish(const CachedParams& p, int N, bool few, cudaStream_t st) {
+  const int F = p.H * D;
+  return F <= 128 ? launch_finish<D, 1>(p, N, few, st) : F <= 256 ? launch_finish<D, 2>(p, N, few, st)
+       : F <= 512 ? launch_finish<D, 4>(p, N, few, st) : F <= 1024 ? launch_finish<D, 8>(p, N, few, st)
+                                                                   : launch_finish<D, 16>(p, N, few, st);
 }
 
 hstu_status_t check_cached(const hstu_attn_desc* d, const hstu_cache_desc* c, int32_t max_rows, bool buffers) {
@@ -164,7 +174,7 @@ hstu_status_t check_cached(const hstu_attn_desc* d, const hstu_cache_desc* c, in
 constexpr int kMaxCtas = 256;
 
 struct CachedWs {
-  size_t tiles, items, part, total;
+  size_t rows, part, total;
 };
 
 CachedWs cached_ws(const hstu_attn_desc* d, int N) {
@@ -175,8 +185,7 @@ CachedWs cached_ws(const hstu_attn_desc* d, int N) {
     off = (off + bytes + kWsAlign - 1) / kWsAlign * kWsAlign;
     return at;
   };
-  w.tiles = take(sizeof(int) * (size_t)d->B);
-  w.items = take(sizeof(int) * (size_t)d->B);
+  w.rows = take(sizeof(int4) * (size_t)d->total_tokens);
   // a sum for every item, and one more for every CTA that ends inside one
   const size_t slots = ((size_t)(d->total_tokens / N) + d->B) * d->H + kMaxCtas;
   w.part = take(sizeof(float) * slots * N * d->d_v);
@@ -227,8 +236,7 @@ hstu_status_t hstu_attn_fwd_cached(const hstu_attn_desc* d, const hstu_cache_des
   p.pages = static_cast<const uint8_t*>(c->pages); p.page_times = c->timestamps;
   p.hdr = static_cast<int*>(workspace);
   char* ws = static_cast<char*>(workspace);
-  p.seq_tiles = reinterpret_cast<int*>(ws + w.tiles);
-  p.seq_items = reinterpret_cast<int*>(ws + w.items);
+  p.rows = reinterpret_cast<int4*>(ws + w.rows);
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.T = d->total_tokens; p.B = d->B; p.H = d->H;
   p.page_size = c->page_size; p.page_log = c->page_size == 32 ? 5 : (c->page_size == 64 ? 6 : 7); p.num_pages = c->num_pages; p.max_pages = c->max_pages;
@@ -244,14 +252,8 @@ hstu_status_t hstu_attn_fwd_cached(const hstu_attn_desc* d, const hstu_cache_des
   if (e == cudaSuccess)
     e = N == 8 ? launch_stream_cached(p, c->d, ctas, st) : launch_tc_cached(p, c->d, N, ctas, st);
   if (e == cudaSuccess) {
-    const dim3 grid((unsigned)d->total_tokens);
-    const bool few = d->total_tokens <= sms;
-    if (c->d == 128)
-      e = few ? launch_pdl(finish_kernel<128, 4>, grid, dim3(4 * kFin), 0, st, p, N)
-              : launch_pdl(finish_kernel<128, 1>, grid, dim3(kFin), 0, st, p, N);
-    else
-      e = few ? launch_pdl(finish_kernel<64, 4>, grid, dim3(4 * kFin), 0, st, p, N)
-              : launch_pdl(finish_kernel<64, 1>, grid, dim3(kFin), 0, st, p, N);
+    const bool few = d->total_tokens <= sms;   // fewer rows than SMs: their pieces are many
+    e = c->d == 128 ? dispatch_finish<128>(p, N, few, st) : dispatch_finish<64>(p, N, few, st);
   }
   if (e != cudaSuccess) {
     (void)cudaGetLastError();

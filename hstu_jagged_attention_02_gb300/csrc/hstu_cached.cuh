@@ -35,8 +35,7 @@ struct CachedParams {
   const uint8_t* pages;
   const int64_t* page_times;
   float* part;                // [slots][N][d]
-  int* seq_tiles;             // [B] tiles of all items before the sequence
-  int* seq_items;             // [B] items before it
+  int4* rows;                 // [T] where a row's sums lie (row_record)
   int* hdr;
   int64_t T;
   int B, H, page_size, page_log, num_pages, max_pages, max_rows, max_n, P, Tb, norm;
@@ -78,11 +77,18 @@ struct Start {
   int total, quota;   // tiles in all (0 where the batch is refused), tiles a CTA
 };
 
-// Every CTA counts all sequences' tiles and finds its own beginning; CTA 0
-// also writes the counts for the finishing kernel.  A thread takes `per`
-// neighbouring sequences (one, unless there are more of them than threads: then
-// nothing is read twice).  scan: 2 x 32 ints in shared memory; the caller
-// synchronises before it reads start.
+// A row's record for the finishing kernel: tiles before its block's first
+// item, that item, the block's tiles, and its place in the block with, in bit 30,
+// whether it is a candidate.
+__device__ __forceinline__ int4 row_record(const CachedSeq& s, int r, int N, int tile0, int item0, int tiles) {
+  return make_int4(tile0, item0, tiles, r % N | (r >= s.n - s.m ? 1 << 30 : 0));
+}
+
+// Every CTA counts all sequences' tiles and finds its own beginning; the rows'
+// records are written by one CTA a sequence.  A thread takes `per` neighbouring
+// sequences (one, unless there are more of them than threads: then nothing is
+// read twice).  scan: 2 x 32 ints in shared memory; the caller synchronises
+// before it reads start.
 template <int THREADS>
 __device__ __forceinline__ void cut_work(const CachedParams& p, int N, int* scan, Start* start) {
   constexpr int WARPS = THREADS / 32;
@@ -92,8 +98,8 @@ __device__ __forceinline__ void cut_work(const CachedParams& p, int N, int* scan
   const int lo = min((int)threadIdx.x * per, p.B), hi = min(lo + per, p.B);
   bool bad = threadIdx.x == THREADS - 1 && (p.off[0] != 0 || p.off[p.B] > p.T);
   int tiles = 0, items = 0;
+  CachedSeq s{};
   auto count = [&](int b, int& t, int& i) -> bool {
-    CachedSeq s;
     if (!load_seq(p, b, s)) return false;
     const int blocks = (s.n + N - 1) / N;
     t = 0;
@@ -141,30 +147,45 @@ __device__ __forceinline__ void cut_work(const CachedParams& p, int N, int* scan
   if (any_bad) return;
   const bool mine = first < total && before <= first && first < before + tiles;
   if (per == 1) {
-    if (lo < hi && blockIdx.x == 0) {
-      p.seq_tiles[lo] = before;
-      p.seq_items[lo] = before_items;
-    }
     if (mine) {
       start->b = lo;
       start->rem = first - before;
       start->items = before_items;
     }
-  } else if (mine || blockIdx.x == 0) {
-    bool found = false;
+    // a warp's sequences that are this CTA's to write, one after the other
+    unsigned m = __ballot_sync(0xffffffffu, lo < hi && lo % (int)gridDim.x == (int)blockIdx.x && s.n > 0);
+    for (; m; m &= m - 1) {
+      const int src = __ffs(m) - 1;
+      CachedSeq q;
+      q.row0 = __shfl_sync(0xffffffffu, s.row0, src);
+      q.n = __shfl_sync(0xffffffffu, s.n, src);
+      q.m = __shfl_sync(0xffffffffu, s.m, src);
+      q.L = __shfl_sync(0xffffffffu, s.L, src);
+      int tile0 = __shfl_sync(0xffffffffu, before, src), item0 = __shfl_sync(0xffffffffu, before_items, src);
+      for (int r0 = 0; r0 < q.n; r0 += N) {
+        const int here = block_tiles(q, r0 / N, N);
+        for (int r = r0 + lane; r < min(q.n, r0 + N); r += 32) p.rows[q.row0 + r] = row_record(q, r, N, tile0, item0, here);
+        tile0 += here * p.H;
+        item0 += p.H;
+      }
+    }
+  } else {
     for (int b = lo; b < hi; ++b) {
       int here, i;
       count(b, here, i);
-      if (blockIdx.x == 0) {
-        p.seq_tiles[b] = before;
-        p.seq_items[b] = before_items;
-      }
-      if (mine && !found && first < before + here) {
+      if (mine && first >= before && first < before + here) {
         start->b = b;
         start->rem = first - before;
         start->items = before_items;
-        found = true;
-        if (blockIdx.x != 0) break;
+      }
+      if (b % (int)gridDim.x == (int)blockIdx.x) {
+        int tile0 = before, item0 = before_items;
+        for (int r0 = 0; r0 < s.n; r0 += N) {
+          const int bt = block_tiles(s, r0 / N, N);
+          for (int r = r0; r < min(s.n, r0 + N); ++r) p.rows[s.row0 + r] = row_record(s, r, N, tile0, item0, bt);
+          tile0 += bt * p.H;
+          item0 += p.H;
+        }
       }
       before += here;
       before_items += i;

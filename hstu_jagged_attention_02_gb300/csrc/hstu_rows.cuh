@@ -43,6 +43,11 @@ template <typename T> __device__ __forceinline__ Raw4<T> fetch4(const T* p) {
   return r;
 }
 
+__device__ __forceinline__ void unpack4(const Raw4<__nv_bfloat16>& r, float (&v)[4]) {
+  v[0] = __uint_as_float(r.x.x << 16); v[1] = __uint_as_float(r.x.x & 0xFFFF0000u);
+  v[2] = __uint_as_float(r.x.y << 16); v[3] = __uint_as_float(r.x.y & 0xFFFF0000u);
+}
+
 // A lane's 8 features of a row as FP32 pairs: v[0], v[1] part 0, v[2], v[3] part 1.
 struct Row8 {
   float2 v[4];
