@@ -266,19 +266,17 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 }
 
 // 16 SiLU(z) of two scores given as w = -log2(e) z: w c / (1 + 2^w) with
-// c = -16 / log2(e).  Beyond w = 60 (z < -41) the value is zero in FP16
-// whatever it is, so w is cut there (a NaN stays one); then 1 + 2^w stays
-// below 2^61 and one reciprocal of the product serves both: the special
-// function unit does three operations a pair instead of four.
+// c = -16 / log2(e).  Far below zero 2^w is infinity and the value a zero; the
+// biases are kept below kMostBias so that w itself is not (0 x infinity).
 __device__ __forceinline__ uint32_t silu_pair(float2 w) {
   const float c = -kPScale / kLog2e;
-  const float2 t = make_float2(min_nan(w.x, 60.f), min_nan(w.y, 60.f));
-  const float2 d = __fadd2_rn(make_float2(ex2_approx(t.x), ex2_approx(t.y)), make_float2(1.f, 1.f));
-  const float r = rcp_approx(d.x * d.y);
-  const float2 u = __fmul2_rn(t, make_float2(c, c));
-  const float2 x = __fmul2_rn(u, make_float2(d.y * r, d.x * r));
+  const float2 d = __fadd2_rn(make_float2(ex2_approx(w.x), ex2_approx(w.y)), make_float2(1.f, 1.f));
+  const float2 x = __fmul2_rn(__fmul2_rn(w, make_float2(c, c)), make_float2(rcp_approx(d.x), rcp_approx(d.y)));
   return pack_f16(x.x, x.y);
 }
+// A bias as the kernels use it: times -log2(e), and cut where it mutes for good.
+constexpr float kMostBias = 1e30f;
+__device__ __forceinline__ float scaled_bias(float b) { return min_nan(-kLog2e * b, kMostBias); }
 
 // The power of two that brings a q row whose largest magnitude has the bits
 // `top` (FP32) to [2^14, 2^15), and its inverse; rows below 2^-100 take

@@ -164,12 +164,12 @@ __device__ __forceinline__ void write_piece(const CachedParams& p, const Walk& w
   }
   if (lane < kRows) out.tq[lane] = tq;
   for (int e = lane; e < kTimeSlots; e += 32)
-    out.time_bias[e] = p.rab_time ? -kLog2e * p.rab_time[w.h * p.Tb + min(e, p.Tb - 1)] : 0.f;
+    out.time_bias[e] = p.rab_time ? scaled_bias(p.rab_time[w.h * p.Tb + min(e, p.Tb - 1)]) : 0.f;
   if (lane == 0) {
     out.tmin = tmin;
     out.tmax = tmax;
     out.valid = 1;
-    out.far_bias = p.rab_pos ? -kLog2e * p.rab_pos[w.h * p.P + p.P - 1] : 0.f;
+    out.far_bias = p.rab_pos ? scaled_bias(p.rab_pos[w.h * p.P + p.P - 1]) : 0.f;
     out.h = w.h;
     out.rows = rows;
     out.hist = max(0, min(hist - r0, rows));
@@ -367,7 +367,7 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
           float bl = far_bias;
           if (pmin - (j16 + 15) < p.P - 1 && rp) {         // near tokens: their buckets' own biases, from global memory
             const int a = min(max(pmin - jl, 0), p.P - 1);
-            bl = -kLog2e * __ldg(rp + a);
+            bl = scaled_bias(__ldg(rp + a));
             same = same && a == min(max(pmax - jl, 0), p.P - 1);
           }
           {
@@ -397,7 +397,7 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
               for (int f = 0; f < 2; ++f) {
                 const int r = 2 * t + f, pos = r < nh ? pos0 + r : len;
                 b[f] = pc.time_bias[bit_length(pc.tq[r], tj)];
-                if (rp) b[f] = fmaf(-kLog2e, rp[min(max(pos - j, 0), p.P - 1)], b[f]);
+                if (rp) b[f] += scaled_bias(rp[min(max(pos - j, 0), p.P - 1)]);
                 keep |= j <= pos ? 0xffffu << (16 * f) : 0u;
               }
               const float2 cc = e ? make_float2(c[0][2], c[0][3]) : make_float2(c[0][0], c[0][1]);

@@ -53,9 +53,8 @@ struct Cfg {
   static constexpr int Q_BYTES = N * D * 2;
   static constexpr int ITEMS = N == 128 ? 2 : 4;           // piece records in flight
   static constexpr int NR = D == 64 ? 6 : (N >= 64 ? 3 : 4);   // packed tiles in flight
-  static constexpr int NT = NR + 2;                        // their times live until the scores are done
-  static constexpr int RAW_KS = TILE * D / 2, RAW_V = RAW_KS + TILE * D / 16, RAW_VS = RAW_V + TILE * D / 2;
-  static constexpr int RAW_BYTES = 2 * RAW_V;
+  static constexpr int NT = NR + (N == 32 ? 1 : 2);                        // their times live until the scores are done
+  static constexpr int RAW_BYTES = 2 * TILE * (D / 2 + D / 16);   // the tile's pages' blocks, as they are
   // shared memory
   static constexpr int KP_OFF = 0;
   static constexpr int V_OFF = KP_OFF + 2 * KP_BYTES;
@@ -63,7 +62,8 @@ struct Cfg {
   static constexpr int RAW_OFF = Q_OFF + QB * Q_BYTES;
   static constexpr int TS_OFF = RAW_OFF + NR * RAW_BYTES;
   static constexpr int QT_OFF = TS_OFF + NT * TILE * 8;    // int64 [ITEMS][N] row times
-  static constexpr int KA_OFF = QT_OFF + ITEMS * N * 8;    // float [ITEMS][N] score factors
+  static constexpr int QT32_OFF = QT_OFF + ITEMS * N * 8;  // int32 [ITEMS][N], from the earliest row's
+  static constexpr int KA_OFF = QT32_OFF + ITEMS * N * 4;    // float [ITEMS][N] score factors
   static constexpr int TB_OFF = KA_OFF + ITEMS * N * 4;    // float [ITEMS][kTimeSlots + 1] time biases, the far position's
   static constexpr int SLOT_OFF = (TB_OFF + ITEMS * (kTimeSlots + 1) * 4 + 15) / 16 * 16;
   // barriers
@@ -105,41 +105,48 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return (uint32_t)(r * ROW + ((c ^ ((r >> SH) & M)) << 4));
 }
 
-// A packed tile (codes [128][D/2], scales [128][D/16]) to FP16 rows of 64
-// features a 128-byte swizzled chunk.  A thread takes 32 features of a row at
-// a time; rows from `rows` on become zeros.  With 4 threads a row (D = 128)
-// the upper two write their chunks in the order 2, 3, 0, 1, so that 8
-// neighbouring threads (2 rows) hit 8 different 16-byte banks.
+// Where a decoding thread's parts of a tile lie: it takes 32 features of a row
+// at a time.  With 4 threads a row (D = 128) 8 neighbouring threads take
+// 4 rows x 2 segments: their stores then hit 8 different 16-byte banks, their
+// loads 4 (the loads are a quarter of the stores).
 template <int D>
-__device__ __forceinline__ void decode_tile(const uint8_t* codes, const uint8_t* scales, uint8_t* out, int dw, int lane,
-                                            int rows) {
-  constexpr int SEGS = D / 32, RPW = 32 / SEGS;            // rows a warp takes at a time
+struct DecodePlan {
+  static constexpr int SEGS = D / 32, RPW = 32 / SEGS, STEPS = TILE / (kDecWarps * RPW);   // rows a warp takes at a time
+  int row0;                 // row of step 0; a step is kDecWarps * RPW rows on
+  int code[STEPS], scale[STEPS];   // in the packed tile: blocks of a page, codes and scales of K (V: half a block on)
+  uint32_t out[4];          // of the four 16-byte chunks in the decoded tile, at step 0
+  __device__ __forceinline__ DecodePlan(const PageLayout& lay, int page_log, int dw, int lane) {
+    const int seg = D == 128 ? (lane & 1) + 2 * (lane >> 4) : lane & 1, sub = D == 128 ? (lane >> 1) & 7 : lane >> 1;
+    row0 = dw * RPW + sub;
 #pragma unroll
-  for (int i = 0; i < TILE / (kDecWarps * RPW); ++i) {
-    const int r = (i * kDecWarps + dw) * RPW + lane / SEGS, seg = lane % SEGS;
-    uint4 w = *reinterpret_cast<const uint4*>(codes + r * (D / 2) + seg * 16);
-    uint32_t sc = *reinterpret_cast<const uint16_t*>(scales + r * (D / 16) + seg * 2);
-    if (r >= rows) {
-      w = make_uint4(0, 0, 0, 0);
-      sc = 0;
+    for (int i = 0; i < STEPS; ++i) {
+      const int r = row0 + i * kDecWarps * RPW, at = r & ((1 << page_log) - 1), block = (r >> page_log) * lay.bytes();
+      code[i] = block + at * (D / 2) + seg * 16;
+      scale[i] = block + lay.scales() + at * (D / 16) + seg * 2;
     }
-    const __half2 s = e4m3x2_half2(sc);
-    __half2 s0 = __low2half2(s), s1 = __high2half2(s);
-    const bool swap = SEGS == 4 && seg >= 2;
-    if (SEGS == 4) {
-      const uint4 x = w;
-      const __half2 a = s0, b = s1;
-      w.x = swap ? x.z : x.x; w.y = swap ? x.w : x.y; w.z = swap ? x.x : x.z; w.w = swap ? x.y : x.w;
-      s0 = swap ? b : a; s1 = swap ? a : b;
-    }
-    uint8_t* base = out + (seg / 2) * (TILE * 128);
-    const int c0 = (seg & 1) * 4, x2 = swap ? 2 : 0;
-    *reinterpret_cast<uint4*>(base + swz<128>(r, c0 + (0 ^ x2))) = decode8(w.x, s0);
-    *reinterpret_cast<uint4*>(base + swz<128>(r, c0 + (1 ^ x2))) = decode8(w.y, s0);
-    *reinterpret_cast<uint4*>(base + swz<128>(r, c0 + (2 ^ x2))) = decode8(w.z, s1);
-    *reinterpret_cast<uint4*>(base + swz<128>(r, c0 + (3 ^ x2))) = decode8(w.w, s1);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) out[c] = (seg / 2) * (TILE * 128) + swz<128>(row0, (seg & 1) * 4 + c);
   }
-}
+  // part: the packed K or V; rows from `rows` on become zeros
+  __device__ __forceinline__ void decode(const uint8_t* part, uint8_t* to, int rows) const {
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      uint4 w = *reinterpret_cast<const uint4*>(part + code[i]);
+      uint32_t sc = *reinterpret_cast<const uint16_t*>(part + scale[i]);
+      if (rows < TILE && row0 + i * kDecWarps * RPW >= rows) {
+        w = make_uint4(0, 0, 0, 0);
+        sc = 0;
+      }
+      const __half2 s = e4m3x2_half2(sc);
+      const __half2 s0 = __low2half2(s), s1 = __high2half2(s);
+      uint8_t* base = to + i * (kDecWarps * RPW * 128);   // a multiple of 8 rows on: the same swizzle
+      *reinterpret_cast<uint4*>(base + out[0]) = decode8(w.x, s0);
+      *reinterpret_cast<uint4*>(base + out[1]) = decode8(w.y, s0);
+      *reinterpret_cast<uint4*>(base + out[2]) = decode8(w.z, s1);
+      *reinterpret_cast<uint4*>(base + out[3]) = decode8(w.w, s1);
+    }
+  }
+};
 
 template <int D, int N>
 __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedParams p) {
@@ -151,6 +158,7 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
   auto bar = [&](int i) -> uint32_t { return base_u32 + L::BAR_OFF + 8u * (uint32_t)i; };
   auto piece_at = [&](uint32_t i) -> Piece& { return *reinterpret_cast<Piece*>(base + L::SLOT_OFF + 96 * (int)i); };
   int64_t* qt = reinterpret_cast<int64_t*>(base + L::QT_OFF);
+  int32_t* qt32 = reinterpret_cast<int32_t*>(base + L::QT32_OFF);
   float* kA = reinterpret_cast<float*>(base + L::KA_OFF);
   float* tb = reinterpret_cast<float*>(base + L::TB_OFF);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::MISC_OFF);
@@ -237,13 +245,13 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
           entry = next;
           next = e0 + 32 + lane < npages ? row[e0 + 32 + lane] : -1;
         }
-        // lane l: part l % 5 (K codes, K scales, V codes, V scales, times) of page l / 5 of the tile
-        const int pg = lane / 5, kind = lane % 5;
-        const int id = __shfl_sync(0xffffffffu, entry, (e - e0 + min(pg, ppt - 1)) & 31);
-        const bool there = pg < ppt && e + pg < npages;
+        // lanes 0 .. ppt - 1: a page's block each; the next ppt lanes: its times
+        const int pg = lane & (ppt - 1);
+        const int id = __shfl_sync(0xffffffffu, entry, (e - e0 + pg) & 31);
+        const bool there = lane < 2 * ppt && e + pg < npages;
         const bool good = there && id >= 0 && id < p.num_pages;
         if (there && !good) set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, b);
-        const int n = __popc(__ballot_sync(0xffffffffu, good && kind == 0));
+        const int n = __popc(__ballot_sync(0xffffffffu, good && lane < ppt));
         const uint32_t rs = tk % L::NR, ts = tk % L::NT;
         if (lane == 0) {
           ok = mbar_wait(bar(L::RAWEMPTY + rs), ((tk / L::NR) & 1) ^ 1, wd, 62) &&
@@ -255,20 +263,12 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        if (good) {
-          const uint8_t* src = p.pages + ((int64_t)id * p.H + h) * lay.bytes() + (kind >= 2 ? lay.half() : 0);
-          const uint32_t dst = base_u32 + L::RAW_OFF + rs * L::RAW_BYTES + (kind >= 2 ? L::RAW_V : 0);
-          const int codes = p.page_size * (D / 2), scales = p.page_size * (D / 16);
-          if (kind == 4) {
-            if (timed)
-              bulk_load(base_u32 + L::TS_OFF + ts * (TILE * 8) + pg * p.page_size * 8,
-                        p.page_times + (int64_t)id * p.page_size, (uint32_t)(p.page_size * 8), bar(L::TSFULL + ts));
-          } else if (kind & 1) {
-            bulk_load(dst + L::RAW_KS + pg * scales, src + codes, (uint32_t)scales, bar(L::RAWFULL + rs));
-          } else {
-            bulk_load(dst + pg * codes, src, (uint32_t)codes, bar(L::RAWFULL + rs));
-          }
-        }
+        if (good && lane < ppt)
+          bulk_load(base_u32 + L::RAW_OFF + rs * L::RAW_BYTES + pg * lay.bytes(), p.pages + ((int64_t)id * p.H + h) * lay.bytes(),
+                    (uint32_t)lay.bytes(), bar(L::RAWFULL + rs));
+        else if (good && timed)
+          bulk_load(base_u32 + L::TS_OFF + ts * (TILE * 8) + pg * p.page_size * 8, p.page_times + ((int64_t)id << p.page_log),
+                    (uint32_t)(p.page_size * 8), bar(L::TSFULL + ts));
       }
       if (!ok) break;
       w.next(p, N);
@@ -290,6 +290,9 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
   } else if (warp >= kDecWarp0 && warp < kDecWarp0 + kDecWarps) {
     // --------------------------------------------------------- decoding, q
     const int dw = warp - kDecWarp0;
+    const PageLayout lay(p.page_size, D);
+    const DecodePlan<D> plan(lay, p.page_log, dw, lane);
+    const int half_block = lay.half();
     uint32_t it = 0, tk = 0;
     bool ok = true;
     while (ok) {
@@ -313,8 +316,8 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
         }
         if (dw == 1) {   // the head's biases, times -log2(e)
           for (int e = lane; e < kTimeSlots; e += 32)
-            tb[sl * (kTimeSlots + 1) + e] = p.rab_time ? -kLog2e * p.rab_time[h * p.Tb + min(e, p.Tb - 1)] : 0.f;
-          if (lane == 0) tb[sl * (kTimeSlots + 1) + kTimeSlots] = p.rab_pos ? -kLog2e * p.rab_pos[h * p.P + p.P - 1] : 0.f;
+            tb[sl * (kTimeSlots + 1) + e] = p.rab_time ? scaled_bias(p.rab_time[h * p.Tb + min(e, p.Tb - 1)]) : 0.f;
+          if (lane == 0) tb[sl * (kTimeSlots + 1) + kTimeSlots] = p.rab_pos ? scaled_bias(p.rab_pos[h * p.P + p.P - 1]) : 0.f;
         }
         if (dw == 0) {   // the rows' times, and their range
           int64_t mn = INT64_MAX, mx = INT64_MIN;
@@ -337,6 +340,7 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
             pc.tmin = mn;
             pc.tmax = mx;
           }
+          for (int r = lane; r < N; r += 32) qt32[sl * N + r] = (int32_t)(qt[sl * N + r] - mn);   // used where it fits
         }
         ok = mbar_wait(bar(L::QEMPTY + qbuf), ((it / L::QB) & 1) ^ 1, wd, 66);
         if (!ok) break;
@@ -378,11 +382,11 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
         if (!ok) break;
         const uint8_t* raw = base + L::RAW_OFF + rs * L::RAW_BYTES;
         const int rows = len - t * TILE;
-        decode_tile<D>(raw, raw + L::RAW_KS, base + L::KP_OFF + st * L::KP_BYTES, dw, lane, rows);
+        plan.decode(raw, base + L::KP_OFF + st * L::KP_BYTES, rows);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::KREADY + st));
-        decode_tile<D>(raw + L::RAW_V, raw + L::RAW_VS, base + L::V_OFF + st * L::KV_BYTES, dw, lane, rows);
+        plan.decode(raw + half_block, base + L::V_OFF + st * L::KV_BYTES, rows);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -518,6 +522,7 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
       const bool one_time = !p.rab_time || tmin == tmax;
       const float* ka = kA + sl * N + half * COLS;
       const int64_t* tq = qt + sl * N + half * COLS;
+      const int32_t* tq32 = qt32 + sl * N + half * COLS;
       const uint32_t tk0 = tk;                           // of the piece's first tile
       tk += t1 - t0;
       for (int t = t0 + ((tk0 ^ group) & 1); t < t1; t += 2) {
@@ -535,7 +540,7 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
         if (pmin - (t * TILE + wq * 32 + 31) < p.P - 1 && rp) {
           const int a = min(max(pmin - j, 0), p.P - 1);
           same = same && a == min(max(pmax - j, 0), p.P - 1);
-          bias = -kLog2e * __ldg(rp + a);
+          bias = scaled_bias(__ldg(rp + a));
         }
         {
           const int a = bit_length(tmin, tj);
@@ -545,6 +550,10 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
         same = same || j >= len;
         const bool fast = __all_sync(0xffffffffu, same);
         const bool whole = __all_sync(0xffffffffu, j < len);
+        // else only the time buckets may differ (tokens far back), by gaps of 32 bits
+        const int64_t rel = tj - tmin;
+        const bool far = !fast && __all_sync(0xffffffffu, pmin - j >= p.P - 1 && rel > -kNarrowTsSpan && rel < kNarrowTsSpan) &&
+                         tmax - tmin < kNarrowTsSpan;
         ok = mbar_wait(bar(L::SFULL + st), (k >> 1) & 1, wd, 80);
         if (!ok) break;
         fence_after_sync();
@@ -569,6 +578,20 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
 #pragma unroll
               for (int c = 0; c < CH / 2; ++c) h2[c] = j < len ? h2[c] : 0u;
             }
+          } else if (far) {
+            const int rel32 = (int)rel;
+            const float fb = tbl[kTimeSlots];
+#pragma unroll
+            for (int c = 0; c < CH; c += 4) {
+              const float4 k4 = *reinterpret_cast<const float4*>(ka + c0 + c);
+              const int4 q4 = *reinterpret_cast<const int4*>(tq32 + c0 + c);
+              const float2 b01 = make_float2(tbl[32 - __clz(abs(q4.x - rel32))] + fb, tbl[32 - __clz(abs(q4.y - rel32))] + fb);
+              const float2 b23 = make_float2(tbl[32 - __clz(abs(q4.z - rel32))] + fb, tbl[32 - __clz(abs(q4.w - rel32))] + fb);
+              h2[c / 2] = silu_pair(__ffma2_rn(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
+                                               make_float2(k4.x, k4.y), b01));
+              h2[c / 2 + 1] = silu_pair(__ffma2_rn(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])),
+                                                   make_float2(k4.z, k4.w), b23));
+            }
           } else {
 #pragma unroll
             for (int c = 0; c < CH; c += 2) {
@@ -579,7 +602,7 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
                 const int col = half * COLS + c0 + c + e;
                 const int pos = col < hist ? pos0 + col : len;
                 float bb = tbl[bit_length(tq[c0 + c + e], tj)];
-                if (rp) bb = fmaf(-kLog2e, rp[min(max(pos - j, 0), p.P - 1)], bb);
+                if (rp) bb += scaled_bias(rp[min(max(pos - j, 0), p.P - 1)]);
                 w[e] = fmaf(__uint_as_float(v[c + e]), ka[c0 + c + e], bb);
                 keep |= (j <= pos && j < len) ? 0xffffu << (16 * e) : 0u;
               }
