@@ -8,13 +8,13 @@
 //
 // The cached tokens are the M side of the first product and the features that
 // of the second, so the tensor core's fixed 128 is filled however few rows
-// there are, and N follows the rows (16, 32, 64 or 128): a decode step's one
-// row costs N = 16 columns of products and scores, not 128.  A thread of the
-// score step holds one cached token, whose position and time biases are the
-// same for every candidate of a request: one table lookup a tile and thread
-// where the block's rows share the position and time buckets towards the token,
-// as they do for candidates and for tokens far back; otherwise (rows near the
-// tokens, a time bucket's border inside the block) a lookup a score.
+// there are, and N follows the rows (32, 64 or 128; up to 8 rows have a kernel
+// of their own).  A thread of the score step holds one cached token, whose
+// position and time biases are the same for every candidate of a request: one
+// table lookup a tile and thread where the block's rows share the position and
+// time buckets towards the token, as they do for candidates and for tokens far
+// back; a time lookup a score where only a time bucket's border lies inside the
+// block; otherwise (rows near the tokens) both lookups a score.
 //
 // The pages reach shared memory as they are (cp.async.bulk, 9/16 byte a
 // feature) and are decoded there to FP16, where code x scale is exact.  q is
@@ -22,11 +22,22 @@
 // to 2^14 is exact down to 2^-28 of that feature; the power goes back in with
 // alpha.
 //
-// Roles (27 warps): 0-15 scores (two groups of 8 that take tiles in turn; warp w
-// of a group: TMEM lanes 32 (w % 4), columns half w / 4), 16-23 decoding and q,
-// 24 page copies and the CTA's list of pieces, 25 S products and TMEM, 26 PV products.  Two tile buffers {K, V}; P takes K's
-// place once the tile's S is complete.  Work is dealt evenly (hstu_cached.cuh).
-// Every wait is bounded.
+// Roles (27 warps): 0-15 scores (warp w: TMEM lanes 32 (w % 4), columns quarter
+// w / 4 of the tile), 16-23 decoding and q, 24 page copies and the CTA's list of
+// pieces, 25 S products and TMEM, 26 PV products.  Two tile buffers {K, V}; P
+// takes K's place once the tile's S is complete.  Work is dealt evenly
+// (hstu_cached.cuh).  Every wait is bounded.
+//
+// What bounds it: a tile buffer's round of decoding K (1,000 cycles), the S
+// product (900), the scores (3,000 with their biases), the PV product (1,300)
+// and back, which two buffers share: 3,300 cycles a tile of 128 tokens x 128
+// rows, where the tensor core itself needs 1,000.  A third buffer does not fit
+// beside the packed tiles.  Scores by 16 warps on one tile or by two groups of
+// 8 on a tile each take the same time with 128 rows (86 us for 32 users x 128
+// candidates over some 158,000 cached tokens, four heads of 128), and with fewer
+// rows or the near tokens' lookups the 16 are ahead (27 against 30 us, 75
+// against 78 us).  One reciprocal for two scores, or Newton steps in its place,
+// bought nothing: without any SiLU at all the kernel took 9% less.
 #include "hstu_cached.cuh"
 #include "tc_ptx.cuh"
 
@@ -37,8 +48,8 @@ namespace {
 using namespace tc;
 
 constexpr int TILE = kCachedTile;
-constexpr int kEpiWarps = 8, kDecWarps = 8;     // score warps: two groups of 8, one a tile buffer
-constexpr int kDecWarp0 = 2 * kEpiWarps, kCopyWarp = kDecWarp0 + kDecWarps, kSWarp = kCopyWarp + 1, kPvWarp = kSWarp + 1;
+constexpr int kEpiWarps = 16, kDecWarps = 8;    // score warps, decoding warps
+constexpr int kDecWarp0 = kEpiWarps, kCopyWarp = kDecWarp0 + kDecWarps, kSWarp = kCopyWarp + 1, kPvWarp = kSWarp + 1;
 constexpr int kThreads = (kPvWarp + 1) * 32;     // 27 warps, 7 a sub-partition: 72 registers
 
 template <int D, int N>
@@ -175,7 +186,7 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
       else if ((i >= L::TSEMPTY && i < L::ITEMFULL) || (i >= L::PREADY && i < L::OFULL) || (i >= L::OEMPTY && i < L::DRAIN))
         n = kEpiWarps;
       else if (i >= L::ITEMEMPTY && i < L::QTFULL)
-        n = kDecWarps + 2 * kEpiWarps + 2;
+        n = kDecWarps + kEpiWarps + 2;
       else if (i == L::DRAIN)
         n = 2;
       mbar_init(bar(i), n);
@@ -397,61 +408,65 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
     }
   } else if (warp == kSWarp) {
     // ---------------------------------------------------------- S^T = K Q^T
-    if (lane == 0) {
+    {   // the whole warp walks, so that the operands are uniform values; one elected lane issues
+      auto wait = [](bool done) { return (bool)__all_sync(0xffffffffu, done); };   // one answer for the warp
       constexpr uint32_t IDESC = idesc_f16(TILE, N, false, false);
       uint32_t it = 0, tk = 0;
       bool ok = true;
       while (ok) {
         const uint32_t sl = it % L::ITEMS, qbuf = it % L::QB;
-        ok = mbar_wait(bar(L::ITEMFULL + sl), (it / L::ITEMS) & 1, wd, 69);
+        ok = wait(mbar_wait(bar(L::ITEMFULL + sl), (it / L::ITEMS) & 1, wd, 69));
         if (!ok) break;
         const Piece& pc = piece_at(sl);
         if (!pc.valid) break;
         const int nt = pc.tile1 - pc.tile0;
-        mbar_arrive(bar(L::ITEMEMPTY + sl));
-        ok = mbar_wait(bar(L::QFULL + qbuf), (it / L::QB) & 1, wd, 70);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::ITEMEMPTY + sl));
+        ok = wait(mbar_wait(bar(L::QFULL + qbuf), (it / L::QB) & 1, wd, 70));
         if (!ok) break;
         ++it;
         const SDesc dq = sdesc_w(base_u32 + L::Q_OFF + qbuf * L::Q_BYTES, 16, 1024);
         for (int t = 0; t < nt; ++t, ++tk) {
           const uint32_t st = tk & 1;
           // the S buffer of tile tk - 2 was read before its PV, which freed the tile buffer
-          ok = mbar_wait(bar(L::KREADY + st), (tk >> 1) & 1, wd, 71);
+          ok = wait(mbar_wait(bar(L::KREADY + st), (tk >> 1) & 1, wd, 71));
           if (!ok) break;
           fence_after_sync();
           const SDesc dk = sdesc_w(base_u32 + L::KP_OFF + st * L::KP_BYTES, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss_w(tmem + st * N, dk + ((kk >> 2) * L::CHUNK + (kk & 3) * 32), dq + ((kk >> 2) * (N * 128) + (kk & 3) * 32),
+            mma_ss_e(tmem + st * N, dk + ((kk >> 2) * L::CHUNK + (kk & 3) * 32), dq + ((kk >> 2) * (N * 128) + (kk & 3) * 32),
                      IDESC, kk > 0 ? 1u : 0u);
-          mma_commit(bar(L::SFULL + st));
+          mma_commit_e(bar(L::SFULL + st));
         }
         if (!ok) break;
-        mma_commit(bar(L::QEMPTY + qbuf));
+        mma_commit_e(bar(L::QEMPTY + qbuf));
       }
-      mma_commit(bar(L::DRAIN));
+      mma_commit_e(bar(L::DRAIN));
       drain(bar(L::DRAIN), 0);
     }
   } else if (warp == kPvWarp) {
     // --------------------------------------------------------- O^T += V^T P
-    if (lane == 0) {
+    {
+      auto wait = [](bool done) { return (bool)__all_sync(0xffffffffu, done); };
       constexpr uint32_t IDESC = idesc_f16(128, N, true, true);
       uint32_t it = 0, tk = 0;
       bool ok = true;
       while (ok) {
         const uint32_t sl = it % L::ITEMS, ob = it & 1;
-        ok = mbar_wait(bar(L::ITEMFULL + sl), (it / L::ITEMS) & 1, wd, 72);
+        ok = wait(mbar_wait(bar(L::ITEMFULL + sl), (it / L::ITEMS) & 1, wd, 72));
         if (!ok) break;
         const Piece& pc = piece_at(sl);
         if (!pc.valid) break;
         const int nt = pc.tile1 - pc.tile0;
-        mbar_arrive(bar(L::ITEMEMPTY + sl));
-        ok = mbar_wait(bar(L::OEMPTY + ob), ((it >> 1) & 1) ^ 1, wd, 73);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::ITEMEMPTY + sl));
+        ok = wait(mbar_wait(bar(L::OEMPTY + ob), ((it >> 1) & 1) ^ 1, wd, 73));
         if (!ok) break;
         ++it;
         for (int t = 0; t < nt; ++t, ++tk) {
           const uint32_t st = tk & 1;
-          ok = mbar_wait(bar(L::VREADY + st), (tk >> 1) & 1, wd, 74) && mbar_wait(bar(L::PREADY + st), (tk >> 1) & 1, wd, 75);
+          ok = wait(mbar_wait(bar(L::VREADY + st), (tk >> 1) & 1, wd, 74) && mbar_wait(bar(L::PREADY + st), (tk >> 1) & 1, wd, 75));
           if (!ok) break;
           fence_after_sync();
           // with 64 features the upper half of M reads the same features again; its rows are not used
@@ -459,21 +474,21 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
           const SDesc dp = sdesc_rows<L::P_ROW>(base_u32 + L::KP_OFF + st * L::KP_BYTES, N == 128 ? L::CHUNK : 16, 8 * L::P_ROW);
 #pragma unroll
           for (int kk = 0; kk < TILE / 16; ++kk)
-            mma_ss_w(tmem + (2 + ob) * N, dv + kk * 2048, dp + kk * (16 * L::P_ROW), IDESC, (t > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(bar(L::STEMPTY + st));
+            mma_ss_e(tmem + (2 + ob) * N, dv + kk * 2048, dp + kk * (16 * L::P_ROW), IDESC, (t > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_e(bar(L::STEMPTY + st));
         }
         if (!ok) break;
-        mma_commit(bar(L::OFULL + ob));
+        mma_commit_e(bar(L::OFULL + ob));
       }
-      mma_commit(bar(L::DRAIN));
+      mma_commit_e(bar(L::DRAIN));
       drain(bar(L::DRAIN), 0);
     }
   } else {
     // -------------------------------------------------------------- scores
-    constexpr int COLS = N / 2;                    // columns of a warp
-    constexpr int CH = 16;                         // columns in registers at a time
-    const int group = warp >> 3, wq = warp & 3, half = (warp >> 2) & 1;
-    const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16) + half * COLS;
+    constexpr int COLS = N / 4;                    // columns of a warp
+    constexpr int CH = COLS < 16 ? COLS : 16;      // columns in registers at a time
+    const int wq = warp & 3, col0 = (warp >> 2) * COLS;
+    const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16) + col0;
     const int r = wq * 32 + lane;                  // this thread's token in a tile, and feature in O
     uint32_t it = 0, tk = 0;
     bool ok = true;
@@ -482,7 +497,8 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
     uint32_t pend_it = 0;
     int pend_slot = 0, pend_rows = 0;
     auto load_cols = [&](uint32_t addr, uint32_t (&v)[CH]) {
-      tmem_ld16(addr, v);
+      if constexpr (CH == 16) tmem_ld16(addr, v);
+      else tmem_ld8(addr, v);
     };
     auto write_sum = [&]() -> bool {
       const uint32_t ob = pend_it & 1;
@@ -497,7 +513,7 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
         if (D == 128 || wq < 2) {
 #pragma unroll
           for (int c = 0; c < CH; ++c)
-            if (half * COLS + c0 + c < pend_rows) dst[(half * COLS + c0 + c) * D] = __uint_as_float(v[c]);
+            if (col0 + c0 + c < pend_rows) dst[(col0 + c0 + c) * D] = __uint_as_float(v[c]);
         }
       }
       fence_before_sync();
@@ -520,17 +536,15 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
       const float* rp = p.rab_pos ? p.rab_pos + pc.h * p.P : nullptr;
       const float* tbl = tb + sl * (kTimeSlots + 1);
       const bool one_time = !p.rab_time || tmin == tmax;
-      const float* ka = kA + sl * N + half * COLS;
-      const int64_t* tq = qt + sl * N + half * COLS;
-      const int32_t* tq32 = qt32 + sl * N + half * COLS;
-      const uint32_t tk0 = tk;                           // of the piece's first tile
-      tk += t1 - t0;
-      for (int t = t0 + ((tk0 ^ group) & 1); t < t1; t += 2) {
-        const uint32_t k = tk0 + (t - t0), st = group, ts = k % L::NT;
+      const float* ka = kA + sl * N + col0;
+      const int64_t* tq = qt + sl * N + col0;
+      const int32_t* tq32 = qt32 + sl * N + col0;
+      for (int t = t0; t < t1; ++t, ++tk) {
+        const uint32_t st = tk & 1, ts = tk % L::NT;
         const int j = t * TILE + r;
         int64_t tj = 0;
         if (timed) {
-          ok = mbar_wait(bar(L::TSFULL + ts), (k / L::NT) & 1, wd, 79);
+          ok = mbar_wait(bar(L::TSFULL + ts), (tk / L::NT) & 1, wd, 79);
           if (!ok) break;
           tj = *reinterpret_cast<const int64_t*>(base + L::TS_OFF + ts * (TILE * 8) + r * 8);
         }
@@ -554,67 +568,81 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
         const int64_t rel = tj - tmin;
         const bool far = !fast && __all_sync(0xffffffffu, pmin - j >= p.P - 1 && rel > -kNarrowTsSpan && rel < kNarrowTsSpan) &&
                          tmax - tmin < kNarrowTsSpan;
-        ok = mbar_wait(bar(L::SFULL + st), (k >> 1) & 1, wd, 80);
+        ok = mbar_wait(bar(L::SFULL + st), (tk >> 1) & 1, wd, 80);
         if (!ok) break;
         fence_after_sync();
         uint8_t* ps = base + L::KP_OFF + st * L::KP_BYTES;
-#pragma unroll 1
-        for (int c0 = 0; c0 < COLS; c0 += CH) {
-          uint32_t v[CH];
-          load_cols(lane_base + st * N + c0, v);
+        // P over K: row = token, 16-byte chunks of 8 columns
+        auto put = [&](int c0, const uint32_t (&h2)[CH / 2]) {
+#pragma unroll
+          for (int c = 0; c < CH / 8; ++c) {
+            const int col = col0 + c0 + c * 8;
+            const uint32_t at = N >= 64 ? (col / 64) * L::CHUNK + swz<L::P_ROW>(r, (col % 64) / 8) : swz<L::P_ROW>(r, col / 8);
+            *reinterpret_cast<uint4*>(ps + at) = make_uint4(h2[4 * c], h2[4 * c + 1], h2[4 * c + 2], h2[4 * c + 3]);
+          }
+        };
+        if (fast) {   // the warp's columns all at once: their loads' latency is paid once
+          uint32_t v[COLS / CH][CH];
+#pragma unroll
+          for (int i = 0; i < COLS / CH; ++i) load_cols(lane_base + st * N + i * CH, v[i]);
           tmem_wait_ld();
-          uint32_t h2[CH / 2];
-          if (fast) {
-            const float2 b2 = make_float2(bias, bias);
+          const float2 b2 = make_float2(bias, bias);
+#pragma unroll
+          for (int i = 0; i < COLS / CH; ++i) {
+            uint32_t h2[CH / 2];
 #pragma unroll
             for (int c = 0; c < CH; c += 4) {
-              const float4 k4 = *reinterpret_cast<const float4*>(ka + c0 + c);
-              h2[c / 2] = silu_pair(__ffma2_rn(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
+              const float4 k4 = *reinterpret_cast<const float4*>(ka + i * CH + c);
+              h2[c / 2] = silu_pair(__ffma2_rn(make_float2(__uint_as_float(v[i][c]), __uint_as_float(v[i][c + 1])),
                                                make_float2(k4.x, k4.y), b2));
-              h2[c / 2 + 1] = silu_pair(__ffma2_rn(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])),
+              h2[c / 2 + 1] = silu_pair(__ffma2_rn(make_float2(__uint_as_float(v[i][c + 2]), __uint_as_float(v[i][c + 3])),
                                                    make_float2(k4.z, k4.w), b2));
             }
             if (!whole) {
 #pragma unroll
               for (int c = 0; c < CH / 2; ++c) h2[c] = j < len ? h2[c] : 0u;
             }
-          } else if (far) {
-            const int rel32 = (int)rel;
-            const float fb = tbl[kTimeSlots];
-#pragma unroll
-            for (int c = 0; c < CH; c += 4) {
-              const float4 k4 = *reinterpret_cast<const float4*>(ka + c0 + c);
-              const int4 q4 = *reinterpret_cast<const int4*>(tq32 + c0 + c);
-              const float2 b01 = make_float2(tbl[32 - __clz(abs(q4.x - rel32))] + fb, tbl[32 - __clz(abs(q4.y - rel32))] + fb);
-              const float2 b23 = make_float2(tbl[32 - __clz(abs(q4.z - rel32))] + fb, tbl[32 - __clz(abs(q4.w - rel32))] + fb);
-              h2[c / 2] = silu_pair(__ffma2_rn(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
-                                               make_float2(k4.x, k4.y), b01));
-              h2[c / 2 + 1] = silu_pair(__ffma2_rn(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])),
-                                                   make_float2(k4.z, k4.w), b23));
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < CH; c += 2) {
-              float w[2];
-              uint32_t keep = 0;
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int col = half * COLS + c0 + c + e;
-                const int pos = col < hist ? pos0 + col : len;
-                float bb = tbl[bit_length(tq[c0 + c + e], tj)];
-                if (rp) bb += scaled_bias(rp[min(max(pos - j, 0), p.P - 1)]);
-                w[e] = fmaf(__uint_as_float(v[c + e]), ka[c0 + c + e], bb);
-                keep |= (j <= pos && j < len) ? 0xffffu << (16 * e) : 0u;
-              }
-              h2[c / 2] = silu_pair(make_float2(w[0], w[1])) & keep;
-            }
+            put(i * CH, h2);
           }
-          // P over K: row = token, 16-byte chunks of 8 columns
+        } else {
+#pragma unroll 1
+          for (int c0 = 0; c0 < COLS; c0 += CH) {
+            uint32_t v[CH];
+            load_cols(lane_base + st * N + c0, v);
+            tmem_wait_ld();
+            uint32_t h2[CH / 2];
+            if (far) {
+              const int rel32 = (int)rel;
+              const float fb = tbl[kTimeSlots];
 #pragma unroll
-          for (int c = 0; c < CH / 8; ++c) {
-            const int col = half * COLS + c0 + c * 8;
-            const uint32_t at = N >= 64 ? (col / 64) * L::CHUNK + swz<L::P_ROW>(r, (col % 64) / 8) : swz<L::P_ROW>(r, col / 8);
-            *reinterpret_cast<uint4*>(ps + at) = make_uint4(h2[4 * c], h2[4 * c + 1], h2[4 * c + 2], h2[4 * c + 3]);
+              for (int c = 0; c < CH; c += 4) {
+                const float4 k4 = *reinterpret_cast<const float4*>(ka + c0 + c);
+                const int4 q4 = *reinterpret_cast<const int4*>(tq32 + c0 + c);
+                const float2 b01 = make_float2(tbl[32 - __clz(abs(q4.x - rel32))] + fb, tbl[32 - __clz(abs(q4.y - rel32))] + fb);
+                const float2 b23 = make_float2(tbl[32 - __clz(abs(q4.z - rel32))] + fb, tbl[32 - __clz(abs(q4.w - rel32))] + fb);
+                h2[c / 2] = silu_pair(__ffma2_rn(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
+                                                 make_float2(k4.x, k4.y), b01));
+                h2[c / 2 + 1] = silu_pair(__ffma2_rn(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])),
+                                                     make_float2(k4.z, k4.w), b23));
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < CH; c += 2) {
+                float w[2];
+                uint32_t keep = 0;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int col = col0 + c0 + c + e;
+                  const int pos = col < hist ? pos0 + col : len;
+                  float bb = tbl[bit_length(tq[c0 + c + e], tj)];
+                  if (rp) bb += scaled_bias(rp[min(max(pos - j, 0), p.P - 1)]);
+                  w[e] = fmaf(__uint_as_float(v[c + e]), ka[c0 + c + e], bb);
+                  keep |= (j <= pos && j < len) ? 0xffffu << (16 * e) : 0u;
+                }
+                h2[c / 2] = silu_pair(make_float2(w[0], w[1])) & keep;
+              }
+            }
+            put(c0, h2);
           }
         }
         fence_before_sync();
@@ -632,16 +660,10 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
       if (!ok) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::ITEMEMPTY + sl));
-      if (((tk - 1) & 1) == (uint32_t)group) {           // the group of the piece's last tile writes its sum
-        if (pend) {
-          ok = write_sum();                              // (an older one is out by now, or is waited for here)
-          if (!ok) break;
-        }
-        pend = true;
-        pend_it = it;
-        pend_slot = slot;
-        pend_rows = rows;
-      }
+      pend = true;
+      pend_it = it;
+      pend_slot = slot;
+      pend_rows = rows;
       ++it;
     }
     if (ok && pend) write_sum();
