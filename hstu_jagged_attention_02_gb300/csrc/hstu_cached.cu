@@ -23,13 +23,16 @@ namespace {
 __device__ __forceinline__ float silu(float z) { return z < -1e4f ? 0.f : z / (1.f + expf(-z)); }
 
 constexpr int kFinThreads = 128;   // of a CTA with a warp a row
+constexpr int kFewWarps = 16;      // of a CTA with a row
 
 // NV: the row's features in steps of 128 (4 a lane).
 template <int D, int NV, int kWarps>
 __global__ void __launch_bounds__(kWarps == 1 ? kFinThreads : 32 * kWarps) finish_kernel(const __grid_constant__ CachedParams p,
                                                                                          int N) {
   constexpr int LANES = D / 4;
-  __shared__ __align__(16) float4 sums[kWarps > 1 ? kWarps - 1 : 1][kWarps > 1 ? NV * 32 : 1];
+  constexpr int SHARE = kWarps / NV > 0 ? kWarps / NV : 1;   // warps that share a step's pieces
+  static_assert(kWarps == 1 || kWarps % NV == 0, "as many warps for every step");
+  __shared__ __align__(16) float4 sums[kWarps > 1 ? kWarps : 1][kWarps > 1 ? 32 : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = kWarps == 1 ? (int64_t)blockIdx.x * (kFinThreads / 32) + warp : blockIdx.x;
   const int F = p.H * D;
@@ -55,37 +58,58 @@ __global__ void __launch_bounds__(kWarps == 1 ? kFinThreads : 32 * kWarps) finis
     }
     if (on && p.u && p.y) u[i] = fetch4(p.u + row + i * 128);
   }
+  // the pieces of features f .. f + 3: their number, and the first one's sum
   const float* rows = p.part + (int64_t)(rec.w & 0x3fffffff) * D;
+  auto pieces = [&](int f, const float*& src) -> int {
+    const int h = f / D;
+    if (f >= F || rec.z <= 0) return 0;
+    const int at = rec.x + h * rec.z, c0 = at / quota;
+    src = rows + (int64_t)(rec.y + h + c0) * N * D + f % D;
+    return (at + rec.z - 1) / quota - c0 + 1;
+  };
+  const int64_t next = (int64_t)N * D;    // floats from a piece's sum to the next one's
   float o[NV][4];
   float sum = 0.f;
+  if constexpr (kWarps == 1) {
+    const float* src[NV];
+    int n[NV], most = 0;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int f = i * 128 + lane * 4, h = f / D;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (f < F && rec.z > 0) {
-      const int at = rec.x + h * rec.z, c1 = (at + rec.z - 1) / quota;
-      const float* src = rows + (int64_t)(rec.y + h) * N * D + f % D;
-#pragma unroll 4
-      for (int c = at / quota + (kWarps > 1 ? warp : 0); c <= c1; c += kWarps) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)c * N * D));
-        a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-      }
+    for (int i = 0; i < NV; ++i) {
+      n[i] = pieces(i * 128 + lane * 4, src[i]);
+      most = max(most, n[i]);
+      o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     }
-    o[i][0] = a.x; o[i][1] = a.y; o[i][2] = a.z; o[i][3] = a.w;
-  }
-  if (kWarps > 1) {
-    if (warp > 0) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) sums[warp - 1][i * 32 + lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-    }
-    __syncthreads();
-    if (warp > 0) return;
-    for (int w = 0; w < kWarps - 1; ++w) {
+    for (int c = 0; c < most; ++c) {      // a piece of every step at a time: their loads are under way together
+      float4 x[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const float4 x = sums[w][i * 32 + lane];
-        o[i][0] += x.x; o[i][1] += x.y; o[i][2] += x.z; o[i][3] += x.w;
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < n[i]) x[i] = __ldcg(reinterpret_cast<const float4*>(src[i] + c * next));
       }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) { o[i][0] += x[i].x; o[i][1] += x[i].y; o[i][2] += x[i].z; o[i][3] += x[i].w; }
+    }
+  } else {
+    const float* src = nullptr;
+    const int n = pieces((warp / SHARE) * 128 + lane * 4, src);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int c = warp % SHARE; c < n; c += SHARE) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(src + c * next));
+      a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+    }
+    sums[warp][lane] = a;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      a = sums[i * SHARE][lane];
+#pragma unroll
+      for (int w = 1; w < SHARE; ++w) {
+        const float4 x = sums[i * SHARE + w][lane];
+        a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+      }
+      o[i][0] = a.x; o[i][1] = a.y; o[i][2] = a.z; o[i][3] = a.w;
     }
   }
 #pragma unroll
@@ -142,7 +166,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? kFinThreads : 32 * kWarps) finis
 
 template <int D, int NV>
 cudaError_t launch_finish(const CachedParams& p, int N, bool few, cudaStream_t st) {
-  if (few) return launch_pdl(finish_kernel<D, NV, 8>, dim3((unsigned)p.T), dim3(256), 0, st, p, N);
+  if (few) return launch_pdl(finish_kernel<D, NV, kFewWarps>, dim3((unsigned)p.T), dim3(32 * kFewWarps), 0, st, p, N);
   const unsigned ctas = (unsigned)((p.T + kFinThreads / 32 - 1) / (kFinThreads / 32));
   return launch_pdl(finish_kernel<D, NV, 1>, dim3(ctas), dim3(kFinThreads), 0, st, p, N);
 }
