@@ -67,7 +67,8 @@ class _Call:
     def _workspace(self, bytes_, workspace):
         if workspace is None:
             workspace = torch.zeros(bytes_, device=self.device, dtype=torch.uint8)
-        _need(workspace.device == self.device and workspace.dtype == torch.uint8, "workspace must be uint8 on the cache's device")
+        _need(workspace.device == self.device and workspace.dtype == torch.uint8 and workspace.is_contiguous(),
+              "workspace must be contiguous uint8 on the cache's device")
         self.ws, self.ws_bytes = workspace, workspace.numel()
 
     def _prepare(self, name, *args):

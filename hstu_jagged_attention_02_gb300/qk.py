@@ -144,6 +144,7 @@ class QKProblem:
         need = max(fwd_b, bwd_b if backward else 0)
         if workspace is None:
             workspace = torch.zeros(need, device=dev, dtype=torch.uint8)
+        _need(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace must be contiguous uint8")
         self.ws, self.ws_bytes = workspace, workspace.numel()
         common = (_ptr(num_tokens), _ptr(positions), _ptr(cos), _ptr(sin), _ptr(q_gain), _ptr(k_gain), _ptr(self.q),
                   _ptr(self.k))
@@ -178,6 +179,7 @@ class Launch:
     __slots__ = ("index", "fn", "name", "args", "keep")
 
     def __init__(self, device, fn, name, *args):
+        _need(device.type == "cuda", f"{name} needs tensors on a CUDA device, not on {device}")
         self.index = device.index if device.index is not None else torch.cuda.current_device()
         self.fn, self.name, self.keep = fn, name, args
         self.args = tuple(C.ctypes.byref(a) if isinstance(a, C.ctypes.Structure) else a for a in args)

@@ -583,7 +583,7 @@ hstu_status_t hstu_cache_read(const hstu_cache_desc* cache, const hstu_cache_rea
  * The descriptor is the attention's: dtype and out_dtype BF16, d_qk == d_v ==
  * the cache's d, H <= its H * d limit, total_tokens = rows, max_seq_len = N
  * bounding every L + m, no flags, no dropout.  max_rows bounds every n (it
- * picks the tile's width: 16, 32, 64 or 128 rows).
+ * picks the tile's width: 8, 32, 64 or 128 rows).
  *
  * Precision: K, V and q enter the tensor cores exactly; 16 SiLU(z) is rounded
  * once to FP16 (so scores of 4094 and more overflow to infinity; a bias of
