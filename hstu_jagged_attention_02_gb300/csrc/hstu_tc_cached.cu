@@ -331,7 +331,7 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
           if (lane == 0) tb[sl * (kTimeSlots + 1) + kTimeSlots] = p.rab_pos ? scaled_bias(p.rab_pos[h * p.P + p.P - 1]) : 0.f;
         }
         if (dw == 0) {   // the rows' times, and their range
-          int64_t mn = INT64_MAX, mx = INT64_MIN;
+          int64_t mn = timed ? INT64_MAX : 0, mx = timed ? INT64_MIN : 0;
           for (int r = lane; r < N; r += 32) {
             int64_t t = 0;
             if (timed && r < rows) {
@@ -564,10 +564,11 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
         same = same || j >= len;
         const bool fast = __all_sync(0xffffffffu, same);
         const bool whole = __all_sync(0xffffffffu, j < len);
-        // else only the time buckets may differ (tokens far back), by gaps of 32 bits
+        // else gaps of 32 bits where they fit; far: only the time buckets may differ
         const int64_t rel = tj - tmin;
-        const bool far = !fast && __all_sync(0xffffffffu, pmin - j >= p.P - 1 && rel > -kNarrowTsSpan && rel < kNarrowTsSpan) &&
-                         tmax - tmin < kNarrowTsSpan;
+        const bool narrow = !fast && __all_sync(0xffffffffu, j >= len || (rel > -kNarrowTsSpan && rel < kNarrowTsSpan)) &&
+                            tmax - tmin < kNarrowTsSpan;
+        const bool far = pmin - (t * TILE + wq * 32 + 31) >= p.P - 1;
         ok = mbar_wait(bar(L::SFULL + st), (tk >> 1) & 1, wd, 80);
         if (!ok) break;
         fence_after_sync();
@@ -611,7 +612,7 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
             load_cols(lane_base + st * N + c0, v);
             tmem_wait_ld();
             uint32_t h2[CH / 2];
-            if (far) {
+            if (narrow && far) {
               const int rel32 = (int)rel;
               const float fb = tbl[kTimeSlots];
 #pragma unroll
@@ -624,6 +625,31 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
                                                  make_float2(k4.x, k4.y), b01));
                 h2[c / 2 + 1] = silu_pair(__ffma2_rn(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])),
                                                      make_float2(k4.z, k4.w), b23));
+              }
+            } else if (narrow) {
+              const int rel32 = (int)rel, base_gap = pos0 - j, cand_gap = len - j;   // a row's distance, less its column
+#pragma unroll
+              for (int c = 0; c < CH; c += 4) {
+                const float4 k4 = *reinterpret_cast<const float4*>(ka + c0 + c);
+                const int4 q4 = *reinterpret_cast<const int4*>(tq32 + c0 + c);
+                const float kf[4] = {k4.x, k4.y, k4.z, k4.w};
+                const int qf[4] = {q4.x, q4.y, q4.z, q4.w};
+                float w[4];
+                uint32_t keep[2] = {0, 0};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int col = col0 + c0 + c + e, gap = col < hist ? base_gap + col : cand_gap;
+                  float bb = tbl[32 - __clz(abs(qf[e] - rel32))];
+                  if (rp) bb += scaled_bias(__ldg(rp + min(max(gap, 0), p.P - 1)));
+                  w[e] = fmaf(__uint_as_float(v[c + e]), kf[e], bb);
+                  keep[e >> 1] |= gap >= 0 ? 0xffffu << (16 * (e & 1)) : 0u;
+                }
+                h2[c / 2] = silu_pair(make_float2(w[0], w[1])) & keep[0];
+                h2[c / 2 + 1] = silu_pair(make_float2(w[2], w[3])) & keep[1];
+              }
+              if (!whole) {
+#pragma unroll
+                for (int c = 0; c < CH / 2; ++c) h2[c] = j < len ? h2[c] : 0u;
               }
             } else {
 #pragma unroll
