@@ -72,6 +72,7 @@ __device__ __forceinline__ int block_tiles(const CachedSeq& s, int qb, int N) {
 
 // Where a CTA's part of the work begins.
 struct Start {
+  CachedSeq s;        // the sequence it begins in
   int b, rem;         // sequence, and tiles of it that belong to CTAs before
   int items;          // items before the sequence
   int total, quota;   // tiles in all (0 where the batch is refused), tiles a CTA
@@ -148,6 +149,7 @@ __device__ __forceinline__ void cut_work(const CachedParams& p, int N, int* scan
   const bool mine = first < total && before <= first && first < before + tiles;
   if (per == 1) {
     if (mine) {
+      start->s = s;
       start->b = lo;
       start->rem = first - before;
       start->items = before_items;
@@ -174,6 +176,7 @@ __device__ __forceinline__ void cut_work(const CachedParams& p, int N, int* scan
       int here, i;
       count(b, here, i);
       if (mine && first >= before && first < before + here) {
+        start->s = s;
         start->b = b;
         start->rem = first - before;
         start->items = before_items;
@@ -203,7 +206,7 @@ struct Walk {
     left = min(st.quota, st.total - first);
     b = st.b; items = st.items; qb = 0; h = 0; tile = 0; tiles = 0;
     if (left <= 0) return;
-    load_seq(p, b, s);
+    s = st.s;
     int rem = st.rem;
     tiles = block_tiles(s, qb, N);
     while (rem >= tiles * p.H) {
