@@ -309,7 +309,11 @@ __device__ __forceinline__ int bit_length(int64_t a, int64_t b) {
 constexpr int kTimeSlots = 65;   // bit lengths 0 .. 64
 
 // Rows of a block: as few as the longest sequence asks for.  Up to 8 rows go
-// through the streaming kernel, more through the tensor-memory one.
+// through the streaming kernel, more through the tensor-memory one.  Single
+// calls for 32 users over some 160,000 cached tokens, four heads of 128, by
+// candidates a user: 1: 40.6 us (with 32 rows a block through tensor memory
+// 55.9), 8: 46.7 (58.0), 32: 58.0 (with 128 rows a block 78.5), 64: 65 (79.5),
+// 128: 87.
 inline int cached_block_rows(int max_rows) {
   return max_rows <= 8 ? 8 : (max_rows <= 32 ? 32 : (max_rows <= 64 ? 64 : 128));
 }

@@ -6,7 +6,7 @@
 // matrix instruction (m16n8k16, FP16 -> FP32) takes them; a decoded tile is
 // not written to shared memory and read again as in the tensor-memory kernel,
 // whose 128 KB of traffic for 18 KB of cache would bound few rows by the shared
-// memory's rate.  A warp takes 16 tokens at a time:
+// memory's rate.  A warp takes 32 tokens at a time, in two halves of 16:
 //
 //   S^T [16 tokens x 8 rows] = K Q^T      lane (g, t), g = lane / 4, t = lane % 4, holds tokens tok(g), tok(g) + 8,
 //                                         features [t d/4, (t + 1) d/4): the products' inner index runs over the
@@ -16,17 +16,27 @@
 //                                         [g d/8, (g + 1) d/8), pairs of tokens put together by byte permutes
 //
 // tok(r) = 0, 2, 4, 6, 1, 3, 5, 7: neighbouring t then read rows of both
-// parities, half as many bank conflicts.  q stays in registers (FP16, scaled
-// per row by a power of two: hstu_cached.cuh), so does O.
+// parities, half as many bank conflicts.  O stays in registers; q (FP16, scaled
+// per row by a power of two: hstu_cached.cuh) comes from shared memory, once
+// for both halves.  A lane looks up the bias of one token, once for all rows
+// where they share it.
 //
-// A piece's 16-token steps are dealt to the warps in turn.  Each warp copies its
-// own steps ahead (cp.async, three in flight) into a ring of its own, so that no
-// warp waits for another; one warp that copied for all of them took 1,650
-// cycles a tile to issue the copies, twice what the others take to use them.  One more warp
-// walks the CTA's pieces and prepares their records (the rows in FP16, their
-// factors, the head's time biases) a few pieces ahead.  At a piece's end each
-// warp leaves its sum in shared memory and goes on; the last one adds them up,
-// in the warps' order.  Every wait on a barrier is bounded.
+// A piece's steps are dealt to the warps in turn.  Each warp copies its own
+// steps ahead (cp.async, two or three in flight) into a ring of its own, so that
+// no warp waits for another; one warp that copied for all of them took 1,650
+// cycles a tile to issue the copies, twice what the others take to use them.
+// One more warp walks the CTA's pieces and prepares their records (the rows in
+// FP16, their factors, the head's time biases) a few pieces ahead.  At a piece's
+// end each warp leaves its sum in shared memory and goes on; the last one adds
+// them up, in the warps' order.  Every wait on a barrier is bounded.
+//
+// What bounds it: instructions, 790 for 32 tokens of 128 features, at 1.9 a
+// cycle with the four warps a sub-partition that the registers allow, and 4 us
+// of lookups before the first product.  32 users with one row each over some
+// 162,000 cached tokens, four heads of 128: 35.0 us, 2.7 TB/s of cache (of 6.8
+// measured for a copy).  Steps of 16 tokens: 36.6 us (the lookups and the
+// copies' addresses twice as often), but 9.1 against 9.6 us for a single row over
+// 300 tokens.
 #include "hstu_cached.cuh"
 #include "tc_ptx.cuh"
 
@@ -50,19 +60,20 @@ struct __align__(16) SPiece {
   int valid;                   // 0: no more pieces
   int b, h, rows, hist;        // sequence, head; rows of the block, history rows among them
   int pos0, L;                 // position of its first row, cached tokens
-  int step0, step1, slot;      // 16-token steps; where the sum goes
+  int step0, step1, slot;      // 32-token steps; where the sum goes
 };
 
 template <int D>
 struct SCfg {
   static constexpr int WARPS = 16, THREADS = (WARPS + 1) * 32;        // 17 warps, 5 a sub-partition
   static constexpr int REGS = 96;
-  static constexpr int DEPTH = 3;                                     // steps in flight a warp
+  static constexpr int TOKENS = 32;                                   // of a step: two matrix instructions' M
+  static constexpr int DEPTH = D == 128 ? 2 : 3;                      // steps in flight a warp
   static constexpr int PIECES = DEPTH + 1;   // records: a warp's copies run up to DEPTH pieces ahead of its work
   // a step: K codes, V codes, K scales, V scales, times
-  static constexpr int CODES = 16 * (D / 2), SCALES = 16 * (D / 16);
+  static constexpr int CODES = TOKENS * (D / 2), SCALES = TOKENS * (D / 16);
   static constexpr int STEP_V = CODES, STEP_KS = 2 * CODES, STEP_VS = STEP_KS + SCALES, STEP_T = STEP_VS + SCALES;
-  static constexpr int STEP = STEP_T + 128;
+  static constexpr int STEP = STEP_T + TOKENS * 8;
   static constexpr int SUM_OFF = WARPS * DEPTH * STEP;                // float [WARPS][kRows][D], or of half the rows twice
   static constexpr int PIECE_OFF = SUM_OFF + WARPS * kRows * D * 4;   // SPiece [PIECES]
   static constexpr int BAR_OFF = PIECE_OFF + PIECES * (int)sizeof(SPiece<D>);   // records full, empty; sums free [2]
@@ -177,8 +188,8 @@ __device__ __forceinline__ void write_piece(const CachedParams& p, const Walk& w
     out.L = w.s.L;
     out.b = w.b;
     out.table = p.table + (int64_t)w.b * p.max_pages;
-    out.step0 = w.tile * (kCachedTile / 16);
-    out.step1 = min((w.tile + w.take()) * (kCachedTile / 16), (w.s.L + 15) / 16);
+    out.step0 = w.tile * (kCachedTile / SCfg<D>::TOKENS);
+    out.step1 = min((w.tile + w.take()) * (kCachedTile / SCfg<D>::TOKENS), (w.s.L + SCfg<D>::TOKENS - 1) / SCfg<D>::TOKENS);
     out.slot = w.slot(p);
   }
   __syncwarp();
@@ -244,7 +255,7 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
   float* sums = reinterpret_cast<float*>(smem + C::SUM_OFF);
   const uint8_t* ring = smem + warp * (C::DEPTH * C::STEP);
   const uint32_t ring0 = smem0 + warp * (C::DEPTH * C::STEP);
-  const int spp_log = p.page_log - 4;    // 16-token steps of a page
+  const int spp_log = p.page_log - 5;    // steps of a page
   bool ok = true, wide = false;          // wide: the last piece's sums took the whole space
 
   // The copies run ahead of the work: `issued` and `worked` steps of this warp
@@ -279,7 +290,7 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
   auto fill = [&]() {
     while (issued - worked < (uint32_t)C::DEPTH && look()) {
       if (ipage >= 0 && ipage < p.num_pages) {
-        const int place = (ist & ((1 << spp_log) - 1)) << 4;
+        const int place = (ist & ((1 << spp_log) - 1)) * C::TOKENS;
         const uint8_t* block = p.pages + ((int64_t)ipage * p.H + ih) * lay.bytes();
         const uint8_t* codes = block + place * (D / 2) + lane * 16;
         const uint32_t dst = ring0 + (issued % C::DEPTH) * C::STEP + lane * 16;
@@ -288,13 +299,13 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
           copy16(dst + 512 * i, codes + 512 * i);
           copy16(dst + C::STEP_V + 512 * i, codes + lay.half() + 512 * i);
         }
-        constexpr int NS = C::SCALES / 16;   // lanes that copy K scales, V scales; 8 more the times
+        constexpr int NS = C::SCALES / 16;   // lanes that copy K scales, V scales
         const uint8_t* scales = block + lay.scales() + place * (D / 16) + lane * 16;
         if (lane < NS) copy16(dst + C::STEP_KS, scales);
         else if (lane < 2 * NS) copy16(dst + C::STEP_KS, scales + lay.half() - C::SCALES);
-        else if (lane < 2 * NS + 8 && p.times)
-          copy16(dst + C::STEP_KS, reinterpret_cast<const uint8_t*>(p.page_times + ((int64_t)ipage << p.page_log) + place) +
-                                       (lane - 2 * NS) * 16);
+        if (p.times && lane >= 16)           // and the times
+          copy16(dst - 256 + C::STEP_T, reinterpret_cast<const uint8_t*>(p.page_times + ((int64_t)ipage << p.page_log) + place) +
+                                            (lane - 16) * 16);
       } else if (lane == 0) {
         set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, ib);
       }
@@ -337,35 +348,42 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
         else copy_wait<0>();
         __syncwarp();
         const uint8_t* part = ring + (worked % C::DEPTH) * C::STEP;
-        const int j16 = step * 16;                         // first token of the step
+        const int js = step * C::TOKENS;                   // first token of the step
         {
-          float c[2][4] = {};     // two chains of products, added at their end
+          float c[2][4] = {};     // scores of its two halves
           {
-            uint32_t k0[D / 32], k1[D / 32];
-            load_words<D / 32>(part + at.k, k0);
-            load_words<D / 32>(part + at.k + 8 * (D / 2), k1);
-            const uint8_t* ks = part + at.ks;
-            const __half2 s0 = e4m3x2_half2(D == 128 ? *reinterpret_cast<const uint16_t*>(ks) : *ks);
-            const __half2 s1 = e4m3x2_half2(D == 128 ? *reinterpret_cast<const uint16_t*>(ks + 8 * (D / 16)) : ks[8 * (D / 16)]);
+            uint32_t k[4][D / 32];
+            uint32_t ks[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {                  // tokens token_of(g) + 8 i
+              load_words<D / 32>(part + at.k + 8 * i * (D / 2), k[i]);
+              const uint8_t* sp = part + at.ks + 8 * i * (D / 16);
+              ks[i] = D == 128 ? *reinterpret_cast<const uint16_t*>(sp) : *sp;
+            }
+            __half2 sc[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[i] = e4m3x2_half2(ks[i]);
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) {             // 8 features at a time: two inner steps
               const bool hi = D == 128 && x >= 2;
-              const uint4 a = decode8(k0[x], hi ? __high2half2(s0) : __low2half2(s0));
-              const uint4 b = decode8(k1[x], hi ? __high2half2(s1) : __low2half2(s1));
               const uint2 q0 = pc.q[2 * x][lane], q1 = pc.q[2 * x + 1][lane];
-              mma16816(c[0], a.x, b.x, a.y, b.y, q0.x, q0.y);
-              mma16816(c[1], a.z, b.z, a.w, b.w, q1.x, q1.y);
-            }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) c[0][e] += c[1][e];
+              for (int half = 0; half < 2; ++half) {
+                const __half2 s0 = sc[2 * half], s1 = sc[2 * half + 1];
+                const uint4 a = decode8(k[2 * half][x], hi ? __high2half2(s0) : __low2half2(s0));
+                const uint4 b = decode8(k[2 * half + 1][x], hi ? __high2half2(s1) : __low2half2(s1));
+                mma16816(c[half], a.x, b.x, a.y, b.y, q0.x, q0.y);
+                mma16816(c[half], a.z, b.z, a.w, b.w, q1.x, q1.y);
+              }
+            }
           }
-          // a lane looks up the bias of token lane % 16 towards the block's rows, if they share it
-          const int jl = j16 + (lane & 15);
+          // a lane looks up the bias of its token towards the block's rows, if they share it
+          const int jl = js + lane;
           int64_t tl = 0;
-          if (p.times) tl = reinterpret_cast<const int64_t*>(part + C::STEP_T)[lane & 15];
+          if (p.times) tl = reinterpret_cast<const int64_t*>(part + C::STEP_T)[lane];
           bool same = jl <= pmin;
           float bl = far_bias;
-          if (pmin - (j16 + 15) < p.P - 1 && rp) {         // near tokens: their buckets' own biases, from global memory
+          if (pmin - (js + C::TOKENS - 1) < p.P - 1 && rp) {   // near tokens: their buckets' own biases, from global memory
             const int a = min(max(pmin - jl, 0), p.P - 1);
             bl = scaled_bias(__ldg(rp + a));
             same = same && a == min(max(pmax - jl, 0), p.P - 1);
@@ -378,19 +396,21 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
               same = same && min(a, p.Tb - 1) == min(bit_length(tmax, tl), p.Tb - 1) && (tl <= tmin || tl >= tmax);
             }
           }
-          // scores of tokens j0 (c[0], c[1]) and j0 + 8 (c[2], c[3]) for rows 2t, 2t + 1
-          const int j0 = j16 + token_of(g);
-          uint32_t pr[2];
+          // scores of tokens token_of(g) + 8 i (c[i / 2][2 (i % 2)], and the next) for rows 2t, 2t + 1
+          const int j0 = js + token_of(g);
+          uint32_t pr[4];
           const float2 k2 = *reinterpret_cast<const float2*>(pc.ka + 2 * t);
           if (__all_sync(0xffffffffu, same || jl >= len)) {
-            const float b0 = __shfl_sync(0xffffffffu, bl, token_of(g)), b1 = __shfl_sync(0xffffffffu, bl, token_of(g) + 8);
-            pr[0] = silu_pair(__ffma2_rn(make_float2(c[0][0], c[0][1]), k2, make_float2(b0, b0)));
-            pr[1] = silu_pair(__ffma2_rn(make_float2(c[0][2], c[0][3]), k2, make_float2(b1, b1)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float b = __shfl_sync(0xffffffffu, bl, token_of(g) + 8 * i);
+              pr[i] = silu_pair(__ffma2_rn(make_float2(c[i >> 1][2 * (i & 1)], c[i >> 1][2 * (i & 1) + 1]), k2, make_float2(b, b)));
+            }
           } else {
-#pragma unroll 1
-            for (int e = 0; e < 2; ++e) {
-              const int j = j0 + 8 * e;
-              const int64_t tj = __shfl_sync(0xffffffffu, tl, token_of(g) + 8 * e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = j0 + 8 * i;
+              const int64_t tj = __shfl_sync(0xffffffffu, tl, token_of(g) + 8 * i);
               float b[2];
               uint32_t keep = 0;
 #pragma unroll
@@ -400,38 +420,42 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
                 if (rp) b[f] += scaled_bias(rp[min(max(pos - j, 0), p.P - 1)]);
                 keep |= j <= pos ? 0xffffu << (16 * f) : 0u;
               }
-              const float2 cc = e ? make_float2(c[0][2], c[0][3]) : make_float2(c[0][0], c[0][1]);
-              const uint32_t v = silu_pair(__ffma2_rn(cc, k2, make_float2(b[0], b[1]))) & keep;
-              if (e) pr[1] = v;
-              else pr[0] = v;
+              pr[i] = silu_pair(__ffma2_rn(make_float2(c[i >> 1][2 * (i & 1)], c[i >> 1][2 * (i & 1) + 1]), k2,
+                                           make_float2(b[0], b[1]))) & keep;
             }
           }
-          uint32_t vs[4];
+          const bool tail = js + C::TOKENS > len;          // tokens behind the cache's end: neither scores nor values
+          if (tail) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) vs[e] = part[at.vs[e & 1] + 8 * (e >> 1) * (D / 16)];
-          if (j16 + 16 > len) {                            // tokens behind the cache's end: neither scores nor values
-#pragma unroll
-            for (int e = 0; e < 2; ++e) pr[e] = j0 + 8 * e < len ? pr[e] : 0u;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (j16 + token_of(2 * t + (e & 1)) + 8 * (e >> 1) >= len) vs[e] = 0;
+            for (int i = 0; i < 4; ++i) pr[i] = j0 + 8 * i < len ? pr[i] : 0u;
           }
-          const uint32_t b0 = transpose8x8(pr[0]), b1 = transpose8x8(pr[1]);
-          // values: a code of each of two tokens to a byte, so that the decoded pairs are pairs of tokens
-          const __half2 s01 = e4m3x2_half2(vs[0] | (vs[1] << 8)), s23 = e4m3x2_half2(vs[2] | (vs[3] << 8));
-          uint32_t v[4][D / 64];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) load_words<D / 64>(part + at.v[e & 1] + 8 * (e >> 1) * (D / 2), v[e]);
+          for (int half = 0; half < 2; ++half) {
+            uint32_t vs[4];
 #pragma unroll
-          for (int x = 0; x < D / 64; ++x) {               // 8 features of the lane's D / 8
-            auto even = [](uint32_t a, uint32_t b) { return (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u); };
-            auto odd = [](uint32_t a, uint32_t b) { return ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u); };
-            const uint4 e0 = decode8(even(v[0][x], v[1][x]), s01), o0 = decode8(odd(v[0][x], v[1][x]), s01);
-            const uint4 e1 = decode8(even(v[2][x], v[3][x]), s23), o1 = decode8(odd(v[2][x], v[3][x]), s23);
-            mma16816(o[4 * x], e0.x, o0.x, e1.x, o1.x, b0, b1);
-            mma16816(o[4 * x + 1], e0.y, o0.y, e1.y, o1.y, b0, b1);
-            mma16816(o[4 * x + 2], e0.z, o0.z, e1.z, o1.z, b0, b1);
-            mma16816(o[4 * x + 3], e0.w, o0.w, e1.w, o1.w, b0, b1);
+            for (int e = 0; e < 4; ++e) vs[e] = part[at.vs[e & 1] + (16 * half + 8 * (e >> 1)) * (D / 16)];
+            if (tail) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (js + token_of(2 * t + (e & 1)) + 16 * half + 8 * (e >> 1) >= len) vs[e] = 0;
+            }
+            const uint32_t b0 = transpose8x8(pr[2 * half]), b1 = transpose8x8(pr[2 * half + 1]);
+            // values: a code of each of two tokens to a byte, so that the decoded pairs are pairs of tokens
+            const __half2 s01 = e4m3x2_half2(vs[0] | (vs[1] << 8)), s23 = e4m3x2_half2(vs[2] | (vs[3] << 8));
+            uint32_t v[4][D / 64];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) load_words<D / 64>(part + at.v[e & 1] + (16 * half + 8 * (e >> 1)) * (D / 2), v[e]);
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) {             // 8 features of the lane's D / 8
+              auto even = [](uint32_t a, uint32_t b) { return (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u); };
+              auto odd = [](uint32_t a, uint32_t b) { return ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u); };
+              const uint4 e0 = decode8(even(v[0][x], v[1][x]), s01), o0 = decode8(odd(v[0][x], v[1][x]), s01);
+              const uint4 e1 = decode8(even(v[2][x], v[3][x]), s23), o1 = decode8(odd(v[2][x], v[3][x]), s23);
+              mma16816(o[4 * x], e0.x, o0.x, e1.x, o1.x, b0, b1);
+              mma16816(o[4 * x + 1], e0.y, o0.y, e1.y, o1.y, b0, b1);
+              mma16816(o[4 * x + 2], e0.z, o0.z, e1.z, o1.z, b0, b1);
+              mma16816(o[4 * x + 3], e0.w, o0.w, e1.w, o1.w, b0, b1);
+            }
           }
         }
         __syncwarp();
