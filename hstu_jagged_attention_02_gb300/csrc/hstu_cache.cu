@@ -16,8 +16,8 @@
 // quotient by the reciprocal, rounded to 16 significant bits, decides rightly.
 // A normed or rotated key is known to 2^-20 of its terms only; where the
 // codes (or the scale) of x - d and x + d differ, the warp computes its rows
-// again in FP64 and compares with the borders themselves.  That happens to
-// about one row in a thousand.
+// again as sums of two FP32 numbers, good to 2^-44, and compares with the
+// borders themselves.  That happens to about one row in a thousand.
 #include "hstu_fp4.cuh"
 #include "hstu_internal.h"
 #include "hstu_rows.cuh"
@@ -109,32 +109,64 @@ __device__ __forceinline__ bool encode_banded(const float2 (&x)[2], const float2
   return sure && (diff & (nonzero * 15u)) == 0;
 }
 
-// The same from FP64 (every border compared with itself); bad: a NaN in the group.
-__device__ __noinline__ Coded encode_f64(double x0, double x1, double x2, double x3, double top, bool bad) {
-  const double x[4] = {x0, x1, x2, x3};
+// A number as the sum of two FP32 ones, h the nearest to it: 2^-48 of it in
+// precision, on the FP32 units (an FP64 path of the same steps took 7 us to the
+// 1 us of this one; the exactness of sums and products in two parts is Dekker's
+// and Knuth's).
+struct Two {
+  float h, l;
+};
+__device__ __forceinline__ Two sum_of(float a, float b) {          // exact
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two join(float h, float l) {            // exact for |l| <= |h|
+  const float s = __fadd_rn(h, l);
+  return {s, __fsub_rn(l, __fsub_rn(s, h))};
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+  const Two s = sum_of(a.h, b.h);
+  return join(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+}
+__device__ __forceinline__ Two operator*(Two a, float f) {
+  const float p = __fmul_rn(a.h, f);
+  return join(p, __fmaf_rn(a.l, f, __fmaf_rn(a.h, f, -p)));
+}
+__device__ __forceinline__ Two operator-(Two a) { return {-a.h, -a.l}; }
+// whether |a| lies above a border, or on it too
+__device__ __forceinline__ float over(Two a, float border) { return __fadd_rn(__fsub_rn(a.h, border), a.l); }
+
+// 1 / sqrt(a): one Newton step with its quadratic term from the FP32 value.
+__device__ __forceinline__ Two rsqrt_two(Two a) {
+  const float r = rsqrtf(a.h), p = __fmul_rn(r, r), e = __fmaf_rn(r, r, -p);
+  const float t = __fsub_rn(__fmaf_rn(-a.h, p, 1.f), __fmaf_rn(a.h, e, __fmul_rn(a.l, p)));   // 1 - a r^2
+  return join(r, __fmul_rn(r, __fmul_rn(t, __fmaf_rn(0.375f, t, 0.5f))));
+}
+
+// The same from two parts each (every border compared with itself); bad: a NaN in the group.
+__device__ __forceinline__ Coded encode_two(const Two (&x)[4], Two top, bool bad) {
   Coded c;
   // the nearest scale by its FP32 neighbour, then its two borders (halves between scales) times 6
-  c.scale = e4m3_of((float)(top / 6.0));
+  c.scale = e4m3_of(top.h * 0.16666667f);
   if (c.scale < 0x7eu) {
-    const double here = e4m3_float(c.scale), up = e4m3_float(c.scale + 1);
-    const double border = 3.0 * (here + up);
-    if (top > border || (top == border && (c.scale & 1))) c.scale += 1;
+    const float d = over(top, 3.f * (e4m3_float(c.scale) + e4m3_float(c.scale + 1)));
+    if (d > 0.f || (d == 0.f && (c.scale & 1))) c.scale += 1;
   }
   if (c.scale > 0 && c.scale < 0x7fu) {
-    const double here = e4m3_float(c.scale), down = e4m3_float(c.scale - 1);
-    const double border = 3.0 * (here + down);
-    if (top < border || (top == border && (c.scale & 1))) c.scale -= 1;
+    const float d = over(top, 3.f * (e4m3_float(c.scale) + e4m3_float(c.scale - 1)));
+    if (d < 0.f || (d == 0.f && (c.scale & 1))) c.scale -= 1;
   }
-  const double s = e4m3_float(c.scale);
+  const float s = e4m3_float(c.scale);
   if (bad) c.scale = 0x7fu;
   c.codes = 0;
+#pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const double a = fabs(x[e]);
+    const Two a = x[e].h < 0.f ? -x[e] : x[e];
     uint32_t m = 0;
-    if (s > 0.0)
-      m = (a > 0.25 * s) + (a >= 0.75 * s) + (a > 1.25 * s) + (a >= 1.75 * s) + (a > 2.5 * s) + (a >= 3.5 * s) +
-          (a > 5.0 * s);
-    c.codes |= (m | (x[e] < 0.0 ? 8u : 0u)) << (4 * e);
+    if (s > 0.f)
+      m = (over(a, 0.25f * s) > 0.f) + (over(a, 0.75f * s) >= 0.f) + (over(a, 1.25f * s) > 0.f) + (over(a, 1.75f * s) >= 0.f) +
+          (over(a, 2.5f * s) > 0.f) + (over(a, 3.5f * s) >= 0.f) + (over(a, 5.f * s) > 0.f);
+    c.codes |= (m | (x[e].h < 0.f ? 8u : 0u)) << (4 * e);
   }
   return c;
 }
@@ -183,7 +215,7 @@ struct KeyTurn {
   bool quad, any_quad;
 };
 
-// A lane's 8 features of a key, normed and turned, coded from FP32; false where FP64 has to decide.
+// A lane's 8 features of a key, normed and turned, coded from FP32; false where that does not decide them.
 template <int LANES>
 __device__ __forceinline__ bool key_f32(const AppendParams& p, const KeyTurn& kt, const Angles& an, const Row8& gain, int lane,
                                         Row8 x, Coded& cx, Coded& cy) {
@@ -237,50 +269,79 @@ __device__ __forceinline__ bool key_f32(const AppendParams& p, const KeyTurn& kt
   return a && b;
 }
 
-// The same in FP64, from the loaded features: the parts' codes in x (low and
-// high half), their scales in y.  how: bit 0
-// turns, 1 moved, 2 quad, 3 any_quad.
+// The same in two parts each, from the loaded features: the parts' codes in x
+// (low and high half), their scales in y.  how: bit 0 turns, 1 moved, 2 quad,
+// 3 any_quad.
 template <int LANES>
-__device__ __noinline__ uint2 key_f64(const AppendParams& p, int how, int f0, int f1, int lane, Row8 v, Angles an) {
-  const float x0[4] = {v.v[0].x, v.v[0].y, v.v[1].x, v.v[1].y}, y0[4] = {v.v[2].x, v.v[2].y, v.v[3].x, v.v[3].y};
+__device__ __noinline__ uint2 key_two(const AppendParams& p, int how, int f0, int f1, int lane, Row8 v, Angles an) {
+  const float x0[8] = {v.v[0].x, v.v[0].y, v.v[1].x, v.v[1].y, v.v[2].x, v.v[2].y, v.v[3].x, v.v[3].y};
   const float c[4] = {an.c[0].x, an.c[0].y, an.c[1].x, an.c[1].y}, s[4] = {an.s[0].x, an.s[0].y, an.s[1].x, an.s[1].y};
   const bool quad = how & 4, any_quad = how & 8;
-  double x[4], y[4], rs = 1.0;
+  Two rs = {1.f, 0.f};
   if (p.norm) {
-    double ss = 0.0;
-    for (int e = 0; e < 4; ++e) ss += (double)x0[e] * x0[e] + (double)y0[e] * y0[e];
-    rs = 1.0 / sqrt(row_sum<LANES>(ss) / (8 * LANES) + (double)p.eps);
+    Two ss = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {     // a BF16 number's square is an FP32 number
+      const Two a = sum_of(ss.h, __fmul_rn(x0[e], x0[e]));
+      ss = {a.h, __fadd_rn(ss.l, a.l)};
+    }
+    ss = join(ss.h, ss.l);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1)
+      ss = ss + Two{__shfl_xor_sync(0xffffffffu, ss.h, o), __shfl_xor_sync(0xffffffffu, ss.l, o)};
+    rs = rsqrt_two(ss * (1.f / (8 * LANES)) + Two{p.eps, 0.f});
   }
+  Two x[4], y[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    x[e] = x0[e] * rs * (p.gain ? (double)p.gain[f0 + e] : 1.0) * p.k_scale;
-    y[e] = y0[e] * rs * (p.gain ? (double)p.gain[f1 + e] : 1.0) * p.k_scale;
+    x[e] = rs * x0[e] * (p.gain ? p.gain[f0 + e] : 1.f) * p.k_scale;
+    y[e] = rs * x0[4 + e] * (p.gain ? p.gain[f1 + e] : 1.f) * p.k_scale;
   }
   if (how & 1) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      double& a = p.interleaved ? (e < 2 ? x[2 * e] : y[2 * e - 4]) : x[e];
-      double& b = p.interleaved ? (e < 2 ? x[2 * e + 1] : y[2 * e - 3]) : y[e];
-      const double u = a * c[e] - b * s[e], w = b * c[e] + a * s[e];
+      Two& a = p.interleaved ? (e < 2 ? x[2 * e] : y[2 * e - 4]) : x[e];
+      Two& b = p.interleaved ? (e < 2 ? x[2 * e + 1] : y[2 * e - 3]) : y[e];
+      const Two u = a * c[e] + -(b * s[e]), w = b * c[e] + a * s[e];
       a = u;
       b = w;
     }
   }
-  if (how & 2) to_neighbours<LANES>(x, y, lane, p.rot);
-  double tx = 0.0, ty = 0.0;
-  double bx = 0.0, by = 0.0;        // 1: a NaN, which the maximum passes over
+  if (how & 2) {
+    float xh[4], xl[4], yh[4], yl[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { xh[e] = x[e].h; xl[e] = x[e].l; yh[e] = y[e].h; yl[e] = y[e].l; }
+    to_neighbours<LANES>(xh, yh, lane, p.rot);
+    to_neighbours<LANES>(xl, yl, lane, p.rot);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { x[e] = {xh[e], xl[e]}; y[e] = {yh[e], yl[e]}; }
+  }
+  // a group's largest magnitude: in the order of (h, l), as one 64-bit number
+  unsigned long long tx = 0, ty = 0;
+  float bx = 0.f, by = 0.f;           // 1: a NaN
+  auto largest = [](Two& a, unsigned long long& top, float& bad) {
+    if (!(fabsf(a.h) <= 3.4028234e38f)) a.l = 0.f;                  // infinities have no second part
+    if (a.h != a.h) {
+      bad = 1.f;
+    } else {
+      const Two m = a.h < 0.f ? -a : a;
+      const uint32_t low = __float_as_uint(m.l);
+      const unsigned long long key = ((unsigned long long)__float_as_uint(fabsf(m.h)) << 32) | (low ^ ((int)low < 0 ? 0xffffffffu : 0x80000000u));
+      top = key > top ? key : top;
+    }
+  };
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    tx = fmax(tx, fabs(x[e]));
-    ty = fmax(ty, fabs(y[e]));
-    if (x[e] != x[e]) bx = 1.0;
-    if (y[e] != y[e]) by = 1.0;
+    largest(x[e], tx, bx);
+    largest(y[e], ty, by);
   }
-  auto mx = [](double a, double b) { return fmax(a, b); };
-  group_tops(tx, ty, quad, any_quad, mx);
-  group_tops(bx, by, quad, any_quad, mx);
-  const Coded cx = encode_f64(x[0], x[1], x[2], x[3], tx, bx != 0.0);
-  const Coded cy = encode_f64(y[0], y[1], y[2], y[3], ty, by != 0.0);
+  group_tops(tx, ty, quad, any_quad, [](unsigned long long a, unsigned long long b) { return a > b ? a : b; });
+  group_tops(bx, by, quad, any_quad, [](float a, float b) { return fmaxf(a, b); });
+  auto value = [](unsigned long long key) -> Two {
+    const uint32_t low = (uint32_t)key;
+    return {__uint_as_float((uint32_t)(key >> 32)), key ? __uint_as_float(low ^ ((int)low < 0 ? 0x80000000u : 0xffffffffu)) : 0.f};
+  };
+  const Coded cx = encode_two(x, value(tx), bx != 0.f), cy = encode_two(y, value(ty), by != 0.f);
   return make_uint2((cx.codes & 0xffffu) | (cy.codes << 16), cx.scale | (cy.scale << 8));
 }
 
@@ -409,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const __grid_consta
         Coded cx, cy;
         const bool sure = key_f32<LANES>(p, kt, an, gain, lane, kx, cx, cy);
         if (__any_sync(0xffffffffu, !sure && head < p.H)) {
-          const uint2 r = key_f64<LANES>(
+          const uint2 r = key_two<LANES>(
               p, (kt.pt.turns ? 1 : 0) | (kt.moved ? 2 : 0) | (kt.quad ? 4 : 0) | (kt.any_quad ? 8 : 0), kt.pt.f0, kt.pt.f1,
               lane, kx, an);
           cx.codes = r.x & 0xffffu; cy.codes = r.x >> 16;

@@ -212,3 +212,20 @@ def test_tables_that_do_not_fit_are_reported(what):
     assert pr.device_error() == C.HSTU_ERR_DEVICE_CHECK
     pr.ws.zero_()
     assert pr.device_error() == 0
+
+
+def test_many_keys_near_borders():
+    """Enough normed and rotated keys that hundreds of rows hold a feature
+    within 2^-20 of a border, where FP32 alone cannot tell the sides apart."""
+    from hstu_jagged_attention_02_gb300.cache import hstu_cache_append, hstu_cache_read
+    H, d, page, rot = 8, 128, 128, 128
+    b = Batch([12000, 9000], [0, 0], H, d, page, seed=77)
+    c = _cache(b, H, d, page, k_exp=1)
+    gain = (1 + 0.3 * torch.randn(d, generator=torch.Generator().manual_seed(2))).cuda()
+    tab = R.rope_tables(12000, rot)
+    cos, sin = (torch.from_numpy(x).cuda() for x in tab)
+    hstu_cache_append(c, b.k, b.v, b.off, b.cache_lens, b.table, timestamps=b.times, cos=cos, sin=sin, norm=True, eps=1e-5,
+                      k_gain=gain)
+    k, _, _ = hstu_cache_read(c, b.off, b.starts, b.table)
+    want = R.qk_forward(_f64(b.k), _f64(gain), tab[0][b.pos], tab[1][b.pos], False, True, float(np.float32(1e-5)))
+    np.testing.assert_array_equal(_f64(k), R.four_bit(want, 1))
