@@ -140,7 +140,9 @@ __global__ void __launch_bounds__(kQkThreads) qk_fwd_kernel(const __grid_constan
 template <typename TI, int D>
 __global__ void __launch_bounds__(kBwdThreads) qk_bwd_kernel(const __grid_constant__ QkParams p, int chunks) {
   constexpr int LANES = D / 8, PER = 32 / LANES, WARPS = kBwdThreads / 32;
-  __shared__ __align__(16) float red[WARPS][2][D];
+  // the warps' sums; at the end the groups' sums and errors
+  constexpr int ROWS = 8 * kBwdThreads / (2 * D) > WARPS ? 8 * kBwdThreads / (2 * D) : WARPS;
+  __shared__ __align__(16) float red[ROWS][2][D];
   __shared__ int last;
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES, sub = lane / LANES;
@@ -179,34 +181,58 @@ __global__ void __launch_bounds__(kBwdThreads) qk_bwd_kernel(const __grid_consta
       const int64_t at = (int64_t)checked_position(p, t) * (p.rot >> 1) + 4 * l;
       an.load(p.cos + at, p.sin + at, -1.f);
     }
-    auto work = [&](auto W) {
-      constexpr int w = decltype(W)::value;
-      if (r * PER >= p.H[w]) return;
-      const bool on = h < p.H[w];
-      Row8 g(g0[w], g1[w]);
-      if (pt.turns) an.turn(g, p.interleaved);
-      if (p.norm) {
-        const Row8 gain = load_gain(p.gain[w], pt);
-        Row8 x(x0[w], x1[w]), e = g;
-        e.times(gain);
-        const float ss = row_sum<LANES>(x.dot(x)), se = row_sum<LANES>(x.dot(e));
-        const float rs = rsqrtf(fmaf(ss, 1.f / D, p.eps));
-        const float m = -se * rs * (1.f / D);      // - mean(e gain x r)
-        x.times(rs);
+    // q's rows (1), k's (2) or both (3): side by side, so that their sums' shuffles overlap
+    auto work = [&](auto WHICH) {
+      constexpr int W0 = decltype(WHICH)::value == 2 ? 1 : 0, W1 = decltype(WHICH)::value == 1 ? 1 : 2;
+      Row8 g[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (on) dg[w][i] = __ffma2_rn(g.v[i], x.v[i], dg[w][i]);
-          g.v[i] = __fmul2_rn(__ffma2_rn(x.v[i], make_float2(m, m), e.v[i]), make_float2(rs, rs));
+      for (int w = W0; w < W1; ++w) {
+        g[w] = Row8(g0[w], g1[w]);
+        if (pt.turns) an.turn(g[w], p.interleaved);
+      }
+      if (p.norm) {
+        Row8 x[2], e[2];
+        float ss[2], se[2];
+#pragma unroll
+        for (int w = W0; w < W1; ++w) {
+          x[w] = Row8(x0[w], x1[w]);
+          e[w] = g[w];
+          e[w].times(load_gain(p.gain[w], pt));
+          ss[w] = x[w].dot(x[w]);
+          se[w] = x[w].dot(e[w]);
+        }
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int w = W0; w < W1; ++w) {
+            ss[w] += __shfl_xor_sync(0xffffffffu, ss[w], o);
+            se[w] += __shfl_xor_sync(0xffffffffu, se[w], o);
+          }
+#pragma unroll
+        for (int w = W0; w < W1; ++w) {
+          const float rs = rsqrtf(fmaf(ss[w], 1.f / D, p.eps));
+          const float m = -se[w] * rs * (1.f / D);      // - mean(e gain x r)
+          const bool on = h < p.H[w];
+          x[w].times(rs);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (on) dg[w][i] = __ffma2_rn(g[w].v[i], x[w].v[i], dg[w][i]);
+            g[w].v[i] = __fmul2_rn(__ffma2_rn(x[w].v[i], make_float2(m, m), e[w].v[i]), make_float2(rs, rs));
+          }
         }
       }
-      if (on) {
-        TI* dst = static_cast<TI*>(p.out[w]) + t * p.os[w][0] + h * p.os[w][1];
-        store_part(dst + pt.f0, g.v[0], g.v[1]);
-        store_part(dst + pt.f1, g.v[2], g.v[3]);
+#pragma unroll
+      for (int w = W0; w < W1; ++w) {
+        if (h < p.H[w]) {
+          TI* dst = static_cast<TI*>(p.out[w]) + t * p.os[w][0] + h * p.os[w][1];
+          store_part(dst + pt.f0, g[w].v[0], g[w].v[1]);
+          store_part(dst + pt.f1, g[w].v[2], g[w].v[3]);
+        }
       }
     };
-    work(std::integral_constant<int, 0>());
-    work(std::integral_constant<int, 1>());
+    if (r * PER < min(p.H[0], p.H[1])) work(std::integral_constant<int, 3>());
+    else if (r * PER < p.H[0]) work(std::integral_constant<int, 1>());
+    else work(std::integral_constant<int, 2>());
     t += dt;
     r += dr;
     if (r >= chunks) {
@@ -240,31 +266,44 @@ __global__ void __launch_bounds__(kBwdThreads) qk_bwd_kernel(const __grid_consta
   __syncthreads();
   if (!last) return;
   __threadfence();
-  // 2 D columns, the rows dealt to kBwdThreads / (2 D) groups; every sum
-  // carries its rounding errors along (two-sum), as FP64 has a 64th of the rate
-  static_assert(WARPS * 2 * D >= 2 * kBwdThreads, "the groups' sums share the warps' space");
-  constexpr int GROUPS = kBwdThreads / (2 * D);
-  const int col = threadIdx.x % (2 * D), grp = threadIdx.x / (2 * D);
-  float sum = 0.f, err = 0.f;
-  auto add = [&](float v) {
+  // 2 D columns, 4 a thread, the rows dealt to kBwdThreads / (D / 2) groups with
+  // all of a group's loads under way together; every sum carries its rounding
+  // errors along (two-sum), as FP64 has a 64th of the rate
+  constexpr int QUADS = D / 2, GROUPS = kBwdThreads / QUADS, DEEP = D == 128 ? 20 : (D == 64 ? 10 : 5);
+  const int quad = threadIdx.x % QUADS, grp = threadIdx.x / QUADS;
+  auto add = [](float& sum, float& err, float v) {
     const float s = sum + v, back = s - sum;
     err += (sum - (s - back)) + (v - back);
     sum = s;
   };
-#pragma unroll 8
-  for (int b = grp; b < (int)gridDim.x; b += GROUPS) add(__ldcg(p.partial + (size_t)b * 2 * D + col));
-  float2* pairs = reinterpret_cast<float2*>(&red[0][0][0]);
+  float sum[4] = {}, err[4] = {};
+  for (int b0 = grp; b0 < (int)gridDim.x; b0 += GROUPS * DEEP) {
+    float4 v[DEEP];
+#pragma unroll
+    for (int i = 0; i < DEEP; ++i) {
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (b0 + i * GROUPS < (int)gridDim.x)
+        v[i] = __ldcg(reinterpret_cast<const float4*>(p.partial + (size_t)(b0 + i * GROUPS) * 2 * D) + quad);
+    }
+#pragma unroll
+    for (int i = 0; i < DEEP; ++i) {
+      add(sum[0], err[0], v[i].x); add(sum[1], err[1], v[i].y); add(sum[2], err[2], v[i].z); add(sum[3], err[3], v[i].w);
+    }
+  }
+  float* sums = &red[0][0][0];            // [GROUPS][2 D] sums, then as many errors
   __syncthreads();
-  pairs[threadIdx.x] = make_float2(sum, err);
+  *reinterpret_cast<float4*>(sums + grp * 2 * D + 4 * quad) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+  *reinterpret_cast<float4*>(sums + 4 * kBwdThreads + grp * 2 * D + 4 * quad) = make_float4(err[0], err[1], err[2], err[3]);
   __syncthreads();
-  if (grp == 0) {
-    for (int k = 1; k < GROUPS; ++k) {
-      const float2 o = pairs[k * 2 * D + col];
-      add(o.x);
-      err += o.y;
+  if (threadIdx.x < 2 * D) {
+    const int col = threadIdx.x;
+    float s = 0.f, e = 0.f;
+    for (int k = 0; k < GROUPS; ++k) {
+      add(s, e, sums[k * 2 * D + col]);
+      e += sums[4 * kBwdThreads + k * 2 * D + col];
     }
     float* dst = p.dgain[col / D];
-    if (dst) dst[col % D] = sum + err;
+    if (dst) dst[col % D] = s + e;
   }
   if (threadIdx.x == 0) p.hdr[WS_NEXT] = 0;   // ready for the workspace's next call
 }
