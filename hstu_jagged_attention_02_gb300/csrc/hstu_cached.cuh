@@ -308,6 +308,20 @@ __device__ __forceinline__ int bit_length(int64_t a, int64_t b) {
 }
 constexpr int kTimeSlots = 65;   // bit lengths 0 .. 64
 
+// A head's biases as the kernels use them: by time bucket, then the last
+// position bucket's.  A warp; the loads are under way together.
+__device__ __forceinline__ void store_time_biases(const CachedParams& p, int h, float* to, int lane) {
+  constexpr int EACH = (kTimeSlots + 31) / 32;
+  float b[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) b[i] = p.rab_time ? p.rab_time[h * p.Tb + min(lane + 32 * i, p.Tb - 1)] : 0.f;
+  const float far = p.rab_pos ? p.rab_pos[h * p.P + p.P - 1] : 0.f;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i)
+    if (lane + 32 * i < kTimeSlots) to[lane + 32 * i] = scaled_bias(b[i]);
+  if (lane == 0) to[kTimeSlots] = scaled_bias(far);
+}
+
 // Rows of a block: as few as the longest sequence asks for.  Up to 8 rows go
 // through the streaming kernel, more through the tensor-memory one.  Single
 // calls for 32 users over some 160,000 cached tokens, four heads of 128, by

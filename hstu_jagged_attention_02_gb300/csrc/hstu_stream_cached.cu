@@ -54,8 +54,7 @@ struct __align__(16) SPiece {
   uint2 q[D / 16][32];         // the products' right operands, a lane's two registers an inner step
   int64_t tq[kRows], tmin, tmax;   // the rows' times and their range
   float ka[kRows];             // score factors
-  float time_bias[kTimeSlots]; // of the head by bucket, times -log2(e)
-  float far_bias;              // of the head's last position bucket, so too
+  float time_bias[kTimeSlots + 1];   // of the head by bucket, then its last position bucket's, times -log2(e)
   const int32_t* table;        // the sequence's pages
   int valid;                   // 0: no more pieces
   int b, h, rows, hist;        // sequence, head; rows of the block, history rows among them
@@ -174,13 +173,11 @@ __device__ __forceinline__ void write_piece(const CachedParams& p, const Walk& w
     tmax = b > tmax ? b : tmax;
   }
   if (lane < kRows) out.tq[lane] = tq;
-  for (int e = lane; e < kTimeSlots; e += 32)
-    out.time_bias[e] = p.rab_time ? scaled_bias(p.rab_time[w.h * p.Tb + min(e, p.Tb - 1)]) : 0.f;
+  store_time_biases(p, w.h, out.time_bias, lane);
   if (lane == 0) {
     out.tmin = tmin;
     out.tmax = tmax;
     out.valid = 1;
-    out.far_bias = p.rab_pos ? scaled_bias(p.rab_pos[w.h * p.P + p.P - 1]) : 0.f;
     out.h = w.h;
     out.rows = rows;
     out.hist = max(0, min(hist - r0, rows));
@@ -337,7 +334,7 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
       const int len = pc.L, pos0 = pc.pos0, nh = pc.hist;  // (rows behind the history rows are at len)
       const int pmin = nh > 0 ? pos0 : len, pmax = nh == rows ? pos0 + rows - 1 : len;
       const bool one_time = !p.rab_time || pc.tmin == pc.tmax;
-      const float far_bias = pc.far_bias;
+      const float far_bias = pc.time_bias[kTimeSlots];
       const float* rp = p.rab_pos ? p.rab_pos + pc.h * p.P : nullptr;
       const int step1 = pc.step1;
       int step = pc.step0 + first;

@@ -325,21 +325,17 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
           x[i] = make_uint4(0, 0, 0, 0);
           if (r < rows) x[i] = *reinterpret_cast<const uint4*>(p.q + ((row0 + r) * p.H + h) * D + c * 8);
         }
-        if (dw == 1) {   // the head's biases, times -log2(e)
-          for (int e = lane; e < kTimeSlots; e += 32)
-            tb[sl * (kTimeSlots + 1) + e] = p.rab_time ? scaled_bias(p.rab_time[h * p.Tb + min(e, p.Tb - 1)]) : 0.f;
-          if (lane == 0) tb[sl * (kTimeSlots + 1) + kTimeSlots] = p.rab_pos ? scaled_bias(p.rab_pos[h * p.P + p.P - 1]) : 0.f;
-        }
+        if (dw == 1) store_time_biases(p, h, tb + sl * (kTimeSlots + 1), lane);
         if (dw == 0) {   // the rows' times, and their range
-          int64_t mn = timed ? INT64_MAX : 0, mx = timed ? INT64_MIN : 0;
-          for (int r = lane; r < N; r += 32) {
-            int64_t t = 0;
-            if (timed && r < rows) {
-              t = p.times[row0 + r];
-              mn = t < mn ? t : mn;
-              mx = t > mx ? t : mx;
+          int64_t row_time[N / 32], mn = timed ? INT64_MAX : 0, mx = timed ? INT64_MIN : 0;
+#pragma unroll
+          for (int i = 0; i < N / 32; ++i) row_time[i] = timed && lane + 32 * i < rows ? p.times[row0 + lane + 32 * i] : 0;
+#pragma unroll
+          for (int i = 0; i < N / 32; ++i) {
+            if (timed && lane + 32 * i < rows) {
+              mn = row_time[i] < mn ? row_time[i] : mn;
+              mx = row_time[i] > mx ? row_time[i] : mx;
             }
-            qt[sl * N + r] = t;
           }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) {
@@ -351,7 +347,11 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
             pc.tmin = mn;
             pc.tmax = mx;
           }
-          for (int r = lane; r < N; r += 32) qt32[sl * N + r] = (int32_t)(qt[sl * N + r] - mn);   // used where it fits
+#pragma unroll
+          for (int i = 0; i < N / 32; ++i) {
+            qt[sl * N + lane + 32 * i] = row_time[i];
+            qt32[sl * N + lane + 32 * i] = (int32_t)(row_time[i] - mn);   // used where it fits
+          }
         }
         ok = mbar_wait(bar(L::QEMPTY + qbuf), ((it / L::QB) & 1) ^ 1, wd, 66);
         if (!ok) break;
