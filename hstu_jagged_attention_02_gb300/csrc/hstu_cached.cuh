@@ -81,12 +81,13 @@ struct Start {
 // A row's record for the finishing kernel: tiles before its block's first
 // item, that item, the block's tiles, and its place in the block with, in bit 30,
 // whether it is a candidate.
-__device__ __forceinline__ int4 row_record(const CachedSeq& s, int r, int N, int tile0, int item0, int tiles) {
-  return make_int4(tile0, item0, tiles, r % N | (r >= s.n - s.m ? 1 << 30 : 0));
+__device__ __forceinline__ int4 row_record(int tile0, int item0, int tiles, int place, bool candidate) {
+  return make_int4(tile0, item0, tiles, place | (candidate ? 1 << 30 : 0));
 }
 
-// Every CTA counts all sequences' tiles and finds its own beginning; the rows'
-// records are written by one CTA a sequence.  A thread takes `per` neighbouring
+// Every CTA counts all sequences' tiles and finds its own beginning.  The rows'
+// records are written by the CTA that begins their block (write_records), those
+// of a sequence without cached tokens here.  A thread takes `per` neighbouring
 // sequences (one, unless there are more of them than threads: then nothing is
 // read twice).  scan: 2 x 32 ints in shared memory; the caller synchronises
 // before it reads start.
@@ -155,21 +156,12 @@ __device__ __forceinline__ void cut_work(const CachedParams& p, int N, int* scan
       start->items = before_items;
     }
     // a warp's sequences that are this CTA's to write, one after the other
-    unsigned m = __ballot_sync(0xffffffffu, lo < hi && lo % (int)gridDim.x == (int)blockIdx.x && s.n > 0);
+    unsigned m = __ballot_sync(0xffffffffu, lo < hi && lo % (int)gridDim.x == (int)blockIdx.x && s.n > 0 && s.L == 0);
     for (; m; m &= m - 1) {
       const int src = __ffs(m) - 1;
-      CachedSeq q;
-      q.row0 = __shfl_sync(0xffffffffu, s.row0, src);
-      q.n = __shfl_sync(0xffffffffu, s.n, src);
-      q.m = __shfl_sync(0xffffffffu, s.m, src);
-      q.L = __shfl_sync(0xffffffffu, s.L, src);
-      int tile0 = __shfl_sync(0xffffffffu, before, src), item0 = __shfl_sync(0xffffffffu, before_items, src);
-      for (int r0 = 0; r0 < q.n; r0 += N) {
-        const int here = block_tiles(q, r0 / N, N);
-        for (int r = r0 + lane; r < min(q.n, r0 + N); r += 32) p.rows[q.row0 + r] = row_record(q, r, N, tile0, item0, here);
-        tile0 += here * p.H;
-        item0 += p.H;
-      }
+      const int64_t row0 = __shfl_sync(0xffffffffu, s.row0, src);
+      const int n = __shfl_sync(0xffffffffu, s.n, src);
+      for (int r = lane; r < n; r += 32) p.rows[row0 + r] = row_record(0, 0, 0, 0, true);
     }
   } else {
     for (int b = lo; b < hi; ++b) {
@@ -181,15 +173,8 @@ __device__ __forceinline__ void cut_work(const CachedParams& p, int N, int* scan
         start->rem = first - before;
         start->items = before_items;
       }
-      if (b % (int)gridDim.x == (int)blockIdx.x) {
-        int tile0 = before, item0 = before_items;
-        for (int r0 = 0; r0 < s.n; r0 += N) {
-          const int bt = block_tiles(s, r0 / N, N);
-          for (int r = r0; r < min(s.n, r0 + N); ++r) p.rows[s.row0 + r] = row_record(s, r, N, tile0, item0, bt);
-          tile0 += bt * p.H;
-          item0 += p.H;
-        }
-      }
+      if (s.L == 0 && b % (int)gridDim.x == (int)blockIdx.x)
+        for (int r = 0; r < s.n; ++r) p.rows[s.row0 + r] = row_record(0, 0, 0, 0, true);
       before += here;
       before_items += i;
     }
@@ -200,10 +185,12 @@ __device__ __forceinline__ void cut_work(const CachedParams& p, int N, int* scan
 struct Walk {
   CachedSeq s;
   int b, qb, h, tile, tiles, items, left;
+  int line;           // tiles before the piece, all CTAs' work in a row
 
   __device__ __forceinline__ void begin(const CachedParams& p, const Start& st, int N) {
     const int first = (int)blockIdx.x * st.quota;
     left = min(st.quota, st.total - first);
+    line = first;
     b = st.b; items = st.items; qb = 0; h = 0; tile = 0; tiles = 0;
     if (left <= 0) return;
     s = st.s;
@@ -220,7 +207,15 @@ struct Walk {
   // the piece at hand: tiles [tile, tile + take())
   __device__ __forceinline__ int take() const { return min(left, tiles - tile); }
   __device__ __forceinline__ int slot(const CachedParams& p) const { return items + qb * p.H + h + (int)blockIdx.x; }
+  // the records of a block's rows, with its first piece; a warp
+  __device__ __forceinline__ void write_records(const CachedParams& p, int N, int lane) const {
+    if (h > 0 || tile > 0) return;
+    const int r0 = qb * N, rows = min(N, s.n - r0);
+    for (int r = lane; r < rows; r += 32)
+      p.rows[s.row0 + r0 + r] = row_record(line, items + qb * p.H, tiles, r, r0 + r >= s.n - s.m);
+  }
   __device__ __forceinline__ void next(const CachedParams& p, int N) {
+    line += take();
     left -= take();
     tile = 0;
     if (left <= 0 || ++h < p.H) return;

@@ -243,6 +243,7 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
       else if (lane == 0) pieces[at].valid = 0;
       if (lane == 0) mbar_arrive(piece_full(at));
       if (!some) break;
+      w.write_records(p, kRows, lane);
       w.next(p, kRows);
     }
     return;

@@ -243,6 +243,7 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
       }
       __syncwarp();
       ++it;
+      w.write_records(p, N, lane);
       // the block table's entries, 32 at a time: lane i holds entry e0 + i
       const int32_t* row = p.table + (int64_t)b * p.max_pages;
       const int npages = (s.L + p.page_size - 1) / p.page_size;
