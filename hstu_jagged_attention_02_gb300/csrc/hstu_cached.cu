@@ -59,13 +59,14 @@ __global__ void __launch_bounds__(kWarps == 1 ? kFinThreads : 32 * kWarps) finis
     if (on && p.u && p.y) u[i] = fetch4(p.u + row + i * 128);
   }
   // the pieces of features f .. f + 3: their number, and the first one's sum
-  const float* rows = p.part + (int64_t)(rec.w & 0x3fffffff) * D;
+  const float* rows = p.part + (int64_t)(rec.w & 0xffff) * D;
+  const int last = (rec.w >> 16) & 0xff;
   auto pieces = [&](int f, const float*& src) -> int {
     const int h = f / D;
     if (f >= F || rec.z <= 0) return 0;
     const int at = rec.x + h * rec.z, c0 = at / quota;
     src = rows + (int64_t)(rec.y + h + c0) * N * D + f % D;
-    return (at + rec.z - 1) / quota - c0 + 1;
+    return (at + rec.z - last) / quota - c0 + 1;
   };
   const int64_t next = (int64_t)N * D;    // floats from a piece's sum to the next one's
   float o[NV][4];
@@ -187,10 +188,10 @@ hstu_status_t check_cached(const hstu_attn_desc* d, const hstu_cache_desc* c, in
   if (d->H != c->H || d->d_qk != c->d) return HSTU_ERR_INVALID_ARG;
   if (d->flags != 0) return HSTU_ERR_INVALID_ARG;
   if (d->total_tokens > ((int64_t)1 << 30)) return HSTU_ERR_UNSUPPORTED;   // one CTA a row finishes
-  // tiles of all items are counted in 32 bits
+  // the tiles' costs of all items are counted in 32 bits
   const int N = cached_block_rows(max_rows);
   const double items = ((double)d->total_tokens / N + d->B) * d->H;
-  if (items * (d->max_seq_len / (double)kCachedTile + 1) > 2e9) return HSTU_ERR_UNSUPPORTED;
+  if (items * (d->max_seq_len / (double)kCachedTile + 1) * kNearCost > 2e9) return HSTU_ERR_UNSUPPORTED;
   if (d->dtype != HSTU_BF16 || d->out_dtype != HSTU_BF16 || d->dropout_p > 0.f) return HSTU_ERR_UNSUPPORTED;
   return HSTU_OK;
 }

@@ -63,33 +63,57 @@ __device__ __forceinline__ bool load_seq(const CachedParams& p, int b, CachedSeq
          (int64_t)s.L + s.m <= p.max_n && s.L <= (int64_t)p.max_pages * p.page_size;
 }
 
-// Tiles of block qb of N rows.
-__device__ __forceinline__ int block_tiles(const CachedSeq& s, int qb, int N) {
-  const int last = min(s.n, (qb + 1) * N) - 1, hist = s.n - s.m;
+// What a tile costs, by the ways the tensor-memory kernel scores it: near
+// tiles, where a block's rows differ in position bucket or mask, take 5.0 us
+// with 128 rows, the others 1.9.  Where a batch has near tiles the work is cut
+// by these costs, else by tiles.
+constexpr int kFarCost = 2, kNearCost = 5;
+
+// Tiles of a block of rows: far ones, then near ones.
+struct BlockTiles {
+  int far, near;
+  __device__ __forceinline__ int all() const { return far + near; }
+  __device__ __forceinline__ int cost(bool weighted) const { return weighted ? kFarCost * far + kNearCost * near : far + near; }
+  // cost of the tiles before tile t, and the first tile with at least `c` before it
+  __device__ __forceinline__ int before(int t, bool weighted) const {
+    return weighted ? kFarCost * min(t, far) + kNearCost * max(t - far, 0) : t;
+  }
+  __device__ __forceinline__ int tile_at(int c, bool weighted) const {
+    if (!weighted) return c;
+    return c <= kFarCost * far ? (c + kFarCost - 1) / kFarCost : far + (c - kFarCost * far + kNearCost - 1) / kNearCost;
+  }
+};
+__device__ __forceinline__ BlockTiles block_tiles(const CachedParams& p, const CachedSeq& s, int qb, int N) {
+  const int first = qb * N, last = min(s.n, first + N) - 1, hist = s.n - s.m;
   const int seen = last >= hist ? s.L : s.L - hist + last + 1;
-  return (seen + kCachedTile - 1) / kCachedTile;
+  const int tiles = (seen + kCachedTile - 1) / kCachedTile;
+  // blocks of several rows, history rows among them: tiles within the position buckets' reach of the first row
+  const int reach = p.rab_pos ? p.P : 1;
+  const int far = N > 8 && first < hist && last > first ? min(max(s.L - hist + first - reach + 2, 0) / kCachedTile, tiles) : tiles;
+  return {far, tiles - far};
 }
 
 // Where a CTA's part of the work begins.
 struct Start {
   CachedSeq s;        // the sequence it begins in
-  int b, rem;         // sequence, and tiles of it that belong to CTAs before
+  int b, rem;         // its number, and the cost of its tiles that belong to CTAs before
   int items;          // items before the sequence
-  int total, quota;   // tiles in all (0 where the batch is refused), tiles a CTA
+  int total, quota;   // cost in all (0 where the batch is refused), cost a CTA
+  int weighted;       // by tiles' costs, or by tiles
 };
 
-// A row's record for the finishing kernel: tiles before its block's first
-// item, that item, the block's tiles, and its place in the block with, in bit 30,
-// whether it is a candidate.
-__device__ __forceinline__ int4 row_record(int tile0, int item0, int tiles, int place, bool candidate) {
-  return make_int4(tile0, item0, tiles, place | (candidate ? 1 << 30 : 0));
+// A row's record for the finishing kernel: the cost of the tiles before its
+// block's first item, that item, an item's cost, and its place in the block with,
+// from bit 16 on, the last tile's cost and, in bit 30, whether it is a candidate.
+__device__ __forceinline__ int4 row_record(int line, int item0, int cost, int place, int last, bool candidate) {
+  return make_int4(line, item0, cost, place | (last << 16) | (candidate ? 1 << 30 : 0));
 }
 
 // Every CTA counts all sequences' tiles and finds its own beginning.  The rows'
 // records are written by the CTA that begins their block (write_records), those
 // of a sequence without cached tokens here.  A thread takes `per` neighbouring
 // sequences (one, unless there are more of them than threads: then nothing is
-// read twice).  scan: 2 x 32 ints in shared memory; the caller synchronises
+// read twice).  scan: 3 x 32 ints in shared memory; the caller synchronises
 // before it reads start.
 template <int THREADS>
 __device__ __forceinline__ void cut_work(const CachedParams& p, int N, int* scan, Start* start) {
@@ -99,61 +123,84 @@ __device__ __forceinline__ void cut_work(const CachedParams& p, int N, int* scan
   const int per = (p.B + THREADS - 1) / THREADS;
   const int lo = min((int)threadIdx.x * per, p.B), hi = min(lo + per, p.B);
   bool bad = threadIdx.x == THREADS - 1 && (p.off[0] != 0 || p.off[p.B] > p.T);
-  int tiles = 0, items = 0;
   CachedSeq s{};
-  auto count = [&](int b, int& t, int& i) -> bool {
+  // far and near tiles of all heads, items
+  auto count = [&](int b, int (&n)[3]) -> bool {
     if (!load_seq(p, b, s)) return false;
     const int blocks = (s.n + N - 1) / N;
-    t = 0;
-    for (int qb = 0; qb < blocks; ++qb) t += block_tiles(s, qb, N);
-    t *= p.H;
-    i = blocks * p.H;
+    n[0] = n[1] = 0;
+    for (int qb = 0; qb < blocks; ++qb) {
+      const BlockTiles t = block_tiles(p, s, qb, N);
+      n[0] += t.far;
+      n[1] += t.near;
+    }
+    n[0] *= p.H;
+    n[1] *= p.H;
+    n[2] = blocks * p.H;
     return true;
   };
+  int own[3] = {};
   for (int b = lo; b < hi; ++b) {
-    int t, i;
-    if (!count(b, t, i)) {
+    int n[3];
+    if (!count(b, n)) {
       bad = true;
       set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, b);
       break;
     }
-    tiles += t;
-    items += i;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) own[i] += n[i];
   }
   if (bad) set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, -1);
-  auto scan_warp = [&](int& t, int& it) {
+  auto scan_warp = [&](int (&x)[3]) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, t, o), c = __shfl_up_sync(0xffffffffu, it, o);
-      if (lane >= o) { t += a; it += c; }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int a = __shfl_up_sync(0xffffffffu, x[i], o);
+        if (lane >= o) x[i] += a;
+      }
     }
   };
-  int t = tiles, it = items;
-  scan_warp(t, it);
-  if (lane == 31) { scan[warp] = t; scan[32 + warp] = it; }
+  int before[3] = {own[0], own[1], own[2]};
+  scan_warp(before);
+  if (lane == 31) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) scan[32 * i + warp] = before[i];
+  }
   const int any_bad = __syncthreads_or(bad);
   // every warp adds the warps' sums up for itself
-  int wt = lane < WARPS ? scan[lane] : 0, wi = lane < WARPS ? scan[32 + lane] : 0;
-  scan_warp(wt, wi);
-  const int total = any_bad ? 0 : __shfl_sync(0xffffffffu, wt, 31);
-  int before = t - tiles, before_items = it - items;
-  const int pt = __shfl_sync(0xffffffffu, wt, max(warp - 1, 0)), pi = __shfl_sync(0xffffffffu, wi, max(warp - 1, 0));
-  if (warp > 0) { before += pt; before_items += pi; }
-  const int quota = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+  int all[3], sum[2];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) all[i] = lane < WARPS ? scan[32 * i + lane] : 0;
+  scan_warp(all);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) sum[i] = __shfl_sync(0xffffffffu, all[i], 31);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int others = __shfl_sync(0xffffffffu, all[i], max(warp - 1, 0));
+    before[i] += (warp > 0 ? others : 0) - own[i];
+  }
+  const bool weighted = sum[1] > 0;
+  auto cost = [&](const int (&n)[3]) { return BlockTiles{n[0], n[1]}.cost(weighted); };
+  const int total = any_bad ? 0 : BlockTiles{sum[0], sum[1]}.cost(weighted);
+  // a CTA's share holds a tile's beginning: no CTA between an item's first and last goes without a tile of it
+  const int quota = max((total + (int)gridDim.x - 1) / (int)gridDim.x, weighted ? kNearCost : 1);
   const int first = (int)blockIdx.x * quota;
   if (threadIdx.x == 0) {
     start->total = total;
     start->quota = quota;
+    start->weighted = weighted;
     if (blockIdx.x == 0) p.hdr[WS_CA_QUOTA] = any_bad ? -1 : quota;
   }
   if (any_bad) return;
-  const bool mine = first < total && before <= first && first < before + tiles;
+  int at = cost(before);
+  const bool mine = first < total && at <= first && first < at + cost(own);
   if (per == 1) {
     if (mine) {
       start->s = s;
       start->b = lo;
-      start->rem = first - before;
-      start->items = before_items;
+      start->rem = first - at;
+      start->items = before[2];
     }
     // a warp's sequences that are this CTA's to write, one after the other
     unsigned m = __ballot_sync(0xffffffffu, lo < hi && lo % (int)gridDim.x == (int)blockIdx.x && s.n > 0 && s.L == 0);
@@ -161,79 +208,99 @@ __device__ __forceinline__ void cut_work(const CachedParams& p, int N, int* scan
       const int src = __ffs(m) - 1;
       const int64_t row0 = __shfl_sync(0xffffffffu, s.row0, src);
       const int n = __shfl_sync(0xffffffffu, s.n, src);
-      for (int r = lane; r < n; r += 32) p.rows[row0 + r] = row_record(0, 0, 0, 0, true);
+      for (int r = lane; r < n; r += 32) p.rows[row0 + r] = row_record(0, 0, 0, 0, 0, true);
     }
   } else {
+    int items = before[2];
     for (int b = lo; b < hi; ++b) {
-      int here, i;
-      count(b, here, i);
-      if (mine && first >= before && first < before + here) {
+      int n[3];
+      count(b, n);
+      if (mine && first >= at && first < at + cost(n)) {
         start->s = s;
         start->b = b;
-        start->rem = first - before;
-        start->items = before_items;
+        start->rem = first - at;
+        start->items = items;
       }
       if (s.L == 0 && b % (int)gridDim.x == (int)blockIdx.x)
-        for (int r = 0; r < s.n; ++r) p.rows[s.row0 + r] = row_record(0, 0, 0, 0, true);
-      before += here;
-      before_items += i;
+        for (int r = 0; r < s.n; ++r) p.rows[s.row0 + r] = row_record(0, 0, 0, 0, 0, true);
+      at += cost(n);
+      items += n[2];
     }
   }
 }
 
-// A CTA's walk over its pieces: every thread that calls it sees the same.
+// A CTA's walk over its pieces: every thread that calls it sees the same.  All
+// items' tiles in a line, each as long as it costs: a CTA takes the tiles that
+// begin in its part of the line.
 struct Walk {
   CachedSeq s;
-  int b, qb, h, tile, tiles, items, left;
-  int line;           // tiles before the piece, all CTAs' work in a row
+  BlockTiles tiles;
+  int b, qb, h, tile, items;
+  int line, end;      // where the item begins in the line, and the CTA's part ends
+  bool more, weighted;
 
   __device__ __forceinline__ void begin(const CachedParams& p, const Start& st, int N) {
     const int first = (int)blockIdx.x * st.quota;
-    left = min(st.quota, st.total - first);
-    line = first;
-    b = st.b; items = st.items; qb = 0; h = 0; tile = 0; tiles = 0;
-    if (left <= 0) return;
+    weighted = st.weighted;
+    end = min(first + st.quota, st.total);
+    more = first < st.total;
+    b = st.b; items = st.items; qb = 0; h = 0; tile = 0; line = first; tiles = {0, 0};
+    if (!more) return;
     s = st.s;
     int rem = st.rem;
-    tiles = block_tiles(s, qb, N);
-    while (rem >= tiles * p.H) {
-      rem -= tiles * p.H;
+    tiles = block_tiles(p, s, qb, N);
+    while (rem >= tiles.cost(weighted) * p.H) {
+      rem -= tiles.cost(weighted) * p.H;
       ++qb;
-      tiles = block_tiles(s, qb, N);
+      tiles = block_tiles(p, s, qb, N);
     }
-    h = rem / tiles;
-    tile = rem % tiles;
+    const int cost = tiles.cost(weighted);
+    h = rem / cost;
+    rem -= h * cost;
+    line = first - rem;
+    tile = tiles.tile_at(rem, weighted);
+    if (tile >= tiles.all()) next_item(p, N);   // the item's last tile began before
   }
   // the piece at hand: tiles [tile, tile + take())
-  __device__ __forceinline__ int take() const { return min(left, tiles - tile); }
+  __device__ __forceinline__ int take() const {
+    const int room = end - line;
+    return (room >= tiles.cost(weighted) ? tiles.all() : min(tiles.tile_at(room, weighted), tiles.all())) - tile;
+  }
   __device__ __forceinline__ int slot(const CachedParams& p) const { return items + qb * p.H + h + (int)blockIdx.x; }
   // the records of a block's rows, with its first piece; a warp
   __device__ __forceinline__ void write_records(const CachedParams& p, int N, int lane) const {
     if (h > 0 || tile > 0) return;
-    const int r0 = qb * N, rows = min(N, s.n - r0);
+    const int r0 = qb * N, rows = min(N, s.n - r0), cost = tiles.cost(weighted);
+    const int last = cost - tiles.before(tiles.all() - 1, weighted);
     for (int r = lane; r < rows; r += 32)
-      p.rows[s.row0 + r0 + r] = row_record(line, items + qb * p.H, tiles, r, r0 + r >= s.n - s.m);
+      p.rows[s.row0 + r0 + r] = row_record(line, items + qb * p.H, cost, r, last, r0 + r >= s.n - s.m);
   }
   __device__ __forceinline__ void next(const CachedParams& p, int N) {
-    line += take();
-    left -= take();
+    if (tile + take() < tiles.all()) more = false;
+    else next_item(p, N);
+  }
+
+ private:
+  __device__ __forceinline__ void next_item(const CachedParams& p, int N) {
+    line += tiles.cost(weighted);
     tile = 0;
-    if (left <= 0 || ++h < p.H) return;
+    more = line < end;
+    if (!more || ++h < p.H) return;
     h = 0;
     do {
       ++qb;
       if (qb * N >= s.n) {
         items += ((s.n + N - 1) / N) * p.H;
         qb = 0;
-        s.n = 0;                 // some later sequence has tiles: left > 0
+        s.n = 0;                 // some later sequence has tiles: the line goes on
         while (s.n == 0 && ++b < p.B) load_seq(p, b, s);
         if (s.n == 0) {
-          left = 0;
+          more = false;
           return;
         }
       }
-      tiles = block_tiles(s, qb, N);
-    } while (tiles == 0);
+      tiles = block_tiles(p, s, qb, N);
+    } while (tiles.all() == 0);
   }
 };
 

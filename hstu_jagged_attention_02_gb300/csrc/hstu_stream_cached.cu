@@ -197,7 +197,7 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
   using C = SCfg<D>;
   constexpr int MT = D / 16;             // 16-feature tiles of O
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int scan[64];
+  __shared__ int scan[96];
   __shared__ Start start;
   __shared__ int abort_flag, left_sums[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -238,7 +238,7 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
       if (lane == 0) ok = mbar_wait(piece_empty(at), ((np / C::PIECES) & 1) ^ 1, wd, 91);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
-      const bool some = w.left > 0;
+      const bool some = w.more;
       if (some) write_piece<D>(p, w, pieces[at]);
       else if (lane == 0) pieces[at].valid = 0;
       if (lane == 0) mbar_arrive(piece_full(at));

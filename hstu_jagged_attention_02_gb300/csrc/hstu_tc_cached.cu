@@ -86,6 +86,7 @@ struct Cfg {
   static constexpr int BAR_OFF = SLOT_OFF + ITEMS * 96;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr int BYTES = MISC_OFF + 512;
+  static_assert(16 + sizeof(Start) <= 128, "the start's place");
   static constexpr uint32_t TMEM_COLS = 4 * N;             // S 0, 1 and O 0, 1
   static_assert(BYTES + 1024 <= (int)kMaxSmemPerCta, "one CTA's shared memory");
 };
@@ -175,7 +176,7 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base + L::MISC_OFF + 4);
   Start* start = reinterpret_cast<Start*>(base + L::MISC_OFF + 16);
-  int* scan = reinterpret_cast<int*>(base + L::MISC_OFF + 64);   // [2][32] warp sums
+  int* scan = reinterpret_cast<int*>(base + L::MISC_OFF + 128);   // [3][32] warp sums
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -222,7 +223,7 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
     const PageLayout lay(p.page_size, D);
     Walk w;
     w.begin(p, *start, N);
-    while (ok && w.left > 0) {
+    while (ok && w.more) {
       const int take = w.take(), tile = w.tile, b = w.b, h = w.h;
       const CachedSeq s = w.s;
       const uint32_t sl = it % L::ITEMS;
