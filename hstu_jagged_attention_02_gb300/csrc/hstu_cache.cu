@@ -1,14 +1,22 @@
 // Appending to and reading from the paged 4-bit cache (hstu_cache_append,
 // hstu_cache_read).
 //
-// Append: bound by the BF16 rows it reads (2 d bytes in, 9 d / 16 out), if the
-// instructions are few.  d / 8 lanes hold a row (hstu_rows.cuh: both features
+// Append: the BF16 rows it reads and the packed ones it writes (2 d bytes in,
+// 9 d / 16 out) would bound it, but coding a feature takes more instructions than
+// that leaves room for: 161,000 tokens of four heads of 128, normed and rotated,
+// take 215 us (2.0 TB/s; 63 us at the rate of a copy), 1,050 warp instructions a
+// token at 2.6 a cycle.  Keys that go in as they are take 154 us; more loads in
+// flight (through shared memory) or more warps (80 registers) took longer.  The
+// read is bound by what it writes: 74 us, 5.8 TB/s.
+//
+// d / 8 lanes hold a row (hstu_rows.cuh: both features
 // of a pair in one lane), a warp takes a token at a time, its keys' and values'
 // passes of 256 features side by side, all loads first.  A warp walks
 // tokens_per_warp neighbouring tokens, so that the sequence and the page are
 // looked up once for them (in a small batch each warp has one token: there the
-// chain of lookups is the time).  A group's maximum goes over the 2 or 4 lanes
-// that share it.
+// chain of lookups is the time): one token a warp 64 tokens 9.9 us (single call),
+// 161,000 tokens 252, four 18.1 and 219; reading 6.8 and 124, 8.8 and 75.  A
+// group's maximum goes over the 2 or 4 lanes that share it.
 //
 // Roundings are decided as on real numbers.  A value x that is exact in FP32
 // (a BF16 input) meets a border only exactly: its quotient by the scale (4
@@ -326,7 +334,8 @@ __device__ __noinline__ uint2 key_two(const AppendParams& p, int how, int f0, in
     } else {
       const Two m = a.h < 0.f ? -a : a;
       const uint32_t low = __float_as_uint(m.l);
-      const unsigned long long key = ((unsigned long long)__float_as_uint(fabsf(m.h)) << 32) | (low ^ ((int)low < 0 ? 0xffffffffu : 0x80000000u));
+      const unsigned long long key = ((unsigned long long)__float_as_uint(fabsf(m.h)) << 32) |
+                                     (low ^ ((int)low < 0 ? 0xffffffffu : 0x80000000u));
       top = key > top ? key : top;
     }
   };
@@ -595,7 +604,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// several tokens a warp once every warp the GPU holds has one
+// several tokens a warp once every warp the GPU holds has one (measured at the top)
 int tokens_per_warp(int64_t T) { return T > 152 * 48 ? kManyTokens : 1; }
 
 int page_log(int page_size) { return page_size == 32 ? 5 : (page_size == 64 ? 6 : 7); }

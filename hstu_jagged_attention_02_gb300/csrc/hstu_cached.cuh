@@ -3,16 +3,17 @@
 //
 // A sequence's n rows form blocks of N; a block's keys are the 128-token
 // tiles [0, tiles) of its cache, up to the last position that one of its rows
-// sees.  An item is a (block, head).  All items' tiles in a row, ordered by
-// sequence, block, head and tile, are cut into equal parts, one a CTA; a CTA's
-// part of an item is a piece, and leaves one FP32 sum [N][d] in the workspace
-// at slot item + CTA (no two pieces share one: every further piece crosses
-// the border of an item, of a CTA, or both).
+// sees.  An item is a (block, head).  All items' tiles in a line, ordered by
+// sequence, block, head and tile, are cut into parts of equal cost, one a CTA; a
+// CTA's part of an item is a piece, and leaves one FP32 sum [N][d] in the
+// workspace at slot item + CTA (no two pieces share one: every further piece
+// crosses the border of an item, of a CTA, or both).  So a long cache with one
+// row fills the machine as well as many users do, and the sums are added in the
+// same order every time.
 #pragma once
 
 #include "hstu_fp4.cuh"
 #include "hstu_internal.h"
-#include "hstu_seq_search.cuh"
 
 namespace hstu {
 
@@ -45,7 +46,7 @@ struct CachedParams {
 };
 
 // header words of the cached attention's workspace (beside WS_ERR)
-enum : int { WS_CA_QUOTA = 16 };   // tiles a CTA, -1 where the batch was refused
+enum : int { WS_CA_QUOTA = 16 };   // cost a CTA, -1 where the batch was refused
 
 struct CachedSeq {
   int64_t row0;   // first row
@@ -66,7 +67,10 @@ __device__ __forceinline__ bool load_seq(const CachedParams& p, int b, CachedSeq
 // What a tile costs, by the ways the tensor-memory kernel scores it: near
 // tiles, where a block's rows differ in position bucket or mask, take 5.0 us
 // with 128 rows, the others 1.9.  Where a batch has near tiles the work is cut
-// by these costs, else by tiles.
+// by these costs, else by tiles: first passes of 900 to 2,100 rows by tiles
+// 65.8 us (the CTAs at the sequences' beginnings end after 51 us, the others after
+// 30), by these costs 52.6.  Single calls: costs of 2 and 5 55.9 us, 1 and 2
+// 59.0, 2 and 3 65.2.
 constexpr int kFarCost = 2, kNearCost = 5;
 
 // Tiles of a block of rows: far ones, then near ones.

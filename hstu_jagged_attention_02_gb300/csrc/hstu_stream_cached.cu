@@ -33,10 +33,10 @@
 // What bounds it: instructions, 790 for 32 tokens of 128 features, at 1.9 a
 // cycle with the four warps a sub-partition that the registers allow, and 4 us
 // of lookups before the first product.  32 users with one row each over some
-// 162,000 cached tokens, four heads of 128: 35.0 us, 2.7 TB/s of cache (of 6.8
-// measured for a copy).  Steps of 16 tokens: 36.6 us (the lookups and the
-// copies' addresses twice as often), but 9.1 against 9.6 us for a single row over
-// 300 tokens.
+// 162,000 cached tokens, four heads of 128: 32.9 us with the finishing kernel,
+// 2.9 TB/s of cache (of 6.8 measured for a copy).  Steps of 16 tokens took 1.6 us
+// more (the lookups and the copies' addresses twice as often), but 0.5 us less
+// for a single row over 300 tokens, which takes 9.2.
 #include "hstu_cached.cuh"
 #include "tc_ptx.cuh"
 
@@ -402,7 +402,8 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float b = __shfl_sync(0xffffffffu, bl, token_of(g) + 8 * i);
-              pr[i] = silu_pair(__ffma2_rn(make_float2(c[i >> 1][2 * (i & 1)], c[i >> 1][2 * (i & 1) + 1]), k2, make_float2(b, b)));
+              pr[i] = silu_pair(__ffma2_rn(make_float2(c[i >> 1][2 * (i & 1)], c[i >> 1][2 * (i & 1) + 1]), k2,
+                                           make_float2(b, b)));
             }
           } else {
 #pragma unroll

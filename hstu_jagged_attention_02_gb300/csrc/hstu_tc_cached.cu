@@ -33,11 +33,13 @@
 // and back, which two buffers share: 3,300 cycles a tile of 128 tokens x 128
 // rows, where the tensor core itself needs 1,000.  A third buffer does not fit
 // beside the packed tiles.  Scores by 16 warps on one tile or by two groups of
-// 8 on a tile each take the same time with 128 rows (86 us for 32 users x 128
-// candidates over some 158,000 cached tokens, four heads of 128), and with fewer
-// rows or the near tokens' lookups the 16 are ahead (27 against 30 us, 75
-// against 78 us).  One reciprocal for two scores, or Newton steps in its place,
-// bought nothing: without any SiLU at all the kernel took 9% less.
+// 8 on a tile each take the same time with 128 rows (32 users x 128 candidates
+// over some 158,000 cached tokens, four heads of 128: 81 us with the finishing
+// kernel, 510 TFLOP/s), and with fewer rows or the near tokens' lookups the 16 are
+// ahead (27 against 30 us, 75 against 78 us, before other steps).  One reciprocal
+// for two scores, or Newton steps in its place, bought nothing: without any SiLU
+// at all the kernel took 9% less.  Gaps in 32 bits where they fit took first
+// passes from 74 to 65 us.
 #include "hstu_cached.cuh"
 #include "tc_ptx.cuh"
 
@@ -468,7 +470,8 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
         ++it;
         for (int t = 0; t < nt; ++t, ++tk) {
           const uint32_t st = tk & 1;
-          ok = wait(mbar_wait(bar(L::VREADY + st), (tk >> 1) & 1, wd, 74) && mbar_wait(bar(L::PREADY + st), (tk >> 1) & 1, wd, 75));
+          ok = wait(mbar_wait(bar(L::VREADY + st), (tk >> 1) & 1, wd, 74) &&
+                    mbar_wait(bar(L::PREADY + st), (tk >> 1) & 1, wd, 75));
           if (!ok) break;
           fence_after_sync();
           // with 64 features the upper half of M reads the same features again; its rows are not used

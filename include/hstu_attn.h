@@ -587,7 +587,9 @@ hstu_status_t hstu_cache_read(const hstu_cache_desc* cache, const hstu_cache_rea
  *
  * Precision: K, V and q enter the tensor cores exactly; 16 SiLU(z) is rounded
  * once to FP16 (so scores of 4094 and more overflow to infinity; a bias of
- * minus infinity leaves the pair out); sums, norm and gate are FP32 and o and
+ * minus infinity leaves the pair out, and a NaN value in a token that a history
+ * row does not see yet still reaches it where both lie in one block of rows);
+ * sums, norm and gate are FP32 and o and
  * y are rounded once.  The cache's tiles are dealt evenly to the CTAs and
  * partial sums added in a fixed order: equal inputs give equal bits.
  * ------------------------------------------------------------------------ */
