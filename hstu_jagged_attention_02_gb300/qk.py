@@ -218,6 +218,7 @@ class QKNormRopeFunction(torch.autograd.Function):
         return pr.q_out, pr.k_out
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, q_gain, k_gain, positions, cos, sin, num_tokens = ctx.saved_tensors
         rot_dim, interleaved, norm, eps = ctx.how
@@ -238,7 +239,9 @@ def hstu_qk_norm_rope(q, k, positions=None, cos=None, sin=None, *, q_gain=None, 
     (either may be None): returns (q', k') for hstu_attention.  cos, sin:
     rope_tables; positions: jagged_positions, or any int32 [T] below
     max_position.  num_tokens: one int64 on the device, tokens in use of a
-    padded batch (rows behind it come back as zeros)."""
+    padded batch (rows behind it come back as zeros).  There is no second
+    derivative.  Into a CUDA graph goes QKProblem's forward and backward, rather
+    than autograd's."""
     if rot_dim is None:
         rot_dim = 0 if cos is None else 2 * cos.shape[1]
     return QKNormRopeFunction.apply(q, k, q_gain, k_gain, positions, cos, sin, num_tokens, int(rot_dim), bool(interleaved),

@@ -405,7 +405,8 @@ hstu_status_t hstu_attn_fwd_delta(const hstu_attn_desc* desc, const hstu_attn_de
  * The tables are the caller's ([max_position, rot_dim / 2] FP32 each), and
  * so are the positions: a candidate of the ranking task has the position
  * h_end of its sequence, like in the attention's position buckets.  Sums and
- * products are FP32, each output is rounded once.  Backward, with e = the
+ * products are FP32 (mean(x^2) + eps has to be a normal FP32 number), each output
+ * is rounded once.  Backward, with e = the
  * incoming gradient turned back by the rotation:
  *   dgain_i = sum over tokens and heads of e_i x_i r
  *   dx = r (e gain - x r mean(e gain x r))                  (norm = 0: dx = e)
@@ -589,8 +590,8 @@ hstu_status_t hstu_cache_read(const hstu_cache_desc* cache, const hstu_cache_rea
  * once to FP16 (so scores of 4094 and more overflow to infinity; a bias of
  * minus infinity leaves the pair out, and a NaN value in a token that a history
  * row does not see yet still reaches it where both lie in one block of rows);
- * sums, norm and gate are FP32 and o and
- * y are rounded once.  The cache's tiles are dealt evenly to the CTAs and
+ * sums, norm and gate are FP32 and o and y are rounded once.  The cache's tiles
+ * are dealt to the CTAs by their cost, whatever sequence they belong to, and
  * partial sums added in a fixed order: equal inputs give equal bits.
  * ------------------------------------------------------------------------ */
 typedef struct {

@@ -148,3 +148,12 @@ def test_captured_step_beside_another():
     s.kc, s.vc = _f64(rd.k), _f64(rd.v)
     s.tc = rd.timestamps.cpu().numpy()
     s.check(at)
+
+
+def test_no_second_derivative():
+    from hstu_jagged_attention_02_gb300.qk import hstu_qk_norm_rope
+    q = torch.randn(3, 2, 64, generator=torch.Generator().manual_seed(58)).cuda().requires_grad_()
+    out, _ = hstu_qk_norm_rope(q, None)
+    (g,) = torch.autograd.grad(out.square().sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
