@@ -11,10 +11,11 @@
 // there are, and N follows the rows (32, 64 or 128; up to 8 rows have a kernel
 // of their own).  A thread of the score step holds one cached token, whose
 // position and time biases are the same for every candidate of a request: one
-// table lookup a tile and thread where the block's rows share the position and
-// time buckets towards the token, as they do for candidates and for tokens far
-// back; a time lookup a score where only a time bucket's border lies inside the
-// block; otherwise (rows near the tokens) both lookups a score.
+// table lookup a token where the block's rows share the position and time
+// buckets towards it, as they do for candidates and for tokens far back (the
+// decoding warps make it, while they wait for a tile buffer); a time lookup a
+// score where only a time bucket's border lies inside the block; otherwise (rows
+// near the tokens) both lookups a score.
 //
 // The pages reach shared memory as they are (cp.async.bulk, 9/16 byte a
 // feature) and are decoded there to FP16, where code x scale is exact.  q is
@@ -23,23 +24,24 @@
 // alpha.
 //
 // Roles (27 warps): 0-15 scores (warp w: TMEM lanes 32 (w % 4), columns quarter
-// w / 4 of the tile), 16-23 decoding and q, 24 page copies and the CTA's list of
-// pieces, 25 S products and TMEM, 26 PV products.  Two tile buffers {K, V}; P
+// w / 4 of the tile), 16-23 decoding, q and the tokens' biases, 24 page copies and
+// the CTA's list of pieces, 25 S products and TMEM, 26 PV products.  Two tile buffers {K, V}; P
 // takes K's place once the tile's S is complete.  Work is dealt evenly
 // (hstu_cached.cuh).  Every wait is bounded.
 //
 // What bounds it: a tile buffer's round of decoding K (1,000 cycles), the S
-// product (900), the scores (3,000 with their biases), the PV product (1,300)
-// and back, which two buffers share: 3,300 cycles a tile of 128 tokens x 128
-// rows, where the tensor core itself needs 1,000.  A third buffer does not fit
-// beside the packed tiles.  Scores by 16 warps on one tile or by two groups of
-// 8 on a tile each take the same time with 128 rows (32 users x 128 candidates
-// over some 158,000 cached tokens, four heads of 128: 81 us with the finishing
-// kernel, 510 TFLOP/s), and with fewer rows or the near tokens' lookups the 16 are
-// ahead (27 against 30 us, 75 against 78 us, before other steps).  One reciprocal
-// for two scores, or Newton steps in its place, bought nothing: without any SiLU
-// at all the kernel took 9% less.  Gaps in 32 bits where they fit took first
-// passes from 74 to 65 us.
+// product (1,100), the scores (2,450), the PV product (1,300) and back, which two
+// buffers share: 3,200 cycles a tile of 128 tokens x 128 rows, where the tensor
+// core itself needs 1,000.  A third buffer does not fit beside the packed tiles.
+// 32 users x 128 candidates over some 158,000 cached tokens, four heads of 128:
+// 80 us with the finishing kernel, 520 TFLOP/s.  Scores by 16 warps on one tile or
+// by two groups of 8 on a tile each take the same time with 128 rows; with fewer
+// rows or the near tokens' lookups the 16 were ahead (27 against 30 us, 75 against
+// 78 us, before other steps).  One reciprocal for two scores, or Newton steps in
+// its place, bought nothing: without any SiLU at all the kernel took 9% less.  Gaps
+// in 32 bits where they fit took first passes from 74 to 65 us.  Biases found by
+// the decoding warps instead of every score warp: new rows and candidates of 32
+// users 20.7 -> 19.2 us, 128 candidates 81.4 -> 80.0, first passes 51.6 -> 53.5.
 #include "hstu_cached.cuh"
 #include "tc_ptx.cuh"
 
@@ -64,7 +66,7 @@ struct Cfg {
   static constexpr int P_ROW = N >= 64 ? 128 : N * 2;      // bytes of a row of a P chunk
   static constexpr int QB = N == 128 ? 1 : 2;              // q buffers
   static constexpr int Q_BYTES = N * D * 2;
-  static constexpr int ITEMS = N == 128 ? 2 : 4;           // piece records in flight
+  static constexpr int ITEMS = N == 128 ? 2 : 3;           // piece records in flight
   static constexpr int NR = D == 64 ? 6 : (N >= 64 ? 3 : 4);   // packed tiles in flight
   static constexpr int NT = NR + (N == 32 ? 1 : 2);                        // their times live until the scores are done
   static constexpr int RAW_BYTES = 2 * TILE * (D / 2 + D / 16);   // the tile's pages' blocks, as they are
@@ -78,7 +80,9 @@ struct Cfg {
   static constexpr int QT32_OFF = QT_OFF + ITEMS * N * 8;  // int32 [ITEMS][N], from the earliest row's
   static constexpr int KA_OFF = QT32_OFF + ITEMS * N * 4;    // float [ITEMS][N] score factors
   static constexpr int TB_OFF = KA_OFF + ITEMS * N * 4;    // float [ITEMS][kTimeSlots + 1] time biases, the far position's
-  static constexpr int SLOT_OFF = (TB_OFF + ITEMS * (kTimeSlots + 1) * 4 + 15) / 16 * 16;
+  static constexpr int BIAS_OFF = TB_OFF + ITEMS * (kTimeSlots + 1) * 4;   // float [2][TILE] of a tile's tokens, where rows share them
+  static constexpr int MODE_OFF = BIAS_OFF + 2 * TILE * 4;                 // int [2][4] how 32 tokens are scored
+  static constexpr int SLOT_OFF = (MODE_OFF + 32 + 15) / 16 * 16;
   // barriers
   static constexpr int RAWFULL = 0, RAWEMPTY = RAWFULL + NR, TSFULL = RAWEMPTY + NR, TSEMPTY = TSFULL + NT,
                        ITEMFULL = TSEMPTY + NT, ITEMEMPTY = ITEMFULL + ITEMS, QTFULL = ITEMEMPTY + ITEMS,
@@ -104,6 +108,10 @@ struct __align__(16) Piece {
   int slot;           // of its sum
 };
 static_assert(sizeof(Piece) <= 96, "a slot holds a piece");
+
+// How 32 tokens of a tile are scored: one bias a token for all rows; all tokens exist; gaps of 32 bits; the last
+// position bucket.
+enum : int { kFast = 1, kWhole = 2, kNarrow = 4, kFar = 8 };
 
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
@@ -175,6 +183,8 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
   int32_t* qt32 = reinterpret_cast<int32_t*>(base + L::QT32_OFF);
   float* kA = reinterpret_cast<float*>(base + L::KA_OFF);
   float* tb = reinterpret_cast<float*>(base + L::TB_OFF);
+  float* token_bias = reinterpret_cast<float*>(base + L::BIAS_OFF);
+  int* modes = reinterpret_cast<int*>(base + L::MODE_OFF);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base + L::MISC_OFF + 4);
   Start* start = reinterpret_cast<Start*>(base + L::MISC_OFF + 16);
@@ -387,14 +397,56 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
         }
       }
       const int t0 = pc.tile0, t1 = pc.tile1, len = pc.L;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::ITEMEMPTY + sl));
-      ++it;
+      const float* tbl = tb + sl * (kTimeSlots + 1);
+      if (dw < 4) {      // the first four warps also find the tokens' biases, from the rows' range of times
+        ok = mbar_wait(bar(L::QTFULL + sl), (it / L::ITEMS) & 1, wd, 81);
+        if (!ok) break;
+      }
+      const int64_t tmin = pc.tmin, tmax = pc.tmax;
+      const int pmin = pc.hist > 0 ? pc.pos0 : len, pmax = pc.hist == pc.rows ? pc.pos0 + pc.rows - 1 : len;
+      const float* rp = p.rab_pos ? p.rab_pos + pc.h * p.P : nullptr;
+      const bool one_time = !p.rab_time || tmin == tmax;
       for (int t = t0; t < t1; ++t, ++tk) {
         const uint32_t rs = tk % L::NR, st = tk & 1;
-        ok = mbar_wait(bar(L::RAWFULL + rs), (tk / L::NR) & 1, wd, 67) &&
-             mbar_wait(bar(L::STEMPTY + st), ((tk >> 1) & 1) ^ 1, wd, 68);
+        ok = mbar_wait(bar(L::RAWFULL + rs), (tk / L::NR) & 1, wd, 67);
         if (!ok) break;
+        float bias = 0.f;
+        int mode = 0;
+        if (dw < 4) {    // while the tile buffer is still in use
+          const uint32_t ts = tk % L::NT;
+          const int r = dw * 32 + lane, j = t * TILE + r;
+          int64_t tj = 0;
+          if (timed) {
+            ok = mbar_wait(bar(L::TSFULL + ts), (tk / L::NT) & 1, wd, 79);
+            if (!ok) break;
+            tj = *reinterpret_cast<const int64_t*>(base + L::TS_OFF + ts * (TILE * 8) + r * 8);
+          }
+          // one bias for all of the block's rows?
+          bool same = j <= pmin;
+          bias = tbl[kTimeSlots];                            // far tokens share the last position bucket
+          const bool far = pmin - (t * TILE + dw * 32 + 31) >= p.P - 1;
+          if (!far && rp) {
+            const int a = min(max(pmin - j, 0), p.P - 1);
+            same = same && a == min(max(pmax - j, 0), p.P - 1);
+            bias = scaled_bias(__ldg(rp + a));
+          }
+          const int a = bit_length(tmin, tj);
+          bias += tbl[a];
+          if (!one_time) same = same && min(a, p.Tb - 1) == min(bit_length(tmax, tj), p.Tb - 1) && (tj <= tmin || tj >= tmax);
+          const int64_t rel = tj - tmin;
+          const bool fast = __all_sync(0xffffffffu, same || j >= len);
+          const bool whole = __all_sync(0xffffffffu, j < len);
+          // else gaps of 32 bits where they fit
+          const bool narrow = __all_sync(0xffffffffu, j >= len || (rel > -kNarrowTsSpan && rel < kNarrowTsSpan)) &&
+                              tmax - tmin < kNarrowTsSpan;
+          mode = (fast ? kFast : 0) | (whole ? kWhole : 0) | (narrow ? kNarrow : 0) | (far ? kFar : 0);
+        }
+        ok = mbar_wait(bar(L::STEMPTY + st), ((tk >> 1) & 1) ^ 1, wd, 68);
+        if (!ok) break;
+        if (dw < 4) {
+          token_bias[st * TILE + dw * 32 + lane] = bias;
+          if (lane == 0) modes[st * 4 + dw] = mode;
+        }
         const uint8_t* raw = base + L::RAW_OFF + rs * L::RAW_BYTES;
         const int rows = len - t * TILE;
         plan.decode(raw, base + L::KP_OFF + st * L::KP_BYTES, rows);
@@ -409,6 +461,10 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
           mbar_arrive(bar(L::RAWEMPTY + rs));
         }
       }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::ITEMEMPTY + sl));
+      ++it;
     }
   } else if (warp == kSWarp) {
     // ---------------------------------------------------------- S^T = K Q^T
@@ -536,44 +592,27 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
       ok = mbar_wait(bar(L::QTFULL + sl), (it / L::ITEMS) & 1, wd, 78);
       if (!ok) break;
       const int len = pc.L, pos0 = pc.pos0, hist = pc.hist, rows = pc.rows, t0 = pc.tile0, t1 = pc.tile1, slot = pc.slot;
-      const int64_t tmin = pc.tmin, tmax = pc.tmax;
-      const int pmin = hist > 0 ? pos0 : len, pmax = hist == rows ? pos0 + rows - 1 : len;
+      const int64_t tmin = pc.tmin;
       const float* rp = p.rab_pos ? p.rab_pos + pc.h * p.P : nullptr;
       const float* tbl = tb + sl * (kTimeSlots + 1);
-      const bool one_time = !p.rab_time || tmin == tmax;
       const float* ka = kA + sl * N + col0;
       const int64_t* tq = qt + sl * N + col0;
       const int32_t* tq32 = qt32 + sl * N + col0;
       for (int t = t0; t < t1; ++t, ++tk) {
         const uint32_t st = tk & 1, ts = tk % L::NT;
         const int j = t * TILE + r;
+        ok = mbar_wait(bar(L::KREADY + st), (tk >> 1) & 1, wd, 82);   // the tokens' biases come with K
+        if (!ok) break;
+        const int mode = modes[st * 4 + wq];
+        const float bias = token_bias[st * TILE + r];
+        const bool fast = mode & kFast, whole = mode & kWhole, narrow = mode & kNarrow, far = mode & kFar;
         int64_t tj = 0;
-        if (timed) {
-          ok = mbar_wait(bar(L::TSFULL + ts), (tk / L::NT) & 1, wd, 79);
+        if (!fast && timed) {
+          ok = mbar_wait(bar(L::TSFULL + ts), (tk / L::NT) & 1, wd, 83);
           if (!ok) break;
           tj = *reinterpret_cast<const int64_t*>(base + L::TS_OFF + ts * (TILE * 8) + r * 8);
         }
-        // one bias for all of the block's rows?
-        bool same = j <= pmin;
-        float bias = tbl[kTimeSlots];                      // far tokens share the last position bucket
-        if (pmin - (t * TILE + wq * 32 + 31) < p.P - 1 && rp) {
-          const int a = min(max(pmin - j, 0), p.P - 1);
-          same = same && a == min(max(pmax - j, 0), p.P - 1);
-          bias = scaled_bias(__ldg(rp + a));
-        }
-        {
-          const int a = bit_length(tmin, tj);
-          bias += tbl[a];
-          if (!one_time) same = same && min(a, p.Tb - 1) == min(bit_length(tmax, tj), p.Tb - 1) && (tj <= tmin || tj >= tmax);
-        }
-        same = same || j >= len;
-        const bool fast = __all_sync(0xffffffffu, same);
-        const bool whole = __all_sync(0xffffffffu, j < len);
-        // else gaps of 32 bits where they fit; far: only the time buckets may differ
-        const int64_t rel = tj - tmin;
-        const bool narrow = !fast && __all_sync(0xffffffffu, j >= len || (rel > -kNarrowTsSpan && rel < kNarrowTsSpan)) &&
-                            tmax - tmin < kNarrowTsSpan;
-        const bool far = pmin - (t * TILE + wq * 32 + 31) >= p.P - 1;
+        const int rel32 = (int)(tj - tmin);      // used where it fits
         ok = mbar_wait(bar(L::SFULL + st), (tk >> 1) & 1, wd, 80);
         if (!ok) break;
         fence_after_sync();
@@ -618,7 +657,6 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
             tmem_wait_ld();
             uint32_t h2[CH / 2];
             if (narrow && far) {
-              const int rel32 = (int)rel;
               const float fb = tbl[kTimeSlots];
 #pragma unroll
               for (int c = 0; c < CH; c += 4) {
@@ -632,7 +670,7 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
                                                      make_float2(k4.z, k4.w), b23));
               }
             } else if (narrow) {
-              const int rel32 = (int)rel, base_gap = pos0 - j, cand_gap = len - j;   // a row's distance, less its column
+              const int base_gap = pos0 - j, cand_gap = len - j;   // a row's distance, less its column
 #pragma unroll
               for (int c = 0; c < CH; c += 4) {
                 const float4 k4 = *reinterpret_cast<const float4*>(ka + c0 + c);
