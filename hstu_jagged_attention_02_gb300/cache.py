@@ -81,7 +81,9 @@ class _Call:
 class AppendProblem(_Call):
     """k, v [T, H, d] BF16 of the batch's new tokens on their way into the
     cache: run() writes them at the last positions of each sequence
-    (cache_lens counts them already), keys through norm and rotation."""
+    (cache_lens counts them already), keys through norm and rotation.  k, v are
+    read in place where their features are contiguous and heads and tokens lie
+    multiples of 16 bytes apart, else copied once, here."""
 
     def __init__(self, cache: PagedCache, k, v, seq_offsets, cache_lens, block_table, *, timestamps=None, cos=None, sin=None,
                  rot_dim: Optional[int] = None, interleaved: bool = False, norm: bool = False, eps: float = 1e-6, k_gain=None,
@@ -151,7 +153,7 @@ class CachedProblem(_Call):
     """New rows over the cache: forward() fills o [T, H, d] and y [T, H*d]
     BF16.  The last num_targets[b] rows of a sequence are candidates (their own
     k, v are read), those before them its newest history tokens, already
-    appended."""
+    appended.  q, k, v, u that are not contiguous are copied once, here."""
 
     def __init__(self, cache: PagedCache, q, k, v, u, seq_offsets, cache_lens, block_table, *, max_rows: int, max_seq_len: int,
                  alpha: float, num_targets=None, timestamps=None, rab_pos=None, rab_time=None, norm: str = "layernorm",
