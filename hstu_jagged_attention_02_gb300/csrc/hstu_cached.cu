@@ -197,7 +197,7 @@ hstu_status_t check_cached(const hstu_attn_desc* d, const hstu_cache_desc* c, in
   // the tiles' costs of all items are counted in 32 bits
   const int N = cached_block_rows(max_rows);
   const double items = ((double)d->total_tokens / N + d->B) * d->H;
-  if (items * (d->max_seq_len / (double)kCachedTile + 1) * kNearCost > 2e9) return HSTU_ERR_UNSUPPORTED;
+  if (items * (d->max_seq_len / (double)kCachedTile + 1) * kMostTileCost > 2e9) return HSTU_ERR_UNSUPPORTED;
   if (d->dtype != HSTU_BF16 || d->out_dtype != HSTU_BF16 || d->dropout_p > 0.f) return HSTU_ERR_UNSUPPORTED;
   return HSTU_OK;
 }

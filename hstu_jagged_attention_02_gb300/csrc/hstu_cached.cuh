@@ -67,24 +67,29 @@ __device__ __forceinline__ bool load_seq(const CachedParams& p, int b, CachedSeq
 // What a tile costs, by the ways the tensor-memory kernel scores it: near
 // tiles, where a block's rows differ in position bucket or mask, take 5.0 us
 // with 128 rows, the others 1.9.  Where a batch has near tiles the work is cut
-// by these costs, else by tiles: first passes of 900 to 2,100 rows by tiles
-// 65.8 us (the CTAs at the sequences' beginnings end after 51 us, the others after
-// 30), by these costs 52.6.  Single calls: costs of 2 and 5 55.9 us, 1 and 2
-// 59.0, 2 and 3 65.2.
-constexpr int kFarCost = 2, kNearCost = 5;
+// by these costs, else by tiles: first passes of 4 histories of 900 to 2,100 rows
+// by tiles 65.8 us (the CTAs at the sequences' beginnings end after 51 us, the
+// others after 30), by costs 52.6.  In halves of a far tile's cost: sums over 12
+// batches of first passes of 100 to 6,000 rows (128 rows a block) 4: 955 us, 5:
+// 925, 6: 887, 7: 893, 8: 905; 32 users' new rows and candidates (32 rows a block)
+// 5: 19.2 us, 6: 20.1.
+constexpr int kFarCost = 2, kMostTileCost = 6;
+__device__ __forceinline__ int near_cost(int N) { return N == 128 ? 6 : 5; }
 
-// Tiles of a block of rows: far ones, then near ones.
+// Tiles of a block of rows: far ones, then near ones.  near_c: what a near one
+// costs, or 0 where every tile counts 1.
 struct BlockTiles {
   int far, near;
   __device__ __forceinline__ int all() const { return far + near; }
-  __device__ __forceinline__ int cost(bool weighted) const { return weighted ? kFarCost * far + kNearCost * near : far + near; }
+  __device__ __forceinline__ int cost(int near_c) const { return near_c ? kFarCost * far + near_c * near : far + near; }
   // cost of the tiles before tile t, and the first tile with at least `c` before it
-  __device__ __forceinline__ int before(int t, bool weighted) const {
-    return weighted ? kFarCost * min(t, far) + kNearCost * max(t - far, 0) : t;
+  __device__ __forceinline__ int before(int t, int near_c) const {
+    return near_c ? kFarCost * min(t, far) + near_c * max(t - far, 0) : t;
   }
-  __device__ __forceinline__ int tile_at(int c, bool weighted) const {
-    if (!weighted) return c;
-    return c <= kFarCost * far ? (c + kFarCost - 1) / kFarCost : far + (c - kFarCost * far + kNearCost - 1) / kNearCost;
+  __device__ __forceinline__ int tile_at(int c, int near_c) const {
+    if (!near_c) return c;
+    const int rest = c - kFarCost * far;
+    return rest <= 0 ? (c + kFarCost - 1) / kFarCost : far + (near_c == 6 ? (rest + 5) / 6 : (rest + 4) / 5);
   }
 };
 __device__ __forceinline__ BlockTiles block_tiles(const CachedParams& p, const CachedSeq& s, int qb, int N) {
@@ -103,7 +108,7 @@ struct Start {
   int b, rem;         // its number, and the cost of its tiles that belong to CTAs before
   int items;          // items before the sequence
   int total, quota;   // cost in all (0 where the batch is refused), cost a CTA
-  int weighted;       // by tiles' costs, or by tiles
+  int near_c;         // what a near tile costs, or 0: cut by tiles
 };
 
 // A row's record for the finishing kernel: the cost of the tiles before its
@@ -184,16 +189,16 @@ __device__ __forceinline__ void cut_work(const CachedParams& p, int N, int* scan
     const int others = __shfl_sync(0xffffffffu, all[i], max(warp - 1, 0));
     before[i] += (warp > 0 ? others : 0) - own[i];
   }
-  const bool weighted = sum[1] > 0;
-  auto cost = [&](const int (&n)[3]) { return BlockTiles{n[0], n[1]}.cost(weighted); };
-  const int total = any_bad ? 0 : BlockTiles{sum[0], sum[1]}.cost(weighted);
+  const int near_c = sum[1] > 0 ? near_cost(N) : 0;
+  auto cost = [&](const int (&n)[3]) { return BlockTiles{n[0], n[1]}.cost(near_c); };
+  const int total = any_bad ? 0 : BlockTiles{sum[0], sum[1]}.cost(near_c);
   // a CTA's share holds a tile's beginning: no CTA between an item's first and last goes without a tile of it
-  const int quota = max((total + (int)gridDim.x - 1) / (int)gridDim.x, weighted ? kNearCost : 1);
+  const int quota = max((total + (int)gridDim.x - 1) / (int)gridDim.x, max(near_c, 1));
   const int first = (int)blockIdx.x * quota;
   if (threadIdx.x == 0) {
     start->total = total;
     start->quota = quota;
-    start->weighted = weighted;
+    start->near_c = near_c;
     if (blockIdx.x == 0) p.hdr[WS_CA_QUOTA] = any_bad ? -1 : quota;
   }
   if (any_bad) return;
@@ -241,11 +246,12 @@ struct Walk {
   BlockTiles tiles;
   int b, qb, h, tile, items;
   int line, end;      // where the item begins in the line, and the CTA's part ends
-  bool more, weighted;
+  int near_c;
+  bool more;
 
   __device__ __forceinline__ void begin(const CachedParams& p, const Start& st, int N) {
     const int first = (int)blockIdx.x * st.quota;
-    weighted = st.weighted;
+    near_c = st.near_c;
     end = min(first + st.quota, st.total);
     more = first < st.total;
     b = st.b; items = st.items; qb = 0; h = 0; tile = 0; line = first; tiles = {0, 0};
@@ -253,29 +259,29 @@ struct Walk {
     s = st.s;
     int rem = st.rem;
     tiles = block_tiles(p, s, qb, N);
-    while (rem >= tiles.cost(weighted) * p.H) {
-      rem -= tiles.cost(weighted) * p.H;
+    while (rem >= tiles.cost(near_c) * p.H) {
+      rem -= tiles.cost(near_c) * p.H;
       ++qb;
       tiles = block_tiles(p, s, qb, N);
     }
-    const int cost = tiles.cost(weighted);
+    const int cost = tiles.cost(near_c);
     h = rem / cost;
     rem -= h * cost;
     line = first - rem;
-    tile = tiles.tile_at(rem, weighted);
+    tile = tiles.tile_at(rem, near_c);
     if (tile >= tiles.all()) next_item(p, N);   // the item's last tile began before
   }
   // the piece at hand: tiles [tile, tile + take())
   __device__ __forceinline__ int take() const {
     const int room = end - line;
-    return (room >= tiles.cost(weighted) ? tiles.all() : min(tiles.tile_at(room, weighted), tiles.all())) - tile;
+    return (room >= tiles.cost(near_c) ? tiles.all() : min(tiles.tile_at(room, near_c), tiles.all())) - tile;
   }
   __device__ __forceinline__ int slot(const CachedParams& p) const { return items + qb * p.H + h + (int)blockIdx.x; }
   // the records of a block's rows, with its first piece; a warp
   __device__ __forceinline__ void write_records(const CachedParams& p, int N, int lane) const {
     if (h > 0 || tile > 0) return;
-    const int r0 = qb * N, rows = min(N, s.n - r0), cost = tiles.cost(weighted);
-    const int last = cost - tiles.before(tiles.all() - 1, weighted);
+    const int r0 = qb * N, rows = min(N, s.n - r0), cost = tiles.cost(near_c);
+    const int last = cost - tiles.before(tiles.all() - 1, near_c);
     for (int r = lane; r < rows; r += 32)
       p.rows[s.row0 + r0 + r] = row_record(line, items + qb * p.H, cost, r, last, r0 + r >= s.n - s.m);
   }
@@ -286,7 +292,7 @@ struct Walk {
 
  private:
   __device__ __forceinline__ void next_item(const CachedParams& p, int N) {
-    line += tiles.cost(weighted);
+    line += tiles.cost(near_c);
     tile = 0;
     more = line < end;
     if (!more || ++h < p.H) return;
