@@ -47,8 +47,8 @@ __global__ void __launch_bounds__(kWarps == 1 ? kFinThreads : 32 * kWarps) finis
   const int quota = p.hdr[WS_CA_QUOTA];
   const int64_t total = p.off[p.B];
   const int4 rec = p.rows[t];
-  if (quota < 0 || t >= total) return;    // a refused batch, a padded batch's row
-  const bool candidate = (rec.w >> 30) & 1;
+  if (quota < 0 || t >= total) return;    // a refused batch or a wait that ran out, a padded batch's row
+  const bool candidate = p.nt && ((rec.w >> 30) & 1);
   const int64_t row = t * F + lane * 4;
   // the row's own loads, under way while the sums are added up
   Raw4<__nv_bfloat16> q[NV], k[NV], v[NV], u[NV];
@@ -66,13 +66,11 @@ __global__ void __launch_bounds__(kWarps == 1 ? kFinThreads : 32 * kWarps) finis
   }
   // the pieces of features f .. f + 3: their number, and the first one's sum
   const float* rows = p.part + (int64_t)(rec.w & 0xffff) * D;
-  const int last = (rec.w >> 16) & 0xff;
   auto pieces = [&](int f, const float*& src) -> int {
-    const int h = f / D;
-    if (f >= F || rec.z <= 0) return 0;
-    const int at = rec.x + h * rec.z, c0 = at / quota;
-    src = rows + (int64_t)(rec.y + h + c0) * N * D + f % D;
-    return (at + rec.z - last) / quota - c0 + 1;
+    if (f >= F) return 0;
+    const RowPieces r = row_pieces(rec, f / D, quota, N, p.slots);
+    src = rows + r.slot * N * D + f % D;
+    return (int)r.n;
   };
   const int64_t next = (int64_t)N * D;    // floats from a piece's sum to the next one's
   float o[NV][4];
@@ -192,7 +190,7 @@ hstu_status_t check_cached(const hstu_attn_desc* d, const hstu_cache_desc* c, in
   if ((s = check_cache_desc(c, buffers)) != HSTU_OK) return s;
   if (max_rows < 1) return HSTU_ERR_INVALID_ARG;
   if (d->H != c->H || d->d_qk != c->d) return HSTU_ERR_INVALID_ARG;
-  if (d->flags != 0) return HSTU_ERR_INVALID_ARG;
+  if (d->flags & ~HSTU_FLAG_TEST_TIMEOUT) return HSTU_ERR_INVALID_ARG;
   if (d->total_tokens > ((int64_t)1 << 30)) return HSTU_ERR_UNSUPPORTED;   // one CTA a row finishes
   // the tiles' costs of all items are counted in 32 bits
   const int N = cached_block_rows(max_rows);
@@ -206,6 +204,7 @@ constexpr int kMaxCtas = 256;
 
 struct CachedWs {
   size_t rows, part, total;
+  int64_t slots;   // sums
 };
 
 CachedWs cached_ws(const hstu_attn_desc* d, int N) {
@@ -218,8 +217,8 @@ CachedWs cached_ws(const hstu_attn_desc* d, int N) {
   };
   w.rows = take(sizeof(int4) * (size_t)d->total_tokens);
   // a sum for every item, and one more for every CTA that ends inside one
-  const size_t slots = ((size_t)(d->total_tokens / N) + d->B) * d->H + kMaxCtas;
-  w.part = take(sizeof(float) * slots * N * d->d_v);
+  w.slots = (d->total_tokens / N + d->B) * d->H + kMaxCtas;
+  w.part = take(sizeof(float) * (size_t)w.slots * N * d->d_v);
   w.total = off;
   return w;
 }
@@ -269,7 +268,9 @@ hstu_status_t hstu_attn_fwd_cached(const hstu_attn_desc* d, const hstu_cache_des
   char* ws = static_cast<char*>(workspace);
   p.rows = reinterpret_cast<int4*>(ws + w.rows);
   p.part = reinterpret_cast<float*>(ws + w.part);
-  p.T = d->total_tokens; p.B = d->B; p.H = d->H;
+  p.T = d->total_tokens; p.B = d->B; p.H = d->H; p.slots = w.slots;
+  p.withhold = (d->flags & HSTU_FLAG_TEST_TIMEOUT) ? 1 : 0;
+  p.wait_ns = p.withhold ? 1000000ull : 2000000000ull;
   p.page_size = c->page_size; p.page_log = c->page_size == 32 ? 5 : (c->page_size == 64 ? 6 : 7);
   p.num_pages = c->num_pages; p.max_pages = c->max_pages;
   p.max_rows = a->max_rows; p.max_n = d->max_seq_len; p.P = d->num_pos_buckets; p.Tb = d->num_time_buckets;

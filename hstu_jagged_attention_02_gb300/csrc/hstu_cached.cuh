@@ -38,15 +38,17 @@ struct CachedParams {
   float* part;                // [slots][N][d]
   int4* rows;                 // [T] where a row's sums lie (row_record)
   int* hdr;
-  int64_t T;
+  int64_t T, slots;           // rows, sums that part has room for
+  uint64_t wait_ns;           // limit of a wait
   int B, H, page_size, page_log, num_pages, max_pages, max_rows, max_n, P, Tb, norm;
+  int withhold;               // test only: CTA 0 prepares no piece
   float alpha, inv_n, eps;
   float k_scale;              // 2^k_exp
   float o_scale;              // 2^v_exp / 16 / N of a tensor-core sum
 };
 
 // header words of the cached attention's workspace (beside WS_ERR)
-enum : int { WS_CA_QUOTA = 16 };   // cost a CTA, -1 where the batch was refused
+enum : int { WS_CA_QUOTA = 16 };   // cost a CTA, -1 where the batch was refused or a wait ran out
 
 struct CachedSeq {
   int64_t row0;   // first row
@@ -116,6 +118,24 @@ struct Start {
 // from bit 16 on, the last tile's cost and, in bit 30, whether it is a candidate.
 __device__ __forceinline__ int4 row_record(int line, int item0, int cost, int place, int last, bool candidate) {
   return make_int4(line, item0, cost, place | (last << 16) | (candidate ? 1 << 30 : 0));
+}
+
+// A row's sums of head h: the slot of the first and their number, 0 where the
+// record does not lead to slots that exist.  A CTA whose wait ran out leaves the
+// records of its blocks unwritten; whatever the workspace held there, nothing
+// outside it is read.
+struct RowPieces {
+  int64_t slot;
+  int64_t n;
+};
+__host__ __device__ __forceinline__ RowPieces row_pieces(int4 rec, int h, int quota, int N, int64_t slots) {
+  RowPieces r{0, 0};
+  if (rec.z <= 0 || rec.y < 0 || (rec.w & 0xffff) >= N) return r;
+  const uint32_t at = (uint32_t)rec.x + (uint32_t)h * (uint32_t)rec.z, last = (uint32_t)(rec.w >> 16) & 0xffu;
+  const uint32_t c0 = at / (uint32_t)quota, c1 = (at + (uint32_t)rec.z - last) / (uint32_t)quota;
+  r.slot = (int64_t)rec.y + h + c0;
+  if (c1 >= c0 && r.slot + (c1 - c0) < slots) r.n = (int64_t)(c1 - c0) + 1;
+  return r;
 }
 
 // Every CTA counts all sequences' tiles and finds its own beginning.  The rows'

@@ -226,13 +226,13 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
   wd.abort = &abort_flag;
   wd.err = p.hdr + WS_ERR;
   wd.err_info = p.hdr + WS_ERR_INFO;
-  wd.limit_ns = 2000000000ull;
+  wd.limit_ns = p.wait_ns;
 
   if (warp == C::WARPS) {
     // ------------------------------------------------------------- records
     Walk w;
     w.begin(p, start, kRows);
-    bool ok = true;
+    bool ok = !(p.withhold && blockIdx.x == 0);
     for (uint32_t np = 0; ok; ++np) {
       const uint32_t at = np % C::PIECES;
       if (lane == 0) ok = mbar_wait(piece_empty(at), ((np / C::PIECES) & 1) ^ 1, wd, 91);
@@ -246,6 +246,7 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
       w.write_records(p, kRows, lane);
       w.next(p, kRows);
     }
+    if (!ok) p.hdr[WS_CA_QUOTA] = -1;    // records are missing: the finishing kernel leaves everything as it is
     return;
   }
 
@@ -508,6 +509,7 @@ __global__ void __maxnreg__(SCfg<D>::REGS) cached_stream_kernel(const __grid_con
     }
   }
   copy_wait<0>();
+  if (!ok) p.hdr[WS_CA_QUOTA] = -1;
 }
 
 template <int D>

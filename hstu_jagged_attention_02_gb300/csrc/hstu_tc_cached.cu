@@ -224,13 +224,13 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
   wd.abort = abort_flag;
   wd.err = p.hdr + WS_ERR;
   wd.err_info = p.hdr + WS_ERR_INFO;
-  wd.limit_ns = 2000000000ull;
+  wd.limit_ns = p.wait_ns;
   const bool timed = p.times != nullptr;
 
   if (warp == kCopyWarp) {
     // -------------------------------------------------- pieces, page copies
     uint32_t it = 0, tk = 0;     // pieces, tiles so far
-    bool ok = true;
+    bool ok = !(p.withhold && blockIdx.x == 0);
     const int ppt = TILE / p.page_size;
     const PageLayout lay(p.page_size, D);
     Walk w;
@@ -741,6 +741,7 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
+  if (threadIdx.x == 0 && *abort_flag) p.hdr[WS_CA_QUOTA] = -1;   // records and sums are missing: nothing is finished
   if (warp == kSWarp) tmem_dealloc(tmem, L::TMEM_COLS);
 }
 

@@ -90,7 +90,8 @@ typedef enum { HSTU_NORM_NONE = 0, HSTU_NORM_LAYERNORM = 1 } hstu_norm_t;
                                             a millisecond, so the timeout path runs without a hang; the
                                             result is HSTU_ERR_TIMEOUT.  In hstu_layer_fwd it applies to the
                                             tensor-core input projection instead (its CTA 0 skips its first
-                                            load), and hstu_layer_bwd rejects it */
+                                            load), and hstu_layer_bwd rejects it.  In hstu_attn_fwd_cached
+                                            CTA 0 prepares none of its work */
 #define HSTU_FLAG_U_FP32 (1u << 2)       /* u is FP32 whatever dtype is (requires out_dtype FP32).  The
                                             gate multiplies y element by element, so a BF16 rounding of u
                                             is never averaged out; q, k, v stay in dtype */
@@ -583,8 +584,11 @@ hstu_status_t hstu_cache_read(const hstu_cache_desc* cache, const hstu_cache_rea
  *
  * The descriptor is the attention's: dtype and out_dtype BF16, d_qk == d_v ==
  * the cache's d, H <= its H * d limit, total_tokens = rows, max_seq_len = N
- * bounding every L + m, no flags, no dropout.  max_rows bounds every n (it
- * picks the tile's width: 8, 32, 64 or 128 rows).
+ * bounding every L + m, no flags but HSTU_FLAG_TEST_TIMEOUT, no dropout.
+ * max_rows bounds every n (it picks the tile's width for all sequences of the
+ * call: 8, 32, 64 or 128 rows).  Outputs are left as they are where the batch
+ * is refused on the device; where a wait ran out (HSTU_ERR_TIMEOUT) they are
+ * undefined.
  *
  * Precision: K, V and q enter the tensor cores exactly; 16 SiLU(z) is rounded
  * once to FP16 (so scores of 4094 and more overflow to infinity; a bias of
