@@ -24,7 +24,8 @@ def rope_tables(max_position: int, rot_dim: int, base: float = 10000.0, device="
 def jagged_positions(seq_offsets, num_targets=None, starts=None, total_tokens: Optional[int] = None):
     """Position of every packed token: its index in its sequence (plus
     starts[b]), a candidate's the one behind the history, as in the
-    attention's position buckets.  int32 [T]."""
+    attention's position buckets.  (Rows over a cache that holds some of them
+    already: cached_positions.)  int32 [T]."""
     T = int(seq_offsets[-1]) if total_tokens is None else total_tokens
     t = torch.arange(T, device=seq_offsets.device)
     b = torch.searchsorted(seq_offsets, t, right=True).sub_(1).clamp_(max=seq_offsets.numel() - 2)
@@ -34,6 +35,18 @@ def jagged_positions(seq_offsets, num_targets=None, starts=None, total_tokens: O
     if starts is not None:
         pos = pos + starts[b]
     return pos.to(torch.int32)
+
+
+def cached_positions(seq_offsets, cache_lens, num_targets=None, total_tokens: Optional[int] = None):
+    """Position of every packed row of hstu_attention_cached: cache_lens[b]
+    counts a sequence's new history rows already (they were appended), so
+    those are the last positions below it, as in the cache, and a candidate
+    has cache_lens[b].  The tables of the rotation need a row more than the
+    longest cache.  int32 [T]."""
+    history = seq_offsets[1:] - seq_offsets[:-1]
+    if num_targets is not None:
+        history = history - num_targets
+    return jagged_positions(seq_offsets, num_targets, cache_lens - history, total_tokens)
 
 
 def _need(ok, what):
@@ -237,8 +250,8 @@ def hstu_qk_norm_rope(q, k, positions=None, cos=None, sin=None, *, q_gain=None, 
                       eps: float = 1e-6, rot_dim: Optional[int] = None, interleaved: bool = False, num_tokens=None):
     """Differentiable norm and rotation of q [T, Hq, d] and k [T, Hk, d]
     (either may be None): returns (q', k') for hstu_attention.  cos, sin:
-    rope_tables; positions: jagged_positions, or any int32 [T] below
-    max_position.  num_tokens: one int64 on the device, tokens in use of a
+    rope_tables; positions: jagged_positions, cached_positions, or any int32
+    [T] below max_position.  num_tokens: one int64 on the device, tokens in use of a
     padded batch (rows behind it come back as zeros).  There is no second
     derivative.  Into a CUDA graph goes QKProblem's forward and backward, rather
     than autograd's."""
