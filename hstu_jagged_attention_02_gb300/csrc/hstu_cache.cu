@@ -447,23 +447,21 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const __grid_consta
   if (p.gain) gain = Row8(fetch4(p.gain + kt.pt.f0), fetch4(p.gain + kt.pt.f1));
   const PageLayout lay(1 << p.page_log, D);
   for (; t < t_end; ++t) {
-    const bool placed = pl.at(p, p.lens, t, total);
+    bool placed = pl.at(p, p.lens, t, total);
     if (!fits(off0, total, p.T, p.hdr) || t >= total) return;
-    if (!placed) {
+    const Slot sl = pl.slot;
+    if (placed && p.rot && sl.pos >= p.max_pos) {   // behind the tables
+      if (lane == 0) set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, pl.seq.b);
+      placed = false;
+    }
+    if (!placed) {    // this token is left out; the next ones may belong to other sequences
       if (t + 1 < t_end) load(t + 1, 0);
       continue;
     }
-    const Slot sl = pl.slot;
     Angles an;
-    if (p.rot) {
-      if (sl.pos >= p.max_pos) {
-        if (lane == 0) set_error(p.hdr, HSTU_ERR_DEVICE_CHECK, pl.seq.b);
-        return;
-      }
-      if (kt.pt.turns) {
-        const int64_t at = (int64_t)sl.pos * (p.rot >> 1) + 4 * l;
-        an.load(p.cos + at, p.sin + at, 1.f);
-      }
+    if (p.rot && kt.pt.turns) {
+      const int64_t at = (int64_t)sl.pos * (p.rot >> 1) + 4 * l;
+      an.load(p.cos + at, p.sin + at, 1.f);
     }
     uint8_t* block = p.pages + sl.page * p.H * (int64_t)lay.bytes();
     const int place_c = sl.place * lay.code_row, place_s = lay.scales() + sl.place * lay.scale_row;

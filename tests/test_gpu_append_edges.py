@@ -1,0 +1,56 @@
+"""Appending to the paged 4-bit cache at its edges: a token that has no place
+among tokens that have one, infinities and products beyond FP32, tables whose
+entries are larger than one.  What is held is compared bit by bit with the
+64-bit form (tests/serving_ref.py), as in tests/test_gpu_cache.py."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests import serving_ref as R  # noqa: E402
+from tests.test_gpu_cache import Batch, _cache, _f64  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("big", [False, True])
+@pytest.mark.parametrize("bad", ["table", "page"])
+def test_a_token_without_a_place_costs_no_other_its_own(big, bad):
+    """Sequences of two tokens, the first ones behind the rotation's tables or
+    in a page that does not exist, next to valid ones: with many tokens a warp
+    takes four neighbours, of several sequences."""
+    from hstu_jagged_attention_02_gb300 import binding as C
+    from hstu_jagged_attention_02_gb300.cache import AppendProblem, hstu_cache_read
+    H, d, page = 2, 64, 64
+    top = 7400 if big else 300                                    # rows of the tables
+    new, cached = [2, 2, 3, 1, top - 8], [top - 1, 0, top, 5, 0]   # 0: one inside, one behind; 2: all behind
+    b = Batch(new, cached, H, d, page, seed=60)
+    c = _cache(b, H, d, page)
+    c.timestamps.fill_(-1)
+    tab = R.rope_tables(top if bad == "table" else top + 8, d)
+    if bad == "page":       # the pages of the tokens that are behind the tables in the other case
+        b.table[0, top // page], b.table[2, top // page] = b.num_pages, -1
+        b.table[2, (top + 2) // page] = -1
+    cos, sin = (torch.from_numpy(x).cuda() for x in tab)
+    pr = AppendProblem(c, b.k, b.v, b.off, b.cache_lens, b.table, timestamps=b.times, cos=cos, sin=sin, norm=True, eps=1e-5)
+    pr.run()
+    assert pr.device_error() == C.HSTU_ERR_DEVICE_CHECK
+    # the tokens whose position and page exist, read back one sequence at a time
+    off, kept = b.off.tolist(), 0
+    for s in range(len(new)):
+        good = [i for i in range(new[s]) if cached[s] + i < top] if bad == "table" else \
+            [i for i in range(new[s]) if 0 <= int(b.table[s, (cached[s] + i) // page]) < b.num_pages]
+        if not good:
+            continue
+        assert good == list(range(len(good)))
+        n = len(good)
+        k, v, t = hstu_cache_read(c, torch.tensor([0, n]).cuda(), b.starts[s:s + 1].contiguous(), b.table[s:s + 1].contiguous())
+        r = slice(off[s], off[s] + n)
+        at = np.arange(cached[s], cached[s] + n)
+        want = R.qk_forward(_f64(b.k[r]), None, tab[0][at], tab[1][at], False, True, float(np.float32(1e-5)))
+        np.testing.assert_array_equal(_f64(k), R.four_bit(want), err_msg=f"keys of {s}")
+        np.testing.assert_array_equal(_f64(v), R.four_bit(_f64(b.v[r])), err_msg=f"values of {s}")
+        assert torch.equal(t, b.times[r])
+        kept += n
+    # and nothing else was written: sequence 0 keeps its first, 2 nothing
+    assert int((c.timestamps != -1).sum()) == kept
