@@ -95,10 +95,11 @@ __device__ __forceinline__ uint2 encode_exact(const Row8& x, float top) {
 }
 
 // 4 features known to +-d, and their group's largest magnitude to [lo, hi]:
-// false where that does not decide the result.
+// false where that does not decide the result (a NaN may be two infinities of
+// this path's own, each a number beyond FP32 times the cache's power of two).
 __device__ __forceinline__ bool encode_banded(const float2 (&x)[2], const float2 (&d)[2], float lo, float hi, Coded& c) {
   c.scale = e4m3_of(hi * (0.16666667f * 1.0000005f));
-  const bool sure = c.scale == e4m3_of(lo * (0.16666667f * 0.9999995f));
+  const bool sure = c.scale == e4m3_of(lo * (0.16666667f * 0.9999995f)) && c.scale != 0x7fu;
   const float inv = inverse(e4m3_float(c.scale));
   const float2 i2 = make_float2(inv, inv), n2 = make_float2(-inv, -inv);
   uint32_t lower = 0, upper = 0;
@@ -120,10 +121,12 @@ __device__ __forceinline__ bool encode_banded(const float2 (&x)[2], const float2
 // A number as the sum of two FP32 ones, h the nearest to it: 2^-48 of it in
 // precision, on the FP32 units (an FP64 path of the same steps took 7 us to the
 // 1 us of this one; the exactness of sums and products in two parts is Dekker's
-// and Knuth's).
+// and Knuth's).  A result that is not finite has no second part, where the
+// steps for it would make an infinity a NaN.
 struct Two {
   float h, l;
 };
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.4028234663852886e38f; }
 __device__ __forceinline__ Two sum_of(float a, float b) {          // exact
   const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
   return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
@@ -134,11 +137,11 @@ __device__ __forceinline__ Two join(float h, float l) {            // exact for 
 }
 __device__ __forceinline__ Two operator+(Two a, Two b) {
   const Two s = sum_of(a.h, b.h);
-  return join(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+  return finite(s.h) ? join(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l))) : Two{s.h, 0.f};
 }
 __device__ __forceinline__ Two operator*(Two a, float f) {
   const float p = __fmul_rn(a.h, f);
-  return join(p, __fmaf_rn(a.l, f, __fmaf_rn(a.h, f, -p)));
+  return finite(p) ? join(p, __fmaf_rn(a.l, f, __fmaf_rn(a.h, f, -p))) : Two{p, 0.f};
 }
 __device__ __forceinline__ Two operator-(Two a) { return {-a.h, -a.l}; }
 // whether |a| lies above a border, or on it too
@@ -302,8 +305,8 @@ __device__ __noinline__ uint2 key_two(const AppendParams& p, int how, int f0, in
   Two x[4], y[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    x[e] = rs * x0[e] * (p.gain ? p.gain[f0 + e] : 1.f) * p.k_scale;
-    y[e] = rs * x0[4 + e] * (p.gain ? p.gain[f1 + e] : 1.f) * p.k_scale;
+    x[e] = rs * x0[e] * (p.gain ? p.gain[f0 + e] : 1.f);
+    y[e] = rs * x0[4 + e] * (p.gain ? p.gain[f1 + e] : 1.f);
   }
   if (how & 1) {
 #pragma unroll
@@ -314,6 +317,11 @@ __device__ __noinline__ uint2 key_two(const AppendParams& p, int how, int f0, in
       a = u;
       b = w;
     }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {     // the power of two last: what passes FP32 here lies above every border
+    x[e] = x[e] * p.k_scale;
+    y[e] = y[e] * p.k_scale;
   }
   if (how & 2) {
     float xh[4], xl[4], yh[4], yl[4];
@@ -328,7 +336,6 @@ __device__ __noinline__ uint2 key_two(const AppendParams& p, int how, int f0, in
   unsigned long long tx = 0, ty = 0;
   float bx = 0.f, by = 0.f;           // 1: a NaN
   auto largest = [](Two& a, unsigned long long& top, float& bad) {
-    if (!(fabsf(a.h) <= 3.4028234e38f)) a.l = 0.f;                  // infinities have no second part
     if (a.h != a.h) {
       bad = 1.f;
     } else {

@@ -491,7 +491,8 @@ hstu_status_t hstu_qk_norm_rope_bwd(const hstu_qk_desc* desc, const hstu_qk_bwd_
  * v_exp for values, one power of two for the whole cache:
  *
  *   s = e4m3(max |x| 2^-E / 6), at most 448;  code = e2m1(x 2^-E / s), at most 6
- *   value = code s 2^E        (s = 0: all values 0; a NaN in the group: all NaN)
+ *   value = code s 2^E        (s = 0: all values 0; a NaN in the group: all NaN;
+ *                              an infinity: the largest code of s = 448)
  *
  * both rounded to nearest, ties to the even mantissa, as real numbers would be
  * (the borders are decided exactly).  A value has 6 significant bits: it is a

@@ -54,3 +54,46 @@ def test_a_token_without_a_place_costs_no_other_its_own(big, bad):
         kept += n
     # and nothing else was written: sequence 0 keeps its first, 2 nothing
     assert int((c.timestamps != -1).sum()) == kept
+
+
+@pytest.mark.parametrize("d,rot,inter", [(64, 32, False), (128, 64, True), (128, 8, False), (64, 16, True), (128, 32, False)])
+def test_infinite_keys_that_are_turned(d, rot, inter):
+    # an infinity goes in as the largest code of the largest scale, in a feature that is turned as in one that is not;
+    # where the turn itself has no value (infinity less infinity, infinity times zero) the group is NaN
+    from hstu_jagged_attention_02_gb300.cache import hstu_cache_append, hstu_cache_read
+    H, page, n = 3, 32, 40
+    b = Batch([n], [0], H, d, page, seed=61)
+    c = _cache(b, H, d, page)
+    x = _f64(b.k)
+    g = np.random.default_rng(62)
+    for t in range(1, n):
+        x[t, t % H, g.integers(0, d)] = np.inf if t % 2 else -np.inf
+        if t % 5 == 0:
+            x[t, t % H, g.integers(0, d)] = np.nan
+    x[3, :, 0], x[3, :, rot // 2] = np.inf, np.inf          # both of a pair of halves
+    x[7, :, 0], x[7, :, 1] = -np.inf, np.inf                # both of a pair of neighbours
+    k = torch.from_numpy(x).bfloat16().cuda()
+    tab = R.rope_tables(n, rot)
+    cos, sin = (torch.from_numpy(z).cuda() for z in tab)
+    hstu_cache_append(c, k, b.v, b.off, b.cache_lens, b.table, timestamps=b.times, cos=cos, sin=sin, interleaved=inter)
+    got, _, _ = hstu_cache_read(c, b.off, b.starts, b.table)
+    with np.errstate(invalid="ignore"):
+        want = R.four_bit(R.turn(_f64(k), tab[0], tab[1], inter))
+    assert np.isnan(want).any() and (np.abs(want) == 2688.0).any() and not np.isnan(want[1]).all()
+    np.testing.assert_array_equal(_f64(got), want)
+
+
+@pytest.mark.parametrize("rot,k_exp", [(32, -32), (64, -32), (64, 0), (64, 32)])
+def test_keys_near_the_types_end(rot, k_exp):
+    # magnitudes up to 2^126: the power of two alone would take them beyond FP32, the result is the largest code
+    from hstu_jagged_attention_02_gb300.cache import hstu_cache_append, hstu_cache_read
+    H, d, page, n = 2, 64, 32, 64
+    b = Batch([n], [0], H, d, page, seed=63)
+    c = _cache(b, H, d, page, k_exp=k_exp)
+    e = torch.randint(60, 126, (n, H, d // 16, 1), generator=torch.Generator().manual_seed(64)).double()
+    k = (b.k.double().cpu().clamp(-1.9, 1.9).view(n, H, d // 16, 16) * 2.0 ** e).view(n, H, d).bfloat16().cuda()
+    tab = R.rope_tables(n, rot)
+    cos, sin = (torch.from_numpy(z).cuda() for z in tab)
+    hstu_cache_append(c, k, b.v, b.off, b.cache_lens, b.table, timestamps=b.times, cos=cos, sin=sin)
+    got, _, _ = hstu_cache_read(c, b.off, b.starts, b.table)
+    np.testing.assert_array_equal(_f64(got), R.four_bit(R.turn(_f64(k), tab[0], tab[1], False), k_exp))
