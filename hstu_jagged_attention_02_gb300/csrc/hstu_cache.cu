@@ -38,6 +38,9 @@ namespace {
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kManyTokens = 4;
 constexpr float kBand = 1.05e-06f;   // 2^-20 of a feature's terms, its quotient by the scale included, and a little
+// The terms of a turned feature are |a c| + |b s| <= m (|a| + |b|), m the
+// largest cosine or sine of the lane's pairs; kBand is for m <= 1 and grows with
+// m (tables may carry a factor).
 
 struct AppendParams {
   const int64_t* off;
@@ -227,26 +230,27 @@ struct KeyTurn {
 };
 
 // A lane's 8 features of a key, normed and turned, coded from FP32; false where that does not decide them.
+// turn_band: kBand, of the terms of turned features.
 template <int LANES>
-__device__ __forceinline__ bool key_f32(const AppendParams& p, const KeyTurn& kt, const Angles& an, const Row8& gain, int lane,
-                                        Row8 x, Coded& cx, Coded& cy) {
+__device__ __forceinline__ bool key_f32(const AppendParams& p, const KeyTurn& kt, const Angles& an, float turn_band,
+                                        const Row8& gain, int lane, Row8 x, Coded& cx, Coded& cy) {
   float rs = p.k_scale;
   if (p.norm) rs *= rsqrtf(fmaf(row_sum<LANES>(x.dot(x)), 1.f / (8 * LANES), p.eps));
   x.times(rs);
   if (p.gain) x.times(gain);
   Row8 d;
-  const float2 band = make_float2(kBand, kBand);
+  const float2 band = make_float2(kBand, kBand), tband = make_float2(turn_band, turn_band);
   auto mag = [](float2 a) { return make_float2(fabsf(a.x), fabsf(a.y)); };
   if (kt.pt.turns) {
     if (p.interleaved) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float m = kBand * (fabsf(x.v[e].x) + fabsf(x.v[e].y));
+        const float m = turn_band * (fabsf(x.v[e].x) + fabsf(x.v[e].y));
         d.v[e] = make_float2(m, m);
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) d.v[e] = d.v[e + 2] = __fmul2_rn(__fadd2_rn(mag(x.v[e]), mag(x.v[e + 2])), band);
+      for (int e = 0; e < 2; ++e) d.v[e] = d.v[e + 2] = __fmul2_rn(__fadd2_rn(mag(x.v[e]), mag(x.v[e + 2])), tband);
     }
     an.turn(x, p.interleaved);
   } else {
@@ -466,9 +470,11 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const __grid_consta
       continue;
     }
     Angles an;
+    float turn_band = kBand;
     if (p.rot && kt.pt.turns) {
       const int64_t at = (int64_t)sl.pos * (p.rot >> 1) + 4 * l;
       an.load(p.cos + at, p.sin + at, 1.f);
+      turn_band *= fmaxf(1.f, an.largest());
     }
     uint8_t* block = p.pages + sl.page * p.H * (int64_t)lay.bytes();
     const int place_c = sl.place * lay.code_row, place_s = lay.scales() + sl.place * lay.scale_row;
@@ -482,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const __grid_consta
       else if (t + 1 < t_end) load(t + 1, 0);
       if (work) {
         Coded cx, cy;
-        const bool sure = key_f32<LANES>(p, kt, an, gain, lane, kx, cx, cy);
+        const bool sure = key_f32<LANES>(p, kt, an, turn_band, gain, lane, kx, cx, cy);
         if (__any_sync(0xffffffffu, !sure && head < p.H)) {
           const uint2 r = key_two<LANES>(
               p, (kt.pt.turns ? 1 : 0) | (kt.moved ? 2 : 0) | (kt.quad ? 4 : 0) | (kt.any_quad ? 8 : 0), kt.pt.f0, kt.pt.f1,

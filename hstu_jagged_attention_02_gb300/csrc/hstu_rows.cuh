@@ -100,6 +100,14 @@ struct Angles {
     c[0] = make_float2(a.x, a.y); c[1] = make_float2(a.z, a.w);
     s[0] = make_float2(b.x * dir, b.y * dir); s[1] = make_float2(b.z * dir, b.w * dir);
   }
+  // the largest magnitude among them
+  __device__ __forceinline__ float largest() const {
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      m = fmaxf(m, fmaxf(fmaxf(fabsf(c[e].x), fabsf(c[e].y)), fmaxf(fabsf(s[e].x), fabsf(s[e].y))));
+    return m;
+  }
   __device__ __forceinline__ void turn(Row8& r, bool interleaved) const {
     if (interleaved) {
       const float cc[4] = {c[0].x, c[0].y, c[1].x, c[1].y}, ss[4] = {s[0].x, s[0].y, s[1].x, s[1].y};

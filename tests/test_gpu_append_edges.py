@@ -97,3 +97,22 @@ def test_keys_near_the_types_end(rot, k_exp):
     hstu_cache_append(c, k, b.v, b.off, b.cache_lens, b.table, timestamps=b.times, cos=cos, sin=sin)
     got, _, _ = hstu_cache_read(c, b.off, b.starts, b.table)
     np.testing.assert_array_equal(_f64(got), R.four_bit(R.turn(_f64(k), tab[0], tab[1], False), k_exp))
+
+
+@pytest.mark.parametrize("factor,k_exp,inter", [(16.0, 5, False), (100.0, 7, True), (1.25, 1, False)])
+def test_tables_with_entries_above_one(factor, k_exp, inter):
+    """Cosines and sines that carry a factor (as schemes for longer contexts
+    fold one in): the features near a border grow with it, and are decided all
+    the same."""
+    from hstu_jagged_attention_02_gb300.cache import hstu_cache_append, hstu_cache_read
+    H, d, page, n = 8, 128, 128, 12000
+    b = Batch([n], [0], H, d, page, seed=65)
+    c = _cache(b, H, d, page, k_exp=k_exp)
+    gain = (1 + 0.3 * torch.randn(d, generator=torch.Generator().manual_seed(66))).cuda()
+    tab = [(x * np.float32(factor)).astype(np.float32) for x in R.rope_tables(n, d)]
+    cos, sin = (torch.from_numpy(x).cuda() for x in tab)
+    hstu_cache_append(c, b.k, b.v, b.off, b.cache_lens, b.table, timestamps=b.times, cos=cos, sin=sin, norm=True, eps=1e-5,
+                      k_gain=gain, interleaved=inter)
+    k, _, _ = hstu_cache_read(c, b.off, b.starts, b.table)
+    want = R.qk_forward(_f64(b.k), _f64(gain), tab[0], tab[1], inter, True, float(np.float32(1e-5)))
+    np.testing.assert_array_equal(_f64(k), R.four_bit(want, k_exp))
