@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(kBwdThreads) qk_bwd_kernel(const __grid_consta
       e += sums[4 * kBwdThreads + k * 2 * D + col];
     }
     float* dst = p.dgain[col / D];
-    if (dst) dst[col % D] = s + e;
+    // of a sum that is not finite the errors are NaN (infinity less infinity): it stands as it is
+    if (dst) dst[col % D] = fabsf(s) <= 3.4028234663852886e38f ? s + e : s;
   }
   if (threadIdx.x == 0) p.hdr[WS_NEXT] = 0;   // ready for the workspace's next call
 }
