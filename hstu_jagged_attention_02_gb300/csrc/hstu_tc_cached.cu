@@ -112,6 +112,9 @@ static_assert(sizeof(Piece) <= 96, "a slot holds a piece");
 // How 32 tokens of a tile are scored: one bias a token for all rows; all tokens exist; gaps of 32 bits; the last
 // position bucket.
 enum : int { kFast = 1, kWhole = 2, kNarrow = 4, kFar = 8 };
+// Binary digits of a gap to the block's earliest row: two such gaps differ by less than 2^31.
+constexpr int kNarrowBits = 30;
+static_assert(kNarrowTsSpan == (int64_t)1 << kNarrowBits, "as in the other kernels");
 
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
@@ -405,7 +408,7 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
       const int64_t tmin = pc.tmin, tmax = pc.tmax;
       const int pmin = pc.hist > 0 ? pc.pos0 : len, pmax = pc.hist == pc.rows ? pc.pos0 + pc.rows - 1 : len;
       const float* rp = p.rab_pos ? p.rab_pos + pc.h * p.P : nullptr;
-      const bool one_time = !p.rab_time || tmin == tmax;
+      const bool one_time = !p.rab_time || tmin == tmax, one_span = bit_length(tmin, tmax) <= kNarrowBits;
       for (int t = t0; t < t1; ++t, ++tk) {
         const uint32_t rs = tk % L::NR, st = tk & 1;
         ok = mbar_wait(bar(L::RAWFULL + rs), (tk / L::NR) & 1, wd, 67);
@@ -433,12 +436,10 @@ __global__ void __maxnreg__(72) cached_tc_kernel(const __grid_constant__ CachedP
           const int a = bit_length(tmin, tj);
           bias += tbl[a];
           if (!one_time) same = same && min(a, p.Tb - 1) == min(bit_length(tmax, tj), p.Tb - 1) && (tj <= tmin || tj >= tmax);
-          const int64_t rel = tj - tmin;
           const bool fast = __all_sync(0xffffffffu, same || j >= len);
           const bool whole = __all_sync(0xffffffffu, j < len);
-          // else gaps of 32 bits where they fit
-          const bool narrow = __all_sync(0xffffffffu, j >= len || (rel > -kNarrowTsSpan && rel < kNarrowTsSpan)) &&
-                              tmax - tmin < kNarrowTsSpan;
+          // else gaps of 32 bits where they fit (their lengths say so whatever the times are; differences may wrap)
+          const bool narrow = __all_sync(0xffffffffu, j >= len || a <= kNarrowBits) && one_span;
           mode = (fast ? kFast : 0) | (whole ? kWhole : 0) | (narrow ? kNarrow : 0) | (far ? kFar : 0);
         }
         ok = mbar_wait(bar(L::STEMPTY + st), ((tk >> 1) & 1) ^ 1, wd, 68);
