@@ -94,7 +94,8 @@ class QKProblem:
     q and k are used in place where their features are contiguous and heads
     and tokens lie multiples of 16 bytes apart (parts of one projection's
     output, say), else copied once, here.  The outputs are allocated unless
-    given; inplace=True writes over q and k."""
+    given; inplace=True writes over q and k (not with the backward of a norm,
+    which needs them)."""
 
     def __init__(self, q, k, positions=None, cos=None, sin=None, *, rot_dim: Optional[int] = None,
                  interleaved: bool = False, norm: bool = True, eps: float = 1e-6, q_gain=None, k_gain=None,
@@ -140,6 +141,9 @@ class QKProblem:
         backward = dq_out is not None or dk_out is not None
         _need(not backward or ((dq_out is None) == (q is None) and (dk_out is None) == (k is None)),
               "the backward needs the gradients of both outputs")
+        for x, out in ((self.q, self.q_out), (self.k, self.k_out)):
+            _need(not (backward and norm) or x is None or x.numel() == 0 or x.data_ptr() != out.data_ptr(),
+                  "the norm's backward needs the inputs, which a forward in place overwrites")
         self.dq, self.dk = (new(q), new(k)) if backward else (None, None)
         gain = lambda t, g: torch.empty(d, device=dev, dtype=torch.float32) \
             if backward and norm and want_gain_grads and t is not None and g is not None else None  # noqa: E731
