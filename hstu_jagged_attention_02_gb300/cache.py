@@ -10,7 +10,7 @@ import torch
 
 from . import binding as C
 from .attention import _ptr
-from .qk import Launch, _need, _rows, _same_device, device_error
+from .qk import Launch, _need, _rows, _same_device, _strides, device_error
 
 
 class PagedCache:
@@ -112,7 +112,7 @@ class AppendProblem(_Call):
         a = C.hstu_cache_append_args()
         a.B, a.rot_dim, a.interleaved, a.norm, a.eps = B, rot_dim, int(interleaved), int(norm), eps
         a.total_tokens, a.max_position = T, cos.shape[0] if rot_dim else 0
-        a.k_strides, a.v_strides = (self.k.stride(0), self.k.stride(1)), (self.v.stride(0), self.v.stride(1))
+        a.k_strides, a.v_strides = _strides(self.k), _strides(self.v)
         a.seq_offsets, a.cache_lens, a.block_table = _ptr(seq_offsets), _ptr(cache_lens), _ptr(block_table)
         a.token_times, a.cos, a.sin, a.k_gain, a.k, a.v = (_ptr(t) for t in (timestamps, cos, sin, k_gain, self.k, self.v))
         self.args = a

@@ -60,7 +60,8 @@ def _same_device(device, **tensors):
 
 
 def _strides(t):
-    return (0, 0) if t is None else (t.stride(0), t.stride(1))
+    # (those of a tensor without elements lead nowhere and follow no rule)
+    return (0, 0) if t is None or t.numel() == 0 else (t.stride(0), t.stride(1))
 
 
 def _rows(t, name):
