@@ -16,7 +16,8 @@ from .qk import Launch, _need, _rows, _same_device, _strides, device_error
 class PagedCache:
     """Pages of one layer's keys and values (see the cache section of
     hstu_attn.h): pages uint8 [num_pages, H, bytes], timestamps int64
-    [num_pages, page_size] or None.  Allocated here (zeroed) unless given.
+    [num_pages, page_size] or None.  Allocated here (zeroed, on the current
+    stream) unless given.
     Which page belongs to whom is the caller's book-keeping (block tables)."""
 
     def __init__(self, num_pages: Optional[int] = None, *, H: int, d: int, page_size: int = 64, k_exp: int = 0, v_exp: int = 0,

@@ -192,24 +192,42 @@ class QKProblem:
 
 class Launch:
     """One C call with its arguments put together once: calling it launches on
-    the given stream, or on the current one of the tensors' device."""
+    the given stream, or on the current one of the tensors' device.
 
-    __slots__ = ("index", "fn", "name", "args", "keep")
+    What a problem makes for itself (a zeroed workspace, copies of tensors in
+    other layouts) is queued on the stream that is current then; the first call
+    on another stream waits for that one.  The caller's own tensors are the
+    caller's to wait for.  A call that is being captured waits for nothing: make
+    the problem before the capture begins (torch.cuda.graph synchronises)."""
+
+    __slots__ = ("index", "fn", "name", "args", "keep", "made", "known")
 
     def __init__(self, device, fn, name, *args):
         _need(device.type == "cuda", f"{name} needs tensors on a CUDA device, not on {device}")
         self.index = device.index if device.index is not None else torch.cuda.current_device()
         self.fn, self.name, self.keep = fn, name, args
         self.args = tuple(C.ctypes.byref(a) if isinstance(a, C.ctypes.Structure) else a for a in args)
+        self.made = torch.cuda.current_stream(self.index)
+        self.known = {self.made.cuda_stream}    # streams that have waited
 
     def __call__(self, stream=None):
         if torch._C._cuda_getDevice() != self.index:    # the launches go to the current device
             with torch.cuda.device(self.index):
                 return self(stream)
         s = torch._C._cuda_getCurrentRawStream(self.index) if stream is None else stream.cuda_stream
+        if s not in self.known:
+            self._wait(stream if stream is not None else torch.cuda.current_stream(self.index))
         status = self.fn(*self.args, s)
         if status:
             raise C.HSTUError(status, self.name)
+
+    def _wait(self, stream):
+        for s in (stream, self.made):
+            with torch.cuda.stream(s):
+                if torch.cuda.is_current_stream_capturing():
+                    return
+        stream.wait_stream(self.made)
+        self.known.add(stream.cuda_stream)
 
 
 def device_error(device, workspace, stream=None) -> int:
