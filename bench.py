@@ -185,7 +185,8 @@ def _code_only(text: str) -> str:
 def kernel_sources_sha(role: str):
     """Hash of the code an attention kernel is compiled from: its translation
     unit and device headers, the kernel parameter block of hstu_internal.h
-    and the public header's declarations (comments left out)."""
+    and the public header as far as the attention's descriptor (comments left
+    out; the declarations behind it are of calls, which no kernel sees)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "hstu_jagged_attention_02_gb300", "csrc")
     for fn in KERNEL_SOURCES[role]:
@@ -193,7 +194,8 @@ def kernel_sources_sha(role: str):
     internal = open(os.path.join(csrc, "hstu_internal.h")).read()
     i = internal.index("struct AttnParams {")
     h.update(_code_only(internal[i:internal.index("};", i)]).encode())
-    h.update(_code_only(open(os.path.join(ROOT, "include", "hstu_attn.h")).read()).encode())
+    public = open(os.path.join(ROOT, "include", "hstu_attn.h")).read()
+    h.update(_code_only(public[:public.index("} hstu_attn_desc;")]).encode())
     return h.hexdigest()[:16]
 
 
