@@ -199,20 +199,29 @@ class CachedProblem(_Call):
         self._launch(stream)
 
 
+# What the device finds wrong with offsets, lengths or page numbers raises nothing
+# in the calls below, which drop the workspace that they make: a token without a
+# place is left out, the rows of a refused batch hold nothing.  To look, hold a
+# problem and ask its device_error(), or pass workspace= (zeroed uint8, 256 bytes
+# but for the attention) and ask qk.device_error(device, workspace).
+
 def hstu_cache_append(cache: PagedCache, k, v, seq_offsets, cache_lens, block_table, **kw) -> None:
-    """Append once (AppendProblem's arguments)."""
+    """Append once (AppendProblem's arguments).  Device errors: only with a
+    workspace of the caller's (above)."""
     AppendProblem(cache, k, v, seq_offsets, cache_lens, block_table, **kw).run()
 
 
 def hstu_cache_read(cache: PagedCache, seq_offsets, starts, block_table, **kw):
-    """(k, v, timestamps) of the asked positions (ReadProblem's arguments)."""
+    """(k, v, timestamps) of the asked positions (ReadProblem's arguments; rows
+    behind the last sequence hold nothing).  Device errors as in hstu_cache_append."""
     pr = ReadProblem(cache, seq_offsets, starts, block_table, **kw)
     pr.run()
     return pr.k, pr.v, pr.timestamps
 
 
 def hstu_attention_cached(cache: PagedCache, q, k, v, u, seq_offsets, cache_lens, block_table, **kw):
-    """(o, y) of new rows over the cache (CachedProblem's arguments)."""
+    """(o, y) of new rows over the cache (CachedProblem's arguments; rows behind
+    the last sequence hold nothing).  Device errors as in hstu_cache_append."""
     pr = CachedProblem(cache, q, k, v, u, seq_offsets, cache_lens, block_table, **kw)
     pr.forward()
     return pr.o, pr.y

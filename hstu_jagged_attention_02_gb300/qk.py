@@ -231,6 +231,9 @@ class Launch:
 
 
 def device_error(device, workspace, stream=None) -> int:
+    """The first error that a call with this workspace found on the device (0:
+    none), kept until the header, its first 256 bytes, is zeroed.  Waits for
+    the stream (default: the current one)."""
     with torch.cuda.device(device):
         s = stream if stream is not None else torch.cuda.current_stream()
         return C.hstu_get_device_error(workspace.data_ptr(), s.cuda_stream)
@@ -240,10 +243,10 @@ class QKNormRopeFunction(torch.autograd.Function):
     """(q', k') of q, k; gradients for q, k and the gains."""
 
     @staticmethod
-    def forward(ctx, q, k, q_gain, k_gain, positions, cos, sin, num_tokens, rot_dim, interleaved, norm, eps):
+    def forward(ctx, q, k, q_gain, k_gain, positions, cos, sin, num_tokens, rot_dim, interleaved, norm, eps, workspace):
         pr = QKProblem(q.detach() if q is not None else None, k.detach() if k is not None else None, positions, cos, sin,
                        rot_dim=rot_dim, interleaved=interleaved, norm=norm, eps=eps, q_gain=q_gain, k_gain=k_gain,
-                       num_tokens=num_tokens)
+                       num_tokens=num_tokens, workspace=workspace)
         if num_tokens is not None:   # rows behind the batch are written by nobody
             for t in (pr.q_out, pr.k_out):
                 if t is not None:
@@ -266,19 +269,23 @@ class QKNormRopeFunction(torch.autograd.Function):
                 if t is not None:
                     t.zero_()
         pr.backward()
-        return (pr.dq, pr.dk, pr.d_q_gain, pr.d_k_gain) + (None,) * 8
+        return (pr.dq, pr.dk, pr.d_q_gain, pr.d_k_gain) + (None,) * 9
 
 
 def hstu_qk_norm_rope(q, k, positions=None, cos=None, sin=None, *, q_gain=None, k_gain=None, norm: bool = True,
-                      eps: float = 1e-6, rot_dim: Optional[int] = None, interleaved: bool = False, num_tokens=None):
+                      eps: float = 1e-6, rot_dim: Optional[int] = None, interleaved: bool = False, num_tokens=None,
+                      workspace=None):
     """Differentiable norm and rotation of q [T, Hq, d] and k [T, Hk, d]
     (either may be None): returns (q', k') for hstu_attention.  cos, sin:
     rope_tables; positions: jagged_positions, cached_positions, or any int32
     [T] below max_position.  num_tokens: one int64 on the device, tokens in use of a
-    padded batch (rows behind it come back as zeros).  There is no second
-    derivative.  Into a CUDA graph goes QKProblem's forward and backward, rather
+    padded batch (rows behind it come back as zeros).  A position outside the
+    tables raises nothing here: the device records it in the forward's
+    workspace.  Give one to look (256 zeroed bytes, uint8, 256-byte aligned;
+    device_error(device, workspace) != 0), or use QKProblem, which keeps its
+    own.  There is no second derivative.  Into a CUDA graph goes QKProblem's forward and backward, rather
     than autograd's."""
     if rot_dim is None:
         rot_dim = 0 if cos is None else 2 * cos.shape[1]
     return QKNormRopeFunction.apply(q, k, q_gain, k_gain, positions, cos, sin, num_tokens, int(rot_dim), bool(interleaved),
-                                    bool(norm), float(eps))
+                                    bool(norm), float(eps), workspace)
