@@ -4,9 +4,10 @@
 // Append: the BF16 rows it reads and the packed ones it writes (2 d bytes in,
 // 9 d / 16 out) would bound it, but coding a feature takes more instructions than
 // that leaves room for: 161,000 tokens of four heads of 128, normed and rotated,
-// take 215 us (2.0 TB/s; 63 us at the rate of a copy), 1,050 warp instructions a
-// token at 2.6 a cycle.  Keys that go in as they are take 154 us; more loads in
-// flight (through shared memory) or more warps (80 registers) took longer.  The
+// take 220 us (2.0 TB/s; 63 us at the rate of a copy), 1,084 warp instructions a
+// token at 2.6 a cycle: issue slots are busy 63% of the time, with the 20 warps an
+// SM that 96 registers leave.  Keys that go in as they are take 134 us; more loads
+// in flight (through shared memory) or more warps (80 registers) took longer.  The
 // read is bound by what it writes: 74 us, 5.8 TB/s.
 //
 // d / 8 lanes hold a row (hstu_rows.cuh: both features
@@ -14,14 +15,15 @@
 // passes of 256 features side by side, all loads first.  A warp walks
 // tokens_per_warp neighbouring tokens, so that the sequence and the page are
 // looked up once for them (in a small batch each warp has one token: there the
-// chain of lookups is the time): one token a warp 64 tokens 9.9 us (single call),
-// 161,000 tokens 252, four 18.1 and 219; reading 6.8 and 124, 8.8 and 75.  A
-// group's maximum goes over the 2 or 4 lanes that share it.
+// chain of lookups is the time; both sides at tokens_per_warp).  A group's
+// maximum goes over the 2 or 4 lanes that share it.
 //
 // Roundings are decided as on real numbers.  A value x that is exact in FP32
 // (a BF16 input) meets a border only exactly: its quotient by the scale (4
-// significant bits) lies at least 2^-13 from a border or on it, so the
-// quotient by the reciprocal, rounded to 16 significant bits, decides rightly.
+// significant bits) lies on a border or more than 2^-8 of it away, since x is at
+// most 255 units and a border times a scale fewer than 128, of the same or a
+// coarser unit.  So the quotient by the reciprocal, rounded to 16 significant
+// bits, decides rightly.
 // A normed or rotated key is known to 2^-20 of its terms only; where the
 // codes (or the scale) of x - d and x + d differ, the warp computes its rows
 // again as sums of two FP32 numbers, good to 2^-44, and compares with the
@@ -88,7 +90,7 @@ __device__ __forceinline__ float inverse(float s) {
 // 8 features that are exact in FP32, top the largest magnitude of their group:
 // codes (32 bits) and the scale's byte.
 __device__ __forceinline__ uint2 encode_exact(const Row8& x, float top) {
-  const float want = snap(top * 0.16666667f);                 // a border lies 2^-14 away, or is met
+  const float want = snap(top * 0.16666667f);                 // a border is met, or more than 2^-8 of it away
   const uint32_t scale = e4m3_of(top == top ? want : top);    // a NaN stays one
   const float inv = inverse(e4m3_float(scale));
   uint32_t codes = 0;
@@ -615,7 +617,12 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// several tokens a warp once every warp the GPU holds has one (measured at the top)
+// One token a warp in a small batch, else four.  Eight sequences, four heads of
+// 128, one call after the other, by tokens, one and four a warp: append 1,000 6.8
+// and 13.7 us, 4,000 11.1 and 14.6, 7,300 15.4 and 18.4, 12,000 21.4 and 22.3,
+// 24,000 38.6 and 36.3, 48,000 76 and 68; read 1,000 3.2 and 3.7, 4,000 3.8 and
+// 4.0, 7,300 5.5 and 4.6, 12,000 7.9 and 5.9, 48,000 37 and 25.  The switch lies
+// between the read's (5,000) and the append's (some 20,000).
 int tokens_per_warp(int64_t T) { return T > 152 * 48 ? kManyTokens : 1; }
 
 int page_log(int page_size) { return page_size == 32 ? 5 : (page_size == 64 ? 6 : 7); }

@@ -74,7 +74,7 @@ __device__ __forceinline__ bool load_seq(const CachedParams& p, int b, CachedSeq
 // others after 30), by costs 52.6.  In halves of a far tile's cost: sums over 12
 // batches of first passes of 100 to 6,000 rows (128 rows a block) 4: 955 us, 5:
 // 925, 6: 887, 7: 893, 8: 905; 32 users' new rows and candidates (32 rows a block)
-// 5: 19.2 us, 6: 20.1.
+// 5: 19.2 us, 6: 20.1; 12 batches of up to 64 rows (64 rows a block) 5: 247.8, 6: 248.2.
 constexpr int kFarCost = 2, kMostTileCost = 6;
 __device__ __forceinline__ int near_cost(int N) { return N == 128 ? 6 : 5; }
 
