@@ -283,8 +283,8 @@ def hstu_qk_norm_rope(q, k, positions=None, cos=None, sin=None, *, q_gain=None, 
     tables raises nothing here: the device records it in the forward's
     workspace.  Give one to look (256 zeroed bytes, uint8, 256-byte aligned;
     device_error(device, workspace) != 0), or use QKProblem, which keeps its
-    own.  There is no second derivative.  Into a CUDA graph goes QKProblem's forward and backward, rather
-    than autograd's."""
+    own.  There is no second derivative.  Into a CUDA graph goes QKProblem's
+    forward and backward, rather than autograd's."""
     if rot_dim is None:
         rot_dim = 0 if cos is None else 2 * cos.shape[1]
     return QKNormRopeFunction.apply(q, k, q_gain, k_gain, positions, cos, sin, num_tokens, int(rot_dim), bool(interleaved),

@@ -513,7 +513,8 @@ hstu_status_t hstu_qk_norm_rope_bwd(const hstu_qk_desc* desc, const hstu_qk_bwd_
  * are.  Inconsistent offsets or lengths and page numbers outside the cache
  * are found on the device (HSTU_ERR_DEVICE_CHECK); nothing outside the given
  * buffers is touched then.  An append or a read leaves out the tokens that
- * have no place (or no row of the tables) and does all others.
+ * have no place (or no row of the tables) and does all others, unless the
+ * offsets do not fit the rows: then it does nothing.
  * ------------------------------------------------------------------------ */
 typedef struct {
   uint32_t struct_size;      /* sizeof(hstu_cache_desc) */
