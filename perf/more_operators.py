@@ -354,8 +354,8 @@ def run(s):
         out["copy"] = s["copy"]
     if c["bits"] == 8:
         if "read" not in s:
-            s["read"] = [(s["m16"][at:at + n], s["v16"][at:at + n]) for at, n in s["where"]]
-        h.read_moments(s["read"])
+            s["read"] = h.reader([(s["m16"][at:at + n], s["v16"][at:at + n]) for at, n in s["where"]])
+        s["read"].run()
         out.update(m=s["m16"], v=s["v16"])
     return out
 
