@@ -114,12 +114,61 @@ class hstu_attn_cached_args(ctypes.Structure):
                             "rab_time", "q", "k", "v", "u", "o", "y")]
 
 
+class hstu_ln_desc(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32)] + [(n, _i32) for n in ("x_dtype", "y_dtype", "D")] + \
+        [("eps", ctypes.c_float), ("reserved", ctypes.c_uint32)] + \
+        [(n, _i64) for n in ("rows", "x_stride", "y_stride", "dx_stride", "dres_stride")]
+
+
+class hstu_ln_fwd_args(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("num_rows", "x", "weight", "bias", "y", "mean", "rstd")]
+
+
+class hstu_ln_bwd_args(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("num_rows", "x", "weight", "mean", "rstd", "dy", "dres", "dx", "d_weight", "d_bias")]
+
+
+class hstu_group_desc(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32)] + [(n, _i32) for n in ("groups", "K", "N", "y_dtype", "dx_dtype")] + \
+        [("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)] + \
+        [(n, _i64) for n in ("rows", "x_stride", "y_stride", "dx_stride")]
+
+
+class hstu_group_fwd_args(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("group_offsets", "x", "w", "y")]
+
+
+class hstu_group_bwd_args(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("group_offsets", "x", "w", "dy", "dx", "dw")]
+
+
+class hstu_adamw_desc(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32)] + [(n, _i32) for n in ("state_bits", "grad_dtype", "num_tensors")] + \
+        [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps")] + \
+        [("seed", ctypes.c_uint64), ("steps_done", _i64), ("chunks", _i64)]
+
+
+class hstu_adamw_tensor(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("param", "grad", "copy", "m", "v", "m_exp", "v_exp")] + \
+        [("n", _i64), ("weight_decay", ctypes.c_float), ("lr_scale", ctypes.c_float)]
+
+
+class hstu_adamw_step_args(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("lr", "grad_scale", "skip")]
+
+
+class hstu_adamw_moments(ctypes.Structure):
+    _fields_ = [("m", _vp), ("v", _vp)]
+
+
 EXPORTED = ("hstu_attn_workspace_size", "hstu_attn_fwd", "hstu_attn_bwd", "hstu_attn_debug_plan",
             "hstu_get_device_error", "hstu_status_string", "hstu_last_launch_count",
             "hstu_time_next_attention_kernel", "hstu_last_error_detail", "hstu_attn_fwd_noalloc",
             "hstu_layer_workspace_size", "hstu_layer_fwd", "hstu_layer_bwd", "hstu_attn_fwd_delta",
             "hstu_qk_workspace_size", "hstu_qk_norm_rope_fwd", "hstu_qk_norm_rope_bwd", "hstu_cache_bytes",
-            "hstu_cache_append", "hstu_cache_read", "hstu_attn_cached_workspace_size", "hstu_attn_fwd_cached")
+            "hstu_cache_append", "hstu_cache_read", "hstu_attn_cached_workspace_size", "hstu_attn_fwd_cached",
+            "hstu_ln_workspace_size", "hstu_ln_fwd", "hstu_ln_bwd", "hstu_group_workspace_size", "hstu_group_fwd", "hstu_group_bwd", "hstu_adamw_workspace_size",
+            "hstu_adamw_init", "hstu_adamw_step", "hstu_adamw_read_init", "hstu_adamw_read", "hstu_adamw_steps")
 
 _lib = None
 
@@ -165,11 +214,26 @@ def load(build_if_missing: bool = True):
     L.hstu_cache_read.argtypes = [P(hstu_cache_desc), P(hstu_cache_read_args), _vp, sz, _vp]
     L.hstu_attn_cached_workspace_size.argtypes = [P(hstu_attn_desc), P(hstu_cache_desc), ctypes.c_int32, size_p]
     L.hstu_attn_fwd_cached.argtypes = [P(hstu_attn_desc), P(hstu_cache_desc), P(hstu_attn_cached_args), _vp, sz, _vp]
+    L.hstu_ln_workspace_size.argtypes = [P(hstu_ln_desc), size_p, size_p]
+    L.hstu_ln_fwd.argtypes = [P(hstu_ln_desc), P(hstu_ln_fwd_args), _vp, sz, _vp]
+    L.hstu_ln_bwd.argtypes = [P(hstu_ln_desc), P(hstu_ln_bwd_args), _vp, sz, _vp]
+    L.hstu_group_workspace_size.argtypes = [P(hstu_group_desc), size_p, size_p]
+    L.hstu_group_fwd.argtypes = [P(hstu_group_desc), P(hstu_group_fwd_args), _vp, sz, _vp]
+    L.hstu_group_bwd.argtypes = [P(hstu_group_desc), P(hstu_group_bwd_args), _vp, sz, _vp]
+    tensors = P(hstu_adamw_tensor)
+    L.hstu_adamw_workspace_size.argtypes = [P(hstu_adamw_desc), tensors, size_p]
+    L.hstu_adamw_init.argtypes = [P(hstu_adamw_desc), tensors, _vp, sz, _vp]
+    L.hstu_adamw_step.argtypes = [P(hstu_adamw_desc), P(hstu_adamw_step_args), _vp, sz, _vp]
+    L.hstu_adamw_read_init.argtypes = [P(hstu_adamw_desc), tensors, P(hstu_adamw_moments), _i32, _vp, sz, _vp]
+    L.hstu_adamw_read.argtypes = [P(hstu_adamw_desc), _vp, sz, _vp]
+    L.hstu_adamw_steps.argtypes = [_vp, _vp, P(_i64)]
     for name in ("hstu_attn_workspace_size", "hstu_attn_fwd", "hstu_attn_bwd", "hstu_attn_debug_plan",
                  "hstu_get_device_error", "hstu_layer_workspace_size", "hstu_layer_fwd", "hstu_layer_bwd",
                  "hstu_attn_fwd_delta", "hstu_qk_workspace_size", "hstu_qk_norm_rope_fwd", "hstu_qk_norm_rope_bwd",
                  "hstu_cache_bytes", "hstu_cache_append", "hstu_cache_read", "hstu_attn_cached_workspace_size",
-                 "hstu_attn_fwd_cached"):
+                 "hstu_attn_fwd_cached", "hstu_ln_workspace_size", "hstu_ln_fwd", "hstu_ln_bwd",
+                 "hstu_group_workspace_size", "hstu_group_fwd", "hstu_group_bwd", "hstu_adamw_workspace_size",
+                 "hstu_adamw_init", "hstu_adamw_step", "hstu_adamw_read_init", "hstu_adamw_read", "hstu_adamw_steps"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -312,6 +376,67 @@ def hstu_attn_cached_workspace_size(desc, cache, max_rows: int) -> int:
 def hstu_attn_fwd_cached(desc, cache, args, workspace: int, workspace_bytes: int, stream: int):
     _check(load().hstu_attn_fwd_cached(ctypes.byref(desc), ctypes.byref(cache), ctypes.byref(args), workspace,
                                        workspace_bytes, stream), "hstu_attn_fwd_cached")
+
+
+def hstu_ln_workspace_size(desc):
+    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(load().hstu_ln_workspace_size(ctypes.byref(desc), ctypes.byref(f), ctypes.byref(b)), "hstu_ln_workspace_size")
+    return int(f.value), int(b.value)
+
+
+def hstu_ln_fwd(desc, args, workspace: int, workspace_bytes: int, stream: int):
+    _check(load().hstu_ln_fwd(ctypes.byref(desc), ctypes.byref(args), workspace, workspace_bytes, stream), "hstu_ln_fwd")
+
+
+def hstu_ln_bwd(desc, args, workspace: int, workspace_bytes: int, stream: int):
+    _check(load().hstu_ln_bwd(ctypes.byref(desc), ctypes.byref(args), workspace, workspace_bytes, stream), "hstu_ln_bwd")
+
+
+def hstu_group_workspace_size(desc):
+    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(load().hstu_group_workspace_size(ctypes.byref(desc), ctypes.byref(f), ctypes.byref(b)),
+           "hstu_group_workspace_size")
+    return int(f.value), int(b.value)
+
+
+def hstu_group_fwd(desc, args, workspace: int, workspace_bytes: int, stream: int):
+    _check(load().hstu_group_fwd(ctypes.byref(desc), ctypes.byref(args), workspace, workspace_bytes, stream),
+           "hstu_group_fwd")
+
+
+def hstu_group_bwd(desc, args, workspace: int, workspace_bytes: int, stream: int):
+    _check(load().hstu_group_bwd(ctypes.byref(desc), ctypes.byref(args), workspace, workspace_bytes, stream),
+           "hstu_group_bwd")
+
+
+def hstu_adamw_workspace_size(desc, tensors) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().hstu_adamw_workspace_size(ctypes.byref(desc), tensors, ctypes.byref(n)), "hstu_adamw_workspace_size")
+    return int(n.value)
+
+
+def hstu_adamw_init(desc, tensors, workspace: int, workspace_bytes: int, stream: int):
+    _check(load().hstu_adamw_init(ctypes.byref(desc), tensors, workspace, workspace_bytes, stream), "hstu_adamw_init")
+
+
+def hstu_adamw_step(desc, args, workspace: int, workspace_bytes: int, stream: int):
+    _check(load().hstu_adamw_step(ctypes.byref(desc), ctypes.byref(args), workspace, workspace_bytes, stream),
+           "hstu_adamw_step")
+
+
+def hstu_adamw_read_init(desc, tensors, outs, out_dtype: int, workspace: int, workspace_bytes: int, stream: int):
+    _check(load().hstu_adamw_read_init(ctypes.byref(desc), tensors, outs, out_dtype, workspace, workspace_bytes, stream),
+           "hstu_adamw_read_init")
+
+
+def hstu_adamw_read(desc, workspace: int, workspace_bytes: int, stream: int):
+    _check(load().hstu_adamw_read(ctypes.byref(desc), workspace, workspace_bytes, stream), "hstu_adamw_read")
+
+
+def hstu_adamw_steps(workspace: int, stream: int) -> int:
+    n = ctypes.c_int64(0)
+    _check(load().hstu_adamw_steps(workspace, stream, ctypes.byref(n)), "hstu_adamw_steps")
+    return int(n.value)
 
 
 def hstu_get_device_error(workspace: int, stream: int) -> int:

@@ -625,6 +625,224 @@ hstu_status_t hstu_attn_fwd_cached(const hstu_attn_desc* desc, const hstu_cache_
                                    const hstu_attn_cached_args* args, void* workspace, size_t workspace_bytes,
                                    hstu_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Layer norm over the D features of a row, with weight and bias, and its
+ * backward (what the input of a projection goes through; the attention's own
+ * norm-gate has neither weight nor bias):
+ *
+ *   mean = mean(x);  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ *   y = (x - mean) rstd weight + bias
+ * Backward, with h = (x - mean) rstd and e = dy weight:
+ *   dx = rstd (e - mean(e) - h mean(e h)) [+ dres]
+ *   d_weight = sum over rows of dy h;   d_bias = sum over rows of dy
+ *
+ * x (and dx, dres) and y (or dy) are BF16 or FP32 each on its own; weight,
+ * bias, the statistics and their gradients are FP32.  Sums and products are
+ * FP32, each output is rounded once.  Rows are strided: features contiguous,
+ * rows any number of elements apart (rows that are 16-byte aligned with D a
+ * multiple of 8 take wide loads).  1 <= D <= 16384.  An output may be an input
+ * of the same type (same pointer and stride); other overlaps are the
+ * caller's error.  d_weight and d_bias are summed in an order that depends on
+ * the sizes only: equal inputs give equal bits.
+ *
+ * The workspace (256-byte aligned) starts with a 256-byte header that must be
+ * zero before its first use; an error found on the device (num_rows outside
+ * [0, rows]: HSTU_ERR_DEVICE_CHECK, no row is taken) stays in it until the
+ * caller zeroes it.  Calls that overlap in time need workspaces of their own.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  uint32_t struct_size;      /* sizeof(hstu_ln_desc) */
+  int32_t x_dtype;           /* of x, dx, dres */
+  int32_t y_dtype;           /* of y (forward), dy (backward) */
+  int32_t D;
+  float eps;
+  uint32_t reserved;         /* must be 0 */
+  int64_t rows;
+  int64_t x_stride;          /* elements from row to row */
+  int64_t y_stride;          /* of y, or of dy */
+  int64_t dx_stride;         /* backward only */
+  int64_t dres_stride;       /* backward with dres only */
+} hstu_ln_desc;
+
+typedef struct {
+  const int64_t* num_rows;   /* device: rows to work on, <= rows; rows behind them are left as they are and
+                                do not count.  NULL: all */
+  const void* x;             /* [rows, D] strided */
+  const float* weight;       /* [D] or NULL (ones) */
+  const float* bias;         /* [D] or NULL (zeros) */
+  void* y;                   /* out [rows, D] strided */
+  float* mean;               /* out [rows] or NULL */
+  float* rstd;               /* out [rows] or NULL */
+} hstu_ln_fwd_args;
+
+typedef struct {
+  const int64_t* num_rows;
+  const void* x;
+  const float* weight;
+  const float* mean;         /* the forward's */
+  const float* rstd;
+  const void* dy;            /* [rows, D] strided */
+  const void* dres;          /* [rows, D] strided, added to dx, or NULL */
+  void* dx;                  /* out [rows, D] strided */
+  float* d_weight;           /* out [D] or NULL (not wanted) */
+  float* d_bias;             /* out [D] or NULL */
+} hstu_ln_bwd_args;
+
+hstu_status_t hstu_ln_workspace_size(const hstu_ln_desc* desc, size_t* fwd_bytes, size_t* bwd_bytes);
+hstu_status_t hstu_ln_fwd(const hstu_ln_desc* desc, const hstu_ln_fwd_args* args, void* workspace,
+                          size_t workspace_bytes, hstu_stream_t stream);
+hstu_status_t hstu_ln_bwd(const hstu_ln_desc* desc, const hstu_ln_bwd_args* args, void* workspace,
+                          size_t workspace_bytes, hstu_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Products of ragged groups of rows, each with a weight matrix of its own (a
+ * projection per kind of token, scenario or expert), and their gradients:
+ *
+ *   y[r]  = x[r] W[g]                       for the rows r of group g
+ *   dx[r] = dy[r] W[g]^T
+ *   dW[g] = sum over its rows of x[r]^T dy[r]   (zero for a group without rows)
+ *
+ * Rows lie in the order of their groups: group g has rows
+ * [group_offsets[g], group_offsets[g + 1]), offsets on the device, from 0 on,
+ * not decreasing, the last one at most `rows`.  Rows behind the last group
+ * are left as they are and not read into any result.  x, W, dy are BF16, sums FP32 on the tensor cores; y and dx
+ * are rounded once to their type, dW is FP32.  K and N are multiples of 8, rows
+ * a multiple of 16 bytes apart (any row stride that is a multiple of 8
+ * elements); W and dW are dense [groups][K][N].  Up to 4096 groups.  Equal
+ * inputs give equal bits.
+ *
+ * The workspace (256-byte aligned) starts with a 256-byte header that must be
+ * zero before its first use.  Offsets that break the rules above
+ * (HSTU_ERR_DEVICE_CHECK: nothing is computed) and a pipeline wait that ran
+ * out (HSTU_ERR_TIMEOUT) stay in it until the caller zeroes it.  Calls that
+ * overlap in time need workspaces of their own.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  uint32_t struct_size;      /* sizeof(hstu_group_desc) */
+  int32_t groups;            /* 1 .. 4096 */
+  int32_t K, N;
+  int32_t y_dtype;           /* of y: HSTU_BF16 or HSTU_FP32 */
+  int32_t dx_dtype;          /* of dx */
+  uint32_t flags;            /* 0, or HSTU_FLAG_TEST_TIMEOUT: the first load is withheld and waits give up
+                                after about a millisecond */
+  uint32_t reserved;         /* must be 0 */
+  int64_t rows;              /* T */
+  int64_t x_stride;          /* elements from row to row, multiples of 8 */
+  int64_t y_stride;          /* of y (forward) and dy (backward) */
+  int64_t dx_stride;         /* backward only */
+} hstu_group_desc;
+
+typedef struct {
+  const int64_t* group_offsets; /* [groups + 1] */
+  const void* x;             /* [T, K] strided, BF16 */
+  const void* w;             /* [groups, K, N] BF16 */
+  void* y;                   /* out [T, N] strided */
+} hstu_group_fwd_args;
+
+typedef struct {
+  const int64_t* group_offsets;
+  const void* x;             /* for dw */
+  const void* w;             /* for dx */
+  const void* dy;            /* [T, N] strided, BF16 */
+  void* dx;                  /* out [T, K] strided, or NULL (not wanted) */
+  float* dw;                 /* out [groups, K, N], or NULL (not wanted) */
+} hstu_group_bwd_args;
+
+hstu_status_t hstu_group_workspace_size(const hstu_group_desc* desc, size_t* fwd_bytes, size_t* bwd_bytes);
+hstu_status_t hstu_group_fwd(const hstu_group_desc* desc, const hstu_group_fwd_args* args, void* workspace,
+                             size_t workspace_bytes, hstu_stream_t stream);
+hstu_status_t hstu_group_bwd(const hstu_group_desc* desc, const hstu_group_bwd_args* args, void* workspace,
+                             size_t workspace_bytes, hstu_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * An AdamW step over many tensors in one launch:
+ *
+ *   g = grad grad_scale
+ *   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr' wd) - lr' / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ *
+ * with t the step (counted on the device, from steps_done + 1 on) and
+ * lr' = lr times the tensor's lr_scale.  Parameters are FP32; a tensor may
+ * have a BF16 copy (the projections' operands), which is written with the
+ * rounded new value.  Gradients are FP32 or BF16.  FP32 arithmetic; m and v
+ * are computed product by product without contraction.
+ *
+ * state_bits 32: m and v are FP32.  state_bits 8: 256 neighbouring elements of
+ * a tensor form a block with one byte E a moment, the FP32 exponent field of
+ * its largest finite magnitude, at least 16.  m is a sign, 4 exponent bits (bias 7) and 3
+ * of mantissa, times 2^(E - 134); v is 5 exponent bits (bias 15) and 3 of
+ * mantissa, times 2^(E - 142).  The parameters take the new moments before
+ * they are rounded.  Rounding is up or down at random, so that means are kept
+ * (rounding to the nearest would leave v as it is for ever: a step's decay of a
+ * thousandth is far below half a step of 3 bits): the magnitude's 20 bits
+ * that fall away get 16 r + 8 added, r 16 random bits.  Element e of the
+ * blocks (all blocks counted through the tensors in their order) takes word e mod 4 of Philox4x32-10
+ * (Salmon, Moraes, Dror, Shaw, SC 2011) at counter (e div 4, t), key seed;
+ * its low half serves m, the high half v.  A new m that is not finite is kept as
+ * NaN (code 127), such a v as the largest value.
+ *
+ * hstu_adamw_init checks the tensors (host array), lays out the workspace (256-byte aligned)
+ * and synchronises the stream; a stream that is being captured is refused
+ * (HSTU_ERR_INVALID_ARG).  hstu_adamw_step launches one kernel and may be captured: each
+ * replay is a step.  A descriptor that is not the one the workspace was laid out
+ * for is found on the device (HSTU_ERR_DEVICE_CHECK, nothing is written).  lr and grad_scale on the device, where given, are read at
+ * every step in place of the descriptor's lr (and of one).  skip, where given, is
+ * read at every step: not zero, nothing changes and the step does not count (a
+ * batch whose gradients overflowed).
+ * hstu_adamw_read writes the tensors' moments as FP32 or BF16 values (8-bit
+ * moments are exact in either, but for what BF16 and FP32 call subnormal):
+ * hstu_adamw_read_init lays out a workspace of its own for it.
+ *
+ * Tensors must not overlap.  Pointers are 16-byte aligned (8-bit codes 4,
+ * BF16 8; exponent bytes any).  One call at a time on a workspace.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  uint32_t struct_size;      /* sizeof(hstu_adamw_desc) */
+  int32_t state_bits;        /* 32 or 8 */
+  int32_t grad_dtype;        /* HSTU_BF16 or HSTU_FP32 */
+  int32_t num_tensors;       /* >= 0 */
+  double lr, beta1, beta2, eps;
+  uint64_t seed;             /* of the 8-bit moments' rounding */
+  int64_t steps_done;        /* init: steps taken before; -1: what the workspace has counted is kept */
+  int64_t chunks;            /* set by init (read_init): the length of the workspace's list */
+} hstu_adamw_desc;
+
+typedef struct {
+  float* param;              /* [n] */
+  const void* grad;          /* [n], or NULL: this tensor is left as it is */
+  void* copy;                /* [n] BF16, or NULL */
+  void* m;                   /* [n] FP32, or uint8 codes */
+  void* v;
+  uint8_t* m_exp;            /* [ceil(n / 256)], 8 bits only */
+  uint8_t* v_exp;
+  int64_t n;                 /* elements, >= 0 */
+  float weight_decay;
+  float lr_scale;
+} hstu_adamw_tensor;
+
+typedef struct {
+  const float* lr;           /* device, or NULL: desc->lr */
+  const float* grad_scale;   /* device, or NULL: 1 */
+  const int32_t* skip;       /* device, or NULL: 0 */
+} hstu_adamw_step_args;
+
+typedef struct {
+  void* m;                   /* out [n], or NULL (not wanted); 16-byte aligned */
+  void* v;
+} hstu_adamw_moments;
+
+hstu_status_t hstu_adamw_workspace_size(const hstu_adamw_desc* desc, const hstu_adamw_tensor* tensors, size_t* bytes);
+hstu_status_t hstu_adamw_init(hstu_adamw_desc* desc, const hstu_adamw_tensor* tensors, void* workspace,
+                              size_t workspace_bytes, hstu_stream_t stream);
+hstu_status_t hstu_adamw_step(const hstu_adamw_desc* desc, const hstu_adamw_step_args* args, void* workspace,
+                              size_t workspace_bytes, hstu_stream_t stream);
+hstu_status_t hstu_adamw_read_init(hstu_adamw_desc* desc, const hstu_adamw_tensor* tensors,
+                                   const hstu_adamw_moments* outs, int32_t out_dtype, void* workspace,
+                                   size_t workspace_bytes, hstu_stream_t stream);
+hstu_status_t hstu_adamw_read(const hstu_adamw_desc* desc, void* workspace, size_t workspace_bytes, hstu_stream_t stream);
+/* Steps counted on this workspace (steps_done included).  Synchronises the stream. */
+hstu_status_t hstu_adamw_steps(const void* workspace, hstu_stream_t stream, int64_t* steps);
+
 /* Reads the device error word of the last call that used this workspace
  * (HSTU_OK when none).  Synchronises the stream. */
 hstu_status_t hstu_get_device_error(const void* workspace, hstu_stream_t stream, int32_t* code);
@@ -640,8 +858,8 @@ const char* hstu_status_string(hstu_status_t status);
 const char* hstu_last_error_detail(void);
 
 /* Number of this library's kernels that the last successful hstu_attn_fwd,
- * hstu_attn_bwd, hstu_attn_fwd_delta, hstu_layer_*, hstu_qk_* or hstu_cache_*
- * or hstu_attn_fwd_cached call on this thread launched (for launch accounting; cuBLAS's kernels inside
+ * hstu_attn_bwd, hstu_attn_fwd_delta, hstu_layer_*, hstu_qk_*, hstu_cache_*,
+ * hstu_attn_fwd_cached, hstu_ln_*, hstu_group_* or hstu_adamw_* call on this thread launched (for launch accounting; cuBLAS's kernels inside
  * the layer calls are not counted). */
 int32_t hstu_last_launch_count(void);
 
