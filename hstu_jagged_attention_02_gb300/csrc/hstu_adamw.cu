@@ -10,8 +10,11 @@
 // the warp.  Decoding and encoding work on the bits of FP32 numbers: a code shifted
 // by 20 is the bit pattern of its value times a power of two (the small codes those of
 // subnormal numbers), so rounding up or down at random is one integer addition below the cut.
+#include <cuda_fp16.h>
 #include <stdlib.h>
 #include <string.h>
+
+#include <type_traits>
 
 #include "hstu_internal.h"
 
@@ -20,11 +23,11 @@ namespace hstu {
 namespace {
 
 constexpr int kBlock = 256;     // elements that share an exponent byte
-constexpr int kChunk = 2048;
-constexpr int kAdamThreads = kChunk / 8;
+constexpr int kMaxChunk = 2048; // of a chunk, a power of two from kBlock on
+constexpr int kAdamThreads = 256;
 constexpr int kMOff = 134, kVOff = 142, kLeastExp = 16;
 
-// What the header of the workspace holds behind the error words (64 bytes on).
+// What the header of the workspace holds behind the error words.
 struct AdamState {
   double pow1, pow2;    // beta^t of the next step
   int64_t steps;        // steps counted
@@ -32,7 +35,7 @@ struct AdamState {
   int32_t kind;         // state_bits, grad_dtype: what the list was made for
   float c1, c2;         // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t) of the next step
 };
-constexpr size_t kStateOff = 64;
+constexpr size_t kStateOff = 128;   // another line than the counter of CTAs
 
 struct __align__(16) AdamChunk {
   float* p;
@@ -43,7 +46,7 @@ struct __align__(16) AdamChunk {
   uint8_t* me;
   uint8_t* ve;
   int64_t quad0;        // groups of 4 elements before this chunk, all tensors
-  int32_t n;            // elements, <= kChunk
+  int32_t n;            // elements, <= kMaxChunk
   float wd, lr_scale;
   int32_t pad;
 };
@@ -149,24 +152,34 @@ __device__ __forceinline__ void put4(uint8_t* at, int live, uint32_t x) {
   }
 }
 
-// Values of 4 codes of a block with exponent byte e.  m: sign, 4 and 3 bits, 127 a NaN; v: 5 and 3 bits.
-__device__ __forceinline__ void decode_m(uint32_t codes, int e, float (&v)[4]) {
-  const float unit = pow2f(e - kMOff);
+// A sum of pairs behind products, which must not become a fused product and sum (as the paired sum does,
+// whatever its rounding mode says).
+__device__ __forceinline__ float2 sum2(float2 x, float2 y) { return make_float2(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y)); }
+
+// Values of 4 codes of a block, unit its power of two.  m: e4m3 by the conversion to FP16 (127 a NaN);
+// v: a code 20 bits up is the bit pattern of its value times 2^-112.
+__device__ __forceinline__ void decode_m(uint32_t codes, float unit, float2 (&v)[2]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t c = codes >> (8 * i);
-    const float x = __uint_as_float((c & 127u) << 20) * 0x1p120f * unit;
-    const float y = (c & 127u) == 127u ? __int_as_float(0x7fffffff) : x;
-    v[i] = __uint_as_float(__float_as_uint(y) | (c & 128u) << 24);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t x;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(x) : "r"(codes >> (16 * h)));
+    v[h] = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&x)), make_float2(unit, unit));
   }
 }
-__device__ __forceinline__ void decode_v(uint32_t codes, int e, float (&v)[4]) {
-  const float unit = pow2f(e - kVOff);
+__device__ __forceinline__ void decode_v(uint32_t codes, float unit, float2 (&v)[2]) {
+  constexpr uint32_t mask = 255u << 20;
+  const float2 up = make_float2(0x1p112f, 0x1p112f), u = make_float2(unit, unit);
+  v[0] = make_float2(__uint_as_float(codes << 20 & mask), __uint_as_float(codes << 12 & mask));
+  v[1] = make_float2(__uint_as_float(codes << 4 & mask), __uint_as_float(codes >> 4 & mask));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float((codes >> (8 * i) & 255u) << 20) * 0x1p112f * unit;
+  for (int h = 0; h < 2; ++h) v[h] = __fmul2_rn(__fmul2_rn(v[h], up), u);
 }
 
-// |x| rounded up or down by the 20-bit noise; up: 2^(off - e)
+// Noise for the 20 bits that fall away: 16 r + 8, r a word's low half (m) or high half (v).
+__device__ __forceinline__ uint32_t noise_m(uint32_t w) { return (w & 0xffffu) * 16u + 8u; }
+__device__ __forceinline__ uint32_t noise_v(uint32_t w) { return (w >> 16) * 16u + 8u; }
+
+// Code of one value rounded up or down by the noise, whatever the value; up: 2^(off - e).
 __device__ __forceinline__ uint32_t code_m(float x, float up, uint32_t noise) {
   const float a = fabsf(x) * up * 0x1p-120f;
   const uint32_t c = min((__float_as_uint(a) + noise) >> 20, 126u);
@@ -177,27 +190,103 @@ __device__ __forceinline__ uint32_t code_v(float x, float up, uint32_t noise) {
   const uint32_t c = min((__float_as_uint(a) + noise) >> 20, 255u);
   return x < __int_as_float(0x7f800000) ? c : 255u;
 }
-// the exponent byte of a block from this lane's 8 values
-__device__ __forceinline__ int block_exp(const float (&x)[2][4]) {
+// The top bytes of 4 words.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+// The same for 4 values of a block that holds finite numbers only: what is largest lies below 2^8 (m)
+// or 2^16 (v) times the unit, so no code reaches the end of the range, and the sign stays where it is.
+// (bits + 16 r + 8) << 4, as two multiply-adds: the code in the top byte.
+__device__ __forceinline__ uint32_t rounded(float a, uint32_t r, uint32_t& sum) {
+  sum = __float_as_uint(a);
+  asm("" : "+r"(sum));   // nvcc 13.0 loses a shift of the first half of a paired product without this
+  sum = r * 16u + sum;
+  return sum * 16u + 128u;
+}
+__device__ __forceinline__ uint32_t codes_m(const float2 (&x)[2], float up, const uint4& w) {
+  const float2 u = make_float2(up, up), d = make_float2(0x1p-120f, 0x1p-120f);
+  const float2 a = __fmul2_rn(__fmul2_rn(x[0], u), d), b = __fmul2_rn(__fmul2_rn(x[1], u), d);
+  const float f[4] = {a.x, a.y, b.x, b.y};
+  const uint32_t r[4] = {w.x & 0xffffu, w.y & 0xffffu, w.z & 0xffffu, w.w & 0xffffu};
+  uint32_t z[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t sum;
+    z[i] = rounded(f[i], r[i], sum);
+    z[i] = (z[i] & 0x7fffffffu) | (sum & 0x80000000u);
+  }
+  return top_bytes(z[0], z[1], z[2], z[3]);
+}
+__device__ __forceinline__ uint32_t codes_v(const float2 (&x)[2], float up, const uint4& w) {
+  const float2 u = make_float2(up, up), d = make_float2(0x1p-112f, 0x1p-112f);
+  const float2 a = __fmul2_rn(__fmul2_rn(x[0], u), d), b = __fmul2_rn(__fmul2_rn(x[1], u), d);
+  const float f[4] = {a.x, a.y, b.x, b.y};
+  const uint32_t r[4] = {w.x >> 16, w.y >> 16, w.z >> 16, w.w >> 16};
+  uint32_t z[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t sum;
+    z[i] = rounded(f[i], r[i], sum);
+  }
+  return top_bytes(z[0], z[1], z[2], z[3]);
+}
+
+constexpr uint32_t kInfBits = 0x7f800000u;
+// the largest magnitude of a lane's 8 values, a NaN where there is one, as bits
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t top_bits(const float2 (&x)[2][2]) {
+  const float a = max3(fabsf(x[0][0].x), fabsf(x[0][0].y), fabsf(x[0][1].x));
+  const float b = max3(fabsf(x[0][1].y), fabsf(x[1][0].x), fabsf(x[1][0].y));
+  return __float_as_uint(max3(a, b, max3(fabsf(x[1][1].x), fabsf(x[1][1].y), 0.f))) & 0x7fffffffu;
+}
+// the same of the finite ones
+__device__ __forceinline__ uint32_t top_finite_bits(const float2 (&x)[2][2]) {
   uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t b = __float_as_uint(x[j][i]) & 0x7fffffffu;
-      if (b < 0x7f800000u) top = max(top, b);
-    }
-  return max((int)(__reduce_max_sync(0xffffffffu, top) >> 23), kLeastExp);
+  for (int j = 0; j < 4; ++j) {
+    const float2 v = x[j >> 1][j & 1];
+    const uint32_t a = __float_as_uint(v.x) & 0x7fffffffu, b = __float_as_uint(v.y) & 0x7fffffffu;
+    if (a < kInfBits) top = max(top, a);
+    if (b < kInfBits) top = max(top, b);
+  }
+  return top;
 }
+__device__ __forceinline__ int exp_byte(uint32_t top) { return max((int)(top >> 23), kLeastExp); }
 
 __device__ __forceinline__ float sqrt_approx(float x) {
   float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
+__device__ __forceinline__ void pairs(const float (&a)[4], float2 (&b)[2]) {
+  b[0] = make_float2(a[0], a[1]);
+  b[1] = make_float2(a[2], a[3]);
+}
+__device__ __forceinline__ void singles(const float2 (&b)[2], float (&a)[4]) {
+  a[0] = b[0].x; a[1] = b[0].y; a[2] = b[1].x; a[3] = b[1].y;
+}
+
+// A record by its 16-byte parts, the same for all lanes.
+template <typename R>
+__device__ __forceinline__ R get_record(const R* at) {
+  R r;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(R) / 16); ++i) reinterpret_cast<uint4*>(&r)[i] = __ldg(reinterpret_cast<const uint4*>(at) + i);
+  return r;
+}
+
 template <int BITS, typename TG>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamParams p) {
+__global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_constant__ AdamParams p) {
   pdl_wait();
   AdamState* st = reinterpret_cast<AdamState*>(reinterpret_cast<char*>(p.hdr) + kStateOff);
   if (st->chunks != p.chunks || st->kind != p.kind) {
@@ -205,83 +294,127 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
     return;
   }
   if (p.skip && *p.skip != 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x < p.chunks) {
-    const AdamChunk c = p.list[blockIdx.x];
-    const int at0 = warp * kBlock + 4 * lane;
-    if (warp * kBlock < c.n) {
-      const TG* gp = static_cast<const TG*>(c.g);
-      float w[2][4], g[2][4], m[2][4], v[2][4];
+  const int lane = threadIdx.x & 31;
+  const float lr0 = p.lr_at ? *p.lr_at : p.lr, scale = p.scale ? *p.scale : 1.f;
+  const float c1s = st->c1, c2s = st->c2;
+  const uint64_t t = (uint64_t)st->steps + 1;
+  const float2 b1 = make_float2(p.b1, p.b1), a1 = make_float2(p.a1, p.a1), b2 = make_float2(p.b2, p.b2),
+               a2 = make_float2(p.a2, p.a2), eps = make_float2(p.eps, p.eps), c2 = make_float2(c2s, c2s);
+  constexpr int kWarps = kAdamThreads / 32;
+  for (int i = blockIdx.x * kWarps + (threadIdx.x >> 5); i < p.chunks; i += gridDim.x * kWarps) {
+    const AdamChunk c = get_record(p.list + i);
+    int exps = 0;   // lane b: the bytes of block b, m's and v's
+    if (BITS == 8 && lane * kBlock < c.n) exps = c.me[lane] | c.ve[lane] << 8;
+    int new_exps = 0;
+    const float lr = lr0 * c.lr_scale, keep1 = 1.f - lr * c.wd, c1 = -lr * c1s;
+    const float2 keep = make_float2(keep1, keep1), step = make_float2(c1, c1);
+#pragma unroll 1
+    for (int blk = 0; blk * kBlock < c.n; ++blk) {
+      const int at0 = blk * kBlock + 4 * lane;
+      float2 w[2][2], g[2][2], m[2][2], v[2][2];
       uint32_t mc[2], vc[2];
-      int me = 0, ve = 0;
+      auto load = [&](auto FULL) {
+        constexpr bool full = decltype(FULL)::value;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int at = at0 + 128 * j, live = c.n - at;
-        get4(c.p + at, live, w[j]);
-        get4(gp + at, live, g[j]);
-        if constexpr (BITS == 32) {
-          get4(static_cast<const float*>(c.m) + at, live, m[j]);
-          get4(static_cast<const float*>(c.v) + at, live, v[j]);
-        } else {
-          mc[j] = get4(static_cast<const uint8_t*>(c.m) + at, live);
-          vc[j] = get4(static_cast<const uint8_t*>(c.v) + at, live);
+        for (int j = 0; j < 2; ++j) {
+          const int at = at0 + 128 * j, live = full ? 4 : c.n - at;
+          float a[4];
+          get4(c.p + at, live, a); pairs(a, w[j]);
+          get4(static_cast<const TG*>(c.g) + at, live, a); pairs(a, g[j]);
+          if constexpr (BITS == 32) {
+            get4(static_cast<const float*>(c.m) + at, live, a); pairs(a, m[j]);
+            get4(static_cast<const float*>(c.v) + at, live, a); pairs(a, v[j]);
+          } else {
+            mc[j] = get4(static_cast<const uint8_t*>(c.m) + at, live);
+            vc[j] = get4(static_cast<const uint8_t*>(c.v) + at, live);
+          }
         }
-      }
+      };
+      const bool whole = c.n >= (blk + 1) * kBlock;
+      if (whole) load(std::true_type());
+      else load(std::false_type());
+      float um = 0.f, uv = 0.f;
       if constexpr (BITS == 8) {
-        me = c.me[warp];
-        ve = c.ve[warp];
+        const int e = __shfl_sync(0xffffffffu, exps, blk);
+        um = pow2f((e & 255) - kMOff);
+        uv = pow2f((e >> 8) - kVOff);
       }
-      const float lr = (p.lr_at ? *p.lr_at : p.lr) * c.lr_scale, keep = 1.f - lr * c.wd;
-      const float c1 = -lr * st->c1, c2 = st->c2, scale = p.scale ? *p.scale : 1.f;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if constexpr (BITS == 8) {
-          decode_m(mc[j], me, m[j]);
-          decode_v(vc[j], ve, v[j]);
+          decode_m(mc[j], um, m[j]);
+          decode_v(vc[j], uv, v[j]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int h = 0; h < 2; ++h) {
           // products and sums one by one: the codes go by their last bits
-          const float gs = __fmul_rn(g[j][i], scale);
-          m[j][i] = __fadd_rn(__fmul_rn(m[j][i], p.b1), __fmul_rn(gs, p.a1));
-          v[j][i] = __fadd_rn(__fmul_rn(v[j][i], p.b2), __fmul_rn(__fmul_rn(gs, gs), p.a2));
-          const float d = fmaf(sqrt_approx(v[j][i]), c2, p.eps);
-          w[j][i] = fmaf(__fdividef(m[j][i], d), c1, w[j][i] * keep);
+          const float2 gs = __fmul2_rn(g[j][h], make_float2(scale, scale));
+          m[j][h] = sum2(__fmul2_rn(m[j][h], b1), __fmul2_rn(gs, a1));
+          v[j][h] = sum2(__fmul2_rn(v[j][h], b2), __fmul2_rn(__fmul2_rn(gs, gs), a2));
+          const float2 d = __ffma2_rn(make_float2(sqrt_approx(v[j][h].x), sqrt_approx(v[j][h].y)), c2, eps);
+          const float2 u = __fmul2_rn(m[j][h], make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+          w[j][h] = __ffma2_rn(u, step, __fmul2_rn(w[j][h], keep));
         }
       }
+      uint32_t nm[2] = {}, nv[2] = {};
       if constexpr (BITS == 8) {
-        me = block_exp(m);
-        ve = block_exp(v);
-      }
+        uint32_t tm = __reduce_max_sync(0xffffffffu, top_bits(m)), tv = __reduce_max_sync(0xffffffffu, top_bits(v));
+        const bool wild = max(tm, tv) >= kInfBits;   // the same for the whole warp
+        if (wild) {
+          tm = __reduce_max_sync(0xffffffffu, top_finite_bits(m));
+          tv = __reduce_max_sync(0xffffffffu, top_finite_bits(v));
+        }
+        const int me = exp_byte(tm), ve = exp_byte(tv);
+        const float up_m = pow2f(kMOff - me), up_v = pow2f(kVOff - ve);
+        if (lane == blk) new_exps = me | ve << 8;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int at = at0 + 128 * j, live = c.n - at;
-        if (live <= 0) continue;
-        put4(c.p + at, live, w[j]);
-        if (c.copy) put4(c.copy + at, live, w[j]);
-        if constexpr (BITS == 32) {
-          put4(static_cast<float*>(c.m) + at, live, m[j]);
-          put4(static_cast<float*>(c.v) + at, live, v[j]);
-        } else {
-          const uint64_t quad = (uint64_t)c.quad0 + (uint64_t)(at >> 2), t = (uint64_t)st->steps + 1;
-          const uint4 r = philox((uint32_t)quad, (uint32_t)(quad >> 32), (uint32_t)t, (uint32_t)(t >> 32),
-                                 (uint32_t)p.seed, (uint32_t)(p.seed >> 32));
-          const uint32_t word[4] = {r.x, r.y, r.z, r.w};
-          const float up_m = pow2f(kMOff - me), up_v = pow2f(kVOff - ve);
-          uint32_t a = 0, b = 0;
+        for (int j = 0; j < 2; ++j) {
+          const uint64_t quad = (uint64_t)c.quad0 + (uint32_t)((at0 + 128 * j) >> 2);
+          const uint4 r = philox((uint32_t)quad, (uint32_t)(quad >> 32), (uint32_t)t, (uint32_t)(t >> 32), (uint32_t)p.seed,
+                                 (uint32_t)(p.seed >> 32));
+          if (!wild) {
+            nm[j] = codes_m(m[j], up_m, r);
+            nv[j] = codes_v(v[j], up_v, r);
+          } else {
+            float x[4], y[4];
+            singles(m[j], x);
+            singles(v[j], y);
+            const uint32_t word[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            a |= code_m(m[j][i], up_m, ((word[i] & 0xffffu) << 4) + 8) << (8 * i);
-            b |= code_v(v[j][i], up_v, (word[i] >> 16 << 4) + 8) << (8 * i);
+            for (int e = 0; e < 4; ++e) {
+              nm[j] |= code_m(x[e], up_m, noise_m(word[e])) << (8 * e);
+              nv[j] |= code_v(y[e], up_v, noise_v(word[e])) << (8 * e);
+            }
           }
-          put4(static_cast<uint8_t*>(c.m) + at, live, a);
-          put4(static_cast<uint8_t*>(c.v) + at, live, b);
         }
       }
-      if (BITS == 8 && lane == 0) {
-        c.me[warp] = (uint8_t)me;
-        c.ve[warp] = (uint8_t)ve;
-      }
+      auto store = [&](auto FULL) {
+        constexpr bool full = decltype(FULL)::value;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int at = at0 + 128 * j, live = full ? 4 : c.n - at;
+          if (!full && live <= 0) continue;
+          float a[4];
+          singles(w[j], a);
+          put4(c.p + at, live, a);
+          if (c.copy) put4(c.copy + at, live, a);
+          if constexpr (BITS == 32) {
+            singles(m[j], a);
+            put4(static_cast<float*>(c.m) + at, live, a);
+            singles(v[j], a);
+            put4(static_cast<float*>(c.v) + at, live, a);
+          } else {
+            put4(static_cast<uint8_t*>(c.m) + at, live, nm[j]);
+            put4(static_cast<uint8_t*>(c.v) + at, live, nv[j]);
+          }
+        }
+      };
+      if (whole) store(std::true_type());
+      else store(std::false_type());
+    }
+    if (BITS == 8 && lane * kBlock < c.n) {
+      c.me[lane] = (uint8_t)new_exps;
+      c.ve[lane] = (uint8_t)(new_exps >> 8);
     }
   }
   // the CTA that ends last counts the step, when all have read what belongs to it
@@ -299,31 +432,66 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
   }
 }
 
+// A warp takes a chunk, four blocks at a time where it has them: a lane 16 neighbouring elements twice.
 template <int BITS, typename TO>
 __global__ void __launch_bounds__(kAdamThreads)
-adamw_read_kernel(int* hdr, const ReadChunk* __restrict__ list, int64_t chunks, int kind) {
+adamw_read_kernel(int* hdr, const ReadChunk* __restrict__ list, int chunks, int kind) {
   pdl_wait();
   const AdamState* st = reinterpret_cast<const AdamState*>(reinterpret_cast<const char*>(hdr) + kStateOff);
   if (st->chunks != chunks || st->kind != kind) {
     if (blockIdx.x == 0 && threadIdx.x == 0) set_error(hdr, HSTU_ERR_DEVICE_CHECK, -1);
     return;
   }
-  const ReadChunk c = list[blockIdx.x];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  constexpr int kWarps = kAdamThreads / 32;
+  for (int i = blockIdx.x * kWarps + (threadIdx.x >> 5); i < chunks; i += gridDim.x * kWarps) {
+    const ReadChunk c = get_record(list + i);
+    const int n = (int)c.n;
+    int exps = 0;
+    if (BITS == 8 && lane * kBlock < n) exps = c.me[lane] | c.ve[lane] << 8;
+#pragma unroll 1
+    for (int blk = 0; blk * kBlock < n; blk += 2) {
+      uint32_t mc[4], vc[4];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int at = warp * kBlock + 128 * j + 4 * lane, live = (int)c.n - at;
-    if (live <= 0) continue;
-    float m[4], v[4];
-    if constexpr (BITS == 32) {
-      get4(static_cast<const float*>(c.m) + at, live, m);
-      get4(static_cast<const float*>(c.v) + at, live, v);
-    } else {
-      decode_m(get4(static_cast<const uint8_t*>(c.m) + at, live), c.me[warp], m);
-      decode_v(get4(static_cast<const uint8_t*>(c.v) + at, live), c.ve[warp], v);
+      for (int j = 0; j < 4; ++j) {
+        const int at = blk * kBlock + 128 * j + 4 * lane, live = n - at;
+        if constexpr (BITS == 8) {
+          if (c.om) mc[j] = get4(static_cast<const uint8_t*>(c.m) + at, live);
+          if (c.ov) vc[j] = get4(static_cast<const uint8_t*>(c.v) + at, live);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = blk * kBlock + 128 * j + 4 * lane, live = n - at;
+        float um = 0.f, uv = 0.f;
+        if constexpr (BITS == 8) {
+          const int e = __shfl_sync(0xffffffffu, exps, (blk + (j >> 1)) & 31);
+          um = pow2f((e & 255) - kMOff);
+          uv = pow2f((e >> 8) - kVOff);
+        }
+        if (live <= 0) continue;
+        float x[4];
+        float2 y[2];
+        if (c.om) {
+          if constexpr (BITS == 8) {
+            decode_m(mc[j], um, y);
+            singles(y, x);
+          } else {
+            get4(static_cast<const float*>(c.m) + at, live, x);
+          }
+          put4(static_cast<TO*>(c.om) + at, live, x);
+        }
+        if (c.ov) {
+          if constexpr (BITS == 8) {
+            decode_v(vc[j], uv, y);
+            singles(y, x);
+          } else {
+            get4(static_cast<const float*>(c.v) + at, live, x);
+          }
+          put4(static_cast<TO*>(c.ov) + at, live, x);
+        }
+      }
     }
-    if (c.om) put4(static_cast<TO*>(c.om) + at, live, m);
-    if (c.ov) put4(static_cast<TO*>(c.ov) + at, live, v);
   }
 }
 
@@ -337,33 +505,43 @@ hstu_status_t check_desc(const hstu_adamw_desc* d) {
   const double b[2] = {d->beta1, d->beta2};
   for (double x : b)
     if (!(x >= 0.0 && x < 1.0)) return HSTU_ERR_INVALID_ARG;
-  // eps keeps the quotient's divisor a normal FP32 number
-  if (!(d->eps >= 1e-30 && d->eps < 1e30) || !(d->lr >= 0.0 && d->lr < 1e30)) return HSTU_ERR_INVALID_ARG;
+  // from 1e-12 on the square root of a subnormal v counts for nothing beside it
+  if (!(d->eps >= 1e-12 && d->eps < 1e30) || !(d->lr >= 0.0 && d->lr < 1e30)) return HSTU_ERR_INVALID_ARG;
   return HSTU_OK;
+}
+
+// Elements of a chunk: a warp takes one at a time, and every warp of the GPU (4,864) should have three or more, as
+// the last round is short for some.
+int chunk_of(const hstu_adamw_desc* d, const hstu_adamw_tensor* t) {
+  int64_t blocks = 0;
+  for (int i = 0; i < d->num_tensors; ++i) blocks += (t[i].n + kBlock - 1) / kBlock;
+  int chunk = kBlock;
+  while (chunk < kMaxChunk && blocks / (2 * chunk / kBlock) >= 3 * 4864) chunk *= 2;
+  return chunk;
 }
 
 // The tensors' checks, and the chunks of their list.
 hstu_status_t check_tensors(const hstu_adamw_desc* d, const hstu_adamw_tensor* t, bool stepped, int64_t* chunks) {
   if (d->num_tensors > 0 && !t) return HSTU_ERR_INVALID_ARG;
   int64_t total = 0;
-  const size_t code = d->state_bits == 8 ? 4 : 16;
   for (int i = 0; i < d->num_tensors; ++i) {
     const hstu_adamw_tensor& x = t[i];
     if (x.n < 0) return HSTU_ERR_INVALID_ARG;
     if (x.n > ((int64_t)1 << 44)) return HSTU_ERR_UNSUPPORTED;
     if (x.n == 0) continue;
-    if (!x.m || !x.v || !aligned(x.m, code) || !aligned(x.v, code)) return HSTU_ERR_INVALID_ARG;
+    if (!x.m || !x.v || !aligned(x.m, 16) || !aligned(x.v, 16)) return HSTU_ERR_INVALID_ARG;
     if (d->state_bits == 8 && (!x.m_exp || !x.v_exp)) return HSTU_ERR_INVALID_ARG;
     if (stepped) {
       if (!x.param || !aligned(x.param, 16) || !aligned(x.copy, 8)) return HSTU_ERR_INVALID_ARG;
-      if (!aligned(x.grad, d->grad_dtype == HSTU_FP32 ? 16 : 8)) return HSTU_ERR_INVALID_ARG;
+      if (!aligned(x.grad, 16)) return HSTU_ERR_INVALID_ARG;
       if (!(x.weight_decay >= 0.f && x.weight_decay < 1e30f) || !(x.lr_scale >= 0.f && x.lr_scale < 1e30f))
         return HSTU_ERR_INVALID_ARG;
-      if (!x.grad) continue;   // left as it is
     }
-    total += (x.n + kChunk - 1) / kChunk;
   }
-  if (total > 0x7fffffff) return HSTU_ERR_UNSUPPORTED;
+  const int chunk = chunk_of(d, t);
+  for (int i = 0; i < d->num_tensors; ++i)
+    if (!stepped || t[i].grad) total += (t[i].n + chunk - 1) / chunk;
+  if (total > 0x7ff00000) return HSTU_ERR_UNSUPPORTED;
   *chunks = total;
   return HSTU_OK;
 }
@@ -381,6 +559,19 @@ hstu_status_t cuda_failed(cudaError_t e, const char* what) {
   (void)cudaGetLastError();
   set_error_detail(e, what);
   return HSTU_ERR_CUDA;
+}
+
+// CTAs for a warp a chunk, at most `most`
+unsigned ctas_for(int64_t chunks, int most) {
+  const int64_t n = (chunks + kAdamThreads / 32 - 1) / (kAdamThreads / 32);
+  return (unsigned)(n < 1 ? 1 : (n < most ? n : most));
+}
+
+hstu_status_t device_sms(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? HSTU_OK : cuda_failed(e, "reading the number of SMs");
 }
 
 int kind_of(const hstu_adamw_desc* d, bool read, int out_dtype) {
@@ -447,10 +638,11 @@ hstu_status_t hstu_adamw_init(hstu_adamw_desc* d, const hstu_adamw_tensor* tenso
     return HSTU_ERR_WORKSPACE;
   }
   int64_t at = 0, block = 0;
+  const int chunk = chunk_of(d, tensors);
   const size_t msize = d->state_bits == 8 ? 1 : 4, gsize = d->grad_dtype == HSTU_FP32 ? 4 : 2;
   for (int i = 0; i < d->num_tensors; ++i) {
     const hstu_adamw_tensor& x = tensors[i];
-    for (int64_t e = 0; x.grad && e < x.n; e += kChunk) {
+    for (int64_t e = 0; x.grad && e < x.n; e += chunk) {
       AdamChunk& c = list[at++];
       c.p = x.param + e;
       c.g = static_cast<const char*>(x.grad) + e * gsize;
@@ -460,7 +652,7 @@ hstu_status_t hstu_adamw_init(hstu_adamw_desc* d, const hstu_adamw_tensor* tenso
       c.me = x.m_exp ? x.m_exp + e / kBlock : nullptr;
       c.ve = x.v_exp ? x.v_exp + e / kBlock : nullptr;
       c.quad0 = block * (kBlock / 4) + e / 4;
-      c.n = (int32_t)(x.n - e < kChunk ? x.n - e : kChunk);
+      c.n = (int32_t)(x.n - e < chunk ? x.n - e : chunk);
       c.wd = x.weight_decay;
       c.lr_scale = x.lr_scale;
     }
@@ -485,7 +677,7 @@ hstu_status_t hstu_adamw_step(const hstu_adamw_desc* d, const hstu_adamw_step_ar
                               size_t workspace_bytes, hstu_stream_t stream) {
   hstu_status_t s = check_desc(d);
   if (s != HSTU_OK) return s;
-  if (!a || d->chunks < 0 || d->chunks > 0x7fffffff) return HSTU_ERR_INVALID_ARG;
+  if (!a || d->chunks < 0 || d->chunks > 0x7ff00000) return HSTU_ERR_INVALID_ARG;
   for (const void* ptr : {(const void*)a->lr, (const void*)a->grad_scale, (const void*)a->skip})
     if (!aligned(ptr, 4)) return HSTU_ERR_INVALID_ARG;
   if ((s = check_ws(workspace, workspace_bytes, list_bytes(d->chunks))) != HSTU_OK) return s;
@@ -498,7 +690,9 @@ hstu_status_t hstu_adamw_step(const hstu_adamw_desc* d, const hstu_adamw_step_ar
   p.a1 = (float)(1.0 - d->beta1); p.a2 = (float)(1.0 - d->beta2); p.eps = (float)d->eps;
   p.beta1 = d->beta1; p.beta2 = d->beta2; p.seed = d->seed;
   reset_launches();
-  const dim3 grid((unsigned)(d->chunks > 0 ? d->chunks : 1)), block(kAdamThreads);
+  int sms = 0;
+  if ((s = device_sms(&sms)) != HSTU_OK) return s;
+  const dim3 grid(ctas_for(d->chunks, 4 * sms)), block(kAdamThreads);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool f32 = d->grad_dtype == HSTU_FP32;
   const cudaError_t e = d->state_bits == 32
@@ -529,10 +723,11 @@ hstu_status_t hstu_adamw_read_init(hstu_adamw_desc* d, const hstu_adamw_tensor* 
     return HSTU_ERR_WORKSPACE;
   }
   int64_t at = 0;
+  const int chunk = chunk_of(d, tensors);
   const size_t msize = d->state_bits == 8 ? 1 : 4, osize = out_dtype == HSTU_FP32 ? 4 : 2;
   for (int i = 0; i < d->num_tensors; ++i) {
     const hstu_adamw_tensor& x = tensors[i];
-    for (int64_t e = 0; e < x.n; e += kChunk) {
+    for (int64_t e = 0; e < x.n; e += chunk) {
       ReadChunk& c = list[at++];
       c.m = static_cast<const char*>(x.m) + e * msize;
       c.v = static_cast<const char*>(x.v) + e * msize;
@@ -540,7 +735,7 @@ hstu_status_t hstu_adamw_read_init(hstu_adamw_desc* d, const hstu_adamw_tensor* 
       c.ve = x.v_exp ? x.v_exp + e / kBlock : nullptr;
       c.om = outs[i].m ? static_cast<char*>(outs[i].m) + e * osize : nullptr;
       c.ov = outs[i].v ? static_cast<char*>(outs[i].v) + e * osize : nullptr;
-      c.n = x.n - e < kChunk ? x.n - e : kChunk;
+      c.n = x.n - e < chunk ? x.n - e : chunk;
     }
   }
   AdamState state{};
@@ -558,21 +753,23 @@ hstu_status_t hstu_adamw_read_init(hstu_adamw_desc* d, const hstu_adamw_tensor* 
 hstu_status_t hstu_adamw_read(const hstu_adamw_desc* d, void* workspace, size_t workspace_bytes, hstu_stream_t stream) {
   hstu_status_t s = check_desc(d);
   if (s != HSTU_OK) return s;
-  if (d->chunks < 0 || d->chunks > 0x7fffffff) return HSTU_ERR_INVALID_ARG;
+  if (d->chunks < 0 || d->chunks > 0x7ff00000) return HSTU_ERR_INVALID_ARG;
   if ((s = check_ws(workspace, workspace_bytes, list_bytes(d->chunks))) != HSTU_OK) return s;
   reset_launches();
   if (d->chunks == 0) return HSTU_OK;
   int* hdr = static_cast<int*>(workspace);
   const ReadChunk* list = reinterpret_cast<const ReadChunk*>(static_cast<char*>(workspace) + kWsHeaderBytes);
-  const dim3 grid((unsigned)d->chunks), block(kAdamThreads);
+  int sms = 0;
+  if ((s = device_sms(&sms)) != HSTU_OK) return s;
+  const dim3 grid(ctas_for(d->chunks, 8 * sms)), block(kAdamThreads);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int kind = kind_of(d, true, d->grad_dtype);
   const bool f32 = d->grad_dtype == HSTU_FP32;
   const cudaError_t e = d->state_bits == 32
-                            ? (f32 ? launch_pdl(adamw_read_kernel<32, float>, grid, block, 0, st, hdr, list, d->chunks, kind)
-                                   : launch_pdl(adamw_read_kernel<32, __nv_bfloat16>, grid, block, 0, st, hdr, list, d->chunks, kind))
-                            : (f32 ? launch_pdl(adamw_read_kernel<8, float>, grid, block, 0, st, hdr, list, d->chunks, kind)
-                                   : launch_pdl(adamw_read_kernel<8, __nv_bfloat16>, grid, block, 0, st, hdr, list, d->chunks, kind));
+                            ? (f32 ? launch_pdl(adamw_read_kernel<32, float>, grid, block, 0, st, hdr, list, (int)d->chunks, kind)
+                                   : launch_pdl(adamw_read_kernel<32, __nv_bfloat16>, grid, block, 0, st, hdr, list, (int)d->chunks, kind))
+                            : (f32 ? launch_pdl(adamw_read_kernel<8, float>, grid, block, 0, st, hdr, list, (int)d->chunks, kind)
+                                   : launch_pdl(adamw_read_kernel<8, __nv_bfloat16>, grid, block, 0, st, hdr, list, (int)d->chunks, kind));
   if (e != cudaSuccess) return cuda_failed(e, "launching adamw_read_kernel");
   note_launches(1);
   return HSTU_OK;

@@ -55,8 +55,8 @@ class AdamW:
     one-element tensors on the device, read at every step; skip: not zero, the
     step changes and counts nothing.  seed: of the 8-bit moments' rounding.
 
-    All tensors are contiguous and 16-byte aligned (the 8-bit codes to 4 bytes)
-    and must not overlap."""
+    All tensors are contiguous and 16-byte aligned (copies to 8 bytes, exponent
+    bytes to any) and must not overlap."""
 
     def __init__(self, params, grads=None, *, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.0, lr_scale=1.0,
                  copies=None, moments=None, state_bits: int = 32, grad_scale=None, skip=None, steps: int = 0, seed: int = 0,
@@ -90,7 +90,7 @@ class AdamW:
             _need(isinstance(m, Moments8) == (bits == 8), "all moments have 32 bits, or all 8")
             for t in m[:2]:
                 _need(t.numel() == p.numel() and t.is_contiguous() and t.dtype == (torch.uint8 if bits == 8 else torch.float32)
-                      and t.data_ptr() % (4 if bits == 8 else 16) == 0, f"moments {i} do not match their parameter")
+                      and t.data_ptr() % 16 == 0, f"moments {i} do not match their parameter")
             for t in m[2:]:
                 _need(t.numel() == (p.numel() + BLOCK - 1) // BLOCK and t.is_contiguous() and t.dtype == torch.uint8,
                       f"moments {i} need a byte for every {BLOCK} elements")
@@ -127,7 +127,7 @@ class AdamW:
             return
         p = self.params[i]
         _need(g.device == p.device and g.numel() == p.numel() and g.dtype == self.grad_dtype and g.is_contiguous() and
-              g.data_ptr() % (16 if g.dtype == torch.float32 else 8) == 0,
+              g.data_ptr() % 16 == 0,
               f"gradient {i} must be contiguous {self.grad_dtype} of its parameter's size, 16-byte aligned")
 
     @property

@@ -793,15 +793,15 @@ hstu_status_t hstu_group_bwd(const hstu_group_desc* desc, const hstu_group_bwd_a
  * moments are exact in either, but for what BF16 and FP32 call subnormal):
  * hstu_adamw_read_init lays out a workspace of its own for it.
  *
- * Tensors must not overlap.  Pointers are 16-byte aligned (8-bit codes 4,
- * BF16 8; exponent bytes any).  One call at a time on a workspace.
+ * Tensors must not overlap.  Pointers are 16-byte aligned (copies
+ * 8 bytes; exponent bytes any).  One call at a time on a workspace.
  * ------------------------------------------------------------------------ */
 typedef struct {
   uint32_t struct_size;      /* sizeof(hstu_adamw_desc) */
   int32_t state_bits;        /* 32 or 8 */
   int32_t grad_dtype;        /* HSTU_BF16 or HSTU_FP32 */
   int32_t num_tensors;       /* >= 0 */
-  double lr, beta1, beta2, eps;
+  double lr, beta1, beta2, eps;  /* 0 <= beta < 1, eps >= 1e-12 */
   uint64_t seed;             /* of the 8-bit moments' rounding */
   int64_t steps_done;        /* init: steps taken before; -1: what the workspace has counted is kept */
   int64_t chunks;            /* set by init (read_init): the length of the workspace's list */
