@@ -28,6 +28,25 @@ constexpr int kABytes = 128 * 64 * 2;
 enum : int { B_FULL = 0, B_EMPTY = B_FULL + kStagesMax, B_AFULL = B_EMPTY + kStagesMax, B_AEMPTY = B_AFULL + 2,
              B_DRAIN = B_AEMPTY + 2, B_COUNT };
 
+// two 32 x 32 buffers a storing warp
+constexpr int staging_bytes(int element) { return kEpiWarps * 2 * 1024 * element; }
+
+// 16 lanes x 32 columns: registers 4 j, 4 j + 1 are columns 8 j + 2 (t % 4) + {0, 1} of lane t / 4, the next two
+// those of lane t / 4 + 8
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// four 8 x 8 matrices of 16-bit elements, transposed: lane l gives the address of row l % 8 of matrix l / 8
+__device__ __forceinline__ void stmatrix_trans(uint32_t at, const uint32_t (&m)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(m[0]), "r"(m[1]),
+               "r"(m[2]), "r"(m[3])
+               : "memory");
+}
+
 // Walks the tiles blockIdx.x, blockIdx.x + gridDim.x, ..: t = row block x feature blocks + feature block.
 struct Tiles {
   const int* start;
@@ -52,14 +71,14 @@ struct Tiles {
 template <bool KMAJOR, typename TO>
 __global__ void __launch_bounds__(kThreads, 1)
 group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ CUtensorMap tmw,
-                  const __grid_constant__ CUtensorMap tmr) {
+                  const __grid_constant__ CUtensorMap tmr, const __grid_constant__ CUtensorMap tmo) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[B_COUNT];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   const uint32_t raw_u32 = smem_u32(smem_raw), base = (raw_u32 + 1023u) & ~1023u;
   const int stage_bytes = kABytes + p.row_block * 128;
-  int* start = reinterpret_cast<int*>(smem_raw + (base - raw_u32) + p.stages * stage_bytes);
+  int* start = reinterpret_cast<int*>(smem_raw + (base - raw_u32) + p.stages * stage_bytes + staging_bytes(sizeof(TO)));
   int* first = start + p.E + 1;
   auto bar = [&](int i) -> uint32_t { return smem_u32(bars) + 8u * (uint32_t)i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -174,45 +193,86 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
       drain(bar(B_DRAIN), 0);
     }
   } else {
-    // thread l of warp w has feature 32 (w % 4) + l of the tile, a register a row
+    // a warp stores 32 features of 32 rows at a time, through its two staging buffers [row][feature]
     const int wq = warp & 3, half = warp >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
+    constexpr int kBuf = 1024 * sizeof(TO);
+    const uint32_t stg = base + p.stages * stage_bytes + warp * 2 * kBuf;
+    const uint8_t* stg_ptr = smem_raw + (stg - raw_u32);
     TO* out = static_cast<TO*>(p.out);
-    uint32_t n = 0;
+    // where this lane's row of an 8 x 8 matrix goes: matrix l / 8 of 4 has features 8 (m % 2).. and rows 8 (m / 2)..
+    const uint32_t lane_row = (lane >> 4) * 8 + (lane & 7), lane_chunk = (lane >> 3 & 1) ^ (lane >> 1 & 3);
+    uint32_t n = 0, buf = 0;
     for (; w.at(total); w.next(), ++n) {
       const uint32_t ab = n & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(bar(B_AFULL + ab), (n >> 1) & 1, wd, 64))) break;
       fence_after_sync();
-      const int f = w.f0 + wq * 32 + lane;
-      const bool in = f < p.features;
+      const int f = w.f0 + wq * 32;
 #pragma unroll 1
       for (int c = half * 32; c < w.rows; c += 64) {
-        uint32_t v[32];
-        tmem_ld32(lane_base + ab * 256 + c, v);
-        tmem_wait_ld();
-        TO* at = out + (int64_t)(w.row0 + c) * p.out_stride + f;
-        const int live = w.rows - c;
+        const uint32_t to = stg + buf * kBuf;
+        const uint8_t* from = stg_ptr + buf * kBuf;
+        if (lane == 0) bulk_wait_read<1>();   // the buffer's last store has read it
+        __syncwarp();
         if constexpr (sizeof(TO) == 4) {
+          // lanes are features: a row at a time, 32 neighbouring words
+          uint32_t v[32];
+          tmem_ld32(lane_base + ab * 256 + c, v);
+          tmem_wait_ld();
 #pragma unroll
           for (int r = 0; r < 32; ++r)
-            if (r < live && in) at[r * p.out_stride] = __uint_as_float(v[r]);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + r * 128 + lane * 4), "r"(v[r]) : "memory");
         } else {
-          // neighbouring features meet in one lane: even lanes take the even rows, odd ones the odd rows
-          const bool odd = lane & 1;
-          at += odd ? p.out_stride - 1 : 0;
+          // 16 features x 32 rows a load, whose registers are 8 x 8 matrices [feature][row]; stored transposed,
+          // 16-byte chunk k of row r at k ^ (r / 2 % 4)
+          uint32_t v[2][16];
+          tmem_ld_16x256b_x4(lane_base + ab * 256 + c, v[0]);
+          tmem_ld_16x256b_x4(lane_base + (16u << 16) + ab * 256 + c, v[1]);
+          tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < 32; r += 2) {
-            const float mine = __uint_as_float(odd ? v[r + 1] : v[r]);
-            const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? v[r] : v[r + 1]), 1);
-            const uint32_t two = odd ? pack_bf16(other, mine) : pack_bf16(mine, other);
-            if (r + odd < live && in) *reinterpret_cast<uint32_t*>(at + r * p.out_stride) = two;
-          }
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              uint32_t m[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int at = 4 * (j + (k >> 1)) + 2 * (k & 1);
+                m[k] = pack_bf16(__uint_as_float(v[h][at]), __uint_as_float(v[h][at + 1]));
+              }
+              stmatrix_trans(to + (lane_row + 8 * j) * 64 + ((lane_chunk ^ (2 * h)) << 4), m);
+            }
         }
+        const int live = w.rows - c;
+        if (live >= 32) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (f < p.features) tma_store_2d(&tmo, to, f, w.row0 + c);
+            bulk_commit();
+          }
+        } else {
+          // the group's last rows: a tile store would go on into the next group's
+          __syncwarp();
+          constexpr int kChunks = 32 * sizeof(TO) / 16, kRows = 32 / kChunks;
+          const int chunk = lane % kChunks, col = f + chunk * (16 / (int)sizeof(TO));
+#pragma unroll
+          for (int r = lane / kChunks; r < 32; r += kRows) {
+            const int place = sizeof(TO) == 2 ? chunk ^ (r >> 1 & 3) : chunk;
+            const uint4 x = *reinterpret_cast<const uint4*>(from + r * (32 * sizeof(TO)) + place * 16);
+            if (r < live && col < p.features)
+              *reinterpret_cast<uint4*>(out + (int64_t)(w.row0 + c + r) * p.out_stride + col) = x;
+          }
+          __syncwarp();
+          if (lane == 0) bulk_commit();   // an empty group, so that a buffer's group is always the last but one
+        }
+        buf ^= 1;
       }
       fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_AEMPTY + ab));
     }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
   fence_before_sync();
   __syncthreads();
@@ -223,20 +283,26 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
 template <bool KMAJOR, typename TO>
 cudaError_t launch_t(GroupParams p, const void* rows, int64_t row_stride, const void* w, int K, int N, int sms,
                      cudaStream_t st) {
-  CUtensorMap mw, mr;
+  CUtensorMap mw, mr, mo;
   const uint64_t wd[3] = {(uint64_t)N, (uint64_t)K, (uint64_t)p.E}, ws[2] = {(uint64_t)N * 2, (uint64_t)N * K * 2};
   const uint32_t wbox[3] = {64, KMAJOR ? 128u : 64u, 1};
   const uint64_t rd[2] = {(uint64_t)p.depth, (uint64_t)p.rows}, rs[1] = {(uint64_t)row_stride * 2};
-  const uint32_t rbox[2] = {64, (uint32_t)p.box_rows};
+  const uint32_t rbox[2] = {64, (uint32_t)p.box_rows}, obox[2] = {32, 32};
+  const uint64_t od[2] = {(uint64_t)p.features, (uint64_t)p.rows}, os[1] = {(uint64_t)p.out_stride * sizeof(TO)};
   if (!make_tmap_tile(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, w, wd, ws, wbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_tile(&mr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, rd, rs, rbox, CU_TENSOR_MAP_SWIZZLE_128B))
+      !make_tmap_tile(&mr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, rd, rs, rbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_tile(&mo, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.out,
+                      od, os, obox, sizeof(TO) == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
-  const size_t smem = 1024 + (size_t)p.stages * (kABytes + p.row_block * 128) + 8 * ((size_t)p.E + 1);
+  const size_t fixed = 1024 + staging_bytes(sizeof(TO)) + 8 * ((size_t)p.E + 1), stage = kABytes + p.row_block * 128;
+  p.stages = (int)((kMaxSmemPerCta - 1024 - fixed) / stage);   // (the rest: barriers and the scan's sums)
+  if (p.stages > kStagesMax) p.stages = kStagesMax;
+  const size_t smem = fixed + p.stages * stage;
   auto kern = group_rows_kernel<KMAJOR, TO>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t most = (p.rows / p.row_block + p.E) * (int64_t)((p.features + 127) / 128);
-  return launch_pdl(kern, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), smem, st, p, mw, mr);
+  return launch_pdl(kern, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), smem, st, p, mw, mr, mo);
 }
 
 hstu_status_t check_desc(const hstu_group_desc* d) {
@@ -278,13 +344,9 @@ size_t bwd_bytes(const hstu_group_desc* d) {
   return kWsHeaderBytes + sizeof(float) * 128 * 256 * (size_t)group_dw_slots(d->rows, d->groups, d->K, d->N, kSizeSms);
 }
 
-// rows of a tile and the ring that fits beside the lists of groups
 void set_tile(GroupParams& p, int sms) {
   p.row_block = group_row_block(p.rows, p.E, p.features, sms);
   p.box_rows = p.row_block < 64 ? 32 : 64;
-  const int stage = kABytes + p.row_block * 128;
-  p.stages = (int)((kMaxSmemPerCta - 2048 - 8 * ((size_t)p.E + 1)) / stage);
-  if (p.stages > kStagesMax) p.stages = kStagesMax;
 }
 
 }  // namespace
@@ -346,10 +408,10 @@ hstu_status_t hstu_group_fwd(const hstu_group_desc* d, const hstu_group_fwd_args
   GroupParams p{};
   p.off = a->group_offsets; p.hdr = static_cast<int*>(workspace);
   p.rows = d->rows; p.E = d->groups; p.features = d->N; p.depth = d->K;
-  p.out = a->y; p.out_stride = d->y_stride;
+  p.out = a->y; p.out_stride = d->rows == 1 ? d->N : d->y_stride;
   p.test_timeout = (d->flags & HSTU_FLAG_TEST_TIMEOUT) ? 1 : 0;
   set_tile(p, sms);
-  const int64_t xs = d->rows == 1 ? (d->K + 7) / 8 * 8 : d->x_stride;
+  const int64_t xs = d->rows == 1 ? d->K : d->x_stride;
   const cudaError_t e = launch_group_rows(p, false, d->y_dtype, a->x, xs, a->w, d->K, d->N, sms,
                                           reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) {
@@ -383,12 +445,12 @@ hstu_status_t hstu_group_bwd(const hstu_group_desc* d, const hstu_group_bwd_args
   GroupParams p{};
   p.off = a->group_offsets; p.hdr = static_cast<int*>(workspace);
   p.rows = d->rows; p.E = d->groups;
-  const int64_t ys = d->rows <= 1 ? (d->N + 7) / 8 * 8 : d->y_stride, xs = d->rows <= 1 ? (d->K + 7) / 8 * 8 : d->x_stride;
+  const int64_t ys = d->rows <= 1 ? d->N : d->y_stride, xs = d->rows <= 1 ? d->K : d->x_stride;
   cudaError_t e = cudaSuccess;
   int launches = 0;
   if (a->dx && d->rows > 0) {
     p.features = d->K; p.depth = d->N;
-    p.out = a->dx; p.out_stride = d->dx_stride;
+    p.out = a->dx; p.out_stride = d->rows == 1 ? d->K : d->dx_stride;
     set_tile(p, sms);
     e = launch_group_rows(p, true, d->dx_dtype, a->dy, ys, a->w, d->K, d->N, sms, st);
     launches = 1;

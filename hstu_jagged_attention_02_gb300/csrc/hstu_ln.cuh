@@ -130,6 +130,7 @@ auto dispatch_shape(int D, bool wide, F&& go) {
     return go(Shape<8, 512, 4>());
   }
   if (D <= 128) return go(Shape<1, 32, 4>());
+  if (D <= 320) return go(Shape<1, 32, 10>());
   if (D <= 512) return go(Shape<1, 32, 16>());
   if (D <= 1024) return go(Shape<1, 32, 32>());
   if (D <= 4096) return go(Shape<1, 512, 8>());
@@ -144,6 +145,6 @@ constexpr int kWarpTeams = 8;   // warps of a CTA whose teams are warps
 // launches (hstu_ln_fwd.cu, hstu_ln_bwd.cu)
 cudaError_t launch_ln_fwd(const ln::LnParams& p, int x_dtype, int y_dtype, bool wide, int sms, cudaStream_t st);
 cudaError_t launch_ln_bwd(const ln::LnParams& p, int x_dtype, int y_dtype, bool wide, int sms, cudaStream_t st);
-constexpr int kLnMaxBwdCtas = 304;   // rows of partial sums in the backward's workspace
+constexpr int kLnMaxBwdCtas = 160;   // rows of partial sums in the backward's workspace
 
 }  // namespace hstu

@@ -3,9 +3,9 @@
 //   h = (x - mean) rstd, e = dy weight
 //   dx = rstd (e - mean(e) - h mean(e h)) [+ dres];  d_weight = sum dy h, d_bias = sum dy
 //
-// HBM-bound: x and dy are read once, dx written once.  Teams (warps, or CTAs
+// HBM-bound: x and dy are read once, dx written once.  Teams (a warp, or up to a CTA
 // for wide rows) walk the rows and keep each feature's two sums in registers; a CTA
-// adds its warps' sums in shared memory and leaves a row of 2 D sums in the
+// adds its teams' sums in shared memory and leaves a row of 2 D sums in the
 // workspace, and a second kernel adds these rows, column by column, in their
 // order.
 #include "hstu_ln.cuh"
@@ -16,142 +16,243 @@ namespace {
 
 using namespace ln;
 
+// A CTA an SM, cut into teams of 32 to 512 threads: 16 warps leave 128 registers a thread, of which a lane's sums
+// take 2 N V.  Short rows are read one ahead of the row that is worked on, and keep the weight in registers.
+constexpr int kBwdThreads = 512;
+
+// Sums of two values over a team of L threads, which has the barrier team + 1 and red for itself.
+template <int L>
+__device__ __forceinline__ float2 team_sum_of(float2 v, float2* red, int team) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
+  if constexpr (L > 32) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x % L >> 5] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(L) : "memory");
+    v = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < L / 32; ++w) {
+      v.x += red[w].x;
+      v.y += red[w].y;
+    }
+  }
+  return v;
+}
+
 template <typename TX, typename TY, int V, int L, int N>
-__global__ void __launch_bounds__(L == 32 ? 32 * kWarpTeams : L) ln_bwd_kernel(const __grid_constant__ LnParams p) {
-  extern __shared__ float sums[];   // warps' teams: [warps][2][D]
-  __shared__ float2 red[2][L / 32];
-  constexpr int TEAMS = L == 32 ? kWarpTeams : 1;
+__global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const __grid_constant__ LnParams p) {
+  extern __shared__ float sums[];   // [teams][2][D]
+  constexpr int TEAMS = kBwdThreads / L, E = N * V;
+  static_assert(E % 2 == 0, "features are worked on in pairs");
+  __shared__ float2 red[2][TEAMS][L / 32];
+  // registers of a row as it is read; the weight is kept where it finds room beside 5 E of sums and of the row
+  constexpr int RAW = N * (V == 1 ? 2 : (int)(sizeof(TX) + sizeof(TY)) * 2);
+  constexpr bool KEEP = E <= 16, AHEAD = 4 * E + (KEEP ? E : 0) + RAW <= 100, TWICE = E > 16;
   pdl_wait();
-  const int team = L == 32 ? threadIdx.x >> 5 : 0, l = threadIdx.x % L;
+  const int team = threadIdx.x / L, l = threadIdx.x % L;
   const int64_t rows = live_rows(p), step = (int64_t)gridDim.x * TEAMS;
-  float sw[N][V], sb[N][V];
+  auto at = [&](int i) { return (i * L + l) * V; };   // first of the lane's features in part i
+  // features behind D count as zeros: of dy and of the weight
+  float2 sw[E / 2], sb[E / 2], kept[KEEP ? E / 2 : 1];
 #pragma unroll
-  for (int i = 0; i < N; ++i)
+  for (int k = 0; k < E / 2; ++k) sw[k] = sb[k] = make_float2(0.f, 0.f);
+  auto weight = [&](float2 (&w)[E / 2]) {
+    float a[N][V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) sw[i][e] = sb[i][e] = 0.f;
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) a[i][e] = at(i) < p.D ? 1.f : 0.f;
+      if (p.weight && at(i) < p.D) {
+        Pack<float, V> c;
+        c.load(p.weight + at(i));
+        c.get(a[i]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) w[k] = make_float2(a[2 * k / V][2 * k % V], a[(2 * k + 1) / V][(2 * k + 1) % V]);
+  };
+  if constexpr (KEEP) weight(kept);
   const float inv = 1.f / (float)p.D;
   int turn = 0;
-  for (int64_t r = (int64_t)blockIdx.x * TEAMS + team; r < rows; r += step) {
+  Pack<TX, V> rx[N];
+  Pack<TY, V> rg[N];
+  float mean = 0.f, rstd = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    rx[i] = Pack<TX, V>();
+    rg[i] = Pack<TY, V>();
+  }
+  auto fetch = [&](int64_t r) {
+    if (r >= rows) return;
     const TX* x = static_cast<const TX*>(p.x) + r * p.xs;
     const TY* dy = static_cast<const TY*>(p.dy) + r * p.ys;
-    Pack<TX, V> rx[N];
-    Pack<TY, V> rg[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int f = (i * L + l) * V;
-      if (f < p.D) {
-        rx[i].load(x + f);
-        rg[i].load(dy + f);
+      if (at(i) < p.D) {
+        rx[i].load(x + at(i));
+        rg[i].load(dy + at(i));
       }
     }
-    const float mean = p.mean[r], rstd = p.rstd[r];
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int f = (i * L + l) * V;
-      if (f < p.D) {
-        float h[V], g[V], w[V];
-        rx[i].get(h);
-        rg[i].get(g);
-        if (p.weight) {
-          Pack<float, V> c;
-          c.load(p.weight + f);
-          c.get(w);
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          h[e] = (h[e] - mean) * rstd;
-          sw[i][e] = fmaf(g[e], h[e], sw[i][e]);
-          sb[i][e] += g[e];
-          const float t = p.weight ? g[e] * w[e] : g[e];
-          s.x += t;
-          s.y = fmaf(t, h[e], s.y);
-        }
-      }
-    }
-    s = team_sum<L>(s, red[turn]);
-    turn ^= 1;
-    const float m0 = s.x * inv, m1 = s.y * inv;
+    mean = p.mean[r];
+    rstd = p.rstd[r];
+  };
+  int64_t r = (int64_t)blockIdx.x * TEAMS + team;
+  fetch(r);
+  for (; r < rows; r += step) {
     TX* dx = static_cast<TX*>(p.dx) + r * p.dxs;
     const TX* dres = static_cast<const TX*>(p.dres) + r * p.drs;
+    auto store = [&](int i, float (&o)[V]) {
+      if (p.dres) {
+        Pack<TX, V> c;
+        float add[V];
+        c.load(dres + at(i));
+        c.get(add);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int f = (i * L + l) * V;
-      if (f < p.D) {
-        float h[V], g[V], w[V], a[V];
+        for (int e = 0; e < V; ++e) o[e] += add[e];
+      }
+      put(dx + at(i), o);
+    };
+    const float mean_r = mean, rstd_r = rstd;
+    const float2 scale = make_float2(rstd_r, rstd_r), shift = make_float2(-mean_r * rstd_r, -mean_r * rstd_r);
+    float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+    if constexpr (!TWICE) {
+      float2 h[E / 2], t[E / 2];   // x, dy; then h and t = dy weight
+      {
+        float x[N][V], g[N][V];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          rx[i].get(x[i]);
+          rg[i].get(g[i]);
+        }
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) {
+          h[k] = make_float2(x[2 * k / V][2 * k % V], x[(2 * k + 1) / V][(2 * k + 1) % V]);
+          t[k] = make_float2(g[2 * k / V][2 * k % V], g[(2 * k + 1) / V][(2 * k + 1) % V]);
+        }
+      }
+      if constexpr (AHEAD) fetch(r + step);
+      float2 w[E / 2];
+      if constexpr (!KEEP) weight(w);
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        h[k] = __ffma2_rn(h[k], scale, shift);
+        sw[k] = __ffma2_rn(t[k], h[k], sw[k]);
+        sb[k] = __fadd2_rn(sb[k], t[k]);
+        t[k] = __fmul2_rn(t[k], KEEP ? kept[KEEP ? k : 0] : w[k]);
+        s0 = __fadd2_rn(s0, t[k]);
+        s1 = __ffma2_rn(t[k], h[k], s1);
+      }
+      const float2 s = team_sum_of<L>(make_float2(s0.x + s0.y, s1.x + s1.y), red[turn][team], team);
+      // dx = rstd (t - m0 - h m1)
+      const float a1 = -s.y * inv * rstd_r, b1 = -s.x * inv * rstd_r;
+      const float2 a = make_float2(a1, a1), b = make_float2(b1, b1);
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) t[k] = __ffma2_rn(t[k], scale, __ffma2_rn(h[k], a, b));
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (at(i) < p.D) {
+          float o[V];
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] = (i * V + e) % 2 ? t[(i * V + e) / 2].y : t[(i * V + e) / 2].x;
+          store(i, o);
+        }
+      }
+    } else {
+      // rows whose sums fill the registers: h and t are computed twice from what was read
+      auto part = [&](int i, float (&h)[V], float (&g)[V], float (&t)[V]) {
         rx[i].get(h);
         rg[i].get(g);
         if (p.weight) {
           Pack<float, V> c;
-          c.load(p.weight + f);
-          c.get(w);
-        }
-        if (p.dres) {
-          Pack<TX, V> c;
-          c.load(dres + f);
-          c.get(a);
+          c.load(p.weight + at(i));
+          c.get(t);
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float t = p.weight ? g[e] * w[e] : g[e];
-          g[e] = rstd * (t - m0 - (h[e] - mean) * rstd * m1);
-          if (p.dres) g[e] += a[e];
+          h[e] = fmaf(h[e], rstd_r, shift.x);
+          t[e] = p.weight ? g[e] * t[e] : g[e];
         }
-        put(dx + f, g);
+      };
+      float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (at(i) < p.D) {
+          float h[V], g[V], t[V];
+          part(i, h, g, t);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const int k = (i * V + e) / 2;
+            float& cw = (i * V + e) % 2 ? sw[k].y : sw[k].x;
+            float& cb = (i * V + e) % 2 ? sb[k].y : sb[k].x;
+            cw = fmaf(g[e], h[e], cw);
+            cb += g[e];
+            s.x += t[e];
+            s.y = fmaf(t[e], h[e], s.y);
+          }
+        }
+      }
+      s = team_sum_of<L>(s, red[turn][team], team);
+      const float a = -s.y * inv * rstd_r, b = -s.x * inv * rstd_r;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (at(i) < p.D) {
+          float h[V], g[V], t[V];
+          part(i, h, g, t);
+#pragma unroll
+          for (int e = 0; e < V; ++e) t[e] = fmaf(t[e], rstd_r, fmaf(h[e], a, b));
+          store(i, t);
+        }
       }
     }
+    turn ^= 1;
+    if constexpr (!AHEAD) fetch(r + step);
   }
   if (!p.d_weight && !p.d_bias) return;
   float* out = p.partial + (size_t)blockIdx.x * 2 * p.D;
-  if constexpr (L == 32) {
-    float* mine = sums + (size_t)team * 2 * p.D;
+  float* mine = TEAMS > 1 ? sums + (size_t)team * 2 * p.D : out;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int f = (i * L + l) * V;
-      if (f < p.D) {
+  for (int i = 0; i < N; ++i) {
+    const int f = (i * L + l) * V;
+    if (f < p.D) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          mine[f + e] = sw[i][e];
-          mine[p.D + f + e] = sb[i][e];
-        }
+      for (int e = 0; e < V; ++e) {
+        const float2 a = sw[(i * V + e) / 2], b = sb[(i * V + e) / 2];
+        mine[f + e] = (i * V + e) % 2 ? a.y : a.x;
+        mine[p.D + f + e] = (i * V + e) % 2 ? b.y : b.x;
       }
     }
+  }
+  if constexpr (TEAMS > 1) {
     __syncthreads();
-    for (int c = threadIdx.x; c < 2 * p.D; c += 32 * kWarpTeams) {
+    for (int c = threadIdx.x; c < 2 * p.D; c += kBwdThreads) {
       float t = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarpTeams; ++w) t += sums[(size_t)w * 2 * p.D + c];
+      for (int w = 0; w < TEAMS; ++w) t += sums[(size_t)w * 2 * p.D + c];
       out[c] = t;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int f = (i * L + l) * V;
-      if (f < p.D) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          out[f + e] = sw[i][e];
-          out[p.D + f + e] = sb[i][e];
-        }
-      }
     }
   }
 }
 
-// d_weight and d_bias from `rows` rows of 2 D sums: 32 columns a CTA, its 8
-// warps take every 8th row.
-constexpr int kSumWarps = 8;
+// d_weight and d_bias from `rows` (at most kLnMaxBwdCtas) rows of 2 D sums: 32 columns a CTA,
+// its 16 warps take every 16th row, all of a warp's loads under way together.
+constexpr int kSumWarps = 16, kSumDeep = (kLnMaxBwdCtas + kSumWarps - 1) / kSumWarps;
 __global__ void __launch_bounds__(32 * kSumWarps)
 ln_sum_kernel(const float* __restrict__ partial, int rows, int D, float* d_weight, float* d_bias) {
   __shared__ float red[kSumWarps][32];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
-  float s = 0.f;
-  if (c < 2 * D) {
-#pragma unroll 8
-    for (int r = warp; r < rows; r += kSumWarps) s += __ldcg(partial + (size_t)r * 2 * D + c);
+  float v[kSumDeep];
+#pragma unroll
+  for (int i = 0; i < kSumDeep; ++i) {
+    const int r = warp + i * kSumWarps;
+    v[i] = r < rows && c < 2 * D ? __ldcg(partial + (size_t)r * 2 * D + c) : 0.f;
   }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kSumDeep; ++i) s += v[i];
   red[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < 2 * D) {
@@ -166,22 +267,40 @@ ln_sum_kernel(const float* __restrict__ partial, int rows, int D, float* d_weigh
   }
 }
 
+template <typename F>
+auto dispatch_bwd_shape(int D, bool wide, F&& go) {
+  if (wide) {
+    if (D <= 256) return go(Shape<8, 32, 1>());
+    if (D <= 512) return go(Shape<8, 32, 2>());
+    if (D <= 1024) return go(Shape<8, 128, 1>());
+    if (D <= 2048) return go(Shape<8, 256, 1>());
+    if (D <= 4096) return go(Shape<8, 512, 1>());
+    if (D <= 8192) return go(Shape<8, 512, 2>());
+    return go(Shape<8, 512, 4>());
+  }
+  if (D <= 128) return go(Shape<1, 32, 4>());
+  if (D <= 320) return go(Shape<1, 32, 10>());
+  if (D <= 1024) return go(Shape<1, 128, 8>());
+  if (D <= 4096) return go(Shape<1, 512, 8>());
+  return go(Shape<1, 512, 32>());
+}
+
 template <typename TX, typename TY>
 cudaError_t launch_t(const LnParams& p, bool wide, int sms, cudaStream_t st) {
-  return dispatch_shape(p.D, wide, [&](auto S) {
+  return dispatch_bwd_shape(p.D, wide, [&](auto S) {
     using Sh = decltype(S);
-    constexpr int TEAMS = Sh::l == 32 ? kWarpTeams : 1;
+    constexpr int TEAMS = kBwdThreads / Sh::l;
     auto kern = ln_bwd_kernel<TX, TY, Sh::v, Sh::l, Sh::n>;
     int64_t ctas = (p.rows + TEAMS - 1) / TEAMS;
-    const int64_t most = 2 * (int64_t)sms < kLnMaxBwdCtas ? 2 * (int64_t)sms : kLnMaxBwdCtas;
+    const int64_t most = sms < kLnMaxBwdCtas ? sms : kLnMaxBwdCtas;
     if (ctas > most) ctas = most;
     if (ctas < 1) ctas = 1;
-    const size_t smem = Sh::l == 32 ? sizeof(float) * kWarpTeams * 2 * (size_t)p.D : 0;
+    const size_t smem = TEAMS > 1 ? sizeof(float) * TEAMS * 2 * (size_t)p.D : 0;
     if (smem > 48 * 1024) {
       const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (e != cudaSuccess) return e;
     }
-    cudaError_t e = launch_pdl(kern, dim3((unsigned)ctas), dim3(Sh::l == 32 ? 32 * kWarpTeams : Sh::l), smem, st, p);
+    cudaError_t e = launch_pdl(kern, dim3((unsigned)ctas), dim3(kBwdThreads), smem, st, p);
     if (e != cudaSuccess || (!p.d_weight && !p.d_bias)) return e;
     return launch_pdl(ln_sum_kernel, dim3((unsigned)((2 * p.D + 31) / 32)), dim3(32 * kSumWarps), 0, st,
                       (const float*)p.partial, (int)ctas, p.D, p.d_weight, p.d_bias);
