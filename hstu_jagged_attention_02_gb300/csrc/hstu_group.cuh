@@ -27,8 +27,10 @@ struct GroupParams {
   int features;      // of the output: N (forward), K (dx)
   int depth;         // features summed over: K (forward), N (dx)
   int row_block;     // rows of a tile, 32, 64, 128 or 256
+  int pair;          // CTAs work in pairs
   int box_rows;      // rows of a load box
-  int stages;
+  int stages;        // of the ring of loads (of A, where B has slots of its own)
+  int slots;         // of B
   void* out;
   int64_t out_stride;
   int test_timeout;
@@ -108,8 +110,7 @@ cudaError_t launch_group_rows(const grp::GroupParams& p, bool transposed, int ou
                               const void* w, int K, int N, int sms, cudaStream_t st);
 cudaError_t launch_group_dw(const grp::GroupParams& p, const void* x, int64_t x_stride, const void* dy, int64_t dy_stride,
                             int K, int N, int sms, cudaStream_t st, int* launches);
-// rows of a tile, 64-row blocks of a piece, and slots of partial sums
-int group_row_block(int64_t rows, int E, int features, int sms);
+// 64-row blocks of a piece, and slots of partial sums
 int group_dw_blocks(int64_t rows, int E, int K, int N, int sms);
 int64_t group_dw_slots(int64_t rows, int E, int K, int N, int sms);
 

@@ -1,20 +1,23 @@
 // Products of ragged groups of rows with a weight matrix each: y = x W[g]
 // and dx = dy W[g]^T (hstu_group_fwd, the dx of hstu_group_bwd), and the C calls.
 //
-// Transposed: the tensor core's 128 rows are output features, its columns
-// the group's rows.  A group's last tile so costs what it has rows (in 16s), not 128,
-// and a group of one row costs a load of its weights.  D[f, r] = sum_k W[k, f] x[r, k]:
-//   A = 128 features x 64 k of W[g] (features contiguous: MN-major; for dx k is the
+// Transposed: the tensor core's rows are output features, its columns the group's rows.  A
+// group's last tile so costs what it has rows (in 16s or 32s), not 128, and a group of one row
+// costs a load of its weights.  D[f, r] = sum_k W[k, f] x[r, k]:
+//   A = 128 features x 64 k of W[g] a CTA (features contiguous: MN-major; for dx k is the
 //   contiguous side: K-major), from a 3-D map [g][K][N], so that a tile's edge never
 //   reads the next group's weights;
 //   B = up to 256 rows x 64 k of x (K-major).  Rows of the next group that a load brings
 //   along give columns that nobody stores.
-// One persistent CTA an SM, 128 x row_block tiles, a ring of loads, two accumulators in
-// TMEM, so that a tile is stored while the next one is computed.  The tiles of a row block
-// are neighbours in the order of work: its rows and the group's weights come from L2.
+// What bounds large batches is the way from L2 to the SMs (12 TB/s measured: single CTAs that
+// load A and B for each 128 x 256 tile took 324 us for 161,293 rows, 512 -> 2048, whatever the tensor core had
+// to do).  So CTAs work in pairs (cta_group::2: 256 features, each CTA holds half of A and half of
+// B), and walk neighbouring tiles, which have the same rows: where the depth allows (512),
+// B stays in shared memory from one tile to the next and A alone streams.
+// Two accumulators in TMEM, so that a tile is stored while the next one is computed.
 //
-// Roles (320 threads): warps 0-7 store, warp 8 loads, warp 9 issues and owns TMEM.  Every
-// wait is bounded.
+// Roles (320 threads): warps 0-7 store, warp 8 loads, warp 9 issues (the pair's first CTA) and
+// owns TMEM.  Every wait is bounded.
 #include "hstu_group.cuh"
 
 namespace hstu {
@@ -23,13 +26,80 @@ namespace {
 
 using namespace grp;
 
-constexpr int kStagesMax = 9;
+constexpr int kStagesMax = 8, kSlotsMax = 8;
 constexpr int kABytes = 128 * 64 * 2;
-enum : int { B_FULL = 0, B_EMPTY = B_FULL + kStagesMax, B_AFULL = B_EMPTY + kStagesMax, B_AEMPTY = B_AFULL + 2,
-             B_DRAIN = B_AEMPTY + 2, B_COUNT };
+enum : int { B_AFULL = 0, B_AEMPTY = B_AFULL + kStagesMax, B_BFULL = B_AEMPTY + kStagesMax, B_BEMPTY = B_BFULL + kSlotsMax,
+             B_DFULL = B_BEMPTY + kSlotsMax, B_DEMPTY = B_DFULL + 2, B_DRAIN = B_DEMPTY + 2, B_COUNT };
 
-// two 32 x 32 buffers a storing warp
-constexpr int staging_bytes(int element) { return kEpiWarps * 2 * 1024 * element; }
+// ---- what a pair of CTAs needs beside tc_ptx.cuh
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// the address of the same place in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_in_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// tile loads into this CTA that count on a barrier of the pair
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+template <int CG> __device__ __forceinline__ void alloc_tmem(uint32_t dst) {
+  if constexpr (CG == 1) {
+    tmem_alloc(dst, 512);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG> __device__ __forceinline__ void free_tmem(uint32_t taddr) {
+  if constexpr (CG == 1) tmem_dealloc(taddr, 512);
+  else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(512) : "memory");
+}
+template <int CG> __device__ __forceinline__ void mma(uint32_t d, SDesc a, SDesc b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CG == 1) {
+    mma_ss_w(d, a, b, idesc, accumulate);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+// arrives on the barrier (of both CTAs of a pair) when every tcgen05 operation so far has completed
+template <int CG> __device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (CG == 1) mma_commit(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+// a 32 x 32 buffer of each storing warp
+constexpr int staging_bytes(int element) { return kEpiWarps * 1024 * element; }
 
 // 16 lanes x 32 columns: registers 4 j, 4 j + 1 are columns 8 j + 2 (t % 4) + {0, 1} of lane t / 4, the next two
 // those of lane t / 4 + 8
@@ -47,28 +117,51 @@ __device__ __forceinline__ void stmatrix_trans(uint32_t at, const uint32_t (&m)[
                : "memory");
 }
 
-// Walks the tiles blockIdx.x, blockIdx.x + gridDim.x, ..: t = row block x feature blocks + feature block.
+// Walks a CTA's (a pair's) share [t, end) of the tiles: t = row block x feature blocks + feature block.
 struct Tiles {
   const int* start;
   const int* first;
-  int fb, rb, e, row0, rows, f0, t;
-  __device__ __forceinline__ Tiles(const int* start_, const int* first_, int fblocks, int row_block)
-      : start(start_), first(first_), fb(fblocks), rb(row_block), e(0), t(blockIdx.x) {}
-  __device__ __forceinline__ bool at(int total) {
-    if (t >= total) return false;
-    const int blk = t / fb;
-    while (start[e + 1] <= blk) ++e;
+  int fb, rb, wide, e, row0, rows, f0, t, end, begin, blk;
+  __device__ __forceinline__ Tiles(const int* start_, const int* first_, int E, int fblocks, int row_block, int width, int share,
+                                   int shares, bool good)
+      : start(start_), first(first_), fb(fblocks), rb(row_block), wide(width), e(0), t(0), end(0), begin(0), blk(0) {
+    if (!good) return;
+    const int64_t total = (int64_t)start[E] * fblocks;
+    t = begin = (int)(total * share / shares);
+    end = (int)(total * (share + 1) / shares);
+    if (t >= end) return;
+    blk = t / fb;
+    int lo = 0, hi = E;   // the last group that begins at or below blk, and has rows
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= blk) lo = mid;
+      else hi = mid;
+    }
+    e = lo;
+    set();
+  }
+  __device__ __forceinline__ void set() {
     const int in = (blk - start[e]) * rb;
     row0 = first[e] + in;
     rows = min(rb, first[e + 1] - row0);
-    f0 = (t - blk * fb) * 128;
-    return true;
+    f0 = (t - blk * fb) * wide;
   }
-  __device__ __forceinline__ void next() { t += gridDim.x; }
+  __device__ __forceinline__ bool more() const { return t < end; }
+  // whether the tile's rows are new to this share, and needed no more by the next tile
+  __device__ __forceinline__ bool fresh() const { return t == begin || f0 == 0; }
+  __device__ __forceinline__ bool last() const { return t + 1 == end || t + 1 == (blk + 1) * fb; }
+  __device__ __forceinline__ void next() {
+    if (++t >= end) return;
+    if (t == (blk + 1) * fb) {
+      ++blk;
+      while (start[e + 1] <= blk) ++e;
+    }
+    set();
+  }
 };
 
-// KMAJOR: W is read with k contiguous (dx), else with features contiguous (forward)
-template <bool KMAJOR, typename TO>
+// KMAJOR: W is read with k contiguous (dx), else with features contiguous (forward); CG: CTAs that work together
+template <int CG, bool KMAJOR, typename TO>
 __global__ void __launch_bounds__(kThreads, 1)
 group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ CUtensorMap tmw,
                   const __grid_constant__ CUtensorMap tmr, const __grid_constant__ CUtensorMap tmo) {
@@ -77,37 +170,43 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   const uint32_t raw_u32 = smem_u32(smem_raw), base = (raw_u32 + 1023u) & ~1023u;
-  const int stage_bytes = kABytes + p.row_block * 128;
-  int* start = reinterpret_cast<int*>(smem_raw + (base - raw_u32) + p.stages * stage_bytes + staging_bytes(sizeof(TO)));
+  // a ring of A, a ring (or the whole depth) of B, the storing warps' buffers, the lists of groups
+  const int slot_bytes = p.row_block / CG * 128;
+  const uint32_t a_at = base, b_at = a_at + p.stages * kABytes, stg_at = b_at + p.slots * slot_bytes;
+  int* start = reinterpret_cast<int*>(smem_raw + (stg_at - raw_u32) + staging_bytes(sizeof(TO)));
   int* first = start + p.E + 1;
   auto bar = [&](int i) -> uint32_t { return smem_u32(bars) + 8u * (uint32_t)i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 1 ? 0u : cluster_rank();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(bar(B_FULL + s), 1);
-      mbar_init(bar(B_EMPTY + s), 1);
+    for (int s = 0; s < kStagesMax; ++s) {
+      mbar_init(bar(B_AFULL + s), 1);
+      mbar_init(bar(B_AEMPTY + s), 1);
+    }
+    for (int s = 0; s < kSlotsMax; ++s) {
+      mbar_init(bar(B_BFULL + s), 1);
+      mbar_init(bar(B_BEMPTY + s), 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(B_AFULL + s), 1);
-      mbar_init(bar(B_AEMPTY + s), kEpiWarps);
+      mbar_init(bar(B_DFULL + s), 1);
+      mbar_init(bar(B_DEMPTY + s), CG * kEpiWarps);
     }
     mbar_init(bar(B_DRAIN), 1);
     abort_word = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(smem_u32(&tmem_slot), 512);
-    tmem_relinquish();
-  }
+  if (warp == kMmaWarp) alloc_tmem<CG>(smem_u32(&tmem_slot));
   if (warp == kLoadWarp && lane == 0) {
     tma_prefetch_desc(&tmw);
     tma_prefetch_desc(&tmr);
+    tma_prefetch_desc(&tmo);
   }
   pdl_wait();
   const int rb = p.row_block;
   const bool good = scan_groups<kThreads>(p, start, first, [&](int n) { return (n + rb - 1) / rb; });
   fence_before_sync();
-  __syncthreads();
+  if constexpr (CG == 1) __syncthreads();
+  else cluster_sync();   // the peer's barriers are there before anything arrives on them
   fence_after_sync();
   const uint32_t tmem = tmem_slot;
 
@@ -116,38 +215,69 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
   wd.err = p.hdr + WS_ERR;
   wd.err_info = p.hdr + WS_ERR_INFO;
   wd.limit_ns = p.test_timeout ? 1000000ull : 2000000000ull;
-  const int fblocks = (p.features + 127) / 128, kblocks = (p.depth + 63) / 64;
-  const int total = good ? start[p.E] * fblocks : 0;
-  Tiles w(start, first, fblocks, rb);
+  const int wide = 128 * CG, fblocks = (p.features + wide - 1) / wide, kblocks = (p.depth + 63) / 64;
+  const bool resident = p.slots >= kblocks;   // B stays for all of a row block's tiles
+  Tiles w(start, first, p.E, fblocks, rb, wide, blockIdx.x / CG, gridDim.x / CG, good);
+  // columns of a product: the tile's rows in 16s, in 32s for a pair, whose CTAs hold half of them each
+  auto columns = [&]() { return CG == 1 ? (w.rows + 15) & ~15 : (w.rows + 31) & ~31; };
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, used = 0;   // used: stages whose barrier was armed
-      bool ok = true, withhold = p.test_timeout && blockIdx.x == 0;
-      uint32_t last[kStagesMax];
-      for (; ok && w.at(total); w.next()) {
-        const int boxes = (w.rows + p.box_rows - 1) / p.box_rows;
-        const uint32_t box_bytes = (uint32_t)p.box_rows * 128u, bytes = kABytes + boxes * box_bytes;
+      int stage = 0, slot = 0;
+      uint32_t phase = 0, slot_phase = 0, used_a = 0, used_b = 0;
+      uint32_t last_a[kStagesMax], last_b[kSlotsMax];
+      bool ok = true, withhold = p.test_timeout && rank == 0 && w.more() && w.begin == 0;
+      for (; ok && w.more(); w.next()) {
+        const int mine = columns() / CG, boxes = (mine + p.box_rows - 1) / p.box_rows;
+        const uint32_t box_bytes = (uint32_t)p.box_rows * 128u;
+        const bool rows_too = !resident || w.fresh();
+        const int f = w.f0 + (int)rank * 128, row = w.row0 + (int)rank * mine;
         for (int kb = 0; kb < kblocks; ++kb) {
-          ok = mbar_wait(bar(B_EMPTY + stage), phase ^ 1, wd, 61);
+          if (rows_too) {
+            ok = mbar_wait(bar(B_BEMPTY + slot), slot_phase ^ 1, wd, 65);
+            if (!ok) break;
+            const uint32_t dst = b_at + slot * slot_bytes, full = bar(B_BFULL + slot);
+            if (rank == 0) mbar_arrive_expect_tx(full, CG * boxes * box_bytes);
+            for (int b = 0; b < boxes; ++b) {
+              if constexpr (CG == 1) tma_load_2d(dst + b * box_bytes, &tmr, full, kb * 64, row + b * p.box_rows);
+              else pair_load_2d(dst + b * box_bytes, &tmr, in_cta(full, 0), kb * 64, row + b * p.box_rows);
+            }
+            used_b |= 1u << slot;
+#pragma unroll
+            for (int s = 0; s < kSlotsMax; ++s)
+              if (s == slot) last_b[s] = slot_phase;
+            if (++slot == (resident ? kblocks : p.slots)) {
+              slot = 0;
+              slot_phase ^= 1;
+            }
+          }
+          ok = mbar_wait(bar(B_AEMPTY + stage), phase ^ 1, wd, 61);
           if (!ok) break;
           if (withhold) {   // test only: this copy never comes
             withhold = false;
           } else {
-            const uint32_t sA = base + stage * stage_bytes, sB = sA + kABytes, full = bar(B_FULL + stage);
-            mbar_arrive_expect_tx(full, bytes);
-            if (KMAJOR) {
-              tma_load_3d(sA, &tmw, full, kb * 64, w.f0, w.e);
+            const uint32_t dst = a_at + stage * kABytes, full = bar(B_AFULL + stage);
+            if (rank == 0) mbar_arrive_expect_tx(full, CG * kABytes);
+            if constexpr (CG == 1) {
+              if (KMAJOR) {
+                tma_load_3d(dst, &tmw, full, kb * 64, f, w.e);
+              } else {
+                tma_load_3d(dst, &tmw, full, f, kb * 64, w.e);
+                tma_load_3d(dst + kABytes / 2, &tmw, full, f + 64, kb * 64, w.e);
+              }
             } else {
-              tma_load_3d(sA, &tmw, full, w.f0, kb * 64, w.e);
-              tma_load_3d(sA + kABytes / 2, &tmw, full, w.f0 + 64, kb * 64, w.e);
+              const uint32_t there = in_cta(full, 0);
+              if (KMAJOR) {
+                pair_load_3d(dst, &tmw, there, kb * 64, f, w.e);
+              } else {
+                pair_load_3d(dst, &tmw, there, f, kb * 64, w.e);
+                pair_load_3d(dst + kABytes / 2, &tmw, there, f + 64, kb * 64, w.e);
+              }
             }
-            for (int b = 0; b < boxes; ++b) tma_load_2d(sB + b * box_bytes, &tmr, full, kb * 64, w.row0 + b * p.box_rows);
-            used |= 1u << stage;
+            used_a |= 1u << stage;
 #pragma unroll
             for (int s = 0; s < kStagesMax; ++s)
-              if (s == stage) last[s] = phase;
+              if (s == stage) last_a[s] = phase;
           }
           if (++stage == p.stages) {
             stage = 0;
@@ -155,70 +285,85 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
           }
         }
       }
+      if (rank == 0) {   // the barriers count both CTAs' copies
 #pragma unroll
-      for (int s = 0; s < kStagesMax; ++s)
-        if (used >> s & 1) drain(bar(B_FULL + s), last[s]);
+        for (int s = 0; s < kStagesMax; ++s)
+          if (used_a >> s & 1) drain(bar(B_AFULL + s), last_a[s]);
+#pragma unroll
+        for (int s = 0; s < kSlotsMax; ++s)
+          if (used_b >> s & 1) drain(bar(B_BFULL + s), last_b[s]);
+      } else if (!ok) {   // a wait ran out: what this CTA has under way is not counted here
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 1000000ull) {}
+      }
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, n = 0;
+    if (lane == 0 && rank == 0) {
+      int stage = 0, slot = 0;
+      uint32_t phase = 0, slot_phase = 0, n = 0;
       bool ok = true;
-      for (; ok && w.at(total); w.next(), ++n) {
-        const uint32_t ab = n & 1;
-        ok = mbar_wait(bar(B_AEMPTY + ab), ((n >> 1) & 1) ^ 1, wd, 62);
+      for (; ok && w.more(); w.next(), ++n) {
+        const uint32_t d = n & 1;
+        ok = mbar_wait(bar(B_DEMPTY + d), ((n >> 1) & 1) ^ 1, wd, 62);
         if (!ok) break;
         fence_after_sync();
-        // as many columns as there are rows, in 16s
-        const uint32_t idesc = idesc_bf16(128, (w.rows + 15) & ~15, !KMAJOR, false);
+        const uint32_t idesc = idesc_bf16(wide, columns(), !KMAJOR, false);
+        const bool fresh = !resident || w.fresh(), release = !resident || w.last();
         for (int kb = 0; kb < kblocks; ++kb) {
-          ok = mbar_wait(bar(B_FULL + stage), phase, wd, 63);
+          if (fresh) {
+            ok = mbar_wait(bar(B_BFULL + slot), slot_phase, wd, 66);
+            if (!ok) break;
+          }
+          ok = mbar_wait(bar(B_AFULL + stage), phase, wd, 63);
           if (!ok) break;
           fence_after_sync();
-          const uint32_t sA = base + stage * stage_bytes, sB = sA + kABytes;
+          const uint32_t sA = a_at + stage * kABytes, sB = b_at + slot * slot_bytes;
           const SDesc da = KMAJOR ? sdesc_w(sA, 16, 1024) : sdesc_w(sA, kABytes / 2, 1024);
           const SDesc db = sdesc_w(sB, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ss_w(tmem + ab * 256, da + (KMAJOR ? kk * 32 : kk * 2048), db + kk * 32, idesc, kb > 0 || kk > 0 ? 1u : 0u);
-          mma_commit(bar(B_EMPTY + stage));
+            mma<CG>(tmem + d * 256, da + (KMAJOR ? kk * 32 : kk * 2048), db + kk * 32, idesc, kb > 0 || kk > 0 ? 1u : 0u);
+          commit<CG>(bar(B_AEMPTY + stage));
+          if (release) commit<CG>(bar(B_BEMPTY + slot));
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1;
           }
+          if (++slot == (resident ? kblocks : p.slots)) {
+            slot = 0;
+            if (release) slot_phase ^= 1;
+          }
         }
-        if (ok) mma_commit(bar(B_AFULL + ab));
+        if (ok) commit<CG>(bar(B_DFULL + d));
       }
-      mma_commit(bar(B_DRAIN));
+      commit<CG>(bar(B_DRAIN));
       drain(bar(B_DRAIN), 0);
     }
   } else {
-    // a warp stores 32 features of 32 rows at a time, through its two staging buffers [row][feature]
+    // a warp stores 32 features of 32 rows at a time, through its staging buffer [row][feature]
     const int wq = warp & 3, half = warp >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
     constexpr int kBuf = 1024 * sizeof(TO);
-    const uint32_t stg = base + p.stages * stage_bytes + warp * 2 * kBuf;
-    const uint8_t* stg_ptr = smem_raw + (stg - raw_u32);
+    const uint32_t to = stg_at + warp * kBuf;
+    const uint8_t* from = smem_raw + (to - raw_u32);
     TO* out = static_cast<TO*>(p.out);
     // where this lane's row of an 8 x 8 matrix goes: matrix l / 8 of 4 has features 8 (m % 2).. and rows 8 (m / 2)..
     const uint32_t lane_row = (lane >> 4) * 8 + (lane & 7), lane_chunk = (lane >> 3 & 1) ^ (lane >> 1 & 3);
-    uint32_t n = 0, buf = 0;
-    for (; w.at(total); w.next(), ++n) {
-      const uint32_t ab = n & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_AFULL + ab), (n >> 1) & 1, wd, 64))) break;
+    uint32_t n = 0;
+    for (; w.more(); w.next(), ++n) {
+      const uint32_t d = n & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_DFULL + d), (n >> 1) & 1, wd, 64))) break;
       fence_after_sync();
-      const int f = w.f0 + wq * 32;
+      const int f = w.f0 + (int)rank * 128 + wq * 32;
 #pragma unroll 1
       for (int c = half * 32; c < w.rows; c += 64) {
-        const uint32_t to = stg + buf * kBuf;
-        const uint8_t* from = stg_ptr + buf * kBuf;
-        if (lane == 0) bulk_wait_read<1>();   // the buffer's last store has read it
-        __syncwarp();
         if constexpr (sizeof(TO) == 4) {
           // lanes are features: a row at a time, 32 neighbouring words
           uint32_t v[32];
-          tmem_ld32(lane_base + ab * 256 + c, v);
+          tmem_ld32(lane_base + d * 256 + c, v);
           tmem_wait_ld();
+          if (lane == 0) bulk_wait_read<0>();   // the buffer's last store has read it
+          __syncwarp();
 #pragma unroll
           for (int r = 0; r < 32; ++r)
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + r * 128 + lane * 4), "r"(v[r]) : "memory");
@@ -226,9 +371,11 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
           // 16 features x 32 rows a load, whose registers are 8 x 8 matrices [feature][row]; stored transposed,
           // 16-byte chunk k of row r at k ^ (r / 2 % 4)
           uint32_t v[2][16];
-          tmem_ld_16x256b_x4(lane_base + ab * 256 + c, v[0]);
-          tmem_ld_16x256b_x4(lane_base + (16u << 16) + ab * 256 + c, v[1]);
+          tmem_ld_16x256b_x4(lane_base + d * 256 + c, v[0]);
+          tmem_ld_16x256b_x4(lane_base + (16u << 16) + d * 256 + c, v[1]);
           tmem_wait_ld();
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -263,27 +410,30 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
               *reinterpret_cast<uint4*>(out + (int64_t)(w.row0 + c + r) * p.out_stride + col) = x;
           }
           __syncwarp();
-          if (lane == 0) bulk_commit();   // an empty group, so that a buffer's group is always the last but one
         }
-        buf ^= 1;
       }
       fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_AEMPTY + ab));
+      if (lane == 0) {
+        if constexpr (CG == 1) mbar_arrive(bar(B_DEMPTY + d));
+        else arrive_in_cluster(in_cta(bar(B_DEMPTY + d), 0));
+      }
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
   fence_before_sync();
-  __syncthreads();
+  if constexpr (CG == 1) __syncthreads();
+  else cluster_sync();   // nothing of the pair is under way in either CTA
   fence_after_sync();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) free_tmem<CG>(tmem);
 }
 
-template <bool KMAJOR, typename TO>
+template <int CG, bool KMAJOR, typename TO>
 cudaError_t launch_t(GroupParams p, const void* rows, int64_t row_stride, const void* w, int K, int N, int sms,
                      cudaStream_t st) {
   CUtensorMap mw, mr, mo;
+  p.box_rows = p.row_block / CG < 64 ? p.row_block / CG : 64;
   const uint64_t wd[3] = {(uint64_t)N, (uint64_t)K, (uint64_t)p.E}, ws[2] = {(uint64_t)N * 2, (uint64_t)N * K * 2};
   const uint32_t wbox[3] = {64, KMAJOR ? 128u : 64u, 1};
   const uint64_t rd[2] = {(uint64_t)p.depth, (uint64_t)p.rows}, rs[1] = {(uint64_t)row_stride * 2};
@@ -294,15 +444,51 @@ cudaError_t launch_t(GroupParams p, const void* rows, int64_t row_stride, const 
       !make_tmap_tile(&mo, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.out,
                       od, os, obox, sizeof(TO) == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
-  const size_t fixed = 1024 + staging_bytes(sizeof(TO)) + 8 * ((size_t)p.E + 1), stage = kABytes + p.row_block * 128;
-  p.stages = (int)((kMaxSmemPerCta - 1024 - fixed) / stage);   // (the rest: barriers and the scan's sums)
+  // B for the whole depth where that leaves three stages of A, else as many slots as stages
+  const int64_t kblocks = (p.depth + 63) / 64;
+  const size_t fixed = 1024 + staging_bytes(sizeof(TO)) + 8 * ((size_t)p.E + 1), slot = (size_t)p.row_block / CG * 128;
+  const size_t room = kMaxSmemPerCta - 1024 - fixed;   // (1 KB: barriers and the scan's sums)
+  if (kblocks <= kSlotsMax && kblocks * slot + 3 * (size_t)kABytes <= room) {
+    p.slots = (int)kblocks;
+    p.stages = (int)((room - kblocks * slot) / kABytes);
+  } else {
+    p.stages = (int)(room / (kABytes + slot));
+    if (p.stages >= kblocks) p.stages = (int)kblocks - 1;   // (fewer slots than k-blocks: a ring)
+    if (p.stages > kSlotsMax) p.stages = kSlotsMax;
+    p.slots = p.stages;
+  }
   if (p.stages > kStagesMax) p.stages = kStagesMax;
-  const size_t smem = fixed + p.stages * stage;
-  auto kern = group_rows_kernel<KMAJOR, TO>;
+  const size_t smem = fixed + p.stages * (size_t)kABytes + p.slots * slot;
+  auto kern = group_rows_kernel<CG, KMAJOR, TO>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int64_t most = (p.rows / p.row_block + p.E) * (int64_t)((p.features + 127) / 128);
-  return launch_pdl(kern, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), smem, st, p, mw, mr, mo);
+  const int64_t most = (p.rows / p.row_block + p.E) * (int64_t)((p.features + 128 * CG - 1) / (128 * CG));
+  const unsigned grid = (unsigned)(most < sms / CG ? most : sms / CG) * CG;
+  if constexpr (CG == 1) {
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p, mw, mr, mo);
+  } else {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, p, mw, mr, mo);
+  }
+}
+
+template <bool KMAJOR, typename TO>
+cudaError_t launch_shape(const GroupParams& p, const void* rows, int64_t row_stride, const void* w, int K, int N, int sms,
+                         cudaStream_t st) {
+  return p.pair ? launch_t<2, KMAJOR, TO>(p, rows, row_stride, w, K, N, sms, st)
+                : launch_t<1, KMAJOR, TO>(p, rows, row_stride, w, K, N, sms, st);
 }
 
 hstu_status_t check_desc(const hstu_group_desc* d) {
@@ -344,37 +530,39 @@ size_t bwd_bytes(const hstu_group_desc* d) {
   return kWsHeaderBytes + sizeof(float) * 128 * 256 * (size_t)group_dw_slots(d->rows, d->groups, d->K, d->N, kSizeSms);
 }
 
+// A tile's rows, and whether CTAs work in pairs.  What a choice costs: rounds of tiles over the
+// CTAs, a tile taking for each 64 of the depth the longer of its products (2 cycles a row) and of
+// its loads (128 bytes a row of A and B at 42 bytes a cycle, an SM's share of L2's 12 TB/s),
+// and some 1,500 cycles at its ends.
 void set_tile(GroupParams& p, int sms) {
-  p.row_block = group_row_block(p.rows, p.E, p.features, sms);
-  p.box_rows = p.row_block < 64 ? 32 : 64;
+  const int64_t kblocks = (p.depth + 63) / 64, groups = p.rows < p.E ? p.rows : p.E;
+  int64_t best = -1;
+  for (int cg = 1; cg <= 2; ++cg) {   // (pairs where they are ahead)
+    if (cg == 2 && p.features <= 128) continue;
+    for (int rb = 32 * cg; rb <= 256; rb *= 2) {   // (short tiles leave more stages to the weights)
+      const int64_t tiles = (p.rows / rb + groups) * ((p.features + 128 * cg - 1) / (128 * cg));
+      const int64_t rounds = (tiles + sms / cg - 1) / (sms / cg);
+      const bool stays = kblocks <= kSlotsMax && kblocks * (rb / cg) <= 1024;   // B for the whole depth in 128 KB
+      const int64_t loads = 3 * (128 + (stays ? 0 : rb / cg)), products = 2 * rb;
+      const int64_t cost = rounds * (kblocks * (loads > products ? loads : products) + 1500);
+      if (best < 0 || cost < best) {
+        best = cost;
+        p.row_block = rb;
+        p.pair = cg == 2;
+      }
+    }
+  }
 }
 
 }  // namespace
 
-// The tile's rows.  Cost of a choice: waves of tiles over the SMs, a tile costing its rows and
-// about 64 more for its weights' loads and its ends.
-int group_row_block(int64_t rows, int E, int features, int sms) {
-  const int64_t fb = (features + 127) / 128;
-  int64_t best = -1;
-  int take = 256;
-  for (int rb = 256; rb >= 32; rb >>= 1) {
-    const int64_t full = rows / rb + (rows < E ? rows : E), waves = (full * fb + sms - 1) / sms;
-    const int64_t cost = waves * (rb + 64);
-    if (best < 0 || cost < best) {
-      best = cost;
-      take = rb;
-    }
-  }
-  return take;
-}
-
 cudaError_t launch_group_rows(const GroupParams& p, bool transposed, int out_dtype, const void* rows, int64_t row_stride,
                               const void* w, int K, int N, int sms, cudaStream_t st) {
   if (transposed)
-    return out_dtype == HSTU_BF16 ? launch_t<true, __nv_bfloat16>(p, rows, row_stride, w, K, N, sms, st)
-                                  : launch_t<true, float>(p, rows, row_stride, w, K, N, sms, st);
-  return out_dtype == HSTU_BF16 ? launch_t<false, __nv_bfloat16>(p, rows, row_stride, w, K, N, sms, st)
-                                : launch_t<false, float>(p, rows, row_stride, w, K, N, sms, st);
+    return out_dtype == HSTU_BF16 ? launch_shape<true, __nv_bfloat16>(p, rows, row_stride, w, K, N, sms, st)
+                                  : launch_shape<true, float>(p, rows, row_stride, w, K, N, sms, st);
+  return out_dtype == HSTU_BF16 ? launch_shape<false, __nv_bfloat16>(p, rows, row_stride, w, K, N, sms, st)
+                                : launch_shape<false, float>(p, rows, row_stride, w, K, N, sms, st);
 }
 
 }  // namespace hstu
