@@ -117,6 +117,13 @@ __device__ __forceinline__ void stmatrix_trans(uint32_t at, const uint32_t (&m)[
                : "memory");
 }
 
+// the same, on the issuing CTA's barrier alone
+template <int CG> __device__ __forceinline__ void commit_here(uint32_t bar) {
+  if constexpr (CG == 1) mma_commit(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // Walks a CTA's (a pair's) share [t, end) of the tiles: t = row block x feature blocks + feature block.
 struct Tiles {
   const int* start;
@@ -285,6 +292,23 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
           }
         }
       }
+      // Every stage and slot is waited for once more: the products' arrivals come from the pair's first CTA on
+      // their own time, and one that came after this CTA's end would count on a barrier of its successor.
+      for (int i = 0; ok && i < p.stages; ++i) {
+        ok = mbar_wait(bar(B_AEMPTY + stage), phase ^ 1, wd, 67);
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      const int ring = resident ? kblocks : p.slots;
+      for (int i = 0; ok && i < ring; ++i) {
+        ok = mbar_wait(bar(B_BEMPTY + slot), slot_phase ^ 1, wd, 68);
+        if (++slot == ring) {
+          slot = 0;
+          slot_phase ^= 1;
+        }
+      }
       if (rank == 0) {   // the barriers count both CTAs' copies
 #pragma unroll
         for (int s = 0; s < kStagesMax; ++s)
@@ -336,7 +360,7 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
         }
         if (ok) commit<CG>(bar(B_DFULL + d));
       }
-      commit<CG>(bar(B_DRAIN));
+      commit_here<CG>(bar(B_DRAIN));
       drain(bar(B_DRAIN), 0);
     }
   } else {
