@@ -16,7 +16,7 @@
 // B stays in shared memory from one tile to the next and A alone streams.
 // Two accumulators in TMEM, so that a tile is stored while the next one is computed.
 //
-// Roles (320 threads): warps 0-7 store, warp 8 loads, warp 9 issues (the pair's first CTA) and
+// Roles (352 threads): warps 0-7 store, warp 8 loads A, warp 10 B, warp 9 issues (the pair's first CTA) and
 // owns TMEM.  Every wait is bounded.
 #include "hstu_group.cuh"
 
@@ -27,6 +27,7 @@ namespace {
 using namespace grp;
 
 constexpr int kStagesMax = 8, kSlotsMax = 8;
+constexpr int kRowsWarp = 10, kRowsThreads = 11 * 32;
 constexpr int kABytes = 128 * 64 * 2;
 enum : int { B_AFULL = 0, B_AEMPTY = B_AFULL + kStagesMax, B_BFULL = B_AEMPTY + kStagesMax, B_BEMPTY = B_BFULL + kSlotsMax,
              B_DFULL = B_BEMPTY + kSlotsMax, B_DEMPTY = B_DFULL + 2, B_DRAIN = B_DEMPTY + 2, B_COUNT };
@@ -133,9 +134,9 @@ struct Tiles {
                                    int shares, bool good)
       : start(start_), first(first_), fb(fblocks), rb(row_block), wide(width), e(0), t(0), end(0), begin(0), blk(0) {
     if (!good) return;
-    const int64_t total = (int64_t)start[E] * fblocks;
-    t = begin = (int)(total * share / shares);
-    end = (int)(total * (share + 1) / shares);
+    const int total = start[E] * fblocks, each = total / shares, more = total - each * shares;
+    t = begin = each * share + min(share, more);
+    end = begin + each + (share < more ? 1 : 0);
     if (t >= end) return;
     blk = t / fb;
     int lo = 0, hi = E;   // the last group that begins at or below blk, and has rows
@@ -167,9 +168,33 @@ struct Tiles {
   }
 };
 
+// A loading thread's end.  Every stage is waited for once more by both CTAs of a pair: the products' arrivals come from the
+// pair's first CTA on their own time, and one that came after this CTA's end would count on a barrier of its successor.
+// After a wait that ran out: until the copies under way are there.
+template <int CG, int N, typename Bar>
+__device__ __forceinline__ void tail(Bar bar, int empty, int full, int ring, int stage, uint32_t phase, uint32_t used,
+                                     const uint32_t (&last)[N], uint32_t rank, bool ok, const Watchdog& wd, int site) {
+  for (int i = 0; CG == 2 && ok && i < ring; ++i) {
+    if (used >> stage & 1) ok = mbar_wait(bar(empty + stage), phase ^ 1, wd, site);
+    if (++stage == ring) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  if (ok) return;
+  if (rank == 0) {   // the barriers count both CTAs' copies
+#pragma unroll
+    for (int s = 0; s < N; ++s)
+      if (used >> s & 1) drain(bar(full + s), last[s]);
+  } else {   // the other CTA's copies are not counted here
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 1000000ull) {}
+  }
+}
+
 // KMAJOR: W is read with k contiguous (dx), else with features contiguous (forward); CG: CTAs that work together
 template <int CG, bool KMAJOR, typename TO>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kRowsThreads, 1)
 group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ CUtensorMap tmw,
                   const __grid_constant__ CUtensorMap tmr, const __grid_constant__ CUtensorMap tmo) {
   extern __shared__ uint8_t smem_raw[];
@@ -210,7 +235,7 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
   }
   pdl_wait();
   const int rb = p.row_block;
-  const bool good = scan_groups<kThreads>(p, start, first, [&](int n) { return (n + rb - 1) / rb; });
+  const bool good = scan_groups<kRowsThreads>(p, start, first, [&](int n) { return (n + rb - 1) / rb; });
   fence_before_sync();
   if constexpr (CG == 1) __syncthreads();
   else cluster_sync();   // the peer's barriers are there before anything arrives on them
@@ -229,41 +254,22 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
   auto columns = [&]() { return CG == 1 ? (w.rows + 15) & ~15 : (w.rows + 31) & ~31; };
 
   if (warp == kLoadWarp) {
+    // ------------------------------------------------- A
     if (lane == 0) {
-      int stage = 0, slot = 0;
-      uint32_t phase = 0, slot_phase = 0, used_a = 0, used_b = 0;
-      uint32_t last_a[kStagesMax], last_b[kSlotsMax];
+      int stage = 0;
+      uint32_t phase = 0, used = 0;
+      uint32_t last[kStagesMax];
       bool ok = true, withhold = p.test_timeout && rank == 0 && w.more() && w.begin == 0;
       for (; ok && w.more(); w.next()) {
-        const int mine = columns() / CG, boxes = (mine + p.box_rows - 1) / p.box_rows;
-        const uint32_t box_bytes = (uint32_t)p.box_rows * 128u;
-        const bool rows_too = !resident || w.fresh();
-        const int f = w.f0 + (int)rank * 128, row = w.row0 + (int)rank * mine;
+        const int f = w.f0 + (int)rank * 128;
         for (int kb = 0; kb < kblocks; ++kb) {
-          if (rows_too) {
-            ok = mbar_wait(bar(B_BEMPTY + slot), slot_phase ^ 1, wd, 65);
-            if (!ok) break;
-            const uint32_t dst = b_at + slot * slot_bytes, full = bar(B_BFULL + slot);
-            if (rank == 0) mbar_arrive_expect_tx(full, CG * boxes * box_bytes);
-            for (int b = 0; b < boxes; ++b) {
-              if constexpr (CG == 1) tma_load_2d(dst + b * box_bytes, &tmr, full, kb * 64, row + b * p.box_rows);
-              else pair_load_2d(dst + b * box_bytes, &tmr, in_cta(full, 0), kb * 64, row + b * p.box_rows);
-            }
-            used_b |= 1u << slot;
-#pragma unroll
-            for (int s = 0; s < kSlotsMax; ++s)
-              if (s == slot) last_b[s] = slot_phase;
-            if (++slot == (resident ? kblocks : p.slots)) {
-              slot = 0;
-              slot_phase ^= 1;
-            }
-          }
-          ok = mbar_wait(bar(B_AEMPTY + stage), phase ^ 1, wd, 61);
+          if (used >> stage & 1) ok = mbar_wait(bar(B_AEMPTY + stage), phase ^ 1, wd, 61);
           if (!ok) break;
+          used |= 1u << stage;
+          const uint32_t dst = a_at + stage * kABytes, full = bar(B_AFULL + stage);
           if (withhold) {   // test only: this copy never comes
             withhold = false;
           } else {
-            const uint32_t dst = a_at + stage * kABytes, full = bar(B_AFULL + stage);
             if (rank == 0) mbar_arrive_expect_tx(full, CG * kABytes);
             if constexpr (CG == 1) {
               if (KMAJOR) {
@@ -281,45 +287,51 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
                 pair_load_3d(dst + kABytes / 2, &tmw, there, f + 64, kb * 64, w.e);
               }
             }
-            used_a |= 1u << stage;
-#pragma unroll
-            for (int s = 0; s < kStagesMax; ++s)
-              if (s == stage) last_a[s] = phase;
           }
+#pragma unroll
+          for (int s = 0; s < kStagesMax; ++s)
+            if (s == stage) last[s] = phase;
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1;
           }
         }
       }
-      // Every stage and slot is waited for once more: the products' arrivals come from the pair's first CTA on
-      // their own time, and one that came after this CTA's end would count on a barrier of its successor.
-      for (int i = 0; ok && i < p.stages; ++i) {
-        ok = mbar_wait(bar(B_AEMPTY + stage), phase ^ 1, wd, 67);
-        if (++stage == p.stages) {
-          stage = 0;
-          phase ^= 1;
-        }
-      }
+      tail<CG>(bar, B_AEMPTY, B_AFULL, p.stages, stage, phase, used, last, rank, ok, wd, 67);
+    }
+  } else if (warp == kRowsWarp) {
+    // ------------------------------------------------- B
+    if (lane == 0) {
+      int slot = 0;
+      uint32_t phase = 0, used = 0;
+      uint32_t last[kSlotsMax];
+      bool ok = true;
       const int ring = resident ? kblocks : p.slots;
-      for (int i = 0; ok && i < ring; ++i) {
-        ok = mbar_wait(bar(B_BEMPTY + slot), slot_phase ^ 1, wd, 68);
-        if (++slot == ring) {
-          slot = 0;
-          slot_phase ^= 1;
+      for (; ok && w.more(); w.next()) {
+        if (resident && !w.fresh()) continue;
+        const int mine = columns() / CG, boxes = (mine + p.box_rows - 1) / p.box_rows;
+        const uint32_t box_bytes = (uint32_t)p.box_rows * 128u;
+        const int row = w.row0 + (int)rank * mine;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (used >> slot & 1) ok = mbar_wait(bar(B_BEMPTY + slot), phase ^ 1, wd, 65);
+          if (!ok) break;
+          used |= 1u << slot;
+          const uint32_t dst = b_at + slot * slot_bytes, full = bar(B_BFULL + slot);
+          if (rank == 0) mbar_arrive_expect_tx(full, CG * boxes * box_bytes);
+          for (int b = 0; b < boxes; ++b) {
+            if constexpr (CG == 1) tma_load_2d(dst + b * box_bytes, &tmr, full, kb * 64, row + b * p.box_rows);
+            else pair_load_2d(dst + b * box_bytes, &tmr, in_cta(full, 0), kb * 64, row + b * p.box_rows);
+          }
+#pragma unroll
+          for (int s = 0; s < kSlotsMax; ++s)
+            if (s == slot) last[s] = phase;
+          if (++slot == ring) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
       }
-      if (rank == 0) {   // the barriers count both CTAs' copies
-#pragma unroll
-        for (int s = 0; s < kStagesMax; ++s)
-          if (used_a >> s & 1) drain(bar(B_AFULL + s), last_a[s]);
-#pragma unroll
-        for (int s = 0; s < kSlotsMax; ++s)
-          if (used_b >> s & 1) drain(bar(B_BFULL + s), last_b[s]);
-      } else if (!ok) {   // a wait ran out: what this CTA has under way is not counted here
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 1000000ull) {}
-      }
+      tail<CG>(bar, B_BEMPTY, B_BFULL, ring, slot, phase, used, last, rank, ok, wd, 68);
     }
   } else if (warp == kMmaWarp) {
     if (lane == 0 && rank == 0) {
@@ -489,11 +501,11 @@ cudaError_t launch_t(GroupParams p, const void* rows, int64_t row_stride, const 
   const int64_t most = (p.rows / p.row_block + p.E) * (int64_t)((p.features + 128 * CG - 1) / (128 * CG));
   const unsigned grid = (unsigned)(most < sms / CG ? most : sms / CG) * CG;
   if constexpr (CG == 1) {
-    return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p, mw, mr, mo);
+    return launch_pdl(kern, dim3(grid), dim3(kRowsThreads), smem, st, p, mw, mr, mo);
   } else {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kRowsThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
