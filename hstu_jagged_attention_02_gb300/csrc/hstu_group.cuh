@@ -49,11 +49,121 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// mbar_wait for what threads of the other CTA of a pair have written and fenced
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, const Watchdog& wd, int site) {
+  if (!mbar_wait(bar, parity, wd, site)) return false;
+  uint32_t ok;   // complete by now: once more with the cluster's scope
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // After a wait ran out: until the phase completes, or 0.2 s.
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
   while (!mbar_try_wait(bar, parity)) {
     if (globaltimer() - t0 > 200000000ull) break;
+  }
+}
+
+// ---- what a pair of CTAs needs beside tc_ptx.cuh
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// the address of the same place in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_in_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// tile loads into this CTA that count on a barrier of the pair
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+template <int CG> __device__ __forceinline__ void alloc_tmem(uint32_t dst) {
+  if constexpr (CG == 1) {
+    tmem_alloc(dst, 512);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG> __device__ __forceinline__ void free_tmem(uint32_t taddr) {
+  if constexpr (CG == 1) tmem_dealloc(taddr, 512);
+  else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(512) : "memory");
+}
+template <int CG> __device__ __forceinline__ void mma(uint32_t d, SDesc a, SDesc b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CG == 1) {
+    mma_ss_w(d, a, b, idesc, accumulate);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+// arrives on the barrier (of both CTAs of a pair) when every tcgen05 operation so far has completed
+template <int CG> __device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (CG == 1) mma_commit(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+// the same, on the issuing CTA's barrier alone
+template <int CG> __device__ __forceinline__ void commit_here(uint32_t bar) {
+  if constexpr (CG == 1) mma_commit(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// A loading thread's end.  Every stage is waited for once more by both CTAs of a pair: the products' arrivals come from the
+// pair's first CTA on their own time, and one that came after this CTA's end would count on a barrier of its successor.
+// After a wait that ran out: until the copies under way are there.
+template <int CG, int N, typename Bar>
+__device__ __forceinline__ void tail(Bar bar, int empty, int full, int ring, int stage, uint32_t phase, uint32_t used,
+                                     const uint32_t (&last)[N], uint32_t rank, bool ok, const Watchdog& wd, int site) {
+  for (int i = 0; CG == 2 && ok && i < ring; ++i) {
+    if (used >> stage & 1) ok = mbar_wait(bar(empty + stage), phase ^ 1, wd, site);
+    if (++stage == ring) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  if (ok) return;
+  if (rank == 0) {   // the barriers count both CTAs' copies
+#pragma unroll
+    for (int s = 0; s < N; ++s)
+      if (used >> s & 1) drain(bar(full + s), last[s]);
+  } else {   // the other CTA's copies are not counted here
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 1000000ull) {}
   }
 }
 
@@ -104,14 +214,32 @@ __device__ __forceinline__ bool scan_groups(const GroupParams& p, int* start, in
   return true;
 }
 
+// A launch as launch_pdl makes it, of pairs of CTAs where CG is 2.
+template <int CG, typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, int threads, size_t smem, cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 1 ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 }  // namespace grp
 
 cudaError_t launch_group_rows(const grp::GroupParams& p, bool transposed, int out_dtype, const void* rows, int64_t row_stride,
                               const void* w, int K, int N, int sms, cudaStream_t st);
 cudaError_t launch_group_dw(const grp::GroupParams& p, const void* x, int64_t x_stride, const void* dy, int64_t dy_stride,
                             int K, int N, int sms, cudaStream_t st, int* launches);
-// 64-row blocks of a piece, and slots of partial sums
-int group_dw_blocks(int64_t rows, int E, int K, int N, int sms);
-int64_t group_dw_slots(int64_t rows, int E, int K, int N, int sms);
+// bytes of partial sums that any offsets may need
+size_t group_dw_bytes(int64_t rows, int E, int K, int N);
 
 }  // namespace hstu

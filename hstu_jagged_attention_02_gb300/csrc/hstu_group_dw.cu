@@ -1,17 +1,26 @@
 // Weight gradients of ragged groups: dW[g] = sum over the group's rows r of
 // x[r]^T dy[r] (the dw of hstu_group_bwd).
 //
-// Tiles of 128 (K) x 256 (N) of a dW[g], summed over the group's rows in 64s: both
-// operands are read with features contiguous (MN-major).  Rows of the next group (or
-// past the end) in a group's last 64 are cleared in shared memory before the tensor core
-// reads them, in both operands, since 0 x infinity is no zero.
+// Tiles of a dW[g] of 128 features of x a CTA by 256 of dy, summed over the group's rows in
+// 64s: both operands are read with features contiguous (MN-major).  CTAs work in pairs (cta_group::2,
+// 256 x 256; each holds half of both operands) where there is work for all of them, since what bounds is
+// the way from L2 to the SMs.
+//
+// Rows of the next group (or past the end) in a group's last 64 are cleared in shared memory
+// before the tensor core reads them, in both operands, since 0 x infinity is no zero.  Such a block
+// counts on each CTA's own barrier, is cleared by its MMA warp, and taken when both CTAs are through.
+//
+// Precision: the tensor core's sums lose a little at every addition, always towards zero.  The
+// accumulator so is read after 16 blocks (1,024 rows) and added up in registers (128 a thread), while
+// the second accumulator takes the next 16: 2.5e-6 of dW at 6,415 rows in one accumulator, against 6e-7 of a
+// plain FP32 product.
 //
 // Groups of many rows are cut into pieces of about equal length, so that one large group fills
-// the GPU as many small ones do.  A piece that is a whole tile is stored; others leave
-// their sums in the workspace, which a second kernel adds up in the order of the pieces:
-// equal inputs give equal bits.  A group without rows gets zeros.
+// the GPU as many small ones do; pieces are dealt out longest first, back and forth.  A
+// piece that is a whole tile is stored; others leave their sums in the workspace, which a second
+// kernel adds up in the order of the pieces: equal inputs give equal bits.  A group without rows gets zeros.
 //
-// Roles as in hstu_group_rows.cu.
+// Roles as in hstu_group_rows.cu (one warp loads both operands).
 #include "hstu_group.cuh"
 
 namespace hstu {
@@ -20,13 +29,16 @@ namespace {
 
 using namespace grp;
 
-constexpr int kStagesMax = 3;
+constexpr int kStagesMax = 8;
 constexpr int kBox = 64 * 64 * 2;                 // 64 rows x 64 features
-constexpr int kABytes = 2 * kBox, kBBytes = 4 * kBox, kStage = kABytes + kBBytes;
-constexpr int kStaging = kEpiWarps * 2 * 4096;    // two 32 x 32 FP32 buffers a storing warp
-constexpr int kTile = 128 * 256;
-enum : int { B_FULL = 0, B_EMPTY = B_FULL + kStagesMax, B_AFULL = B_EMPTY + kStagesMax, B_AEMPTY = B_AFULL + 2,
-             B_DRAIN = B_AEMPTY + 2, B_COUNT };
+constexpr int kStaging = kEpiWarps * 2 * 4096;    // two 32 x 32 FP32 buffers of each storing warp
+constexpr int kRun = 16;                          // 64-row blocks summed in one accumulator
+constexpr int kSumThreads = 256;
+constexpr int kRanked = kSumThreads;              // groups up to which they are sorted by the length of their pieces
+enum : int { B_FULL = 0, B_EMPTY = B_FULL + kStagesMax, B_DFULL = B_EMPTY + kStagesMax, B_DEMPTY = B_DFULL + 2,
+             B_CLEAR = B_DEMPTY + 2, B_DRAIN = B_CLEAR + kStagesMax, B_COUNT };
+
+template <int CG> constexpr int boxes_of() { return CG == 1 ? 6 : 4; }   // of a stage: 2 of x, the others of dy
 
 // pieces of a group of n rows
 __device__ __forceinline__ int pieces(int n, int kper) {
@@ -34,45 +46,97 @@ __device__ __forceinline__ int pieces(int n, int kper) {
   return blocks <= kper ? 1 : (blocks + kper - 1) / kper;
 }
 
-// The work blockIdx.x, blockIdx.x + gridDim.x, ..: group, piece, tile (in this order, tiles fastest, so that
-// neighbours share their rows), and the slots of partial sums below the group.
-struct Pieces {
-  const int* start;
-  const int* first;
-  int tpg, nt, kper, e, t, slots;
-  int k0, n0, row0, rows, blocks, slot;   // slot < 0: stored whole
-  __device__ __forceinline__ Pieces(const int* start_, const int* first_, int kt_, int nt_, int kper_)
-      : start(start_), first(first_), tpg(kt_ * nt_), nt(nt_), kper(kper_), e(0), t(blockIdx.x), slots(0) {}
-  __device__ __forceinline__ bool at(int total) {
-    if (t >= total) return false;
-    while (start[e + 1] * tpg <= t) {
-      const int np = start[e + 1] - start[e];
-      slots += np > 1 ? np * tpg : 0;
-      ++e;
+// The lists of a call: in the order of work, order[i] the group and start[i] the pieces before it; first[e] as ever.
+struct Lists {
+  int* start;
+  int* first;
+  int* order;
+};
+__device__ __forceinline__ Lists lists_at(void* at, int E) {
+  int* p = static_cast<int*>(at);
+  return Lists{p, p + E + 1, p + 2 * (E + 1)};
+}
+constexpr size_t lists_bytes(int E) { return 4 * (3 * (size_t)E + 2); }
+
+template <int THREADS>
+__device__ __forceinline__ bool make_lists(const GroupParams& p, const Lists& l) {
+  if (!scan_groups<THREADS>(p, l.start, l.first, [&](int n) { return pieces(n, p.kper); })) return false;
+  // up to a group a thread: longest pieces first
+  const int tid = threadIdx.x;
+  static_assert(kRanked <= THREADS, "a group a thread");
+  if (p.E <= kRanked) {
+    int mine = 0, rank = 0, before = 0;
+    if (tid < p.E) {
+      mine = (l.first[tid + 1] - l.first[tid]) / (l.start[tid + 1] - l.start[tid]);
+      l.order[tid] = mine;
     }
-    const int np = start[e + 1] - start[e], in = t - start[e] * tpg, piece = in / tpg, tile = in - piece * tpg;
-    const int n = first[e + 1] - first[e], all = (n + 63) / 64;
+    __syncthreads();
+    if (tid < p.E) {
+#pragma unroll 4
+      for (int e = 0; e < p.E; ++e) {
+        const int other = l.order[e], np = l.start[e + 1] - l.start[e];
+        const bool ahead = other > mine || (other == mine && e < tid);
+        rank += ahead ? 1 : 0;
+        before += ahead ? np : 0;
+      }
+    }
+    __syncthreads();
+    if (tid < p.E) {
+      l.order[rank] = tid;
+      l.start[rank] = before;   // start[E] stays
+    }
+  } else {
+    for (int e = tid; e < p.E; e += THREADS) l.order[e] = e;
+  }
+  __syncthreads();
+  return true;
+}
+
+// A CTA's (a pair's) share of the work, piece after piece, tiles fastest (neighbours share their rows): items
+// q, 2 P - 1 - q, 2 P + q, .. of P shares.
+struct Pieces {
+  Lists l;
+  int tpg, nt, kper, wide, at_group, e, total, share, shares, k, t, slots;
+  int k0, n0, row0, rows, blocks, slot;   // slot < 0: stored whole
+  __device__ __forceinline__ Pieces(const Lists& l_, const GroupParams& p, int width, int share_, int shares_, bool good)
+      : l(l_), tpg(p.kt * p.nt), nt(p.nt), kper(p.kper), wide(width), at_group(0), e(0), total(good ? l_.start[p.E] * p.kt * p.nt : 0),
+        share(share_), shares(shares_), k(0), t(share_), slots(0) {}
+  __device__ __forceinline__ bool more() {
+    if (t >= total) return false;
+    while (l.start[at_group + 1] * tpg <= t) {
+      const int np = l.start[at_group + 1] - l.start[at_group];
+      slots += np > 1 ? np * tpg : 0;
+      ++at_group;
+    }
+    e = l.order[at_group];
+    const int np = l.start[at_group + 1] - l.start[at_group], in = t - l.start[at_group] * tpg, piece = in / tpg,
+              tile = in - piece * tpg;
+    const int n = l.first[e + 1] - l.first[e], all = (n + 63) / 64;
     // pieces as even as whole blocks allow
     const int b0 = (int)((int64_t)all * piece / np), b1 = (int)((int64_t)all * (piece + 1) / np);
-    k0 = tile / nt * 128;
+    k0 = tile / nt * wide;
     n0 = tile % nt * 256;
-    row0 = first[e] + b0 * 64;
+    row0 = l.first[e] + b0 * 64;
     blocks = b1 - b0;
     rows = min(n - b0 * 64, blocks * 64);
     slot = np > 1 ? slots + tile * np + piece : -1;
     return true;
   }
-  __device__ __forceinline__ void next() { t += gridDim.x; }
+  __device__ __forceinline__ void next() {
+    ++k;
+    t = k * shares + (k & 1 ? shares - 1 - share : share);
+  }
 };
 
 // 16-byte chunk c of row r of a 32 x 32 FP32 buffer lies at chunk c ^ (r % 8)
-__device__ __forceinline__ void stage_f32(uint8_t* buf, int lane, const uint32_t (&a)[32]) {
+__device__ __forceinline__ void stage_f32(uint8_t* buf, int lane, const float* a) {
 #pragma unroll
   for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-        make_uint4(a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]);
+    *reinterpret_cast<float4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+        make_float4(a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]);
 }
 
+template <int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ CUtensorMap tmx,
                 const __grid_constant__ CUtensorMap tmg, const __grid_constant__ CUtensorMap tmo,
@@ -81,38 +145,39 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
   __shared__ __align__(8) uint64_t bars[B_COUNT];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
+  constexpr int BOXES = boxes_of<CG>(), kStage = BOXES * kBox;
   const uint32_t raw_u32 = smem_u32(smem_raw), base = (raw_u32 + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw_u32);
   uint8_t* staging = smem + p.stages * kStage;
-  int* start = reinterpret_cast<int*>(staging + kStaging);
-  int* first = start + p.E + 1;
+  const Lists lists = lists_at(staging + kStaging, p.E);
   auto bar = [&](int i) -> uint32_t { return smem_u32(bars) + 8u * (uint32_t)i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 1 ? 0u : cluster_rank();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
+    for (int s = 0; s < kStagesMax; ++s) {
       mbar_init(bar(B_FULL + s), 1);
       mbar_init(bar(B_EMPTY + s), 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(B_AFULL + s), 1);
-      mbar_init(bar(B_AEMPTY + s), kEpiWarps);
+      mbar_init(bar(B_DFULL + s), 1);
+      mbar_init(bar(B_DEMPTY + s), CG * kEpiWarps);
     }
+    for (int s = 0; s < kStagesMax; ++s) mbar_init(bar(B_CLEAR + s), 1);
     mbar_init(bar(B_DRAIN), 1);
     abort_word = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(smem_u32(&tmem_slot), 512);
-    tmem_relinquish();
-  }
+  if (warp == kMmaWarp) alloc_tmem<CG>(smem_u32(&tmem_slot));
   if (warp == kLoadWarp && lane == 0) {
     tma_prefetch_desc(&tmx);
     tma_prefetch_desc(&tmg);
+    tma_prefetch_desc(&tmo);
   }
   pdl_wait();
-  const bool good = scan_groups<kThreads>(p, start, first, [&](int n) { return pieces(n, p.kper); });
+  const bool good = make_lists<kThreads>(p, lists);
   fence_before_sync();
-  __syncthreads();
+  if constexpr (CG == 1) __syncthreads();
+  else cluster_sync();
   fence_after_sync();
   const uint32_t tmem = tmem_slot;
 
@@ -121,8 +186,7 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
   wd.err = p.hdr + WS_ERR;
   wd.err_info = p.hdr + WS_ERR_INFO;
   wd.limit_ns = 2000000000ull;
-  const int total = good ? start[p.E] * p.kt * p.nt : 0;
-  Pieces w(start, first, p.kt, p.nt, p.kper);
+  Pieces w(lists, p, 128 * CG, blockIdx.x / CG, gridDim.x / CG, good);
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
@@ -130,161 +194,186 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
       uint32_t phase = 0, used = 0;
       uint32_t last[kStagesMax];
       bool ok = true;
-      for (; ok && w.at(total); w.next()) {
+      for (; ok && w.more(); w.next()) {
+        const int k0 = w.k0 + (int)rank * 128, n0 = w.n0 + (int)rank * 128;
         for (int kb = 0; kb < w.blocks; ++kb) {
-          ok = mbar_wait(bar(B_EMPTY + stage), phase ^ 1, wd, 71);
+          if (used >> stage & 1) ok = mbar_wait(bar(B_EMPTY + stage), phase ^ 1, wd, 71);
           if (!ok) break;
-          const uint32_t sA = base + stage * kStage, sB = sA + kABytes, full = bar(B_FULL + stage);
-          mbar_arrive_expect_tx(full, kStage);
+          const uint32_t s = base + stage * kStage;
           const int row = w.row0 + kb * 64;
-          for (int c = 0; c < 2; ++c) tma_load_2d(sA + c * kBox, &tmx, full, w.k0 + c * 64, row);
-          for (int c = 0; c < 4; ++c) tma_load_2d(sB + c * kBox, &tmg, full, w.n0 + c * 64, row);
+          const bool cut = w.rows - kb * 64 < 64;   // the group ends inside: each CTA's copies count on its own barrier
+          const uint32_t full = bar(B_FULL + stage);
+          if (cut || rank == 0) mbar_arrive_expect_tx(full, cut || CG == 1 ? kStage : 2 * kStage);
+#pragma unroll
+          for (int c = 0; c < BOXES; ++c) {
+            const CUtensorMap* map = c < 2 ? &tmx : &tmg;
+            const int x = c < 2 ? k0 + c * 64 : n0 + (c - 2) * 64;
+            if (CG == 1 || cut) tma_load_2d(s + c * kBox, map, full, x, row);
+            else pair_load_2d(s + c * kBox, map, in_cta(full, 0), x, row);
+          }
           used |= 1u << stage;
 #pragma unroll
-          for (int s = 0; s < kStagesMax; ++s)
-            if (s == stage) last[s] = phase;
+          for (int q = 0; q < kStagesMax; ++q)
+            if (q == stage) last[q] = phase;
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1;
           }
         }
       }
-#pragma unroll
-      for (int s = 0; s < kStagesMax; ++s)
-        if (used >> s & 1) drain(bar(B_FULL + s), last[s]);
+      tail<CG>(bar, B_EMPTY, B_FULL, p.stages, stage, phase, used, last, rank, ok, wd, 75);
     }
   } else if (warp == kMmaWarp) {
-    constexpr uint32_t IDESC = idesc_bf16(128, 256, true, true);
+    const uint32_t IDESC = idesc_bf16(128 * CG, 256, true, true);
     int stage = 0;
-    uint32_t phase = 0, n = 0;
+    uint32_t phase = 0, n = 0, cuts = 0;
     bool ok = true;
-    for (; ok && w.at(total); w.next()) {
-      if (w.blocks == 0) continue;
-      const uint32_t ab = n & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_AEMPTY + ab), ((n >> 1) & 1) ^ 1, wd, 72));
-      if (!ok) break;
-      fence_after_sync();
-      for (int kb = 0; kb < w.blocks; ++kb) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(B_FULL + stage), phase, wd, 73));
-        if (!ok) break;
+    for (; ok && w.more(); w.next()) {
+      for (int kb = 0; ok && kb < w.blocks; ++kb) {
         const int live = w.rows - kb * 64;
-        if (live < 64) {   // rows of the next group: cleared (a row is 128 bytes of each box, whatever the swizzle)
+        const uint32_t d = n & 1;
+        if (rank == 0 && kb % kRun == 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(B_DEMPTY + d), ((n >> 1) & 1) ^ 1, wd, 72));
+          if (!ok) break;
+        }
+        const bool cut = live < 64;
+        if (rank == 0 || cut) {
+          // (the second CTA's barriers have no other phases than those of such blocks)
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(B_FULL + stage), rank == 0 ? phase : cuts >> stage & 1, wd, 73));
+          if (!ok) break;
+        }
+        if (cut) {
+          // rows of the next group: cleared (a row is 128 bytes of each box, whatever the swizzle)
           uint8_t* s = smem + stage * kStage;
-          for (int c = 0; c < 6; ++c)
+          for (int c = 0; c < BOXES; ++c)
             for (int i = live * 8 + lane; i < 64 * 8; i += 32)
               *reinterpret_cast<uint4*>(s + c * kBox + i * 16) = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
           __syncwarp();
+          if (CG == 2 && rank != 0 && lane == 0) arrive_in_cluster(in_cta(bar(B_CLEAR + stage), 0));
+          if (CG == 2 && rank == 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(B_CLEAR + stage), cuts >> stage & 1, wd, 77));
+            if (!ok) break;
+          }
+          cuts ^= 1u << stage;
         }
-        fence_after_sync();
-        if (lane == 0) {
-          const uint32_t sA = base + stage * kStage, sB = sA + kABytes;
-          const SDesc da = sdesc_w(sA, kBox, 1024), db = sdesc_w(sB, kBox, 1024);
+        if (rank == 0) {
+          fence_after_sync();
+          if (lane == 0) {
+            const uint32_t sA = base + stage * kStage, sB = sA + 2 * kBox;
+            const SDesc da = sdesc_w(sA, kBox, 1024), db = sdesc_w(sB, kBox, 1024);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ss_w(tmem + ab * 256, da + kk * 2048, db + kk * 2048, IDESC, kb > 0 || kk > 0 ? 1u : 0u);
-          mma_commit(bar(B_EMPTY + stage));
+            for (int kk = 0; kk < 4; ++kk)
+              mma<CG>(tmem + d * 256, da + kk * 2048, db + kk * 2048, IDESC, kb % kRun > 0 || kk > 0 ? 1u : 0u);
+            commit<CG>(bar(B_EMPTY + stage));
+            if (kb % kRun == kRun - 1 || kb == w.blocks - 1) commit<CG>(bar(B_DFULL + d));
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (kb % kRun == kRun - 1 || kb == w.blocks - 1) ++n;
         if (++stage == p.stages) {
           stage = 0;
           phase ^= 1;
         }
       }
-      if (ok && lane == 0) mma_commit(bar(B_AFULL + ab));
-      ++n;
     }
-    if (lane == 0) {
-      mma_commit(bar(B_DRAIN));
+    if (rank == 0 && lane == 0) {
+      commit_here<CG>(bar(B_DRAIN));
       drain(bar(B_DRAIN), 0);
     }
     __syncwarp();
   } else {
     const int wq = warp & 3, half = warp >> 2;
-    const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
+    const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16) + half * 128;
     uint8_t* stg = staging + warp * 8192;
     const uint32_t stg_u32 = smem_u32(stg);
-    uint32_t n = 0, sc = 0;
-    for (; w.at(total); w.next()) {
-      const uint32_t ab = n & 1;
-      if (w.blocks > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_AFULL + ab), (n >> 1) & 1, wd, 74))) break;
-        fence_after_sync();
-      }
-#pragma unroll 1
-      for (int cc = 0; cc < 4; ++cc) {
-        const int col = half * 128 + cc * 32;
-        uint32_t v[32];
-        if (w.blocks > 0) {
-          tmem_ld32(lane_base + ab * 256 + col, v);
-          tmem_wait_ld();
-        } else {
+    uint32_t n = 0;
+    bool ok = true;
+    for (; ok && w.more(); w.next()) {
+      float acc[4][32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[c][i] = 0.f;
+      for (int kb = 0; kb < w.blocks; kb += kRun, ++n) {
+        const uint32_t d = n & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(B_DFULL + d), (n >> 1) & 1, wd, 74));
+        if (!ok) break;
+        fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t v[16];
+          tmem_ld16(lane_base + d * 256 + c * 16, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[c / 2][c % 2 * 16 + i] += __uint_as_float(v[i]);
         }
-        const uint32_t at = (sc & 1) * 4096;
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 1) mbar_arrive(bar(B_DEMPTY + d));
+          else arrive_in_cluster(in_cta(bar(B_DEMPTY + d), 0));
+        }
+      }
+      if (!ok) break;
+      const int k0 = w.k0 + (int)rank * 128 + wq * 32;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int col = half * 128 + c * 32;
+        const uint32_t at = c % 2 * 4096;
         if (lane == 0) bulk_wait_read<1>();
         __syncwarp();
-        stage_f32(stg + at, lane, v);
+        stage_f32(stg + at, lane, acc[c]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (w.slot >= 0) tma_store_2d(&tmp, stg_u32 + at, col, w.slot * 128 + wq * 32);
-          else if (w.n0 + col < p.features && w.k0 + wq * 32 < p.depth)
-            tma_store_3d(&tmo, stg_u32 + at, w.n0 + col, w.k0 + wq * 32, w.e);
+          if (w.slot >= 0) tma_store_2d(&tmp, stg_u32 + at, col, w.slot * (128 * CG) + (int)rank * 128 + wq * 32);
+          else if (w.n0 + col < p.features && k0 < p.depth) tma_store_3d(&tmo, stg_u32 + at, w.n0 + col, k0, w.e);
           bulk_commit();
         }
-        ++sc;
-      }
-      if (w.blocks > 0) {
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_AEMPTY + ab));
-        ++n;
       }
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
   fence_before_sync();
-  __syncthreads();
+  if constexpr (CG == 1) __syncthreads();
+  else cluster_sync();
   fence_after_sync();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) free_tmem<CG>(tmem);
 }
 
 // Sums of the pieces' partial sums, in their order: 16 rows of a tile at a time.
-constexpr int kSumThreads = 256;
-__global__ void __launch_bounds__(kSumThreads) group_dw_sum_kernel(const __grid_constant__ GroupParams p) {
-  extern __shared__ int lists[];
-  int* start = lists;
-  int* first = lists + p.E + 1;
+__global__ void __launch_bounds__(kSumThreads) group_dw_sum_kernel(const __grid_constant__ GroupParams p, int wide) {
+  extern __shared__ int room[];
+  const Lists l = lists_at(room, p.E);
   pdl_wait();
-  if (!scan_groups<kSumThreads>(p, start, first, [&](int n) { return pieces(n, p.kper); })) return;
-  const int tpg = p.kt * p.nt;
-  int e = 0, slots = 0, below = 0;   // below: split tiles of the groups below e
+  if (!make_lists<kSumThreads>(p, l)) return;
+  const int tpg = p.kt * p.nt, units = wide / 16;
+  int i = 0, slots = 0, below = 0;   // below: split tiles of the groups before
   const int c4 = threadIdx.x % 64 * 4, r0 = threadIdx.x / 64;
   for (int u = blockIdx.x;; u += gridDim.x) {
-    const int split = u / 8, r = u % 8 * 16 + r0;
-    while (e < p.E) {
-      const int np = start[e + 1] - start[e];
+    const int split = u / units, r = u % units * 16 + r0;
+    while (i < p.E) {
+      const int np = l.start[i + 1] - l.start[i];
       if (np > 1 && split < below + tpg) break;
       if (np > 1) {
         below += tpg;
         slots += np * tpg;
       }
-      ++e;
+      ++i;
     }
-    if (e == p.E) return;
-    const int np = start[e + 1] - start[e], tile = split - below;
-    const int k0 = tile / p.nt * 128, n = tile % p.nt * 256 + c4;
-    const float* src = p.partial + (size_t)(slots + tile * np) * kTile;
+    if (i == p.E) return;
+    const int np = l.start[i + 1] - l.start[i], tile = split - below, e = l.order[i];
+    const int k0 = tile / p.nt * wide, n = tile % p.nt * 256 + c4;
+    const float* src = p.partial + (size_t)(slots + tile * np) * wide * 256;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = r + 4 * i;
+    for (int q = 0; q < 4; ++q) {
+      const int row = r + 4 * q;
       if (k0 + row >= p.depth || n >= p.features) continue;
       float4 s = __ldcg(reinterpret_cast<const float4*>(src + row * 256 + c4));
       for (int k = 1; k < np; ++k) {
-        const float4 a = __ldcg(reinterpret_cast<const float4*>(src + (size_t)k * kTile + row * 256 + c4));
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(src + (size_t)k * wide * 256 + row * 256 + c4));
         s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
       }
       *reinterpret_cast<float4*>(p.dw + ((size_t)e * p.depth + k0 + row) * p.features + n) = s;
@@ -292,53 +381,77 @@ __global__ void __launch_bounds__(kSumThreads) group_dw_sum_kernel(const __grid_
   }
 }
 
-}  // namespace
-
-// 64-row blocks of a piece: what an SM has to do on average, at least 8.
-int group_dw_blocks(int64_t rows, int E, int K, int N, int sms) {
-  const int64_t tpg = (int64_t)((K + 127) / 128) * ((N + 255) / 256);
-  const int64_t b = ((rows + 63) / 64 * tpg + sms - 1) / sms;
-  return (int)(b < 8 ? 8 : b);
+// The shape of a call on a whole GB300 (its SMs set the size of the workspace).
+constexpr int64_t kSms = 152;
+struct DwShape {
+  int cg, kt, nt, kper;
+  int64_t slots;   // of 128 cg x 256 sums
+};
+DwShape dw_shape(int64_t rows, int E, int K, int N) {
+  DwShape s;
+  const int64_t blocks = rows / 64 + (rows < E ? rows : E);   // of all groups, at most
+  s.nt = (N + 255) / 256;
+  // pairs where each has six blocks of a tile's rows to do, and K does not leave many of their tiles half empty
+  const int halves = (K + 127) / 128, pairs = (halves + 1) / 2;
+  s.cg = blocks * pairs * s.nt >= kSms / 2 * 6 && (halves % 2 == 0 || halves >= 5) ? 2 : 1;
+  s.kt = (K + 128 * s.cg - 1) / (128 * s.cg);
+  // a piece: half of what a CTA (a pair) has to do on average, at least 8 blocks
+  const int64_t tiles = (int64_t)s.kt * s.nt, each = ((rows + 63) / 64 * tiles + 2 * kSms / s.cg - 1) / (2 * kSms / s.cg);
+  s.kper = (int)(each < 8 ? 8 : each);
+  // a group of b > kper blocks has at most (b + kper - 1) / kper < 2 b / kper pieces a tile
+  s.slots = (rows + 63) / 64 <= s.kper ? 0 : 2 * (blocks / s.kper + 1) * tiles;
+  return s;
 }
 
-// Slots that any offsets may need: a group of b > kper blocks has at most
-// (b + kper - 1) / kper pieces a tile, b summing to at most rows / 64 + groups.
-int64_t group_dw_slots(int64_t rows, int E, int K, int N, int sms) {
-  const int64_t tpg = (int64_t)((K + 127) / 128) * ((N + 255) / 256);
-  const int64_t kper = group_dw_blocks(rows, E, K, N, sms);
-  const int64_t blocks = rows / 64 + (rows < E ? rows : E);
-  if ((rows + 63) / 64 <= kper) return 0;   // no group is long enough
-  return 2 * (blocks / kper + 1) * tpg;   // a split group has fewer than 2 b / kper pieces
-}
-
-cudaError_t launch_group_dw(const GroupParams& q, const void* x, int64_t x_stride, const void* dy, int64_t dy_stride, int K,
-                            int N, int sms, cudaStream_t st, int* launches) {
-  GroupParams p = q;
-  p.features = N; p.depth = K;
-  p.kt = (K + 127) / 128; p.nt = (N + 255) / 256;
-  p.kper = group_dw_blocks(p.rows, p.E, K, N, 152);
-  const int64_t slots = group_dw_slots(p.rows, p.E, K, N, 152);
+template <int CG>
+cudaError_t launch_t(GroupParams p, const DwShape& sh, const void* x, int64_t x_stride, const void* dy, int64_t dy_stride, int sms,
+                     cudaStream_t st) {
+  const int K = p.depth, N = p.features;
   CUtensorMap mx, mg, mo, mp;
   const uint64_t xd[2] = {(uint64_t)K, (uint64_t)p.rows}, xs[1] = {(uint64_t)x_stride * 2};
   const uint64_t gd[2] = {(uint64_t)N, (uint64_t)p.rows}, gs[1] = {(uint64_t)dy_stride * 2};
   const uint64_t od[3] = {(uint64_t)N, (uint64_t)K, (uint64_t)p.E}, os[2] = {(uint64_t)N * 4, (uint64_t)N * K * 4};
-  const uint64_t pd[2] = {256, (uint64_t)(slots > 0 ? slots : 1) * 128}, ps[1] = {1024};
+  const uint64_t pd[2] = {256, (uint64_t)(sh.slots > 0 ? sh.slots : 1) * 128 * CG}, ps[1] = {1024};
   const uint32_t ibox[2] = {64, 64}, obox[3] = {32, 32, 1};
   if (!make_tmap_tile(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, xd, xs, ibox, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_tile(&mg, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dy, gd, gs, ibox, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_tile(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p.dw, od, os, obox, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_tile(&mp, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.partial, pd, ps, obox, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  const size_t lists = 8 * ((size_t)p.E + 1);
-  p.stages = 1024 + 3 * (size_t)kStage + kStaging + lists + 1024 <= kMaxSmemPerCta ? 3 : 2;
-  const size_t smem = 1024 + (size_t)p.stages * kStage + kStaging + lists;
-  cudaError_t e = cudaFuncSetAttribute(group_dw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const size_t fixed = 1024 + kStaging + lists_bytes(p.E), stage = (size_t)boxes_of<CG>() * kBox;
+  p.stages = (int)((kMaxSmemPerCta - 1024 - fixed) / stage);
+  if (p.stages > kStagesMax) p.stages = kStagesMax;
+  const size_t smem = fixed + p.stages * stage;
+  auto kern = group_dw_kernel<CG>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)p.kt * p.nt * (p.E + p.rows / 64 / p.kper + 1);
-  e = launch_pdl(group_dw_kernel, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), smem, st, p, mx, mg, mo, mp);
+  const unsigned grid = (unsigned)(most < sms / CG ? most : sms / CG) * CG;
+  return launch_cluster<CG>(kern, grid, kThreads, smem, st, p, mx, mg, mo, mp);
+}
+
+}  // namespace
+
+size_t group_dw_bytes(int64_t rows, int E, int K, int N) {
+  const DwShape s = dw_shape(rows, E, K, N);
+  return (size_t)s.slots * 128 * s.cg * 256 * sizeof(float);
+}
+
+cudaError_t launch_group_dw(const GroupParams& q, const void* x, int64_t x_stride, const void* dy, int64_t dy_stride, int K,
+                            int N, int sms, cudaStream_t st, int* launches) {
+  const DwShape s = dw_shape(q.rows, q.E, K, N);
+  GroupParams p = q;
+  p.features = N; p.depth = K;
+  p.kt = s.kt; p.nt = s.nt; p.kper = s.kper;
+  cudaError_t e = s.cg == 2 ? launch_t<2>(p, s, x, x_stride, dy, dy_stride, sms, st)
+                            : launch_t<1>(p, s, x, x_stride, dy, dy_stride, sms, st);
   ++*launches;
-  if (e != cudaSuccess || slots == 0) return e;
-  e = launch_pdl(group_dw_sum_kernel, dim3((unsigned)(4 * sms)), dim3(kSumThreads), lists, st, p);
+  if (e != cudaSuccess || s.slots == 0) return e;
+  const size_t lists = lists_bytes(p.E);
+  if (lists > 48 * 1024 &&
+      (e = cudaFuncSetAttribute(group_dw_sum_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)lists)) != cudaSuccess)
+    return e;
+  e = launch_pdl(group_dw_sum_kernel, dim3((unsigned)(4 * sms)), dim3(kSumThreads), lists, st, p, 128 * s.cg);
   ++*launches;
   return e;
 }

@@ -32,73 +32,6 @@ constexpr int kABytes = 128 * 64 * 2;
 enum : int { B_AFULL = 0, B_AEMPTY = B_AFULL + kStagesMax, B_BFULL = B_AEMPTY + kStagesMax, B_BEMPTY = B_BFULL + kSlotsMax,
              B_DFULL = B_BEMPTY + kSlotsMax, B_DEMPTY = B_DFULL + 2, B_DRAIN = B_DEMPTY + 2, B_COUNT };
 
-// ---- what a pair of CTAs needs beside tc_ptx.cuh
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-// the address of the same place in CTA `rank` of the cluster
-__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void arrive_in_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// tile loads into this CTA that count on a barrier of the pair
-__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4}], [%2];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-      : "memory");
-}
-__device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-template <int CG> __device__ __forceinline__ void alloc_tmem(uint32_t dst) {
-  if constexpr (CG == 1) {
-    tmem_alloc(dst, 512);
-    tmem_relinquish();
-  } else {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(512) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
-}
-template <int CG> __device__ __forceinline__ void free_tmem(uint32_t taddr) {
-  if constexpr (CG == 1) tmem_dealloc(taddr, 512);
-  else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(512) : "memory");
-}
-template <int CG> __device__ __forceinline__ void mma(uint32_t d, SDesc a, SDesc b, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (CG == 1) {
-    mma_ss_w(d, a, b, idesc, accumulate);
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
-        "setp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
-        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
-        : "memory");
-  }
-}
-// arrives on the barrier (of both CTAs of a pair) when every tcgen05 operation so far has completed
-template <int CG> __device__ __forceinline__ void commit(uint32_t bar) {
-  if constexpr (CG == 1) mma_commit(bar);
-  else
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-                 "h"((uint16_t)3)
-                 : "memory");
-}
-
 // a 32 x 32 buffer of each storing warp
 constexpr int staging_bytes(int element) { return kEpiWarps * 1024 * element; }
 
@@ -116,13 +49,6 @@ __device__ __forceinline__ void stmatrix_trans(uint32_t at, const uint32_t (&m)[
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(m[0]), "r"(m[1]),
                "r"(m[2]), "r"(m[3])
                : "memory");
-}
-
-// the same, on the issuing CTA's barrier alone
-template <int CG> __device__ __forceinline__ void commit_here(uint32_t bar) {
-  if constexpr (CG == 1) mma_commit(bar);
-  else
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Walks a CTA's (a pair's) share [t, end) of the tiles: t = row block x feature blocks + feature block.
@@ -167,30 +93,6 @@ struct Tiles {
     set();
   }
 };
-
-// A loading thread's end.  Every stage is waited for once more by both CTAs of a pair: the products' arrivals come from the
-// pair's first CTA on their own time, and one that came after this CTA's end would count on a barrier of its successor.
-// After a wait that ran out: until the copies under way are there.
-template <int CG, int N, typename Bar>
-__device__ __forceinline__ void tail(Bar bar, int empty, int full, int ring, int stage, uint32_t phase, uint32_t used,
-                                     const uint32_t (&last)[N], uint32_t rank, bool ok, const Watchdog& wd, int site) {
-  for (int i = 0; CG == 2 && ok && i < ring; ++i) {
-    if (used >> stage & 1) ok = mbar_wait(bar(empty + stage), phase ^ 1, wd, site);
-    if (++stage == ring) {
-      stage = 0;
-      phase ^= 1;
-    }
-  }
-  if (ok) return;
-  if (rank == 0) {   // the barriers count both CTAs' copies
-#pragma unroll
-    for (int s = 0; s < N; ++s)
-      if (used >> s & 1) drain(bar(full + s), last[s]);
-  } else {   // the other CTA's copies are not counted here
-    const uint64_t t0 = globaltimer();
-    while (globaltimer() - t0 < 1000000ull) {}
-  }
-}
 
 // KMAJOR: W is read with k contiguous (dx), else with features contiguous (forward); CG: CTAs that work together
 template <int CG, bool KMAJOR, typename TO>
@@ -500,24 +402,7 @@ cudaError_t launch_t(GroupParams p, const void* rows, int64_t row_stride, const 
   if (e != cudaSuccess) return e;
   const int64_t most = (p.rows / p.row_block + p.E) * (int64_t)((p.features + 128 * CG - 1) / (128 * CG));
   const unsigned grid = (unsigned)(most < sms / CG ? most : sms / CG) * CG;
-  if constexpr (CG == 1) {
-    return launch_pdl(kern, dim3(grid), dim3(kRowsThreads), smem, st, p, mw, mr, mo);
-  } else {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kRowsThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, p, mw, mr, mo);
-  }
+  return launch_cluster<CG>(kern, grid, kRowsThreads, smem, st, p, mw, mr, mo);
 }
 
 template <bool KMAJOR, typename TO>
@@ -559,11 +444,8 @@ hstu_status_t device_sms(int* sms) {
   return HSTU_ERR_CUDA;
 }
 
-// The workspace has to hold for any GPU of this kind: sized for the SMs of a whole GB300.
-constexpr int kSizeSms = 152;
-
 size_t bwd_bytes(const hstu_group_desc* d) {
-  return kWsHeaderBytes + sizeof(float) * 128 * 256 * (size_t)group_dw_slots(d->rows, d->groups, d->K, d->N, kSizeSms);
+  return kWsHeaderBytes + group_dw_bytes(d->rows, d->groups, d->K, d->N);
 }
 
 // A tile's rows, and whether CTAs work in pairs.  What a choice costs: rounds of tiles over the
@@ -664,7 +546,6 @@ hstu_status_t hstu_group_bwd(const hstu_group_desc* d, const hstu_group_bwd_args
   reset_launches();
   int sms = 0;
   if ((s = device_sms(&sms)) != HSTU_OK) return s;
-  if (sms > kSizeSms) sms = kSizeSms;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   GroupParams p{};
   p.off = a->group_offsets; p.hdr = static_cast<int*>(workspace);

@@ -109,11 +109,14 @@ def test_slots_hold_every_split(E):
     """The workspace's partial sums suffice for any offsets: pieces as the kernel cuts them."""
     rng = np.random.default_rng(E)
     for rows in (1, 600, 5000, 40_000, 300_000):
-        for K, N in ((8, 8), (128, 256), (512, 2048), (264, 520)):
+        for K, N in ((8, 8), (128, 256), (512, 2048), (264, 520), (640, 256)):
             ws = C.hstu_group_workspace_size(_group(groups=E, K=K, N=N, rows=rows, x_stride=K, y_stride=N, dx_stride=K))[1]
-            slots = (ws - 256) // (4 * 128 * 256)
-            tpg = -(-K // 128) * -(-N // 256)
-            kper = max(8, -(-(-(-rows // 64) * tpg) // 152))
+            halves, nt = -(-K // 128), -(-N // 256)
+            pair = (rows // 64 + min(rows, E)) * -(-halves // 2) * nt >= 456 and (halves % 2 == 0 or halves >= 5)
+            cg = 2 if pair else 1
+            slots = (ws - 256) // (4 * 128 * cg * 256)
+            tiles = -(-halves // cg) * nt
+            kper = max(8, -(-(-(-rows // 64) * tiles) // (304 // cg)))
             for k in range(20):
                 share = rng.random(E) ** (10 if k % 2 else 1)
                 n = np.floor(rows * share / share.sum()).astype(int)
@@ -122,7 +125,7 @@ def test_slots_hold_every_split(E):
                     n = [min(kper * 64 + 1, max(0, rows - i * (kper * 64 + 1))) for i in range(E)]
                     blocks = np.array([-(-x // 64) for x in n])
                 pieces = [-(-b // kper) if b > kper else 0 for b in blocks]
-                assert sum(pieces) * tpg <= slots
+                assert sum(pieces) * tiles <= slots
 
 
 def _adamw(**kw):
