@@ -217,7 +217,7 @@ def load(build_if_missing: bool = True):
     L.hstu_ln_workspace_size.argtypes = [P(hstu_ln_desc), size_p, size_p]
     L.hstu_ln_fwd.argtypes = [P(hstu_ln_desc), P(hstu_ln_fwd_args), _vp, sz, _vp]
     L.hstu_ln_bwd.argtypes = [P(hstu_ln_desc), P(hstu_ln_bwd_args), _vp, sz, _vp]
-    L.hstu_group_workspace_size.argtypes = [P(hstu_group_desc), size_p, size_p]
+    L.hstu_group_workspace_size.argtypes = [P(hstu_group_desc), size_p, size_p, size_p]
     L.hstu_group_fwd.argtypes = [P(hstu_group_desc), P(hstu_group_fwd_args), _vp, sz, _vp]
     L.hstu_group_bwd.argtypes = [P(hstu_group_desc), P(hstu_group_bwd_args), _vp, sz, _vp]
     tensors = P(hstu_adamw_tensor)
@@ -393,10 +393,11 @@ def hstu_ln_bwd(desc, args, workspace: int, workspace_bytes: int, stream: int):
 
 
 def hstu_group_workspace_size(desc):
-    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
-    _check(load().hstu_group_workspace_size(ctypes.byref(desc), ctypes.byref(f), ctypes.byref(b)),
+    """(bytes of the forward, of the backward, bytes of the latter that are zero before the first use)."""
+    f, b, z = (ctypes.c_size_t(0) for _ in range(3))
+    _check(load().hstu_group_workspace_size(ctypes.byref(desc), ctypes.byref(f), ctypes.byref(b), ctypes.byref(z)),
            "hstu_group_workspace_size")
-    return int(f.value), int(b.value)
+    return int(f.value), int(b.value), int(z.value)
 
 
 def hstu_group_fwd(desc, args, workspace: int, workspace_bytes: int, stream: int):

@@ -37,7 +37,8 @@ struct GroupParams {
   // weight gradients: tiles of 128 x 256 of [K, N], pieces of at most kper 64-row blocks
   int kt, nt, kper;
   float* dw;
-  float* partial;    // [slots][128][256]
+  int* counters;     // of cut tiles, a storing warp each
+  float* partial;    // [slots][CTAs of a tile][warps][32 x 128]
 };
 
 // 3-D tile load (x innermost, a multiple of 16 bytes)
@@ -237,9 +238,10 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, int threads,
 
 cudaError_t launch_group_rows(const grp::GroupParams& p, bool transposed, int out_dtype, const void* rows, int64_t row_stride,
                               const void* w, int K, int N, int sms, cudaStream_t st);
-cudaError_t launch_group_dw(const grp::GroupParams& p, const void* x, int64_t x_stride, const void* dy, int64_t dy_stride,
-                            int K, int N, int sms, cudaStream_t st, int* launches);
-// bytes of partial sums that any offsets may need
+// room: group_dw_bytes of it, the first group_dw_counters zero before the first call
+cudaError_t launch_group_dw(const grp::GroupParams& p, void* room, const void* x, int64_t x_stride, const void* dy,
+                            int64_t dy_stride, int K, int N, int sms, cudaStream_t st);
+size_t group_dw_counters(int64_t rows, int E, int K, int N);
 size_t group_dw_bytes(int64_t rows, int E, int K, int N);
 
 }  // namespace hstu

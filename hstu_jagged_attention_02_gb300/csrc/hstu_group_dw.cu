@@ -17,8 +17,9 @@
 //
 // Groups of many rows are cut into pieces of about equal length, so that one large group fills
 // the GPU as many small ones do; pieces are dealt out longest first, back and forth.  A
-// piece that is a whole tile is stored; others leave their sums in the workspace, which a second
-// kernel adds up in the order of the pieces: equal inputs give equal bits.  A group without rows gets zeros.
+// piece that is a whole tile is stored; of others each storing warp leaves its sums in the workspace, and the warp
+// that comes last (a counter) adds up all of them, in the order of the pieces: equal inputs give equal bits.  (A second
+// kernel for that took 11 us of 58 with a heavy-tailed batch.)  A group without rows gets zeros.
 //
 // Roles as in hstu_group_rows.cu (one warp loads both operands).
 #include "hstu_group.cuh"
@@ -33,8 +34,7 @@ constexpr int kStagesMax = 8;
 constexpr int kBox = 64 * 64 * 2;                 // 64 rows x 64 features
 constexpr int kStaging = kEpiWarps * 2 * 4096;    // two 32 x 32 FP32 buffers of each storing warp
 constexpr int kRun = 16;                          // 64-row blocks summed in one accumulator
-constexpr int kSumThreads = 256;
-constexpr int kRanked = kSumThreads;              // groups up to which they are sorted by the length of their pieces
+constexpr int kRanked = kThreads;                 // groups up to which they are sorted by the length of their pieces
 enum : int { B_FULL = 0, B_EMPTY = B_FULL + kStagesMax, B_DFULL = B_EMPTY + kStagesMax, B_DEMPTY = B_DFULL + 2,
              B_CLEAR = B_DEMPTY + 2, B_DRAIN = B_CLEAR + kStagesMax, B_COUNT };
 
@@ -58,12 +58,10 @@ __device__ __forceinline__ Lists lists_at(void* at, int E) {
 }
 constexpr size_t lists_bytes(int E) { return 4 * (3 * (size_t)E + 2); }
 
-template <int THREADS>
 __device__ __forceinline__ bool make_lists(const GroupParams& p, const Lists& l) {
-  if (!scan_groups<THREADS>(p, l.start, l.first, [&](int n) { return pieces(n, p.kper); })) return false;
+  if (!scan_groups<kThreads>(p, l.start, l.first, [&](int n) { return pieces(n, p.kper); })) return false;
   // up to a group a thread: longest pieces first
   const int tid = threadIdx.x;
-  static_assert(kRanked <= THREADS, "a group a thread");
   if (p.E <= kRanked) {
     int mine = 0, rank = 0, before = 0;
     if (tid < p.E) {
@@ -86,7 +84,7 @@ __device__ __forceinline__ bool make_lists(const GroupParams& p, const Lists& l)
       l.start[rank] = before;   // start[E] stays
     }
   } else {
-    for (int e = tid; e < p.E; e += THREADS) l.order[e] = e;
+    for (int e = tid; e < p.E; e += kThreads) l.order[e] = e;
   }
   __syncthreads();
   return true;
@@ -96,21 +94,25 @@ __device__ __forceinline__ bool make_lists(const GroupParams& p, const Lists& l)
 // q, 2 P - 1 - q, 2 P + q, .. of P shares.
 struct Pieces {
   Lists l;
-  int tpg, nt, kper, wide, at_group, e, total, share, shares, k, t, slots;
-  int k0, n0, row0, rows, blocks, slot;   // slot < 0: stored whole
+  int tpg, nt, kper, wide, at_group, e, total, share, shares, k, t, slots, splits;   // slots, cut tiles before at_group
+  int k0, n0, row0, rows, blocks;
+  int np, piece, slot, split;   // np > 1: the tile's first slot and its place among cut tiles
   __device__ __forceinline__ Pieces(const Lists& l_, const GroupParams& p, int width, int share_, int shares_, bool good)
       : l(l_), tpg(p.kt * p.nt), nt(p.nt), kper(p.kper), wide(width), at_group(0), e(0), total(good ? l_.start[p.E] * p.kt * p.nt : 0),
-        share(share_), shares(shares_), k(0), t(share_), slots(0) {}
+        share(share_), shares(shares_), k(0), t(share_), slots(0), splits(0) {}
   __device__ __forceinline__ bool more() {
     if (t >= total) return false;
     while (l.start[at_group + 1] * tpg <= t) {
-      const int np = l.start[at_group + 1] - l.start[at_group];
-      slots += np > 1 ? np * tpg : 0;
+      const int n = l.start[at_group + 1] - l.start[at_group];
+      slots += n > 1 ? n * tpg : 0;
+      splits += n > 1 ? tpg : 0;
       ++at_group;
     }
     e = l.order[at_group];
-    const int np = l.start[at_group + 1] - l.start[at_group], in = t - l.start[at_group] * tpg, piece = in / tpg,
-              tile = in - piece * tpg;
+    np = l.start[at_group + 1] - l.start[at_group];
+    const int in = t - l.start[at_group] * tpg;
+    piece = in / tpg;
+    const int tile = in - piece * tpg;
     const int n = l.first[e + 1] - l.first[e], all = (n + 63) / 64;
     // pieces as even as whole blocks allow
     const int b0 = (int)((int64_t)all * piece / np), b1 = (int)((int64_t)all * (piece + 1) / np);
@@ -119,7 +121,8 @@ struct Pieces {
     row0 = l.first[e] + b0 * 64;
     blocks = b1 - b0;
     rows = min(n - b0 * 64, blocks * 64);
-    slot = np > 1 ? slots + tile * np + piece : -1;
+    slot = slots + tile * np;
+    split = splits + tile;
     return true;
   }
   __device__ __forceinline__ void next() {
@@ -139,8 +142,7 @@ __device__ __forceinline__ void stage_f32(uint8_t* buf, int lane, const float* a
 template <int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ CUtensorMap tmx,
-                const __grid_constant__ CUtensorMap tmg, const __grid_constant__ CUtensorMap tmo,
-                const __grid_constant__ CUtensorMap tmp) {
+                const __grid_constant__ CUtensorMap tmg, const __grid_constant__ CUtensorMap tmo) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[B_COUNT];
   __shared__ uint32_t tmem_slot;
@@ -174,7 +176,7 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
     tma_prefetch_desc(&tmo);
   }
   pdl_wait();
-  const bool good = make_lists<kThreads>(p, lists);
+  const bool good = make_lists(p, lists);
   fence_before_sync();
   if constexpr (CG == 1) __syncthreads();
   else cluster_sync();
@@ -316,6 +318,39 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
         }
       }
       if (!ok) break;
+      if (w.np > 1) {
+        // this warp's 32 x 128 of a tile's pieces lie side by side, a float4 a lane
+        constexpr size_t kPart = 32 * 128;
+        const size_t per = kPart * kEpiWarps * CG;
+        float4* parts = reinterpret_cast<float4*>(p.partial + (size_t)w.slot * per + ((size_t)rank * kEpiWarps + warp) * kPart) + lane;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            parts[(size_t)w.piece * (per / 4) + (c * 8 + q) * 32] =
+                make_float4(acc[c][4 * q], acc[c][4 * q + 1], acc[c][4 * q + 2], acc[c][4 * q + 3]);
+        __threadfence();
+        __syncwarp();
+        int* counter = p.counters + ((size_t)w.split * CG + rank) * kEpiWarps + warp;
+        int there = 0;
+        if (lane == 0) there = atomicAdd(counter, 1);
+        there = __shfl_sync(0xffffffffu, there, 0);
+        if (there != w.np - 1) continue;
+        __threadfence();
+        if (lane == 0) *counter = 0;   // for the next call
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float4 s = __ldcg(parts + (c * 8 + q) * 32);
+            for (int k = 1; k < w.np; ++k) {
+              const float4 a = __ldcg(parts + (size_t)k * (per / 4) + (c * 8 + q) * 32);
+              s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
+            }
+            acc[c][4 * q] = s.x; acc[c][4 * q + 1] = s.y; acc[c][4 * q + 2] = s.z; acc[c][4 * q + 3] = s.w;
+          }
+        }
+      }
       const int k0 = w.k0 + (int)rank * 128 + wq * 32;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -327,8 +362,7 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (w.slot >= 0) tma_store_2d(&tmp, stg_u32 + at, col, w.slot * (128 * CG) + (int)rank * 128 + wq * 32);
-          else if (w.n0 + col < p.features && k0 < p.depth) tma_store_3d(&tmo, stg_u32 + at, w.n0 + col, k0, w.e);
+          if (w.n0 + col < p.features && k0 < p.depth) tma_store_3d(&tmo, stg_u32 + at, w.n0 + col, k0, w.e);
           bulk_commit();
         }
       }
@@ -341,44 +375,6 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
   else cluster_sync();
   fence_after_sync();
   if (warp == kMmaWarp) free_tmem<CG>(tmem);
-}
-
-// Sums of the pieces' partial sums, in their order: 16 rows of a tile at a time.
-__global__ void __launch_bounds__(kSumThreads) group_dw_sum_kernel(const __grid_constant__ GroupParams p, int wide) {
-  extern __shared__ int room[];
-  const Lists l = lists_at(room, p.E);
-  pdl_wait();
-  if (!make_lists<kSumThreads>(p, l)) return;
-  const int tpg = p.kt * p.nt, units = wide / 16;
-  int i = 0, slots = 0, below = 0;   // below: split tiles of the groups before
-  const int c4 = threadIdx.x % 64 * 4, r0 = threadIdx.x / 64;
-  for (int u = blockIdx.x;; u += gridDim.x) {
-    const int split = u / units, r = u % units * 16 + r0;
-    while (i < p.E) {
-      const int np = l.start[i + 1] - l.start[i];
-      if (np > 1 && split < below + tpg) break;
-      if (np > 1) {
-        below += tpg;
-        slots += np * tpg;
-      }
-      ++i;
-    }
-    if (i == p.E) return;
-    const int np = l.start[i + 1] - l.start[i], tile = split - below, e = l.order[i];
-    const int k0 = tile / p.nt * wide, n = tile % p.nt * 256 + c4;
-    const float* src = p.partial + (size_t)(slots + tile * np) * wide * 256;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int row = r + 4 * q;
-      if (k0 + row >= p.depth || n >= p.features) continue;
-      float4 s = __ldcg(reinterpret_cast<const float4*>(src + row * 256 + c4));
-      for (int k = 1; k < np; ++k) {
-        const float4 a = __ldcg(reinterpret_cast<const float4*>(src + (size_t)k * wide * 256 + row * 256 + c4));
-        s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
-      }
-      *reinterpret_cast<float4*>(p.dw + ((size_t)e * p.depth + k0 + row) * p.features + n) = s;
-    }
-  }
 }
 
 // The shape of a call on a whole GB300 (its SMs set the size of the workspace).
@@ -395,8 +391,8 @@ DwShape dw_shape(int64_t rows, int E, int K, int N) {
   const int halves = (K + 127) / 128, pairs = (halves + 1) / 2;
   s.cg = blocks * pairs * s.nt >= kSms / 2 * 6 && (halves % 2 == 0 || halves >= 5) ? 2 : 1;
   s.kt = (K + 128 * s.cg - 1) / (128 * s.cg);
-  // a piece: half of what a CTA (a pair) has to do on average, at least 8 blocks
-  const int64_t tiles = (int64_t)s.kt * s.nt, each = ((rows + 63) / 64 * tiles + 2 * kSms / s.cg - 1) / (2 * kSms / s.cg);
+  // a piece: what a CTA (a pair) has to do on average, at least 8 blocks
+  const int64_t tiles = (int64_t)s.kt * s.nt, each = ((rows + 63) / 64 * tiles + kSms / s.cg - 1) / (kSms / s.cg);
   s.kper = (int)(each < 8 ? 8 : each);
   // a group of b > kper blocks has at most (b + kper - 1) / kper < 2 b / kper pieces a tile
   s.slots = (rows + 63) / 64 <= s.kper ? 0 : 2 * (blocks / s.kper + 1) * tiles;
@@ -404,19 +400,17 @@ DwShape dw_shape(int64_t rows, int E, int K, int N) {
 }
 
 template <int CG>
-cudaError_t launch_t(GroupParams p, const DwShape& sh, const void* x, int64_t x_stride, const void* dy, int64_t dy_stride, int sms,
+cudaError_t launch_t(GroupParams p, const void* x, int64_t x_stride, const void* dy, int64_t dy_stride, int sms,
                      cudaStream_t st) {
   const int K = p.depth, N = p.features;
-  CUtensorMap mx, mg, mo, mp;
+  CUtensorMap mx, mg, mo;
   const uint64_t xd[2] = {(uint64_t)K, (uint64_t)p.rows}, xs[1] = {(uint64_t)x_stride * 2};
   const uint64_t gd[2] = {(uint64_t)N, (uint64_t)p.rows}, gs[1] = {(uint64_t)dy_stride * 2};
   const uint64_t od[3] = {(uint64_t)N, (uint64_t)K, (uint64_t)p.E}, os[2] = {(uint64_t)N * 4, (uint64_t)N * K * 4};
-  const uint64_t pd[2] = {256, (uint64_t)(sh.slots > 0 ? sh.slots : 1) * 128 * CG}, ps[1] = {1024};
   const uint32_t ibox[2] = {64, 64}, obox[3] = {32, 32, 1};
   if (!make_tmap_tile(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, xd, xs, ibox, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_tile(&mg, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dy, gd, gs, ibox, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_tile(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p.dw, od, os, obox, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_tile(&mp, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.partial, pd, ps, obox, CU_TENSOR_MAP_SWIZZLE_128B))
+      !make_tmap_tile(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p.dw, od, os, obox, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   const size_t fixed = 1024 + kStaging + lists_bytes(p.E), stage = (size_t)boxes_of<CG>() * kBox;
   p.stages = (int)((kMaxSmemPerCta - 1024 - fixed) / stage);
@@ -427,33 +421,30 @@ cudaError_t launch_t(GroupParams p, const DwShape& sh, const void* x, int64_t x_
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)p.kt * p.nt * (p.E + p.rows / 64 / p.kper + 1);
   const unsigned grid = (unsigned)(most < sms / CG ? most : sms / CG) * CG;
-  return launch_cluster<CG>(kern, grid, kThreads, smem, st, p, mx, mg, mo, mp);
+  return launch_cluster<CG>(kern, grid, kThreads, smem, st, p, mx, mg, mo);
 }
 
 }  // namespace
 
+// counters of cut tiles (each has two slots or more), then the slots
+size_t group_dw_counters(int64_t rows, int E, int K, int N) {
+  const DwShape s = dw_shape(rows, E, K, N);
+  return ((size_t)s.slots / 2 * s.cg * kEpiWarps * sizeof(int) + kWsAlign - 1) / kWsAlign * kWsAlign;
+}
 size_t group_dw_bytes(int64_t rows, int E, int K, int N) {
   const DwShape s = dw_shape(rows, E, K, N);
-  return (size_t)s.slots * 128 * s.cg * 256 * sizeof(float);
+  return group_dw_counters(rows, E, K, N) + (size_t)s.slots * 128 * s.cg * 256 * sizeof(float);
 }
 
-cudaError_t launch_group_dw(const GroupParams& q, const void* x, int64_t x_stride, const void* dy, int64_t dy_stride, int K,
-                            int N, int sms, cudaStream_t st, int* launches) {
+cudaError_t launch_group_dw(const GroupParams& q, void* room, const void* x, int64_t x_stride, const void* dy,
+                            int64_t dy_stride, int K, int N, int sms, cudaStream_t st) {
   const DwShape s = dw_shape(q.rows, q.E, K, N);
   GroupParams p = q;
   p.features = N; p.depth = K;
   p.kt = s.kt; p.nt = s.nt; p.kper = s.kper;
-  cudaError_t e = s.cg == 2 ? launch_t<2>(p, s, x, x_stride, dy, dy_stride, sms, st)
-                            : launch_t<1>(p, s, x, x_stride, dy, dy_stride, sms, st);
-  ++*launches;
-  if (e != cudaSuccess || s.slots == 0) return e;
-  const size_t lists = lists_bytes(p.E);
-  if (lists > 48 * 1024 &&
-      (e = cudaFuncSetAttribute(group_dw_sum_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)lists)) != cudaSuccess)
-    return e;
-  e = launch_pdl(group_dw_sum_kernel, dim3((unsigned)(4 * sms)), dim3(kSumThreads), lists, st, p, 128 * s.cg);
-  ++*launches;
-  return e;
+  p.counters = static_cast<int*>(room);
+  p.partial = reinterpret_cast<float*>(static_cast<char*>(room) + group_dw_counters(q.rows, q.E, K, N));
+  return s.cg == 2 ? launch_t<2>(p, x, x_stride, dy, dy_stride, sms, st) : launch_t<1>(p, x, x_stride, dy, dy_stride, sms, st);
 }
 
 }  // namespace hstu

@@ -489,9 +489,10 @@ using namespace hstu;
 
 extern "C" {
 
-hstu_status_t hstu_group_workspace_size(const hstu_group_desc* desc, size_t* fwd, size_t* bwd) {
+hstu_status_t hstu_group_workspace_size(const hstu_group_desc* desc, size_t* fwd, size_t* bwd, size_t* zero) {
   const hstu_status_t s = check_desc(desc);
   if (s != HSTU_OK) return s;
+  if (zero) *zero = kWsHeaderBytes + group_dw_counters(desc->rows, desc->groups, desc->K, desc->N);
   if (fwd) *fwd = kWsHeaderBytes;
   if (bwd) *bwd = bwd_bytes(desc);
   return HSTU_OK;
@@ -565,8 +566,8 @@ hstu_status_t hstu_group_bwd(const hstu_group_desc* d, const hstu_group_bwd_args
       e = cudaMemsetAsync(a->dw, 0, sizeof(float) * (size_t)d->groups * d->K * d->N, st);
     } else {
       p.dw = a->dw;
-      p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kWsHeaderBytes);
-      e = launch_group_dw(p, a->x, xs, a->dy, ys, d->K, d->N, sms, st, &launches);
+      e = launch_group_dw(p, static_cast<char*>(workspace) + kWsHeaderBytes, a->x, xs, a->dy, ys, d->K, d->N, sms, st);
+      ++launches;
     }
   }
   if (e != cudaSuccess) {

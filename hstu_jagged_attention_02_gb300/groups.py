@@ -89,11 +89,11 @@ class GroupProblem:
         d.y_dtype, d.dx_dtype = _DTYPES[out_dtype], _DTYPES[dx_dtype]
         d.x_stride, d.y_stride = _step(self.x, K), _step(self.y, N)
         self.desc = d
-        fwd_b, bwd_b = C.hstu_group_workspace_size(d)
+        fwd_b, bwd_b, zero = C.hstu_group_workspace_size(d)
         need = max(fwd_b, bwd_b if backward else 0)
         if workspace is None:
             workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-            workspace[:256].zero_()
+            workspace[:zero].zero_()
         _need(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace must be contiguous uint8")
         self.ws, self.ws_bytes = workspace, workspace.numel()
         lib, at = C.load(), (self.ws.data_ptr(), self.ws_bytes)

@@ -711,11 +711,11 @@ hstu_status_t hstu_ln_bwd(const hstu_ln_desc* desc, const hstu_ln_bwd_args* args
  * elements); W and dW are dense [groups][K][N].  Up to 4096 groups.  Equal
  * inputs give equal bits.
  *
- * The workspace (256-byte aligned) starts with a 256-byte header that must be
- * zero before its first use.  Offsets that break the rules above
- * (HSTU_ERR_DEVICE_CHECK: nothing is computed) and a pipeline wait that ran
- * out (HSTU_ERR_TIMEOUT) stay in it until the caller zeroes it.  Calls that
- * overlap in time need workspaces of their own.
+ * The workspace is 256-byte aligned; its first zero_bytes (the backward's; 256 for
+ * the forward: the header) must be zero before its first use.  Offsets that break the
+ * rules above (HSTU_ERR_DEVICE_CHECK: nothing is computed) and a pipeline wait that
+ * ran out (HSTU_ERR_TIMEOUT) stay in the header; after an error the zero_bytes
+ * have to be zeroed again.  Calls that overlap in time need workspaces of their own.
  * ------------------------------------------------------------------------ */
 typedef struct {
   uint32_t struct_size;      /* sizeof(hstu_group_desc) */
@@ -748,7 +748,8 @@ typedef struct {
   float* dw;                 /* out [groups, K, N], or NULL (not wanted) */
 } hstu_group_bwd_args;
 
-hstu_status_t hstu_group_workspace_size(const hstu_group_desc* desc, size_t* fwd_bytes, size_t* bwd_bytes);
+hstu_status_t hstu_group_workspace_size(const hstu_group_desc* desc, size_t* fwd_bytes, size_t* bwd_bytes,
+                                        size_t* zero_bytes);
 hstu_status_t hstu_group_fwd(const hstu_group_desc* desc, const hstu_group_fwd_args* args, void* workspace,
                              size_t workspace_bytes, hstu_stream_t stream);
 hstu_status_t hstu_group_bwd(const hstu_group_desc* desc, const hstu_group_bwd_args* args, void* workspace,

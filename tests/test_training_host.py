@@ -110,13 +110,13 @@ def test_slots_hold_every_split(E):
     rng = np.random.default_rng(E)
     for rows in (1, 600, 5000, 40_000, 300_000):
         for K, N in ((8, 8), (128, 256), (512, 2048), (264, 520), (640, 256)):
-            ws = C.hstu_group_workspace_size(_group(groups=E, K=K, N=N, rows=rows, x_stride=K, y_stride=N, dx_stride=K))[1]
+            _, ws, zero = C.hstu_group_workspace_size(_group(groups=E, K=K, N=N, rows=rows, x_stride=K, y_stride=N, dx_stride=K))
             halves, nt = -(-K // 128), -(-N // 256)
             pair = (rows // 64 + min(rows, E)) * -(-halves // 2) * nt >= 456 and (halves % 2 == 0 or halves >= 5)
             cg = 2 if pair else 1
-            slots = (ws - 256) // (4 * 128 * cg * 256)
+            slots = (ws - zero) // (4 * 128 * cg * 256)
             tiles = -(-halves // cg) * nt
-            kper = max(8, -(-(-(-rows // 64) * tiles) // (304 // cg)))
+            kper = max(8, -(-(-(-rows // 64) * tiles) // (152 // cg)))
             for k in range(20):
                 share = rng.random(E) ** (10 if k % 2 else 1)
                 n = np.floor(rows * share / share.sum()).astype(int)
@@ -126,6 +126,7 @@ def test_slots_hold_every_split(E):
                     blocks = np.array([-(-x // 64) for x in n])
                 pieces = [-(-b // kper) if b > kper else 0 for b in blocks]
                 assert sum(pieces) * tiles <= slots
+                assert 256 + sum(1 for x in pieces if x) * tiles * cg * 8 * 4 <= zero
 
 
 def _adamw(**kw):
@@ -165,8 +166,10 @@ def test_adamw_tensors(kw, status):
 
 
 def test_adamw_workspaces():
-    assert C.hstu_adamw_workspace_size(_adamw(), _tensor()) == 256 + 80
-    assert C.hstu_adamw_workspace_size(_adamw(), _tensor(n=2049)) == 256 + 2 * 80
+    # a record of 80 bytes a chunk, of a block where there are few of them, of up to 8
+    assert C.hstu_adamw_workspace_size(_adamw(), _tensor()) == 256 + 4 * 80
+    assert C.hstu_adamw_workspace_size(_adamw(), _tensor(n=2049)) == 256 + 9 * 80
+    assert C.hstu_adamw_workspace_size(_adamw(), _tensor(n=1 << 30)) == 256 + (1 << 19) * 80
     assert C.hstu_adamw_workspace_size(_adamw(num_tensors=0), None) == 256
     for ws in ((0, 1 << 20), (PTR + 128, 1 << 20), (PTR, 256)):
         assert _status(C.hstu_adamw_init, _adamw(), _tensor(), *ws, 0) == WS
