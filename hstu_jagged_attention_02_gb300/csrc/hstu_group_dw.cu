@@ -56,26 +56,28 @@ __device__ __forceinline__ Lists lists_at(void* at, int E) {
   int* p = static_cast<int*>(at);
   return Lists{p, p + E + 1, p + 2 * (E + 1)};
 }
-constexpr size_t lists_bytes(int E) { return 4 * (3 * (size_t)E + 2); }
+constexpr size_t lists_bytes(int E) { return 4 * 3 * ((size_t)E + 1); }
 
 __device__ __forceinline__ bool make_lists(const GroupParams& p, const Lists& l) {
   if (!scan_groups<kThreads>(p, l.start, l.first, [&](int n) { return pieces(n, p.kper); })) return false;
-  // up to a group a thread: longest pieces first
   const int tid = threadIdx.x;
   if (p.E <= kRanked) {
-    int mine = 0, rank = 0, before = 0;
+    // longest pieces first
+    int np = 1, mine = 0;
     if (tid < p.E) {
-      mine = (l.first[tid + 1] - l.first[tid]) / (l.start[tid + 1] - l.start[tid]);
+      np = l.start[tid + 1] - l.start[tid];
+      mine = (l.first[tid + 1] - l.first[tid]) / np;
       l.order[tid] = mine;
     }
     __syncthreads();
+    int rank = 0, before = 0;
     if (tid < p.E) {
 #pragma unroll 4
       for (int e = 0; e < p.E; ++e) {
-        const int other = l.order[e], np = l.start[e + 1] - l.start[e];
+        const int other = l.order[e], others = l.start[e + 1] - l.start[e];
         const bool ahead = other > mine || (other == mine && e < tid);
         rank += ahead ? 1 : 0;
-        before += ahead ? np : 0;
+        before += ahead ? others : 0;
       }
     }
     __syncthreads();
@@ -94,11 +96,11 @@ __device__ __forceinline__ bool make_lists(const GroupParams& p, const Lists& l)
 // q, 2 P - 1 - q, 2 P + q, .. of P shares.
 struct Pieces {
   Lists l;
-  int tpg, nt, kper, wide, at_group, e, total, share, shares, k, t, slots, splits;   // slots, cut tiles before at_group
+  int tpg, nt, wide, at_group, e, total, share, shares, k, t, slots, splits;   // slots, cut tiles before at_group
   int k0, n0, row0, rows, blocks;
   int np, piece, slot, split;   // np > 1: the tile's first slot and its place among cut tiles
   __device__ __forceinline__ Pieces(const Lists& l_, const GroupParams& p, int width, int share_, int shares_, bool good)
-      : l(l_), tpg(p.kt * p.nt), nt(p.nt), kper(p.kper), wide(width), at_group(0), e(0), total(good ? l_.start[p.E] * p.kt * p.nt : 0),
+      : l(l_), tpg(p.kt * p.nt), nt(p.nt), wide(width), at_group(0), e(0), total(good ? l_.start[p.E] * p.kt * p.nt : 0),
         share(share_), shares(shares_), k(0), t(share_), slots(0), splits(0) {}
   __device__ __forceinline__ bool more() {
     if (t >= total) return false;
@@ -391,11 +393,23 @@ DwShape dw_shape(int64_t rows, int E, int K, int N) {
   const int halves = (K + 127) / 128, pairs = (halves + 1) / 2;
   s.cg = blocks * pairs * s.nt >= kSms / 2 * 6 && (halves % 2 == 0 || halves >= 5) ? 2 : 1;
   s.kt = (K + 128 * s.cg - 1) / (128 * s.cg);
-  // a piece: what a CTA (a pair) has to do on average, at least 8 blocks
-  const int64_t tiles = (int64_t)s.kt * s.nt, each = ((rows + 63) / 64 * tiles + kSms / s.cg - 1) / (kSms / s.cg);
-  s.kper = (int)(each < 8 ? 8 : each);
+  // a piece: what a CTA (a pair) has to do on average, at least 8 blocks; of one group, whose pieces are all alike, the
+  // length of two rounds at most that ends first, a cut tile's sums counted as 8 blocks (written, read)
+  const int64_t tiles = (int64_t)s.kt * s.nt, shares = kSms / s.cg, all = (rows + 63) / 64, each = (all * tiles + shares - 1) / shares;
+  int64_t kper = each < 8 ? 8 : each;
+  if (E == 1) {
+    int64_t best = -1;
+    for (int64_t np = 1; np * tiles <= 2 * shares && np <= all; ++np) {
+      const int64_t len = (all + np - 1) / np, cost = (np * tiles + shares - 1) / shares * (len + (np > 1 ? 8 : 0));
+      if (len >= 8 && (best < 0 || cost < best)) {
+        best = cost;
+        kper = len;
+      }
+    }
+  }
+  s.kper = (int)kper;
   // a group of b > kper blocks has at most (b + kper - 1) / kper < 2 b / kper pieces a tile
-  s.slots = (rows + 63) / 64 <= s.kper ? 0 : 2 * (blocks / s.kper + 1) * tiles;
+  s.slots = all <= kper ? 0 : 2 * (blocks / kper + 1) * tiles;
   return s;
 }
 
@@ -413,7 +427,7 @@ cudaError_t launch_t(GroupParams p, const void* x, int64_t x_stride, const void*
       !make_tmap_tile(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p.dw, od, os, obox, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   const size_t fixed = 1024 + kStaging + lists_bytes(p.E), stage = (size_t)boxes_of<CG>() * kBox;
-  p.stages = (int)((kMaxSmemPerCta - 1024 - fixed) / stage);
+  p.stages = (int)((kMaxSmemPerCta - 512 - fixed) / stage);   // (512: barriers and the scan's sums)
   if (p.stages > kStagesMax) p.stages = kStagesMax;
   const size_t smem = fixed + p.stages * stage;
   auto kern = group_dw_kernel<CG>;

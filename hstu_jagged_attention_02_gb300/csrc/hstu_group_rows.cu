@@ -385,7 +385,7 @@ cudaError_t launch_t(GroupParams p, const void* rows, int64_t row_stride, const 
   // B for the whole depth where that leaves three stages of A, else as many slots as stages
   const int64_t kblocks = (p.depth + 63) / 64;
   const size_t fixed = 1024 + staging_bytes(sizeof(TO)) + 8 * ((size_t)p.E + 1), slot = (size_t)p.row_block / CG * 128;
-  const size_t room = kMaxSmemPerCta - 1024 - fixed;   // (1 KB: barriers and the scan's sums)
+  const size_t room = kMaxSmemPerCta - 512 - fixed;   // (512: barriers and the scan's sums)
   if (kblocks <= kSlotsMax && kblocks * slot + 3 * (size_t)kABytes <= room) {
     p.slots = (int)kblocks;
     p.stages = (int)((room - kblocks * slot) / kABytes);

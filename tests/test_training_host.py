@@ -104,7 +104,7 @@ def test_group_calls(bwd, desc, kw, ws, status):
     assert _status(fn, _group(**desc), _full(cls, **kw), *ws, 0) == status
 
 
-@pytest.mark.parametrize("E", [1, 2, 7, 60])
+@pytest.mark.parametrize("E", [2, 7, 60])
 def test_slots_hold_every_split(E):
     """The workspace's partial sums suffice for any offsets: pieces as the kernel cuts them."""
     rng = np.random.default_rng(E)
