@@ -227,6 +227,10 @@ class AttentionWorkload:
     n_batches = N_SEEDS
     dropout_p = 0.0   # --dropout: the fused dropout on y (fixed seed and offset)
     plan_once = True  # the forward plans the backward too (--plan-each-call: each call plans for itself)
+    optimizer = None  # --optimizer: what a layer's step ends with
+
+    def make_optimizer(self, pr):
+        return None
 
     def dropout(self):
         return None if not self.dropout_p else (self.dropout_p, 20240601, 0)
@@ -306,6 +310,11 @@ class LayerWorkload(AttentionWorkload):
     def problem(self, b, dev):
         from hstu_jagged_attention_02_gb300.layer import LayerProblem
         return LayerProblem(b, device=dev, dropout=self.dropout())
+
+    def make_optimizer(self, pr):
+        if self.optimizer is None:
+            return None
+        return pr.optimizer(lr=1e-4, weight_decay=0.01, state_bits=8 if self.optimizer == "adamw8" else 32)
 
     def flops(self, b):
         f, bw = useful_flops(b)
@@ -486,6 +495,7 @@ def run_gpu(args, wl, rank, world, local_rank):
     batches = wl.batches(rank)
     nb = len(batches)
     probs = [wl.problem(b, dev) for b in batches]
+    opts = [wl.make_optimizer(pr) for pr in probs]
     flops = [wl.flops(b) for b in batches]
     stream = torch.cuda.current_stream()
 
@@ -506,7 +516,11 @@ def run_gpu(args, wl, rank, world, local_rank):
         if ev is not None and "bwd" in roles:
             C.hstu_time_next_attention_kernel(ev[2].cuda_event, ev[3].cuda_event)
         pr.backward()
-        return n + C.hstu_last_launch_count()
+        n += C.hstu_last_launch_count()
+        if opts[i % nb] is not None:
+            opts[i % nb].step()
+            n += C.hstu_last_launch_count()
+        return n
 
     t_w = time.perf_counter()
     for w in range(max(args.warmup, 0)):
@@ -593,10 +607,10 @@ def run_gpu(args, wl, rank, world, local_rank):
         elapsed_ms, tot_flops = dp.reduce_step_time(elapsed_ms, tot_flops, device=dev)
 
     # ---- end to end through the C ABI with host buffers
-    e2e = run_e2e(args, wl, probs, flops, stream, world)
+    e2e = run_e2e(args, wl, probs, flops, stream, world, opts=opts)
     e2e["read_back"] = "the step's result: " + ("the candidates' outputs" if not wl.has_backward
                                                  else "the parameter gradients (activation gradients stay on the device)")
-    e2e_all = run_e2e(args, wl, probs, flops, stream, world, all_outputs=True)
+    e2e_all = run_e2e(args, wl, probs, flops, stream, world, all_outputs=True, opts=opts)
     e2e["all_outputs"] = {k: e2e_all[k] for k in ("value", "d2h_bytes_per_step", "ms_per_step", "repeats")}
 
     if rank != 0:
@@ -649,6 +663,8 @@ def run_gpu(args, wl, rank, world, local_rank):
                      else "stream launches")
     if wl.dropout_p:
         cfg["dropout_p"] = wl.dropout_p
+    if wl.optimizer:
+        cfg["optimizer"] = wl.optimizer
     cfg.update({"per_rank_batches": nb, "mean_tokens_per_batch": float(np.mean([b.T for b in batches]))})
     line = {"metric": wl.metric, "value": value, "unit": UNIT, "n_gpus": world, "steps": args.steps,
             "warmup": args.warmup, "ms_per_step": elapsed_ms / args.steps, "higher_is_better": True,
@@ -669,7 +685,7 @@ def run_gpu(args, wl, rank, world, local_rank):
     print(json.dumps(line), flush=True)
 
 
-def run_e2e(args, wl, probs, flops, stream, world, all_outputs=False):
+def run_e2e(args, wl, probs, flops, stream, world, all_outputs=False, opts=None):
     """Same metric through the public C ABI with pinned host buffers: each step
     copies its inputs host -> device, runs forward + backward and copies the
     step's result back: the parameter gradients of a training step (the
@@ -713,6 +729,8 @@ def run_e2e(args, wl, probs, flops, stream, world, all_outputs=False):
         pr.forward(stream)
         if wl.has_backward:
             pr.backward(stream)
+        if opts is not None and opts[j] is not None:
+            opts[j].step(stream)
         computed = torch.cuda.Event()
         computed.record(stream)
         with torch.cuda.stream(down):
@@ -777,6 +795,8 @@ def main():
                     help="capture the timed steps as a CUDA graph and time its replay")
     ap.add_argument("--dropout", type=float, default=0.0,
                     help="fused dropout probability on y (heavy_tailed and layer workloads)")
+    ap.add_argument("--optimizer", default="none", choices=["none", "adamw", "adamw8"],
+                    help="layer workload: an AdamW step over the layer's parameters ends each step (moments in 32 or 8 bits)")
     ap.add_argument("--plan-each-call", action="store_true",
                     help="heavy_tailed: the forward and the backward each run their own planner")
     args = ap.parse_args()
@@ -787,6 +807,10 @@ def main():
         if not wl.has_backward:
             ap.error("--dropout applies to training workloads only")
         wl.dropout_p = args.dropout
+    if args.optimizer != "none":
+        if args.workload != "layer":
+            ap.error("--optimizer applies to the layer workload only")
+        wl.optimizer = args.optimizer
     if args.warmup < 3:
         args.warmup = 3
     world = int(os.environ.get("WORLD_SIZE", "1"))

@@ -88,3 +88,24 @@ class LayerProblem:
 
     def device_error(self, stream=None) -> int:
         return C.hstu_get_device_error(self.ws.data_ptr(), _stream_handle(stream))
+
+    def optimizer(self, **how):
+        """AdamW (optim.py, which takes how: lr, betas, weight_decay, state_bits,
+        ..) for this layer's parameters: FP32 masters of w1 and w2, made here,
+        whose BF16 copies are the layer's own w1 and w2, and the bias tables
+        where their gradients are wanted.  step() after backward() changes what
+        the next forward() reads.  A list weight_decay or lr_scale is in the order
+        w1, w2, rab_pos, rab_time; by default the bias tables do not decay."""
+        from .optim import AdamW
+        if not self.backward_enabled:
+            raise ValueError("a layer without a backward has no gradients to step by")
+        params, grads, copies = [self.w1.float(), self.w2.float()], [self.dw1, self.dw2], [self.w1, self.w2]
+        for table, grad in ((self.rab_pos, self.d_rab_pos), (self.rab_time, self.d_rab_time)):
+            if table is not None and grad is not None:
+                params.append(table)
+                grads.append(grad)
+                copies.append(None)
+        decay = how.pop("weight_decay", 0.0)
+        if isinstance(decay, (int, float)):
+            decay = [decay, decay] + [0.0] * (len(params) - 2)
+        return AdamW(params, grads, copies=copies, weight_decay=decay, **how)

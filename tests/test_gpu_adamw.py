@@ -79,6 +79,36 @@ def test_steps(bits, grad):
     assert opt.steps() == 4 and opt.device_error() == 0
 
 
+@pytest.mark.parametrize("sizes", [(8_000_003, 300_000), (1000, 33_000_001, 5)])
+def test_long_lists(sizes):
+    """Chunks of several blocks: codes, moments and parameters of some blocks of every tensor."""
+    from hstu_jagged_attention_02_gb300.optim import AdamW
+    for bits in (8, 32):
+        params, grads = _tensors(sizes, 11)
+        before = [p.clone() for p in params]
+        opt = AdamW(params, grads, state_bits=bits, seed=77, **HYPER)
+        opt.step()
+        assert opt.device_error() == 0
+        block, rng = 0, np.random.default_rng(1)
+        for p, q, g, mom in zip(params, before, grads, opt.moments):
+            blocks = (p.numel() + 255) // 256
+            for k in sorted({0, blocks - 1, *rng.integers(0, blocks, 60).tolist()}):
+                at = slice(k * 256, min(p.numel(), k * 256 + 256))
+                zero = np.zeros(at.stop - at.start, np.float32)
+                m, v = R.moments(zero, zero, _np(g[at]), 0.9, 0.999)
+                want, moved = R.adamw(_np(q[at]).astype(np.float64), m.astype(np.float64), v.astype(np.float64), 1, 1e-3, 0.9,
+                                      0.999, 1e-8, 0.0)
+                assert np.all(np.abs(_np(p[at]) - want) <= 2.0 ** -22 * np.abs(want) + 2.0 ** -19 * moved)
+                if bits == 32:
+                    assert np.array_equal(_np(mom[0][at]), m) and np.array_equal(_np(mom[1][at]), v)
+                    continue
+                word = R.words(block + k, m.size, 1, 77)
+                for x, codes, exps, kind in ((m, mom.m, mom.m_exp, "m"), (v, mom.v, mom.v_exp, "v")):
+                    code, e = R.encode(x, word, kind)
+                    assert np.array_equal(codes[at].cpu().numpy(), code) and int(exps[k]) == int(e[0])
+            block += blocks
+
+
 def test_8_bit_moments_keep_their_means():
     """Without gradients v decays by a thousandth a step, far below half a step of its format.  A
     value's rounding moves it by at most an eighth of itself with variance at most (1/16)^2 of it a step:

@@ -76,6 +76,36 @@ def test_forward_and_backward(sizes, K, N, yt, dxt):
     _check_all(pr, x, w, off, dy, yt, dxt)
 
 
+@pytest.mark.parametrize("sizes,K,N,yt,dxt", [
+    ((1, 0, 20_000, 300, 37, 9_999, 64, 65, 9_000), 512, 512, "bf16", "bf16"),    # rows stay in shared memory (K), stream (N)
+    ((30_011, 2), 264, 1032, "fp32", "fp32"), ((12_345, 23_456), 1096, 640, "bf16", "fp32"),
+    ((700,) * 40, 320, 2048, "bf16", "bf16"), ((40_000,), 64, 768, "fp32", "bf16"),
+    (tuple(200 + 37 * i for i in range(60)), 520, 264, "bf16", "bf16"),
+])
+def test_large_batches(sizes, K, N, yt, dxt):
+    """CTAs in pairs, groups cut into pieces; compared on the GPU in 64 bits."""
+    from hstu_jagged_attention_02_gb300.groups import GroupProblem
+    x, w, off, dy = _inputs(sizes, K, N, seed=K + N + len(sizes))
+    pr = GroupProblem(x, w, off, out_dtype=TYPES[yt], dy=dy, dx_dtype=TYPES[dxt])
+    for t in (pr.y, pr.dx, pr.dw):
+        t.fill_(float("nan"))
+    pr.forward()
+    pr.backward()
+    assert pr.device_error() == 0
+    near = lambda got, want, size, half, n: bool(((got.double() - want).abs() <= half * want.abs() + _loss(n) * size).all())  # noqa: E731
+    o = off.tolist()
+    for g, (a, b) in enumerate(zip(o, o[1:])):
+        xs, ws, gs = x[a:b].double(), w[g].double(), dy[a:b].double()
+        assert near(pr.y[a:b], xs @ ws, xs.abs() @ ws.abs(), HALF[yt], K), (g, "y")
+        assert near(pr.dx[a:b], gs @ ws.T, gs.abs() @ ws.abs().T, HALF[dxt], N), (g, "dx")
+        assert near(pr.dw[g], xs.T @ gs, xs.abs().T @ gs.abs(), 2.0 ** -24, b - a), (g, "dw")
+    first = [t.clone() for t in (pr.y, pr.dx, pr.dw)]
+    for _ in range(3):
+        pr.forward()
+        pr.backward()
+    assert all(torch.equal(t, f) for t, f in zip((pr.y, pr.dx, pr.dw), first))
+
+
 def test_many_groups():
     from hstu_jagged_attention_02_gb300.groups import GroupProblem
     rng = np.random.default_rng(1)
