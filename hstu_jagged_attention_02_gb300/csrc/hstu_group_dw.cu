@@ -340,16 +340,27 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
         if (there != w.np - 1) continue;
         __threadfence();
         if (lane == 0) *counter = 0;   // for the next call
+        // (this warp's own sums are among them)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            float4 s = __ldcg(parts + (c * 8 + q) * 32);
-            for (int k = 1; k < w.np; ++k) {
-              const float4 a = __ldcg(parts + (size_t)k * (per / 4) + (c * 8 + q) * 32);
-              s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
+          for (int q = 0; q < 32; ++q) acc[c][q] = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < w.np; ++k) {
+          const float4* part = parts + (size_t)k * (per / 4);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float4 v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = __ldcg(part + (c * 4 + q) * 32);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float* a = &acc[c / 2][c % 2 * 16 + 4 * q];
+              a[0] += v[q].x;
+              a[1] += v[q].y;
+              a[2] += v[q].z;
+              a[3] += v[q].w;
             }
-            acc[c][4 * q] = s.x; acc[c][4 * q + 1] = s.y; acc[c][4 * q + 2] = s.z; acc[c][4 * q + 3] = s.w;
           }
         }
       }
@@ -393,15 +404,18 @@ DwShape dw_shape(int64_t rows, int E, int K, int N) {
   const int halves = (K + 127) / 128, pairs = (halves + 1) / 2;
   s.cg = blocks * pairs * s.nt >= kSms / 2 * 6 && (halves % 2 == 0 || halves >= 5) ? 2 : 1;
   s.kt = (K + 128 * s.cg - 1) / (128 * s.cg);
-  // a piece: what a CTA (a pair) has to do on average, at least 8 blocks; of one group, whose pieces are all alike, the
+  // A piece: what a CTA (a pair) has to do on average, and not so little that adding up the pieces (2 to 3 us each, one
+  // after the other) takes longer than they do (0.6 us a block): at least 2 sqrt(blocks); of one group, whose pieces are all alike, the
   // length of two rounds at most that ends first, a cut tile's sums counted as 8 blocks (written, read)
   const int64_t tiles = (int64_t)s.kt * s.nt, shares = kSms / s.cg, all = (rows + 63) / 64, each = (all * tiles + shares - 1) / shares;
-  int64_t kper = each < 8 ? 8 : each;
+  int64_t least = 8;
+  while (least * least < 4 * all) ++least;
+  int64_t kper = each < least ? least : each;
   if (E == 1) {
     int64_t best = -1;
     for (int64_t np = 1; np * tiles <= 2 * shares && np <= all; ++np) {
       const int64_t len = (all + np - 1) / np, cost = (np * tiles + shares - 1) / shares * (len + (np > 1 ? 8 : 0));
-      if (len >= 8 && (best < 0 || cost < best)) {
+      if (len >= least && (best < 0 || cost < best)) {
         best = cost;
         kper = len;
       }

@@ -1,7 +1,7 @@
 // Layer norm with weight and bias: what the forward (hstu_ln_fwd.cu) and the
 // backward (hstu_ln_bwd.cu) share.
 //
-// A row lies in the registers of a team, a warp or (from 1,024 features on) a
+// A row lies in the registers of a team, 8 lanes to a warp or (from 1,024 features on) a
 // CTA: thread l of a team of L has the features (i L + l) V + [0, V) for i < N,
 // V = 8 where rows are 16-byte aligned (16 or 32 bytes a load, a warp's loads
 // cover 256 features), else 1 (a warp's load covers 32 neighbouring features).
@@ -94,7 +94,7 @@ __device__ __forceinline__ void put(T* p, const float (&v)[1]) { *p = from_f<T>(
 template <int L>
 __device__ __forceinline__ float2 team_sum(float2 v, float2* red) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = (L < 32 ? L : 32) / 2; o > 0; o >>= 1) {
     v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
     v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
   }
@@ -122,6 +122,8 @@ template <int V, int L, int N> struct Shape {
 template <typename F>
 auto dispatch_shape(int D, bool wide, F&& go) {
   if (wide) {
+    if (D <= 64) return go(Shape<8, 8, 1>());
+    if (D <= 128) return go(Shape<8, 16, 1>());
     if (D <= 256) return go(Shape<8, 32, 1>());
     if (D <= 512) return go(Shape<8, 32, 2>());
     if (D <= 1024) return go(Shape<8, 32, 4>());
@@ -129,7 +131,8 @@ auto dispatch_shape(int D, bool wide, F&& go) {
     if (D <= 8192) return go(Shape<8, 256, 4>());
     return go(Shape<8, 512, 4>());
   }
-  if (D <= 128) return go(Shape<1, 32, 4>());
+  if (D <= 32) return go(Shape<1, 8, 4>());
+  if (D <= 128) return go(Shape<1, 16, 8>());
   if (D <= 320) return go(Shape<1, 32, 10>());
   if (D <= 512) return go(Shape<1, 32, 16>());
   if (D <= 1024) return go(Shape<1, 32, 32>());
@@ -138,7 +141,7 @@ auto dispatch_shape(int D, bool wide, F&& go) {
 }
 
 constexpr int kMaxD = 16384;
-constexpr int kWarpTeams = 8;   // warps of a CTA whose teams are warps
+constexpr int kTeamsThreads = 256;   // threads of a CTA whose teams are warps or parts of them
 
 }  // namespace ln
 

@@ -16,7 +16,7 @@ namespace {
 
 using namespace ln;
 
-// A CTA an SM, cut into teams of 32 to 512 threads: 16 warps leave 128 registers a thread, of which a lane's sums
+// A CTA an SM, cut into teams of 8 to 512 threads: 16 warps leave 128 registers a thread, of which a lane's sums
 // take 2 N V.  Short rows are read one ahead of the row that is worked on, and keep the weight in registers.
 constexpr int kBwdThreads = 512;
 
@@ -24,7 +24,7 @@ constexpr int kBwdThreads = 512;
 template <int L>
 __device__ __forceinline__ float2 team_sum_of(float2 v, float2* red, int team) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = (L < 32 ? L : 32) / 2; o > 0; o >>= 1) {
     v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
     v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
   }
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const __grid_con
   extern __shared__ float sums[];   // [teams][2][D]
   constexpr int TEAMS = kBwdThreads / L, E = N * V;
   static_assert(E % 2 == 0, "features are worked on in pairs");
-  __shared__ float2 red[2][TEAMS][L / 32];
+  __shared__ float2 red[2][L <= 32 ? 1 : TEAMS][L <= 32 ? 1 : L / 32];
   // registers of a row as it is read; the weight is kept where it finds room beside 5 E of sums and of the row
   constexpr int RAW = N * (V == 1 ? 2 : (int)(sizeof(TX) + sizeof(TY)) * 2);
   constexpr bool KEEP = E <= 16, AHEAD = 4 * E + (KEEP ? E : 0) + RAW <= 100, TWICE = E > 16;
@@ -100,7 +100,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const __grid_con
   };
   int64_t r = (int64_t)blockIdx.x * TEAMS + team;
   fetch(r);
-  for (; r < rows; r += step) {
+  // (the teams of a warp go on together: one without a row has zeros for dy and stores nothing)
+  const int ahead = L < 32 ? (threadIdx.x & 31) / L : 0;
+  for (; r - ahead < rows; r += step) {
+    const int D = L >= 32 || r < rows ? p.D : 0;
+    if (L < 32 && D == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        rx[i] = Pack<TX, V>();
+        rg[i] = Pack<TY, V>();
+      }
+      mean = rstd = 0.f;
+    }
     TX* dx = static_cast<TX*>(p.dx) + r * p.dxs;
     const TX* dres = static_cast<const TX*>(p.dres) + r * p.drs;
     auto store = [&](int i, float (&o)[V]) {
@@ -144,7 +155,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const __grid_con
         s0 = __fadd2_rn(s0, t[k]);
         s1 = __ffma2_rn(t[k], h[k], s1);
       }
-      const float2 s = team_sum_of<L>(make_float2(s0.x + s0.y, s1.x + s1.y), red[turn][team], team);
+      const float2 s = team_sum_of<L>(make_float2(s0.x + s0.y, s1.x + s1.y), red[turn][L <= 32 ? 0 : team], team);
       // dx = rstd (t - m0 - h m1)
       const float a1 = -s.y * inv * rstd_r, b1 = -s.x * inv * rstd_r;
       const float2 a = make_float2(a1, a1), b = make_float2(b1, b1);
@@ -152,7 +163,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const __grid_con
       for (int k = 0; k < E / 2; ++k) t[k] = __ffma2_rn(t[k], scale, __ffma2_rn(h[k], a, b));
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (at(i) < p.D) {
+        if (at(i) < D) {
           float o[V];
 #pragma unroll
           for (int e = 0; e < V; ++e) o[e] = (i * V + e) % 2 ? t[(i * V + e) / 2].y : t[(i * V + e) / 2].x;
@@ -178,7 +189,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const __grid_con
       float2 s = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (at(i) < p.D) {
+        if (at(i) < D) {
           float h[V], g[V], t[V];
           part(i, h, g, t);
 #pragma unroll
@@ -193,11 +204,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const __grid_con
           }
         }
       }
-      s = team_sum_of<L>(s, red[turn][team], team);
+      s = team_sum_of<L>(s, red[turn][L <= 32 ? 0 : team], team);
       const float a = -s.y * inv * rstd_r, b = -s.x * inv * rstd_r;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (at(i) < p.D) {
+        if (at(i) < D) {
           float h[V], g[V], t[V];
           part(i, h, g, t);
 #pragma unroll
@@ -270,6 +281,8 @@ ln_sum_kernel(const float* __restrict__ partial, int rows, int D, float* d_weigh
 template <typename F>
 auto dispatch_bwd_shape(int D, bool wide, F&& go) {
   if (wide) {
+    if (D <= 64) return go(Shape<8, 8, 1>());
+    if (D <= 128) return go(Shape<8, 16, 1>());
     if (D <= 256) return go(Shape<8, 32, 1>());
     if (D <= 512) return go(Shape<8, 32, 2>());
     if (D <= 1024) return go(Shape<8, 128, 1>());
@@ -278,7 +291,8 @@ auto dispatch_bwd_shape(int D, bool wide, F&& go) {
     if (D <= 8192) return go(Shape<8, 512, 2>());
     return go(Shape<8, 512, 4>());
   }
-  if (D <= 128) return go(Shape<1, 32, 4>());
+  if (D <= 32) return go(Shape<1, 8, 4>());
+  if (D <= 128) return go(Shape<1, 16, 8>());
   if (D <= 320) return go(Shape<1, 32, 10>());
   if (D <= 1024) return go(Shape<1, 128, 8>());
   if (D <= 4096) return go(Shape<1, 512, 8>());

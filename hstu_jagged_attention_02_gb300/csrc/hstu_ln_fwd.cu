@@ -12,25 +12,26 @@ namespace {
 using namespace ln;
 
 template <typename TX, typename TY, int V, int L, int N>
-__global__ void __launch_bounds__(L == 32 ? 32 * kWarpTeams : L) ln_fwd_kernel(const __grid_constant__ LnParams p) {
-  __shared__ float2 red[2][L / 32];
-  constexpr int TEAMS = L == 32 ? kWarpTeams : 1;
+__global__ void __launch_bounds__(L <= 32 ? kTeamsThreads : L) ln_fwd_kernel(const __grid_constant__ LnParams p) {
+  __shared__ float2 red[2][L <= 32 ? 1 : L / 32];
+  constexpr int TEAMS = L <= 32 ? kTeamsThreads / L : 1;
   pdl_wait();
-  const int64_t r = (int64_t)blockIdx.x * TEAMS + (L == 32 ? threadIdx.x >> 5 : 0);
-  if (r >= live_rows(p)) return;
-  const int l = threadIdx.x % L;
+  const int64_t r = (int64_t)blockIdx.x * TEAMS + (L <= 32 ? threadIdx.x / L : 0), rows = live_rows(p);
+  // (a warp goes on while one of its teams has a row)
+  if (r - (L < 32 ? (threadIdx.x & 31) / L : 0) >= rows) return;
+  const int l = threadIdx.x % L, D = L >= 32 || r < rows ? p.D : 0;
   const TX* x = static_cast<const TX*>(p.x) + r * p.xs;
   Pack<TX, V> raw[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int f = (i * L + l) * V;
-    if (f < p.D) raw[i].load(x + f);
+    if (f < D) raw[i].load(x + f);
   }
   float v[N][V];
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    if ((i * L + l) * V < p.D) {
+    if ((i * L + l) * V < D) {
       raw[i].get(v[i]);
 #pragma unroll
       for (int e = 0; e < V; ++e) s += v[i][e];
@@ -44,7 +45,7 @@ __global__ void __launch_bounds__(L == 32 ? 32 * kWarpTeams : L) ln_fwd_kernel(c
   float q = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    if ((i * L + l) * V < p.D) {
+    if ((i * L + l) * V < D) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         v[i][e] -= mean;
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(L == 32 ? 32 * kWarpTeams : L) ln_fwd_kernel(c
     }
   }
   const float rstd = rsqrtf(fmaf(team_sum<L>(q, red[1]), inv, p.eps));
-  if (l == 0) {
+  if (l == 0 && D > 0) {
     if (p.mean) p.mean[r] = mean;
     if (p.rstd) p.rstd[r] = rstd;
   }
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(L == 32 ? 32 * kWarpTeams : L) ln_fwd_kernel(c
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int f = (i * L + l) * V;
-    if (f < p.D) {
+    if (f < D) {
       Pack<float, V> c;
       float w[V], b[V];
       if (p.weight) { c.load(p.weight + f); c.get(w); }
@@ -82,9 +83,9 @@ template <typename TX, typename TY>
 cudaError_t launch_t(const LnParams& p, bool wide, cudaStream_t st) {
   return dispatch_shape(p.D, wide, [&](auto S) {
     using Sh = decltype(S);
-    constexpr int TEAMS = Sh::l == 32 ? kWarpTeams : 1;
+    constexpr int TEAMS = Sh::l <= 32 ? kTeamsThreads / Sh::l : 1;
     return launch_pdl(ln_fwd_kernel<TX, TY, Sh::v, Sh::l, Sh::n>, dim3((unsigned)((p.rows + TEAMS - 1) / TEAMS)),
-                      dim3(Sh::l == 32 ? 32 * kWarpTeams : Sh::l), 0, st, p);
+                      dim3(Sh::l <= 32 ? kTeamsThreads : Sh::l), 0, st, p);
   });
 }
 

@@ -116,7 +116,7 @@ def test_slots_hold_every_split(E):
             cg = 2 if pair else 1
             slots = (ws - zero) // (4 * 128 * cg * 256)
             tiles = -(-halves // cg) * nt
-            kper = max(8, -(-(-(-rows // 64) * tiles) // (152 // cg)))
+            kper = max(8, int(np.ceil(2 * np.sqrt(-(-rows // 64)))), -(-(-(-rows // 64) * tiles) // (152 // cg)))
             for k in range(20):
                 share = rng.random(E) ** (10 if k % 2 else 1)
                 n = np.floor(rows * share / share.sum()).astype(int)
