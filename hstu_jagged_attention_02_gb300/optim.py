@@ -9,7 +9,7 @@ import torch
 from . import binding as C
 from .attention import _ptr
 from .norm import _DTYPES
-from .qk import Launch, _need, _same_device, device_error
+from .qk import Launch, _need, device_error
 
 BLOCK = 256   # elements that share an exponent byte
 
@@ -33,10 +33,6 @@ def zero_moments(param, bits: int = 32):
     byte = dict(device=dev, dtype=torch.uint8)
     return Moments8(*(torch.zeros(n, **byte) for _ in range(2)),
                     *(torch.full(((n + BLOCK - 1) // BLOCK,), 16, **byte) for _ in range(2)))
-
-
-def _span(t):
-    return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
 
 
 class AdamW:
@@ -80,22 +76,30 @@ class AdamW:
             grad_dtype = next((g.dtype for g in self.grads if g is not None), torch.float32)
         _need(grad_dtype in _DTYPES, f"gradients must be BF16 or FP32, got {grad_dtype}")
         self.grad_dtype = grad_dtype
-        spans = []
+        spans, rows = [], []
+        half = torch.uint8 if bits == 8 else torch.float32
         for i, (p, c, m) in enumerate(zip(self.params, self.copies, self.moments)):
-            _same_device(dev, param=p, copy=c, **{f"moments[{k}]": t for k, t in enumerate(m)})
-            _need(p.dtype == torch.float32 and p.is_contiguous() and p.data_ptr() % 16 == 0,
-                  f"parameter {i} must be contiguous FP32, 16-byte aligned")
-            _need(c is None or (c.dtype == torch.bfloat16 and c.numel() == p.numel() and c.is_contiguous() and
-                                c.data_ptr() % 8 == 0), f"copy {i} must be contiguous BF16 of its parameter's size")
-            _need(isinstance(m, Moments8) == (bits == 8), "all moments have 32 bits, or all 8")
-            for t in m[:2]:
-                _need(t.numel() == p.numel() and t.is_contiguous() and t.dtype == (torch.uint8 if bits == 8 else torch.float32)
-                      and t.data_ptr() % 16 == 0, f"moments {i} do not match their parameter")
-            for t in m[2:]:
-                _need(t.numel() == (p.numel() + BLOCK - 1) // BLOCK and t.is_contiguous() and t.dtype == torch.uint8,
-                      f"moments {i} need a byte for every {BLOCK} elements")
-            spans += [_span(t) for t in (p, c, *m) if t is not None and t.numel()]
-        spans.sort()
+            n_i, at = p.numel(), p.data_ptr()
+            if p.device != dev or p.dtype != torch.float32 or not p.is_contiguous() or at % 16:
+                raise ValueError(f"parameter {i} must be contiguous FP32 on {dev}, 16-byte aligned")
+            spans.append((at, at + 4 * n_i))
+            c_at = None
+            if c is not None:
+                c_at = c.data_ptr()
+                if c.device != dev or c.dtype != torch.bfloat16 or c.numel() != n_i or not c.is_contiguous() or c_at % 8:
+                    raise ValueError(f"copy {i} must be contiguous BF16 of its parameter's size, on {dev}")
+                spans.append((c_at, c_at + 2 * n_i))
+            if isinstance(m, Moments8) != (bits == 8):
+                raise ValueError("all moments have 32 bits, or all 8")
+            m_at = [t.data_ptr() for t in m]
+            blocks = (n_i + BLOCK - 1) // BLOCK
+            for k, t in enumerate(m):
+                size, kind = (n_i, half) if k < 2 else (blocks, torch.uint8)
+                if t.device != dev or t.dtype != kind or t.numel() != size or not t.is_contiguous() or (k < 2 and m_at[k] % 16):
+                    raise ValueError(f"moments {i} do not match their parameter ({'values' if k < 2 else f'a byte for every {BLOCK}'})")
+                spans.append((m_at[k], m_at[k] + size * t.element_size()))
+            rows.append((at, c_at, m_at, n_i))
+        spans = sorted(x for x in spans if x[1] > x[0])
         _need(all(a[1] <= b[0] for a, b in zip(spans, spans[1:])), "parameters, copies and moments must not overlap")
         for i, g in enumerate(self.grads):
             self._check_grad(i, g)
@@ -111,9 +115,9 @@ class AdamW:
         d.seed, d.steps_done = int(seed) & 0xFFFFFFFFFFFFFFFF, int(steps)
         self.desc = d
         self._table = (C.hstu_adamw_tensor * n)()
-        for i, (p, c, m) in enumerate(zip(self.params, self.copies, self.moments)):
-            self._table[i] = C.hstu_adamw_tensor(_ptr(p), _ptr(self.grads[i]), _ptr(c), *(_ptr(t) for t in m),
-                                                 *([None] * (4 - len(m))), p.numel(), wd[i], ls[i])
+        for i, (at, c_at, m_at, n_i) in enumerate(rows):
+            self._table[i] = C.hstu_adamw_tensor(at or None, _ptr(self.grads[i]), c_at, *m_at, *([None] * (4 - len(m_at))), n_i,
+                                                 wd[i], ls[i])
         _need(steps >= 0, "steps must not be negative")
         need = C.hstu_adamw_workspace_size(d, self._table)
         self.ws, self.ws_bytes = torch.zeros(need, device=dev, dtype=torch.uint8), need
@@ -126,9 +130,9 @@ class AdamW:
         if g is None:
             return
         p = self.params[i]
-        _need(g.device == p.device and g.numel() == p.numel() and g.dtype == self.grad_dtype and g.is_contiguous() and
-              g.data_ptr() % 16 == 0,
-              f"gradient {i} must be contiguous {self.grad_dtype} of its parameter's size, 16-byte aligned")
+        if (g.device != p.device or g.numel() != p.numel() or g.dtype != self.grad_dtype or not g.is_contiguous() or
+                g.data_ptr() % 16):
+            raise ValueError(f"gradient {i} must be contiguous {self.grad_dtype} of its parameter's size, 16-byte aligned")
 
     @property
     def lr(self):
@@ -195,8 +199,9 @@ class MomentsReader:
         for p, pair in zip(optimizer.params, self.outs):
             _need(len(pair) == 2, "a pair (m, v) for each tensor")
             for t in pair:
-                _need(t is None or (t.device == dev and t.dtype == dtype and t.numel() == p.numel() and t.is_contiguous() and
-                                    t.data_ptr() % 16 == 0), "a moment's values must be contiguous, 16-byte aligned, of one type")
+                if t is not None and (t.device != dev or t.dtype != dtype or t.numel() != p.numel() or not t.is_contiguous() or
+                                      t.data_ptr() % 16):
+                    raise ValueError("a moment's values must be contiguous, 16-byte aligned, of one type")
         d = C.hstu_adamw_desc.from_buffer_copy(optimizer.desc)
         self.desc = d
         table = (C.hstu_adamw_moments * len(self.outs))(*(C.hstu_adamw_moments(_ptr(a), _ptr(b)) for a, b in self.outs))
