@@ -7,6 +7,8 @@
 // row blocks (or of pieces of work) into shared memory, of which each role
 // walks its share with a cursor.
 #pragma once
+#include <atomic>
+
 #include "hstu_internal.h"
 #include "tc_ptx.cuh"
 
@@ -104,6 +106,22 @@ __device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* ma
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+// the same into all CTAs of the mask, at the same places; counts on the barrier of each one's pair
+__device__ __forceinline__ void pair_load_2d_multi(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, uint16_t mask) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 [%0], [%1, "
+      "{%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "h"(mask)
+      : "memory");
+}
+__device__ __forceinline__ void pair_load_3d_multi(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                                   uint16_t mask) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 [%0], [%1, "
+      "{%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "h"(mask)
+      : "memory");
+}
 template <int CG> __device__ __forceinline__ void alloc_tmem(uint32_t dst) {
   if constexpr (CG == 1) {
     tmem_alloc(dst, 512);
@@ -128,12 +146,12 @@ template <int CG> __device__ __forceinline__ void mma(uint32_t d, SDesc a, SDesc
         : "memory");
   }
 }
-// arrives on the barrier (of both CTAs of a pair) when every tcgen05 operation so far has completed
-template <int CG> __device__ __forceinline__ void commit(uint32_t bar) {
+// arrives on the barrier (of all CTAs of the mask) when every tcgen05 operation so far has completed
+template <int CG> __device__ __forceinline__ void commit(uint32_t bar, uint16_t mask) {
   if constexpr (CG == 1) mma_commit(bar);
   else
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-                 "h"((uint16_t)3)
+                 "h"(mask)
                  : "memory");
 }
 
@@ -215,7 +233,7 @@ __device__ __forceinline__ bool scan_groups(const GroupParams& p, int* start, in
   return true;
 }
 
-// A launch as launch_pdl makes it, of pairs of CTAs where CG is 2.
+// A launch as launch_pdl makes it, in clusters of CG CTAs.
 template <int CG, typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, int threads, size_t smem, cudaStream_t st, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
@@ -232,6 +250,32 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, int threads,
   cfg.attrs = attr;
   cfg.numAttrs = CG == 1 ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Clusters of CG such CTAs that run at once on the current device (a GPC whose SMs are no multiple of CG leaves
+// some idle), looked up once a kernel: *known starts as 0.
+template <int CG, typename... KArgs>
+cudaError_t clusters_at_once(void (*kernel)(KArgs...), int threads, size_t smem, int sms, std::atomic<int>* known, int* count) {
+  *count = sms / CG;
+  if constexpr (CG <= 2) return cudaSuccess;
+  int n = known->load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(CG);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    known->store(n, std::memory_order_relaxed);
+  }
+  if (n < *count) *count = n;
+  return cudaSuccess;
 }
 
 }  // namespace grp

@@ -96,11 +96,11 @@ __device__ __forceinline__ bool make_lists(const GroupParams& p, const Lists& l)
 // q, 2 P - 1 - q, 2 P + q, .. of P shares.
 struct Pieces {
   Lists l;
-  int tpg, nt, wide, at_group, e, total, share, shares, k, t, slots, splits;   // slots, cut tiles before at_group
+  int tpg, nt, wide, across, at_group, e, total, share, shares, k, t, slots, splits;   // slots, cut tiles before at_group
   int k0, n0, row0, rows, blocks;
   int np, piece, slot, split;   // np > 1: the tile's first slot and its place among cut tiles
-  __device__ __forceinline__ Pieces(const Lists& l_, const GroupParams& p, int width, int share_, int shares_, bool good)
-      : l(l_), tpg(p.kt * p.nt), nt(p.nt), wide(width), at_group(0), e(0), total(good ? l_.start[p.E] * p.kt * p.nt : 0),
+  __device__ __forceinline__ Pieces(const Lists& l_, const GroupParams& p, int width, int columns, int share_, int shares_, bool good)
+      : l(l_), tpg(p.kt * p.nt), nt(p.nt), wide(width), across(columns), at_group(0), e(0), total(good ? l_.start[p.E] * p.kt * p.nt : 0),
         share(share_), shares(shares_), k(0), t(share_), slots(0), splits(0) {}
   __device__ __forceinline__ bool more() {
     if (t >= total) return false;
@@ -119,7 +119,7 @@ struct Pieces {
     // pieces as even as whole blocks allow
     const int b0 = (int)((int64_t)all * piece / np), b1 = (int)((int64_t)all * (piece + 1) / np);
     k0 = tile / nt * wide;
-    n0 = tile % nt * 256;
+    n0 = tile % nt * across;
     row0 = l.first[e] + b0 * 64;
     blocks = b1 - b0;
     rows = min(n - b0 * 64, blocks * 64);
@@ -141,7 +141,8 @@ __device__ __forceinline__ void stage_f32(uint8_t* buf, int lane, const float* a
         make_float4(a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]);
 }
 
-template <int CG>
+// CG CTAs hold a tile, PAIRS tiles side by side (along dy) share what they read of x
+template <int CG, int PAIRS>
 __global__ void __launch_bounds__(kThreads, 1)
 group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ CUtensorMap tmx,
                 const __grid_constant__ CUtensorMap tmg, const __grid_constant__ CUtensorMap tmo) {
@@ -156,11 +157,13 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
   const Lists lists = lists_at(staging + kStaging, p.E);
   auto bar = [&](int i) -> uint32_t { return smem_u32(bars) + 8u * (uint32_t)i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CG == 1 ? 0u : cluster_rank();
+  // this CTA's place in its tile, its tile's among those that share x, and the tile's first CTA
+  const uint32_t in_cluster = CG * PAIRS == 1 ? 0u : cluster_rank(), rank = in_cluster % CG, tile = in_cluster / CG;
+  const uint32_t first_cta = tile * CG;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStagesMax; ++s) {
       mbar_init(bar(B_FULL + s), 1);
-      mbar_init(bar(B_EMPTY + s), 1);
+      mbar_init(bar(B_EMPTY + s), PAIRS);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(B_DFULL + s), 1);
@@ -180,7 +183,7 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
   pdl_wait();
   const bool good = make_lists(p, lists);
   fence_before_sync();
-  if constexpr (CG == 1) __syncthreads();
+  if constexpr (CG * PAIRS == 1) __syncthreads();
   else cluster_sync();
   fence_after_sync();
   const uint32_t tmem = tmem_slot;
@@ -190,7 +193,8 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
   wd.err = p.hdr + WS_ERR;
   wd.err_info = p.hdr + WS_ERR_INFO;
   wd.limit_ns = 2000000000ull;
-  Pieces w(lists, p, 128 * CG, blockIdx.x / CG, gridDim.x / CG, good);
+  Pieces w(lists, p, 128 * CG, 256 * PAIRS, blockIdx.x / (CG * PAIRS), gridDim.x / (CG * PAIRS), good);
+  const uint16_t pair_mask = (uint16_t)(3u << first_cta), all_mask = PAIRS == 1 ? pair_mask : (uint16_t)15u;
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
@@ -199,7 +203,7 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
       uint32_t last[kStagesMax];
       bool ok = true;
       for (; ok && w.more(); w.next()) {
-        const int k0 = w.k0 + (int)rank * 128, n0 = w.n0 + (int)rank * 128;
+        const int k0 = w.k0 + (int)rank * 128, n0 = w.n0 + (int)tile * 256 + (int)rank * 128;
         for (int kb = 0; kb < w.blocks; ++kb) {
           if (used >> stage & 1) ok = mbar_wait(bar(B_EMPTY + stage), phase ^ 1, wd, 71);
           if (!ok) break;
@@ -212,8 +216,13 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
           for (int c = 0; c < BOXES; ++c) {
             const CUtensorMap* map = c < 2 ? &tmx : &tmg;
             const int x = c < 2 ? k0 + c * 64 : n0 + (c - 2) * 64;
-            if (CG == 1 || cut) tma_load_2d(s + c * kBox, map, full, x, row);
-            else pair_load_2d(s + c * kBox, map, in_cta(full, 0), x, row);
+            if (CG == 1 || cut) {
+              tma_load_2d(s + c * kBox, map, full, x, row);
+            } else if (PAIRS == 1 || c >= 2) {
+              pair_load_2d(s + c * kBox, map, in_cta(full, first_cta), x, row);
+            } else if (c == (int)tile) {   // each tile's CTA reads one of x's two boxes for both
+              pair_load_2d_multi(s + c * kBox, map, in_cta(full, first_cta), x, row, (uint16_t)(5u << rank));
+            }
           }
           used |= 1u << stage;
 #pragma unroll
@@ -254,7 +263,7 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
               *reinterpret_cast<uint4*>(s + c * kBox + i * 16) = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
           __syncwarp();
-          if (CG == 2 && rank != 0 && lane == 0) arrive_in_cluster(in_cta(bar(B_CLEAR + stage), 0));
+          if (CG == 2 && rank != 0 && lane == 0) arrive_in_cluster(in_cta(bar(B_CLEAR + stage), first_cta));
           if (CG == 2 && rank == 0) {
             ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(B_CLEAR + stage), cuts >> stage & 1, wd, 77));
             if (!ok) break;
@@ -269,8 +278,8 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma<CG>(tmem + d * 256, da + kk * 2048, db + kk * 2048, IDESC, kb % kRun > 0 || kk > 0 ? 1u : 0u);
-            commit<CG>(bar(B_EMPTY + stage));
-            if (kb % kRun == kRun - 1 || kb == w.blocks - 1) commit<CG>(bar(B_DFULL + d));
+            commit<CG>(bar(B_EMPTY + stage), all_mask);
+            if (kb % kRun == kRun - 1 || kb == w.blocks - 1) commit<CG>(bar(B_DFULL + d), pair_mask);
           }
           __syncwarp();
         }
@@ -316,15 +325,16 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
         __syncwarp();
         if (lane == 0) {
           if constexpr (CG == 1) mbar_arrive(bar(B_DEMPTY + d));
-          else arrive_in_cluster(in_cta(bar(B_DEMPTY + d), 0));
+          else arrive_in_cluster(in_cta(bar(B_DEMPTY + d), first_cta));
         }
       }
       if (!ok) break;
       if (w.np > 1) {
         // this warp's 32 x 128 of a tile's pieces lie side by side, a float4 a lane
         constexpr size_t kPart = 32 * 128;
-        const size_t per = kPart * kEpiWarps * CG;
-        float4* parts = reinterpret_cast<float4*>(p.partial + (size_t)w.slot * per + ((size_t)rank * kEpiWarps + warp) * kPart) + lane;
+        const size_t per = kPart * kEpiWarps * CG * PAIRS;
+        float4* parts = reinterpret_cast<float4*>(p.partial + (size_t)w.slot * per +
+                                                  ((size_t)in_cluster * kEpiWarps + warp) * kPart) + lane;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -333,7 +343,7 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
                 make_float4(acc[c][4 * q], acc[c][4 * q + 1], acc[c][4 * q + 2], acc[c][4 * q + 3]);
         __threadfence();
         __syncwarp();
-        int* counter = p.counters + ((size_t)w.split * CG + rank) * kEpiWarps + warp;
+        int* counter = p.counters + ((size_t)w.split * CG * PAIRS + in_cluster) * kEpiWarps + warp;
         int there = 0;
         if (lane == 0) there = atomicAdd(counter, 1);
         there = __shfl_sync(0xffffffffu, there, 0);
@@ -364,7 +374,7 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
           }
         }
       }
-      const int k0 = w.k0 + (int)rank * 128 + wq * 32;
+      const int k0 = w.k0 + (int)rank * 128 + wq * 32, n0 = w.n0 + (int)tile * 256;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int col = half * 128 + c * 32;
@@ -375,7 +385,7 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (w.n0 + col < p.features && k0 < p.depth) tma_store_3d(&tmo, stg_u32 + at, w.n0 + col, k0, w.e);
+          if (n0 + col < p.features && k0 < p.depth) tma_store_3d(&tmo, stg_u32 + at, n0 + col, k0, w.e);
           bulk_commit();
         }
       }
@@ -384,7 +394,7 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
     __syncwarp();
   }
   fence_before_sync();
-  if constexpr (CG == 1) __syncthreads();
+  if constexpr (CG * PAIRS == 1) __syncthreads();
   else cluster_sync();
   fence_after_sync();
   if (warp == kMmaWarp) free_tmem<CG>(tmem);
@@ -393,21 +403,24 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
 // The shape of a call on a whole GB300 (its SMs set the size of the workspace).
 constexpr int64_t kSms = 152;
 struct DwShape {
-  int cg, kt, nt, kper;
-  int64_t slots;   // of 128 cg x 256 sums
+  int cg, pairs, kt, nt, kper;   // tiles of 128 cg x 256 pairs
+  int64_t slots;                 // of as many sums
 };
 DwShape dw_shape(int64_t rows, int E, int K, int N) {
   DwShape s;
   const int64_t blocks = rows / 64 + (rows < E ? rows : E);   // of all groups, at most
-  s.nt = (N + 255) / 256;
+  const int nt = (N + 255) / 256;
   // pairs where each has six blocks of a tile's rows to do, and K does not leave many of their tiles half empty
   const int halves = (K + 127) / 128, pairs = (halves + 1) / 2;
-  s.cg = blocks * pairs * s.nt >= kSms / 2 * 6 && (halves % 2 == 0 || halves >= 5) ? 2 : 1;
+  s.cg = blocks * pairs * nt >= kSms / 2 * 6 && (halves % 2 == 0 || halves >= 5) ? 2 : 1;
+  // two pairs side by side, which read x once, where that leaves few tiles empty and work for all
+  s.pairs = s.cg == 2 && (nt % 2 == 0 || nt >= 5) && blocks * pairs * ((nt + 1) / 2) >= kSms / 4 * 12 ? 2 : 1;
+  s.nt = (nt + s.pairs - 1) / s.pairs;
   s.kt = (K + 128 * s.cg - 1) / (128 * s.cg);
   // A piece: what a CTA (a pair) has to do on average, and not so little that adding up the pieces (2 to 3 us each, one
   // after the other) takes longer than they do (0.6 us a block): at least 2 sqrt(blocks); of one group, whose pieces are all alike, the
   // length of two rounds at most that ends first, a cut tile's sums counted as 8 blocks (written, read)
-  const int64_t tiles = (int64_t)s.kt * s.nt, shares = kSms / s.cg, all = (rows + 63) / 64, each = (all * tiles + shares - 1) / shares;
+  const int64_t tiles = (int64_t)s.kt * s.nt, shares = kSms / (s.cg * s.pairs), all = (rows + 63) / 64, each = (all * tiles + shares - 1) / shares;
   int64_t least = 8;
   while (least * least < 4 * all) ++least;
   int64_t kper = each < least ? least : each;
@@ -427,7 +440,7 @@ DwShape dw_shape(int64_t rows, int E, int K, int N) {
   return s;
 }
 
-template <int CG>
+template <int CG, int PAIRS>
 cudaError_t launch_t(GroupParams p, const void* x, int64_t x_stride, const void* dy, int64_t dy_stride, int sms,
                      cudaStream_t st) {
   const int K = p.depth, N = p.features;
@@ -444,12 +457,15 @@ cudaError_t launch_t(GroupParams p, const void* x, int64_t x_stride, const void*
   p.stages = (int)((kMaxSmemPerCta - 512 - fixed) / stage);   // (512: barriers and the scan's sums)
   if (p.stages > kStagesMax) p.stages = kStagesMax;
   const size_t smem = fixed + p.stages * stage;
-  auto kern = group_dw_kernel<CG>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  auto kern = group_dw_kernel<CG, PAIRS>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
+  static std::atomic<int> known;
+  int shares = 0;
+  if ((e = clusters_at_once<CG * PAIRS>(kern, kThreads, smem, sms, &known, &shares)) != cudaSuccess) return e;
   const int64_t most = (int64_t)p.kt * p.nt * (p.E + p.rows / 64 / p.kper + 1);
-  const unsigned grid = (unsigned)(most < sms / CG ? most : sms / CG) * CG;
-  return launch_cluster<CG>(kern, grid, kThreads, smem, st, p, mx, mg, mo);
+  const unsigned grid = (unsigned)(most < shares ? most : shares) * CG * PAIRS;
+  return launch_cluster<CG * PAIRS>(kern, grid, kThreads, smem, st, p, mx, mg, mo);
 }
 
 }  // namespace
@@ -457,11 +473,11 @@ cudaError_t launch_t(GroupParams p, const void* x, int64_t x_stride, const void*
 // counters of cut tiles (each has two slots or more), then the slots
 size_t group_dw_counters(int64_t rows, int E, int K, int N) {
   const DwShape s = dw_shape(rows, E, K, N);
-  return ((size_t)s.slots / 2 * s.cg * kEpiWarps * sizeof(int) + kWsAlign - 1) / kWsAlign * kWsAlign;
+  return ((size_t)s.slots / 2 * s.cg * s.pairs * kEpiWarps * sizeof(int) + kWsAlign - 1) / kWsAlign * kWsAlign;
 }
 size_t group_dw_bytes(int64_t rows, int E, int K, int N) {
   const DwShape s = dw_shape(rows, E, K, N);
-  return group_dw_counters(rows, E, K, N) + (size_t)s.slots * 128 * s.cg * 256 * sizeof(float);
+  return group_dw_counters(rows, E, K, N) + (size_t)s.slots * 128 * s.cg * 256 * s.pairs * sizeof(float);
 }
 
 cudaError_t launch_group_dw(const GroupParams& q, void* room, const void* x, int64_t x_stride, const void* dy,
@@ -472,7 +488,8 @@ cudaError_t launch_group_dw(const GroupParams& q, void* room, const void* x, int
   p.kt = s.kt; p.nt = s.nt; p.kper = s.kper;
   p.counters = static_cast<int*>(room);
   p.partial = reinterpret_cast<float*>(static_cast<char*>(room) + group_dw_counters(q.rows, q.E, K, N));
-  return s.cg == 2 ? launch_t<2>(p, x, x_stride, dy, dy_stride, sms, st) : launch_t<1>(p, x, x_stride, dy, dy_stride, sms, st);
+  if (s.pairs == 2) return launch_t<2, 2>(p, x, x_stride, dy, dy_stride, sms, st);
+  return s.cg == 2 ? launch_t<2, 1>(p, x, x_stride, dy, dy_stride, sms, st) : launch_t<1, 1>(p, x, x_stride, dy, dy_stride, sms, st);
 }
 
 }  // namespace hstu

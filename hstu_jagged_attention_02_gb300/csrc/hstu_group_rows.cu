@@ -261,8 +261,8 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma<CG>(tmem + d * 256, da + (KMAJOR ? kk * 32 : kk * 2048), db + kk * 32, idesc, kb > 0 || kk > 0 ? 1u : 0u);
-          commit<CG>(bar(B_AEMPTY + stage));
-          if (release) commit<CG>(bar(B_BEMPTY + slot));
+          commit<CG>(bar(B_AEMPTY + stage), 3);
+          if (release) commit<CG>(bar(B_BEMPTY + slot), 3);
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1;
@@ -272,7 +272,7 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
             if (release) slot_phase ^= 1;
           }
         }
-        if (ok) commit<CG>(bar(B_DFULL + d));
+        if (ok) commit<CG>(bar(B_DFULL + d), 3);
       }
       commit_here<CG>(bar(B_DRAIN));
       drain(bar(B_DRAIN), 0);
