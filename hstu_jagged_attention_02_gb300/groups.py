@@ -56,7 +56,8 @@ class GroupProblem:
 
     x and dy are used in place where their features are contiguous and rows a
     multiple of 16 bytes apart, else copied once, here.  The outputs are
-    allocated unless given.  Rows behind the last group are left as they are."""
+    allocated unless given and lie apart from the inputs.  Rows behind the last
+    group are left as they are."""
 
     def __init__(self, x, w, group_offsets, *, out_dtype: Optional[torch.dtype] = None, dy=None, y=None, dx=None, dw=None,
                  dx_dtype: Optional[torch.dtype] = None, want_dx: bool = True, want_dw: bool = True, workspace=None,
@@ -78,6 +79,9 @@ class GroupProblem:
                                    ("dx", dx, (rows, K), dx_dtype), ("dw", dw, (E, K, N), torch.float32)):
             _need(t is None or (t.shape == shape and t.dtype == dt), f"{name} must be {dt} {shape}")
         _need(dw is None or dw.is_contiguous(), "dw must be contiguous")
+        read = {t.data_ptr() for t in (x, w, dy) if t is not None and t.numel()}
+        for name, t in (("y", y), ("dx", dx), ("dw", dw)):
+            _need(t is None or t.numel() == 0 or t.data_ptr() not in read, f"{name} must lie apart from what is read")
         self.x, self.w, self.offsets = _rows16(x, "x"), w, group_offsets
         self.y = y if y is not None else torch.empty(rows, N, device=dev, dtype=out_dtype)
         _check_out(self.y, "y")

@@ -41,8 +41,9 @@ class LNProblem:
     from dy (and adds dres, the gradient that reached x past the norm).
 
     x, dy, dres are used in place where their features are contiguous, else
-    copied once, here.  The outputs are allocated unless given.  mean and rstd
-    may be those of an earlier forward."""
+    copied once, here.  The outputs are allocated unless given; y may be x
+    (without a backward), dx may be dy or dres, of the same type and strides.
+    mean and rstd may be those of an earlier forward."""
 
     def __init__(self, x, weight=None, bias=None, *, eps: float = 1e-5, out_dtype: Optional[torch.dtype] = None,
                  dy=None, dres=None, y=None, dx=None, mean=None, rstd=None, num_rows=None, want_weight_grad=None,
@@ -73,6 +74,8 @@ class LNProblem:
         f32 = dict(device=dev, dtype=torch.float32)
         self.y = y if y is not None else torch.empty(rows, D, device=dev, dtype=out_dtype)
         _own_rows(self.y, "y")
+        _need(dy is None or y is None or y.numel() == 0 or y.data_ptr() != self.x.data_ptr(),
+              "the backward needs x, which a forward in place overwrites")
         self.mean = mean if mean is not None else torch.empty(rows, **f32)
         self.rstd = rstd if rstd is not None else torch.empty(rows, **f32)
         backward = dy is not None

@@ -2,6 +2,7 @@
 hstu_adamw_* of libhstu_attn.so.  Marshalling and checks of arguments only."""
 from __future__ import annotations
 
+import bisect
 from typing import NamedTuple, Optional
 
 import torch
@@ -35,6 +36,13 @@ def zero_moments(param, bits: int = 32):
                     *(torch.full(((n + BLOCK - 1) // BLOCK,), 16, **byte) for _ in range(2)))
 
 
+def _apart(spans, t):
+    """Whether t shares no byte with spans (sorted, apart from each other)."""
+    lo, hi = t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+    i = bisect.bisect_right(spans, (lo, hi))
+    return lo == hi or ((i == 0 or spans[i - 1][1] <= lo) and (i == len(spans) or spans[i][0] >= hi))
+
+
 class AdamW:
     """AdamW for a list of FP32 tensors: step() updates the parameters, their
     moments and their BF16 copies in place, in one launch.
@@ -52,7 +60,7 @@ class AdamW:
     step changes and counts nothing.  seed: of the 8-bit moments' rounding.
 
     All tensors are contiguous and 16-byte aligned (copies to 8 bytes, exponent
-    bytes to any) and must not overlap."""
+    bytes to any), must not overlap and stay where they are."""
 
     def __init__(self, params, grads=None, *, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.0, lr_scale=1.0,
                  copies=None, moments=None, state_bits: int = 32, grad_scale=None, skip=None, steps: int = 0, seed: int = 0,
@@ -101,8 +109,11 @@ class AdamW:
             rows.append((at, c_at, m_at, n_i))
         spans = sorted(x for x in spans if x[1] > x[0])
         _need(all(a[1] <= b[0] for a, b in zip(spans, spans[1:])), "parameters, copies and moments must not overlap")
+        self._written = spans
         for i, g in enumerate(self.grads):
             self._check_grad(i, g)
+        # what the device writes stays where it is while this object lives, even if a parameter's data moves
+        self._held = [t.detach() for t in self.params]
         self.lr_at = lr if isinstance(lr, torch.Tensor) else None
         for name, t, dt in (("lr", self.lr_at, torch.float32), ("grad_scale", grad_scale, torch.float32), ("skip", skip, torch.int32)):
             _need(t is None or (t.dtype == dt and t.numel() == 1 and t.device == dev), f"{name} must be one {dt} on {dev}")
@@ -125,6 +136,7 @@ class AdamW:
         self._step = Launch(dev, C.load().hstu_adamw_step, "hstu_adamw_step", d, self.args, self.ws.data_ptr(), need)
         with torch.cuda.device(dev):
             C.hstu_adamw_init(d, self._table, self.ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+        self._sent = True
 
     def _check_grad(self, i, g):
         if g is None:
@@ -133,6 +145,8 @@ class AdamW:
         if (g.device != p.device or g.numel() != p.numel() or g.dtype != self.grad_dtype or not g.is_contiguous() or
                 g.data_ptr() % 16):
             raise ValueError(f"gradient {i} must be contiguous {self.grad_dtype} of its parameter's size, 16-byte aligned")
+        if not _apart(self._written, g):
+            raise ValueError(f"gradient {i} overlaps what a step writes")
 
     @property
     def lr(self):
@@ -145,20 +159,22 @@ class AdamW:
         self.desc.lr = float(value)
 
     def _follow_grads(self, stream):
-        """The parameters' present .grad; a list that changed is sent anew."""
-        changed = False
+        """The parameters' present .grad; a list that changed is sent anew.  A
+        step that raises leaves the device's list to be sent by the next one."""
         for i, p in enumerate(self.params):
             g = p.grad
-            at = _ptr(g)
-            if at != self._table[i].grad or g is not self.grads[i]:
+            if g is not self.grads[i] or _ptr(g) != self._table[i].grad:
                 self._check_grad(i, g)
-                changed = changed or at != self._table[i].grad
-                self._table[i].grad, self.grads[i] = at, g
-        if changed:
+                self._sent = self._sent and _ptr(g) == self._table[i].grad
+                self._table[i].grad, self.grads[i] = _ptr(g), g
+            if p.data_ptr() != (self._table[i].param or 0):
+                raise ValueError(f"parameter {i} is not where it was")
+        if not self._sent:
             self.desc.steps_done = -1   # what the device has counted stays
             with torch.cuda.device(self.device):
                 s = stream if stream is not None else torch.cuda.current_stream()
                 C.hstu_adamw_init(self.desc, self._table, self.ws.data_ptr(), self.ws_bytes, s.cuda_stream)
+            self._sent = True
 
     def step(self, stream=None):
         if self.dynamic:
@@ -202,6 +218,8 @@ class MomentsReader:
                 if t is not None and (t.device != dev or t.dtype != dtype or t.numel() != p.numel() or not t.is_contiguous() or
                                       t.data_ptr() % 16):
                     raise ValueError("a moment's values must be contiguous, 16-byte aligned, of one type")
+                if t is not None and not _apart(optimizer._written, t):
+                    raise ValueError("a moment's values overlap what a step writes")
         d = C.hstu_adamw_desc.from_buffer_copy(optimizer.desc)
         self.desc = d
         table = (C.hstu_adamw_moments * len(self.outs))(*(C.hstu_adamw_moments(_ptr(a), _ptr(b)) for a, b in self.outs))

@@ -708,8 +708,8 @@ hstu_status_t hstu_ln_bwd(const hstu_ln_desc* desc, const hstu_ln_bwd_args* args
  * are left as they are and not read into any result.  x, W, dy are BF16, sums FP32 on the tensor cores; y and dx
  * are rounded once to their type, dW is FP32.  K and N are multiples of 8, rows
  * a multiple of 16 bytes apart (any row stride that is a multiple of 8
- * elements); W and dW are dense [groups][K][N].  Up to 4096 groups.  Equal
- * inputs give equal bits.
+ * elements); W and dW are dense [groups][K][N].  Up to 4096 groups.  Outputs
+ * must not overlap inputs.  Equal inputs give equal bits.
  *
  * The workspace is 256-byte aligned; its first zero_bytes (the backward's; 256 for
  * the forward: the header) must be zero before its first use.  Offsets that break the

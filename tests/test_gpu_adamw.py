@@ -267,3 +267,30 @@ def test_another_list_is_found():
                                             s.cuda_stream) == C.HSTU_ERR_INVALID_ARG
     graph.replay()
     torch.cuda.synchronize()
+
+
+def test_a_step_that_raised_sends_the_list_with_the_next():
+    from hstu_jagged_attention_02_gb300.optim import AdamW
+    params, grads = _tensors([300, 2048], 11)
+    other, _ = _tensors([300, 2048], 11)
+    leaves = [p.requires_grad_() for p in params]
+    opt, ref = AdamW(leaves, None, grad_dtype=torch.float32, **HYPER), AdamW(other, grads, **HYPER)
+    for p, g in zip(leaves, grads):
+        p.grad = g.clone()
+    opt.step()
+    ref.step()
+    kept = leaves[1].grad
+    leaves[0].grad = 2 * grads[0]
+    leaves[1].grad = torch.zeros(2049, device="cuda")[1:]   # not 16-byte aligned
+    with pytest.raises(ValueError):
+        opt.step()
+    assert opt.steps() == 1
+    leaves[1].grad = kept
+    opt.step()
+    grads[0].mul_(2)
+    ref.step()
+    assert all(torch.equal(a.detach(), b) for a, b in zip(leaves, other)) and opt.steps() == 2
+    leaves[0].data = leaves[0].data.clone()
+    with pytest.raises(ValueError, match="is not where it was"):
+        opt.step()
+    assert opt.steps() == 2

@@ -215,3 +215,28 @@ def test_autograd_and_broadcast_gradients():
         assert torch.equal(leaf.grad, g)
     y = hstu_ln(leaves[0].detach()[:0], w, b)
     assert y.shape == (0, 128)
+
+
+@pytest.mark.parametrize("D", [256, 376, 384, 392, 512])
+def test_sums_of_a_cta_fill_its_shared_memory(D):
+    """The backward's sums of 16 rows at a time are 48 KB at 384 features: what a launch gets unasked, and no more."""
+    from hstu_jagged_attention_02_gb300.norm import LNProblem
+    x, w, b, dy, dres = _inputs(77, D, "bf16", "bf16", 77 + D)
+    pr = LNProblem(x, w, b, eps=EPS, dy=dy, dres=dres)
+    pr.forward()
+    pr.backward()
+    _check_all(pr, x, w, b, dy, dres, "bf16", "bf16")
+
+
+def test_gradients_in_place():
+    from hstu_jagged_attention_02_gb300.norm import LNProblem
+    for D in (72, 301, 1500):
+        x, w, b, dy, dres = _inputs(50, D, "fp32", "fp32", D)
+        ref = LNProblem(x, w, b, eps=EPS, dy=dy, dres=dres)
+        ref.forward()
+        ref.backward()
+        for name in ("dy", "dres"):
+            t = dict(dy=dy.clone(), dres=dres.clone())
+            pr = LNProblem(x, w, b, eps=EPS, dx=t[name], mean=ref.mean, rstd=ref.rstd, **t)
+            pr.backward()
+            assert torch.equal(t[name], ref.dx) and torch.equal(pr.d_weight, ref.d_weight) and torch.equal(pr.d_bias, ref.d_bias)
