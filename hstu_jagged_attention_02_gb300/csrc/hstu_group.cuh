@@ -7,8 +7,6 @@
 // row blocks (or of pieces of work) into shared memory, of which each role
 // walks its share with a cursor.
 #pragma once
-#include <atomic>
-
 #include "hstu_internal.h"
 #include "tc_ptx.cuh"
 
@@ -31,6 +29,7 @@ struct GroupParams {
   int row_block;     // rows of a tile, 32, 64, 128 or 256
   int pair;          // CTAs work in pairs
   int box_rows;      // rows of a load box
+  int one_w;         // a stage's part of W comes in one copy
   int stages;        // of the ring of loads (of A, where B has slots of its own)
   int slots;         // of B
   void* out;
@@ -38,6 +37,7 @@ struct GroupParams {
   int test_timeout;
   // weight gradients: tiles of 128 x 256 of [K, N], pieces of at most kper 64-row blocks
   int kt, nt, kper;
+  int one_x, one_dy; // a stage's part of x (dy) comes in one copy
   float* dw;
   int* counters;     // of cut tiles, a storing warp each
   float* partial;    // [slots][CTAs of a tile][warps][32 x 128]
@@ -49,6 +49,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
           dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// 4-D tile load
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int u) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u)
       : "memory");
 }
 
@@ -106,20 +115,11 @@ __device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* ma
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// the same into all CTAs of the mask, at the same places; counts on the barrier of each one's pair
-__device__ __forceinline__ void pair_load_2d_multi(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, uint16_t mask) {
+__device__ __forceinline__ void pair_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int u) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 [%0], [%1, "
-      "{%3, %4}], [%2], %5;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "h"(mask)
-      : "memory");
-}
-__device__ __forceinline__ void pair_load_3d_multi(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
-                                                   uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 [%0], [%1, "
-      "{%3, %4, %5}], [%2], %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "h"(mask)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u)
       : "memory");
 }
 template <int CG> __device__ __forceinline__ void alloc_tmem(uint32_t dst) {
@@ -162,24 +162,27 @@ template <int CG> __device__ __forceinline__ void commit_here(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// A loading thread's end.  Every stage is waited for once more by both CTAs of a pair: the products' arrivals come from the
+// A loading thread's end; (stage, phase) is the next to be loaded, `loads` the loads so far.  Every stage is waited for once
+// more by both CTAs of a pair: the products' arrivals come from the
 // pair's first CTA on their own time, and one that came after this CTA's end would count on a barrier of its successor.
 // After a wait that ran out: until the copies under way are there.
-template <int CG, int N, typename Bar>
-__device__ __forceinline__ void tail(Bar bar, int empty, int full, int ring, int stage, uint32_t phase, uint32_t used,
-                                     const uint32_t (&last)[N], uint32_t rank, bool ok, const Watchdog& wd, int site) {
+template <int CG, typename Bar>
+__device__ __forceinline__ void tail(Bar bar, int empty, int full, int ring, int stage, uint32_t phase, uint32_t loads,
+                                     uint32_t rank, bool ok, const Watchdog& wd, int site) {
+  int s = stage;
+  uint32_t ph = phase;
   for (int i = 0; CG == 2 && ok && i < ring; ++i) {
-    if (used >> stage & 1) ok = mbar_wait(bar(empty + stage), phase ^ 1, wd, site);
-    if (++stage == ring) {
-      stage = 0;
-      phase ^= 1;
+    if (loads >= (uint32_t)ring || s < stage) ok = mbar_wait(bar(empty + s), ph ^ 1, wd, site);
+    if (++s == ring) {
+      s = 0;
+      ph ^= 1;
     }
   }
   if (ok) return;
   if (rank == 0) {   // the barriers count both CTAs' copies
-#pragma unroll
-    for (int s = 0; s < N; ++s)
-      if (used >> s & 1) drain(bar(full + s), last[s]);
+    for (s = 0; s < ring; ++s)
+      if (s < stage) drain(bar(full + s), phase);
+      else if (loads >= (uint32_t)ring) drain(bar(full + s), phase ^ 1);
   } else {   // the other CTA's copies are not counted here
     const uint64_t t0 = globaltimer();
     while (globaltimer() - t0 < 1000000ull) {}
@@ -250,32 +253,6 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, int threads,
   cfg.attrs = attr;
   cfg.numAttrs = CG == 1 ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
-// Clusters of CG such CTAs that run at once on the current device (a GPC whose SMs are no multiple of CG leaves
-// some idle), looked up once a kernel: *known starts as 0.
-template <int CG, typename... KArgs>
-cudaError_t clusters_at_once(void (*kernel)(KArgs...), int threads, size_t smem, int sms, std::atomic<int>* known, int* count) {
-  *count = sms / CG;
-  if constexpr (CG <= 2) return cudaSuccess;
-  int n = known->load(std::memory_order_relaxed);
-  if (n == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(CG);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-    if (e != cudaSuccess) return e;
-    known->store(n, std::memory_order_relaxed);
-  }
-  if (n < *count) *count = n;
-  return cudaSuccess;
 }
 
 }  // namespace grp

@@ -32,7 +32,7 @@ using namespace grp;
 
 constexpr int kStagesMax = 8;
 constexpr int kBox = 64 * 64 * 2;                 // 64 rows x 64 features
-constexpr int kStaging = kEpiWarps * 2 * 4096;    // two 32 x 32 FP32 buffers of each storing warp
+constexpr int kStaging = kEpiWarps * 4096;        // a 32 x 32 FP32 buffer of each storing warp
 constexpr int kRun = 16;                          // 64-row blocks summed in one accumulator
 constexpr int kRanked = kThreads;                 // groups up to which they are sorted by the length of their pieces
 enum : int { B_FULL = 0, B_EMPTY = B_FULL + kStagesMax, B_DFULL = B_EMPTY + kStagesMax, B_DEMPTY = B_DFULL + 2,
@@ -96,11 +96,11 @@ __device__ __forceinline__ bool make_lists(const GroupParams& p, const Lists& l)
 // q, 2 P - 1 - q, 2 P + q, .. of P shares.
 struct Pieces {
   Lists l;
-  int tpg, nt, wide, across, at_group, e, total, share, shares, k, t, slots, splits;   // slots, cut tiles before at_group
+  int tpg, nt, wide, at_group, e, total, share, shares, k, t, slots, splits;   // slots, cut tiles before at_group
   int k0, n0, row0, rows, blocks;
   int np, piece, slot, split;   // np > 1: the tile's first slot and its place among cut tiles
-  __device__ __forceinline__ Pieces(const Lists& l_, const GroupParams& p, int width, int columns, int share_, int shares_, bool good)
-      : l(l_), tpg(p.kt * p.nt), nt(p.nt), wide(width), across(columns), at_group(0), e(0), total(good ? l_.start[p.E] * p.kt * p.nt : 0),
+  __device__ __forceinline__ Pieces(const Lists& l_, const GroupParams& p, int width, int share_, int shares_, bool good)
+      : l(l_), tpg(p.kt * p.nt), nt(p.nt), wide(width), at_group(0), e(0), total(good ? l_.start[p.E] * p.kt * p.nt : 0),
         share(share_), shares(shares_), k(0), t(share_), slots(0), splits(0) {}
   __device__ __forceinline__ bool more() {
     if (t >= total) return false;
@@ -119,7 +119,7 @@ struct Pieces {
     // pieces as even as whole blocks allow
     const int b0 = (int)((int64_t)all * piece / np), b1 = (int)((int64_t)all * (piece + 1) / np);
     k0 = tile / nt * wide;
-    n0 = tile % nt * across;
+    n0 = tile % nt * 256;
     row0 = l.first[e] + b0 * 64;
     blocks = b1 - b0;
     rows = min(n - b0 * 64, blocks * 64);
@@ -141,8 +141,8 @@ __device__ __forceinline__ void stage_f32(uint8_t* buf, int lane, const float* a
         make_float4(a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]);
 }
 
-// CG CTAs hold a tile, PAIRS tiles side by side (along dy) share what they read of x
-template <int CG, int PAIRS>
+// CG: CTAs that work together
+template <int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ CUtensorMap tmx,
                 const __grid_constant__ CUtensorMap tmg, const __grid_constant__ CUtensorMap tmo) {
@@ -157,13 +157,11 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
   const Lists lists = lists_at(staging + kStaging, p.E);
   auto bar = [&](int i) -> uint32_t { return smem_u32(bars) + 8u * (uint32_t)i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // this CTA's place in its tile, its tile's among those that share x, and the tile's first CTA
-  const uint32_t in_cluster = CG * PAIRS == 1 ? 0u : cluster_rank(), rank = in_cluster % CG, tile = in_cluster / CG;
-  const uint32_t first_cta = tile * CG;
+  const uint32_t rank = CG == 1 ? 0u : cluster_rank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStagesMax; ++s) {
       mbar_init(bar(B_FULL + s), 1);
-      mbar_init(bar(B_EMPTY + s), PAIRS);
+      mbar_init(bar(B_EMPTY + s), 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(B_DFULL + s), 1);
@@ -183,7 +181,7 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
   pdl_wait();
   const bool good = make_lists(p, lists);
   fence_before_sync();
-  if constexpr (CG * PAIRS == 1) __syncthreads();
+  if constexpr (CG == 1) __syncthreads();
   else cluster_sync();
   fence_after_sync();
   const uint32_t tmem = tmem_slot;
@@ -193,101 +191,111 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
   wd.err = p.hdr + WS_ERR;
   wd.err_info = p.hdr + WS_ERR_INFO;
   wd.limit_ns = 2000000000ull;
-  Pieces w(lists, p, 128 * CG, 256 * PAIRS, blockIdx.x / (CG * PAIRS), gridDim.x / (CG * PAIRS), good);
-  const uint16_t pair_mask = (uint16_t)(3u << first_cta), all_mask = PAIRS == 1 ? pair_mask : (uint16_t)15u;
+  Pieces w(lists, p, 128 * CG, blockIdx.x / CG, gridDim.x / CG, good);
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
       int stage = 0;
-      uint32_t phase = 0, used = 0;
-      uint32_t last[kStagesMax];
+      uint32_t phase = 0, loads = 0;
       bool ok = true;
-      for (; ok && w.more(); w.next()) {
-        const int k0 = w.k0 + (int)rank * 128, n0 = w.n0 + (int)tile * 256 + (int)rank * 128;
-        for (int kb = 0; kb < w.blocks; ++kb) {
-          if (used >> stage & 1) ok = mbar_wait(bar(B_EMPTY + stage), phase ^ 1, wd, 71);
-          if (!ok) break;
-          const uint32_t s = base + stage * kStage;
-          const int row = w.row0 + kb * 64;
-          const bool cut = w.rows - kb * 64 < 64;   // the group ends inside: each CTA's copies count on its own barrier
-          const uint32_t full = bar(B_FULL + stage);
-          if (cut || rank == 0) mbar_arrive_expect_tx(full, cut || CG == 1 ? kStage : 2 * kStage);
+      const uint32_t there = CG == 1 ? bar(B_FULL) : in_cta(bar(B_FULL), 0);   // the pair's barriers
+      auto copies = [&](uint32_t dst, const CUtensorMap* map, int boxes, bool one, uint32_t full, bool here, int x, int row) {
+        if (one) {
+          if (CG == 1 || here) tma_load_3d(dst, map, full, 0, row, x >> 6);
+          else pair_load_3d(dst, map, full, 0, row, x >> 6);
+        } else {
 #pragma unroll
-          for (int c = 0; c < BOXES; ++c) {
-            const CUtensorMap* map = c < 2 ? &tmx : &tmg;
-            const int x = c < 2 ? k0 + c * 64 : n0 + (c - 2) * 64;
-            if (CG == 1 || cut) {
-              tma_load_2d(s + c * kBox, map, full, x, row);
-            } else if (PAIRS == 1 || c >= 2) {
-              pair_load_2d(s + c * kBox, map, in_cta(full, first_cta), x, row);
-            } else if (c == (int)tile) {   // each tile's CTA reads one of x's two boxes for both
-              pair_load_2d_multi(s + c * kBox, map, in_cta(full, first_cta), x, row, (uint16_t)(5u << rank));
-            }
+          for (int c = 0; c < boxes; ++c) {
+            if (CG == 1 || here) tma_load_2d(dst + c * kBox, map, full, x + c * 64, row);
+            else pair_load_2d(dst + c * kBox, map, full, x + c * 64, row);
           }
-          used |= 1u << stage;
-#pragma unroll
-          for (int q = 0; q < kStagesMax; ++q)
-            if (q == stage) last[q] = phase;
+        }
+      };
+      for (; ok && w.more(); w.next()) {
+        const int k0 = w.k0 + (int)rank * 128, n0 = w.n0 + (int)rank * 128;
+        int row = w.row0;
+        for (int left = w.rows; left > 0; left -= 64, row += 64) {
+          if (loads >= (uint32_t)p.stages) ok = mbar_wait(bar(B_EMPTY + stage), phase ^ 1, wd, 71);
+          if (!ok) break;
+          ++loads;
+          const uint32_t s = base + stage * kStage, mine = bar(B_FULL + stage);
+          const bool cut = CG == 2 && left < 64;   // the group ends inside: each CTA's copies count on its own barrier
+          const uint32_t full = cut ? mine : there + 8u * (uint32_t)stage;
+          if (cut || rank == 0) mbar_arrive_expect_tx(mine, cut || CG == 1 ? kStage : 2 * kStage);
+          copies(s, &tmx, 2, p.one_x, full, cut, k0, row);
+          copies(s + 2 * kBox, &tmg, BOXES - 2, p.one_dy, full, cut, n0, row);
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1;
           }
         }
       }
-      tail<CG>(bar, B_EMPTY, B_FULL, p.stages, stage, phase, used, last, rank, ok, wd, 75);
+      tail<CG>(bar, B_EMPTY, B_FULL, p.stages, stage, phase, loads, rank, ok, wd, 75);
     }
   } else if (warp == kMmaWarp) {
     const uint32_t IDESC = idesc_bf16(128 * CG, 256, true, true);
     int stage = 0;
     uint32_t phase = 0, n = 0, cuts = 0;
     bool ok = true;
-    for (; ok && w.more(); w.next()) {
-      for (int kb = 0; ok && kb < w.blocks; ++kb) {
-        const int live = w.rows - kb * 64;
-        const uint32_t d = n & 1;
-        if (rank == 0 && kb % kRun == 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(B_DEMPTY + d), ((n >> 1) & 1) ^ 1, wd, 72));
-          if (!ok) break;
-        }
-        const bool cut = live < 64;
-        if (rank == 0 || cut) {
-          // (the second CTA's barriers have no other phases than those of such blocks)
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(B_FULL + stage), rank == 0 ? phase : cuts >> stage & 1, wd, 73));
-          if (!ok) break;
-        }
-        if (cut) {
-          // rows of the next group: cleared (a row is 128 bytes of each box, whatever the swizzle)
-          uint8_t* s = smem + stage * kStage;
-          for (int c = 0; c < BOXES; ++c)
-            for (int i = live * 8 + lane; i < 64 * 8; i += 32)
-              *reinterpret_cast<uint4*>(s + c * kBox + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (CG == 2 && rank != 0 && lane == 0) arrive_in_cluster(in_cta(bar(B_CLEAR + stage), first_cta));
-          if (CG == 2 && rank == 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(B_CLEAR + stage), cuts >> stage & 1, wd, 77));
-            if (!ok) break;
-          }
-          cuts ^= 1u << stage;
-        }
-        if (rank == 0) {
-          fence_after_sync();
-          if (lane == 0) {
-            const uint32_t sA = base + stage * kStage, sB = sA + 2 * kBox;
-            const SDesc da = sdesc_w(sA, kBox, 1024), db = sdesc_w(sB, kBox, 1024);
+    // a block's products and their arrivals
+    auto products = [&](int at, uint32_t d, bool first, bool last) {
+      fence_after_sync();
+      const uint32_t sA = base + at * kStage, sB = sA + 2 * kBox;
+      const SDesc da = sdesc_w(sA, kBox, 1024), db = sdesc_w(sB, kBox, 1024);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma<CG>(tmem + d * 256, da + kk * 2048, db + kk * 2048, IDESC, kb % kRun > 0 || kk > 0 ? 1u : 0u);
-            commit<CG>(bar(B_EMPTY + stage), all_mask);
-            if (kb % kRun == kRun - 1 || kb == w.blocks - 1) commit<CG>(bar(B_DFULL + d), pair_mask);
+      for (int kk = 0; kk < 4; ++kk) mma<CG>(tmem + d * 256, da + kk * 2048, db + kk * 2048, IDESC, first && kk == 0 ? 0u : 1u);
+      commit<CG>(bar(B_EMPTY + at), 3);
+      if (last) commit<CG>(bar(B_DFULL + d), 3);
+    };
+    for (; ok && w.more(); w.next()) {
+      // whole blocks, one thread's work
+      const int whole = w.rows >> 6;
+      if (rank == 0 && lane == 0) {
+        int at = stage;
+        uint32_t ph = phase, acc = n;
+        for (int kb = 0; kb < whole; ++kb) {
+          const bool first = kb % kRun == 0, last = kb % kRun == kRun - 1 || kb == w.blocks - 1;
+          if (first) ok = mbar_wait(bar(B_DEMPTY + (acc & 1)), ((acc >> 1) & 1) ^ 1, wd, 72);
+          if (ok) ok = mbar_wait(bar(B_FULL + at), ph, wd, 73);
+          if (!ok) break;
+          products(at, acc & 1, first, last);
+          acc += last ? 1u : 0u;
+          if (++at == p.stages) {
+            at = 0;
+            ph ^= 1;
           }
-          __syncwarp();
         }
-        if (kb % kRun == kRun - 1 || kb == w.blocks - 1) ++n;
-        if (++stage == p.stages) {
-          stage = 0;
-          phase ^= 1;
-        }
+      }
+      __syncwarp();
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      n += whole / kRun + (whole == w.blocks && whole % kRun != 0 ? 1 : 0);
+      phase ^= (uint32_t)((stage + whole) / p.stages) & 1u;
+      stage = (stage + whole) % p.stages;
+      if (whole == w.blocks) continue;
+      // a block in which the group ends
+      const bool first = whole % kRun == 0;
+      if (rank == 0 && first) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_DEMPTY + (n & 1)), ((n >> 1) & 1) ^ 1, wd, 72));
+      // (the second CTA's barriers have no other phases than those of such blocks)
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_FULL + stage), rank == 0 ? phase : cuts >> stage & 1, wd, 73));
+      if (!ok) break;
+      // rows of the next group: cleared (a row is 128 bytes of each box, whatever the swizzle)
+      uint8_t* s = smem + stage * kStage;
+      for (int c = 0; c < BOXES; ++c)
+        for (int i = (w.rows & 63) * 8 + lane; i < 64 * 8; i += 32)
+          *reinterpret_cast<uint4*>(s + c * kBox + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (CG == 2 && rank != 0 && lane == 0) arrive_in_cluster(in_cta(bar(B_CLEAR + stage), 0));
+      if (CG == 2 && rank == 0) ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(B_CLEAR + stage), cuts >> stage & 1, wd, 77));
+      if (!ok) break;
+      cuts ^= 1u << stage;
+      if (rank == 0 && lane == 0) products(stage, n & 1, first, true);
+      __syncwarp();
+      ++n;
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
       }
     }
     if (rank == 0 && lane == 0) {
@@ -298,7 +306,7 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
   } else {
     const int wq = warp & 3, half = warp >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16) + half * 128;
-    uint8_t* stg = staging + warp * 8192;
+    uint8_t* stg = staging + warp * 4096;
     const uint32_t stg_u32 = smem_u32(stg);
     uint32_t n = 0;
     bool ok = true;
@@ -325,16 +333,16 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
         __syncwarp();
         if (lane == 0) {
           if constexpr (CG == 1) mbar_arrive(bar(B_DEMPTY + d));
-          else arrive_in_cluster(in_cta(bar(B_DEMPTY + d), first_cta));
+          else arrive_in_cluster(in_cta(bar(B_DEMPTY + d), 0));
         }
       }
       if (!ok) break;
       if (w.np > 1) {
         // this warp's 32 x 128 of a tile's pieces lie side by side, a float4 a lane
         constexpr size_t kPart = 32 * 128;
-        const size_t per = kPart * kEpiWarps * CG * PAIRS;
+        const size_t per = kPart * kEpiWarps * CG;
         float4* parts = reinterpret_cast<float4*>(p.partial + (size_t)w.slot * per +
-                                                  ((size_t)in_cluster * kEpiWarps + warp) * kPart) + lane;
+                                                  ((size_t)rank * kEpiWarps + warp) * kPart) + lane;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -343,29 +351,33 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
                 make_float4(acc[c][4 * q], acc[c][4 * q + 1], acc[c][4 * q + 2], acc[c][4 * q + 3]);
         __threadfence();
         __syncwarp();
-        int* counter = p.counters + ((size_t)w.split * CG * PAIRS + in_cluster) * kEpiWarps + warp;
+        int* counter = p.counters + ((size_t)w.split * CG + rank) * kEpiWarps + warp;
         int there = 0;
         if (lane == 0) there = atomicAdd(counter, 1);
         there = __shfl_sync(0xffffffffu, there, 0);
         if (there != w.np - 1) continue;
         __threadfence();
         if (lane == 0) *counter = 0;   // for the next call
-        // (this warp's own sums are among them)
+        // in the order of the pieces; a warp's own sums stay where they are if they are the first or second
+        const bool keeps = w.piece <= 1;
+        if (!keeps) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int q = 0; q < 32; ++q) acc[c][q] = 0.f;
+            for (int q = 0; q < 32; ++q) acc[c][q] = 0.f;
+        }
 #pragma unroll 1
         for (int k = 0; k < w.np; ++k) {
+          if (keeps && k == w.piece) continue;
           const float4* part = parts + (size_t)k * (per / 4);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            float4 v[4];
+          for (int c = 0; c < 4; ++c) {
+            float4 v[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = __ldcg(part + (c * 4 + q) * 32);
+            for (int q = 0; q < 8; ++q) v[q] = __ldcg(part + (c * 8 + q) * 32);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float* a = &acc[c / 2][c % 2 * 16 + 4 * q];
+            for (int q = 0; q < 8; ++q) {
+              float* a = &acc[c][4 * q];
               a[0] += v[q].x;
               a[1] += v[q].y;
               a[2] += v[q].z;
@@ -374,18 +386,17 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
           }
         }
       }
-      const int k0 = w.k0 + (int)rank * 128 + wq * 32, n0 = w.n0 + (int)tile * 256;
+      const int k0 = w.k0 + (int)rank * 128 + wq * 32, n0 = w.n0;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int col = half * 128 + c * 32;
-        const uint32_t at = c % 2 * 4096;
-        if (lane == 0) bulk_wait_read<1>();
+        if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
-        stage_f32(stg + at, lane, acc[c]);
+        stage_f32(stg, lane, acc[c]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (n0 + col < p.features && k0 < p.depth) tma_store_3d(&tmo, stg_u32 + at, n0 + col, k0, w.e);
+          if (n0 + col < p.features && k0 < p.depth) tma_store_3d(&tmo, stg_u32, n0 + col, k0, w.e);
           bulk_commit();
         }
       }
@@ -394,7 +405,7 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
     __syncwarp();
   }
   fence_before_sync();
-  if constexpr (CG * PAIRS == 1) __syncthreads();
+  if constexpr (CG == 1) __syncthreads();
   else cluster_sync();
   fence_after_sync();
   if (warp == kMmaWarp) free_tmem<CG>(tmem);
@@ -403,7 +414,7 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
 // The shape of a call on a whole GB300 (its SMs set the size of the workspace).
 constexpr int64_t kSms = 152;
 struct DwShape {
-  int cg, pairs, kt, nt, kper;   // tiles of 128 cg x 256 pairs
+  int cg, kt, nt, kper;   // tiles of 128 cg x 256
   int64_t slots;                 // of as many sums
 };
 DwShape dw_shape(int64_t rows, int E, int K, int N) {
@@ -413,14 +424,12 @@ DwShape dw_shape(int64_t rows, int E, int K, int N) {
   // pairs where each has six blocks of a tile's rows to do, and K does not leave many of their tiles half empty
   const int halves = (K + 127) / 128, pairs = (halves + 1) / 2;
   s.cg = blocks * pairs * nt >= kSms / 2 * 6 && (halves % 2 == 0 || halves >= 5) ? 2 : 1;
-  // two pairs side by side, which read x once, where that leaves few tiles empty and work for all
-  s.pairs = s.cg == 2 && (nt % 2 == 0 || nt >= 5) && blocks * pairs * ((nt + 1) / 2) >= kSms / 4 * 12 ? 2 : 1;
-  s.nt = (nt + s.pairs - 1) / s.pairs;
+  s.nt = nt;
   s.kt = (K + 128 * s.cg - 1) / (128 * s.cg);
   // A piece: what a CTA (a pair) has to do on average, and not so little that adding up the pieces (2 to 3 us each, one
   // after the other) takes longer than they do (0.6 us a block): at least 2 sqrt(blocks); of one group, whose pieces are all alike, the
   // length of two rounds at most that ends first, a cut tile's sums counted as 8 blocks (written, read)
-  const int64_t tiles = (int64_t)s.kt * s.nt, shares = kSms / (s.cg * s.pairs), all = (rows + 63) / 64, each = (all * tiles + shares - 1) / shares;
+  const int64_t tiles = (int64_t)s.kt * s.nt, shares = kSms / s.cg, all = (rows + 63) / 64, each = (all * tiles + shares - 1) / shares;
   int64_t least = 8;
   while (least * least < 4 * all) ++least;
   int64_t kper = each < least ? least : each;
@@ -440,7 +449,7 @@ DwShape dw_shape(int64_t rows, int E, int K, int N) {
   return s;
 }
 
-template <int CG, int PAIRS>
+template <int CG>
 cudaError_t launch_t(GroupParams p, const void* x, int64_t x_stride, const void* dy, int64_t dy_stride, int sms,
                      cudaStream_t st) {
   const int K = p.depth, N = p.features;
@@ -449,23 +458,30 @@ cudaError_t launch_t(GroupParams p, const void* x, int64_t x_stride, const void*
   const uint64_t gd[2] = {(uint64_t)N, (uint64_t)p.rows}, gs[1] = {(uint64_t)dy_stride * 2};
   const uint64_t od[3] = {(uint64_t)N, (uint64_t)K, (uint64_t)p.E}, os[2] = {(uint64_t)N * 4, (uint64_t)N * K * 4};
   const uint32_t ibox[2] = {64, 64}, obox[3] = {32, 32, 1};
-  if (!make_tmap_tile(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, xd, xs, ibox, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_tile(&mg, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dy, gd, gs, ibox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  // [features / 64][rows][64]: a stage's boxes side by side in one copy
+  p.one_x = K % 64 == 0;
+  p.one_dy = N % 64 == 0;
+  const uint64_t xd3[3] = {64, (uint64_t)p.rows, (uint64_t)K / 64}, xs3[2] = {(uint64_t)x_stride * 2, 128};
+  const uint64_t gd3[3] = {64, (uint64_t)p.rows, (uint64_t)N / 64}, gs3[2] = {(uint64_t)dy_stride * 2, 128};
+  const uint32_t xbox[3] = {64, 64, 2}, gbox[3] = {64, 64, boxes_of<CG>() - 2};
+  auto side = [](CUtensorMap* m, bool one, const void* at, const uint64_t* d2, const uint64_t* s2, const uint32_t* b2,
+                 const uint64_t* d3, const uint64_t* s3, const uint32_t* b3) {
+    return one ? make_tmap_tile(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, at, d3, s3, b3, CU_TENSOR_MAP_SWIZZLE_128B)
+               : make_tmap_tile(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, at, d2, s2, b2, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if (!side(&mx, p.one_x, x, xd, xs, ibox, xd3, xs3, xbox) || !side(&mg, p.one_dy, dy, gd, gs, ibox, gd3, gs3, gbox) ||
       !make_tmap_tile(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p.dw, od, os, obox, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   const size_t fixed = 1024 + kStaging + lists_bytes(p.E), stage = (size_t)boxes_of<CG>() * kBox;
   p.stages = (int)((kMaxSmemPerCta - 512 - fixed) / stage);   // (512: barriers and the scan's sums)
   if (p.stages > kStagesMax) p.stages = kStagesMax;
   const size_t smem = fixed + p.stages * stage;
-  auto kern = group_dw_kernel<CG, PAIRS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  auto kern = group_dw_kernel<CG>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  static std::atomic<int> known;
-  int shares = 0;
-  if ((e = clusters_at_once<CG * PAIRS>(kern, kThreads, smem, sms, &known, &shares)) != cudaSuccess) return e;
   const int64_t most = (int64_t)p.kt * p.nt * (p.E + p.rows / 64 / p.kper + 1);
-  const unsigned grid = (unsigned)(most < shares ? most : shares) * CG * PAIRS;
-  return launch_cluster<CG * PAIRS>(kern, grid, kThreads, smem, st, p, mx, mg, mo);
+  const unsigned grid = (unsigned)(most < sms / CG ? most : sms / CG) * CG;
+  return launch_cluster<CG>(kern, grid, kThreads, smem, st, p, mx, mg, mo);
 }
 
 }  // namespace
@@ -473,11 +489,11 @@ cudaError_t launch_t(GroupParams p, const void* x, int64_t x_stride, const void*
 // counters of cut tiles (each has two slots or more), then the slots
 size_t group_dw_counters(int64_t rows, int E, int K, int N) {
   const DwShape s = dw_shape(rows, E, K, N);
-  return ((size_t)s.slots / 2 * s.cg * s.pairs * kEpiWarps * sizeof(int) + kWsAlign - 1) / kWsAlign * kWsAlign;
+  return ((size_t)s.slots / 2 * s.cg * kEpiWarps * sizeof(int) + kWsAlign - 1) / kWsAlign * kWsAlign;
 }
 size_t group_dw_bytes(int64_t rows, int E, int K, int N) {
   const DwShape s = dw_shape(rows, E, K, N);
-  return group_dw_counters(rows, E, K, N) + (size_t)s.slots * 128 * s.cg * 256 * s.pairs * sizeof(float);
+  return group_dw_counters(rows, E, K, N) + (size_t)s.slots * 128 * s.cg * 256 * sizeof(float);
 }
 
 cudaError_t launch_group_dw(const GroupParams& q, void* room, const void* x, int64_t x_stride, const void* dy,
@@ -488,8 +504,7 @@ cudaError_t launch_group_dw(const GroupParams& q, void* room, const void* x, int
   p.kt = s.kt; p.nt = s.nt; p.kper = s.kper;
   p.counters = static_cast<int*>(room);
   p.partial = reinterpret_cast<float*>(static_cast<char*>(room) + group_dw_counters(q.rows, q.E, K, N));
-  if (s.pairs == 2) return launch_t<2, 2>(p, x, x_stride, dy, dy_stride, sms, st);
-  return s.cg == 2 ? launch_t<2, 1>(p, x, x_stride, dy, dy_stride, sms, st) : launch_t<1, 1>(p, x, x_stride, dy, dy_stride, sms, st);
+  return s.cg == 2 ? launch_t<2>(p, x, x_stride, dy, dy_stride, sms, st) : launch_t<1>(p, x, x_stride, dy, dy_stride, sms, st);
 }
 
 }  // namespace hstu

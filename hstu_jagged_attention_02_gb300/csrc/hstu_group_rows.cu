@@ -159,15 +159,15 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
     // ------------------------------------------------- A
     if (lane == 0) {
       int stage = 0;
-      uint32_t phase = 0, used = 0;
-      uint32_t last[kStagesMax];
+      uint32_t phase = 0, loads = 0;
+      const uint32_t there0 = CG == 1 ? 0u : in_cta(bar(B_AFULL), 0);
       bool ok = true, withhold = p.test_timeout && rank == 0 && w.more() && w.begin == 0;
       for (; ok && w.more(); w.next()) {
         const int f = w.f0 + (int)rank * 128;
         for (int kb = 0; kb < kblocks; ++kb) {
-          if (used >> stage & 1) ok = mbar_wait(bar(B_AEMPTY + stage), phase ^ 1, wd, 61);
+          if (loads >= (uint32_t)p.stages) ok = mbar_wait(bar(B_AEMPTY + stage), phase ^ 1, wd, 61);
           if (!ok) break;
-          used |= 1u << stage;
+          ++loads;
           const uint32_t dst = a_at + stage * kABytes, full = bar(B_AFULL + stage);
           if (withhold) {   // test only: this copy never comes
             withhold = false;
@@ -176,64 +176,59 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
             if constexpr (CG == 1) {
               if (KMAJOR) {
                 tma_load_3d(dst, &tmw, full, kb * 64, f, w.e);
+              } else if (p.one_w) {
+                tma_load_4d(dst, &tmw, full, 0, kb * 64, f >> 6, w.e);
               } else {
                 tma_load_3d(dst, &tmw, full, f, kb * 64, w.e);
                 tma_load_3d(dst + kABytes / 2, &tmw, full, f + 64, kb * 64, w.e);
               }
             } else {
-              const uint32_t there = in_cta(full, 0);
+              const uint32_t there = there0 + 8u * (uint32_t)stage;
               if (KMAJOR) {
                 pair_load_3d(dst, &tmw, there, kb * 64, f, w.e);
+              } else if (p.one_w) {
+                pair_load_4d(dst, &tmw, there, 0, kb * 64, f >> 6, w.e);
               } else {
                 pair_load_3d(dst, &tmw, there, f, kb * 64, w.e);
                 pair_load_3d(dst + kABytes / 2, &tmw, there, f + 64, kb * 64, w.e);
               }
             }
           }
-#pragma unroll
-          for (int s = 0; s < kStagesMax; ++s)
-            if (s == stage) last[s] = phase;
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1;
           }
         }
       }
-      tail<CG>(bar, B_AEMPTY, B_AFULL, p.stages, stage, phase, used, last, rank, ok, wd, 67);
+      tail<CG>(bar, B_AEMPTY, B_AFULL, p.stages, stage, phase, loads, rank, ok, wd, 67);
     }
   } else if (warp == kRowsWarp) {
     // ------------------------------------------------- B
     if (lane == 0) {
       int slot = 0;
-      uint32_t phase = 0, used = 0;
-      uint32_t last[kSlotsMax];
+      uint32_t phase = 0, loads = 0;
       bool ok = true;
       const int ring = resident ? kblocks : p.slots;
+      const uint32_t there0 = CG == 1 ? 0u : in_cta(bar(B_BFULL), 0);
       for (; ok && w.more(); w.next()) {
         if (resident && !w.fresh()) continue;
-        const int mine = columns() / CG, boxes = (mine + p.box_rows - 1) / p.box_rows;
-        const uint32_t box_bytes = (uint32_t)p.box_rows * 128u;
+        const int mine = columns() / CG;
         const int row = w.row0 + (int)rank * mine;
         for (int kb = 0; kb < kblocks; ++kb) {
-          if (used >> slot & 1) ok = mbar_wait(bar(B_BEMPTY + slot), phase ^ 1, wd, 65);
+          if (loads >= (uint32_t)ring) ok = mbar_wait(bar(B_BEMPTY + slot), phase ^ 1, wd, 65);
           if (!ok) break;
-          used |= 1u << slot;
+          ++loads;
           const uint32_t dst = b_at + slot * slot_bytes, full = bar(B_BFULL + slot);
-          if (rank == 0) mbar_arrive_expect_tx(full, CG * boxes * box_bytes);
-          for (int b = 0; b < boxes; ++b) {
-            if constexpr (CG == 1) tma_load_2d(dst + b * box_bytes, &tmr, full, kb * 64, row + b * p.box_rows);
-            else pair_load_2d(dst + b * box_bytes, &tmr, in_cta(full, 0), kb * 64, row + b * p.box_rows);
-          }
-#pragma unroll
-          for (int s = 0; s < kSlotsMax; ++s)
-            if (s == slot) last[s] = phase;
+          if (rank == 0) mbar_arrive_expect_tx(full, CG * slot_bytes);
+          if constexpr (CG == 1) tma_load_2d(dst, &tmr, full, kb * 64, row);
+          else pair_load_2d(dst, &tmr, there0 + 8u * (uint32_t)slot, kb * 64, row);
           if (++slot == ring) {
             slot = 0;
             phase ^= 1;
           }
         }
       }
-      tail<CG>(bar, B_BEMPTY, B_BFULL, ring, slot, phase, used, last, rank, ok, wd, 68);
+      tail<CG>(bar, B_BEMPTY, B_BFULL, ring, slot, phase, loads, rank, ok, wd, 68);
     }
   } else if (warp == kMmaWarp) {
     if (lane == 0 && rank == 0) {
@@ -371,13 +366,18 @@ template <int CG, bool KMAJOR, typename TO>
 cudaError_t launch_t(GroupParams p, const void* rows, int64_t row_stride, const void* w, int K, int N, int sms,
                      cudaStream_t st) {
   CUtensorMap mw, mr, mo;
-  p.box_rows = p.row_block / CG < 64 ? p.row_block / CG : 64;
+  p.box_rows = p.row_block / CG;
+  // [g][features / 64][k][64]: a stage's two boxes in one copy
+  p.one_w = !KMAJOR && N % 64 == 0;
+  const uint64_t wd4[4] = {64, (uint64_t)K, (uint64_t)N / 64, (uint64_t)p.E}, ws4[3] = {(uint64_t)N * 2, 128, (uint64_t)N * K * 2};
+  const uint32_t wbox4[4] = {64, 64, 2, 1};
   const uint64_t wd[3] = {(uint64_t)N, (uint64_t)K, (uint64_t)p.E}, ws[2] = {(uint64_t)N * 2, (uint64_t)N * K * 2};
   const uint32_t wbox[3] = {64, KMAJOR ? 128u : 64u, 1};
   const uint64_t rd[2] = {(uint64_t)p.depth, (uint64_t)p.rows}, rs[1] = {(uint64_t)row_stride * 2};
   const uint32_t rbox[2] = {64, (uint32_t)p.box_rows}, obox[2] = {32, 32};
   const uint64_t od[2] = {(uint64_t)p.features, (uint64_t)p.rows}, os[1] = {(uint64_t)p.out_stride * sizeof(TO)};
-  if (!make_tmap_tile(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, w, wd, ws, wbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  if (!(p.one_w ? make_tmap_tile(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, w, wd4, ws4, wbox4, CU_TENSOR_MAP_SWIZZLE_128B)
+                : make_tmap_tile(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, w, wd, ws, wbox, CU_TENSOR_MAP_SWIZZLE_128B)) ||
       !make_tmap_tile(&mr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, rd, rs, rbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_tile(&mo, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.out,
                       od, os, obox, sizeof(TO) == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE))

@@ -114,10 +114,8 @@ def test_slots_hold_every_split(E):
             halves, nt = -(-K // 128), -(-N // 256)
             pair = (rows // 64 + min(rows, E)) * -(-halves // 2) * nt >= 456 and (halves % 2 == 0 or halves >= 5)
             cg = 2 if pair else 1
-            two = pair and (nt % 2 == 0 or nt >= 5) and (rows // 64 + min(rows, E)) * -(-halves // 2) * -(-nt // 2) >= 456
-            cg, wide = (4, 2) if two else (cg, 1)   # CTAs of a tile, of 256 columns each
             slots = (ws - zero) // (4 * 128 * cg * 256)
-            tiles = -(-halves // (cg // wide)) * -(-nt // wide)
+            tiles = -(-halves // cg) * nt
             kper = max(8, int(np.ceil(2 * np.sqrt(-(-rows // 64)))), -(-(-(-rows // 64) * tiles) // (152 // cg)))
             for k in range(20):
                 share = rng.random(E) ** (10 if k % 2 else 1)
