@@ -135,31 +135,38 @@ template <int CG> __device__ __forceinline__ void free_tmem(uint32_t taddr) {
   if constexpr (CG == 1) tmem_dealloc(taddr, 512);
   else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(512) : "memory");
 }
+// Issued by one elected lane of a converged warp, which runs the loop around them as one, so that operands are
+// uniform values (an issuing thread alone took 800 cycles for a stage's four products, which take the tensor core 512).
 template <int CG> __device__ __forceinline__ void mma(uint32_t d, SDesc a, SDesc b, uint32_t idesc, uint32_t accumulate) {
   if constexpr (CG == 1) {
-    mma_ss_w(d, a, b, idesc, accumulate);
+    mma_ss_e(d, a, b, idesc, accumulate);
   } else {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
-        "setp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\telect.sync _|e, 0xffffffff;\n\tmov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t@e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
         "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
         : "memory");
   }
 }
-// arrives on the barrier (of all CTAs of the mask) when every tcgen05 operation so far has completed
-template <int CG> __device__ __forceinline__ void commit(uint32_t bar, uint16_t mask) {
-  if constexpr (CG == 1) mma_commit(bar);
+// arrives on the barrier (of both CTAs of a pair) when every tcgen05 operation so far has completed
+template <int CG> __device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (CG == 1) mma_commit_e(bar);
   else
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-                 "h"(mask)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
 }
 
 // the same, on the issuing CTA's barrier alone
 template <int CG> __device__ __forceinline__ void commit_here(uint32_t bar) {
-  if constexpr (CG == 1) mma_commit(bar);
+  if constexpr (CG == 1) mma_commit_e(bar);
   else
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
 }
 
 // A loading thread's end; (stage, phase) is the next to be loaded, `loads` the loads so far.  Every stage is waited for once

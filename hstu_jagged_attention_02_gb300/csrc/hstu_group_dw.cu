@@ -237,47 +237,48 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
     int stage = 0;
     uint32_t phase = 0, n = 0, cuts = 0;
     bool ok = true;
+    auto wait = [&](uint32_t at, uint32_t parity, int site) { return __all_sync(0xffffffffu, mbar_wait(at, parity, wd, site)) != 0; };
+    const SDesc da0 = sdesc_w(base, kBox, 1024), db0 = sdesc_w(base + 2 * kBox, kBox, 1024);
     // a block's products and their arrivals
-    auto products = [&](int at, uint32_t d, bool first, bool last) {
+    auto products = [&](uint32_t first, bool last) {
       fence_after_sync();
-      const uint32_t sA = base + at * kStage, sB = sA + 2 * kBox;
-      const SDesc da = sdesc_w(sA, kBox, 1024), db = sdesc_w(sB, kBox, 1024);
+      const uint32_t d = tmem + (n & 1) * 256;
+      const SDesc da = da0 + stage * kStage, db = db0 + stage * kStage;
+      mma<CG>(d, da, db, IDESC, first ? 0u : 1u);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) mma<CG>(tmem + d * 256, da + kk * 2048, db + kk * 2048, IDESC, first && kk == 0 ? 0u : 1u);
-      commit<CG>(bar(B_EMPTY + at), 3);
-      if (last) commit<CG>(bar(B_DFULL + d), 3);
+      for (int kk = 1; kk < 4; ++kk) mma<CG>(d, da + kk * 2048, db + kk * 2048, IDESC, 1u);
+      commit<CG>(bar(B_EMPTY) + stage * 8);
+      if (last) commit<CG>(bar(B_DFULL) + (n & 1) * 8);
+    };
+    auto next = [&]() {
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
     };
     for (; ok && w.more(); w.next()) {
-      // whole blocks, one thread's work
       const int whole = w.rows >> 6;
-      if (rank == 0 && lane == 0) {
-        int at = stage;
-        uint32_t ph = phase, acc = n;
+      if (rank == 0) {
         for (int kb = 0; kb < whole; ++kb) {
           const bool first = kb % kRun == 0, last = kb % kRun == kRun - 1 || kb == w.blocks - 1;
-          if (first) ok = mbar_wait(bar(B_DEMPTY + (acc & 1)), ((acc >> 1) & 1) ^ 1, wd, 72);
-          if (ok) ok = mbar_wait(bar(B_FULL + at), ph, wd, 73);
+          if (first) ok = wait(bar(B_DEMPTY) + (n & 1) * 8, ((n >> 1) & 1) ^ 1, 72);
+          if (ok) ok = wait(bar(B_FULL) + stage * 8, phase, 73);
           if (!ok) break;
-          products(at, acc & 1, first, last);
-          acc += last ? 1u : 0u;
-          if (++at == p.stages) {
-            at = 0;
-            ph ^= 1;
-          }
+          products(first, last);
+          n += last ? 1u : 0u;
+          next();
         }
+      } else {
+        phase ^= (uint32_t)((stage + whole) / p.stages) & 1u;
+        stage = (stage + whole) % p.stages;
       }
-      __syncwarp();
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
-      n += whole / kRun + (whole == w.blocks && whole % kRun != 0 ? 1 : 0);
-      phase ^= (uint32_t)((stage + whole) / p.stages) & 1u;
-      stage = (stage + whole) % p.stages;
       if (whole == w.blocks) continue;
       // a block in which the group ends
       const bool first = whole % kRun == 0;
-      if (rank == 0 && first) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_DEMPTY + (n & 1)), ((n >> 1) & 1) ^ 1, wd, 72));
+      if (rank == 0 && first) ok = wait(bar(B_DEMPTY) + (n & 1) * 8, ((n >> 1) & 1) ^ 1, 72);
       // (the second CTA's barriers have no other phases than those of such blocks)
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_FULL + stage), rank == 0 ? phase : cuts >> stage & 1, wd, 73));
+      if (ok) ok = wait(bar(B_FULL) + stage * 8, rank == 0 ? phase : cuts >> stage & 1, 73);
       if (!ok) break;
       // rows of the next group: cleared (a row is 128 bytes of each box, whatever the swizzle)
       uint8_t* s = smem + stage * kStage;
@@ -290,17 +291,14 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
       if (CG == 2 && rank == 0) ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(B_CLEAR + stage), cuts >> stage & 1, wd, 77));
       if (!ok) break;
       cuts ^= 1u << stage;
-      if (rank == 0 && lane == 0) products(stage, n & 1, first, true);
-      __syncwarp();
+      if (rank == 0) products(first, true);
       ++n;
-      if (++stage == p.stages) {
-        stage = 0;
-        phase ^= 1;
-      }
+      next();
     }
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
+      __syncwarp();
       commit_here<CG>(bar(B_DRAIN));
-      drain(bar(B_DRAIN), 0);
+      if (lane == 0) drain(bar(B_DRAIN), 0);
     }
     __syncwarp();
   } else {

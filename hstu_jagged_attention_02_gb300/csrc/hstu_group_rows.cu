@@ -231,46 +231,48 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
       tail<CG>(bar, B_BEMPTY, B_BFULL, ring, slot, phase, loads, rank, ok, wd, 68);
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       int stage = 0, slot = 0;
       uint32_t phase = 0, slot_phase = 0, n = 0;
+      const SDesc da0 = KMAJOR ? sdesc_w(a_at, 16, 1024) : sdesc_w(a_at, kABytes / 2, 1024), db0 = sdesc_w(b_at, 16, 1024);
+      const int ring = resident ? kblocks : p.slots;
+      auto wait = [&](uint32_t at, uint32_t parity, int site) { return __all_sync(0xffffffffu, mbar_wait(at, parity, wd, site)) != 0; };
       bool ok = true;
       for (; ok && w.more(); w.next(), ++n) {
-        const uint32_t d = n & 1;
-        ok = mbar_wait(bar(B_DEMPTY + d), ((n >> 1) & 1) ^ 1, wd, 62);
+        const uint32_t d = tmem + (n & 1) * 256;
+        ok = wait(bar(B_DEMPTY) + (n & 1) * 8, ((n >> 1) & 1) ^ 1, 62);
         if (!ok) break;
-        fence_after_sync();
         const uint32_t idesc = idesc_bf16(wide, columns(), !KMAJOR, false);
         const bool fresh = !resident || w.fresh(), release = !resident || w.last();
         for (int kb = 0; kb < kblocks; ++kb) {
           if (fresh) {
-            ok = mbar_wait(bar(B_BFULL + slot), slot_phase, wd, 66);
+            ok = wait(bar(B_BFULL) + slot * 8, slot_phase, 66);
             if (!ok) break;
           }
-          ok = mbar_wait(bar(B_AFULL + stage), phase, wd, 63);
+          ok = wait(bar(B_AFULL) + stage * 8, phase, 63);
           if (!ok) break;
           fence_after_sync();
-          const uint32_t sA = a_at + stage * kABytes, sB = b_at + slot * slot_bytes;
-          const SDesc da = KMAJOR ? sdesc_w(sA, 16, 1024) : sdesc_w(sA, kABytes / 2, 1024);
-          const SDesc db = sdesc_w(sB, 16, 1024);
+          const SDesc da = da0 + stage * kABytes, db = db0 + slot * slot_bytes;
+          mma<CG>(d, da, db, idesc, kb > 0 ? 1u : 0u);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma<CG>(tmem + d * 256, da + (KMAJOR ? kk * 32 : kk * 2048), db + kk * 32, idesc, kb > 0 || kk > 0 ? 1u : 0u);
-          commit<CG>(bar(B_AEMPTY + stage), 3);
-          if (release) commit<CG>(bar(B_BEMPTY + slot), 3);
+          for (int kk = 1; kk < 4; ++kk) mma<CG>(d, da + (KMAJOR ? kk * 32 : kk * 2048), db + kk * 32, idesc, 1u);
+          commit<CG>(bar(B_AEMPTY) + stage * 8);
+          if (release) commit<CG>(bar(B_BEMPTY) + slot * 8);
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1;
           }
-          if (++slot == (resident ? kblocks : p.slots)) {
+          if (++slot == ring) {
             slot = 0;
             if (release) slot_phase ^= 1;
           }
         }
-        if (ok) commit<CG>(bar(B_DFULL + d), 3);
+        if (ok) commit<CG>(bar(B_DFULL) + (n & 1) * 8);
       }
+      __syncwarp();
       commit_here<CG>(bar(B_DRAIN));
-      drain(bar(B_DRAIN), 0);
+      if (lane == 0) drain(bar(B_DRAIN), 0);
+      __syncwarp();
     }
   } else {
     // a warp stores 32 features of 32 rows at a time, through its staging buffer [row][feature]
