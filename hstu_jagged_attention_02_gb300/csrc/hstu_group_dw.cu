@@ -194,44 +194,44 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
   Pieces w(lists, p, 128 * CG, blockIdx.x / CG, gridDim.x / CG, good);
 
   if (warp == kLoadWarp) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, loads = 0;
-      bool ok = true;
-      const uint32_t there = CG == 1 ? bar(B_FULL) : in_cta(bar(B_FULL), 0);   // the pair's barriers
-      auto copies = [&](uint32_t dst, const CUtensorMap* map, int boxes, bool one, uint32_t full, bool here, int x, int row) {
-        if (one) {
-          if (CG == 1 || here) tma_load_3d(dst, map, full, 0, row, x >> 6);
-          else pair_load_3d(dst, map, full, 0, row, x >> 6);
-        } else {
+    int stage = 0;
+    uint32_t phase = 0, loads = 0;
+    bool ok = true;
+    const uint32_t there = CG == 1 ? bar(B_FULL) : in_cta(bar(B_FULL), 0);   // the pair's barriers
+    auto copies = [&](uint32_t dst, const CUtensorMap* map, int boxes, bool one, uint32_t full, bool here, int x, int row) {
+      if (one) {
+        if (CG == 1 || here) load_3d<false>(dst, map, full, 0, row, x >> 6);
+        else load_3d<true>(dst, map, full, 0, row, x >> 6);
+      } else {
 #pragma unroll
-          for (int c = 0; c < boxes; ++c) {
-            if (CG == 1 || here) tma_load_2d(dst + c * kBox, map, full, x + c * 64, row);
-            else pair_load_2d(dst + c * kBox, map, full, x + c * 64, row);
-          }
-        }
-      };
-      for (; ok && w.more(); w.next()) {
-        const int k0 = w.k0 + (int)rank * 128, n0 = w.n0 + (int)rank * 128;
-        int row = w.row0;
-        for (int left = w.rows; left > 0; left -= 64, row += 64) {
-          if (loads >= (uint32_t)p.stages) ok = mbar_wait(bar(B_EMPTY + stage), phase ^ 1, wd, 71);
-          if (!ok) break;
-          ++loads;
-          const uint32_t s = base + stage * kStage, mine = bar(B_FULL + stage);
-          const bool cut = CG == 2 && left < 64;   // the group ends inside: each CTA's copies count on its own barrier
-          const uint32_t full = cut ? mine : there + 8u * (uint32_t)stage;
-          if (cut || rank == 0) mbar_arrive_expect_tx(mine, cut || CG == 1 ? kStage : 2 * kStage);
-          copies(s, &tmx, 2, p.one_x, full, cut, k0, row);
-          copies(s + 2 * kBox, &tmg, BOXES - 2, p.one_dy, full, cut, n0, row);
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1;
-          }
+        for (int c = 0; c < boxes; ++c) {
+          if (CG == 1 || here) load_2d<false>(dst + c * kBox, map, full, x + c * 64, row);
+          else load_2d<true>(dst + c * kBox, map, full, x + c * 64, row);
         }
       }
-      tail<CG>(bar, B_EMPTY, B_FULL, p.stages, stage, phase, loads, rank, ok, wd, 75);
+    };
+    for (; ok && w.more(); w.next()) {
+      const int k0 = w.k0 + (int)rank * 128, n0 = w.n0 + (int)rank * 128;
+      int row = w.row0;
+      for (int left = w.rows; left > 0; left -= 64, row += 64) {
+        if (loads >= (uint32_t)p.stages) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_EMPTY) + stage * 8, phase ^ 1, wd, 71)) != 0;
+        if (!ok) break;
+        ++loads;
+        const uint32_t s = base + stage * kStage, mine = bar(B_FULL) + stage * 8;
+        const bool cut = CG == 2 && left < 64;   // the group ends inside: each CTA's copies count on its own barrier
+        const uint32_t full = cut ? mine : there + 8u * (uint32_t)stage;
+        if (lane == 0 && (cut || rank == 0)) mbar_arrive_expect_tx(mine, cut || CG == 1 ? kStage : 2 * kStage);
+        __syncwarp();
+        copies(s, &tmx, 2, p.one_x, full, cut, k0, row);
+        copies(s + 2 * kBox, &tmg, BOXES - 2, p.one_dy, full, cut, n0, row);
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
     }
+    if (lane == 0) tail<CG>(bar, B_EMPTY, B_FULL, p.stages, stage, phase, loads, rank, ok, wd, 75);
+    __syncwarp();
   } else if (warp == kMmaWarp) {
     const uint32_t IDESC = idesc_bf16(128 * CG, 256, true, true);
     int stage = 0;

@@ -157,79 +157,64 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------- A
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, loads = 0;
-      const uint32_t there0 = CG == 1 ? 0u : in_cta(bar(B_AFULL), 0);
-      bool ok = true, withhold = p.test_timeout && rank == 0 && w.more() && w.begin == 0;
-      for (; ok && w.more(); w.next()) {
-        const int f = w.f0 + (int)rank * 128;
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (loads >= (uint32_t)p.stages) ok = mbar_wait(bar(B_AEMPTY + stage), phase ^ 1, wd, 61);
-          if (!ok) break;
-          ++loads;
-          const uint32_t dst = a_at + stage * kABytes, full = bar(B_AFULL + stage);
-          if (withhold) {   // test only: this copy never comes
-            withhold = false;
+    int stage = 0;
+    uint32_t phase = 0, loads = 0;
+    const uint32_t there = CG == 1 ? bar(B_AFULL) : in_cta(bar(B_AFULL), 0);   // the pair's barriers
+    bool ok = true, withhold = p.test_timeout && rank == 0 && w.more() && w.begin == 0;
+    for (; ok && w.more(); w.next()) {
+      const int f = w.f0 + (int)rank * 128;
+      for (int kb = 0; kb < kblocks; ++kb) {
+        if (loads >= (uint32_t)p.stages) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_AEMPTY) + stage * 8, phase ^ 1, wd, 61)) != 0;
+        if (!ok) break;
+        ++loads;
+        if (withhold) {   // test only: this copy never comes
+          withhold = false;
+        } else {
+          const uint32_t dst = a_at + stage * kABytes, full = there + stage * 8;
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(B_AFULL) + stage * 8, CG * kABytes);
+          __syncwarp();
+          if (KMAJOR) {
+            load_3d<CG == 2>(dst, &tmw, full, kb * 64, f, w.e);
+          } else if (p.one_w) {
+            load_4d<CG == 2>(dst, &tmw, full, 0, kb * 64, f >> 6, w.e);
           } else {
-            if (rank == 0) mbar_arrive_expect_tx(full, CG * kABytes);
-            if constexpr (CG == 1) {
-              if (KMAJOR) {
-                tma_load_3d(dst, &tmw, full, kb * 64, f, w.e);
-              } else if (p.one_w) {
-                tma_load_4d(dst, &tmw, full, 0, kb * 64, f >> 6, w.e);
-              } else {
-                tma_load_3d(dst, &tmw, full, f, kb * 64, w.e);
-                tma_load_3d(dst + kABytes / 2, &tmw, full, f + 64, kb * 64, w.e);
-              }
-            } else {
-              const uint32_t there = there0 + 8u * (uint32_t)stage;
-              if (KMAJOR) {
-                pair_load_3d(dst, &tmw, there, kb * 64, f, w.e);
-              } else if (p.one_w) {
-                pair_load_4d(dst, &tmw, there, 0, kb * 64, f >> 6, w.e);
-              } else {
-                pair_load_3d(dst, &tmw, there, f, kb * 64, w.e);
-                pair_load_3d(dst + kABytes / 2, &tmw, there, f + 64, kb * 64, w.e);
-              }
-            }
-          }
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1;
+            load_3d<CG == 2>(dst, &tmw, full, f, kb * 64, w.e);
+            load_3d<CG == 2>(dst + kABytes / 2, &tmw, full, f + 64, kb * 64, w.e);
           }
         }
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
-      tail<CG>(bar, B_AEMPTY, B_AFULL, p.stages, stage, phase, loads, rank, ok, wd, 67);
     }
+    if (lane == 0) tail<CG>(bar, B_AEMPTY, B_AFULL, p.stages, stage, phase, loads, rank, ok, wd, 67);
+    __syncwarp();
   } else if (warp == kRowsWarp) {
     // ------------------------------------------------- B
-    if (lane == 0) {
-      int slot = 0;
-      uint32_t phase = 0, loads = 0;
-      bool ok = true;
-      const int ring = resident ? kblocks : p.slots;
-      const uint32_t there0 = CG == 1 ? 0u : in_cta(bar(B_BFULL), 0);
-      for (; ok && w.more(); w.next()) {
-        if (resident && !w.fresh()) continue;
-        const int mine = columns() / CG;
-        const int row = w.row0 + (int)rank * mine;
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (loads >= (uint32_t)ring) ok = mbar_wait(bar(B_BEMPTY + slot), phase ^ 1, wd, 65);
-          if (!ok) break;
-          ++loads;
-          const uint32_t dst = b_at + slot * slot_bytes, full = bar(B_BFULL + slot);
-          if (rank == 0) mbar_arrive_expect_tx(full, CG * slot_bytes);
-          if constexpr (CG == 1) tma_load_2d(dst, &tmr, full, kb * 64, row);
-          else pair_load_2d(dst, &tmr, there0 + 8u * (uint32_t)slot, kb * 64, row);
-          if (++slot == ring) {
-            slot = 0;
-            phase ^= 1;
-          }
+    int slot = 0;
+    uint32_t phase = 0, loads = 0;
+    bool ok = true;
+    const int ring = resident ? kblocks : p.slots;
+    const uint32_t there = CG == 1 ? bar(B_BFULL) : in_cta(bar(B_BFULL), 0);
+    for (; ok && w.more(); w.next()) {
+      if (resident && !w.fresh()) continue;
+      const int row = w.row0 + (int)rank * (columns() / CG);
+      for (int kb = 0; kb < kblocks; ++kb) {
+        if (loads >= (uint32_t)ring) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_BEMPTY) + slot * 8, phase ^ 1, wd, 65)) != 0;
+        if (!ok) break;
+        ++loads;
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(B_BFULL) + slot * 8, CG * slot_bytes);
+        __syncwarp();
+        load_2d<CG == 2>(b_at + slot * slot_bytes, &tmr, there + slot * 8, kb * 64, row);
+        if (++slot == ring) {
+          slot = 0;
+          phase ^= 1;
         }
       }
-      tail<CG>(bar, B_BEMPTY, B_BFULL, ring, slot, phase, loads, rank, ok, wd, 68);
     }
+    if (lane == 0) tail<CG>(bar, B_BEMPTY, B_BFULL, ring, slot, phase, loads, rank, ok, wd, 68);
+    __syncwarp();
   } else if (warp == kMmaWarp) {
     if (rank == 0) {
       int stage = 0, slot = 0;
