@@ -3,8 +3,14 @@
 //
 // Tiles of a dW[g] of 128 features of x a CTA by 256 of dy, summed over the group's rows in
 // 64s: both operands are read with features contiguous (MN-major).  CTAs work in pairs (cta_group::2,
-// 256 x 256; each holds half of both operands) where there is work for all of them, since what bounds is
-// the way from L2 to the SMs.
+// 256 x 256; each holds half of both operands) where there is work for all of them: for large batches single CTAs
+// come to the 12 TB/s at which the SMs read L2 (161,293 rows, 512 x 2048: 308 us against 248).
+//
+// What bounds a pair is what its loading and issuing warps do for a stage (4 products of 128 tensor-core cycles):
+// a copy an operand where the width is a multiple of 64 (a 3-D map, 64 features innermost), both warps run their loops as one with
+// an elected lane (uniform operands): 293 us with a copy for each 64 features and single threads, 234 us so (231-250, by
+// the clock: the board is at its power limit then), cuBLAS's product of one group of that size 208-211 us.  Stages: 267 us with
+// 4, 248 with 5, 246 with 6.  Two pairs side by side that share x by multicast were no faster (252 us).
 //
 // Rows of the next group (or past the end) in a group's last 64 are cleared in shared memory
 // before the tensor core reads them, in both operands, since 0 x infinity is no zero.  Such a block
@@ -12,7 +18,7 @@
 //
 // Precision: the tensor core's sums lose a little at every addition, always towards zero.  The
 // accumulator so is read after 16 blocks (1,024 rows) and added up in registers (128 a thread), while
-// the second accumulator takes the next 16: 2.5e-6 of dW at 6,415 rows in one accumulator, against 6e-7 of a
+// the second accumulator takes the next 16: 2.5e-6 of dW at 6,415 rows in one accumulator, 0.9e-6 so, against 0.6e-6 of a
 // plain FP32 product.
 //
 // Groups of many rows are cut into pieces of about equal length, so that one large group fills

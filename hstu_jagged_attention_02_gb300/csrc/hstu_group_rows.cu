@@ -9,11 +9,15 @@
 //   reads the next group's weights;
 //   B = up to 256 rows x 64 k of x (K-major).  Rows of the next group that a load brings
 //   along give columns that nobody stores.
-// What bounds large batches is the way from L2 to the SMs (12 TB/s measured: single CTAs that
+// What bounded large batches was the way from L2 to the SMs (12 TB/s measured: single CTAs that
 // load A and B for each 128 x 256 tile took 324 us for 161,293 rows, 512 -> 2048, whatever the tensor core had
 // to do).  So CTAs work in pairs (cta_group::2: 256 features, each CTA holds half of A and half of
 // B), and walk neighbouring tiles, which have the same rows: where the depth allows (512),
-// B stays in shared memory from one tile to the next and A alone streams.
+// B stays in shared memory from one tile to the next and A alone streams: 250 us (cuBLAS's product of one group of that
+// size 231-249; the board is at its power limit), dx 240 us (195-204).  What is left of a stage's 780 cycles beyond
+// the tensor core's 512: waits of 50 cycles each on barriers that are there already, commits (75 each), and
+// in the forward the storing warps, 5,000 cycles for a pair's 256 x 256.  The loading and issuing warps run their
+// loops as one with an elected lane, so that operands are uniform values.
 // Two accumulators in TMEM, so that a tile is stored while the next one is computed.
 //
 // Roles (352 threads): warps 0-7 store, warp 8 loads A, warp 10 B, warp 9 issues (the pair's first CTA) and
