@@ -8,6 +8,11 @@
 // adds its teams' sums in shared memory and leaves a row of 2 D sums in the
 // workspace, and a second kernel adds these rows, column by column, in their
 // order.
+//
+// 16,410 rows of 512, BF16: 14.2 us (floor 7.5), of which the second kernel takes 3: 16 warps an SM, whose lanes' sums
+// and rows fill 128 registers, wait for loads (a third of the stalls) and shuffles.  4,099 FP32 rows of 301: 5.3 us, two launches.
+// Teams of 64 lanes with half of the sums each were slower (20 us), and narrow rows want more of them than a warp
+// gives: 107,181 rows of 89 took 31 us with a warp a row, 12 us with 16 lanes.
 #include "hstu_ln.cuh"
 
 namespace hstu {

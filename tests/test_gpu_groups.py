@@ -259,3 +259,29 @@ def test_a_wait_that_runs_out_ends_the_call():
     assert again.device_error() == 0
     want = torch.cat([x[:100].double() @ w[0].double(), x[100:].double() @ w[1].double()])
     assert torch.allclose(again.y.double(), want, rtol=2.0 ** -8, atol=1e-3)
+
+
+@pytest.mark.parametrize("sizes,K,N", [
+    ((257, 0, 16_000, 63), 256, 264), ((4_000, 13_000), 264, 256), ((9_000, 9_100, 1), 192, 576),   # pairs
+    ((200, 7, 64), 192, 72), ((200, 7, 64), 72, 192), ((1, 90, 33), 64, 320),
+])
+def test_columns_of_wider_tensors(sizes, K, N):
+    """Operands and results with other data (NaN) beside their columns; widths that come in one copy and that do not."""
+    from hstu_jagged_attention_02_gb300.groups import GroupProblem
+    x0, w, off, dy0 = _inputs(sizes, K, N, seed=K + 3 * N)
+    T = x0.shape[0]
+    wide = lambda n, at, dt=torch.bfloat16: torch.full((T, n + 200), float("nan"), device="cuda", dtype=dt)[:, at:at + n]  # noqa: E731
+    x, dy, y, dx = wide(K, 64), wide(N, 8), wide(N, 128), wide(K, 16, torch.float32)
+    x.copy_(x0)
+    dy.copy_(dy0)
+    pr = GroupProblem(x, w, off, dy=dy, y=y, dx=dx)
+    assert pr.x is x and pr.dy is dy and pr.y is y and pr.dx is dx
+    pr.forward()
+    pr.backward()
+    assert pr.device_error() == 0
+    ref = GroupProblem(x0, w, off, dy=dy0, dx_dtype=torch.float32)
+    ref.forward()
+    ref.backward()
+    assert torch.equal(y, ref.y) and torch.equal(dx, ref.dx) and torch.equal(pr.dw, ref.dw)
+    assert bool(torch.isnan(y._base[:, :128]).all()) and bool(torch.isnan(dx._base[:, K + 16:]).all())
+    _check_all(ref, x0, w, off, dy0, "bf16", "fp32")
