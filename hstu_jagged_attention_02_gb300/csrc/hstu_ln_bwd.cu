@@ -11,7 +11,7 @@
 //
 // 16,410 rows of 512, BF16: 14.2 us (floor 7.5), of which the second kernel takes 3: 16 warps an SM, whose lanes' sums
 // and rows fill 128 registers, wait for loads (a third of the stalls) and shuffles.  4,099 FP32 rows of 301: 5.3 us, two launches.
-// Teams of 64 lanes with half of the sums each were slower (20 us), and narrow rows want more of them than a warp
+// Teams of 64 lanes with half of the sums each were slower (20 us); narrow rows want more of them than a warp
 // gives: 107,181 rows of 89 took 31 us with a warp a row, 12 us with 16 lanes.
 #include "hstu_ln.cuh"
 
@@ -283,16 +283,25 @@ ln_sum_kernel(const float* __restrict__ partial, int rows, int D, float* d_weigh
   }
 }
 
-template <typename F>
+// SHORT (both sides BF16): a row's 16 features a lane leave room for the next row's, and smaller teams have more rows under
+// way (16,000 rows of 1,024 22.3 us against 26.5, of 2,048 38.9 against 47.6; 8,000 of 4,096 40.1 against 52.4).  With
+// an FP32 side there is none, and 8 features a lane are ahead (8,000 FP32 rows of 4,096 73.4 us against 84.1).
+template <bool SHORT, typename F>
 auto dispatch_bwd_shape(int D, bool wide, F&& go) {
   if (wide) {
     if (D <= 64) return go(Shape<8, 8, 1>());
     if (D <= 128) return go(Shape<8, 16, 1>());
     if (D <= 256) return go(Shape<8, 32, 1>());
     if (D <= 512) return go(Shape<8, 32, 2>());
-    if (D <= 1024) return go(Shape<8, 128, 1>());
-    if (D <= 2048) return go(Shape<8, 256, 1>());
-    if (D <= 4096) return go(Shape<8, 512, 1>());
+    if constexpr (SHORT) {
+      if (D <= 1024) return go(Shape<8, 64, 2>());
+      if (D <= 2048) return go(Shape<8, 128, 2>());
+      if (D <= 4096) return go(Shape<8, 256, 2>());
+    } else {
+      if (D <= 1024) return go(Shape<8, 128, 1>());
+      if (D <= 2048) return go(Shape<8, 256, 1>());
+      if (D <= 4096) return go(Shape<8, 512, 1>());
+    }
     if (D <= 8192) return go(Shape<8, 512, 2>());
     return go(Shape<8, 512, 4>());
   }
@@ -306,7 +315,7 @@ auto dispatch_bwd_shape(int D, bool wide, F&& go) {
 
 template <typename TX, typename TY>
 cudaError_t launch_t(const LnParams& p, bool wide, int sms, cudaStream_t st) {
-  return dispatch_bwd_shape(p.D, wide, [&](auto S) {
+  return dispatch_bwd_shape<sizeof(TX) + sizeof(TY) == 4>(p.D, wide, [&](auto S) {
     using Sh = decltype(S);
     constexpr int TEAMS = kBwdThreads / Sh::l;
     auto kern = ln_bwd_kernel<TX, TY, Sh::v, Sh::l, Sh::n>;
@@ -315,7 +324,7 @@ cudaError_t launch_t(const LnParams& p, bool wide, int sms, cudaStream_t st) {
     if (ctas > most) ctas = most;
     if (ctas < 1) ctas = 1;
     const size_t smem = TEAMS > 1 ? sizeof(float) * TEAMS * 2 * (size_t)p.D : 0;
-    if (smem > 48 * 1024) {
+    if (smem > 32 * 1024) {   // (48 KB, what is static among them, go unasked)
       const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (e != cudaSuccess) return e;
     }

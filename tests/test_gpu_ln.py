@@ -217,9 +217,9 @@ def test_autograd_and_broadcast_gradients():
     assert y.shape == (0, 128)
 
 
-@pytest.mark.parametrize("D", [256, 376, 384, 392, 512])
+@pytest.mark.parametrize("D", [256, 376, 384, 392, 512, 760, 768, 1024, 1528, 1536, 2048, 2152, 3056, 4096, 8192])
 def test_sums_of_a_cta_fill_its_shared_memory(D):
-    """The backward's sums of 16 rows at a time are 48 KB at 384 features: what a launch gets unasked, and no more."""
+    """The backward's sums of the rows a CTA has at a time are 48 KB at 384, 768, 1,536 features: what a launch gets unasked."""
     from hstu_jagged_attention_02_gb300.norm import LNProblem
     x, w, b, dy, dres = _inputs(77, D, "bf16", "bf16", 77 + D)
     pr = LNProblem(x, w, b, eps=EPS, dy=dy, dres=dres)
