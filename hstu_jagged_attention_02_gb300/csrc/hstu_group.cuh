@@ -120,24 +120,6 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, ui
         : "memory");
   }
 }
-template <bool PAIR>
-__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int u) {
-  if constexpr (PAIR) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, %5, %6}], [%2];\n\t}" ::"r"(
-            dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];\n\t}" ::"r"(
-            dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u)
-        : "memory");
-  }
-}
 template <int CG> __device__ __forceinline__ void alloc_tmem(uint32_t dst) {
   if constexpr (CG == 1) {
     tmem_alloc(dst, 512);

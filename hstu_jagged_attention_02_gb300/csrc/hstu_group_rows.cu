@@ -180,7 +180,7 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
           if (KMAJOR) {
             load_3d<CG == 2>(dst, &tmw, full, kb * 64, f, w.e);
           } else if (p.one_w) {
-            load_4d<CG == 2>(dst, &tmw, full, 0, kb * 64, f >> 6, w.e);
+            load_3d<CG == 2>(dst, &tmw, full, 0, w.e * p.depth + kb * 64, f >> 6);
           } else {
             load_3d<CG == 2>(dst, &tmw, full, f, kb * 64, w.e);
             load_3d<CG == 2>(dst + kABytes / 2, &tmw, full, f + 64, kb * 64, w.e);
@@ -358,17 +358,17 @@ cudaError_t launch_t(GroupParams p, const void* rows, int64_t row_stride, const 
                      cudaStream_t st) {
   CUtensorMap mw, mr, mo;
   p.box_rows = p.row_block / CG;
-  // [g][features / 64][k][64]: a stage's two boxes in one copy
-  p.one_w = !KMAJOR && N % 64 == 0;
-  const uint64_t wd4[4] = {64, (uint64_t)K, (uint64_t)N / 64, (uint64_t)p.E}, ws4[3] = {(uint64_t)N * 2, 128, (uint64_t)N * K * 2};
-  const uint32_t wbox4[4] = {64, 64, 2, 1};
+  // [features / 64][g K + k][64]: a stage's two boxes in one copy, where no box of k goes on into the next group's
+  p.one_w = !KMAJOR && N % 64 == 0 && K % 64 == 0;
+  const uint64_t wd1[3] = {64, (uint64_t)K * p.E, (uint64_t)N / 64}, ws1[2] = {(uint64_t)N * 2, 128};
+  const uint32_t wbox1[3] = {64, 64, 2};
   const uint64_t wd[3] = {(uint64_t)N, (uint64_t)K, (uint64_t)p.E}, ws[2] = {(uint64_t)N * 2, (uint64_t)N * K * 2};
   const uint32_t wbox[3] = {64, KMAJOR ? 128u : 64u, 1};
   const uint64_t rd[2] = {(uint64_t)p.depth, (uint64_t)p.rows}, rs[1] = {(uint64_t)row_stride * 2};
   const uint32_t rbox[2] = {64, (uint32_t)p.box_rows}, obox[2] = {32, 32};
   const uint64_t od[2] = {(uint64_t)p.features, (uint64_t)p.rows}, os[1] = {(uint64_t)p.out_stride * sizeof(TO)};
-  if (!(p.one_w ? make_tmap_tile(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, w, wd4, ws4, wbox4, CU_TENSOR_MAP_SWIZZLE_128B)
-                : make_tmap_tile(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, w, wd, ws, wbox, CU_TENSOR_MAP_SWIZZLE_128B)) ||
+  if (!make_tmap_tile(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, w, p.one_w ? wd1 : wd, p.one_w ? ws1 : ws,
+                      p.one_w ? wbox1 : wbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_tile(&mr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, rd, rs, rbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_tile(&mo, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.out,
                       od, os, obox, sizeof(TO) == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE))
