@@ -425,9 +425,12 @@ DwShape dw_shape(int64_t rows, int E, int K, int N) {
   DwShape s;
   const int64_t blocks = rows / 64 + (rows < E ? rows : E);   // of all groups, at most
   const int nt = (N + 255) / 256;
-  // pairs where each has six blocks of a tile's rows to do, and K does not leave many of their tiles half empty
+  // pairs where each has 46 blocks of a tile's rows to do, and K does not leave many of their tiles half empty.  Groups of
+  // equal size, single CTAs against pairs: 4 x 600 rows of 512 and 2,048 11.6 us against 13.0, 4 x 3,000 36.3 against 37.8 (40
+  // blocks a pair), 4 x 4,000 43.7 against 41.5 (53); of 512 and 512: 4 x 10,000 34.0 against 36.5 (33), 4 x 15,000 44.8
+  // against 43.5 (50), 4 x 30,000 98 against 91
   const int halves = (K + 127) / 128, pairs = (halves + 1) / 2;
-  s.cg = blocks * pairs * nt >= kSms / 2 * 6 && (halves % 2 == 0 || halves >= 5) ? 2 : 1;
+  s.cg = blocks * pairs * nt >= kSms / 2 * 46 && (halves % 2 == 0 || halves >= 5) ? 2 : 1;
   s.nt = nt;
   s.kt = (K + 128 * s.cg - 1) / (128 * s.cg);
   // A piece: what a CTA (a pair) has to do on average, and not so little that adding up the pieces (2 to 3 us each, one

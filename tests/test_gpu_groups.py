@@ -81,6 +81,7 @@ def test_forward_and_backward(sizes, K, N, yt, dxt):
     ((30_011, 2), 264, 1032, "fp32", "fp32"), ((12_345, 23_456), 1096, 640, "bf16", "fp32"),
     ((700,) * 40, 320, 2048, "bf16", "bf16"), ((40_000,), 64, 768, "fp32", "bf16"),
     (tuple(200 + 37 * i for i in range(60)), 520, 264, "bf16", "bf16"),
+    ((1, 0, 20_000, 300, 37, 9_999, 64, 65, 9_000), 512, 2048, "fp32", "bf16"), ((40_001,), 512, 1024, "bf16", "bf16"),
 ])
 def test_large_batches(sizes, K, N, yt, dxt):
     """CTAs in pairs, groups cut into pieces; compared on the GPU in 64 bits."""
@@ -262,7 +263,8 @@ def test_a_wait_that_runs_out_ends_the_call():
 
 
 @pytest.mark.parametrize("sizes,K,N", [
-    ((257, 0, 16_000, 63), 256, 264), ((4_000, 13_000), 264, 256), ((9_000, 9_100, 1), 192, 576),   # pairs
+    ((257, 0, 12_000, 63), 1024, 1096), ((4_000, 9_000), 1032, 1024), ((6_000, 6_100, 1), 960, 1088),   # pairs
+    ((257, 0, 6_000, 63), 256, 264), ((9_000, 1), 264, 256),
     ((200, 7, 64), 192, 72), ((200, 7, 64), 72, 192), ((1, 90, 33), 64, 320),
 ])
 def test_columns_of_wider_tensors(sizes, K, N):

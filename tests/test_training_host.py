@@ -112,7 +112,7 @@ def test_slots_hold_every_split(E):
         for K, N in ((8, 8), (128, 256), (512, 2048), (264, 520), (640, 256)):
             _, ws, zero = C.hstu_group_workspace_size(_group(groups=E, K=K, N=N, rows=rows, x_stride=K, y_stride=N, dx_stride=K))
             halves, nt = -(-K // 128), -(-N // 256)
-            pair = (rows // 64 + min(rows, E)) * -(-halves // 2) * nt >= 456 and (halves % 2 == 0 or halves >= 5)
+            pair = (rows // 64 + min(rows, E)) * -(-halves // 2) * nt >= 3496 and (halves % 2 == 0 or halves >= 5)
             cg = 2 if pair else 1
             slots = (ws - zero) // (4 * 128 * cg * 256)
             tiles = -(-halves // cg) * nt
