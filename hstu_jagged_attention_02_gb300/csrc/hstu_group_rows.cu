@@ -442,7 +442,9 @@ size_t bwd_bytes(const hstu_group_desc* d) {
 // A tile's rows, and whether CTAs work in pairs.  What a choice costs: rounds of tiles over the
 // CTAs, a tile taking for each 64 of the depth the longer of its products (2 cycles a row) and of
 // its loads (128 bytes a row of A and B at 42 bytes a cycle, an SM's share of L2's 12 TB/s),
-// and some 1,500 cycles at its ends.
+// and some 1,500 cycles at its ends.  Single CTAs against pairs, 512 -> 2,048: 8 x 8 rows 6.5 us against 7.9, 4 x 1,500
+// 18.1 against 14.6, 16 x 1,000 38.1 against 32.8; dx of the same 13.4 against 14.8, 15.7 against 16.4 (taken), 45.2
+// against 29.1; 256 -> 256, 8 x 12,500 rows 18.3 against 23.9.  It errs by 12% at 4 x 1,000 rows of 1,024 -> 1,024 (pairs 11.8, single 10.5).
 void set_tile(GroupParams& p, int sms) {
   const int64_t kblocks = (p.depth + 63) / 64, groups = p.rows < p.E ? p.rows : p.E;
   int64_t best = -1;
