@@ -17,6 +17,7 @@ using namespace tc;
 
 constexpr int kMaxGroups = 4096;
 constexpr int kThreads = 10 * 32;   // 8 warps read accumulators, one loads, one issues the products
+constexpr int kRun = 16;            // blocks of 64 summed in one accumulator
 constexpr int kEpiWarps = 8, kLoadWarp = 8, kMmaWarp = 9;
 
 struct GroupParams {

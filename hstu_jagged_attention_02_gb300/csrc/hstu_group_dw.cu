@@ -39,7 +39,6 @@ using namespace grp;
 constexpr int kStagesMax = 8;
 constexpr int kBox = 64 * 64 * 2;                 // 64 rows x 64 features
 constexpr int kStaging = kEpiWarps * 4096;        // a 32 x 32 FP32 buffer of each storing warp
-constexpr int kRun = 16;                          // 64-row blocks summed in one accumulator
 constexpr int kRanked = kThreads;                 // groups up to which they are sorted by the length of their pieces
 enum : int { B_FULL = 0, B_EMPTY = B_FULL + kStagesMax, B_DFULL = B_EMPTY + kStagesMax, B_DEMPTY = B_DFULL + 2,
              B_CLEAR = B_DEMPTY + 2, B_DRAIN = B_CLEAR + kStagesMax, B_COUNT };

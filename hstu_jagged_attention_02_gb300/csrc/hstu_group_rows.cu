@@ -20,6 +20,12 @@
 // loops as one with an elected lane, so that operands are uniform values.
 // Two accumulators in TMEM, so that a tile is stored while the next one is computed.
 //
+// Precision: as in hstu_group_dw.cu, the tensor core's sums lose a little at every addition, always towards zero.
+// Beyond a depth of 1,024 (DEEP) an accumulator so is read after 1,024 of it and added up in the storing warps'
+// registers, while the other one takes the next 1,024: FP32 results are 1.0e-6 off whatever the depth, where one
+// accumulator is 2.1e-6 off at 2,048 and 7.6e-5 at 65,536 (a plain FP32 product 0.2e-6 and 0.4e-6); dx of 161,288 rows
+// with a depth of 2,048 takes 257 us for 254.  Every 512 it would be 0.5e-6 and 274 us.
+//
 // Roles (352 threads): warps 0-7 store, warp 8 loads A, warp 10 B, warp 9 issues (the pair's first CTA) and
 // owns TMEM.  Every wait is bounded.
 #include "hstu_group.cuh"
@@ -98,8 +104,9 @@ struct Tiles {
   }
 };
 
-// KMAJOR: W is read with k contiguous (dx), else with features contiguous (forward); CG: CTAs that work together
-template <int CG, bool KMAJOR, typename TO>
+// KMAJOR: W is read with k contiguous (dx), else with features contiguous (forward); CG: CTAs that work together;
+// DEEP: a tile takes more than one accumulator
+template <int CG, bool KMAJOR, bool DEEP, typename TO>
 __global__ void __launch_bounds__(kRowsThreads, 1)
 group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ CUtensorMap tmw,
                   const __grid_constant__ CUtensorMap tmr, const __grid_constant__ CUtensorMap tmo) {
@@ -227,36 +234,40 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
       const int ring = resident ? kblocks : p.slots;
       auto wait = [&](uint32_t at, uint32_t parity, int site) { return __all_sync(0xffffffffu, mbar_wait(at, parity, wd, site)) != 0; };
       bool ok = true;
-      for (; ok && w.more(); w.next(), ++n) {
-        const uint32_t d = tmem + (n & 1) * 256;
-        ok = wait(bar(B_DEMPTY) + (n & 1) * 8, ((n >> 1) & 1) ^ 1, 62);
-        if (!ok) break;
+      for (; ok && w.more(); w.next()) {
         const uint32_t idesc = idesc_bf16(wide, columns(), !KMAJOR, false);
         const bool fresh = !resident || w.fresh(), release = !resident || w.last();
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (fresh) {
-            ok = wait(bar(B_BFULL) + slot * 8, slot_phase, 66);
-            if (!ok) break;
-          }
-          ok = wait(bar(B_AFULL) + stage * 8, phase, 63);
+        // an accumulator after the other, each of at most kRun blocks of the depth
+        for (int k0 = 0; ok && k0 < kblocks; k0 += DEEP ? kRun : kblocks, ++n) {
+          const int end = DEEP ? min(kblocks, k0 + kRun) : kblocks;
+          const uint32_t d = tmem + (n & 1) * 256;
+          ok = wait(bar(B_DEMPTY) + (n & 1) * 8, ((n >> 1) & 1) ^ 1, 62);
           if (!ok) break;
-          fence_after_sync();
-          const SDesc da = da0 + stage * kABytes, db = db0 + slot * slot_bytes;
-          mma<CG>(d, da, db, idesc, kb > 0 ? 1u : 0u);
+          for (int kb = k0; kb < end; ++kb) {
+            if (fresh) {
+              ok = wait(bar(B_BFULL) + slot * 8, slot_phase, 66);
+              if (!ok) break;
+            }
+            ok = wait(bar(B_AFULL) + stage * 8, phase, 63);
+            if (!ok) break;
+            fence_after_sync();
+            const SDesc da = da0 + stage * kABytes, db = db0 + slot * slot_bytes;
+            mma<CG>(d, da, db, idesc, kb > k0 ? 1u : 0u);
 #pragma unroll
-          for (int kk = 1; kk < 4; ++kk) mma<CG>(d, da + (KMAJOR ? kk * 32 : kk * 2048), db + kk * 32, idesc, 1u);
-          commit<CG>(bar(B_AEMPTY) + stage * 8);
-          if (release) commit<CG>(bar(B_BEMPTY) + slot * 8);
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1;
+            for (int kk = 1; kk < 4; ++kk) mma<CG>(d, da + (KMAJOR ? kk * 32 : kk * 2048), db + kk * 32, idesc, 1u);
+            commit<CG>(bar(B_AEMPTY) + stage * 8);
+            if (release) commit<CG>(bar(B_BEMPTY) + slot * 8);
+            if (++stage == p.stages) {
+              stage = 0;
+              phase ^= 1;
+            }
+            if (++slot == ring) {
+              slot = 0;
+              if (release) slot_phase ^= 1;
+            }
           }
-          if (++slot == ring) {
-            slot = 0;
-            if (release) slot_phase ^= 1;
-          }
+          if (ok) commit<CG>(bar(B_DFULL) + (n & 1) * 8);
         }
-        if (ok) commit<CG>(bar(B_DFULL) + (n & 1) * 8);
       }
       __syncwarp();
       commit_here<CG>(bar(B_DRAIN));
@@ -273,74 +284,124 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
     TO* out = static_cast<TO*>(p.out);
     // where this lane's row of an 8 x 8 matrix goes: matrix l / 8 of 4 has features 8 (m % 2).. and rows 8 (m / 2)..
     const uint32_t lane_row = (lane >> 4) * 8 + (lane & 7), lane_chunk = (lane >> 3 & 1) ^ (lane >> 1 & 3);
-    uint32_t n = 0;
-    for (; w.more(); w.next(), ++n) {
-      const uint32_t d = n & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_DFULL + d), (n >> 1) & 1, wd, 64))) break;
-      fence_after_sync();
-      const int f = w.f0 + (int)rank * 128 + wq * 32;
-#pragma unroll 1
-      for (int c = half * 32; c < w.rows; c += 64) {
-        if constexpr (sizeof(TO) == 4) {
-          // lanes are features: a row at a time, 32 neighbouring words
-          uint32_t v[32];
-          tmem_ld32(lane_base + d * 256 + c, v);
-          tmem_wait_ld();
-          if (lane == 0) bulk_wait_read<0>();   // the buffer's last store has read it
-          __syncwarp();
+    // 32 columns of an accumulator from c on.  FP32: lanes are features, a register a row.  BF16: 16 features x 32 rows
+    // a load, whose registers are 8 x 8 matrices [feature][row].
+    auto read16 = [&](uint32_t d, int c, int h, uint32_t (&v)[16]) {
+      if constexpr (sizeof(TO) == 4) tmem_ld16(lane_base + d * 256 + c + 16 * h, v);
+      else tmem_ld_16x256b_x4(lane_base + ((uint32_t)(16 * h) << 16) + d * 256 + c, v);
+    };
+    // stores the tile's rows from c on, 32 at most: v[h] is what read16 gives for h
+    auto store = [&](int f, int c, const uint32_t (&v)[2][16]) {
+      if (lane == 0) bulk_wait_read<0>();   // the buffer's last store has read it
+      __syncwarp();
+      if constexpr (sizeof(TO) == 4) {
+        // a row at a time, 32 neighbouring words
 #pragma unroll
-          for (int r = 0; r < 32; ++r)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + r * 128 + lane * 4), "r"(v[r]) : "memory");
-        } else {
-          // 16 features x 32 rows a load, whose registers are 8 x 8 matrices [feature][row]; stored transposed,
-          // 16-byte chunk k of row r at k ^ (r / 2 % 4)
-          uint32_t v[2][16];
-          tmem_ld_16x256b_x4(lane_base + d * 256 + c, v[0]);
-          tmem_ld_16x256b_x4(lane_base + (16u << 16) + d * 256 + c, v[1]);
-          tmem_wait_ld();
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
+        for (int r = 0; r < 32; ++r)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + r * 128 + lane * 4), "r"(v[r >> 4][r & 15]) : "memory");
+      } else {
+        // transposed, 16-byte chunk k of row r at k ^ (r / 2 % 4)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              uint32_t m[4];
+          for (int j = 0; j < 4; j += 2) {
+            uint32_t m[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int at = 4 * (j + (k >> 1)) + 2 * (k & 1);
-                m[k] = pack_bf16(__uint_as_float(v[h][at]), __uint_as_float(v[h][at + 1]));
-              }
-              stmatrix_trans(to + (lane_row + 8 * j) * 64 + ((lane_chunk ^ (2 * h)) << 4), m);
+            for (int k = 0; k < 4; ++k) {
+              const int at = 4 * (j + (k >> 1)) + 2 * (k & 1);
+              m[k] = pack_bf16(__uint_as_float(v[h][at]), __uint_as_float(v[h][at + 1]));
             }
-        }
-        const int live = w.rows - c;
-        if (live >= 32) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (f < p.features) tma_store_2d(&tmo, to, f, w.row0 + c);
-            bulk_commit();
+            stmatrix_trans(to + (lane_row + 8 * j) * 64 + ((lane_chunk ^ (2 * h)) << 4), m);
           }
-        } else {
-          // the group's last rows: a tile store would go on into the next group's
-          __syncwarp();
-          constexpr int kChunks = 32 * sizeof(TO) / 16, kRows = 32 / kChunks;
-          const int chunk = lane % kChunks, col = f + chunk * (16 / (int)sizeof(TO));
-#pragma unroll
-          for (int r = lane / kChunks; r < 32; r += kRows) {
-            const int place = sizeof(TO) == 2 ? chunk ^ (r >> 1 & 3) : chunk;
-            const uint4 x = *reinterpret_cast<const uint4*>(from + r * (32 * sizeof(TO)) + place * 16);
-            if (r < live && col < p.features)
-              *reinterpret_cast<uint4*>(out + (int64_t)(w.row0 + c + r) * p.out_stride + col) = x;
-          }
-          __syncwarp();
-        }
       }
+      const int live = w.rows - c;
+      if (live >= 32) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (f < p.features) tma_store_2d(&tmo, to, f, w.row0 + c);
+          bulk_commit();
+        }
+      } else {
+        // the group's last rows: a tile store would go on into the next group's
+        __syncwarp();
+        constexpr int kChunks = 32 * sizeof(TO) / 16, kRows = 32 / kChunks;
+        const int chunk = lane % kChunks, col = f + chunk * (16 / (int)sizeof(TO));
+#pragma unroll
+        for (int r = lane / kChunks; r < 32; r += kRows) {
+          const int place = sizeof(TO) == 2 ? chunk ^ (r >> 1 & 3) : chunk;
+          const uint4 x = *reinterpret_cast<const uint4*>(from + r * (32 * sizeof(TO)) + place * 16);
+          if (r < live && col < p.features)
+            *reinterpret_cast<uint4*>(out + (int64_t)(w.row0 + c + r) * p.out_stride + col) = x;
+        }
+        __syncwarp();
+      }
+    };
+    auto release = [&](uint32_t d) {
       fence_before_sync();
       __syncwarp();
       if (lane == 0) {
         if constexpr (CG == 1) mbar_arrive(bar(B_DEMPTY + d));
         else arrive_in_cluster(in_cta(bar(B_DEMPTY + d), 0));
+      }
+    };
+    uint32_t n = 0;
+    bool ok = true;
+    for (; ok && w.more(); w.next()) {
+      const int f = w.f0 + (int)rank * 128 + wq * 32;
+      if constexpr (!DEEP) {
+        const uint32_t d = n & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(B_DFULL + d), (n >> 1) & 1, wd, 64)) != 0;
+        if (!ok) break;
+        fence_after_sync();
+#pragma unroll 1
+        for (int c = half * 32; c < w.rows; c += 64) {
+          uint32_t v[2][16];
+          read16(d, c, 0, v[0]);
+          read16(d, c, 1, v[1]);
+          tmem_wait_ld();
+          store(f, c, v);
+        }
+        release(d);
+        ++n;
+      } else {
+        float acc[4][2][16];   // columns 64 i + 32 half..
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) acc[i][e >> 4][e & 15] = 0.f;
+        for (int kb = 0; kb < kblocks; kb += kRun, ++n) {
+          const uint32_t d = n & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(B_DFULL + d), (n >> 1) & 1, wd, 64)) != 0;
+          if (!ok) break;
+          fence_after_sync();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = half * 32 + 64 * i;
+            if (c < w.rows) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t v[16];
+                read16(d, c, h, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[i][h][e] += __uint_as_float(v[e]);
+              }
+            }
+          }
+          release(d);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = half * 32 + 64 * i;
+          if (c < w.rows) {
+            uint32_t v[2][16];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e >> 4][e & 15] = __float_as_uint(acc[i][e >> 4][e & 15]);
+            store(f, c, v);
+          }
+        }
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -353,7 +414,7 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
   if (warp == kMmaWarp) free_tmem<CG>(tmem);
 }
 
-template <int CG, bool KMAJOR, typename TO>
+template <int CG, bool KMAJOR, bool DEEP, typename TO>
 cudaError_t launch_t(GroupParams p, const void* rows, int64_t row_stride, const void* w, int K, int N, int sms,
                      cudaStream_t st) {
   CUtensorMap mw, mr, mo;
@@ -388,7 +449,7 @@ cudaError_t launch_t(GroupParams p, const void* rows, int64_t row_stride, const 
   }
   if (p.stages > kStagesMax) p.stages = kStagesMax;
   const size_t smem = fixed + p.stages * (size_t)kABytes + p.slots * slot;
-  auto kern = group_rows_kernel<CG, KMAJOR, TO>;
+  auto kern = group_rows_kernel<CG, KMAJOR, DEEP, TO>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t most = (p.rows / p.row_block + p.E) * (int64_t)((p.features + 128 * CG - 1) / (128 * CG));
@@ -399,8 +460,11 @@ cudaError_t launch_t(GroupParams p, const void* rows, int64_t row_stride, const 
 template <bool KMAJOR, typename TO>
 cudaError_t launch_shape(const GroupParams& p, const void* rows, int64_t row_stride, const void* w, int K, int N, int sms,
                          cudaStream_t st) {
-  return p.pair ? launch_t<2, KMAJOR, TO>(p, rows, row_stride, w, K, N, sms, st)
-                : launch_t<1, KMAJOR, TO>(p, rows, row_stride, w, K, N, sms, st);
+  if (p.depth > 64 * kRun)
+    return p.pair ? launch_t<2, KMAJOR, true, TO>(p, rows, row_stride, w, K, N, sms, st)
+                  : launch_t<1, KMAJOR, true, TO>(p, rows, row_stride, w, K, N, sms, st);
+  return p.pair ? launch_t<2, KMAJOR, false, TO>(p, rows, row_stride, w, K, N, sms, st)
+                : launch_t<1, KMAJOR, false, TO>(p, rows, row_stride, w, K, N, sms, st);
 }
 
 hstu_status_t check_desc(const hstu_group_desc* d) {
