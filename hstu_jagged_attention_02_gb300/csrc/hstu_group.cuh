@@ -20,6 +20,13 @@ constexpr int kThreads = 10 * 32;   // 8 warps read accumulators, one loads, one
 constexpr int kRun = 16;            // blocks of 64 summed in one accumulator
 constexpr int kEpiWarps = 8, kLoadWarp = 8, kMmaWarp = 9;
 
+// Counters of the weight gradients' cut tiles, at the same place of the workspace for every shape.
+constexpr int kDwCounters = 152 * kEpiWarps;
+constexpr size_t kDwCounterBytes = kDwCounters * sizeof(int);
+__device__ __forceinline__ void clear_counters(int* at, int thread, int threads) {
+  for (int i = thread; i < kDwCounters; i += threads) at[i] = 0;
+}
+
 struct GroupParams {
   const int64_t* off;
   int* hdr;
@@ -40,7 +47,7 @@ struct GroupParams {
   int kt, nt, kper;
   int one_x, one_dy; // a stage's part of x (dy) comes in one copy
   float* dw;
-  int* counters;     // of cut tiles, a storing warp each
+  int* counters;     // of cut tiles, a storing warp each; row products: cleared for the weight gradients behind them, or NULL
   float* partial;    // [slots][CTAs of a tile][warps][32 x 128]
 };
 
@@ -265,10 +272,10 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, int threads,
 
 cudaError_t launch_group_rows(const grp::GroupParams& p, bool transposed, int out_dtype, const void* rows, int64_t row_stride,
                               const void* w, int K, int N, int sms, cudaStream_t st);
-// room: group_dw_bytes of it, the first group_dw_counters zero before the first call
-cudaError_t launch_group_dw(const grp::GroupParams& p, void* room, const void* x, int64_t x_stride, const void* dy,
-                            int64_t dy_stride, int K, int N, int sms, cudaStream_t st);
-size_t group_dw_counters(int64_t rows, int E, int K, int N);
+// p.counters: group_dw_bytes of room, whose counters launch_group_rows or launch_group_dw_clear has cleared
+cudaError_t launch_group_dw(const grp::GroupParams& p, const void* x, int64_t x_stride, const void* dy, int64_t dy_stride,
+                            int K, int N, int sms, cudaStream_t st);
+cudaError_t launch_group_dw_clear(int* counters, cudaStream_t st);
 size_t group_dw_bytes(int64_t rows, int E, int K, int N);
 
 }  // namespace hstu

@@ -25,7 +25,9 @@
 // the GPU as many small ones do; pieces are dealt out longest first, back and forth.  A
 // piece that is a whole tile is stored; of others each storing warp leaves its sums in the workspace, and the warp
 // that comes last (a counter) adds up all of them, in the order of the pieces: equal inputs give equal bits.  (A second
-// kernel for that took 11 us of 58 with a heavy-tailed batch.)  A group without rows gets zeros.
+// kernel for that took 11 us of 58 with a heavy-tailed batch.)  A group without rows gets zeros.  The counters lie at the
+// same place for every shape and are cleared by the call (by dx's kernel, or by one of its own), so that a workspace
+// may have served other shapes and operators before.
 //
 // Roles as in hstu_group_rows.cu (one warp loads both operands).
 #include "hstu_group.cuh"
@@ -360,7 +362,6 @@ group_dw_kernel(const __grid_constant__ GroupParams p, const __grid_constant__ C
         there = __shfl_sync(0xffffffffu, there, 0);
         if (there != w.np - 1) continue;
         __threadfence();
-        if (lane == 0) *counter = 0;   // for the next call
         // in the order of the pieces; a warp's own sums stay where they are if they are the first or second
         const bool keeps = w.piece <= 1;
         if (!keeps) {
@@ -450,7 +451,9 @@ DwShape dw_shape(int64_t rows, int E, int K, int N) {
     }
   }
   s.kper = (int)kper;
-  // a group of b > kper blocks has at most (b + kper - 1) / kper < 2 b / kper pieces a tile
+  // a group of b > kper blocks has at most (b + kper - 1) / kper < 2 b / kper pieces a tile; such groups have more than
+  // 64 kper rows, so there are fewer than all / kper of them, and fewer than all tiles / kper <= shares cut tiles (of one
+  // group at most tiles, where np >= 2: no more than shares)
   s.slots = all <= kper ? 0 : 2 * (blocks / kper + 1) * tiles;
   return s;
 }
@@ -492,24 +495,29 @@ cudaError_t launch_t(GroupParams p, const void* x, int64_t x_stride, const void*
 
 }  // namespace
 
-// counters of cut tiles (each has two slots or more), then the slots
-size_t group_dw_counters(int64_t rows, int E, int K, int N) {
-  const DwShape s = dw_shape(rows, E, K, N);
-  return ((size_t)s.slots / 2 * s.cg * kEpiWarps * sizeof(int) + kWsAlign - 1) / kWsAlign * kWsAlign;
-}
+// counters, a warp of a cut tile each (at most kSms / cg cut tiles of cg CTAs), then the slots
+static_assert(kSms * kEpiWarps <= kDwCounters && kDwCounterBytes % kWsAlign == 0, "counters of cut tiles");
 size_t group_dw_bytes(int64_t rows, int E, int K, int N) {
   const DwShape s = dw_shape(rows, E, K, N);
-  return group_dw_counters(rows, E, K, N) + (size_t)s.slots * 128 * s.cg * 256 * sizeof(float);
+  return kDwCounterBytes + (size_t)s.slots * 128 * s.cg * 256 * sizeof(float);
 }
 
-cudaError_t launch_group_dw(const GroupParams& q, void* room, const void* x, int64_t x_stride, const void* dy,
-                            int64_t dy_stride, int K, int N, int sms, cudaStream_t st) {
+__global__ void __launch_bounds__(256) group_clear_kernel(int* counters) {
+  pdl_wait();
+  clear_counters(counters, threadIdx.x, 256);
+}
+
+cudaError_t launch_group_dw_clear(int* counters, cudaStream_t st) {
+  return launch_pdl(group_clear_kernel, dim3(1), dim3(256), 0, st, counters);
+}
+
+cudaError_t launch_group_dw(const GroupParams& q, const void* x, int64_t x_stride, const void* dy, int64_t dy_stride, int K,
+                            int N, int sms, cudaStream_t st) {
   const DwShape s = dw_shape(q.rows, q.E, K, N);
   GroupParams p = q;
   p.features = N; p.depth = K;
   p.kt = s.kt; p.nt = s.nt; p.kper = s.kper;
-  p.counters = static_cast<int*>(room);
-  p.partial = reinterpret_cast<float*>(static_cast<char*>(room) + group_dw_counters(q.rows, q.E, K, N));
+  p.partial = reinterpret_cast<float*>(reinterpret_cast<char*>(q.counters) + kDwCounterBytes);
   return s.cg == 2 ? launch_t<2>(p, x, x_stride, dy, dy_stride, sms, st) : launch_t<1>(p, x, x_stride, dy, dy_stride, sms, st);
 }
 

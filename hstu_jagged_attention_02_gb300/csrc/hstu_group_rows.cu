@@ -147,6 +147,7 @@ group_rows_kernel(const __grid_constant__ GroupParams p, const __grid_constant__
     tma_prefetch_desc(&tmo);
   }
   pdl_wait();
+  if (p.counters && blockIdx.x == 0) clear_counters(p.counters, threadIdx.x, kRowsThreads);
   const int rb = p.row_block;
   const bool good = scan_groups<kRowsThreads>(p, start, first, [&](int n) { return (n + rb - 1) / rb; });
   fence_before_sync();
@@ -549,7 +550,7 @@ extern "C" {
 hstu_status_t hstu_group_workspace_size(const hstu_group_desc* desc, size_t* fwd, size_t* bwd, size_t* zero) {
   const hstu_status_t s = check_desc(desc);
   if (s != HSTU_OK) return s;
-  if (zero) *zero = kWsHeaderBytes + group_dw_counters(desc->rows, desc->groups, desc->K, desc->N);
+  if (zero) *zero = kWsHeaderBytes + kDwCounterBytes;
   if (fwd) *fwd = kWsHeaderBytes;
   if (bwd) *bwd = bwd_bytes(desc);
   return HSTU_OK;
@@ -611,6 +612,7 @@ hstu_status_t hstu_group_bwd(const hstu_group_desc* d, const hstu_group_bwd_args
   const int64_t ys = d->rows <= 1 ? d->N : d->y_stride, xs = d->rows <= 1 ? d->K : d->x_stride;
   cudaError_t e = cudaSuccess;
   int launches = 0;
+  if (a->dw && d->rows > 0) p.counters = reinterpret_cast<int*>(static_cast<char*>(workspace) + kWsHeaderBytes);
   if (a->dx && d->rows > 0) {
     p.features = d->K; p.depth = d->N;
     p.out = a->dx; p.out_stride = d->rows == 1 ? d->K : d->dx_stride;
@@ -623,7 +625,11 @@ hstu_status_t hstu_group_bwd(const hstu_group_desc* d, const hstu_group_bwd_args
       e = cudaMemsetAsync(a->dw, 0, sizeof(float) * (size_t)d->groups * d->K * d->N, st);
     } else {
       p.dw = a->dw;
-      e = launch_group_dw(p, static_cast<char*>(workspace) + kWsHeaderBytes, a->x, xs, a->dy, ys, d->K, d->N, sms, st);
+      if (!a->dx) {
+        e = launch_group_dw_clear(p.counters, st);
+        ++launches;
+      }
+      if (e == cudaSuccess) e = launch_group_dw(p, a->x, xs, a->dy, ys, d->K, d->N, sms, st);
       ++launches;
     }
   }

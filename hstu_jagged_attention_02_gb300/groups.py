@@ -57,7 +57,9 @@ class GroupProblem:
     x and dy are used in place where their features are contiguous and rows a
     multiple of 16 bytes apart, else copied once, here.  The outputs are
     allocated unless given and lie apart from the inputs.  Rows behind the last
-    group are left as they are."""
+    group are left as they are.  A workspace that is given (uint8, 256-byte
+    aligned, as hstu_group_workspace_size says) has zeros in its first 256 bytes
+    before its first use; it may serve problems of any shape, one call at a time."""
 
     def __init__(self, x, w, group_offsets, *, out_dtype: Optional[torch.dtype] = None, dy=None, y=None, dx=None, dw=None,
                  dx_dtype: Optional[torch.dtype] = None, want_dx: bool = True, want_dw: bool = True, workspace=None,

@@ -711,11 +711,13 @@ hstu_status_t hstu_ln_bwd(const hstu_ln_desc* desc, const hstu_ln_bwd_args* args
  * elements); W and dW are dense [groups][K][N].  Up to 4096 groups.  Outputs
  * must not overlap inputs.  Equal inputs give equal bits.
  *
- * The workspace is 256-byte aligned; its first zero_bytes (the backward's; 256 for
- * the forward: the header) must be zero before its first use.  Offsets that break the
- * rules above (HSTU_ERR_DEVICE_CHECK: nothing is computed) and a pipeline wait that
- * ran out (HSTU_ERR_TIMEOUT) stay in the header; after an error the zero_bytes
- * have to be zeroed again.  Calls that overlap in time need workspaces of their own.
+ * The workspace is 256-byte aligned; its first 256 bytes, the header, must be zero
+ * before its first use.  Offsets that break the rules above (HSTU_ERR_DEVICE_CHECK:
+ * nothing is computed) and a pipeline wait that ran out (HSTU_ERR_TIMEOUT) stay in the
+ * header until the caller zeroes it.  zero_bytes are the header and the counters behind
+ * it, the same for every shape; the backward clears its counters itself, so a workspace may serve
+ * calls of other shapes and operators in turn.  Calls that overlap in time need
+ * workspaces of their own.
  * ------------------------------------------------------------------------ */
 typedef struct {
   uint32_t struct_size;      /* sizeof(hstu_group_desc) */
