@@ -16,6 +16,7 @@ namespace grp {
 using namespace tc;
 
 constexpr int kMaxGroups = 4096;
+constexpr size_t kMaxDynamic = kMaxSmemPerCta - 512;   // (512: barriers and the scan's sums)
 constexpr int kThreads = 10 * 32;   // 8 warps read accumulators, one loads, one issues the products
 constexpr int kRun = 16;            // blocks of 64 summed in one accumulator
 constexpr int kEpiWarps = 8, kLoadWarp = 8, kMmaWarp = 9;

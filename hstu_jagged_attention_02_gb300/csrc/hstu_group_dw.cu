@@ -482,11 +482,11 @@ cudaError_t launch_t(GroupParams p, const void* x, int64_t x_stride, const void*
       !make_tmap_tile(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p.dw, od, os, obox, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   const size_t fixed = 1024 + kStaging + lists_bytes(p.E), stage = (size_t)boxes_of<CG>() * kBox;
-  p.stages = (int)((kMaxSmemPerCta - 512 - fixed) / stage);   // (512: barriers and the scan's sums)
+  p.stages = (int)((kMaxDynamic - fixed) / stage);
   if (p.stages > kStagesMax) p.stages = kStagesMax;
   const size_t smem = fixed + p.stages * stage;
   auto kern = group_dw_kernel<CG>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDynamic);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)p.kt * p.nt * (p.E + p.rows / 64 / p.kper + 1);
   const unsigned grid = (unsigned)(most < sms / CG ? most : sms / CG) * CG;

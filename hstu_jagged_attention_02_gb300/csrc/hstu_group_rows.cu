@@ -438,7 +438,7 @@ cudaError_t launch_t(GroupParams p, const void* rows, int64_t row_stride, const 
   // B for the whole depth where that leaves three stages of A, else as many slots as stages
   const int64_t kblocks = (p.depth + 63) / 64;
   const size_t fixed = 1024 + staging_bytes(sizeof(TO)) + 8 * ((size_t)p.E + 1), slot = (size_t)p.row_block / CG * 128;
-  const size_t room = kMaxSmemPerCta - 512 - fixed;   // (512: barriers and the scan's sums)
+  const size_t room = kMaxDynamic - fixed;
   if (kblocks <= kSlotsMax && kblocks * slot + 3 * (size_t)kABytes <= room) {
     p.slots = (int)kblocks;
     p.stages = (int)((room - kblocks * slot) / kABytes);
@@ -451,7 +451,7 @@ cudaError_t launch_t(GroupParams p, const void* rows, int64_t row_stride, const 
   if (p.stages > kStagesMax) p.stages = kStagesMax;
   const size_t smem = fixed + p.stages * (size_t)kABytes + p.slots * slot;
   auto kern = group_rows_kernel<CG, KMAJOR, DEEP, TO>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDynamic);
   if (e != cudaSuccess) return e;
   const int64_t most = (p.rows / p.row_block + p.E) * (int64_t)((p.features + 128 * CG - 1) / (128 * CG));
   const unsigned grid = (unsigned)(most < sms / CG ? most : sms / CG) * CG;

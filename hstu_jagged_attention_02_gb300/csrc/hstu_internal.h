@@ -196,6 +196,8 @@ bool make_tmap_tile(CUtensorMap* map, CUtensorMapDataType dt, int rank, const vo
 size_t tc_bwd_smem_bytes(int H, int P, int Tb);
 bool tc_fwd_supported(int dtype, int dqk, int dv);
 size_t tc_fwd_smem_bytes(int d, int H, int P, int Tb);
+// Kernels whose dynamic shared memory goes by the call set their limit to a constant, the most that any call takes: the
+// limit is the process's, and a call on another host thread must not find it lowered between its own setting and launch.
 constexpr size_t kMaxSmemPerCta = 227 * 1024;
 bool tc_bwd_supported(int dtype, int dqk, int dv);
 cudaError_t launch_tc_fwd(const AttnParams& p, cudaStream_t stream);

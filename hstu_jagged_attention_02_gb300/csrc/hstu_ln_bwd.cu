@@ -320,12 +320,14 @@ cudaError_t launch_t(const LnParams& p, bool wide, int sms, cudaStream_t st) {
     constexpr int TEAMS = kBwdThreads / Sh::l;
     auto kern = ln_bwd_kernel<TX, TY, Sh::v, Sh::l, Sh::n>;
     int64_t ctas = (p.rows + TEAMS - 1) / TEAMS;
-    const int64_t most = sms < kLnMaxBwdCtas ? sms : kLnMaxBwdCtas;
-    if (ctas > most) ctas = most;
+    const int64_t limit = sms < kLnMaxBwdCtas ? sms : kLnMaxBwdCtas;
+    if (ctas > limit) ctas = limit;
     if (ctas < 1) ctas = 1;
     const size_t smem = TEAMS > 1 ? sizeof(float) * TEAMS * 2 * (size_t)p.D : 0;
-    if (smem > 32 * 1024) {   // (48 KB, what is static among them, go unasked)
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr size_t most = TEAMS > 1 ? sizeof(float) * TEAMS * 2 * Sh::l * Sh::n * Sh::v : 0;   // a row's features in registers
+    static_assert(most <= 64 * 1024, "teams' sums");
+    if constexpr (most > 32 * 1024) {   // (48 KB, what is static among them, go unasked)
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
       if (e != cudaSuccess) return e;
     }
     cudaError_t e = launch_pdl(kern, dim3((unsigned)ctas), dim3(kBwdThreads), smem, st, p);
