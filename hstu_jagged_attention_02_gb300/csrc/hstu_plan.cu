@@ -331,7 +331,8 @@ cudaError_t launch_plan(const PlanParams& p_in, cudaStream_t stream) {
   p.stage_off = p.B + 1 <= kPlanStageSeqs;
   p.stage_rec = p.cap_blocks <= kPlanStageBlocks;
   const size_t smem = plan_smem_bytes(p);
-  cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)(kMaxSmemPerCta - 1024));   // (1,024: what is static)
   if (e != cudaSuccess) return e;
   plan_kernel<<<p.npass == 2 ? 2 : 1, kPlanThreads, smem, stream>>>(p);
   return cudaGetLastError();

@@ -297,7 +297,7 @@ template <typename TI, typename TO, int D>
 cudaError_t bwd_launch(const AttnParams& p, int items, cudaStream_t st) {
   const size_t sm = bwd_smem<D>(p.P, p.Tb);
   cudaError_t e = cudaFuncSetAttribute(simt_bwd_kernel<TI, TO, D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmemPerCta);
   if (e != cudaSuccess) return e;
   simt_bwd_kernel<TI, TO, D><<<items, NT, sm, st>>>(p);
   return cudaGetLastError();

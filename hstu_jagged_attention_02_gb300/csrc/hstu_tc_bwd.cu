@@ -973,7 +973,7 @@ cudaError_t launch_t(const AttnParams& p, cudaStream_t st) {
   const size_t smem = tc_bwd_smem_bytes(p.H, p.P, p.Tb);
   const void* fn = reinterpret_cast<const void*>(hstu_bwd_tc_kernel<TO>);
   cudaError_t e = cudaFuncSetAttribute(hstu_bwd_tc_kernel<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+                                       (int)kMaxSmemPerCta);
   if (e != cudaSuccess) {
     set_launch_detail(e, "hstu_bwd_tc_kernel (smem attribute)", fn, kThreads, smem);
     return e;

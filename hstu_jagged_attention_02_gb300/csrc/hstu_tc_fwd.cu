@@ -917,7 +917,7 @@ static cudaError_t launch_fwd_t(const AttnParams& p, cudaStream_t st) {
   const size_t smem = tc_fwd_smem_bytes(D, p.H, p.P, p.Tb);
   const void* fn = reinterpret_cast<const void*>(hstu_fwd_tc_kernel<D, TO, DELTA>);
   cudaError_t e = cudaFuncSetAttribute(hstu_fwd_tc_kernel<D, TO, DELTA>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmemPerCta);
   if (e != cudaSuccess) {
     set_launch_detail(e, "hstu_fwd_tc_kernel (smem attribute)", fn, kThreads, smem);
     return e;
