@@ -131,7 +131,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const __grid_con
       put(dx + at(i), o);
     };
     const float mean_r = mean, rstd_r = rstd;
-    const float2 scale = make_float2(rstd_r, rstd_r), shift = make_float2(-mean_r * rstd_r, -mean_r * rstd_r);
+    // h = x rstd - mean rstd with that product in two parts: rounded to one it would leave 2^-24 of |mean| rstd where rows
+    // lie far from zero (as near as (x - mean) rstd, and 140 us for 163 with 161,293 rows of 512, FP32 and BF16)
+    const float sh = -mean_r * rstd_r, sl = fmaf(-mean_r, rstd_r, -sh);
+    const float2 scale = make_float2(rstd_r, rstd_r), shift = make_float2(sh, sh), low = make_float2(sl, sl);
     float2 s0 = make_float2(0.f, 0.f), s1 = s0;
     if constexpr (!TWICE) {
       float2 h[E / 2], t[E / 2];   // x, dy; then h and t = dy weight
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const __grid_con
       if constexpr (!KEEP) weight(w);
 #pragma unroll
       for (int k = 0; k < E / 2; ++k) {
-        h[k] = __ffma2_rn(h[k], scale, shift);
+        h[k] = __fadd2_rn(__ffma2_rn(h[k], scale, shift), low);
         sw[k] = __ffma2_rn(t[k], h[k], sw[k]);
         sb[k] = __fadd2_rn(sb[k], t[k]);
         t[k] = __fmul2_rn(t[k], KEEP ? kept[KEEP ? k : 0] : w[k]);
@@ -176,25 +179,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const __grid_con
         }
       }
     } else {
-      // rows whose sums fill the registers: h and t are computed twice from what was read
+      // rows whose sums fill the registers: h and t are computed twice from what was read (single features behind D as
+      // zeros of the weight, without a branch, so that the weight's loads go together)
       auto part = [&](int i, float (&h)[V], float (&g)[V], float (&t)[V]) {
         rx[i].get(h);
         rg[i].get(g);
-        if (p.weight) {
+        if (p.weight && (V > 1 || at(i) < D)) {
           Pack<float, V> c;
           c.load(p.weight + at(i));
           c.get(t);
+        } else if (V == 1) {
+          t[0] = 0.f;
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          h[e] = fmaf(h[e], rstd_r, shift.x);
+          h[e] = (h[e] - mean_r) * rstd_r;
           t[e] = p.weight ? g[e] * t[e] : g[e];
         }
       };
       float2 s = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (at(i) < D) {
+        if (V == 1 || at(i) < D) {
           float h[V], g[V], t[V];
           part(i, h, g, t);
 #pragma unroll
@@ -310,6 +316,7 @@ auto dispatch_bwd_shape(int D, bool wide, F&& go) {
   if (D <= 320) return go(Shape<1, 32, 10>());
   if (D <= 1024) return go(Shape<1, 128, 8>());
   if (D <= 4096) return go(Shape<1, 512, 8>());
+  if (D <= 8192) return go(Shape<1, 512, 16>());
   return go(Shape<1, 512, 32>());
 }
 
