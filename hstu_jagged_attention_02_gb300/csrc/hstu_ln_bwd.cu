@@ -52,15 +52,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const __grid_con
   constexpr int TEAMS = kBwdThreads / L, E = N * V;
   static_assert(E % 2 == 0, "features are worked on in pairs");
   __shared__ float2 red[2][L <= 32 ? 1 : TEAMS][L <= 32 ? 1 : L / 32];
-  // registers of a row as it is read; the weight is kept where it finds room beside 5 E of sums and of the row
+  // registers of a row as it is read.  Up to 16 features a lane h, dy weight and the weight stay in registers beside the sums
+  // (5 E), and the next row is read ahead where that leaves room for it; beyond, a row is computed twice
   constexpr int RAW = N * (V == 1 ? 2 : (int)(sizeof(TX) + sizeof(TY)) * 2);
-  constexpr bool KEEP = E <= 16, AHEAD = 4 * E + (KEEP ? E : 0) + RAW <= 100, TWICE = E > 16;
+  constexpr bool TWICE = E > 16, AHEAD = !TWICE && 5 * E + RAW <= 100;
   pdl_wait();
   const int team = threadIdx.x / L, l = threadIdx.x % L;
   const int64_t rows = live_rows(p), step = (int64_t)gridDim.x * TEAMS;
   auto at = [&](int i) { return (i * L + l) * V; };   // first of the lane's features in part i
   // features behind D count as zeros: of dy and of the weight
-  float2 sw[E / 2], sb[E / 2], kept[KEEP ? E / 2 : 1];
+  float2 sw[E / 2], sb[E / 2], kept[TWICE ? 1 : E / 2];
 #pragma unroll
   for (int k = 0; k < E / 2; ++k) sw[k] = sb[k] = make_float2(0.f, 0.f);
   auto weight = [&](float2 (&w)[E / 2]) {
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const __grid_con
 #pragma unroll
     for (int k = 0; k < E / 2; ++k) w[k] = make_float2(a[2 * k / V][2 * k % V], a[(2 * k + 1) / V][(2 * k + 1) % V]);
   };
-  if constexpr (KEEP) weight(kept);
+  if constexpr (!TWICE) weight(kept);
   const float inv = 1.f / (float)p.D;
   int turn = 0;
   Pack<TX, V> rx[N];
@@ -152,14 +153,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const __grid_con
         }
       }
       if constexpr (AHEAD) fetch(r + step);
-      float2 w[E / 2];
-      if constexpr (!KEEP) weight(w);
 #pragma unroll
       for (int k = 0; k < E / 2; ++k) {
         h[k] = __fadd2_rn(__ffma2_rn(h[k], scale, shift), low);
         sw[k] = __ffma2_rn(t[k], h[k], sw[k]);
         sb[k] = __fadd2_rn(sb[k], t[k]);
-        t[k] = __fmul2_rn(t[k], KEEP ? kept[KEEP ? k : 0] : w[k]);
+        t[k] = __fmul2_rn(t[k], kept[k]);
         s0 = __fadd2_rn(s0, t[k]);
         s1 = __ffma2_rn(t[k], h[k], s1);
       }
