@@ -288,6 +288,11 @@ __device__ __forceinline__ R get_record(const R* at) {
   return r;
 }
 
+// A block's bytes, m's and v's; one below the least (memory that was zeroed, say) counts as that.
+__device__ __forceinline__ int exps_of(const uint8_t* me, const uint8_t* ve, int block) {
+  return max((int)me[block], kLeastExp) | max((int)ve[block], kLeastExp) << 8;
+}
+
 template <int BITS, typename TG>
 __global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_constant__ AdamParams p) {
   pdl_wait();
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_con
   for (int i = blockIdx.x * kWarps + (threadIdx.x >> 5); i < p.chunks; i += gridDim.x * kWarps) {
     const AdamChunk c = get_record(p.list + i);
     int exps = 0;   // lane b: the bytes of block b, m's and v's
-    if (BITS == 8 && lane * kBlock < c.n) exps = c.me[lane] | c.ve[lane] << 8;
+    if (BITS == 8 && lane * kBlock < c.n) exps = exps_of(c.me, c.ve, lane);
     int new_exps = 0;
     const float lr = lr0 * c.lr_scale, keep1 = 1.f - lr * c.wd, c1 = -lr * c1s;
     const float2 keep = make_float2(keep1, keep1), step = make_float2(c1, c1);
@@ -451,7 +456,7 @@ adamw_read_kernel(int* hdr, const ReadChunk* __restrict__ list, int chunks, int 
     const ReadChunk c = get_record(list + i);
     const int n = (int)c.n;
     int exps = 0;
-    if (BITS == 8 && lane * kBlock < n) exps = c.me[lane] | c.ve[lane] << 8;
+    if (BITS == 8 && lane * kBlock < n) exps = exps_of(c.me, c.ve, lane);
 #pragma unroll 1
     for (int blk = 0; blk * kBlock < n; blk += 2) {
       uint32_t mc[4], vc[4];

@@ -772,7 +772,7 @@ hstu_status_t hstu_group_bwd(const hstu_group_desc* desc, const hstu_group_bwd_a
  *
  * state_bits 32: m and v are FP32.  state_bits 8: 256 neighbouring elements of
  * a tensor form a block with one byte E a moment, the FP32 exponent field of
- * its largest finite magnitude, at least 16.  m is a sign, 4 exponent bits (bias 7) and 3
+ * its largest finite magnitude, at least 16 (a byte below 16 counts as 16).  m is a sign, 4 exponent bits (bias 7) and 3
  * of mantissa, times 2^(E - 134); v is 5 exponent bits (bias 15) and 3 of
  * mantissa, times 2^(E - 142).  The parameters take the new moments before
  * they are rounded.  Rounding is up or down at random, so that means are kept
