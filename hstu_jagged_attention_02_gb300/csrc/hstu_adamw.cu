@@ -36,7 +36,7 @@ struct AdamState {
   int64_t steps;        // steps counted
   int64_t chunks;       // of the list
   int32_t kind;         // state_bits, grad_dtype: what the list was made for
-  float c1, c2;         // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t) of the next step
+  float c1, c2;         // 1 / (1 - beta1^t), 1 / (1 - beta2^t) of the next step
 };
 constexpr size_t kStateOff = 128;   // another line than the counter of CTAs
 
@@ -260,6 +260,9 @@ __device__ __forceinline__ uint32_t top_finite_bits(const float2 (&x)[2][2]) {
 }
 __device__ __forceinline__ int exp_byte(uint32_t top) { return max((int)(top >> 23), kLeastExp); }
 
+// The hardware's root and reciprocal, off by a step of FP32 (2^-23) at most each, beside the half steps of the update's other
+// products and sums: the moments do not go through them.  They take subnormal numbers for zero; the denominator lies
+// between eps and 2^126.
 __device__ __forceinline__ float sqrt_approx(float x) {
   float y;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -359,7 +362,9 @@ __global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_con
           const float2 gs = __fmul2_rn(g[j][h], make_float2(scale, scale));
           m[j][h] = sum2(__fmul2_rn(m[j][h], b1), __fmul2_rn(gs, a1));
           v[j][h] = sum2(__fmul2_rn(v[j][h], b2), __fmul2_rn(__fmul2_rn(gs, gs), a2));
-          const float2 d = __ffma2_rn(make_float2(sqrt_approx(v[j][h].x), sqrt_approx(v[j][h].y)), c2, eps);
+          // v / (1 - beta2^t) before the root, which takes a subnormal number for zero: its root, below 2^-63, counts for
+          // nothing beside eps, while that of a subnormal v may
+          const float2 vh = __fmul2_rn(v[j][h], c2), d = __fadd2_rn(make_float2(sqrt_approx(vh.x), sqrt_approx(vh.y)), eps);
           const float2 u = __fmul2_rn(m[j][h], make_float2(rcp_approx(d.x), rcp_approx(d.y)));
           w[j][h] = __ffma2_rn(u, step, __fmul2_rn(w[j][h], keep));
         }
@@ -434,7 +439,7 @@ __global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_con
       st->pow1 *= p.beta1;
       st->pow2 *= p.beta2;
       st->c1 = (float)(1.0 / (1.0 - st->pow1));
-      st->c2 = (float)(1.0 / sqrt(1.0 - st->pow2));
+      st->c2 = (float)(1.0 / (1.0 - st->pow2));
       st->steps += 1;
     }
   }
@@ -513,7 +518,7 @@ hstu_status_t check_desc(const hstu_adamw_desc* d) {
   const double b[2] = {d->beta1, d->beta2};
   for (double x : b)
     if (!(x >= 0.0 && x < 1.0)) return HSTU_ERR_INVALID_ARG;
-  // from 1e-12 on the square root of a subnormal v counts for nothing beside it
+  // from 1e-12 on the square root of a subnormal number counts for nothing beside it
   if (!(d->eps >= 1e-12 && d->eps < 1e30) || !(d->lr >= 0.0 && d->lr < 1e30)) return HSTU_ERR_INVALID_ARG;
   return HSTU_OK;
 }
@@ -675,7 +680,7 @@ hstu_status_t hstu_adamw_init(hstu_adamw_desc* d, const hstu_adamw_tensor* tenso
   state.pow1 = pow(d->beta1, (double)(state.steps + 1));
   state.pow2 = pow(d->beta2, (double)(state.steps + 1));
   state.c1 = (float)(1.0 / (1.0 - state.pow1));
-  state.c2 = (float)(1.0 / sqrt(1.0 - state.pow2));
+  state.c2 = (float)(1.0 / (1.0 - state.pow2));
   state.chunks = chunks;
   state.kind = kind_of(d, false, 0);
   s = send(workspace, state, keep, list, (size_t)chunks * sizeof(AdamChunk), st);
