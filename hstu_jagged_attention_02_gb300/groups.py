@@ -10,7 +10,7 @@ import torch
 
 from . import binding as C
 from .attention import _ptr
-from .norm import _DTYPES, _own_rows
+from .norm import _DTYPES, _apart, _own_rows
 from .qk import Launch, _need, _same_device, device_error
 
 
@@ -56,7 +56,8 @@ class GroupProblem:
 
     x and dy are used in place where their features are contiguous and rows a
     multiple of 16 bytes apart, else copied once, here.  The outputs are
-    allocated unless given and lie apart from the inputs.  Rows behind the last
+    allocated unless given and lie apart from the inputs (columns of one buffer
+    do), dx and dw from each other.  Rows behind the last
     group are left as they are.  A workspace that is given (uint8, 256-byte
     aligned, as hstu_group_workspace_size says) has zeros in its first 256 bytes
     before its first use; it may serve problems of any shape, one call at a time."""
@@ -85,6 +86,11 @@ class GroupProblem:
         for name, t in (("y", y), ("dx", dx), ("dw", dw)):
             _need(t is None or t.numel() == 0 or t.data_ptr() not in read, f"{name} must lie apart from what is read")
         self.x, self.w, self.offsets = _rows16(x, "x"), w, group_offsets
+        self.dy = None if dy is None else _rows16(dy, "dy")
+        for name, t in (("y", y), ("dx", dx), ("dw", dw)):
+            if t is not None:
+                _apart(name, t, x=self.x, w=w, dy=self.dy, group_offsets=group_offsets)
+        _apart("dx", dx, dw=dw)
         self.y = y if y is not None else torch.empty(rows, N, device=dev, dtype=out_dtype)
         _check_out(self.y, "y")
         backward = dy is not None
@@ -107,7 +113,6 @@ class GroupProblem:
         self._forward = Launch(dev, lib.hstu_group_fwd, "hstu_group_fwd", self.desc, self.fwd_args, *at)
         if backward:
             _need(want_dx or want_dw, "the backward needs something to compute")
-            self.dy = _rows16(dy, "dy")
             if want_dx:
                 self.dx = dx if dx is not None else torch.empty(rows, K, device=dev, dtype=dx_dtype)
                 _check_out(self.dx, "dx")

@@ -5,6 +5,7 @@ from __future__ import annotations
 
 from typing import Optional
 
+import numpy as np
 import torch
 
 from . import binding as C
@@ -30,6 +31,51 @@ def _own_rows(t, name):
           f"{name} needs contiguous features and rows that do not overlap")
 
 
+def _runs(t):
+    """(first byte, bytes of a run, bytes from run to run, runs) of the memory
+    behind a vector, or a matrix whose features are contiguous."""
+    size, at = t.element_size(), t.data_ptr()
+    if t.is_contiguous() or t.dim() != 2:
+        return at, t.numel() * size, 0, 1
+    rows, width = t.shape
+    run, pitch = ((width - 1) * t.stride(1) + 1) * size, t.stride(0) * size
+    return (at, run, pitch, rows) if pitch > run else (at, (rows - 1) * pitch + run, 0, 1)
+
+
+def _touch(a, b):
+    """Whether two tensors (vectors, rows of features, or dense) share a byte.
+    Cuts of the columns of one buffer lie apart."""
+    if a is None or b is None or a.numel() == 0 or b.numel() == 0:
+        return False
+    a, b = sorted((_runs(a), _runs(b)), key=lambda r: -r[3])
+    hull = lambda r: r[0] + r[2] * (r[3] - 1) + r[1]  # noqa: E731
+    if hull(a) <= b[0] or hull(b) <= a[0]:
+        return False
+    if a[3] == 1:
+        return True
+    # the runs of a that begin last at or before a run of b, and the next ones
+    starts = b[0] + b[2] * np.arange(b[3], dtype=np.int64)
+    i = (starts - a[0]) // a[2]
+    for k in (i, i + 1):
+        at = a[0] + a[2] * np.clip(k, 0, a[3] - 1)
+        if np.any((at < starts + b[1]) & (starts < at + a[1])):
+            return True
+    return False
+
+
+def _same_rows(a, b):
+    """Whether two matrices are the same rows, of the same type."""
+    return (a is not None and b is not None and a.data_ptr() == b.data_ptr() and a.dtype == b.dtype and a.shape == b.shape and
+            (a.shape[0] == 1 or a.stride(0) == b.stride(0)))
+
+
+def _apart(name, out, may_be=(), **others):
+    """An output shares no memory with the others, but for those that it may be."""
+    for other, t in others.items():
+        _need(not _touch(out, t) or (other in may_be and _same_rows(out, t)),
+              f"{name} shares memory with {other}" + (", and is not the same rows" if other in may_be else ""))
+
+
 def _step(t):
     return 0 if t is None or t.numel() == 0 else t.stride(0)
 
@@ -42,8 +88,9 @@ class LNProblem:
 
     x, dy, dres are used in place where their features are contiguous, else
     copied once, here.  The outputs are allocated unless given; y may be x
-    (without a backward), dx may be dy or dres, of the same type and strides.
-    mean and rstd may be those of an earlier forward."""
+    (without a backward), dx may be x, dy or dres, of the same type and strides;
+    they share no memory otherwise with what their call reads.  mean and rstd
+    may be those of an earlier forward."""
 
     def __init__(self, x, weight=None, bias=None, *, eps: float = 1e-5, out_dtype: Optional[torch.dtype] = None,
                  dy=None, dres=None, y=None, dx=None, mean=None, rstd=None, num_rows=None, want_weight_grad=None,
@@ -76,6 +123,17 @@ class LNProblem:
         _own_rows(self.y, "y")
         _need(dy is None or y is None or y.numel() == 0 or y.data_ptr() != self.x.data_ptr(),
               "the backward needs x, which a forward in place overwrites")
+        if y is not None:
+            _apart("y", y, ("x",), x=self.x, weight=weight, bias=bias, num_rows=num_rows, mean=mean, rstd=rstd)
+        if mean is not None and dy is None:   # (with dy they are those of an earlier forward: read)
+            for name, t in (("mean", mean), ("rstd", rstd)):
+                _apart(name, t, x=self.x, weight=weight, bias=bias, num_rows=num_rows)
+            _apart("mean", mean, rstd=rstd)
+        self.dy, self.dres = (None if t is None else _as_rows(t, name) for name, t in (("dy", dy), ("dres", dres)))
+        if dx is not None:
+            _own_rows(dx, "dx")
+            _apart("dx", dx, ("x", "dy", "dres"), x=self.x, dy=self.dy, dres=self.dres, weight=weight, num_rows=num_rows,
+                   mean=mean, rstd=rstd)
         self.mean = mean if mean is not None else torch.empty(rows, **f32)
         self.rstd = rstd if rstd is not None else torch.empty(rows, **f32)
         backward = dy is not None
@@ -96,9 +154,7 @@ class LNProblem:
                                            _ptr(self.mean), _ptr(self.rstd))
         self._forward = Launch(dev, lib.hstu_ln_fwd, "hstu_ln_fwd", self.desc, self.fwd_args, *w)
         if backward:
-            self.dy, self.dres = _as_rows(dy, "dy"), None if dres is None else _as_rows(dres, "dres")
             self.dx = dx if dx is not None else torch.empty(rows, D, device=dev, dtype=x.dtype)
-            _own_rows(self.dx, "dx")
             if want_weight_grad if want_weight_grad is not None else weight is not None:
                 self.d_weight = torch.empty(D, **f32)
             if want_bias_grad if want_bias_grad is not None else bias is not None:
