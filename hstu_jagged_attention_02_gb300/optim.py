@@ -51,6 +51,8 @@ class AdamW:
     that parameter is left as it is), or None: the parameters' .grad of the
     moment, looked up at every step (a list that changed is sent anew, which
     waits for the stream; into a CUDA graph goes a step with a list given).
+    Gradients at the copies, where those are autograd's leaves, are not
+    followed: a step that finds one is refused, and wants a list.
     copies: BF16 tensors (or None) written with the rounded parameters, the
     projections' operands.  weight_decay and lr_scale: a number, or one for
     each tensor.  moments: (m, v) FP32 or Moments8 for each tensor, of the same
@@ -161,8 +163,10 @@ class AdamW:
     def _follow_grads(self, stream):
         """The parameters' present .grad; a list that changed is sent anew.  A
         step that raises leaves the device's list to be sent by the next one."""
-        for i, p in enumerate(self.params):
+        for i, (p, c) in enumerate(zip(self.params, self.copies)):
             g = p.grad
+            if g is None and c is not None and c.is_leaf and c.grad is not None:
+                raise ValueError(f"the gradient of parameter {i} lies at its copy, which a step without a list does not follow: give grads")
             if g is not self.grads[i] or _ptr(g) != self._table[i].grad:
                 self._check_grad(i, g)
                 self._sent = self._sent and _ptr(g) == self._table[i].grad

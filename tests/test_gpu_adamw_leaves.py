@@ -1,0 +1,41 @@
+"""AdamW beside autograd: whose gradients a step takes."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+
+def test_gradients_at_the_copies_are_not_passed_over():
+    """Mixed precision: the BF16 copies are the leaves.  A step without a list finds nothing at the masters."""
+    from hstu_jagged_attention_02_gb300.optim import AdamW
+    masters = [torch.randn(300, device="cuda"), torch.randn(64, device="cuda")]
+    leaves = [m.bfloat16().requires_grad_() for m in masters]
+    opt = AdamW(masters, copies=leaves, grad_dtype=torch.bfloat16)
+    (leaves[0].float().square().sum() + leaves[1].float().sum()).backward()
+    before = [m.clone() for m in masters]
+    with pytest.raises(ValueError, match="parameter 0 lies at its copy"):
+        opt.step()
+    assert opt.steps() == 0 and all(torch.equal(a, b) for a, b in zip(masters, before))
+    # with the list it steps, and the leaves follow
+    opt = AdamW(masters, [t.grad for t in leaves], copies=[t.detach() for t in leaves])
+    opt.step()
+    assert opt.steps() == 1 and opt.device_error() == 0
+    assert all(torch.equal(t.detach(), m.bfloat16()) and not torch.equal(m, b) for t, m, b in zip(leaves, masters, before))
+
+
+def test_masters_as_leaves_with_copies():
+    """The masters are the leaves, and the copies are cast from them: their gradients count, whatever the copies are."""
+    from hstu_jagged_attention_02_gb300.optim import AdamW
+    w = torch.randn(300, device="cuda").requires_grad_()
+    copy = w.detach().bfloat16()
+    opt = AdamW([w], copies=[copy])
+    w.square().sum().backward()
+    opt.step()
+    assert opt.steps() == 1 and torch.equal(copy, w.detach().bfloat16())
+    made = w.bfloat16()          # no leaf
+    opt = AdamW([w], copies=[made])
+    opt.step()
+    w.grad = None
+    opt.step()
+    assert opt.steps() == 2 and torch.equal(made.detach(), w.detach().bfloat16())
