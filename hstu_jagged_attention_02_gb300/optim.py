@@ -61,6 +61,10 @@ class AdamW:
     one-element tensors on the device, read at every step; skip: not zero, the
     step changes and counts nothing.  seed: of the 8-bit moments' rounding.
 
+    A step changes the parameters and copies in place as autograd sees it: the
+    backward of a graph that saved them before raises (a replayed CUDA graph's
+    steps are not seen).
+
     All tensors are contiguous and 16-byte aligned (copies to 8 bytes, exponent
     bytes to any), must not overlap and stay where they are."""
 
@@ -116,6 +120,7 @@ class AdamW:
             self._check_grad(i, g)
         # what the device writes stays where it is while this object lives, even if a parameter's data moves
         self._held = [t.detach() for t in self.params]
+        self._changed = [t for t in (*self.params, *self.copies) if t is not None]
         self.lr_at = lr if isinstance(lr, torch.Tensor) else None
         for name, t, dt in (("lr", self.lr_at, torch.float32), ("grad_scale", grad_scale, torch.float32), ("skip", skip, torch.int32)):
             _need(t is None or (t.dtype == dt and t.numel() == 1 and t.device == dev), f"{name} must be one {dt} on {dev}")
@@ -184,6 +189,7 @@ class AdamW:
         if self.dynamic:
             self._follow_grads(stream)
         self._step(stream)
+        torch.autograd.graph.increment_version(self._changed)   # a backward that saved them finds out
 
     def steps(self, stream=None) -> int:
         """Steps counted so far.  Waits for the stream (default: the current one)."""

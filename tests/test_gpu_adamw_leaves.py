@@ -39,3 +39,27 @@ def test_masters_as_leaves_with_copies():
     w.grad = None
     opt.step()
     assert opt.steps() == 2 and torch.equal(made.detach(), w.detach().bfloat16())
+
+
+@pytest.mark.parametrize("how", ["weight", "copy", "detached"])
+def test_a_backward_behind_a_step_finds_out(how):
+    """A graph that saved what a step has changed since raises, as behind any change in place."""
+    from hstu_jagged_attention_02_gb300.groups import hstu_group_linear
+    from hstu_jagged_attention_02_gb300.norm import hstu_ln
+    from hstu_jagged_attention_02_gb300.optim import AdamW
+    x = torch.randn(40, 64, device="cuda").requires_grad_()
+    if how == "copy":
+        master = torch.randn(1, 64, 64, device="cuda")
+        leaf = master.bfloat16().requires_grad_()
+        run = lambda: hstu_group_linear(x.bfloat16(), leaf, torch.tensor([0, 40], device="cuda"))  # noqa: E731
+        opt = AdamW([master], [torch.ones_like(leaf)], copies=[leaf])
+    else:
+        leaf = torch.randn(64, device="cuda").requires_grad_()
+        run = lambda: hstu_ln(x, leaf)  # noqa: E731
+        opt = AdamW([leaf if how == "weight" else leaf.detach()], [torch.ones_like(leaf)])
+    run().float().sum().backward()
+    y = run()
+    opt.step()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.float().sum().backward()
+    run().float().sum().backward()
