@@ -48,7 +48,11 @@ class AdamW:
     moments and their BF16 copies in place, in one launch.
 
     grads: a list of tensors that every step reads (all BF16 or all FP32; None:
-    that parameter is left as it is), or None: the parameters' .grad of the
+    that parameter is left as it is, while the steps count on: there is one
+    count for all, so one whose gradients begin later has no correction of its
+    own for its young moments, and moves by up to (1 - beta1) / sqrt(1 - beta2)
+    lr at first, 3.2 lr with the usual betas; give such parameters an AdamW of
+    their own), or None: the parameters' .grad of the
     moment, looked up at every step (a list that changed is sent anew, which
     waits for the stream; into a CUDA graph goes a step with a list given).
     Gradients at the copies, where those are autograd's leaves, are not

@@ -764,7 +764,8 @@ hstu_status_t hstu_group_bwd(const hstu_group_desc* desc, const hstu_group_bwd_a
  *   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr' wd) - lr' / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
  *
- * with t the step (counted on the device, from steps_done + 1 on) and
+ * with t the step (counted on the device, from steps_done + 1 on; one count for
+ * all tensors, those that had no gradient in earlier steps among them) and
  * lr' = lr times the tensor's lr_scale.  Parameters are FP32; a tensor may
  * have a BF16 copy (the projections' operands), which is written with the
  * rounded new value.  Gradients are FP32 or BF16.  FP32 arithmetic; m and v

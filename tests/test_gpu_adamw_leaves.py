@@ -1,7 +1,10 @@
 """AdamW beside autograd: whose gradients a step takes."""
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
+
+from tests import training_ref as R  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +66,21 @@ def test_a_backward_behind_a_step_finds_out(how):
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.float().sum().backward()
     run().float().sum().backward()
+
+
+def test_one_count_for_all():
+    """A parameter without a gradient for two steps takes the third with the corrections of t = 3."""
+    from hstu_jagged_attention_02_gb300.optim import AdamW
+    first, late = (torch.zeros(256, device="cuda").requires_grad_() for _ in range(2))
+    opt = AdamW([first, late], grad_dtype=torch.float32, lr=1e-3)
+    for t in range(1, 4):
+        first.grad = torch.ones_like(first)
+        late.grad = torch.ones_like(late) if t == 3 else None
+        opt.step()
+        assert t == 3 or not bool(late.detach().any())
+    zero, one = np.zeros(256, np.float32), np.ones(256, np.float32)
+    m, v = R.moments(zero, zero, one, 0.9, 0.999)
+    want, moved = R.adamw(zero.astype(np.float64), m.astype(np.float64), v.astype(np.float64), 3, 1e-3, 0.9, 0.999, 1e-8, 0.0)
+    # the bound of any step: 2^-19 of what it moves by
+    assert np.all(np.abs(late.detach().double().cpu().numpy() - want) <= 2.0 ** -19 * moved)
+    assert opt.steps() == 3 and opt.device_error() == 0
