@@ -56,15 +56,15 @@ class GroupProblem:
 
     x and dy are used in place where their features are contiguous and rows a
     multiple of 16 bytes apart, else copied once, here.  The outputs are
-    allocated unless given and lie apart from the inputs (columns of one buffer
+    allocated unless given (no y without want_y: the backward alone) and lie apart from the inputs (columns of one buffer
     do), dx and dw from each other.  Rows behind the last
     group are left as they are.  A workspace that is given (uint8, 256-byte
     aligned, as hstu_group_workspace_size says) has zeros in its first 256 bytes
     before its first use; it may serve problems of any shape, one call at a time."""
 
     def __init__(self, x, w, group_offsets, *, out_dtype: Optional[torch.dtype] = None, dy=None, y=None, dx=None, dw=None,
-                 dx_dtype: Optional[torch.dtype] = None, want_dx: bool = True, want_dw: bool = True, workspace=None,
-                 flags: int = 0):
+                 dx_dtype: Optional[torch.dtype] = None, want_y: bool = True, want_dx: bool = True, want_dw: bool = True,
+                 workspace=None, flags: int = 0):
         _need(x.dim() == 2 and w.dim() == 3 and w.shape[1] == x.shape[1],
               f"x must be [rows, K] and w [groups, K, N], got {tuple(x.shape)} and {tuple(w.shape)}")
         _need(x.dtype == torch.bfloat16 and w.dtype == torch.bfloat16, f"x and w must be BF16, got {x.dtype} and {w.dtype}")
@@ -91,9 +91,11 @@ class GroupProblem:
             if t is not None:
                 _apart(name, t, x=self.x, w=w, dy=self.dy, group_offsets=group_offsets)
         _apart("dx", dx, dw=dw)
-        self.y = y if y is not None else torch.empty(rows, N, device=dev, dtype=out_dtype)
-        _check_out(self.y, "y")
         backward = dy is not None
+        _need(want_y or (backward and y is None), "a problem without y is one of the backward alone")
+        self.y = y if y is not None or not want_y else torch.empty(rows, N, device=dev, dtype=out_dtype)
+        if want_y:
+            _check_out(self.y, "y")
         self.dx = self.dw = None
         d = C.hstu_group_desc()
         d.struct_size = C.ctypes.sizeof(d)
@@ -126,6 +128,7 @@ class GroupProblem:
             self._backward = Launch(dev, lib.hstu_group_bwd, "hstu_group_bwd", self.bwd_desc, self.bwd_args, *at)
 
     def forward(self, stream=None):
+        _need(self.y is not None, "a problem without y has no forward")
         self._forward(stream)
 
     def backward(self, stream=None):
@@ -151,7 +154,7 @@ class GroupFunction(torch.autograd.Function):
     def backward(ctx, dy):
         x, w, off = ctx.saved_tensors
         want_dx, want_dw = ctx.needs_input_grad[:2]
-        pr = GroupProblem(x, w, off, dy=dy.to(torch.bfloat16), want_dx=want_dx, want_dw=want_dw,
+        pr = GroupProblem(x, w, off, dy=dy.to(torch.bfloat16), want_y=False, want_dx=want_dx, want_dw=want_dw,
                           dx=torch.zeros_like(x, memory_format=torch.contiguous_format) if want_dx else None)
         pr.backward()
         return pr.dx, None if pr.dw is None else pr.dw.to(w.dtype), None, None, None

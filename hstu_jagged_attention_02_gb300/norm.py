@@ -90,11 +90,12 @@ class LNProblem:
     copied once, here.  The outputs are allocated unless given; y may be x
     (without a backward), dx may be x, dy or dres, of the same type and strides;
     they share no memory otherwise with what their call reads.  mean and rstd
-    may be those of an earlier forward."""
+    may be those of an earlier forward; with them want_y=False makes a problem of
+    the backward alone."""
 
     def __init__(self, x, weight=None, bias=None, *, eps: float = 1e-5, out_dtype: Optional[torch.dtype] = None,
                  dy=None, dres=None, y=None, dx=None, mean=None, rstd=None, num_rows=None, want_weight_grad=None,
-                 want_bias_grad=None, workspace=None):
+                 want_bias_grad=None, want_y: bool = True, workspace=None):
         _need(x.dim() == 2, f"x must be [rows, D], got {tuple(x.shape)}")
         _need(x.dtype in _DTYPES, f"x must be BF16 or FP32, got {x.dtype}")
         dev = x.device
@@ -119,8 +120,11 @@ class LNProblem:
         _need(dres is None or dy is not None, "dres is of the backward, which needs dy")
         self.x, self.weight, self.bias, self.num_rows = _as_rows(x, "x"), weight, bias, num_rows
         f32 = dict(device=dev, dtype=torch.float32)
-        self.y = y if y is not None else torch.empty(rows, D, device=dev, dtype=out_dtype)
-        _own_rows(self.y, "y")
+        _need(want_y or (y is None and dy is not None and mean is not None),
+              "a problem without y is one of the backward alone, which needs the forward's mean and rstd")
+        self.y = y if y is not None or not want_y else torch.empty(rows, D, device=dev, dtype=out_dtype)
+        if want_y:
+            _own_rows(self.y, "y")
         _need(dy is None or y is None or y.numel() == 0 or y.data_ptr() != self.x.data_ptr(),
               "the backward needs x, which a forward in place overwrites")
         if y is not None:
@@ -146,7 +150,8 @@ class LNProblem:
         fwd_b, bwd_b = C.hstu_ln_workspace_size(d)
         need = max(fwd_b, bwd_b if backward else 0)
         if workspace is None:
-            workspace = torch.zeros(need, device=dev, dtype=torch.uint8)
+            workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+            workspace[:fwd_b].zero_()   # the header
         _need(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace must be contiguous uint8")
         self.ws, self.ws_bytes = workspace, workspace.numel()
         lib, w = C.load(), (self.ws.data_ptr(), self.ws_bytes)
@@ -169,6 +174,7 @@ class LNProblem:
             self._backward = Launch(dev, lib.hstu_ln_bwd, "hstu_ln_bwd", self.bwd_desc, self.bwd_args, *w)
 
     def forward(self, stream=None):
+        _need(self.y is not None, "a problem without y has no forward")
         self._forward(stream)
 
     def backward(self, stream=None):
@@ -196,7 +202,7 @@ class LNFunction(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, weight, bias, num_rows, mean, rstd = ctx.saved_tensors
-        pr = LNProblem(x, weight, bias, eps=ctx.eps, dy=dy, mean=mean, rstd=rstd, num_rows=num_rows)
+        pr = LNProblem(x, weight, bias, eps=ctx.eps, dy=dy, mean=mean, rstd=rstd, num_rows=num_rows, want_y=False)
         if num_rows is not None:
             pr.dx.zero_()
         pr.backward()
