@@ -323,8 +323,9 @@ class LayerWorkload(AttentionWorkload):
         return f, bw, f + bw + gemm
 
     def host_io(self, pr):
-        ins = [t for t in (pr.offsets, pr.num_targets, pr.num_contexts, pr.timestamps, pr.rab_pos,
-                           pr.rab_time, pr.x, pr.w1, pr.w2, pr.dout) if t is not None]
+        # (with an optimizer the parameters stay on the device: its steps write them)
+        params = () if self.optimizer else (pr.rab_pos, pr.rab_time, pr.w1, pr.w2)
+        ins = [t for t in (pr.offsets, pr.num_targets, pr.num_contexts, pr.timestamps, pr.x, *params, pr.dout) if t is not None]
         outs = [t for t in (pr.out, pr.dx, pr.dw1, pr.dw2, pr.d_rab_pos, pr.d_rab_time) if t is not None]
         return ins, outs
 
@@ -610,6 +611,8 @@ def run_gpu(args, wl, rank, world, local_rank):
     e2e = run_e2e(args, wl, probs, flops, stream, world, opts=opts)
     e2e["read_back"] = "the step's result: " + ("the candidates' outputs" if not wl.has_backward
                                                  else "the parameter gradients (activation gradients stay on the device)")
+    if wl.optimizer:
+        e2e["inputs"] = "the batch; the parameters stay on the device, where the optimizer steps them"
     e2e_all = run_e2e(args, wl, probs, flops, stream, world, all_outputs=True, opts=opts)
     e2e["all_outputs"] = {k: e2e_all[k] for k in ("value", "d2h_bytes_per_step", "ms_per_step", "repeats")}
 
