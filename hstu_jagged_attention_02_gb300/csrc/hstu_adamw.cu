@@ -4,7 +4,7 @@
 // HBM-bound: 28 bytes a parameter in 32 bits, 16 with 8-bit moments (and 2 for a BF16 copy).  The tensors are
 // cut into chunks of 256 to 2,048 elements once, by init, into a list of records that hold all of a
 // chunk's pointers: a warp needs one load before its data, and takes one chunk after the other.
-// 16 layers (21 million parameters): 104 us in 32 bits, 6.1 TB/s (89% of a copy's rate); 8 bits 71.5 us, 5.3 TB/s, with
+// 16 layers (21 million parameters): 104 us in 32 bits, 6.1 TB/s (89% of a copy's rate); 8 bits 70.0 us, 5.4 TB/s, with
 // the arithmetic of the codes (10 rounds of the generator for 4 elements) beside the loads.  Prefetches into L2 and 3
 // CTAs an SM were slower.
 //

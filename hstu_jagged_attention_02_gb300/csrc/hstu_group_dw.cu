@@ -6,11 +6,13 @@
 // 256 x 256; each holds half of both operands) where there is work for all of them: for large batches single CTAs
 // come to the 12 TB/s at which the SMs read L2 (161,293 rows, 512 x 2048: 308 us against 248).
 //
-// What bounds a pair is what its loading and issuing warps do for a stage (4 products of 128 tensor-core cycles):
-// a copy an operand where the width is a multiple of 64 (a 3-D map, 64 features innermost), both warps run their loops as one with
-// an elected lane (uniform operands): 293 us with a copy for each 64 features and single threads, 234 us so (231-250, by
-// the clock: the board is at its power limit then), cuBLAS's product of one group of that size 208-211 us.  Stages: 267 us with
-// 4, 248 with 5, 246 with 6.  Two pairs side by side that share x by multicast were no faster (252 us).
+// What bounds a pair is its loads from L2: a stage (4 products of 128 tensor-core cycles) is 32 KB a CTA, 780 cycles at an SM's
+// share (42 bytes a cycle).  161,293 rows are 531 blocks a pair: 230 us at 1.8 GHz by that, 231-250 measured (by the
+// clock: the board is at its power limit then); cuBLAS's product of one group of that size 200-211 us.  For that, what the
+// loading and issuing warps do for a stage has to be less: a copy an operand where the width is a multiple of 64 (a 3-D map,
+// 64 features innermost), both warps run their loops as one with an elected lane (uniform operands); 293 us with a copy for
+// each 64 features and single threads.  Stages: 267 us with 4, 248 with 5, 246 with 6.  Two pairs side by side that share
+// x by multicast were no faster (252 us), which was tried before the loops were made uniform.
 //
 // Rows of the next group (or past the end) in a group's last 64 are cleared in shared memory
 // before the tensor core reads them, in both operands, since 0 x infinity is no zero.  Such a block

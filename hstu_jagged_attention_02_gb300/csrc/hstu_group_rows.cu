@@ -13,18 +13,21 @@
 // load A and B for each 128 x 256 tile took 324 us for 161,293 rows, 512 -> 2048, whatever the tensor core had
 // to do).  So CTAs work in pairs (cta_group::2: 256 features, each CTA holds half of A and half of
 // B), and walk neighbouring tiles, which have the same rows: where the depth allows (512),
-// B stays in shared memory from one tile to the next and A alone streams: 250 us (cuBLAS's product of one group of that
-// size 231-249; the board is at its power limit), dx 240 us (195-204).  What is left of a stage's 780 cycles beyond
-// the tensor core's 512: waits of 50 cycles each on barriers that are there already, commits (75 each), and
-// in the forward the storing warps, 5,000 cycles for a pair's 256 x 256.  The loading and issuing warps run their
-// loops as one with an elected lane, so that operands are uniform values.
+// B stays in shared memory from one tile to the next and A alone streams: 250-260 us (cuBLAS's product of one group of that
+// size 231-249; the board is at its power limit).  What is left there: the storing warps, 5,000 cycles for a pair's
+// 256 x 256 against 4,096 of the tensor core at a depth of 512, waits of 50 cycles each on barriers that are there
+// already, commits (75 each).  At dx's depth of 2,048 both stream: a stage is 32 KB a CTA, 780 cycles at an SM's
+// share of L2 (42 bytes a cycle) for 512 of the tensor core, which is what dx takes (31 us for 16,410 rows, 2 tiles of 32
+// stages each; 236-257 us for 161,293; cuBLAS 26 and 188-204).  The loading and issuing warps run their loops as one with
+// an elected lane, so that operands are uniform values (800 cycles a stage where they are not: one issuing thread, or an
+// accumulator's place that changes inside the loop over the stages).
 // Two accumulators in TMEM, so that a tile is stored while the next one is computed.
 //
 // Precision: as in hstu_group_dw.cu, the tensor core's sums lose a little at every addition, always towards zero.
 // Beyond a depth of 1,024 (DEEP) an accumulator so is read after 1,024 of it and added up in the storing warps'
-// registers, while the other one takes the next 1,024: FP32 results are 1.0e-6 off whatever the depth, where one
+// registers, while the other one takes the next 1,024: FP32 results are at most 1.0e-6 off whatever the depth, where one
 // accumulator is 2.1e-6 off at 2,048 and 7.6e-5 at 65,536 (a plain FP32 product 0.2e-6 and 0.4e-6); dx of 161,288 rows
-// with a depth of 2,048 takes 257 us for 254.  Every 512 it would be 0.5e-6 and 274 us.
+// with a depth of 2,048 takes 257 us for 254, of 16,410 31.0 for 29.6.  Every 512 it would be 0.5e-6 and 274 us.
 //
 // Roles (352 threads): warps 0-7 store, warp 8 loads A, warp 10 B, warp 9 issues (the pair's first CTA) and
 // owns TMEM.  Every wait is bounded.
@@ -507,9 +510,10 @@ size_t bwd_bytes(const hstu_group_desc* d) {
 // A tile's rows, and whether CTAs work in pairs.  What a choice costs: rounds of tiles over the
 // CTAs, a tile taking for each 64 of the depth the longer of its products (2 cycles a row) and of
 // its loads (128 bytes a row of A and B at 42 bytes a cycle, an SM's share of L2's 12 TB/s),
-// and some 1,500 cycles at its ends.  Single CTAs against pairs, 512 -> 2,048: 8 x 8 rows 6.5 us against 7.9, 4 x 1,500
-// 18.1 against 14.6, 16 x 1,000 38.1 against 32.8; dx of the same 13.4 against 14.8, 15.7 against 16.4 (taken), 45.2
-// against 29.1; 256 -> 256, 8 x 12,500 rows 18.3 against 23.9.  It errs by 12% at 4 x 1,000 rows of 1,024 -> 1,024 (pairs 11.8, single 10.5).
+// and some 1,500 cycles at its ends.  Single CTAs against pairs, 512 -> 2,048: 8 x 8 rows 6.5 us against 8.0, 4 x 1,500
+// 18.4 against 14.9, 16 x 1,000 37.6 against 32.7; dx of the same 13.9 against 15.5, 16.8 against 17.7 (taken), 46.5
+// against 30.9; 256 -> 256, 8 x 12,500 rows 18.6 against 24.3.  It errs by 12% at 4 x 1,000 rows of 1,024 -> 1,024 (pairs
+// 12.0, single 10.6) and at dx of 4 x 600 rows of 512 and 2,048 (16.5, 14.8).
 void set_tile(GroupParams& p, int sms) {
   const int64_t kblocks = (p.depth + 63) / 64, groups = p.rows < p.E ? p.rows : p.E;
   int64_t best = -1;

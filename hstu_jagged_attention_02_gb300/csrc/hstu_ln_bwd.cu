@@ -10,9 +10,10 @@
 // order.
 //
 // 16,410 rows of 512, BF16: 14.2 us (floor 7.5), of which the second kernel takes 3: 16 warps an SM, whose lanes' sums
-// and rows fill 128 registers, wait for loads (a third of the stalls) and shuffles.  4,099 FP32 rows of 301: 5.3 us, two launches.
+// and rows fill 128 registers, wait for loads (a third of the stalls) and shuffles.  4,099 FP32 rows of 301: 5.6 us, two launches.
 // Teams of 64 lanes with half of the sums each were slower (20 us); narrow rows want more of them than a warp
-// gives: 107,181 rows of 89 took 31 us with a warp a row, 12 us with 16 lanes.
+// gives: 107,181 rows of 89 took 31 us with a warp a row, 12 us with 16 lanes.  Rows that are not 16-byte aligned hold 16
+// single features a lane up to 8,192 (2,000 FP32 rows of 5,001 48 us, with 32 a lane 88 and more).
 #include "hstu_ln.cuh"
 
 namespace hstu {
