@@ -180,16 +180,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const __grid_con
       }
     } else {
       // rows whose sums fill the registers: h and t are computed twice from what was read (single features behind D as
-      // zeros of the weight, without a branch, so that the weight's loads go together)
+      // zeros of the weight, without a branch, and read-only loads, so that the weight's go together and before stores)
       auto part = [&](int i, float (&h)[V], float (&g)[V], float (&t)[V]) {
         rx[i].get(h);
         rg[i].get(g);
-        if (p.weight && (V > 1 || at(i) < D)) {
+        if constexpr (V == 1) {
+          t[0] = p.weight && at(i) < D ? __ldg(p.weight + at(i)) : 0.f;
+        } else if (p.weight) {
           Pack<float, V> c;
           c.load(p.weight + at(i));
           c.get(t);
-        } else if (V == 1) {
-          t[0] = 0.f;
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
